@@ -243,6 +243,113 @@ int pisa_decode_append_and_select(const void* q_new, const void* k_new, int Hq,
                                   void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * A paged KV cache (the keys and values that decoding keeps; the selection's blocks of
+ * C = 64 tokens are read from it).  Sequence b's tokens [i P, (i + 1) P), P = page_size,
+ * lie in page table[b, i]; a page holds P tokens of every KV head.  Plain struct, all
+ * memory caller-owned.
+ *   pages       : device, 16-byte aligned; page i starts page_stride bytes after page
+ *                 i - 1 (>= pisa_cache_page_bytes(...), a multiple of 16, so that a pool
+ *                 may interleave layers)
+ *   table       : device int32 [B, max_pages]; entries of tokens a sequence does not hold
+ *                 are not read.  Sequences may share pages that only are read.
+ *   page_size   : 16, 32, 64, 128 or 256 tokens; max_pages * page_size <= 2^27
+ *   kind        : PISA_CACHE_BF16 or PISA_CACHE_E2M1
+ *   k_exp, v_exp: E2M1: keys (values) are held divided by 2^k_exp (2^v_exp), within
+ *                 [-24, 24]; BF16: 0
+ * A page is [Hkv, P / U] records of U = min(P, 64) tokens, a record one run of bytes:
+ *   BF16: K [U, 64], V [U, 64] bf16
+ *   E2M1: K codes [U, 32], K scales [U, 4], V codes [U, 32], V scales [U, 4]
+ * A code byte holds dims 2 i (low nibble) and 2 i + 1 as e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6,
+ * bit 3 the sign), a scale byte the e4m3 factor of 16 dims.  Writing x: scale = e4m3 of
+ * max|x| 2^-exp / 6 (nearest, ties to even, at most 448), code = e2m1 of x 2^-exp / scale
+ * (nearest, ties to even, at most 6; a negative value that rounds to zero may be held as
+ * +0), both zero when the scale rounds to zero; 16 dims with an infinity or a NaN get
+ * the NaN scale and read as NaN.
+ */
+#define PISA_CACHE_BF16 0
+#define PISA_CACHE_E2M1 1
+typedef struct {
+  void* pages;
+  const int32_t* table;
+  int64_t page_stride;
+  int B, Hkv, d, page_size, n_pages, max_pages, kind, k_exp, v_exp;
+} pisa_paged_cache;
+
+/*
+ * bf16 rows of d = 64 of a [B, T, H, d] tensor: device, 16-byte aligned, rows dense, the
+ * other strides in elements and multiples of 8 (so a slice of a fused projection will do).
+ */
+typedef struct {
+  void* data;
+  int64_t stride_b, stride_t, stride_h;
+} pisa_rows;
+
+/* Bytes of a page (0 on bad or unsupported arguments). */
+size_t pisa_cache_page_bytes(int page_size, int Hkv, int kind);
+
+/* Workspace bytes of the cache calls (the same for every size).  It starts with a status
+ * word, which the cache calls set on an error and never clear: zero the workspace once,
+ * before its first use, and read the word of any number of calls with
+ * pisa_check_device_status.  Calls that share a workspace must not overlap on the GPU;
+ * that includes replays of captured graphs. */
+size_t pisa_cache_workspace_bytes(void);
+
+/*
+ * pisa_cache_append -- rotate new queries and keys, put keys and values into the cache.
+ * Token t < counts[b] of sequence b has position start[b] + t.  In the first `rot` dims of
+ * a query or key row the pairs (i, i + rot / 2) (interleaved != 0: (2 i, 2 i + 1)) become
+ * (a c - b s, b c + a s), with c = rotary[p, i], s = rotary[p, rot / 2 + i]; each result is
+ * the 64-bit sum rounded to 32 bits and then to bf16, so the bits do not depend on the
+ * call's shape.  The rotated key, and the value, go into the page.
+ *   q       : rows [B, T, Hq, d], or NULL; k, v: rows [B, T, Hkv, d]
+ *   start   : device int32 [B]; counts: device int32 [B], or NULL (T of each)
+ *   rotary  : device fp32 [n_rot, rot], 16-byte aligned; rot in {0, 16, 32, 48, 64}, 0: no
+ *             rotation (rotary unused)
+ *   q_out   : rows [B, T, Hq, d] for the rotated queries (required with q; may be q)
+ *   k_out   : rows [B, T, Hkv, d] for the rotated keys, or NULL (may be k)
+ *   ws      : workspace for the status word, or NULL
+ * Rows t >= counts[b] of the outputs are left as they were.  A token whose position is
+ * outside [0, max_pages * page_size) or [0, n_rot), or whose page number is outside
+ * [0, n_pages), is left out of every output and flags PISA_ERR_DEVICE_BOUNDS.  Two tokens of
+ * one call must not share a place in the cache.  Hq/Hkv in {1, 2, 4, 8, 16}.
+ */
+int pisa_cache_append(const pisa_paged_cache* cache, int T, const pisa_rows* q, int Hq, const pisa_rows* k,
+                      const pisa_rows* v, const int32_t* start, const int32_t* counts, const float* rotary,
+                      int64_t n_rot, int rot, int interleaved, const pisa_rows* q_out, const pisa_rows* k_out,
+                      void* ws, void* stream);
+
+/*
+ * pisa_cache_read -- cached tokens as dense bf16: row t < counts[b] (NULL: T) of k_out and
+ * v_out (either may be NULL) is the token at position start[b] + t.  Exact: 4-bit values fit
+ * bf16.  Other rows are left as they were; positions and pages out of range as above.
+ */
+int pisa_cache_read(const pisa_paged_cache* cache, int T, const int32_t* start, const int32_t* counts,
+                    const pisa_rows* k_out, const pisa_rows* v_out, void* ws, void* stream);
+
+/*
+ * pisa_cache_attention -- the newest T tokens of each sequence attend over the paged cache
+ * (softmax scale 1/sqrt(d)), all of it or the blocks of a selection.
+ *   q       : rows [B, T, Hq, d]; query t of sequence b has position lengths[b] - T + t
+ *             and sees the tokens up to its own
+ *   lengths : device int32 [B], tokens in the cache, the T new ones included; a length past
+ *             the table's capacity is cut to it and flags PISA_ERR_DEVICE_BOUNDS
+ *   idx     : device int32 [B, Hkv, T, Ksel] blocks of 64 tokens, in any order (as
+ *             pisa_decode_append_and_select writes them, T = 1), entries that are
+ *             negative or begin after the query are skipped, one listed twice counts
+ *             twice; NULL: every token (Ksel ignored)
+ *   out     : device [B, T, Hq, d] dense, 16-byte aligned, fp32 (out_f32 != 0) or bf16
+ *   ws      : workspace of pisa_cache_workspace_bytes(), 256-byte aligned
+ * A query that sees no token gets zeros; tokens that it does not see do not matter,
+ * whatever their values.  One that sees a token in a page outside [0, n_pages) gets NaNs,
+ * and PISA_ERR_DEVICE_BOUNDS is flagged.  1 <= T <= 16, 1 <= Ksel <= 64, Hq/Hkv in
+ * {1, 2, 4, 8, 16}, B * T * Hkv < 2^24.  Sums and softmax in fp32; the weights enter the
+ * product with V as two bf16 parts (bf16 pages) or as fp16 (4-bit pages).
+ */
+int pisa_cache_attention(const pisa_paged_cache* cache, const pisa_rows* q, int T, int Hq, const int32_t* lengths,
+                         const int32_t* idx, int Ksel, void* out, int out_f32, void* ws, size_t ws_bytes,
+                         void* stream);
+
+/*
  * pisa_select_prefill_noalloc -- the prefill selection above for callers that
  * cannot allocate device memory: no workspace argument.  (The paper has no
  * counterpart; this is a deployment convenience of this library.)

@@ -26,6 +26,8 @@ __all__ = [
     "noalloc_prepare", "noalloc_device_status",
     "decode_workspace_bytes",
     "decode_append_and_select", "check_device_status", "status_string", "kernel_launches",
+    "PagedCache", "cache_workspace", "cache_workspace_bytes", "cache_append", "cache_read", "cache_attention",
+    "rotary_table",
     "prefill_phases", "set_phase_events", "D", "C", "G_MERGE",
 ]
 
@@ -99,6 +101,16 @@ def load(path: str | None = None):
     lib.pisa_noalloc_prepare.restype = i32
     lib.pisa_noalloc_device_status.argtypes = [vp]
     lib.pisa_noalloc_device_status.restype = i32
+    lib.pisa_cache_page_bytes.argtypes = [i32, i32, i32]
+    lib.pisa_cache_page_bytes.restype = sz
+    lib.pisa_cache_workspace_bytes.argtypes = []
+    lib.pisa_cache_workspace_bytes.restype = sz
+    lib.pisa_cache_append.argtypes = [vp, i32, vp, i32, vp, vp, vp, vp, vp, i64, i32, i32, vp, vp, vp, vp]
+    lib.pisa_cache_append.restype = i32
+    lib.pisa_cache_read.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp]
+    lib.pisa_cache_read.restype = i32
+    lib.pisa_cache_attention.argtypes = [vp, vp, i32, i32, vp, vp, i32, vp, i32, vp, sz, vp]
+    lib.pisa_cache_attention.restype = i32
     lib.pisa_event_elapsed_ms.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_float)]
     lib.pisa_event_elapsed_ms.restype = i32
     _lib = lib
@@ -406,6 +418,272 @@ def decode_append_and_select(q_new: torch.Tensor, k_new: torch.Tensor, pyr: Pyra
                                              _stream(stream)),
            "pisa_decode_append_and_select")
     return idx, scores
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [
+        ("pages", ctypes.c_void_p),
+        ("table", ctypes.c_void_p),
+        ("page_stride", ctypes.c_int64),
+        ("B", ctypes.c_int),
+        ("Hkv", ctypes.c_int),
+        ("d", ctypes.c_int),
+        ("page_size", ctypes.c_int),
+        ("n_pages", ctypes.c_int),
+        ("max_pages", ctypes.c_int),
+        ("kind", ctypes.c_int),
+        ("k_exp", ctypes.c_int),
+        ("v_exp", ctypes.c_int),
+    ]
+
+
+class _RowsStruct(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("stride_b", ctypes.c_int64),
+        ("stride_t", ctypes.c_int64),
+        ("stride_h", ctypes.c_int64),
+    ]
+
+
+class PagedCache:
+    """Caller-owned paged KV cache: the pages and the table that maps a sequence's tokens to them.
+
+    pages: bf16 [n_pages, Hkv, page_size / U, 2, U, 64] (K, then V), or 4 bits as uint8
+    [n_pages, Hkv, page_size / U, 72 U] (K codes [U, 32], K scales [U, 4], V codes, V scales; e2m1 codes, one
+    e4m3 scale per 16 dims), U = min(page_size, 64).  Only the stride between pages may differ from dense (a
+    pool that interleaves layers).  table: int32 [B, max_pages].  k_exp, v_exp (4 bits only): keys and values
+    are held divided by 2^k_exp and 2^v_exp.  The descriptor is made once; the tensors' contents may change, the
+    tensors may not.
+    """
+
+    __slots__ = ("pages", "table", "page_size", "B", "Hkv", "n_pages", "max_pages", "bits", "device", "_struct",
+                 "_ref")
+
+    def __init__(self, pages: torch.Tensor, table: torch.Tensor, page_size: int, k_exp: int = 0, v_exp: int = 0):
+        if page_size not in (16, 32, 64, 128, 256):
+            raise ValueError("page_size must be 16, 32, 64, 128 or 256")
+        U = min(page_size, 64)
+        if pages.dtype == torch.bfloat16 and pages.dim() == 6:
+            bits, inner = 16, (page_size // U, 2, U, D)
+        elif pages.dtype == torch.uint8 and pages.dim() == 4:
+            bits, inner = 4, (page_size // U, 72 * U)
+        else:
+            raise ValueError("pages must be bf16 [n_pages, Hkv, page_size / U, 2, U, 64] or "
+                             "uint8 [n_pages, Hkv, page_size / U, 72 U]")
+        if tuple(pages.shape[2:]) != inner or pages.shape[0] < 1 or pages.shape[1] < 1:
+            raise ValueError(f"pages of {page_size} tokens must be [n_pages, Hkv, {', '.join(map(str, inner))}]")
+        if not pages[0].is_contiguous():
+            raise ValueError("a page must be contiguous")
+        if table.dtype != torch.int32 or table.dim() != 2 or not table.is_contiguous() or table.numel() < 1:
+            raise ValueError("table must be a contiguous int32 tensor [B, max_pages]")
+        if not pages.is_cuda or table.device != pages.device:
+            raise ValueError("pages and table must be on the same CUDA device")
+        self.pages, self.table, self.page_size, self.bits = pages, table, page_size, bits
+        self.n_pages, self.Hkv = pages.shape[0], pages.shape[1]
+        self.B, self.max_pages = table.shape
+        self.device = pages.device
+        stride = pages.stride(0) if self.n_pages > 1 else pages[0].numel()
+        self._struct = _CacheStruct(pages.data_ptr(), table.data_ptr(), stride * pages.element_size(), self.B,
+                                    self.Hkv, D, page_size, self.n_pages, self.max_pages, 0 if bits == 16 else 1,
+                                    k_exp, v_exp)
+        self._ref = ctypes.byref(self._struct)
+
+    @classmethod
+    def allocate(cls, B: int, n_cap: int, Hkv: int, page_size: int = 64, bits: int = 16, device="cuda",
+                 k_exp: int = 0, v_exp: int = 0) -> "PagedCache":
+        """Pages (zeroed) and a table for B sequences of up to n_cap tokens, sequence b holding pages
+        b * per .. (b + 1) * per - 1."""
+        if page_size not in (16, 32, 64, 128, 256) or bits not in (4, 16) or B < 1 or n_cap < 1 or Hkv < 1:
+            raise ValueError("page_size 16, 32, 64, 128 or 256, bits 4 or 16, B, n_cap and Hkv at least 1")
+        U, per = min(page_size, 64), -(-n_cap // page_size)
+        shape = (B * per, Hkv, page_size // U) + ((2, U, D) if bits == 16 else (72 * U,))
+        pages = torch.zeros(shape, dtype=torch.bfloat16 if bits == 16 else torch.uint8, device=device)
+        table = torch.arange(B * per, dtype=torch.int32, device=pages.device).view(B, per)
+        return cls(pages, table, page_size, k_exp, v_exp)
+
+
+def rotary_table(n: int, rot: int = D, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """Cosines and sines fp32 [n, rot] of positions 0 .. n - 1 at frequencies base^(-2 i / rot), the angles in 64
+    bits (cache_append's `rotary`; any other table of that layout will do as well)."""
+    if rot not in (16, 32, 48, 64) or n < 1:
+        raise ValueError("rot must be 16, 32, 48 or 64 and n at least 1")
+    i = torch.arange(0, rot, 2, dtype=torch.float64, device=device)
+    angle = torch.arange(n, dtype=torch.float64, device=device)[:, None] * base ** (-i / rot)
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def cache_workspace_bytes() -> int:
+    return int(load().pisa_cache_workspace_bytes())
+
+
+def cache_workspace(cache: PagedCache) -> torch.Tensor:
+    """A workspace for the cache calls on this cache's device, its status word zero.  One stream at a time; the
+    word keeps the first error of all the calls (check_device_status)."""
+    return torch.zeros(cache_workspace_bytes(), dtype=torch.uint8, device=cache.device)
+
+
+class _On:
+    """The device and stream of a cache call: the cache's device is made current for the call, tensors allocated
+    in the call belong to the stream that it launches on."""
+
+    __slots__ = ("guard", "raw")
+
+    def __init__(self, cache: PagedCache, stream):
+        dev = cache.device
+        self.guard = None
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError("the stream must be on the cache's device")
+            self.guard = torch.cuda.stream(stream)
+        elif torch.cuda.current_device() != dev.index:
+            self.guard = torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        self.raw = torch.cuda.current_stream().cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _rows(x: torch.Tensor, what: str, cache: PagedCache, B: int, T: int, H: int, written: bool = False):
+    if x.dtype != torch.bfloat16 or x.device != cache.device or tuple(x.shape) != (B, T, H, D):
+        raise ValueError(f"{what} must be a bf16 tensor [{B}, {T}, {H}, {D}] on the cache's device")
+    sb, st, sh, sd = x.stride()
+    if sd != 1:
+        raise ValueError(f"the rows of {what} must be dense")
+    if written and ((B > 1 and sb == 0) or (T > 1 and st == 0) or (H > 1 and sh == 0)):
+        raise ValueError(f"the rows of {what} must not share memory")
+    # (the stride of a dimension of one entry is never used and may be anything)
+    return ctypes.byref(_RowsStruct(x.data_ptr(), sb if B > 1 else 0, st if T > 1 else 0, sh if H > 1 else 0))
+
+
+def _per_sequence(x: torch.Tensor, what: str, cache: PagedCache) -> int:
+    if x.dtype != torch.int32 or x.device != cache.device or x.shape != (cache.B,) or not x.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 tensor [{cache.B}] on the cache's device")
+    return x.data_ptr()
+
+
+def _cache_ws(workspace: torch.Tensor | None, cache: PagedCache, need: int) -> int:
+    if workspace.device != cache.device or not workspace.is_contiguous() or workspace.dtype != torch.uint8:
+        raise ValueError("workspace must be a contiguous uint8 tensor on the cache's device")
+    if workspace.numel() < need:
+        raise PisaError(3, "workspace")
+    return workspace.data_ptr()
+
+
+def cache_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: PagedCache, start: torch.Tensor,
+                 rotary: torch.Tensor | None, counts: torch.Tensor | None = None, interleaved: bool = False,
+                 q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None, stream=None):
+    """Rotate new queries and keys by their positions and put keys and values into the cache.
+
+    q [B, T, Hq, 64] (or None), k and v [B, T, Hkv, 64] bf16, any strides that are multiples of 8; token t of
+    sequence b goes to position start[b] + t (int32 [B]), t < counts[b] (int32 [B]; None: all T).  rotary fp32
+    [n, rot], rot 16, 32, 48 or 64: cosines, then sines of each position (None: no rotation); pairs (i, i +
+    rot / 2), or (2 i, 2 i + 1) when interleaved.  Returns (q_out, k_out): the rotated queries (None without q)
+    and keys, allocated here when not given (rows t >= counts[b] are then not written); q_out may be q and
+    k_out may be k.  workspace: for the status word only, may be None.
+    """
+    if k.dim() != 4:
+        raise ValueError("k must be a bf16 tensor [B, T, Hkv, 64]")
+    B, T, Hkv = cache.B, k.shape[1], cache.Hkv
+    ks, vs = _rows(k, "k", cache, B, T, Hkv), _rows(v, "v", cache, B, T, Hkv)
+    Hq, qs = 0, None
+    if q is not None:
+        if q.dim() != 4:
+            raise ValueError("q must be a bf16 tensor [B, T, Hq, 64]")
+        Hq = q.shape[2]
+        qs = _rows(q, "q", cache, B, T, Hq)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    n_rot = rot = 0
+    if rotary is not None:
+        if (rotary.dtype != torch.float32 or rotary.dim() != 2 or rotary.device != cache.device
+                or not rotary.is_contiguous()):
+            raise ValueError("rotary must be a contiguous fp32 tensor [n, rot] on the cache's device")
+        n_rot, rot = rotary.shape
+        if rot not in (16, 32, 48, 64):
+            raise ValueError("rotary must be [n, rot] with rot 16, 32, 48 or 64")
+    sp = _per_sequence(start, "start", cache)
+    cp = _per_sequence(counts, "counts", cache) if counts is not None else None
+    wp = _cache_ws(workspace, cache, 4) if workspace is not None else None
+    with _On(cache, stream) as on:
+        if q is not None and q_out is None:
+            q_out = torch.empty(B, T, Hq, D, dtype=torch.bfloat16, device=cache.device)
+        if k_out is None:
+            k_out = torch.empty(B, T, Hkv, D, dtype=torch.bfloat16, device=cache.device)
+        qo = _rows(q_out, "q_out", cache, B, T, Hq, True) if q is not None else None
+        ko = _rows(k_out, "k_out", cache, B, T, Hkv, True)
+        _check(load().pisa_cache_append(cache._ref, T, qs, Hq, ks, vs, sp, cp,
+                                        rotary.data_ptr() if rot else None, n_rot, rot, int(interleaved), qo, ko, wp,
+                                        on.raw), "pisa_cache_append")
+    return q_out, k_out
+
+
+def cache_read(cache: PagedCache, start: torch.Tensor, T: int, counts: torch.Tensor | None = None,
+               k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None, stream=None):
+    """Cached tokens start[b] .. start[b] + counts[b] - 1 (T where counts is None) as dense bf16 (k, v)
+    [B, T, Hkv, 64], exactly; allocated here when not given (rows t >= counts[b] are not written)."""
+    B, Hkv = cache.B, cache.Hkv
+    sp = _per_sequence(start, "start", cache)
+    cp = _per_sequence(counts, "counts", cache) if counts is not None else None
+    wp = _cache_ws(workspace, cache, 4) if workspace is not None else None
+    if T < 1:
+        raise ValueError("T must be at least 1")
+    with _On(cache, stream) as on:
+        if k_out is None:
+            k_out = torch.empty(B, T, Hkv, D, dtype=torch.bfloat16, device=cache.device)
+        if v_out is None:
+            v_out = torch.empty(B, T, Hkv, D, dtype=torch.bfloat16, device=cache.device)
+        _check(load().pisa_cache_read(cache._ref, T, sp, cp, _rows(k_out, "k_out", cache, B, T, Hkv, True),
+                                      _rows(v_out, "v_out", cache, B, T, Hkv, True), wp, on.raw), "pisa_cache_read")
+    return k_out, v_out
+
+
+def cache_attention(q: torch.Tensor, cache: PagedCache, lengths: torch.Tensor, idx: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """The newest T tokens of every sequence attend over the cache: all of it, or the blocks of a selection.
+
+    q [B, T, Hq, 64] bf16, 1 <= T <= 16; query t sits at position lengths[b] - T + t (lengths int32 [B], the new
+    tokens included) and sees the tokens up to its own.  idx int32 [B, Hkv, T, Ksel] ([B, Hkv, Ksel] when T is
+    1, as decode_append_and_select returns it): blocks of 64 tokens, -1 skipped.  out [B, T, Hq, 64], bf16
+    (allocated here when not given) or fp32.
+    """
+    if q.dim() != 4:
+        raise ValueError("q must be a bf16 tensor [B, T, Hq, 64]")
+    B, T, Hkv, Hq = cache.B, q.shape[1], cache.Hkv, q.shape[2]
+    qs = _rows(q, "q", cache, B, T, Hq)
+    lp = _per_sequence(lengths, "lengths", cache)
+    Ksel, ip = 0, None
+    if idx is not None:
+        Ksel = idx.shape[-1]
+        if idx.dtype != torch.int32 or idx.device != cache.device or not idx.is_contiguous() or not (
+                tuple(idx.shape) == (B, Hkv, T, Ksel) or (T == 1 and tuple(idx.shape) == (B, Hkv, Ksel))):
+            raise ValueError(f"idx must be a contiguous int32 tensor [{B}, {Hkv}, {T}, Ksel] on the cache's device")
+        if Ksel < 1:
+            raise ValueError("idx lists no blocks")
+        ip = idx.data_ptr()
+    lib = load()
+    need = lib.pisa_cache_workspace_bytes()
+    with _On(cache, stream) as on:
+        if out is None:
+            out = torch.empty(B, T, Hq, D, dtype=torch.bfloat16, device=cache.device)
+        elif (out.dtype not in (torch.bfloat16, torch.float32) or out.device != cache.device
+              or tuple(out.shape) != (B, T, Hq, D) or not out.is_contiguous()):
+            raise ValueError(f"out must be a contiguous bf16 or fp32 tensor [{B}, {T}, {Hq}, {D}]")
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
+        _check(lib.pisa_cache_attention(cache._ref, qs, T, Hq, lp, ip, Ksel, out.data_ptr(),
+                                        int(out.dtype == torch.float32), _cache_ws(workspace, cache, need), need,
+                                        on.raw), "pisa_cache_attention")
+    return out
 
 
 def kernel_launches() -> int:
