@@ -21,35 +21,43 @@
 
 namespace pisa {
 
-constexpr int kCaWarps = 8;
-constexpr int kCaStages = 2;
 constexpr int kPartFloats = 16 * 64 + 32;  // a partial result: O [16][64], row maxima, row sums
-constexpr int kCaGridMax = 304;            // CTAs of the split form: two on each of 152 SMs
+constexpr int kCaGrid = 152;               // CTAs of the split form: one on each SM
 constexpr int kCaMinTiles = 8;             // tiles a CTA of the split form takes at least
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kPShift = 14.f;  // fp16 weights are held times 2^14 (see below)
 
-size_t cache_part_bytes() { return (size_t)kCaGridMax * 2 * kPartFloats * sizeof(float); }
+size_t cache_part_bytes() { return (size_t)kCaGrid * 2 * kPartFloats * sizeof(float); }
 
 template <int KIND>
 struct Cfg;
 template <>
 struct Cfg<PISA_CACHE_BF16> {
-  static constexpr int KT = 32;  // keys of a tile
+  static constexpr int KT = 32;     // keys of a tile
+  static constexpr int kWarps = 8;
+  static constexpr int kStages = 3;
   static constexpr int kRow = kRowBf16;
-  static constexpr int kCtasPerSm = 1;
+  static constexpr float kShift = 0.f;  // weights are held times 2^kShift
+  static constexpr float kSlack = 20.f;  // how far (base 2) a logit may pass the row's reference
 };
 template <>
 struct Cfg<PISA_CACHE_E2M1> {
   static constexpr int KT = 64;
+  static constexpr int kWarps = 12;
+  static constexpr int kStages = 3;
   static constexpr int kRow = kRowE2m1;
-  static constexpr int kCtasPerSm = 2;
+  static constexpr float kShift = 10.f;
+  static constexpr float kSlack = 5.f;
 };
+template <int KIND>
+constexpr int kStageBytes = Cfg<KIND>::KT * Cfg<KIND>::kRow;
+constexpr int kScratch = 1024;  // bytes of a warp's own: a block list, or the weights of 16 keys
+static_assert(kScratch >= 16 * 16 * 4 && kScratch >= kCacheMaxSel * 4, "");
 
+extern __shared__ __align__(128) unsigned char ca_smem[];
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
 __device__ __forceinline__ void cpa16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(ca_smem) + dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cpa_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -61,12 +69,12 @@ template <int KIND>
 __device__ __forceinline__ void ca_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                        uint32_t b1) {
   if (KIND == PISA_CACHE_BF16)
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -75,27 +83,28 @@ __device__ __forceinline__ void ca_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
 __device__ __forceinline__ void ldm_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
+               : "r"(smem_addr(ca_smem) + addr)
                : "memory");
 }
 __device__ __forceinline__ void ldm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
+               : "r"(smem_addr(ca_smem) + addr)
                : "memory");
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
+// (plain loads, which the compiler may schedule; a is an offset into the dynamic shared memory)
+__device__ __forceinline__ uint32_t lds32(uint32_t a) { return *reinterpret_cast<const uint32_t*>(ca_smem + a); }
 __device__ __forceinline__ void lds64(uint32_t a, uint32_t& x, uint32_t& y) {
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(a) : "memory");
+  const uint2 v = *reinterpret_cast<const uint2*>(ca_smem + a);
+  x = v.x;
+  y = v.y;
 }
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
+__device__ __forceinline__ uint32_t lds8(uint32_t a) { return ca_smem[a]; }
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // 16-byte chunk ch (0..7) of row r of a staged matrix of 128-byte rows
@@ -117,7 +126,8 @@ template <int KIND>
 struct RowState {
   uint32_t qa[4][4];  // A fragments of the queries
   float f0, f1;       // logit factors of rows g and g + 8, base 2
-  float m0, m1, l0, l1;
+  float m0, m1;       // the rows' references: weights are 2^(logit - m)
+  float l0, l1;       // this lane's share of the sums of the weights
   float o[8][4];
   bool bad;  // a page out of range was met
 };
@@ -215,27 +225,19 @@ __device__ __forceinline__ int key_of(int h, int j, int e) {
   return KIND == PISA_CACHE_BF16 ? 8 * h + 2 * j + e : 8 * h + j + 4 * e;
 }
 
-// V fragments of 16-key group i: b[n][0..1] for the eight column tiles n.  Keys at or past
-// `limit` (relative to the tile) count as zeros, whatever the memory holds.
-template <int KIND, int U, bool MASK>
-__device__ __forceinline__ void load_v(uint32_t st, int i, int lane, int limit, uint32_t (&vb)[8][2]) {
+// V fragments of 16-key group i: b[n][0..1] for the eight column tiles n.
+template <int KIND, int U>
+__device__ __forceinline__ void load_v(uint32_t st, int i, int lane, uint32_t (&vb)[8][2]) {
   const int g = lane >> 2, j = lane & 3;
   if (KIND == PISA_CACHE_E2M1) {
     using L = E2m1Tile<U>;
-    const uint32_t av = st + L::v(i) + 4 * g, as = st + L::vs(i) + (g >> 1);
-    uint32_t w[4], sc[4];
+    const uint32_t av = st + L::v(i) + j * 32 + 4 * g, as = st + L::vs(i) + j * 4 + (g >> 1);
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {  // keys j, j + 4, j + 8, j + 12
-      w[x] = lds32(av + (j + 4 * x) * 32);
-      sc[x] = lds8(as + (j + 4 * x) * 4);
-      if (MASK && 16 * i + j + 4 * x >= limit) sc[x] = 0;
-    }
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      const uint32_t wa = w[2 * y], wb = w[2 * y + 1];
-      const uint32_t s2 = e4m3x2(sc[2 * y] | (sc[2 * y + 1] << 8));
+    for (int y = 0; y < 2; ++y) {  // keys j and j + 4, then j + 8 and j + 12
+      const uint32_t wa = lds32(av + 256 * y), wb = lds32(av + 256 * y + 128);
+      const uint32_t s2 = e4m3x2(__byte_perm(lds8(as + 32 * y), lds8(as + 32 * y + 16), 0x0040));
       // bytes whose nibbles are one dim of both keys
-      const uint32_t even = (wa & 0x0f0f0f0fu) | ((wb << 4) & 0xf0f0f0f0u);
+      const uint32_t even = (wa & 0x0f0f0f0fu) | (__funnelshift_l(wb, wb, 4) & 0xf0f0f0f0u);
       const uint32_t odd = ((wa >> 4) & 0x0f0f0f0fu) | (wb & 0xf0f0f0f0u);
       uint32_t d[4];
       e2m1x8(even, d);
@@ -247,91 +249,168 @@ __device__ __forceinline__ void load_v(uint32_t st, int i, int lane, int limit, 
     }
   } else {
     const uint32_t sV = st + 32 * 128;
-    uint32_t m0 = 0xffffffffu, m1 = 0xffffffffu;
-    if (MASK) {
-      const int n0 = limit - 16 * i - 2 * j, n1 = n0 - 8;
-      m0 = n0 >= 2 ? 0xffffffffu : n0 == 1 ? 0xffffu : 0u;
-      m1 = n1 >= 2 ? 0xffffffffu : n1 == 1 ? 0xffffu : 0u;
-    }
 #pragma unroll
     for (int dp = 0; dp < 4; ++dp) {
       uint32_t r[4];
       ldm_x4_t(sV + swz128(16 * i + (lane & 7) + 8 * ((lane >> 3) & 1), 2 * dp + (lane >> 4)), r);
-      vb[2 * dp][0] = r[0] & m0;
-      vb[2 * dp][1] = r[1] & m1;
-      vb[2 * dp + 1][0] = r[2] & m0;
-      vb[2 * dp + 1][1] = r[3] & m1;
+      vb[2 * dp][0] = r[0];
+      vb[2 * dp][1] = r[1];
+      vb[2 * dp + 1][0] = r[2];
+      vb[2 * dp + 1][1] = r[3];
     }
   }
 }
 
-// One staged tile of KT keys.  MASK: row g sees the tile's first v0 keys, row g + 8 the first
-// v1 (possibly none); t_lo .. t_hi are the queries of the row tile and lim(t) the keys of
-// the tile that query t sees.
-template <int KIND, int U, bool MASK, typename Lim>
-__device__ __forceinline__ void do_tile(uint32_t st, int lane, RowState<KIND>& s, int v0, int v1, int t_lo, int t_hi,
-                                        int tr0, int tr1, Lim lim) {
+// Makes the values of a staged tile's keys from `limit` on count as zeros, whatever the
+// memory holds (4 bits: a zero scale; a code is always finite).
+template <int KIND, int U>
+__device__ __forceinline__ void clear_v(uint32_t st, int lane, int limit) {
   constexpr int KT = Cfg<KIND>::KT;
-  const int g = lane >> 2, j = lane & 3;
-  float sc[KT / 8][4];
 #pragma unroll
-  for (int nt = 0; nt < KT / 8; ++nt) {
-    sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+  for (int x = 0; x < KT / 32; ++x) {
+    const int key = lane + 32 * x;
+    if (key < limit) continue;
     if (KIND == PISA_CACHE_E2M1) {
       using L = E2m1Tile<U>;
-      const int i = nt >> 1;
-      const int key = 8 * (nt & 1) + (g >> 1) + 4 * (g & 1);
-      uint32_t w0, w1, d0[4], d1[4];
-      lds64(st + L::k(i) + key * 32 + 8 * j, w0, w1);
-      const uint32_t s1 = lds8(st + L::ks(i) + key * 4 + j);
-      const uint32_t s2 = e4m3x2(s1 | (s1 << 8));
-      e2m1x8(w0, d0);
-      e2m1x8(w1, d1);
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        ca_mma<KIND>(sc[nt], s.qa[ks][0], s.qa[ks][1], s.qa[ks][2], s.qa[ks][3], hmul2u(d0[2 * ks], s2),
-                     hmul2u(d0[2 * ks + 1], s2));
-      }
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        ca_mma<KIND>(sc[nt], s.qa[2 + ks][0], s.qa[2 + ks][1], s.qa[2 + ks][2], s.qa[2 + ks][3],
-                     hmul2u(d1[2 * ks], s2), hmul2u(d1[2 * ks + 1], s2));
-      }
+      *reinterpret_cast<uint32_t*>(ca_smem + st + L::vs(key >> 4) + (key & 15) * 4) = 0u;
     } else {
 #pragma unroll
-      for (int kp = 0; kp < 2; ++kp) {
-        uint32_t r[4];
-        ldm_x4(st + swz128(8 * nt + (lane & 7), 4 * kp + (lane >> 3)), r);
-        ca_mma<KIND>(sc[nt], s.qa[2 * kp][0], s.qa[2 * kp][1], s.qa[2 * kp][2], s.qa[2 * kp][3], r[0], r[1]);
-        ca_mma<KIND>(sc[nt], s.qa[2 * kp + 1][0], s.qa[2 * kp + 1][1], s.qa[2 * kp + 1][2], s.qa[2 * kp + 1][3], r[2],
-                     r[3]);
+      for (int c = 0; c < 8; ++c)
+        *reinterpret_cast<uint4*>(ca_smem + st + KT * 128 + key * 128 + 16 * c) = make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
+// Two neighbouring dims (2 d, 2 d + 1) of a staged key's value, in 32 bits.
+template <int KIND, int U>
+__device__ __forceinline__ float2 value2(uint32_t st, int key, int d) {
+  constexpr int KT = Cfg<KIND>::KT;
+  if (KIND == PISA_CACHE_E2M1) {
+    using L = E2m1Tile<U>;
+    const uint32_t c = lds8(st + L::v(key >> 4) + (key & 15) * 32 + d);
+    const uint32_t f = e4m3x2(lds8(st + L::vs(key >> 4) + (key & 15) * 4 + (d >> 3)));
+    uint32_t v[4];
+    e2m1x8(c, v);
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&v[0]));
+    const float s = __low2float(*reinterpret_cast<const __half2*>(&f));
+    return make_float2(x.x * s, x.y * s);
+  }
+  const uint32_t w = lds32(st + KT * 128 + swz128(key, d >> 2) + 4 * (d & 3));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// The weights of a tile as A fragments of 16 keys each, in NP parts that add up to them.
+template <int KIND, int NP>
+struct Weights {
+  uint32_t a[NP][Cfg<KIND>::KT / 16][4];
+};
+
+// The products of two tiles, their instructions side by side: the logits of the tile staged
+// at st_k (QK), and O += P V for the tile staged at st_v with the weights w (PV).
+template <int KIND, int U, int NP, bool QK, bool PV>
+__device__ __forceinline__ void products(uint32_t st_k, uint32_t st_v, int lane, RowState<KIND>& s,
+                                         float (&sc)[Cfg<KIND>::KT / 8][4], const Weights<KIND, NP>& w) {
+  constexpr int KT = Cfg<KIND>::KT;
+  const int g = lane >> 2, j = lane & 3;
+#pragma unroll
+  for (int i = 0; i < KT / 16; ++i) {
+    if (QK) {
+      float(&d0)[4] = sc[2 * i];
+      float(&d1)[4] = sc[2 * i + 1];
+      d0[0] = d0[1] = d0[2] = d0[3] = d1[0] = d1[1] = d1[2] = d1[3] = 0.f;
+      if (KIND == PISA_CACHE_E2M1) {
+        using L = E2m1Tile<U>;
+        const int key = (g >> 1) + 4 * (g & 1);
+        const uint32_t ak = st_k + L::k(i) + key * 32 + 8 * j, as = st_k + L::ks(i) + key * 4 + j;
+        const uint32_t s2 = e4m3x2(__byte_perm(lds8(as), lds8(as + 32), 0x0040));
+        const __half2 p = *reinterpret_cast<const __half2*>(&s2);
+        const __half2 q0 = __low2half2(p), q1 = __high2half2(p);
+        const uint32_t f0 = *reinterpret_cast<const uint32_t*>(&q0), f1 = *reinterpret_cast<const uint32_t*>(&q1);
+        uint32_t x0, x1, y0, y1, b[4], c[4];
+        lds64(ak, x0, x1);
+        lds64(ak + 256, y0, y1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          e2m1x8(h ? x1 : x0, b);
+          e2m1x8(h ? y1 : y0, c);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t(&q)[4] = s.qa[2 * h + k];
+            ca_mma<KIND>(d0, q[0], q[1], q[2], q[3], hmul2u(b[2 * k], f0), hmul2u(b[2 * k + 1], f0));
+            ca_mma<KIND>(d1, q[0], q[1], q[2], q[3], hmul2u(c[2 * k], f1), hmul2u(c[2 * k + 1], f1));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int kp = 0; kp < 2; ++kp) {
+          uint32_t b[4], c[4];
+          ldm_x4(st_k + swz128(16 * i + (lane & 7), 4 * kp + (lane >> 3)), b);
+          ldm_x4(st_k + swz128(16 * i + 8 + (lane & 7), 4 * kp + (lane >> 3)), c);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t(&q)[4] = s.qa[2 * kp + k];
+            ca_mma<KIND>(d0, q[0], q[1], q[2], q[3], b[2 * k], b[2 * k + 1]);
+            ca_mma<KIND>(d1, q[0], q[1], q[2], q[3], c[2 * k], c[2 * k + 1]);
+          }
+        }
+      }
+    }
+    if (PV) {
+      uint32_t vb[8][2];
+      load_v<KIND, U>(st_v, i, lane, vb);
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        const uint32_t(&a)[4] = w.a[p][i];
+#pragma unroll
+        for (int n = 0; n < 8; ++n) ca_mma<KIND>(s.o[n], a[0], a[1], a[2], a[3], vb[n][0], vb[n][1]);
       }
     }
   }
-  // the running maximum (of the logits times their positive factor) and sum
+}
+
+// What the rows of a row tile see of the tile of keys that starts at token `first`.
+struct Sight {
+  int n0, n1;      // tokens that rows g and g + 8 see
+  int n_lo, n_hi;  // tokens that all rows, that any row sees
+};
+
+// The running softmax: logits to weights.  O must hold all earlier tiles.
+template <int KIND, int U, int NP>
+__device__ __forceinline__ void weigh(uint32_t st, int first, const Sight& see, int lane, RowState<KIND>& s,
+                                      float (&sc)[Cfg<KIND>::KT / 8][4], Weights<KIND, NP>& w, float* scratch) {
+  using C = Cfg<KIND>;
+  constexpr int KT = C::KT;
+  const int g = lane >> 2, j = lane & 3;
+  const bool masked = first + KT > see.n_lo;
+  if (masked) {
+#pragma unroll
+    for (int nt = 0; nt < KT / 8; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int key = first + 16 * (nt >> 1) + key_of<KIND>(nt & 1, j, e);
+        if (key >= see.n0) sc[nt][e] = -INFINITY;
+        if (key >= see.n1) sc[nt][2 + e] = -INFINITY;
+      }
+  }
+  // A row's reference m is the maximum of its logits up to where it was last set; it is set
+  // anew only when one passes it by more than kSlack, so that few tiles rescale O.  In fp16 a
+  // weight is held times 2^10: those down to 2^-24 of the reference keep all 11 bits (sums
+  // of many small weights stay unbiased), and 2^kSlack times it still fits.
   float b0 = -INFINITY, b1 = -INFINITY;
 #pragma unroll
-  for (int nt = 0; nt < KT / 8; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (MASK) {
-        const int key = 16 * (nt >> 1) + key_of<KIND>(nt & 1, j, e);
-        if (key >= v0) sc[nt][e] = -INFINITY;
-        if (key >= v1) sc[nt][2 + e] = -INFINITY;
-      }
-      b0 = fmaxf(b0, sc[nt][e]);
-      b1 = fmaxf(b1, sc[nt][2 + e]);
-    }
-#pragma unroll
-  for (int x = 1; x < 4; x <<= 1) {
-    b0 = fmaxf(b0, __shfl_xor_sync(kFull, b0, x));
-    b1 = fmaxf(b1, __shfl_xor_sync(kFull, b1, x));
+  for (int nt = 0; nt < KT / 8; ++nt) {
+    b0 = max3(b0, sc[nt][0], sc[nt][1]);
+    b1 = max3(b1, sc[nt][2], sc[nt][3]);
   }
-  b0 *= s.f0;
-  b1 *= s.f1;
-  if (__any_sync(kFull, b0 > s.m0 || b1 > s.m1)) {
-    const float n0 = fmaxf(s.m0, b0), n1 = fmaxf(s.m1, b1);
-    const float a0 = n0 == -INFINITY ? 1.f : ex2_approx(s.m0 - n0), a1 = n1 == -INFINITY ? 1.f : ex2_approx(s.m1 - n1);
+  if (__any_sync(kFull, b0 * s.f0 > s.m0 + C::kSlack || b1 * s.f1 > s.m1 + C::kSlack)) {
+#pragma unroll
+    for (int x = 1; x < 4; x <<= 1) {
+      b0 = fmaxf(b0, __shfl_xor_sync(kFull, b0, x));
+      b1 = fmaxf(b1, __shfl_xor_sync(kFull, b1, x));
+    }
+    const float n0 = fmaxf(s.m0, b0 * s.f0), n1 = fmaxf(s.m1, b1 * s.f1);
+    const float a0 = n0 == -INFINITY ? 1.f : ex2_approx(s.m0 - n0);
+    const float a1 = n1 == -INFINITY ? 1.f : ex2_approx(s.m1 - n1);
     s.m0 = n0;
     s.m1 = n1;
     s.l0 *= a0;
@@ -344,69 +423,92 @@ __device__ __forceinline__ void do_tile(uint32_t st, int lane, RowState<KIND>& s
       s.o[i][3] *= a1;
     }
   }
-  // p = 2^(logit - max).  In fp16 it is held times 2^14, so that weights down to 2^-28 of
-  // the largest keep all 11 bits (sums of many small weights stay unbiased).
-  const float shift = KIND == PISA_CACHE_E2M1 ? kPShift : 0.f;
-  const float c0 = s.m0 == -INFINITY ? 0.f : shift - s.m0, c1 = s.m1 == -INFINITY ? 0.f : shift - s.m1;
+  const float c0 = s.m0 == -INFINITY ? 0.f : C::kShift - s.m0, c1 = s.m1 == -INFINITY ? 0.f : C::kShift - s.m1;
+  const unsigned long long f0 = f2_pack(s.f0, s.f0), f1 = f2_pack(s.f1, s.f1);
+  const unsigned long long cc0 = f2_pack(c0, c0), cc1 = f2_pack(c1, c1);
+  unsigned long long l0 = f2_pack(s.l0, 0.f), l1 = f2_pack(s.l1, 0.f);
 #pragma unroll
-  for (int nt = 0; nt < KT / 8; ++nt)
+  for (int nt = 0; nt < KT / 8; ++nt) {
+    f2_unpack(f2_fma(f2_pack(sc[nt][0], sc[nt][1]), f0, cc0), sc[nt][0], sc[nt][1]);
+    f2_unpack(f2_fma(f2_pack(sc[nt][2], sc[nt][3]), f1, cc1), sc[nt][2], sc[nt][3]);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      sc[nt][e] = ex2_approx(fmaf(sc[nt][e], s.f0, c0));
-      sc[nt][2 + e] = ex2_approx(fmaf(sc[nt][2 + e], s.f1, c1));
-      s.l0 += sc[nt][e];
-      s.l1 += sc[nt][2 + e];
-    }
-  // O += P V: the logit fragments of 16 keys are the A fragment
+    for (int e = 0; e < 4; ++e) sc[nt][e] = ex2_approx(sc[nt][e]);
+    l0 = f2_add(l0, f2_pack(sc[nt][0], sc[nt][1]));
+    l1 = f2_add(l1, f2_pack(sc[nt][2], sc[nt][3]));
+  }
+  float x, y;
+  f2_unpack(l0, x, y);
+  s.l0 = x + y;
+  f2_unpack(l1, x, y);
+  s.l1 = x + y;
+  if (masked) {
+    // Values that no row sees must not count, not even as 0 * inf.  Nor must those that some
+    // rows see (of the row tile's later queries) reach the others: these few keys are added
+    // one by one to the rows that see them, and cleared like the rest.
+    const int k_lo = min(max(see.n_lo - first, 0), KT), k_hi = min(max(see.n_hi - first, 0), KT);
+    if (k_lo < k_hi) {  // (at most 15 keys: those between the first and the last query)
 #pragma unroll
-  for (int i = 0; i < KT / 16; ++i) {
-    const float(&x)[4] = sc[2 * i];
-    const float(&y)[4] = sc[2 * i + 1];
-    uint32_t hi[4], lo[4];
-    if (KIND == PISA_CACHE_E2M1) {
-      hi[0] = pack_f16x2(x[0], x[1]);
-      hi[1] = pack_f16x2(x[2], x[3]);
-      hi[2] = pack_f16x2(y[0], y[1]);
-      hi[3] = pack_f16x2(y[2], y[3]);
-    } else {  // two bf16 parts hold 16 bits of a weight
-      const float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+      for (int nt = 0; nt < KT / 8; ++nt)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        hi[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
-        lo[k] = pack_bf16x2(v[2 * k] - __uint_as_float(hi[k] << 16), v[2 * k + 1] - __uint_as_float(hi[k] & 0xffff0000u));
-      }
-    }
-    uint32_t vb[8][2];
-    if (!MASK || t_lo == t_hi) {
-      load_v<KIND, U, MASK>(st, i, lane, MASK ? lim(t_lo) : 0, vb);
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        ca_mma<KIND>(s.o[n], hi[0], hi[1], hi[2], hi[3], vb[n][0], vb[n][1]);
-        if (KIND == PISA_CACHE_BF16) ca_mma<KIND>(s.o[n], lo[0], lo[1], lo[2], lo[3], vb[n][0], vb[n][1]);
-      }
-    } else {
-      // the rows belong to several queries, which end at different keys: one pass for each,
-      // so that an infinite or NaN value of a later key does not reach an earlier query by
-      // way of 0 * inf
-      for (int t = t_lo; t <= t_hi; ++t) {
-        load_v<KIND, U, MASK>(st, i, lane, lim(t), vb);
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
-          ca_mma<KIND>(d, hi[0], hi[1], hi[2], hi[3], vb[n][0], vb[n][1]);
-          if (KIND == PISA_CACHE_BF16) ca_mma<KIND>(d, lo[0], lo[1], lo[2], lo[3], vb[n][0], vb[n][1]);
-          if (tr0 == t) {
-            s.o[n][0] += d[0];
-            s.o[n][1] += d[1];
+        for (int e = 0; e < 2; ++e) {
+          const int key = 16 * (nt >> 1) + key_of<KIND>(nt & 1, j, e) - k_lo;
+          if (key >= 0 && key < 16) {
+            scratch[key * 16 + g] = sc[nt][e];
+            scratch[key * 16 + g + 8] = sc[nt][2 + e];
           }
-          if (tr1 == t) {
-            s.o[n][2] += d[2];
-            s.o[n][3] += d[3];
+        }
+      __syncwarp();
+      for (int key = k_lo; key < k_hi; ++key) {
+        const float p0 = scratch[(key - k_lo) * 16 + g], p1 = scratch[(key - k_lo) * 16 + g + 8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float v[2];
+          if (KIND == PISA_CACHE_BF16) {
+            const float2 z = value2<KIND, U>(st, key, 4 * i + j);
+            v[0] = z.x;
+            v[1] = z.y;
+          } else {  // dims 16 j + i and 16 j + 8 + i
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 z = value2<KIND, U>(st, key, 8 * j + 4 * e + (i >> 1));
+              v[e] = i & 1 ? z.y : z.x;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (first + key < see.n0) s.o[i][e] = fmaf(p0, v[e], s.o[i][e]);
+            if (first + key < see.n1) s.o[i][2 + e] = fmaf(p1, v[e], s.o[i][2 + e]);
+          }
+        }
+      }
+      __syncwarp();
+    }
+    clear_v<KIND, U>(st, lane, k_lo);
+    __syncwarp();
+  }
+  // The weights go into the product with V as one fp16 part (4-bit pages) or two bf16 parts,
+  // and one part more for 32-bit results.
+#pragma unroll
+  for (int i = 0; i < KT / 16; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float u = sc[2 * i + (k >> 1)][2 * (k & 1)], v = sc[2 * i + (k >> 1)][2 * (k & 1) + 1];
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        const uint32_t h = KIND == PISA_CACHE_E2M1 ? pack_f16x2(u, v) : pack_bf16x2(u, v);
+        w.a[p][i][k] = h;
+        if (p + 1 < NP) {
+          if (KIND == PISA_CACHE_E2M1) {
+            const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&h));
+            u -= r.x;
+            v -= r.y;
+          } else {
+            u -= __uint_as_float(h << 16);
+            v -= __uint_as_float(h & 0xffff0000u);
           }
         }
       }
     }
-  }
 }
 
 // A unit: the row tile of (sequence b, KV head kv) that starts at row r0.
@@ -417,71 +519,86 @@ struct Unit {
   const int32_t* sel;      // listed blocks, or nullptr
 };
 
-// Tiles [i0, i1) of a unit, shared out among the CTA's warps; on return every warp holds its
-// own partial sums.
-template <int KIND, int U, bool SEL>
+// Tiles [i0, i1) of a unit (SEL: of the listed blocks that begin in sight), shared out among
+// the CTA's warps; on return every warp holds its own partial sums.  A warp copies its tiles
+// ahead into a ring of three stages: while one is on its way, the logits of the next tile and
+// the products with V of the one before are computed side by side.
+template <int KIND, int U, bool SEL, int NP>
 __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit& u, int i0, int i1, uint32_t ring,
-                                          int warp, int lane, RowState<KIND>& s) {
+                                          float* scratch, int warp, int lane, RowState<KIND>& s) {
   using C = Cfg<KIND>;
-  constexpr int KT = C::KT;
+  constexpr int KT = C::KT, W = C::kWarps;
   constexpr int E = KT > U ? KT / U : 1;  // records of a tile
-  constexpr uint32_t kStage = KT * C::kRow;
+  constexpr int kAhead = 32 / E;          // tiles a look ahead covers
+  constexpr uint32_t kStage = kStageBytes<KIND>;
+  static_assert(C::kStages == 3, "");
   const int g = lane >> 2;
   // what each row sees: tokens before n_vis(t) = n - T + t + 1
   const int ra = u.r0 + g, rb = ra + 8;
-  const int tr0 = u.t_first + ra / a.G, tr1 = u.t_first + rb / a.G;
-  const int n0 = ra < u.rows ? u.n - a.T + tr0 + 1 : 0, n1 = rb < u.rows ? u.n - a.T + tr1 + 1 : 0;
+  const int base = u.n - a.T + 1 + u.t_first;
   const int last = min(u.rows, u.r0 + 16) - 1;
-  const int t_lo = u.t_first + u.r0 / a.G, t_hi = u.t_first + last / a.G;
-  const int n_lo = u.n - a.T + t_lo + 1, n_hi = u.n - a.T + t_hi + 1;
+  const Sight see = {ra < u.rows ? base + ra / a.G : 0, rb < u.rows ? base + rb / a.G : 0, base + u.r0 / a.G,
+                     base + last / a.G};
+  int* list = reinterpret_cast<int*>(scratch);  // (SEL: a row tile is one query's, so weigh leaves it alone)
+  if (SEL) {  // the listed blocks that count, in the order of the list
+    int blk[2];
+    unsigned long long some[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = lane + 32 * h;
+      blk[h] = i < a.Ksel ? __ldg(u.sel + i) : -1;
+      some[h] = __ballot_sync(kFull, blk[h] >= 0 && blk[h] < (1 << 21) && blk[h] * kC < see.n_hi);
+    }
+    const unsigned below = (1u << lane) - 1u;
+    if (some[0] >> lane & 1) list[__popc((unsigned)some[0] & below)] = blk[0];
+    if (some[1] >> lane & 1) list[__popc((unsigned)some[0]) + __popc((unsigned)some[1] & below)] = blk[1];
+    __syncwarp();
+    i0 = 0;
+    i1 = (__popc((unsigned)some[0]) + __popc((unsigned)some[1])) * (kC / KT);
+  } else {
+    i1 = min(i1, (max(see.n_hi, 0) + KT - 1) / KT);
+  }
+  const int mine = i1 - i0 > warp ? (i1 - i0 - warp + W - 1) / W : 0;  // the warp's tiles
+  if (mine == 0) return;
   const int32_t* table = a.cache.table + (long long)u.b * a.cache.max_pages;
 
-  // Lane l looks ahead: record l % E of the warp's tile number base + l / E.
-  long long off = -1;
-  int tok = 0x7fffffff;  // the first token of that tile
-  auto look = [&](int base) {
-    const int i = i0 + warp + kCaWarps * (base + lane / E);
-    off = -1;
-    tok = 0x7fffffff;
-    if (i < i1) {
-      int first;
-      if (SEL) {
-        const int blk = u.sel[i * KT / kC];
-        first = blk >= 0 && blk < (1 << 21) ? blk * kC + (i * KT) % kC : 0x7fffffff;
-      } else {
-        first = i * KT;
-      }
-      tok = first;
-      const long long p = (long long)first + (lane % E) * U;
-      if (first < n_hi && p < n_hi) {
-        const int page = __ldg(table + (p >> a.cache.page_shift));
+  auto first_of = [&](int x) {  // the first token of the warp's tile number x
+    const int i = i0 + warp + W * x;
+    return SEL ? list[i * KT / kC] * kC + (i * KT) % kC : i * KT;
+  };
+  // Lane l looks ahead: where record l % E of the warp's tile number x + l / E lies.  Records
+  // that nothing sees are read from the first page instead.
+  long long off = 0;
+  auto look = [&](int x) {
+    int page = 0;
+    off = 0;
+    const int y = x + lane / E;
+    if (y < mine) {
+      const int p = first_of(y) + (lane % E) * U;
+      if (p < see.n_hi) {
+        page = __ldg(table + (p >> a.cache.page_shift));
         if (page >= 0 && page < a.cache.n_pages) {
           off = cache_record(a.cache, C::kRow, page, u.kv, p);
           // (bf16: the tile may start inside a record)
           if (KIND == PISA_CACHE_BF16 && U > KT) off += (p & (U - 1)) * 128;
         } else {
-          off = -2;
+          page = -1;
         }
       }
     }
-    if (__any_sync(kFull, off == -2)) {
-      s.bad = true;
-      if (off == -2) off = -1;
-    }
+    if (__any_sync(kFull, page < 0)) s.bad = true;
   };
-  auto issue = [&](int seq, int stage) {  // the copies of the warp's tile number seq
-    const int l0 = (seq % (32 / E)) * E;
-    const uint32_t dst = ring + stage * kStage;
+  auto issue = [&](int x, uint32_t dst) {  // the copies of the warp's tile number x
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const long long o = __shfl_sync(kFull, off, l0 + e);
-      if (o < 0) continue;
-      const unsigned char* src = a.cache.pages + o;
+      const unsigned char* src = a.cache.pages + __shfl_sync(kFull, off, (x % kAhead) * E + e);
       if (KIND == PISA_CACHE_E2M1) {
         constexpr int kChunks = (U < KT ? U : KT) * kRowE2m1 / 16;
+        src += lane * 16;
+        const uint32_t d = dst + e * U * kRowE2m1 + lane * 16;
 #pragma unroll
         for (int c = 0; c < (kChunks + 31) / 32; ++c)
-          if (c * 32 + lane < kChunks) cpa16(dst + e * U * kRowE2m1 + (c * 32 + lane) * 16, src + (c * 32 + lane) * 16);
+          if ((c + 1) * 32 <= kChunks || c * 32 + lane < kChunks) cpa16(d + c * 512, src + c * 512);
       } else {
         constexpr int kRows = U < KT ? U : KT;  // rows of K (and of V) in this record
 #pragma unroll
@@ -493,63 +610,48 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
         }
       }
     }
-    cpa_commit();
   };
-  const int mine = i1 - i0 > warp ? (i1 - i0 - warp + kCaWarps - 1) / kCaWarps : 0;  // the warp's tiles
-  if (mine == 0) return;
+  float sc[KT / 8][4];
+  Weights<KIND, NP> w;
   look(0);
-  // the tiles being computed lie one look-ahead behind those being issued, so their first
-  // tokens are kept in a queue of the stages
-  int first[kCaStages];
+  issue(0, ring);
+  cpa_commit();
+  if (mine > 1) issue(1, ring + kStage);
+  cpa_commit();
+  cpa_wait<1>();
   __syncwarp();
-#pragma unroll
-  for (int x = 0; x < kCaStages - 1; ++x) {
-    if (x < mine) {
-      if (x && x % (32 / E) == 0) look(x);
-      first[x] = __shfl_sync(kFull, tok, (x % (32 / E)) * E);
-      issue(x, x);
-    } else {
-      first[x] = 0x7fffffff;
-      cpa_commit();
+  const int f0 = first_of(0);
+  products<KIND, U, NP, true, false>(ring, 0, lane, s, sc, w);
+  weigh<KIND, U, NP>(ring, f0, see, lane, s, sc, w, scratch);
+  uint32_t cur = ring, next = ring + kStage, spare = ring + 2 * kStage;
+  for (int x = 0; x + 1 < mine; ++x) {
+    if (x + 2 < mine) {
+      if ((x + 2) % kAhead == 0) look(x + 2);
+      issue(x + 2, spare);
     }
-  }
-  int stage = 0;
-  for (int x = 0; x < mine; ++x) {
-    const int nx = x + kCaStages - 1;
-    int stage_n = stage + kCaStages - 1;
-    if (stage_n >= kCaStages) stage_n -= kCaStages;
-    if (nx < mine) {
-      if (nx % (32 / E) == 0) look(nx);
-      first[kCaStages - 1] = __shfl_sync(kFull, tok, (nx % (32 / E)) * E);
-      issue(nx, stage_n);
-    } else {
-      cpa_commit();
-    }
-    cpa_wait<kCaStages - 1>();
+    cpa_commit();
+    cpa_wait<1>();  // tile x + 1 has come
     __syncwarp();
-    const int f = first[0];
-    if (f < n_hi) {
-      const uint32_t st = ring + stage * kStage;
-      if (f + KT <= n_lo) {
-        do_tile<KIND, U, false>(st, lane, s, 0, 0, 0, 0, 0, 0, [](int) { return 0; });
-      } else {
-        do_tile<KIND, U, true>(st, lane, s, n0 - f, n1 - f, t_lo, t_hi, tr0, tr1,
-                               [&](int t) { return u.n - a.T + t + 1 - f; });
-      }
-    }
-    __syncwarp();  // the stage's reads are done before it is refilled
-#pragma unroll
-    for (int y = 0; y + 1 < kCaStages; ++y) first[y] = first[y + 1];
-    stage = stage + 1 == kCaStages ? 0 : stage + 1;
+    products<KIND, U, NP, true, true>(next, cur, lane, s, sc, w);
+    weigh<KIND, U, NP>(next, first_of(x + 1), see, lane, s, sc, w, scratch);
+    __syncwarp();  // the reads of tile x are done before its stage is refilled
+    const uint32_t t = cur;
+    cur = next;
+    next = spare;
+    spare = t;
   }
+  products<KIND, U, NP, false, true>(0, cur, lane, s, sc, w);
   cpa_wait<0>();
 }
 
 // Merges the warps' partial sums; thread (row, quad) of the CTA gets four dims of the sum over
 // the warps, its row's maximum and sum.
+// (The warps' O go into the ring, which is idle then.)
 template <int KIND>
 __device__ __forceinline__ float4 merge_warps(RowState<KIND>& s, float* mo, float (*ml)[2][16], int warp, int lane,
                                               float& m, float& l) {
+  constexpr int W = Cfg<KIND>::kWarps;
+  static_assert(Cfg<KIND>::kStages * kStageBytes<KIND> >= 4096, "");
   const int g = lane >> 2, j = lane & 3;
 #pragma unroll
   for (int x = 1; x < 4; x <<= 1) {
@@ -563,6 +665,7 @@ __device__ __forceinline__ float4 merge_warps(RowState<KIND>& s, float* mo, floa
     ml[warp][1][g] = s.l0;
     ml[warp][1][g + 8] = s.l1;
   }
+  __syncthreads();  // every warp's tiles are done
   float* o = mo + warp * 1024;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -572,14 +675,14 @@ __device__ __forceinline__ float4 merge_warps(RowState<KIND>& s, float* mo, floa
       o[(g + 8) * 64 + out_dim<KIND>(i, j, e)] = s.o[i][2 + e];
     }
   __syncthreads();
-  const int row = threadIdx.x >> 4, quad = threadIdx.x & 15;
+  const int row = (threadIdx.x >> 4) & 15, quad = threadIdx.x & 15;
   m = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < kCaWarps; ++w) m = fmaxf(m, ml[w][0][row]);
+  for (int w = 0; w < W; ++w) m = fmaxf(m, ml[w][0][row]);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   l = 0.f;
 #pragma unroll
-  for (int w = 0; w < kCaWarps; ++w) {
+  for (int w = 0; w < W; ++w) {
     const float mw = ml[w][0][row], lw = ml[w][1][row];
     const float f = mw == -INFINITY ? 0.f : ex2_approx(mw - m);
     l += mw == -INFINITY ? lw : f * lw;  // (a warp without keys adds 0, or the NaN of a bad page)
@@ -638,19 +741,21 @@ __device__ __forceinline__ long long run_length(long long total, int grid) {
 }
 
 template <int KIND>
+constexpr int kRing = Cfg<KIND>::kWarps* Cfg<KIND>::kStages* kStageBytes<KIND>;
+template <int KIND>
 constexpr int attend_smem() {
-  return kCaWarps * kCaStages * Cfg<KIND>::KT * Cfg<KIND>::kRow + kCaWarps * 1024 * 4 + kCaWarps * 2 * 16 * 4;
+  return kRing<KIND> + Cfg<KIND>::kWarps * (kScratch + 2 * 16 * 4);
 }
 
-template <int KIND, int U, bool SEL>
-__global__ void __launch_bounds__(kCaWarps * 32, Cfg<KIND>::kCtasPerSm) cache_attend_kernel(CacheAttendLaunch a) {
+template <int KIND, int U, bool SEL, int NP>
+__global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_kernel(CacheAttendLaunch a) {
   using C = Cfg<KIND>;
   constexpr int KT = C::KT;
-  extern __shared__ __align__(128) unsigned char ca_smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t ring = smem_addr(ca_smem) + warp * kCaStages * KT * C::kRow;
-  float* mo = reinterpret_cast<float*>(ca_smem + kCaWarps * kCaStages * KT * C::kRow);
-  float(*ml)[2][16] = reinterpret_cast<float(*)[2][16]>(mo + kCaWarps * 1024);
+  const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (uniform to the compiler)
+  const uint32_t ring = warp * C::kStages * kStageBytes<KIND>;                        // (offset into the shared memory)
+  float* mo = reinterpret_cast<float*>(ca_smem);
+  float* scratch = reinterpret_cast<float*>(ca_smem + kRing<KIND> + warp * kScratch);
+  float(*ml)[2][16] = reinterpret_cast<float(*)[2][16]>(ca_smem + kRing<KIND> + C::kWarps * kScratch);
   const int row = threadIdx.x >> 4, quad = threadIdx.x & 15;
   RowState<KIND> s;
   Unit u;
@@ -666,12 +771,12 @@ __global__ void __launch_bounds__(kCaWarps * 32, Cfg<KIND>::kCtasPerSm) cache_at
     u.n = seq_len(a, u.b, over);
     u.sel = a.idx + (((long long)u.b * a.cache.Hkv + u.kv) * a.T + u.t_first) * a.Ksel;
     load_q<KIND>(a, u.b, u.kv, u.t_first, 0, u.rows, lane, s);
-    run_tiles<KIND, U, SEL>(a, u, 0, a.Ksel * (kC / KT), ring, warp, lane, s);
+    run_tiles<KIND, U, SEL, NP>(a, u, 0, 0, ring, scratch, warp, lane, s);
     if (threadIdx.x == 0 && over) set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
     if (lane == 0 && s.bad) set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
     float m, l;
     const float4 acc = merge_warps<KIND>(s, mo, ml, warp, lane, m, l);
-    write_out(a, u, row, quad, acc, l);
+    if (threadIdx.x < 256) write_out(a, u, row, quad, acc, l);
     return;
   }
   // the split form: this CTA's run of the stream of tiles
@@ -723,13 +828,13 @@ __global__ void __launch_bounds__(kCaWarps * 32, Cfg<KIND>::kCtasPerSm) cache_at
     u.kv = un / RT;
     u.r0 = (un % RT) * 16;
     load_q<KIND>(a, u.b, u.kv, 0, u.r0, u.rows, lane, s);
-    run_tiles<KIND, U, SEL>(a, u, i0, i1, ring, warp, lane, s);
+    run_tiles<KIND, U, SEL, NP>(a, u, i0, i1, ring, scratch, warp, lane, s);
     if (lane == 0 && s.bad) set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
     float m, l;
     const float4 acc = merge_warps<KIND>(s, mo, ml, warp, lane, m, l);
     if (i0 == 0 && i1 == nt) {
-      write_out(a, u, row, quad, acc, l);
-    } else {  // slot 0: the run's first unit, slot 1: its last
+      if (threadIdx.x < 256) write_out(a, u, row, quad, acc, l);
+    } else if (threadIdx.x < 256) {  // slot 0: the run's first unit, slot 1: its last
       float* p = a.part + ((long long)blockIdx.x * 2 + slot) * kPartFloats;
       *reinterpret_cast<float4*>(p + row * 64 + 4 * quad) = acc;
       if (quad == 0) {
@@ -816,25 +921,20 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, in
   write_out(a, u, row, quad, acc, l);
 }
 
-template <int KIND, int U, bool SEL>
+template <int KIND, int U, bool SEL, int NP>
 static cudaError_t launch_attend_t(const CacheAttendLaunch& L, cudaStream_t s) {
   using C = Cfg<KIND>;
   constexpr int smem = attend_smem<KIND>();
+  const auto kernel = cache_attend_kernel<KIND, U, SEL, NP>;
   // (the attribute belongs to the device, so it is set for each call's: a host-side cost of about 1 us)
-  cudaError_t e = cudaFuncSetAttribute(cache_attend_kernel<KIND, U, SEL>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  if (SEL) {
-    cache_attend_kernel<KIND, U, SEL>
-        <<<(unsigned)(L.cache.B * L.T * L.cache.Hkv), kCaWarps * 32, smem, s>>>(L);
-    note_launch();
-    return cudaGetLastError();
-  }
   const int RT = (L.T * L.G + 15) / 16;
-  const int grid = 152 * C::kCtasPerSm;
-  cache_attend_kernel<KIND, U, SEL><<<grid, kCaWarps * 32, smem, s>>>(L);
+  const int grid = SEL ? L.cache.B * L.T * L.cache.Hkv : kCaGrid;
+  kernel<<<(unsigned)grid, C::kWarps * 32, smem, s>>>(L);
   note_launch();
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (SEL || e != cudaSuccess) return e;
   cache_join_kernel<C::KT><<<(unsigned)(L.cache.B * L.cache.Hkv * RT * 4), 256, 0, s>>>(L, grid);
   note_launch();
   return cudaGetLastError();
@@ -842,20 +942,23 @@ static cudaError_t launch_attend_t(const CacheAttendLaunch& L, cudaStream_t s) {
 
 template <int KIND, int U>
 static cudaError_t launch_attend_u(const CacheAttendLaunch& L, cudaStream_t s) {
-  return L.idx ? launch_attend_t<KIND, U, true>(L, s) : launch_attend_t<KIND, U, false>(L, s);
+  constexpr int NP = KIND == PISA_CACHE_BF16 ? 2 : 1;  // parts of the weights (see weigh)
+  if (L.idx) return L.out_f32 ? launch_attend_t<KIND, U, true, NP + 1>(L, s) : launch_attend_t<KIND, U, true, NP>(L, s);
+  return L.out_f32 ? launch_attend_t<KIND, U, false, NP + 1>(L, s) : launch_attend_t<KIND, U, false, NP>(L, s);
+}
+
+template <int KIND>
+static cudaError_t launch_attend_k(const CacheAttendLaunch& L, cudaStream_t s) {
+  switch (L.cache.rec_shift) {
+    case 4: return launch_attend_u<KIND, 16>(L, s);
+    case 5: return launch_attend_u<KIND, 32>(L, s);
+    default: return launch_attend_u<KIND, 64>(L, s);
+  }
 }
 
 cudaError_t launch_cache_attend(const CacheAttendLaunch& L, cudaStream_t s) {
-  if (L.cache.kind == PISA_CACHE_BF16) switch (L.cache.rec_shift) {
-      case 4: return launch_attend_u<PISA_CACHE_BF16, 16>(L, s);
-      case 5: return launch_attend_u<PISA_CACHE_BF16, 32>(L, s);
-      default: return launch_attend_u<PISA_CACHE_BF16, 64>(L, s);
-    }
-  switch (L.cache.rec_shift) {
-    case 4: return launch_attend_u<PISA_CACHE_E2M1, 16>(L, s);
-    case 5: return launch_attend_u<PISA_CACHE_E2M1, 32>(L, s);
-    default: return launch_attend_u<PISA_CACHE_E2M1, 64>(L, s);
-  }
+  return L.cache.kind == PISA_CACHE_BF16 ? launch_attend_k<PISA_CACHE_BF16>(L, s)
+                                         : launch_attend_k<PISA_CACHE_E2M1>(L, s);
 }
 
 }  // namespace pisa

@@ -103,9 +103,10 @@ def tolerance(o, pv, sv, big, n, bits, out_dtype):
       2^-17: the exponential (2^-22) and the rounding of its argument (2^-24 of at most 64),
       n 2^-23: the fp32 sums over the keys;
     the weighted sum and the sum of the weights each, so twice, times sum p |v|; and the result's rounding.
-    In fp16 a weight is held times 2^14 with steps of 2^-24 at least, so it is also off by up to 2^-25 / 2^14 of
-    the largest weight, which is at most 1: 2^-39 times sum |v| (this is what is left where the keys that carry
-    the weight have a zero in some dim)."""
+    In fp16 a weight is held times 2^10, relative to a reference that is at most the largest weight, with steps of
+    2^-24 at least (the subnormal numbers), so it is also off by up to half a step: 2^-25 / 2^10 = 2^-35 of the
+    largest weight, which is at most 1.  That is 2^-35 times sum |v|, and what is left where the keys that carry the
+    weight have a zero in some dim."""
     eps = (2.0 ** -11 if bits == 4 else 2.0 ** -16) + 256 * 2.0 ** -24 * big + 2.0 ** -17 + n * 2.0 ** -23
-    pv = pv + (2.0 ** -39 / (2 * eps) * sv if bits == 4 else 0.0)
+    pv = pv + (2.0 ** -35 / (2 * eps) * sv if bits == 4 else 0.0)
     return 2 * eps * pv + torch.finfo(out_dtype).eps / 2 * (o.abs() + 2 * eps * pv)
