@@ -458,7 +458,7 @@ class PagedCache:
     """
 
     __slots__ = ("pages", "table", "page_size", "B", "Hkv", "n_pages", "max_pages", "bits", "device", "_struct",
-                 "_ref")
+                 "_ref", "_index")
 
     def __init__(self, pages: torch.Tensor, table: torch.Tensor, page_size: int, k_exp: int = 0, v_exp: int = 0):
         if page_size not in (16, 32, 64, 128, 256):
@@ -483,6 +483,7 @@ class PagedCache:
         self.n_pages, self.Hkv = pages.shape[0], pages.shape[1]
         self.B, self.max_pages = table.shape
         self.device = pages.device
+        self._index = pages.get_device()
         stride = pages.stride(0) if self.n_pages > 1 else pages[0].numel()
         self._struct = _CacheStruct(pages.data_ptr(), table.data_ptr(), stride * pages.element_size(), self.B,
                                     self.Hkv, D, page_size, self.n_pages, self.max_pages, 0 if bits == 16 else 1,
@@ -523,53 +524,57 @@ def cache_workspace(cache: PagedCache) -> torch.Tensor:
     return torch.zeros(cache_workspace_bytes(), dtype=torch.uint8, device=cache.device)
 
 
-class _On:
-    """The device and stream of a cache call: the cache's device is made current for the call, tensors allocated
-    in the call belong to the stream that it launches on."""
+# (the current stream's handle and the current device's number without the objects around them: a decoding step
+# makes these calls once a layer, and the objects cost as much as the launch)
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+_get_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
-    __slots__ = ("guard", "raw")
 
-    def __init__(self, cache: PagedCache, stream):
-        dev = cache.device
-        self.guard = None
-        if stream is not None:
-            if stream.device != dev:
-                raise ValueError("the stream must be on the cache's device")
-            self.guard = torch.cuda.stream(stream)
-        elif torch.cuda.current_device() != dev.index:
-            self.guard = torch.cuda.device(dev)
+def _on(cache: PagedCache, stream):
+    """What has to be entered so that the cache's device, and `stream` if given, are current in a call (tensors
+    that it allocates then belong to that stream); None where they are."""
+    if stream is not None:
+        if stream.device != cache.device:
+            raise ValueError("the stream must be on the cache's device")
+        return torch.cuda.stream(stream)
+    return None if _get_device() == cache._index else torch.cuda.device(cache.device)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        self.raw = torch.cuda.current_stream().cuda_stream
-        return self
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _current(cache: PagedCache) -> int:
+    return _raw_stream(cache._index) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
 
 
 def _rows(x: torch.Tensor, what: str, cache: PagedCache, B: int, T: int, H: int, written: bool = False):
-    if x.dtype != torch.bfloat16 or x.device != cache.device or tuple(x.shape) != (B, T, H, D):
+    if x.dtype is not torch.bfloat16 or x.shape != (B, T, H, D) or x.get_device() != cache._index:
         raise ValueError(f"{what} must be a bf16 tensor [{B}, {T}, {H}, {D}] on the cache's device")
     sb, st, sh, sd = x.stride()
     if sd != 1:
         raise ValueError(f"the rows of {what} must be dense")
-    if written and ((B > 1 and sb == 0) or (T > 1 and st == 0) or (H > 1 and sh == 0)):
-        raise ValueError(f"the rows of {what} must not share memory")
     # (the stride of a dimension of one entry is never used and may be anything)
-    return ctypes.byref(_RowsStruct(x.data_ptr(), sb if B > 1 else 0, st if T > 1 else 0, sh if H > 1 else 0))
+    if B == 1:
+        sb = 0
+    elif written and sb == 0:
+        raise ValueError(f"the rows of {what} must not share memory")
+    if T == 1:
+        st = 0
+    elif written and st == 0:
+        raise ValueError(f"the rows of {what} must not share memory")
+    if H == 1:
+        sh = 0
+    elif written and sh == 0:
+        raise ValueError(f"the rows of {what} must not share memory")
+    return ctypes.byref(_RowsStruct(x.data_ptr(), sb, st, sh))
 
 
 def _per_sequence(x: torch.Tensor, what: str, cache: PagedCache) -> int:
-    if x.dtype != torch.int32 or x.device != cache.device or x.shape != (cache.B,) or not x.is_contiguous():
+    if (x.dtype is not torch.int32 or x.shape != (cache.B,) or x.get_device() != cache._index
+            or not x.is_contiguous()):
         raise ValueError(f"{what} must be a contiguous int32 tensor [{cache.B}] on the cache's device")
     return x.data_ptr()
 
 
-def _cache_ws(workspace: torch.Tensor | None, cache: PagedCache, need: int) -> int:
-    if workspace.device != cache.device or not workspace.is_contiguous() or workspace.dtype != torch.uint8:
+def _cache_ws(workspace: torch.Tensor, cache: PagedCache, need: int) -> int:
+    if workspace.dtype is not torch.uint8 or workspace.get_device() != cache._index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the cache's device")
     if workspace.numel() < need:
         raise PisaError(3, "workspace")
@@ -589,39 +594,41 @@ def cache_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache
     and keys, allocated here when not given (rows t >= counts[b] are then not written); q_out may be q and
     k_out may be k.  workspace: for the status word only, may be None.
     """
+    guard = _on(cache, stream)
+    if guard is not None:
+        with guard:
+            return cache_append(q, k, v, cache, start, rotary, counts, interleaved, q_out, k_out, workspace)
     if k.dim() != 4:
         raise ValueError("k must be a bf16 tensor [B, T, Hkv, 64]")
     B, T, Hkv = cache.B, k.shape[1], cache.Hkv
     ks, vs = _rows(k, "k", cache, B, T, Hkv), _rows(v, "v", cache, B, T, Hkv)
-    Hq, qs = 0, None
+    Hq, qs, qo = 0, None, None
     if q is not None:
         if q.dim() != 4:
             raise ValueError("q must be a bf16 tensor [B, T, Hq, 64]")
         Hq = q.shape[2]
         qs = _rows(q, "q", cache, B, T, Hq)
+        if q_out is None:
+            q_out = torch.empty(B, T, Hq, D, dtype=torch.bfloat16, device=cache.device)
+        qo = _rows(q_out, "q_out", cache, B, T, Hq, True)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    n_rot = rot = 0
+    if k_out is None:
+        k_out = torch.empty(B, T, Hkv, D, dtype=torch.bfloat16, device=cache.device)
+    n_rot, rot, rp = 0, 0, None
     if rotary is not None:
-        if (rotary.dtype != torch.float32 or rotary.dim() != 2 or rotary.device != cache.device
+        if (rotary.dtype is not torch.float32 or rotary.dim() != 2 or rotary.get_device() != cache._index
                 or not rotary.is_contiguous()):
             raise ValueError("rotary must be a contiguous fp32 tensor [n, rot] on the cache's device")
         n_rot, rot = rotary.shape
         if rot not in (16, 32, 48, 64):
             raise ValueError("rotary must be [n, rot] with rot 16, 32, 48 or 64")
-    sp = _per_sequence(start, "start", cache)
-    cp = _per_sequence(counts, "counts", cache) if counts is not None else None
-    wp = _cache_ws(workspace, cache, 4) if workspace is not None else None
-    with _On(cache, stream) as on:
-        if q is not None and q_out is None:
-            q_out = torch.empty(B, T, Hq, D, dtype=torch.bfloat16, device=cache.device)
-        if k_out is None:
-            k_out = torch.empty(B, T, Hkv, D, dtype=torch.bfloat16, device=cache.device)
-        qo = _rows(q_out, "q_out", cache, B, T, Hq, True) if q is not None else None
-        ko = _rows(k_out, "k_out", cache, B, T, Hkv, True)
-        _check(load().pisa_cache_append(cache._ref, T, qs, Hq, ks, vs, sp, cp,
-                                        rotary.data_ptr() if rot else None, n_rot, rot, int(interleaved), qo, ko, wp,
-                                        on.raw), "pisa_cache_append")
+        rp = rotary.data_ptr()
+    _check((_lib or load()).pisa_cache_append(
+        cache._ref, T, qs, Hq, ks, vs, _per_sequence(start, "start", cache),
+        None if counts is None else _per_sequence(counts, "counts", cache), rp, n_rot, rot, 1 if interleaved else 0,
+        qo, _rows(k_out, "k_out", cache, B, T, Hkv, True),
+        None if workspace is None else _cache_ws(workspace, cache, 4), _current(cache)), "pisa_cache_append")
     return q_out, k_out
 
 
@@ -630,19 +637,22 @@ def cache_read(cache: PagedCache, start: torch.Tensor, T: int, counts: torch.Ten
                workspace: torch.Tensor | None = None, stream=None):
     """Cached tokens start[b] .. start[b] + counts[b] - 1 (T where counts is None) as dense bf16 (k, v)
     [B, T, Hkv, 64], exactly; allocated here when not given (rows t >= counts[b] are not written)."""
+    guard = _on(cache, stream)
+    if guard is not None:
+        with guard:
+            return cache_read(cache, start, T, counts, k_out, v_out, workspace)
     B, Hkv = cache.B, cache.Hkv
-    sp = _per_sequence(start, "start", cache)
-    cp = _per_sequence(counts, "counts", cache) if counts is not None else None
-    wp = _cache_ws(workspace, cache, 4) if workspace is not None else None
     if T < 1:
         raise ValueError("T must be at least 1")
-    with _On(cache, stream) as on:
-        if k_out is None:
-            k_out = torch.empty(B, T, Hkv, D, dtype=torch.bfloat16, device=cache.device)
-        if v_out is None:
-            v_out = torch.empty(B, T, Hkv, D, dtype=torch.bfloat16, device=cache.device)
-        _check(load().pisa_cache_read(cache._ref, T, sp, cp, _rows(k_out, "k_out", cache, B, T, Hkv, True),
-                                      _rows(v_out, "v_out", cache, B, T, Hkv, True), wp, on.raw), "pisa_cache_read")
+    if k_out is None:
+        k_out = torch.empty(B, T, Hkv, D, dtype=torch.bfloat16, device=cache.device)
+    if v_out is None:
+        v_out = torch.empty(B, T, Hkv, D, dtype=torch.bfloat16, device=cache.device)
+    _check((_lib or load()).pisa_cache_read(
+        cache._ref, T, _per_sequence(start, "start", cache),
+        None if counts is None else _per_sequence(counts, "counts", cache),
+        _rows(k_out, "k_out", cache, B, T, Hkv, True), _rows(v_out, "v_out", cache, B, T, Hkv, True),
+        None if workspace is None else _cache_ws(workspace, cache, 4), _current(cache)), "pisa_cache_read")
     return k_out, v_out
 
 
@@ -656,33 +666,34 @@ def cache_attention(q: torch.Tensor, cache: PagedCache, lengths: torch.Tensor, i
     1, as decode_append_and_select returns it): blocks of 64 tokens, -1 skipped.  out [B, T, Hq, 64], bf16
     (allocated here when not given) or fp32.
     """
+    guard = _on(cache, stream)
+    if guard is not None:
+        with guard:
+            return cache_attention(q, cache, lengths, idx, out, workspace)
     if q.dim() != 4:
         raise ValueError("q must be a bf16 tensor [B, T, Hq, 64]")
     B, T, Hkv, Hq = cache.B, q.shape[1], cache.Hkv, q.shape[2]
-    qs = _rows(q, "q", cache, B, T, Hq)
-    lp = _per_sequence(lengths, "lengths", cache)
     Ksel, ip = 0, None
     if idx is not None:
         Ksel = idx.shape[-1]
-        if idx.dtype != torch.int32 or idx.device != cache.device or not idx.is_contiguous() or not (
-                tuple(idx.shape) == (B, Hkv, T, Ksel) or (T == 1 and tuple(idx.shape) == (B, Hkv, Ksel))):
-            raise ValueError(f"idx must be a contiguous int32 tensor [{B}, {Hkv}, {T}, Ksel] on the cache's device")
-        if Ksel < 1:
-            raise ValueError("idx lists no blocks")
+        if (idx.dtype is not torch.int32 or idx.get_device() != cache._index or not idx.is_contiguous() or Ksel < 1
+                or not (idx.shape == (B, Hkv, T, Ksel) or (T == 1 and idx.shape == (B, Hkv, Ksel)))):
+            raise ValueError(f"idx must be a contiguous int32 tensor [{B}, {Hkv}, {T}, Ksel], Ksel at least 1, on the "
+                             "cache's device")
         ip = idx.data_ptr()
-    lib = load()
+    if out is None:
+        out = torch.empty(B, T, Hq, D, dtype=torch.bfloat16, device=cache.device)
+    elif ((out.dtype is not torch.bfloat16 and out.dtype is not torch.float32) or out.get_device() != cache._index
+          or out.shape != (B, T, Hq, D) or not out.is_contiguous()):
+        raise ValueError(f"out must be a contiguous bf16 or fp32 tensor [{B}, {T}, {Hq}, {D}]")
+    lib = _lib or load()
     need = lib.pisa_cache_workspace_bytes()
-    with _On(cache, stream) as on:
-        if out is None:
-            out = torch.empty(B, T, Hq, D, dtype=torch.bfloat16, device=cache.device)
-        elif (out.dtype not in (torch.bfloat16, torch.float32) or out.device != cache.device
-              or tuple(out.shape) != (B, T, Hq, D) or not out.is_contiguous()):
-            raise ValueError(f"out must be a contiguous bf16 or fp32 tensor [{B}, {T}, {Hq}, {D}]")
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
-        _check(lib.pisa_cache_attention(cache._ref, qs, T, Hq, lp, ip, Ksel, out.data_ptr(),
-                                        int(out.dtype == torch.float32), _cache_ws(workspace, cache, need), need,
-                                        on.raw), "pisa_cache_attention")
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
+    _check(lib.pisa_cache_attention(cache._ref, _rows(q, "q", cache, B, T, Hq), T, Hq,
+                                    _per_sequence(lengths, "lengths", cache), ip, Ksel, out.data_ptr(),
+                                    1 if out.dtype is torch.float32 else 0, _cache_ws(workspace, cache, need), need,
+                                    _current(cache)), "pisa_cache_attention")
     return out
 
 

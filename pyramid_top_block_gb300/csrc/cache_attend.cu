@@ -14,7 +14,7 @@
 // Without a list the tiles of all (sequence, KV head, row tile) units form one stream, which
 // is cut into equal runs, one per CTA, whatever the lengths; a unit that ends up in several
 // CTAs is joined by a second kernel from 32-bit partial results.
-#include <mutex>
+#include <atomic>
 
 #include "cache.cuh"
 #include "tc.cuh"
@@ -926,9 +926,17 @@ static cudaError_t launch_attend_t(const CacheAttendLaunch& L, cudaStream_t s) {
   using C = Cfg<KIND>;
   constexpr int smem = attend_smem<KIND>();
   const auto kernel = cache_attend_kernel<KIND, U, SEL, NP>;
-  // (the attribute belongs to the device, so it is set for each call's: a host-side cost of about 1 us)
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the attribute belongs to the device: set once on each of the first 64 (on others at every call)
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (!(done.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_release);
+  }
   const int RT = (L.T * L.G + 15) / 16;
   const int grid = SEL ? L.cache.B * L.T * L.cache.Hkv : kCaGrid;
   kernel<<<(unsigned)grid, C::kWarps * 32, smem, s>>>(L);
