@@ -13,6 +13,8 @@
 // and one for V.  code * scale has six significant bits, so it is exact in fp16 and bf16.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -116,12 +118,51 @@ struct CacheAttendLaunch {
   void* out;
   int out_f32;
   int* status;
-  float* part;  // partial results (see cache_attend.cu)
+  float* part;  // partial results (see cache_attend.cuh)
 };
+
+// The launch is programmatic: a kernel may start while the one before it in the stream ends,
+// and touches memory only after this.
+__device__ __forceinline__ void after_the_one_before() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Launches a kernel that may start while the one before it in the stream ends.
+template <auto kernel, typename... Args>
+static cudaError_t launch_early(dim3 grid, int threads, int smem, cudaStream_t s, Args... args) {
+  if (smem > 48 * 1024) {
+    // the attribute belongs to the device: set once on each of the first 64 (on others at every call)
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (!(done.load(std::memory_order_acquire) & bit)) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+      done.fetch_or(bit, std::memory_order_release);
+    }
+  }
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
 
 cudaError_t launch_cache_append(const CacheAppendLaunch& L, cudaStream_t s);
 cudaError_t launch_cache_read(const CacheReadLaunch& L, cudaStream_t s);
-cudaError_t launch_cache_attend(const CacheAttendLaunch& L, cudaStream_t s);
+cudaError_t launch_cache_attend_bf16(const CacheAttendLaunch& L, cudaStream_t s);
+cudaError_t launch_cache_attend_e2m1(const CacheAttendLaunch& L, cudaStream_t s);
 size_t cache_part_bytes();
 
 }  // namespace pisa

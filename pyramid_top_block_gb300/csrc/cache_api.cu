@@ -91,9 +91,8 @@ int pisa_cache_append(const pisa_paged_cache* cache, int T, const pisa_rows* q, 
   if (rot && (!rotary || !aligned(rotary, 16) || n_rot < 1)) return PISA_ERR_INVALID_ARG;
   if (with_q && !group_ok(Hq, cache->Hkv)) return PISA_ERR_UNSUPPORTED;
   if (!aligned(start, 4) || !aligned(counts, 4) || !aligned(ws, 4)) return PISA_ERR_INVALID_ARG;
-  // 32-bit job numbers: 16 rows of a token each
-  if ((long long)cache->B * T * (((with_q ? Hq : 0) + 2 * cache->Hkv + 15) / 16) >= (1LL << 31))
-    return PISA_ERR_UNSUPPORTED;
+  // 32-bit job numbers: at most one for four rows of a token
+  if ((long long)T * (((with_q ? Hq : 0) + 2 * cache->Hkv + 7) / 4) >= (1LL << 31) - 1024) return PISA_ERR_UNSUPPORTED;
   L.T = T;
   L.Hq = Hq;
   L.start = start;
@@ -115,7 +114,7 @@ int pisa_cache_read(const pisa_paged_cache* cache, int T, const int32_t* start, 
   if ((st = check_rows(k_out, true, L.k_out)) || (st = check_rows(v_out, true, L.v_out))) return st;
   if (!L.k_out.data && !L.v_out.data) return PISA_ERR_INVALID_ARG;
   if (!aligned(start, 4) || !aligned(counts, 4) || !aligned(ws, 4)) return PISA_ERR_INVALID_ARG;
-  if ((long long)cache->B * cache->Hkv * (T / 4 + 1LL) >= (1LL << 31)) return PISA_ERR_UNSUPPORTED;  // 32-bit job numbers
+  if (T >= (1 << 30)) return PISA_ERR_UNSUPPORTED;  // 32-bit token numbers
   L.T = T;
   L.start = start;
   L.counts = counts;
@@ -146,7 +145,8 @@ int pisa_cache_attention(const pisa_paged_cache* cache, const pisa_rows* q, int 
   L.out_f32 = out_f32 != 0;
   L.status = static_cast<int*>(ws);
   L.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kCacheStatusBytes);
-  return cuda_code(launch_cache_attend(L, static_cast<cudaStream_t>(stream)));
+  const auto launch = cache->kind == PISA_CACHE_BF16 ? launch_cache_attend_bf16 : launch_cache_attend_e2m1;
+  return cuda_code(launch(L, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -12,28 +12,49 @@
 
 namespace pisa {
 
-constexpr int kAppWarps = 8;
-constexpr int kAppIter = 4;  // groups of four rows a warp takes at most, their loads issued together
+constexpr int kAppWarps = 4;
+constexpr int kAppBatch = 2;  // groups of four rows whose loads a warp issues together, ahead of their use
 
-// Two rotated elements x c + p s (p the pair's other member, s signed), as the bf16 values
-// that the 64-bit sum rounds to (by way of 32 bits).  In 32 bits the sum is off by at most
-// (|p s| + |r|) 2^-24 (and 2^-149 among the subnormal); where every value within twice that
-// rounds to the same bf16 that is the answer, else the sum is taken in 64 bits (both
-// products are exact there).  So a key has the same bits however it was appended, which
-// matters where it is quantised next.
-__device__ __forceinline__ uint32_t rotate2(float x0, float p0, float c0, float s0, float x1, float p1, float c1,
-                                            float s1) {
-  const float m0 = p0 * s0, m1 = p1 * s1;
-  const float r0 = fmaf(x0, c0, m0), r1 = fmaf(x1, c1, m1);
-  const float e0 = fmaf(fabsf(m0) + fabsf(r0), 0x1p-23f, 0x1p-147f);
-  const float e1 = fmaf(fabsf(m1) + fabsf(r1), 0x1p-23f, 0x1p-147f);
-  uint32_t lo = pack_bf16x2(r0 - e0, r1 - e1);
-  if (lo != pack_bf16x2(r0 + e0, r1 + e1)) {
-    const double d0 = (double)x0 * (double)c0 + (double)p0 * (double)s0;
-    const double d1 = (double)x1 * (double)c1 + (double)p1 * (double)s1;
-    lo = pack_bf16x2((float)d0, (float)d1);
+// x c + p s rounded to 32 bits from (nearly) twice as many: both products and their sum as
+// unevaluated pairs (the error of a product by fma, that of a sum by Knuth's two-sum).
+__device__ __forceinline__ float sum2(float x, float c, float p, float s) {
+  const float h1 = x * c, h2 = p * s;
+  const float l1 = fmaf(x, c, -h1), l2 = fmaf(p, s, -h2);
+  const float h = h1 + h2, z = h - h1;
+  const float l = (h1 - (h - z)) + (h2 - z) + (l1 + l2);
+  return fabsf(h) < INFINITY ? h + l : h;  // (an infinity has no error term)
+}
+
+// Eight rotated elements x c + p s (p the pair's other member, s signed), as the bf16 values
+// that the exact sum rounds to (by way of 32 bits).  In 32 bits the sum r is off by at most
+// (|p s| + |r|) 2^-24 (results below 2^-100 aside); where every value within twice that rounds to the same bf16 that is
+// the answer, else (one element in some thousands) the sums are taken with their errors.
+// So a key has the same bits however it was appended, which matters where it is quantised
+// next.  (64-bit arithmetic in that rare branch cost half of the kernel's time: the compiler
+// hoists the conversions, and the 64-bit pipe is slow.)
+__device__ __forceinline__ void rotate8(uint32_t (&w)[4], const uint32_t (&o)[4], const float (&c)[8],
+                                        const float (&s)[8]) {
+  uint32_t lo[4];
+  bool same = true;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float x0 = __uint_as_float(w[k] << 16), x1 = __uint_as_float(w[k] & 0xffff0000u);
+    const float p0 = __uint_as_float(o[k] << 16), p1 = __uint_as_float(o[k] & 0xffff0000u);
+    const float m0 = p0 * s[2 * k], m1 = p1 * s[2 * k + 1];
+    const float r0 = fmaf(x0, c[2 * k], m0), r1 = fmaf(x1, c[2 * k + 1], m1);
+    const float e0 = (fabsf(m0) + fabsf(r0)) * 0x1p-23f, e1 = (fabsf(m1) + fabsf(r1)) * 0x1p-23f;
+    lo[k] = pack_bf16x2(r0 - e0, r1 - e1);
+    same = same && lo[k] == pack_bf16x2(r0 + e0, r1 + e1);
   }
-  return lo;
+  if (!same) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      lo[k] = pack_bf16x2(sum2(__uint_as_float(w[k] << 16), c[2 * k], __uint_as_float(o[k] << 16), s[2 * k]),
+                          sum2(__uint_as_float(w[k] & 0xffff0000u), c[2 * k + 1],
+                               __uint_as_float(o[k] & 0xffff0000u), s[2 * k + 1]));
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = lo[k];
 }
 
 // The 4-bit form of a row: this lane's 8 of 64 values (bf16 pairs w) and, with the
@@ -73,116 +94,153 @@ __device__ __forceinline__ void quantise8(const uint32_t (&w)[4], int exp, uint3
   }
 }
 
-template <int KIND>
-__global__ void __launch_bounds__(kAppWarps * 32) cache_append_kernel(CacheAppendLaunch a, int parts, int per) {
-  const int lane = threadIdx.x & 31, sub = lane >> 3, c = lane & 7;
-  const unsigned job = blockIdx.x * kAppWarps + (threadIdx.x >> 5);
-  const unsigned tok = job / parts, part = job % parts;
-  if (tok >= (unsigned)a.cache.B * a.T) return;
-  const int b = tok / a.T, t = tok % a.T;
-  const int Hkv = a.cache.Hkv, Hq = a.q.data ? a.Hq : 0;
-  const int rows = Hq + 2 * Hkv, r0 = part * per * 4 + sub;
-  const long long p = (long long)a.start[b] + t;
-  const bool counted = a.counts == nullptr || t < a.counts[b];
-  // the rows of this warp (their addresses do not depend on the position)
-  uint4 x[kAppIter];
+// The rotation of this lane's 8 dims at one position.
+struct Turn {
+  float c[8], s[8];  // cosines and signed sines
+  int from;          // lane that holds the pairs' other members (split halves)
+  bool on;           // whether the dims turn at all
+};
+
+template <bool INTER>
+__device__ __forceinline__ void load_turn(const CacheAppendLaunch& a, long long p, int lane, Turn& t) {
+  const int c = lane & 7;
+  const int half = a.rot >> 4;  // lanes of one half of the rotated dims (split-halves order)
+  t.on = c < 2 * half;
+  t.from = lane;
 #pragma unroll
-  for (int i = 0; i < kAppIter; ++i) {
-    const int r = r0 + 4 * i;
-    if (i < per && r < rows) {
-      const RowsDev& src = r < Hq ? a.q : r < Hq + Hkv ? a.k : a.v;
-      const int h = r < Hq ? r : r < Hq + Hkv ? r - Hq : r - Hq - Hkv;
-      x[i] = *reinterpret_cast<const uint4*>(src.data + b * src.sb + t * src.st + h * src.sh + 8 * c);
-    } else {
-      x[i] = make_uint4(0, 0, 0, 0);
+  for (int e = 0; e < 8; ++e) {
+    t.c[e] = 1.f;
+    t.s[e] = 0.f;
+  }
+  if (!t.on) return;
+  const float* row = a.rotary + p * a.rot;
+  if (INTER) {
+    const float4 u = __ldg(reinterpret_cast<const float4*>(row + 4 * c));
+    const float4 v = __ldg(reinterpret_cast<const float4*>(row + (a.rot >> 1) + 4 * c));
+    const float uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      t.c[e] = uu[e >> 1];
+      t.s[e] = (e & 1) ? vv[e >> 1] : -vv[e >> 1];
+    }
+  } else {
+    const bool low = c < half;
+    t.from = low ? lane + half : lane - half;
+    const float4* u = reinterpret_cast<const float4*>(row + 8 * (low ? c : c - half));
+    const float4* v = reinterpret_cast<const float4*>(row + (a.rot >> 1) + 8 * (low ? c : c - half));
+    const float4 u0 = __ldg(u), u1 = __ldg(u + 1), v0 = __ldg(v), v1 = __ldg(v + 1);
+    const float uu[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+    const float vv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      t.c[e] = uu[e];
+      t.s[e] = low ? -vv[e] : vv[e];
     }
   }
-  if (!counted) return;
+}
+
+// (Lanes that do not turn compute as well and keep their words: cheaper than a branch.)
+template <bool INTER>
+__device__ __forceinline__ void turn_row(const Turn& t, bool rotate, uint32_t (&w)[4]) {
+  uint32_t o[4], y[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    o[k] = INTER ? __byte_perm(w[k], 0, 0x1032) : __shfl_sync(kFull, w[k], t.from);
+    y[k] = w[k];
+  }
+  rotate8(y, o, t.c, t.s);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = t.on && rotate ? y[k] : w[k];
+}
+
+// A warp takes every parts-th group of four rows of one token: the groups of its query rows,
+// then those of its key and value rows (keys first).
+template <int KIND, bool INTER>
+__global__ void __launch_bounds__(kAppWarps * 32, 6) cache_append_kernel(CacheAppendLaunch a, int parts) {
+  after_the_one_before();
+  const int lane = threadIdx.x & 31, sub = lane >> 3, c = lane & 7;
+  const int job = blockIdx.x * kAppWarps + __shfl_sync(kFull, threadIdx.x >> 5, 0);  // (token, part)
+  const int t = job / parts, part = job - t * parts, b = blockIdx.z;
+  if (t >= a.T) return;
+  const int Hkv = a.cache.Hkv, Hq = a.q.data ? a.Hq : 0;
+  const int gq = (Hq + 3) >> 2, groups = gq + ((2 * Hkv + 3) >> 2);
+  // the rows this lane has a part in: query row 4 i + sub of group i, row 4 (i - gq) + sub of
+  // keys and values
+  const __nv_bfloat16* qs = a.q.data + b * a.q.sb + t * a.q.st + (4 * part + sub) * a.q.sh + 8 * c;
+  const long long step = 4 * parts * a.q.sh;
+  uint4 x[kAppBatch];
+#pragma unroll
+  for (int n = 0; n < kAppBatch; ++n) {  // (these loads do not wait for the position)
+    x[n] = make_uint4(0, 0, 0, 0);
+    if (4 * (part + n * parts) + sub < Hq) x[n] = *reinterpret_cast<const uint4*>(qs + n * step);
+  }
+  int ikv = part - gq;
+  if (ikv < 0) ikv += (-ikv + parts - 1) / parts * parts;
+  auto fetch_kv = [&](int i) {
+    const int r = 4 * i + sub;
+    const RowsDev& src = r < Hkv ? a.k : a.v;
+    const int kv = r < Hkv ? r : r - Hkv;
+    uint4 z = make_uint4(0, 0, 0, 0);
+    if (r < 2 * Hkv) z = *reinterpret_cast<const uint4*>(src.data + b * src.sb + t * src.st + kv * src.sh + 8 * c);
+    return z;
+  };
+  uint4 xkv = fetch_kv(ikv);
+  const int count = a.counts ? a.counts[b] : a.T;
+  const long long p = (long long)a.start[b] + t;
+  if (t >= count) return;
   const long long cap = (long long)a.cache.max_pages << a.cache.page_shift;
   bool ok = p >= 0 && p < cap && (a.rot == 0 || p < a.n_rot);
   int page = -1;
+  Turn turn;
   if (ok) {
-    page = a.cache.table[(long long)b * a.cache.max_pages + (p >> a.cache.page_shift)];
+    page = __ldg(a.cache.table + (long long)b * a.cache.max_pages + (p >> a.cache.page_shift));
+    load_turn<INTER>(a, p, lane, turn);
     ok = page >= 0 && page < a.cache.n_pages;
   }
   if (!ok) {  // the token is left out
     if (lane == 0) set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
     return;
   }
-  // this lane's cosines and signed sines, for pairs of elements (8 c + e, its partner)
-  const int half = a.rot >> 4;  // lanes of one half of the rotated dims (split-halves order)
-  const bool turned = c < 2 * half;
-  float cs[8], sn[8];
-  int from = lane;  // lane of the partner elements
+  __nv_bfloat16* qd = a.q_out.data + b * a.q_out.sb + t * a.q_out.st + sub * a.q_out.sh + 8 * c;
+  const long long step_out = 4 * parts * a.q_out.sh;
+  qd += (long long)(4 * part) * a.q_out.sh;
+  for (int i = part; i < gq; i += kAppBatch * parts) {
+    uint4 next[kAppBatch];
+    qs += kAppBatch * step;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    cs[e] = 1.f;
-    sn[e] = 0.f;
-  }
-  if (turned) {
-    const float* row = a.rotary + p * a.rot;
-    if (a.interleaved) {
-      const float4 u = *reinterpret_cast<const float4*>(row + 4 * c);
-      const float4 v = *reinterpret_cast<const float4*>(row + (a.rot >> 1) + 4 * c);
-      const float uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+    for (int n = 0; n < kAppBatch; ++n) {
+      next[n] = make_uint4(0, 0, 0, 0);
+      if (4 * (i + (kAppBatch + n) * parts) + sub < Hq) next[n] = *reinterpret_cast<const uint4*>(qs + n * step);
+    }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        cs[e] = uu[e >> 1];
-        sn[e] = (e & 1) ? vv[e >> 1] : -vv[e >> 1];
-      }
-    } else {
-      const bool low = c < half;
-      from = low ? lane + half : lane - half;
-      const float4* u = reinterpret_cast<const float4*>(row + 8 * (low ? c : c - half));
-      const float4* v = reinterpret_cast<const float4*>(row + (a.rot >> 1) + 8 * (low ? c : c - half));
-      const float4 u0 = u[0], u1 = u[1], v0 = v[0], v1 = v[1];
-      const float uu[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
-      const float vv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        cs[e] = uu[e];
-        sn[e] = low ? -vv[e] : vv[e];
-      }
+    for (int n = 0; n < kAppBatch; ++n) {
+      uint32_t w[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+      turn_row<INTER>(turn, true, w);
+      if (4 * (i + n * parts) + sub < Hq) *reinterpret_cast<uint4*>(qd) = make_uint4(w[0], w[1], w[2], w[3]);
+      qd += step_out;
+      x[n] = next[n];
     }
   }
   const int U = 1 << a.cache.rec_shift, u = (int)(p & (U - 1));
-#pragma unroll
-  for (int i = 0; i < kAppIter; ++i) {
-    if (i >= per) break;
-    const int r = r0 + 4 * i;
-    uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, o[4];
-    if (a.interleaved) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[k] = (w[k] >> 16) | (w[k] << 16);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[k] = __shfl_sync(kFull, w[k], from);
-    }
-    const bool is_v = r >= Hq + Hkv;
-    if (turned && !is_v) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        w[k] = rotate2(__uint_as_float(w[k] << 16), __uint_as_float(o[k] << 16), cs[2 * k], sn[2 * k],
-                       __uint_as_float(w[k] & 0xffff0000u), __uint_as_float(o[k] & 0xffff0000u), cs[2 * k + 1],
-                       sn[2 * k + 1]);
-    }
+  for (int i = ikv; i < groups - gq; i += parts) {
+    const int r = 4 * i + sub;
+    const bool is_v = r >= Hkv, there = r < 2 * Hkv;
+    const int kv = is_v ? r - Hkv : r;
+    uint32_t w[4] = {xkv.x, xkv.y, xkv.z, xkv.w};
+    xkv = fetch_kv(i + parts);
+    turn_row<INTER>(turn, !is_v, w);
     const uint4 y = make_uint4(w[0], w[1], w[2], w[3]);
-    if (r < Hq) {
-      if (a.q_out.data)
-        *reinterpret_cast<uint4*>(a.q_out.data + b * a.q_out.sb + t * a.q_out.st + r * a.q_out.sh + 8 * c) = y;
-    } else if (r < Hq + Hkv && a.k_out.data) {
-      *reinterpret_cast<uint4*>(a.k_out.data + b * a.k_out.sb + t * a.k_out.st + (r - Hq) * a.k_out.sh + 8 * c) = y;
-    }
-    const int kv = is_v ? r - Hq - Hkv : r - Hq;
+    if (!is_v && a.k_out.data)
+      *reinterpret_cast<uint4*>(a.k_out.data + b * a.k_out.sb + t * a.k_out.st + kv * a.k_out.sh + 8 * c) = y;
     if (KIND == PISA_CACHE_BF16) {
-      if (r >= Hq && r < rows) {
+      if (there) {
         unsigned char* rec = a.cache.pages + cache_record(a.cache, kRowBf16, page, kv, p) + (is_v ? U * 128 : 0);
         *reinterpret_cast<uint4*>(rec + u * 128 + 16 * c) = y;
       }
-    } else if (__any_sync(kFull, r >= Hq && r < rows)) {
+    } else {
       uint32_t codes, scale;
       quantise8(w, is_v ? a.cache.v_exp : a.cache.k_exp, codes, scale);
-      if (r >= Hq && r < rows) {
+      if (there) {
         unsigned char* rec = a.cache.pages + cache_record(a.cache, kRowE2m1, page, kv, p) + (is_v ? U * 36 : 0);
         *reinterpret_cast<uint32_t*>(rec + u * 32 + 4 * c) = codes;
         if (!(c & 1)) rec[U * 32 + u * 4 + (c >> 1)] = (unsigned char)scale;
@@ -191,80 +249,113 @@ __global__ void __launch_bounds__(kAppWarps * 32) cache_append_kernel(CacheAppen
   }
 }
 
-// One thread per 8 dims of one token's K and V of one head; tokens run fastest over groups of
-// eight lanes, as they lie in a record.
+// A warp reads kReadBatch groups of four tokens of one head, eight lanes a token.
+constexpr int kReadBatch = 2;
+
 template <int KIND>
-__global__ void __launch_bounds__(256) cache_read_kernel(CacheReadLaunch a, int tok_groups) {
-  const int lane = threadIdx.x & 31, c = lane & 7;
-  const unsigned job = blockIdx.x * 8 + (threadIdx.x >> 5);  // (b, group of 4 tokens, kv), kv fastest
-  const int Hkv = a.cache.Hkv;
-  const unsigned kv = job % Hkv, bg = job / Hkv;
-  const unsigned b = bg / tok_groups;
-  const int t = (int)(bg % tok_groups) * 4 + (lane >> 3);
-  if (b >= (unsigned)a.cache.B || t >= a.T) return;
-  if (a.counts && t >= a.counts[b]) return;
-  const long long p = (long long)a.start[b] + t;
-  const long long cap = (long long)a.cache.max_pages << a.cache.page_shift;
-  int page = -1;
-  if (p >= 0 && p < cap) page = a.cache.table[(long long)b * a.cache.max_pages + (p >> a.cache.page_shift)];
-  if (page < 0 || page >= a.cache.n_pages) {
-    if (c == 0) set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
-    return;
-  }
-  const int U = 1 << a.cache.rec_shift, u = (int)(p & (U - 1));
-  uint4 y[2];
-  if (KIND == PISA_CACHE_BF16) {
-    const unsigned char* rec = a.cache.pages + cache_record(a.cache, kRowBf16, page, kv, p) + u * 128 + 16 * c;
-    y[0] = *reinterpret_cast<const uint4*>(rec);
-    y[1] = *reinterpret_cast<const uint4*>(rec + U * 128);
-  } else {
-    const unsigned char* rec = a.cache.pages + cache_record(a.cache, kRowE2m1, page, kv, p);
+__global__ void __launch_bounds__(256) cache_read_kernel(CacheReadLaunch a) {
+  after_the_one_before();
+  const int lane = threadIdx.x & 31, c = lane & 7, b = blockIdx.z, kv = blockIdx.y;
+  const int t0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * (4 * kReadBatch) + (lane >> 3);
+  const int n = a.counts ? min(a.T, a.counts[b]) : a.T;
+  const long long first = a.start[b], cap = (long long)a.cache.max_pages << a.cache.page_shift;
+  const int32_t* table = a.cache.table + (long long)b * a.cache.max_pages;
+  const int U = 1 << a.cache.rec_shift;
+  constexpr int kRow = KIND == PISA_CACHE_BF16 ? kRowBf16 : kRowE2m1;
+  const unsigned char* rec[kReadBatch];
+  bool ok[kReadBatch];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(rec + i * 36 * U + u * 32 + 4 * c);
-      const uint32_t s = e4m3x2(rec[i * 36 * U + 32 * U + u * 4 + (c >> 1)]);
-      const float f = __low2float(*reinterpret_cast<const __half2*>(&s)) * exp2i(i ? a.cache.v_exp : a.cache.k_exp);
-      uint32_t d[4], o[4];
-      e2m1x8(w, d);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&d[k]));
-        o[k] = pack_bf16x2(v.x * f, v.y * f);
+  for (int i = 0; i < kReadBatch; ++i) {
+    const int t = t0 + 4 * i;
+    const long long p = first + t;
+    int page = 0;
+    ok[i] = t < n;
+    if (ok[i]) {
+      page = p >= 0 && p < cap ? __ldg(table + (p >> a.cache.page_shift)) : -1;
+      if (page < 0 || page >= a.cache.n_pages) {
+        if (c == 0) set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
+        ok[i] = false;
+        page = 0;
       }
-      y[i] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    // (in bounds whether ok or not: the row of p's remainder in page 0)
+    const int u = (int)(p & (U - 1));
+    rec[i] = a.cache.pages + cache_record(a.cache, kRow, page, kv, p) + u * (KIND == PISA_CACHE_BF16 ? 128 : 32);
+  }
+  if (KIND == PISA_CACHE_BF16) {
+    uint4 y[kReadBatch][2];
+#pragma unroll
+    for (int i = 0; i < kReadBatch; ++i) {
+      if (!ok[i]) continue;
+      y[i][0] = *reinterpret_cast<const uint4*>(rec[i] + 16 * c);
+      y[i][1] = *reinterpret_cast<const uint4*>(rec[i] + U * 128 + 16 * c);
+    }
+#pragma unroll
+    for (int i = 0; i < kReadBatch; ++i) {
+      if (!ok[i]) continue;
+      const long long t = t0 + 4 * i;
+      if (a.k_out.data)
+        *reinterpret_cast<uint4*>(a.k_out.data + b * a.k_out.sb + t * a.k_out.st + kv * a.k_out.sh + 8 * c) = y[i][0];
+      if (a.v_out.data)
+        *reinterpret_cast<uint4*>(a.v_out.data + b * a.v_out.sb + t * a.v_out.st + kv * a.v_out.sh + 8 * c) = y[i][1];
+    }
+  } else {
+    uint32_t w[kReadBatch][2], z[kReadBatch][2];
+#pragma unroll
+    for (int i = 0; i < kReadBatch; ++i) {
+      if (!ok[i]) continue;
+      const int u = (int)((first + t0 + 4 * i) & (U - 1));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        w[i][h] = *reinterpret_cast<const uint32_t*>(rec[i] + h * 36 * U + 4 * c);
+        z[i][h] = rec[i][h * 36 * U + 32 * U - 28 * u + (c >> 1)];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kReadBatch; ++i) {
+      if (!ok[i]) continue;
+      const long long t = t0 + 4 * i;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const RowsDev& dst = h ? a.v_out : a.k_out;
+        const uint32_t s = e4m3x2(z[i][h]);
+        const float f = __low2float(*reinterpret_cast<const __half2*>(&s)) * exp2i(h ? a.cache.v_exp : a.cache.k_exp);
+        uint32_t d[4], o[4];
+        e2m1x8(w[i][h], d);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&d[k]));
+          o[k] = pack_bf16x2(v.x * f, v.y * f);
+        }
+        if (dst.data)
+          *reinterpret_cast<uint4*>(dst.data + b * dst.sb + t * dst.st + kv * dst.sh + 8 * c) =
+              make_uint4(o[0], o[1], o[2], o[3]);
+      }
     }
   }
-  const RowsDev* dst[2] = {&a.k_out, &a.v_out};
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (dst[i]->data)
-      *reinterpret_cast<uint4*>(dst[i]->data + b * dst[i]->sb + t * dst[i]->st + kv * dst[i]->sh + 8 * c) = y[i];
 }
 
 cudaError_t launch_cache_append(const CacheAppendLaunch& L, cudaStream_t s) {
-  const int rows = (L.q.data ? L.Hq : 0) + 2 * L.cache.Hkv;
-  const int groups = (rows + 3) / 4;
-  const int parts = (groups + kAppIter - 1) / kAppIter, per = (groups + parts - 1) / parts;
-  const long long jobs = (long long)L.cache.B * L.T * parts;
-  const unsigned blocks = (unsigned)((jobs + kAppWarps - 1) / kAppWarps);
+  const int groups = ((L.q.data ? L.Hq : 0) + 3) / 4 + (2 * L.cache.Hkv + 3) / 4;
+  // One warp a token where there are many; where there are few, as many as there are groups
+  // of rows, so that a step's latency is one row's.
+  const long long tokens = (long long)L.cache.B * L.T;
+  int parts = 1;
+  while (parts < groups && tokens * parts < 152 * 16) ++parts;
+  const dim3 grid((unsigned)(((long long)L.T * parts + kAppWarps - 1) / kAppWarps), 1, (unsigned)L.cache.B);
+  constexpr int kThreads = kAppWarps * 32;
   if (L.cache.kind == PISA_CACHE_BF16)
-    cache_append_kernel<PISA_CACHE_BF16><<<blocks, kAppWarps * 32, 0, s>>>(L, parts, per);
-  else
-    cache_append_kernel<PISA_CACHE_E2M1><<<blocks, kAppWarps * 32, 0, s>>>(L, parts, per);
-  note_launch();
-  return cudaGetLastError();
+    return L.interleaved ? launch_early<cache_append_kernel<PISA_CACHE_BF16, true>>(grid, kThreads, 0, s, L, parts)
+                         : launch_early<cache_append_kernel<PISA_CACHE_BF16, false>>(grid, kThreads, 0, s, L, parts);
+  return L.interleaved ? launch_early<cache_append_kernel<PISA_CACHE_E2M1, true>>(grid, kThreads, 0, s, L, parts)
+                       : launch_early<cache_append_kernel<PISA_CACHE_E2M1, false>>(grid, kThreads, 0, s, L, parts);
 }
 
 cudaError_t launch_cache_read(const CacheReadLaunch& L, cudaStream_t s) {
-  const int tok_groups = (L.T + 3) / 4;
-  const long long jobs = (long long)L.cache.B * tok_groups * L.cache.Hkv;
-  const unsigned blocks = (unsigned)((jobs + 7) / 8);
-  if (L.cache.kind == PISA_CACHE_BF16)
-    cache_read_kernel<PISA_CACHE_BF16><<<blocks, 256, 0, s>>>(L, tok_groups);
-  else
-    cache_read_kernel<PISA_CACHE_E2M1><<<blocks, 256, 0, s>>>(L, tok_groups);
-  note_launch();
-  return cudaGetLastError();
+  const dim3 grid((unsigned)((L.T + 32 * kReadBatch - 1) / (32 * kReadBatch)), (unsigned)L.cache.Hkv,
+                  (unsigned)L.cache.B);
+  if (L.cache.kind == PISA_CACHE_BF16) return launch_early<cache_read_kernel<PISA_CACHE_BF16>>(grid, 256, 0, s, L);
+  return launch_early<cache_read_kernel<PISA_CACHE_E2M1>>(grid, 256, 0, s, L);
 }
 
 }  // namespace pisa

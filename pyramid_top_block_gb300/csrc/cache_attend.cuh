@@ -1,4 +1,4 @@
-// cache_attend.cu -- attention of a sequence's newest tokens over its paged KV cache, all of
+// cache_attend.cuh -- attention of a sequence's newest tokens over its paged KV cache, all of
 // it or the blocks that a selection listed; pages in bf16 or 4 bits.
 //
 //   o = sum_j p_j v_j / sum_j p_j,   p_j = exp(q . k_j / 8 - max_j)
@@ -11,10 +11,13 @@
 // at its rate of about 1024 multiply-adds per clock and SM takes 2/3 of the time the 4-bit
 // bytes take.
 //
-// Without a list the tiles of all (sequence, KV head, row tile) units form one stream, which
-// is cut into equal runs, one per CTA, whatever the lengths; a unit that ends up in several
-// CTAs is joined by a second kernel from 32-bit partial results.
-#include <atomic>
+// Three forms (launch_attend chooses):
+//   direct, 4 to 12 warps a CTA: one CTA per unit (sequence, KV head and query, or row tile),
+//     for listed blocks and for short caches;
+//   split: the tiles of all units form one stream, which is cut into equal runs, one per SM,
+//     whatever the lengths; a unit that ends up in several runs is joined by a second kernel
+//     from 32-bit partial results.
+#pragma once
 
 #include "cache.cuh"
 #include "tc.cuh"
@@ -24,16 +27,18 @@ namespace pisa {
 constexpr int kPartFloats = 16 * 64 + 32;  // a partial result: O [16][64], row maxima, row sums
 constexpr int kCaGrid = 152;               // CTAs of the split form: one on each SM
 constexpr int kCaMinTiles = 8;             // tiles a CTA of the split form takes at least
+constexpr int kCaDirect = 2048;            // tokens of the table up to which the direct form takes a whole cache
 constexpr float kLog2e = 1.4426950408889634f;
 
-size_t cache_part_bytes() { return (size_t)kCaGrid * 2 * kPartFloats * sizeof(float); }
+inline size_t part_bytes() { return (size_t)kCaGrid * 2 * kPartFloats * sizeof(float); }
 
 template <int KIND>
 struct Cfg;
 template <>
 struct Cfg<PISA_CACHE_BF16> {
   static constexpr int KT = 32;     // keys of a tile
-  static constexpr int kWarps = 8;
+  static constexpr int kWarps = 8;  // of the split form, one CTA on an SM
+  static constexpr int kHalf = 4, kThird = 4;  // of the direct form where two CTAs, or more, share an SM
   static constexpr int kStages = 3;
   static constexpr int kRow = kRowBf16;
   static constexpr float kShift = 0.f;  // weights are held times 2^kShift
@@ -43,6 +48,7 @@ template <>
 struct Cfg<PISA_CACHE_E2M1> {
   static constexpr int KT = 64;
   static constexpr int kWarps = 12;
+  static constexpr int kHalf = 6, kThird = 4;
   static constexpr int kStages = 3;
   static constexpr int kRow = kRowE2m1;
   static constexpr float kShift = 10.f;
@@ -139,37 +145,63 @@ __device__ __forceinline__ int out_dim(int i, int j, int e) {
   return KIND == PISA_CACHE_BF16 ? 8 * i + 2 * j + e : 8 * (2 * j + e) + i;
 }
 
-// Loads the query rows r0 + g and r0 + g + 8 of `rows` (row r: query r / G, head r % G).
+// A unit: the row tile of (sequence b, KV head kv) that starts at row r0.
+struct Unit {
+  int b, kv, r0, t_first;  // t_first: the query of row 0
+  int rows;                // rows of (b, kv): queries * G
+  int n;                   // tokens the sequence holds
+  const int32_t* sel;      // listed blocks, or nullptr
+};
+
+// This lane's part of the query rows r0 + g and r0 + g + 8 of a unit (row r: query r / G,
+// head r % G): dims 16 j .. 16 j + 15 of each.
+struct QueryWords {
+  uint32_t w[2][8];
+};
+
+__device__ __forceinline__ void fetch_q(const CacheAttendLaunch& a, const Unit& u, int lane, QueryWords& q) {
+  const int g = lane >> 2, j = lane & 3;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = u.r0 + g + 8 * h;
+    uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
+    if (r < u.rows) {
+      const int t = u.t_first + r / a.G, head = u.kv * a.G + r % a.G;
+      const uint4* p =
+          reinterpret_cast<const uint4*>(a.q.data + u.b * a.q.sb + (long long)t * a.q.st + head * a.q.sh) + 2 * j;
+      x0 = __ldg(p);
+      x1 = __ldg(p + 1);
+    }
+    q.w[h][0] = x0.x; q.w[h][1] = x0.y; q.w[h][2] = x0.z; q.w[h][3] = x0.w;
+    q.w[h][4] = x1.x; q.w[h][5] = x1.y; q.w[h][6] = x1.z; q.w[h][7] = x1.w;
+  }
+}
+
+template <int KIND>
+__device__ __forceinline__ void reset(RowState<KIND>& s) {
+  s.m0 = s.m1 = -INFINITY;
+  s.l0 = s.l1 = 0.f;
+  s.bad = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s.o[i][0] = s.o[i][1] = s.o[i][2] = s.o[i][3] = 0.f;
+}
+
+// The A fragments of the queries and the logit factors.
 // In the 4-bit form the products are taken in fp16: the row is scaled by a power of two so
 // that its largest element lies in [1, 2), where fp16 holds all 8 bits of a bf16 down to
 // 2^-17 of it and is off by at most 2^-25 of it below (the fp32 sums of the products are
 // off by as much).
 template <int KIND>
-__device__ __forceinline__ void load_q(const CacheAttendLaunch& a, int b, int kv, int t_first, int r0, int rows,
-                                       int lane, RowState<KIND>& s) {
-  const int g = lane >> 2, j = lane & 3;
-  uint32_t w[2][8];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = r0 + g + 8 * h;
-    uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
-    if (r < rows) {
-      const int t = t_first + r / a.G, head = kv * a.G + r % a.G;
-      const uint4* p =
-          reinterpret_cast<const uint4*>(a.q.data + b * a.q.sb + (long long)t * a.q.st + head * a.q.sh) + 2 * j;
-      x0 = __ldg(p);
-      x1 = __ldg(p + 1);
-    }
-    w[h][0] = x0.x; w[h][1] = x0.y; w[h][2] = x0.z; w[h][3] = x0.w;
-    w[h][4] = x1.x; w[h][5] = x1.y; w[h][6] = x1.z; w[h][7] = x1.w;
-  }
+__device__ __forceinline__ void make_q(const CacheAttendLaunch& a, const QueryWords& q, int lane, RowState<KIND>& s) {
+  const int j = lane & 3;
   float f[2] = {kScale * kLog2e, kScale * kLog2e};
   if (KIND == PISA_CACHE_E2M1) {
+    uint32_t w[2][8];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t t = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t = __vmaxu2(t, w[h][i] & 0x7fff7fffu);
+      for (int i = 0; i < 8; ++i) t = __vmaxu2(t, q.w[h][i] & 0x7fff7fffu);
       t = max(t & 0xffffu, t >> 16);
       t = max(t, __shfl_xor_sync(kFull, t, 1));
       t = max(t, __shfl_xor_sync(kFull, t, 2));
@@ -179,7 +211,7 @@ __device__ __forceinline__ void load_q(const CacheAttendLaunch& a, int b, int kv
       f[h] *= exp2i(e) * exp2i(a.cache.k_exp);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        w[h][i] = pack_f16x2(__uint_as_float(w[h][i] << 16) * down, __uint_as_float(w[h][i] & 0xffff0000u) * down);
+        w[h][i] = pack_f16x2(__uint_as_float(q.w[h][i] << 16) * down, __uint_as_float(q.w[h][i] & 0xffff0000u) * down);
     }
     // k-step ks of lane j: dims 16 j + 4 ks .. + 3 (two words)
 #pragma unroll
@@ -199,11 +231,11 @@ __device__ __forceinline__ void load_q(const CacheAttendLaunch& a, int b, int kv
         uint32_t lo = 0, hi = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t u = __shfl_sync(kFull, w[h][i], (lane & 28) | ks);
-          const uint32_t v = __shfl_sync(kFull, w[h][4 + i], (lane & 28) | ks);
+          const uint32_t x = __shfl_sync(kFull, q.w[h][i], (lane & 28) | ks);
+          const uint32_t y = __shfl_sync(kFull, q.w[h][4 + i], (lane & 28) | ks);
           if (i == j) {
-            lo = u;
-            hi = v;
+            lo = x;
+            hi = y;
           }
         }
         s.qa[ks][h] = lo;
@@ -212,11 +244,6 @@ __device__ __forceinline__ void load_q(const CacheAttendLaunch& a, int b, int kv
   }
   s.f0 = f[0];
   s.f1 = f[1];
-  s.m0 = s.m1 = -INFINITY;
-  s.l0 = s.l1 = 0.f;
-  s.bad = false;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) s.o[i][0] = s.o[i][1] = s.o[i][2] = s.o[i][3] = 0.f;
 }
 
 // The key (of 16 in a group) behind column element (half h of the group, e) of lane j.
@@ -511,23 +538,17 @@ __device__ __forceinline__ void weigh(uint32_t st, int first, const Sight& see, 
     }
 }
 
-// A unit: the row tile of (sequence b, KV head kv) that starts at row r0.
-struct Unit {
-  int b, kv, r0, t_first;  // t_first: the query of row 0
-  int rows;                // rows of (b, kv): queries * G
-  int n;                   // tokens the sequence holds
-  const int32_t* sel;      // listed blocks, or nullptr
-};
-
-// Tiles [i0, i1) of a unit (SEL: of the listed blocks that begin in sight), shared out among
-// the CTA's warps; on return every warp holds its own partial sums.  A warp copies its tiles
+// Tiles [i0, i1) of a unit (u.sel: all of the listed blocks that begin in sight; blk: this
+// lane's entries of the list, lane and lane + 32), shared out among the CTA's W warps; on return every warp holds its own partial sums.  A warp copies its tiles
 // ahead into a ring of three stages: while one is on its way, the logits of the next tile and
 // the products with V of the one before are computed side by side.
-template <int KIND, int U, bool SEL, int NP>
-__device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit& u, int i0, int i1, uint32_t ring,
-                                          float* scratch, int warp, int lane, RowState<KIND>& s) {
+template <int KIND, int U, int NP, int W, bool LIST>
+__device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit& u, const QueryWords& q,
+                                          const int (&blk)[2], int i0, int i1, uint32_t ring, float* scratch, int warp,
+                                          int lane, RowState<KIND>& s) {
   using C = Cfg<KIND>;
-  constexpr int KT = C::KT, W = C::kWarps;
+  constexpr int KT = C::KT;
+  const bool listed = LIST && u.sel != nullptr;
   constexpr int E = KT > U ? KT / U : 1;  // records of a tile
   constexpr int kAhead = 32 / E;          // tiles a look ahead covers
   constexpr uint32_t kStage = kStageBytes<KIND>;
@@ -539,22 +560,17 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
   const int last = min(u.rows, u.r0 + 16) - 1;
   const Sight see = {ra < u.rows ? base + ra / a.G : 0, rb < u.rows ? base + rb / a.G : 0, base + u.r0 / a.G,
                      base + last / a.G};
-  int* list = reinterpret_cast<int*>(scratch);  // (SEL: a row tile is one query's, so weigh leaves it alone)
-  if (SEL) {  // the listed blocks that count, in the order of the list
-    int blk[2];
-    unsigned long long some[2];
+  int* list = reinterpret_cast<int*>(scratch);  // (listed: a row tile is one query's, so weigh leaves it alone)
+  if (listed) {  // the listed blocks that count, in the order of the list
+    unsigned some[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = lane + 32 * h;
-      blk[h] = i < a.Ksel ? __ldg(u.sel + i) : -1;
+    for (int h = 0; h < 2; ++h)
       some[h] = __ballot_sync(kFull, blk[h] >= 0 && blk[h] < (1 << 21) && blk[h] * kC < see.n_hi);
-    }
     const unsigned below = (1u << lane) - 1u;
-    if (some[0] >> lane & 1) list[__popc((unsigned)some[0] & below)] = blk[0];
-    if (some[1] >> lane & 1) list[__popc((unsigned)some[0]) + __popc((unsigned)some[1] & below)] = blk[1];
+    if (some[0] >> lane & 1) list[__popc(some[0] & below)] = blk[0];
+    if (some[1] >> lane & 1) list[__popc(some[0]) + __popc(some[1] & below)] = blk[1];
     __syncwarp();
-    i0 = 0;
-    i1 = (__popc((unsigned)some[0]) + __popc((unsigned)some[1])) * (kC / KT);
+    i1 = (__popc(some[0]) + __popc(some[1])) * (kC / KT);
   } else {
     i1 = min(i1, (max(see.n_hi, 0) + KT - 1) / KT);
   }
@@ -564,7 +580,7 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
 
   auto first_of = [&](int x) {  // the first token of the warp's tile number x
     const int i = i0 + warp + W * x;
-    return SEL ? list[i * KT / kC] * kC + (i * KT) % kC : i * KT;
+    return listed ? list[i * KT / kC] * kC + (i * KT) % kC : i * KT;
   };
   // Lane l looks ahead: where record l % E of the warp's tile number x + l / E lies.  Records
   // that nothing sees are read from the first page instead.
@@ -618,6 +634,7 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
   cpa_commit();
   if (mine > 1) issue(1, ring + kStage);
   cpa_commit();
+  make_q(a, q, lane, s);
   cpa_wait<1>();
   __syncwarp();
   const int f0 = first_of(0);
@@ -644,13 +661,9 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
   cpa_wait<0>();
 }
 
-// Merges the warps' partial sums; thread (row, quad) of the CTA gets four dims of the sum over
-// the warps, its row's maximum and sum.
-// (The warps' O go into the ring, which is idle then.)
-template <int KIND>
-__device__ __forceinline__ float4 merge_warps(RowState<KIND>& s, float* mo, float (*ml)[2][16], int warp, int lane,
-                                              float& m, float& l) {
-  constexpr int W = Cfg<KIND>::kWarps;
+// Puts the warps' partial sums where merged() finds them: O into the ring, which is idle then.
+template <int KIND, int W>
+__device__ __forceinline__ void merge_warps(RowState<KIND>& s, float* mo, float (*ml)[2][16], int warp, int lane) {
   static_assert(Cfg<KIND>::kStages * kStageBytes<KIND> >= 4096, "");
   const int g = lane >> 2, j = lane & 3;
 #pragma unroll
@@ -675,7 +688,12 @@ __device__ __forceinline__ float4 merge_warps(RowState<KIND>& s, float* mo, floa
       o[(g + 8) * 64 + out_dim<KIND>(i, j, e)] = s.o[i][2 + e];
     }
   __syncthreads();
-  const int row = (threadIdx.x >> 4) & 15, quad = threadIdx.x & 15;
+}
+
+// Dims 4 quad .. + 3 of a row's sum over the warps, the row's reference and sum of weights.
+template <int W>
+__device__ __forceinline__ float4 merged(const float* mo, const float (*ml)[2][16], int row, int quad, float& m,
+                                         float& l) {
   m = -INFINITY;
 #pragma unroll
   for (int w = 0; w < W; ++w) m = fmaxf(m, ml[w][0][row]);
@@ -736,50 +754,80 @@ __device__ __forceinline__ long long tiles_before(const CacheAttendLaunch& a, in
 
 // Tiles per CTA of the split form.
 __device__ __forceinline__ long long run_length(long long total, int grid) {
-  const long long per = (total + grid - 1) / grid;
+  const long long per = total < (1 << 30) ? ((int)total + grid - 1) / grid : (total + grid - 1) / grid;
   return per < kCaMinTiles ? kCaMinTiles : per;
 }
 
-template <int KIND>
-constexpr int kRing = Cfg<KIND>::kWarps* Cfg<KIND>::kStages* kStageBytes<KIND>;
-template <int KIND>
+template <int KIND, int W>
+constexpr int kRing = W* Cfg<KIND>::kStages* kStageBytes<KIND>;
+template <int KIND, int W>
 constexpr int attend_smem() {
-  return kRing<KIND> + Cfg<KIND>::kWarps * (kScratch + 2 * 16 * 4);
+  return kRing<KIND, W> + W * (kScratch + 2 * 16 * 4);
 }
 
-template <int KIND, int U, bool SEL, int NP>
-__global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_kernel(CacheAttendLaunch a) {
+template <int KIND, int U, int NP, int W>
+__global__ void __launch_bounds__(W * 32) cache_attend_direct_kernel(CacheAttendLaunch a) {
   using C = Cfg<KIND>;
-  constexpr int KT = C::KT;
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (uniform to the compiler)
   const uint32_t ring = warp * C::kStages * kStageBytes<KIND>;                        // (offset into the shared memory)
   float* mo = reinterpret_cast<float*>(ca_smem);
-  float* scratch = reinterpret_cast<float*>(ca_smem + kRing<KIND> + warp * kScratch);
-  float(*ml)[2][16] = reinterpret_cast<float(*)[2][16]>(ca_smem + kRing<KIND> + C::kWarps * kScratch);
-  const int row = threadIdx.x >> 4, quad = threadIdx.x & 15;
-  RowState<KIND> s;
+  float* scratch = reinterpret_cast<float*>(ca_smem + kRing<KIND, W> + warp * kScratch);
+  float(*ml)[2][16] = reinterpret_cast<float(*)[2][16]>(ca_smem + kRing<KIND, W> + W * kScratch);
+  after_the_one_before();
+  // one CTA per (b, t, kv) with a list, per (b, row tile, kv) without
+  const unsigned id = blockIdx.x;
   Unit u;
-  bool over;
-  if (SEL) {  // one CTA per (b, t, kv)
-    const unsigned id = blockIdx.x;
-    u.kv = id % a.cache.Hkv;
-    const unsigned bt = id / a.cache.Hkv;
+  u.kv = id % a.cache.Hkv;
+  const unsigned bt = id / a.cache.Hkv;
+  int blk[2] = {-1, -1};
+  if (a.idx) {
     u.t_first = bt % a.T;
     u.b = bt / a.T;
     u.r0 = 0;
     u.rows = a.G;
-    u.n = seq_len(a, u.b, over);
     u.sel = a.idx + (((long long)u.b * a.cache.Hkv + u.kv) * a.T + u.t_first) * a.Ksel;
-    load_q<KIND>(a, u.b, u.kv, u.t_first, 0, u.rows, lane, s);
-    run_tiles<KIND, U, SEL, NP>(a, u, 0, 0, ring, scratch, warp, lane, s);
-    if (threadIdx.x == 0 && over) set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
-    if (lane == 0 && s.bad) set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
-    float m, l;
-    const float4 acc = merge_warps<KIND>(s, mo, ml, warp, lane, m, l);
-    if (threadIdx.x < 256) write_out(a, u, row, quad, acc, l);
-    return;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (lane + 32 * h < a.Ksel) blk[h] = __ldg(u.sel + lane + 32 * h);
+  } else {
+    const unsigned RT = (a.T * a.G + 15) / 16;
+    u.t_first = 0;
+    u.r0 = (bt % RT) * 16;
+    u.b = bt / RT;
+    u.rows = a.T * a.G;
+    u.sel = nullptr;
   }
-  // the split form: this CTA's run of the stream of tiles
+  bool over;
+  u.n = seq_len(a, u.b, over);
+  QueryWords q;
+  fetch_q(a, u, lane, q);
+  RowState<KIND> s;
+  reset(s);
+  run_tiles<KIND, U, NP, W, true>(a, u, q, blk, 0, 1 << 30, ring, scratch, warp, lane, s);
+  if ((threadIdx.x == 0 && over) || (lane == 0 && s.bad)) set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
+  merge_warps<KIND, W>(s, mo, ml, warp, lane);
+  for (int i = threadIdx.x; i < 256; i += W * 32) {
+    float m, l;
+    const float4 acc = merged<W>(mo, ml, i >> 4, i & 15, m, l);
+    write_out(a, u, i >> 4, i & 15, acc, l);
+  }
+}
+
+template <int KIND, int U, int NP>
+__global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_kernel(CacheAttendLaunch a) {
+  using C = Cfg<KIND>;
+  constexpr int KT = C::KT, W = C::kWarps;
+  const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t ring = warp * C::kStages * kStageBytes<KIND>;
+  float* mo = reinterpret_cast<float*>(ca_smem);
+  float* scratch = reinterpret_cast<float*>(ca_smem + kRing<KIND, W> + warp * kScratch);
+  float(*ml)[2][16] = reinterpret_cast<float(*)[2][16]>(ca_smem + kRing<KIND, W> + W * kScratch);
+  after_the_one_before();
+  RowState<KIND> s;
+  Unit u;
+  bool over;
+  const int blk[2] = {-1, -1};
+  // this CTA's run of the stream of tiles
   const int RT = (a.T * a.G + 15) / 16;
   const int units = a.cache.Hkv * RT;  // of a sequence
   const long long total = tiles_before<KT>(a, a.cache.B, units, lane);
@@ -789,7 +837,6 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_kernel
   if (cur >= end) return;
   // the sequence that tile `cur` belongs to: 32 sequences at a time
   long long base = 0;  // tiles before sequence u.b
-  int nt = 0;          // tiles of a unit of it
   u.b = 0;
   for (int b0 = 0; b0 < a.cache.B; b0 += 32) {
     const int n = b0 + lane < a.cache.B ? seq_len(a, b0 + lane, over) : 0;
@@ -815,31 +862,37 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_kernel
   int slot = 0;
   while (cur < end) {
     u.n = seq_len(a, u.b, over);
-    nt = (u.n + KT - 1) / KT;
+    const int nt = (u.n + KT - 1) / KT;  // tiles of a unit of this sequence
     if (nt == 0 || cur >= base + (long long)nt * units) {  // on to the next sequence
       base += (long long)nt * units;
       ++u.b;
       continue;
     }
-    if (threadIdx.x == 0 && over) set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
-    const int un = (int)((cur - base) / nt);
-    const int i0 = (int)((cur - base) - (long long)un * nt);
+    // (tiles of one sequence: below 2^22 * 32 heads * 16 row tiles, within 32 bits)
+    const unsigned at = (unsigned)(cur - base), un = at / (unsigned)nt;
+    const int i0 = (int)(at - un * nt);
     const int i1 = (int)(end - cur < nt - i0 ? i0 + (end - cur) : nt);
     u.kv = un / RT;
     u.r0 = (un % RT) * 16;
-    load_q<KIND>(a, u.b, u.kv, 0, u.r0, u.rows, lane, s);
-    run_tiles<KIND, U, SEL, NP>(a, u, i0, i1, ring, scratch, warp, lane, s);
-    if (lane == 0 && s.bad) set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
-    float m, l;
-    const float4 acc = merge_warps<KIND>(s, mo, ml, warp, lane, m, l);
-    if (i0 == 0 && i1 == nt) {
-      if (threadIdx.x < 256) write_out(a, u, row, quad, acc, l);
-    } else if (threadIdx.x < 256) {  // slot 0: the run's first unit, slot 1: its last
-      float* p = a.part + ((long long)blockIdx.x * 2 + slot) * kPartFloats;
-      *reinterpret_cast<float4*>(p + row * 64 + 4 * quad) = acc;
-      if (quad == 0) {
-        p[1024 + row] = m;
-        p[1040 + row] = l;
+    QueryWords q;
+    fetch_q(a, u, lane, q);
+    reset(s);
+    run_tiles<KIND, U, NP, W, false>(a, u, q, blk, i0, i1, ring, scratch, warp, lane, s);
+    if ((threadIdx.x == 0 && over) || (lane == 0 && s.bad)) set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
+    merge_warps<KIND, W>(s, mo, ml, warp, lane);
+    if (threadIdx.x < 256) {
+      const int row = threadIdx.x >> 4, quad = threadIdx.x & 15;
+      float m, l;
+      const float4 acc = merged<W>(mo, ml, row, quad, m, l);
+      if (i0 == 0 && i1 == nt) {
+        write_out(a, u, row, quad, acc, l);
+      } else {  // slot 0: the run's first unit, slot 1: its last
+        float* p = a.part + ((long long)blockIdx.x * 2 + slot) * kPartFloats;
+        *reinterpret_cast<float4*>(p + row * 64 + 4 * quad) = acc;
+        if (quad == 0) {
+          p[1024 + row] = m;
+          p[1040 + row] = l;
+        }
       }
     }
     slot = 1;
@@ -849,7 +902,8 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_kernel
 }
 
 // Joins the partial results of the units that lie in several runs, and writes zeros for
-// sequences without tokens.  One CTA per (unit, four rows): 4 rows x 16 quads x 4 groups of
+// sequences without tokens.  It starts while the kernel before it runs, and reads what that
+// one only reads too; the partial results after the wait.  One CTA per (unit, four rows): 4 rows x 16 quads x 4 groups of
 // partials.
 template <int KT>
 __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, int grid) {
@@ -858,6 +912,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, in
   const int lane = threadIdx.x & 31;
   const int quad = threadIdx.x & 15, rq = (threadIdx.x >> 4) & 3, grp = threadIdx.x >> 6;
   const int RT = (a.T * a.G + 15) / 16, units = a.cache.Hkv * RT;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const unsigned id = blockIdx.x >> 2;
   const int row = (blockIdx.x & 3) * 4 + rq;
   Unit u;
@@ -871,6 +926,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, in
   u.n = seq_len(a, u.b, over);
   const int nt = (u.n + KT - 1) / KT;
   if (nt == 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (grp == 0) write_out(a, u, row, quad, make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
     return;
   }
@@ -880,6 +936,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, in
   const long long w0 = before + (long long)un * nt, w1 = w0 + nt;
   const int c0 = (int)(w0 / per), c1 = (int)((w1 - 1) / per);
   if (c0 == c1) return;  // a run held all of it and wrote it
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -921,38 +978,34 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, in
   write_out(a, u, row, quad, acc, l);
 }
 
-template <int KIND, int U, bool SEL, int NP>
-static cudaError_t launch_attend_t(const CacheAttendLaunch& L, cudaStream_t s) {
+template <int KIND, int U, int NP, int W>
+static cudaError_t launch_direct(const CacheAttendLaunch& L, unsigned units, cudaStream_t s) {
+  return launch_early<cache_attend_direct_kernel<KIND, U, NP, W>>(units, W * 32, attend_smem<KIND, W>(), s, L);
+}
+
+template <int KIND, int U, int NP>
+static cudaError_t launch_attend(const CacheAttendLaunch& L, cudaStream_t s) {
   using C = Cfg<KIND>;
-  constexpr int smem = attend_smem<KIND>();
-  const auto kernel = cache_attend_kernel<KIND, U, SEL, NP>;
-  // the attribute belongs to the device: set once on each of the first 64 (on others at every call)
-  static std::atomic<unsigned long long> done{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
-  if (!(done.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    done.fetch_or(bit, std::memory_order_release);
-  }
   const int RT = (L.T * L.G + 15) / 16;
-  const int grid = SEL ? L.cache.B * L.T * L.cache.Hkv : kCaGrid;
-  kernel<<<(unsigned)grid, C::kWarps * 32, smem, s>>>(L);
-  note_launch();
-  e = cudaGetLastError();
-  if (SEL || e != cudaSuccess) return e;
-  cache_join_kernel<C::KT><<<(unsigned)(L.cache.B * L.cache.Hkv * RT * 4), 256, 0, s>>>(L, grid);
-  note_launch();
-  return cudaGetLastError();
+  const long long cap = (long long)L.cache.max_pages << L.cache.page_shift;
+  const unsigned units = (unsigned)(L.cache.B * L.cache.Hkv * (L.idx ? L.T : RT));
+  if (L.idx || cap <= kCaDirect) {
+    // The more units there are, the fewer warps share one out, so that all CTAs run at once
+    // (128 x 2 units of 32 blocks: six warps 16.9 us, four 20.2, twelve 22.5).
+    if (units <= kCaGrid) return launch_direct<KIND, U, NP, C::kWarps>(L, units, s);
+    if (units <= 2 * kCaGrid) return launch_direct<KIND, U, NP, C::kHalf>(L, units, s);
+    return launch_direct<KIND, U, NP, C::kThird>(L, units, s);
+  }
+  cudaError_t e = launch_early<cache_attend_split_kernel<KIND, U, NP>>(kCaGrid, C::kWarps * 32,
+                                                                       attend_smem<KIND, C::kWarps>(), s, L);
+  if (e != cudaSuccess) return e;
+  return launch_early<cache_join_kernel<C::KT>>(units * 4, 256, 0, s, L, kCaGrid);
 }
 
 template <int KIND, int U>
 static cudaError_t launch_attend_u(const CacheAttendLaunch& L, cudaStream_t s) {
   constexpr int NP = KIND == PISA_CACHE_BF16 ? 2 : 1;  // parts of the weights (see weigh)
-  if (L.idx) return L.out_f32 ? launch_attend_t<KIND, U, true, NP + 1>(L, s) : launch_attend_t<KIND, U, true, NP>(L, s);
-  return L.out_f32 ? launch_attend_t<KIND, U, false, NP + 1>(L, s) : launch_attend_t<KIND, U, false, NP>(L, s);
+  return L.out_f32 ? launch_attend<KIND, U, NP + 1>(L, s) : launch_attend<KIND, U, NP>(L, s);
 }
 
 template <int KIND>
@@ -962,11 +1015,6 @@ static cudaError_t launch_attend_k(const CacheAttendLaunch& L, cudaStream_t s) {
     case 5: return launch_attend_u<KIND, 32>(L, s);
     default: return launch_attend_u<KIND, 64>(L, s);
   }
-}
-
-cudaError_t launch_cache_attend(const CacheAttendLaunch& L, cudaStream_t s) {
-  return L.cache.kind == PISA_CACHE_BF16 ? launch_attend_k<PISA_CACHE_BF16>(L, s)
-                                         : launch_attend_k<PISA_CACHE_E2M1>(L, s);
 }
 
 }  // namespace pisa
