@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -446,10 +447,8 @@ class _RowsStruct(ctypes.Structure):
     ]
 
 
-# several _RowsStruct as one array of their words (an argument is then byref at its offset): one object a call
-_Rows1, _Rows2, _Rows5 = ctypes.c_int64 * 4, ctypes.c_int64 * 8, ctypes.c_int64 * 20
-_NO_ROWS = (0, 0, 0, 0)
-_byref = ctypes.byref
+# a _RowsStruct as bytes: cheaper to make than the ctypes object, and as good an argument
+_pack_rows = struct.Struct("Pqqq").pack
 
 
 class PagedCache:
@@ -569,7 +568,7 @@ def _rows(x: torch.Tensor, what: str, cache: PagedCache, B: int, T: int, H: int,
         sh = 0
     elif written and sh == 0:
         raise ValueError(f"the rows of {what} must not share memory")
-    return x.data_ptr(), sb, st, sh
+    return _pack_rows(x.data_ptr(), sb, st, sh)
 
 
 def _per_sequence(x: torch.Tensor, what: str, cache: PagedCache) -> int:
@@ -608,7 +607,7 @@ def cache_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache
         raise ValueError("k must be a bf16 tensor [B, T, Hkv, 64]")
     B, T, Hkv = cache.B, k.shape[1], cache.Hkv
     ks, vs = _rows(k, "k", cache, B, T, Hkv), _rows(v, "v", cache, B, T, Hkv)
-    Hq, qs, qo = 0, _NO_ROWS, _NO_ROWS
+    Hq, qs, qo = 0, None, None
     if q is not None:
         if q.dim() != 4:
             raise ValueError("q must be a bf16 tensor [B, T, Hq, 64]")
@@ -630,11 +629,10 @@ def cache_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache
         if rot not in (16, 32, 48, 64):
             raise ValueError("rotary must be [n, rot] with rot 16, 32, 48 or 64")
         rp = rotary.data_ptr()
-    rows = _Rows5(*qs, *ks, *vs, *qo, *_rows(k_out, "k_out", cache, B, T, Hkv, True))
     _check((_lib or load()).pisa_cache_append(
-        cache._ref, T, rows, Hq, _byref(rows, 32), _byref(rows, 64), _per_sequence(start, "start", cache),
+        cache._ref, T, qs, Hq, ks, vs, _per_sequence(start, "start", cache),
         None if counts is None else _per_sequence(counts, "counts", cache), rp, n_rot, rot, 1 if interleaved else 0,
-        _byref(rows, 96), _byref(rows, 128), None if workspace is None else _cache_ws(workspace, cache, 4),
+        qo, _rows(k_out, "k_out", cache, B, T, Hkv, True), None if workspace is None else _cache_ws(workspace, cache, 4),
         _current(cache)), "pisa_cache_append")
     return q_out, k_out
 
@@ -655,10 +653,10 @@ def cache_read(cache: PagedCache, start: torch.Tensor, T: int, counts: torch.Ten
         k_out = torch.empty(B, T, Hkv, D, dtype=torch.bfloat16, device=cache.device)
     if v_out is None:
         v_out = torch.empty(B, T, Hkv, D, dtype=torch.bfloat16, device=cache.device)
-    rows = _Rows2(*_rows(k_out, "k_out", cache, B, T, Hkv, True), *_rows(v_out, "v_out", cache, B, T, Hkv, True))
     _check((_lib or load()).pisa_cache_read(
         cache._ref, T, _per_sequence(start, "start", cache),
-        None if counts is None else _per_sequence(counts, "counts", cache), rows, _byref(rows, 32),
+        None if counts is None else _per_sequence(counts, "counts", cache),
+        _rows(k_out, "k_out", cache, B, T, Hkv, True), _rows(v_out, "v_out", cache, B, T, Hkv, True),
         None if workspace is None else _cache_ws(workspace, cache, 4), _current(cache)), "pisa_cache_read")
     return k_out, v_out
 
@@ -697,7 +695,7 @@ def cache_attention(q: torch.Tensor, cache: PagedCache, lengths: torch.Tensor, i
     need = lib.pisa_cache_workspace_bytes()
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
-    _check(lib.pisa_cache_attention(cache._ref, _Rows1(*_rows(q, "q", cache, B, T, Hq)), T, Hq,
+    _check(lib.pisa_cache_attention(cache._ref, _rows(q, "q", cache, B, T, Hq), T, Hq,
                                     _per_sequence(lengths, "lengths", cache), ip, Ksel, out.data_ptr(),
                                     1 if out.dtype is torch.float32 else 0, _cache_ws(workspace, cache, need), need,
                                     _current(cache)), "pisa_cache_attention")
