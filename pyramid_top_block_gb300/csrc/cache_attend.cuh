@@ -26,7 +26,7 @@ namespace pisa {
 
 constexpr int kPartFloats = 16 * 64 + 32;  // a partial result: O [16][64], row maxima, row sums
 constexpr int kCaGrid = 152;               // CTAs of the split form: one on each SM
-constexpr int kCaMinTiles = 8;             // tiles a CTA of the split form takes at least
+constexpr int kCaMinTiles = 12;            // tiles a CTA of the split form takes at least
 constexpr int kCaDirect = 2048;            // tokens of the table up to which the direct form takes a whole cache
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -47,7 +47,7 @@ struct Cfg<PISA_CACHE_BF16> {
 template <>
 struct Cfg<PISA_CACHE_E2M1> {
   static constexpr int KT = 64;
-  static constexpr int kWarps = 12;
+  static constexpr int kWarps = 12;  // (a multiple of four: an SM's four schedulers share the warps out evenly)
   static constexpr int kHalf = 6, kThird = 4;
   static constexpr int kStages = 3;
   static constexpr int kRow = kRowE2m1;
@@ -766,7 +766,7 @@ constexpr int attend_smem() {
 }
 
 template <int KIND, int U, int NP, int W>
-__global__ void __launch_bounds__(W * 32) cache_attend_direct_kernel(CacheAttendLaunch a) {
+__global__ void __launch_bounds__(W * 32, Cfg<KIND>::kWarps / W) cache_attend_direct_kernel(CacheAttendLaunch a) {
   using C = Cfg<KIND>;
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (uniform to the compiler)
   const uint32_t ring = warp * C::kStages * kStageBytes<KIND>;                        // (offset into the shared memory)
