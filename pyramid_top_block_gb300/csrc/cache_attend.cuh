@@ -752,6 +752,32 @@ __device__ __forceinline__ long long tiles_before(const CacheAttendLaunch& a, in
   return sum * units;
 }
 
+// The sequence that tile `at` of the stream belongs to, and the tiles before that sequence: 32
+// sequences at a time.
+template <int KT>
+__device__ __forceinline__ int seq_of(const CacheAttendLaunch& a, long long at, int units, int lane, long long& base) {
+  base = 0;
+  for (int b0 = 0; b0 < a.cache.B; b0 += 32) {
+    bool over;
+    const int n = b0 + lane < a.cache.B ? seq_len(a, b0 + lane, over) : 0;
+    const long long t = (long long)((n + KT - 1) / KT) * units;
+    long long inc = t;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      const long long y = __shfl_up_sync(kFull, inc, x);
+      if (lane >= x) inc += y;
+    }
+    const unsigned hit = __ballot_sync(kFull, base + inc > at);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      base += __shfl_sync(kFull, inc - t, l);
+      return b0 + l;
+    }
+    base += __shfl_sync(kFull, inc, 31);
+  }
+  return a.cache.B;  // (past the last tile)
+}
+
 // Tiles per CTA of the split form.
 __device__ __forceinline__ long long run_length(long long total, int grid) {
   const long long per = total < (1 << 30) ? ((int)total + grid - 1) / grid : (total + grid - 1) / grid;
@@ -834,28 +860,22 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_
   const long long per = run_length(total, gridDim.x);
   long long cur = per * blockIdx.x;
   const long long end = cur + per < total ? cur + per : total;
+  // sequences without tokens: zeros
+  for (int b = blockIdx.x; b < a.cache.B; b += gridDim.x)
+    if (seq_len(a, b, over) == 0) {
+      const long long at = (long long)b * a.T * a.Hq * kD;
+      for (int i = threadIdx.x; i < a.T * a.Hq * kD / 8; i += W * 32) {
+        if (a.out_f32) {
+          reinterpret_cast<float4*>(static_cast<float*>(a.out) + at)[2 * i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          reinterpret_cast<float4*>(static_cast<float*>(a.out) + at)[2 * i + 1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        } else {
+          reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at)[i] = make_uint4(0, 0, 0, 0);
+        }
+      }
+    }
   if (cur >= end) return;
-  // the sequence that tile `cur` belongs to: 32 sequences at a time
-  long long base = 0;  // tiles before sequence u.b
-  u.b = 0;
-  for (int b0 = 0; b0 < a.cache.B; b0 += 32) {
-    const int n = b0 + lane < a.cache.B ? seq_len(a, b0 + lane, over) : 0;
-    const long long t = (long long)((n + KT - 1) / KT) * units;
-    long long inc = t;
-#pragma unroll
-    for (int x = 1; x < 32; x <<= 1) {
-      const long long y = __shfl_up_sync(kFull, inc, x);
-      if (lane >= x) inc += y;
-    }
-    const unsigned hit = __ballot_sync(kFull, base + inc > cur);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      u.b = b0 + l;
-      base += __shfl_sync(kFull, inc - t, l);
-      break;
-    }
-    base += __shfl_sync(kFull, inc, 31);
-  }
+  long long base;  // tiles before sequence u.b
+  u.b = seq_of<KT>(a, cur, units, lane, base);
   u.t_first = 0;
   u.rows = a.T * a.G;
   u.sel = nullptr;
@@ -901,47 +921,52 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_
   }
 }
 
-// Joins the partial results of the units that lie in several runs, and writes zeros for
-// sequences without tokens.  It starts while the kernel before it runs, and reads what that
-// one only reads too; the partial results after the wait.  One CTA per (unit, four rows): 4 rows x 16 quads x 4 groups of
-// partials.
+// Joins the partial results of the units that lie in several runs.  At most one such unit
+// begins in a run: the one that holds the run's last tile.  Four CTAs a run, four rows each:
+// 4 rows x 16 quads x 4 groups of partials.  The kernel starts while the one before it runs,
+// and reads the lengths, which that one only reads too; the partial results after the wait,
+// which every CTA passes (a grid that ended without it would let the next kernel of the
+// stream overtake the one before).
 template <int KT>
 __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, int grid) {
   __shared__ float4 so[4][4][16];
   __shared__ float sm[4][4], sl[4][4];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int quad = threadIdx.x & 15, rq = (threadIdx.x >> 4) & 3, grp = threadIdx.x >> 6;
   const int RT = (a.T * a.G + 15) / 16, units = a.cache.Hkv * RT;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const unsigned id = blockIdx.x >> 2;
-  const int row = (blockIdx.x & 3) * 4 + rq;
-  Unit u;
-  u.b = id / units;
-  const int un = id % units;
-  u.kv = un / RT;
-  u.r0 = (un % RT) * 16;
-  u.rows = a.T * a.G;
-  u.t_first = 0;
-  bool over;
-  u.n = seq_len(a, u.b, over);
-  const int nt = (u.n + KT - 1) / KT;
-  if (nt == 0) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (grp == 0) write_out(a, u, row, quad, make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
-    return;
-  }
-  const long long before = tiles_before<KT>(a, u.b, units, lane);
+  const int c0 = blockIdx.x >> 2, row = (blockIdx.x & 3) * 4 + rq;
   const long long total = tiles_before<KT>(a, a.cache.B, units, lane);
   const long long per = run_length(total, grid);
-  const long long w0 = before + (long long)un * nt, w1 = w0 + nt;
-  const int c0 = (int)(w0 / per), c1 = (int)((w1 - 1) / per);
-  if (c0 == c1) return;  // a run held all of it and wrote it
+  const long long end = per * (c0 + 1);  // the run's end, if the stream goes on after it
+  bool cut = end < total;
+  Unit u;
+  int c1 = 0;
+  bool first = false;  // whether the unit begins with its run
+  if (cut) {
+    long long base;
+    u.b = seq_of<KT>(a, end - 1, units, lane, base);
+    bool over;
+    u.n = seq_len(a, u.b, over);
+    const int nt = (u.n + KT - 1) / KT;
+    const unsigned un = (unsigned)(end - 1 - base) / (unsigned)nt;
+    u.kv = un / RT;
+    u.r0 = (un % RT) * 16;
+    u.rows = a.T * a.G;
+    u.t_first = 0;
+    u.sel = nullptr;
+    const long long w0 = base + (long long)un * nt, w1 = w0 + nt;
+    cut = w1 > end && w0 >= end - per;
+    first = w0 == end - per;
+    c1 = (int)((w1 - 1) / per);
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!cut) return;
   float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int c = c0 + grp; c <= c1; c += 4) {
-    const int slot = c == c0 && w0 > per * c ? 1 : 0;
+    const int slot = c == c0 && !first ? 1 : 0;
     const float* p = a.part + ((long long)c * 2 + slot) * kPartFloats;
     const float mc = p[1024 + row], lc = p[1040 + row];
     const float4 x = *reinterpret_cast<const float4*>(p + row * 64 + 4 * quad);
@@ -988,8 +1013,8 @@ static cudaError_t launch_attend(const CacheAttendLaunch& L, cudaStream_t s) {
   using C = Cfg<KIND>;
   const int RT = (L.T * L.G + 15) / 16;
   const long long cap = (long long)L.cache.max_pages << L.cache.page_shift;
-  const unsigned units = (unsigned)(L.cache.B * L.cache.Hkv * (L.idx ? L.T : RT));
   if (L.idx || cap <= kCaDirect) {
+    const unsigned units = (unsigned)(L.cache.B * L.cache.Hkv * (L.idx ? L.T : RT));
     // The more units there are, the fewer warps share one out, so that all CTAs run at once
     // (128 x 2 units of 32 blocks: six warps 16.9 us, four 20.2, twelve 22.5).
     if (units <= kCaGrid) return launch_direct<KIND, U, NP, C::kWarps>(L, units, s);
@@ -999,7 +1024,7 @@ static cudaError_t launch_attend(const CacheAttendLaunch& L, cudaStream_t s) {
   cudaError_t e = launch_early<cache_attend_split_kernel<KIND, U, NP>>(kCaGrid, C::kWarps * 32,
                                                                        attend_smem<KIND, C::kWarps>(), s, L);
   if (e != cudaSuccess) return e;
-  return launch_early<cache_join_kernel<C::KT>>(units * 4, 256, 0, s, L, kCaGrid);
+  return launch_early<cache_join_kernel<C::KT>>(kCaGrid * 4, 256, 0, s, L, kCaGrid);
 }
 
 template <int KIND, int U>

@@ -653,3 +653,57 @@ def test_two_graphs_with_one_workspace():
         made[which][0].replay()
         assert torch.equal(made[which][1], made[which][2])
     assert status(ws) == 0
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_many_sequences_in_a_long_table(bits):
+    """257 sequences, many empty, in a table long enough that the tiles of all are one stream."""
+    g = gen(19)
+    B = 257
+    cache = make_cache(g, 8, 2304, 2, 64, bits)
+    lengths = [(b * 7919) % 2300 if b % 3 else 0 for b in range(B)]
+    table = cache.table[torch.arange(B, device=DEV) % 8].contiguous()  # sequences share pages
+    many = pisa.PagedCache(cache.pages, table, 64)
+    q = normal(g, B, 2, 8, 64)
+    ws = pisa.cache_workspace(many)
+    out = torch.full((B, 2, 8, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    pisa.cache_attention(q, many, i32(lengths), out=out, workspace=ws)
+    assert status(ws) == 0
+    some = [b for b in range(B) if b % 16 == 1 or lengths[b] < 3]
+    for b in some:
+        one = pisa.PagedCache(cache.pages, table[b:b + 1].contiguous(), 64)
+        check_attention(one, q[b:b + 1], lengths[b:b + 1], out[b:b + 1])
+    o32 = torch.full((B, 2, 8, 64), 7.0, dtype=torch.float32, device=DEV)
+    pisa.cache_attention(q, many, i32(lengths), out=o32, workspace=ws)
+    for b in range(B):
+        if lengths[b] == 0:
+            assert bool((out[b] == 0).all()) and bool((o32[b] == 0).all())
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_calls_do_not_overtake_one_another(bits):
+    """Kernels of later calls may start early, but the cache is not written while an earlier call reads it."""
+    g = gen(20)
+    tiles = 12  # no unit is cut: the joining kernel has nothing to wait for but the order
+    n = tiles * (64 if bits == 4 else 32)
+    cache = make_cache(g, 1, 4096, 2, 64, bits)
+    start, lengths = i32([0]), i32([n])
+    q = normal(g, 1, 1, 32, 64)
+    new = [(normal(g, 1, n, 2, 64), normal(g, 1, n, 2, 64)) for _ in range(4)]
+    ws = pisa.cache_workspace(cache)
+    want = []
+    for k, v in new:
+        pisa.cache_append(None, k, v, cache, start, None)
+        torch.cuda.synchronize()
+        want.append(pisa.cache_attention(q, cache, lengths, workspace=ws).clone())
+        torch.cuda.synchronize()
+    outs, reads = [], []
+    for i in range(40):
+        k, v = new[i % 4]
+        pisa.cache_append(None, k, v, cache, start, None, k_out=k)
+        outs.append(pisa.cache_attention(q, cache, lengths, workspace=ws))
+        reads.append(pisa.cache_read(cache, start, n))
+    torch.cuda.synchronize()
+    for i in range(40):
+        assert torch.equal(outs[i], want[i % 4]), i
+        assert torch.equal(reads[i][0], reads[i % 4][0]) and torch.equal(reads[i][1], reads[i % 4][1])
