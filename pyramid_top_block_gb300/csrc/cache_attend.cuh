@@ -6,10 +6,15 @@
 //
 // The 16 rows of an mma.sync m16n8k16 tile are the query heads of one KV head's group (and of
 // several queries, where the group is smaller); every warp of a CTA takes its own tiles of
-// keys, and the CTA's warps are merged through shared memory at the end.  Per key the kernel
-// reads 72 or 256 bytes and does 4 * 64 * 16 multiply-adds, so the bytes bound it; mma.sync
-// at its rate of about 1024 multiply-adds per clock and SM takes 2/3 of the time the 4-bit
-// bytes take.
+// keys, and the CTA's warps are merged through shared memory at the end.
+//
+// What bounds it.  Per key and KV head 72 or 256 bytes are read.  bf16 pages: the memory;
+// 8 ragged sequences up to 131072 tokens (384 MB) take 65.7 us = 5.84 TB/s, and a plain
+// read-only sweep of as many bytes 59.5 us.  4-bit pages: the arithmetic; 16 x 131072 tokens
+// (302 MB) take 74.8 us = 4.04 TB/s, without the copies 63, without the products 50.  A tile of
+// 64 keys costs 64 HMMA of 8 clocks and 128 HMUL2 of 2 on each scheduler, which do not overlap
+// on this machine, beside 157 conversions and 37 logic operations on the other pipe (which
+// do): about 250 clocks of an SM a tile, where the tile's bytes take 196.
 //
 // Three forms (launch_attend chooses):
 //   direct, 4 to 12 warps a CTA: one CTA per unit (sequence, KV head and query, or row tile),
@@ -539,9 +544,11 @@ __device__ __forceinline__ void weigh(uint32_t st, int first, const Sight& see, 
 }
 
 // Tiles [i0, i1) of a unit (u.sel: all of the listed blocks that begin in sight; blk: this
-// lane's entries of the list, lane and lane + 32), shared out among the CTA's W warps; on return every warp holds its own partial sums.  A warp copies its tiles
-// ahead into a ring of three stages: while one is on its way, the logits of the next tile and
-// the products with V of the one before are computed side by side.
+// lane's entries of the list, lane and lane + 32), shared out among the CTA's W warps; on
+// return every warp holds its own partial sums.  A warp copies its tiles ahead into a ring of
+// three stages: while one is on its way, the logits of the next tile and the products with V
+// of the one before are computed side by side.  (Keys and values in rings of their own, with
+// two tiles on their way, were 2 to 4 % slower: the memory system is full with one.)
 template <int KIND, int U, int NP, int W, bool LIST>
 __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit& u, const QueryWords& q,
                                           const int (&blk)[2], int i0, int i1, uint32_t ring, float* scratch, int warp,
