@@ -299,8 +299,8 @@ size_t pisa_cache_workspace_bytes(void);
  * Token t < counts[b] of sequence b has position start[b] + t.  In the first `rot` dims of
  * a query or key row the pairs (i, i + rot / 2) (interleaved != 0: (2 i, 2 i + 1)) become
  * (a c - b s, b c + a s), with c = rotary[p, i], s = rotary[p, rot / 2 + i]; each result is
- * the 64-bit sum rounded to 32 bits and then to bf16, so the bits do not depend on the
- * call's shape.  The rotated key, and the value, go into the page.
+ * the exact sum rounded to 32 bits and then to bf16 (below 2^-100 the last bit may differ),
+ * and does not depend on the call's shape.  The rotated key, and the value, go into the page.
  *   q       : rows [B, T, Hq, d], or NULL; k, v: rows [B, T, Hkv, d]
  *   start   : device int32 [B]; counts: device int32 [B], or NULL (T of each)
  *   rotary  : device fp32 [n_rot, rot], 16-byte aligned; rot in {0, 16, 32, 48, 64}, 0: no
