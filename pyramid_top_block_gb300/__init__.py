@@ -519,8 +519,13 @@ def rotary_table(n: int, rot: int = D, base: float = 10000.0, device="cuda") -> 
     return torch.cat([angle.cos(), angle.sin()], 1).float()
 
 
+_cache_ws_bytes = 0  # asked once: it is the same for every size
+
+
 def cache_workspace_bytes() -> int:
-    return int(load().pisa_cache_workspace_bytes())
+    global _cache_ws_bytes
+    _cache_ws_bytes = int(load().pisa_cache_workspace_bytes())
+    return _cache_ws_bytes
 
 
 def cache_workspace(cache: PagedCache) -> torch.Tensor:
@@ -549,9 +554,11 @@ def _current(cache: PagedCache) -> int:
     return _raw_stream(cache._index) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
 
 
-def _rows(x: torch.Tensor, what: str, cache: PagedCache, B: int, T: int, H: int, written: bool = False):
-    if x.dtype is not torch.bfloat16 or x.shape != (B, T, H, D) or x.get_device() != cache._index:
-        raise ValueError(f"{what} must be a bf16 tensor [{B}, {T}, {H}, {D}] on the cache's device")
+def _rows(x: torch.Tensor, what: str, cache: PagedCache, shape: tuple, written: bool = False) -> bytes:
+    """The descriptor of rows of x [B, T, H, 64], checked to have that shape."""
+    if x.dtype is not torch.bfloat16 or x.shape != shape or x.get_device() != cache._index:
+        raise ValueError(f"{what} must be a bf16 tensor {list(shape)} on the cache's device")
+    B, T, H, _ = shape
     sb, st, sh, sd = x.stride()
     if sd != 1:
         raise ValueError(f"the rows of {what} must be dense")
@@ -605,21 +612,23 @@ def cache_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache
             return cache_append(q, k, v, cache, start, rotary, counts, interleaved, q_out, k_out, workspace)
     if k.dim() != 4:
         raise ValueError("k must be a bf16 tensor [B, T, Hkv, 64]")
-    B, T, Hkv = cache.B, k.shape[1], cache.Hkv
-    ks, vs = _rows(k, "k", cache, B, T, Hkv), _rows(v, "v", cache, B, T, Hkv)
+    B, T = cache.B, k.shape[1]
+    shape = (B, T, cache.Hkv, D)
+    ks, vs = _rows(k, "k", cache, shape), _rows(v, "v", cache, shape)
     Hq, qs, qo = 0, None, None
     if q is not None:
         if q.dim() != 4:
             raise ValueError("q must be a bf16 tensor [B, T, Hq, 64]")
         Hq = q.shape[2]
-        qs = _rows(q, "q", cache, B, T, Hq)
+        qshape = (B, T, Hq, D)
+        qs = _rows(q, "q", cache, qshape)
         if q_out is None:
-            q_out = torch.empty(B, T, Hq, D, dtype=torch.bfloat16, device=cache.device)
-        qo = _rows(q_out, "q_out", cache, B, T, Hq, True)
+            q_out = torch.empty(qshape, dtype=torch.bfloat16, device=cache.device)
+        qo = _rows(q_out, "q_out", cache, qshape, True)
     elif q_out is not None:
         raise ValueError("q_out without q")
     if k_out is None:
-        k_out = torch.empty(B, T, Hkv, D, dtype=torch.bfloat16, device=cache.device)
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
     n_rot, rot, rp = 0, 0, None
     if rotary is not None:
         if (rotary.dtype is not torch.float32 or rotary.dim() != 2 or rotary.get_device() != cache._index
@@ -632,7 +641,7 @@ def cache_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache
     _check((_lib or load()).pisa_cache_append(
         cache._ref, T, qs, Hq, ks, vs, _per_sequence(start, "start", cache),
         None if counts is None else _per_sequence(counts, "counts", cache), rp, n_rot, rot, 1 if interleaved else 0,
-        qo, _rows(k_out, "k_out", cache, B, T, Hkv, True), None if workspace is None else _cache_ws(workspace, cache, 4),
+        qo, _rows(k_out, "k_out", cache, shape, True), None if workspace is None else _cache_ws(workspace, cache, 4),
         _current(cache)), "pisa_cache_append")
     return q_out, k_out
 
@@ -646,17 +655,17 @@ def cache_read(cache: PagedCache, start: torch.Tensor, T: int, counts: torch.Ten
     if guard is not None:
         with guard:
             return cache_read(cache, start, T, counts, k_out, v_out, workspace)
-    B, Hkv = cache.B, cache.Hkv
     if T < 1:
         raise ValueError("T must be at least 1")
+    shape = (cache.B, T, cache.Hkv, D)
     if k_out is None:
-        k_out = torch.empty(B, T, Hkv, D, dtype=torch.bfloat16, device=cache.device)
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
     if v_out is None:
-        v_out = torch.empty(B, T, Hkv, D, dtype=torch.bfloat16, device=cache.device)
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
     _check((_lib or load()).pisa_cache_read(
         cache._ref, T, _per_sequence(start, "start", cache),
         None if counts is None else _per_sequence(counts, "counts", cache),
-        _rows(k_out, "k_out", cache, B, T, Hkv, True), _rows(v_out, "v_out", cache, B, T, Hkv, True),
+        _rows(k_out, "k_out", cache, shape, True), _rows(v_out, "v_out", cache, shape, True),
         None if workspace is None else _cache_ws(workspace, cache, 4), _current(cache)), "pisa_cache_read")
     return k_out, v_out
 
@@ -677,7 +686,10 @@ def cache_attention(q: torch.Tensor, cache: PagedCache, lengths: torch.Tensor, i
             return cache_attention(q, cache, lengths, idx, out, workspace)
     if q.dim() != 4:
         raise ValueError("q must be a bf16 tensor [B, T, Hq, 64]")
-    B, T, Hkv, Hq = cache.B, q.shape[1], cache.Hkv, q.shape[2]
+    _, T, Hq, _ = q.shape
+    B, Hkv = cache.B, cache.Hkv
+    shape = (B, T, Hq, D)
+    qs = _rows(q, "q", cache, shape)
     Ksel, ip = 0, None
     if idx is not None:
         Ksel = idx.shape[-1]
@@ -687,15 +699,15 @@ def cache_attention(q: torch.Tensor, cache: PagedCache, lengths: torch.Tensor, i
                              "cache's device")
         ip = idx.data_ptr()
     if out is None:
-        out = torch.empty(B, T, Hq, D, dtype=torch.bfloat16, device=cache.device)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
     elif ((out.dtype is not torch.bfloat16 and out.dtype is not torch.float32) or out.get_device() != cache._index
-          or out.shape != (B, T, Hq, D) or not out.is_contiguous()):
-        raise ValueError(f"out must be a contiguous bf16 or fp32 tensor [{B}, {T}, {Hq}, {D}]")
+          or out.shape != shape or not out.is_contiguous()):
+        raise ValueError(f"out must be a contiguous bf16 or fp32 tensor {list(shape)}")
     lib = _lib or load()
-    need = lib.pisa_cache_workspace_bytes()
+    need = _cache_ws_bytes or cache_workspace_bytes()
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
-    _check(lib.pisa_cache_attention(cache._ref, _rows(q, "q", cache, B, T, Hq), T, Hq,
+    _check(lib.pisa_cache_attention(cache._ref, qs, T, Hq,
                                     _per_sequence(lengths, "lengths", cache), ip, Ksel, out.data_ptr(),
                                     1 if out.dtype is torch.float32 else 0, _cache_ws(workspace, cache, need), need,
                                     _current(cache)), "pisa_cache_attention")
