@@ -7,12 +7,15 @@
 // order the other member of a pair is rot/2 dims away, which is a whole number of lanes, so
 // it comes by shuffle; in the interleaved order it is the neighbouring element.
 //
-// Both kernels only move rows: the bound is the bytes of the rows in and out.
+// Both kernels only move rows, so the bytes of the rows in and out bound them.  Measured: 32768
+// tokens of 32 + 2 + 2 heads into bf16 pages (319 MB) 56.3 us = 5.66 TB/s; 131072 tokens of 2
+// heads read back from 4 bits (86 MB) 16.4 us = 5.24 TB/s; 65 single tokens 4.2 us.
 #include "cache.cuh"
 
 namespace pisa {
 
 constexpr int kAppWarps = 4;
+constexpr int kAppPrefetch = 912;  // tokens ahead (six an SM) whose rows are asked into L2: 61.4 -> 57 us for 32768
 constexpr int kAppBatch = 2;  // groups of four rows whose loads a warp issues together, ahead of their use
 
 // x c + p s rounded to 32 bits from (nearly) twice as many: both products and their sum as
@@ -27,15 +30,16 @@ __device__ __forceinline__ float sum2(float x, float c, float p, float s) {
 
 // Eight rotated elements x c + p s (p the pair's other member, s signed), as the bf16 values
 // that the exact sum rounds to (by way of 32 bits).  In 32 bits the sum r is off by at most
-// (|p s| + |r|) 2^-24 (results below 2^-100 aside); where every value within twice that rounds to the same bf16 that is
-// the answer, else (one element in some thousands) the sums are taken with their errors.
-// So a key has the same bits however it was appended, which matters where it is quantised
-// next.  (64-bit arithmetic in that rare branch cost half of the kernel's time: the compiler
-// hoists the conversions, and the 64-bit pipe is slow.)
+// (|p s| + |r|) 2^-24 (results below 2^-100 aside); where every value within twice that
+// rounds to the same bf16 that is the answer, else (one element in some thousands) the sums
+// are taken with their errors.  So a key has the same bits however it was appended, which
+// matters where it is quantised next.  (64-bit arithmetic in that rare branch cost half of
+// the kernel's time: the compiler hoists the conversions, and the 64-bit pipe is slow.)
+// there: whether the row exists and turns (the zeros of one that does not would take the
+// branch: r - e and r + e of a negative zero differ).
 __device__ __forceinline__ void rotate8(uint32_t (&w)[4], const uint32_t (&o)[4], const float (&c)[8],
-                                        const float (&s)[8]) {
-  uint32_t lo[4];
-  bool same = true;
+                                        const float (&s)[8], bool there) {
+  uint32_t lo[4], differ = 0;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const float x0 = __uint_as_float(w[k] << 16), x1 = __uint_as_float(w[k] & 0xffff0000u);
@@ -44,9 +48,9 @@ __device__ __forceinline__ void rotate8(uint32_t (&w)[4], const uint32_t (&o)[4]
     const float r0 = fmaf(x0, c[2 * k], m0), r1 = fmaf(x1, c[2 * k + 1], m1);
     const float e0 = (fabsf(m0) + fabsf(r0)) * 0x1p-23f, e1 = (fabsf(m1) + fabsf(r1)) * 0x1p-23f;
     lo[k] = pack_bf16x2(r0 - e0, r1 - e1);
-    same = same && lo[k] == pack_bf16x2(r0 + e0, r1 + e1);
+    differ |= lo[k] ^ pack_bf16x2(r0 + e0, r1 + e1);
   }
-  if (!same) {
+  if (differ && there) {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       lo[k] = pack_bf16x2(sum2(__uint_as_float(w[k] << 16), c[2 * k], __uint_as_float(o[k] << 16), s[2 * k]),
@@ -139,7 +143,8 @@ __device__ __forceinline__ void load_turn(const CacheAppendLaunch& a, long long 
   }
 }
 
-// (Lanes that do not turn compute as well and keep their words: cheaper than a branch.)
+// rotate: whether the row exists and turns.  (Lanes that do not turn compute as well and keep
+// their words: cheaper than a branch.)
 template <bool INTER>
 __device__ __forceinline__ void turn_row(const Turn& t, bool rotate, uint32_t (&w)[4]) {
   uint32_t o[4], y[4];
@@ -148,7 +153,7 @@ __device__ __forceinline__ void turn_row(const Turn& t, bool rotate, uint32_t (&
     o[k] = INTER ? __byte_perm(w[k], 0, 0x1032) : __shfl_sync(kFull, w[k], t.from);
     y[k] = w[k];
   }
-  rotate8(y, o, t.c, t.s);
+  rotate8(y, o, t.c, t.s, t.on && rotate);
 #pragma unroll
   for (int k = 0; k < 4; ++k) w[k] = t.on && rotate ? y[k] : w[k];
 }
@@ -163,6 +168,8 @@ __global__ void __launch_bounds__(kAppWarps * 32, 6) cache_append_kernel(CacheAp
   const int t = job / parts, part = job - t * parts, b = blockIdx.z;
   if (t >= a.T) return;
   const int Hkv = a.cache.Hkv, Hq = a.q.data ? a.Hq : 0;
+  // (a prompt's rows behind its count are not even read; a single token's are, rather than wait)
+  if (a.T > 1 && a.counts && t >= a.counts[b]) return;
   const int gq = (Hq + 3) >> 2, groups = gq + ((2 * Hkv + 3) >> 2);
   // the rows this lane has a part in: query row 4 i + sub of group i, row 4 (i - gq) + sub of
   // keys and values
@@ -188,6 +195,17 @@ __global__ void __launch_bounds__(kAppWarps * 32, 6) cache_append_kernel(CacheAp
   const int count = a.counts ? a.counts[b] : a.T;
   const long long p = (long long)a.start[b] + t;
   if (t >= count) return;
+  if (parts == 1 && t + kAppPrefetch < min(count, a.T)) {  // a prompt: a later token's rows and angles into L2
+    const int later = t + kAppPrefetch;
+    for (int r = lane; r < Hq + 2 * Hkv; r += 32) {
+      const RowsDev& from = r < Hq ? a.q : r < Hq + Hkv ? a.k : a.v;
+      const int h = r < Hq ? r : r < Hq + Hkv ? r - Hq : r - Hq - Hkv;
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(from.data + b * from.sb + later * from.st + h * from.sh));
+    }
+    const long long at = (long long)a.start[b] + later;
+    if (lane < 2 && a.rot && at >= 0 && at < a.n_rot)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.rotary + at * a.rot + (a.rot > 32 ? 32 * lane : 0)));
+  }
   const long long cap = (long long)a.cache.max_pages << a.cache.page_shift;
   bool ok = p >= 0 && p < cap && (a.rot == 0 || p < a.n_rot);
   int page = -1;
@@ -204,22 +222,33 @@ __global__ void __launch_bounds__(kAppWarps * 32, 6) cache_append_kernel(CacheAp
   __nv_bfloat16* qd = a.q_out.data + b * a.q_out.sb + t * a.q_out.st + sub * a.q_out.sh + 8 * c;
   const long long step_out = 4 * parts * a.q_out.sh;
   qd += (long long)(4 * part) * a.q_out.sh;
-  for (int i = part; i < gq; i += kAppBatch * parts) {
-    uint4 next[kAppBatch];
-    qs += kAppBatch * step;
+  // (two batches a turn, so that neither is copied)
+  auto fetch_q = [&](int i, uint4 (&z)[kAppBatch]) {
 #pragma unroll
     for (int n = 0; n < kAppBatch; ++n) {
-      next[n] = make_uint4(0, 0, 0, 0);
-      if (4 * (i + (kAppBatch + n) * parts) + sub < Hq) next[n] = *reinterpret_cast<const uint4*>(qs + n * step);
+      z[n] = make_uint4(0, 0, 0, 0);
+      if (4 * (i + n * parts) + sub < Hq) z[n] = *reinterpret_cast<const uint4*>(qs + n * step);
     }
+    qs += kAppBatch * step;
+  };
+  auto put_q = [&](int i, const uint4 (&z)[kAppBatch]) {
 #pragma unroll
     for (int n = 0; n < kAppBatch; ++n) {
-      uint32_t w[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
-      turn_row<INTER>(turn, true, w);
+      uint32_t w[4] = {z[n].x, z[n].y, z[n].z, z[n].w};
+      turn_row<INTER>(turn, 4 * (i + n * parts) + sub < Hq, w);
       if (4 * (i + n * parts) + sub < Hq) *reinterpret_cast<uint4*>(qd) = make_uint4(w[0], w[1], w[2], w[3]);
       qd += step_out;
-      x[n] = next[n];
     }
+  };
+  const int turns = kAppBatch * parts;
+  qs += kAppBatch * step;
+  for (int i = part; i < gq; i += 2 * turns) {
+    uint4 y[kAppBatch];
+    fetch_q(i + turns, y);
+    put_q(i, x);
+    if (i + turns >= gq) break;
+    fetch_q(i + 2 * turns, x);
+    put_q(i + turns, y);
   }
   const int U = 1 << a.cache.rec_shift, u = (int)(p & (U - 1));
   for (int i = ikv; i < groups - gq; i += parts) {
@@ -228,7 +257,7 @@ __global__ void __launch_bounds__(kAppWarps * 32, 6) cache_append_kernel(CacheAp
     const int kv = is_v ? r - Hkv : r;
     uint32_t w[4] = {xkv.x, xkv.y, xkv.z, xkv.w};
     xkv = fetch_kv(i + parts);
-    turn_row<INTER>(turn, !is_v, w);
+    turn_row<INTER>(turn, !is_v && there, w);
     const uint4 y = make_uint4(w[0], w[1], w[2], w[3]);
     if (!is_v && a.k_out.data)
       *reinterpret_cast<uint4*>(a.k_out.data + b * a.k_out.sb + t * a.k_out.st + kv * a.k_out.sh + 8 * c) = y;
