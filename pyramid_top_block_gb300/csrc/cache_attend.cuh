@@ -32,7 +32,6 @@ namespace pisa {
 constexpr int kPartFloats = 16 * 64 + 32;  // a partial result: O [16][64], row maxima, row sums
 constexpr int kCaGrid = 152;               // CTAs of the split form: one on each SM
 constexpr int kCaMinTiles = 12;            // tiles a CTA of the split form takes at least
-constexpr int kCaDirect = 2048;            // tokens of the table up to which the direct form takes a whole cache
 constexpr float kLog2e = 1.4426950408889634f;
 
 inline size_t part_bytes() { return (size_t)kCaGrid * 2 * kPartFloats * sizeof(float); }
@@ -1025,18 +1024,30 @@ static cudaError_t launch_direct(const CacheAttendLaunch& L, unsigned units, cud
   return launch_early<cache_attend_direct_kernel<KIND, U, NP, W>>(units, W * 32, attend_smem<KIND, W>(), s, L);
 }
 
+// Whether the direct form takes whole caches of up to `cap` tokens.  It saves the second kernel and
+// each run's changes of unit.  Direct / split, us a call for full tables, 4 bits (bf16):
+//   units x tokens  64 x 4096 13.6 / 15.3 (16.8 / 19.3)   256 x 4096 24.0 / 34.9 (42.6 / 50.1)
+//                   128 x 8192 24.4 / 29.8 (42.7 / 47.6)  1024 x 4096 71.2 / 108.7 (162 / 173)
+// It loses where units are few for their length (8 x 4096 16.4 / 14.4, 64 x 8192 26.7 / 25.0, with
+// each call's launch), and where few of many units are long: 256 x 16384 full 80.2 / 86.0,
+// ragged 78.7 / 68.0 (156.7 / 166.1, 112.1 / 106.4).
+inline bool takes_direct(long long cap, long long units) {
+  const long long most = 64 * units < 8192 ? 64 * units : 8192;
+  return cap <= (most > 2048 ? most : 2048);
+}
+
 template <int KIND, int U, int NP>
 static cudaError_t launch_attend(const CacheAttendLaunch& L, cudaStream_t s) {
   using C = Cfg<KIND>;
   const int RT = (L.T * L.G + 15) / 16;
   const long long cap = (long long)L.cache.max_pages << L.cache.page_shift;
-  if (L.idx || cap <= kCaDirect) {
-    const unsigned units = (unsigned)(L.cache.B * L.cache.Hkv * (L.idx ? L.T : RT));
+  const long long units = (long long)L.cache.B * L.cache.Hkv * (L.idx ? L.T : RT);
+  if (L.idx || takes_direct(cap, units)) {
     // The more units there are, the fewer warps share one out, so that all CTAs run at once
     // (128 x 2 units of 32 blocks: six warps 16.9 us, four 20.2, twelve 22.5).
-    if (units <= kCaGrid) return launch_direct<KIND, U, NP, C::kWarps>(L, units, s);
-    if (units <= 2 * kCaGrid) return launch_direct<KIND, U, NP, C::kHalf>(L, units, s);
-    return launch_direct<KIND, U, NP, C::kThird>(L, units, s);
+    if (units <= kCaGrid) return launch_direct<KIND, U, NP, C::kWarps>(L, (unsigned)units, s);
+    if (units <= 2 * kCaGrid) return launch_direct<KIND, U, NP, C::kHalf>(L, (unsigned)units, s);
+    return launch_direct<KIND, U, NP, C::kThird>(L, (unsigned)units, s);
   }
   cudaError_t e = launch_early<cache_attend_split_kernel<KIND, U, NP>>(kCaGrid, C::kWarps * 32,
                                                                        attend_smem<KIND, C::kWarps>(), s, L);

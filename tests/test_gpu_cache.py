@@ -707,3 +707,93 @@ def test_calls_do_not_overtake_one_another(bits):
     for i in range(40):
         assert torch.equal(outs[i], want[i % 4]), i
         assert torch.equal(reads[i][0], reads[i % 4][0]) and torch.equal(reads[i][1], reads[i % 4][1])
+
+
+def in_a_wide_table(cache, tokens=20000):
+    """The same cache with room for many more tokens, on pages that do not exist yet: the tiles of all
+    sequences are then one stream, however short they are."""
+    more = -(-tokens // cache.page_size)
+    table = torch.cat([cache.table, torch.full((cache.B, more), -1, dtype=torch.int32, device=DEV)], 1).contiguous()
+    return pisa.PagedCache(cache.pages, table, cache.page_size, cache._struct.k_exp, cache._struct.v_exp)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("B,T,G,Hkv,page,lengths", ALL)
+def test_attention_over_all_in_a_wide_table(bits, B, T, G, Hkv, page, lengths):
+    g = gen(B * 100 + T + 1)
+    cache = in_a_wide_table(make_cache(g, B, max(lengths) + 40, Hkv, page, bits, layers=2))
+    q = normal(g, B, T, G * Hkv, 64)
+    ws = pisa.cache_workspace(cache)
+    out = torch.full((B, T, G * Hkv, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    pisa.cache_attention(q, cache, i32(lengths), out=out, workspace=ws)
+    assert status(ws) == 0
+    check_attention(cache, q, lengths, out)
+    o32 = torch.full(out.shape, 7.0, dtype=torch.float32, device=DEV)
+    pisa.cache_attention(q, cache, i32(lengths), out=o32, workspace=ws)
+    check_attention(cache, q, lengths, o32)
+    assert torch.equal(pisa.cache_attention(q, cache, i32(lengths), workspace=ws), out)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("T,G,page,n", [(1, 16, 64, 100), (4, 4, 16, 130), (3, 16, 128, 1665), (16, 1, 16, 2059)])
+def test_what_a_query_does_not_see_in_a_wide_table(bits, T, G, page, n):
+    g = gen(n + 1)
+    cache = make_cache(g, 2, n + 150, 2, page, bits)
+    q = normal(g, 2, T, 2 * G, 64)
+    lengths = [n, n - 1]
+    for b in range(2):
+        for p in range(lengths[b], n + 64):
+            poison(cache, b, p)
+    cache.table[:, -(-n // page):] = -1
+    cache = in_a_wide_table(cache)
+    ws = pisa.cache_workspace(cache)
+    check_attention(cache, q, lengths, pisa.cache_attention(q, cache, i32(lengths), workspace=ws))
+    assert status(ws) == 0
+    for what in ("k", "v"):
+        for b in range(2):
+            poison(cache, b, lengths[b] - 1, what)
+        out = pisa.cache_attention(q, cache, i32(lengths))
+        check_attention(cache, q, lengths, out, rows={(b, t) for b in range(2) for t in range(T - 1)})
+        assert bool(torch.isnan(out[:, T - 1]).any(-1).all())
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_bad_pages_and_lengths_in_a_wide_table(bits):
+    g = gen(21)
+    short = make_cache(g, 3, 12000, 2, 64, bits)
+    cache = in_a_wide_table(short, 64)
+    q = normal(g, 3, 2, 16, 64)
+    lengths = [12000, 11000, 130]
+    cache.table[1, 100] = cache.n_pages  # in one of the several runs of its units
+    ws = pisa.cache_workspace(cache)
+    out = pisa.cache_attention(q, cache, i32(lengths), workspace=ws)
+    assert status(ws) == 6
+    assert bool(torch.isnan(out[1]).all())
+    for b in (0, 2):
+        good = pisa.PagedCache(cache.pages, cache.table[b:b + 1].contiguous(), 64)
+        check_attention(good, q[b:b + 1], lengths[b:b + 1], out[b:b + 1])
+    ws = pisa.cache_workspace(short)  # a length past the table's end is cut to it, and flagged
+    full = short.max_pages * 64
+    one = pisa.PagedCache(short.pages, short.table[:1].contiguous(), 64)
+    long = pisa.cache_attention(q[:1], one, i32([full + 5]), workspace=ws)
+    assert status(ws) == 6
+    assert torch.equal(long, pisa.cache_attention(q[:1], one, i32([full])))
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_many_sequences_in_a_wide_table(bits):
+    """257 sequences, many empty, some of them cut between runs."""
+    g = gen(22)
+    B = 257
+    cache = make_cache(g, 8, 2304, 2, 64, bits)
+    lengths = [(b * 7919) % 2300 if b % 3 else 0 for b in range(B)]
+    table = cache.table[torch.arange(B, device=DEV) % 8].contiguous()
+    many = in_a_wide_table(pisa.PagedCache(cache.pages, table, 64))
+    q = normal(g, B, 2, 8, 64)
+    ws = pisa.cache_workspace(many)
+    out = torch.full((B, 2, 8, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    pisa.cache_attention(q, many, i32(lengths), out=out, workspace=ws)
+    assert status(ws) == 0
+    for b in [b for b in range(B) if b % 16 == 1 or lengths[b] < 3]:
+        one = pisa.PagedCache(cache.pages, table[b:b + 1].contiguous(), 64)
+        check_attention(one, q[b:b + 1], lengths[b:b + 1], out[b:b + 1])
