@@ -19,8 +19,8 @@
 // Three forms (launch_attend chooses):
 //   direct, 4 to 12 warps a CTA: one CTA per unit (sequence, KV head and query, or row tile),
 //     for listed blocks and for short caches;
-//   split: the tiles of all units form one stream, which is cut into equal runs, one per SM,
-//     whatever the lengths; a unit that ends up in several runs is joined by a second kernel
+//   split: the tiles of all units form one stream, which is cut into runs of equal cost, one
+//     per SM, whatever the lengths; a unit that ends up in several runs is joined by a second kernel
 //     from 32-bit partial results.
 #pragma once
 
@@ -31,7 +31,7 @@ namespace pisa {
 
 constexpr int kPartFloats = 16 * 64 + 32;  // a partial result: O [16][64], row maxima, row sums
 constexpr int kCaGrid = 152;               // CTAs of the split form: one on each SM
-constexpr int kCaMinTiles = 12;            // tiles a CTA of the split form takes at least
+constexpr int kCaMinTiles = 12;            // places a CTA of the split form takes at least
 constexpr float kLog2e = 1.4426950408889634f;
 
 inline size_t part_bytes() { return (size_t)kCaGrid * 2 * kPartFloats * sizeof(float); }
@@ -45,6 +45,7 @@ struct Cfg<PISA_CACHE_BF16> {
   static constexpr int kHalf = 4, kThird = 4;  // of the direct form where two CTAs, or more, share an SM
   static constexpr int kStages = 3;
   static constexpr int kRow = kRowBf16;
+  static constexpr int kChange = 36;  // places of the stream that a unit's end counts as (see unit_places)
   static constexpr float kShift = 0.f;  // weights are held times 2^kShift
   static constexpr float kSlack = 20.f;  // how far (base 2) a logit may pass the row's reference
 };
@@ -55,6 +56,7 @@ struct Cfg<PISA_CACHE_E2M1> {
   static constexpr int kHalf = 6, kThird = 4;
   static constexpr int kStages = 3;
   static constexpr int kRow = kRowE2m1;
+  static constexpr int kChange = 24;
   static constexpr float kShift = 10.f;
   static constexpr float kSlack = 5.f;
 };
@@ -757,26 +759,38 @@ __device__ __forceinline__ int seq_len(const CacheAttendLaunch& a, int b, bool& 
   return n < 0 ? 0 : over ? (int)cap : n;
 }
 
-// Tiles of all units before sequence b (b = B: of all): every warp computes it by itself.
-template <int KT>
-__device__ __forceinline__ long long tiles_before(const CacheAttendLaunch& a, int b, int units, int lane) {
+// Places that a unit of nt tiles has in the stream: its tiles, and some for what a run spends at
+// its end (the warps' merge, the next unit's chain of loads; about 4 us), so that the runs that
+// change units take as long as the others.  Places at the end 0 / 12 / 24 / 36 / 48, us a call:
+//   4 bits  16 x 131072 73.5 / 72.1 / 71.5 / 71.6 / 71.9   64 x 9000 ragged, 8 heads 88.8 / 63.6 / 56.7 / 57.5 / 59.8
+//   bf16    8 x 131072 ragged 64.8 / 63.8 / 63.3 / 63.0 / 63.3   64 x 9000 ragged, 8 heads 119.7 / 103 / 96.3 / 96.5 / 97.4
+template <int KIND>
+__device__ __forceinline__ int unit_places(int nt) {
+  return nt ? nt + Cfg<KIND>::kChange : 0;
+}
+
+// Places of all units before sequence b (b = B: of all): every warp computes it by itself.
+template <int KIND>
+__device__ __forceinline__ long long places_before(const CacheAttendLaunch& a, int b, int units, int lane) {
+  constexpr int KT = Cfg<KIND>::KT;
   long long sum = 0;
   bool over;
-  for (int i = lane; i < b; i += 32) sum += (seq_len(a, i, over) + KT - 1) / KT;
+  for (int i = lane; i < b; i += 32) sum += unit_places<KIND>((seq_len(a, i, over) + KT - 1) / KT);
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(kFull, sum, x);
   return sum * units;
 }
 
-// The sequence that tile `at` of the stream belongs to, and the tiles before that sequence: 32
+// The sequence that place `at` of the stream belongs to, and the places before that sequence: 32
 // sequences at a time.
-template <int KT>
+template <int KIND>
 __device__ __forceinline__ int seq_of(const CacheAttendLaunch& a, long long at, int units, int lane, long long& base) {
+  constexpr int KT = Cfg<KIND>::KT;
   base = 0;
   for (int b0 = 0; b0 < a.cache.B; b0 += 32) {
     bool over;
     const int n = b0 + lane < a.cache.B ? seq_len(a, b0 + lane, over) : 0;
-    const long long t = (long long)((n + KT - 1) / KT) * units;
+    const long long t = (long long)unit_places<KIND>((n + KT - 1) / KT) * units;
     long long inc = t;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
@@ -791,10 +805,10 @@ __device__ __forceinline__ int seq_of(const CacheAttendLaunch& a, long long at, 
     }
     base += __shfl_sync(kFull, inc, 31);
   }
-  return a.cache.B;  // (past the last tile)
+  return a.cache.B;  // (past the last place)
 }
 
-// Tiles per CTA of the split form.
+// Places per CTA of the split form.
 __device__ __forceinline__ long long run_length(long long total, int grid) {
   const long long per = total < (1 << 30) ? ((int)total + grid - 1) / grid : (total + grid - 1) / grid;
   return per < kCaMinTiles ? kCaMinTiles : per;
@@ -869,10 +883,10 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_
   Unit u;
   bool over;
   const int blk[2] = {-1, -1};
-  // this CTA's run of the stream of tiles
+  // this CTA's run of the stream
   const int RT = (a.T * a.G + 15) / 16;
   const int units = a.cache.Hkv * RT;  // of a sequence
-  const long long total = tiles_before<KT>(a, a.cache.B, units, lane);
+  const long long total = places_before<KIND>(a, a.cache.B, units, lane);
   const long long per = run_length(total, gridDim.x);
   long long cur = per * blockIdx.x;
   const long long end = cur + per < total ? cur + per : total;
@@ -890,23 +904,27 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_
       }
     }
   if (cur >= end) return;
-  long long base;  // tiles before sequence u.b
-  u.b = seq_of<KT>(a, cur, units, lane, base);
+  long long base;  // places before sequence u.b
+  u.b = seq_of<KIND>(a, cur, units, lane, base);
   u.t_first = 0;
   u.rows = a.T * a.G;
   u.sel = nullptr;
-  int slot = 0;
   while (cur < end) {
     u.n = seq_len(a, u.b, over);
     const int nt = (u.n + KT - 1) / KT;  // tiles of a unit of this sequence
-    if (nt == 0 || cur >= base + (long long)nt * units) {  // on to the next sequence
-      base += (long long)nt * units;
+    const int places = unit_places<KIND>(nt);
+    if (nt == 0 || cur >= base + (long long)places * units) {  // on to the next sequence
+      base += (long long)places * units;
       ++u.b;
       continue;
     }
-    // (tiles of one sequence: below 2^22 * 32 heads * 16 row tiles, within 32 bits)
-    const unsigned at = (unsigned)(cur - base), un = at / (unsigned)nt;
-    const int i0 = (int)(at - un * nt);
+    // (places of one sequence: below 2^22 * 32 heads * 16 row tiles + 2^15, within 32 bits)
+    const unsigned at = (unsigned)(cur - base), un = at / (unsigned)places;
+    const int i0 = (int)(at - un * places);
+    if (i0 >= nt) {  // behind a unit's tiles
+      cur += places - i0;
+      continue;
+    }
     const int i1 = (int)(end - cur < nt - i0 ? i0 + (end - cur) : nt);
     u.kv = un / RT;
     u.r0 = (un % RT) * 16;
@@ -922,8 +940,8 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_
       const float4 acc = merged<W>(mo, ml, row, quad, m, l);
       if (i0 == 0 && i1 == nt) {
         write_out(a, u, row, quad, acc, l);
-      } else {  // slot 0: the run's first unit, slot 1: its last
-        float* p = a.part + ((long long)blockIdx.x * 2 + slot) * kPartFloats;
+      } else {  // slot 1: a unit that begins in the run, slot 0: one that began before
+        float* p = a.part + ((long long)blockIdx.x * 2 + (i0 == 0)) * kPartFloats;
         *reinterpret_cast<float4*>(p + row * 64 + 4 * quad) = acc;
         if (quad == 0) {
           p[1024 + row] = m;
@@ -931,19 +949,18 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_
         }
       }
     }
-    slot = 1;
-    cur += i1 - i0;
+    cur += i1 < nt ? i1 - i0 : places - i0;
     __syncthreads();  // the merge buffers are free again
   }
 }
 
 // Joins the partial results of the units that lie in several runs.  At most one such unit
-// begins in a run: the one that holds the run's last tile.  Four CTAs a run, four rows each:
+// begins in a run: the one that holds the run's last place.  Four CTAs a run, four rows each:
 // 4 rows x 16 quads x 4 groups of partials.  The kernel starts while the one before it runs,
 // and reads the lengths, which that one only reads too; the partial results after the wait,
 // which every CTA passes (a grid that ended without it would let the next kernel of the
 // stream overtake the one before).
-template <int KT>
+template <int KIND>
 __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, int grid) {
   __shared__ float4 so[4][4][16];
   __shared__ float sm[4][4], sl[4][4];
@@ -952,28 +969,26 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, in
   const int quad = threadIdx.x & 15, rq = (threadIdx.x >> 4) & 3, grp = threadIdx.x >> 6;
   const int RT = (a.T * a.G + 15) / 16, units = a.cache.Hkv * RT;
   const int c0 = blockIdx.x >> 2, row = (blockIdx.x & 3) * 4 + rq;
-  const long long total = tiles_before<KT>(a, a.cache.B, units, lane);
+  const long long total = places_before<KIND>(a, a.cache.B, units, lane);
   const long long per = run_length(total, grid);
   const long long end = per * (c0 + 1);  // the run's end, if the stream goes on after it
   bool cut = end < total;
   Unit u;
   int c1 = 0;
-  bool first = false;  // whether the unit begins with its run
   if (cut) {
     long long base;
-    u.b = seq_of<KT>(a, end - 1, units, lane, base);
+    u.b = seq_of<KIND>(a, end - 1, units, lane, base);
     bool over;
     u.n = seq_len(a, u.b, over);
-    const int nt = (u.n + KT - 1) / KT;
-    const unsigned un = (unsigned)(end - 1 - base) / (unsigned)nt;
+    const int nt = (u.n + Cfg<KIND>::KT - 1) / Cfg<KIND>::KT, places = unit_places<KIND>(nt);
+    const unsigned un = (unsigned)(end - 1 - base) / (unsigned)places;
     u.kv = un / RT;
     u.r0 = (un % RT) * 16;
     u.rows = a.T * a.G;
     u.t_first = 0;
     u.sel = nullptr;
-    const long long w0 = base + (long long)un * nt, w1 = w0 + nt;
+    const long long w0 = base + (long long)un * places, w1 = w0 + nt;
     cut = w1 > end && w0 >= end - per;
-    first = w0 == end - per;
     c1 = (int)((w1 - 1) / per);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -982,7 +997,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, in
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int c = c0 + grp; c <= c1; c += 4) {
-    const int slot = c == c0 && !first ? 1 : 0;
+    const int slot = c == c0 ? 1 : 0;
     const float* p = a.part + ((long long)c * 2 + slot) * kPartFloats;
     const float mc = p[1024 + row], lc = p[1040 + row];
     const float4 x = *reinterpret_cast<const float4*>(p + row * 64 + 4 * quad);
@@ -1025,12 +1040,11 @@ static cudaError_t launch_direct(const CacheAttendLaunch& L, unsigned units, cud
 }
 
 // Whether the direct form takes whole caches of up to `cap` tokens.  It saves the second kernel and
-// each run's changes of unit.  Direct / split, us a call for full tables, 4 bits (bf16):
-//   units x tokens  64 x 4096 13.6 / 15.3 (16.8 / 19.3)   256 x 4096 24.0 / 34.9 (42.6 / 50.1)
-//                   128 x 8192 24.4 / 29.8 (42.7 / 47.6)  1024 x 4096 71.2 / 108.7 (162 / 173)
-// It loses where units are few for their length (8 x 4096 16.4 / 14.4, 64 x 8192 26.7 / 25.0, with
-// each call's launch), and where few of many units are long: 256 x 16384 full 80.2 / 86.0,
-// ragged 78.7 / 68.0 (156.7 / 166.1, 112.1 / 106.4).
+// each run's changes of unit.  Direct / split, us a call, 4 bits (bf16), two KV heads:
+//   units x tokens  32 x 1500 7.4 / 8.3 (7.9 / 10.0)       64 x 4096 13.6 / 14.1 (16.7 / 18.7)
+//                   256 x 4096 23.9 / 34.0 (42.8 / 50.0)   128 x 8192 24.4 / 29.3 (42.5 / 47.7)
+// It loses where units are few for their length (8 x 4096 13.1 / 8.2, 64 x 8192 23.4 / 19.0), and
+// where few of many units are long (256 x 16384 full 76.3 / 79.7, ragged 73.7 / 53.5).
 inline bool takes_direct(long long cap, long long units) {
   const long long most = 64 * units < 8192 ? 64 * units : 8192;
   return cap <= (most > 2048 ? most : 2048);
@@ -1052,7 +1066,7 @@ static cudaError_t launch_attend(const CacheAttendLaunch& L, cudaStream_t s) {
   cudaError_t e = launch_early<cache_attend_split_kernel<KIND, U, NP>>(kCaGrid, C::kWarps * 32,
                                                                        attend_smem<KIND, C::kWarps>(), s, L);
   if (e != cudaSuccess) return e;
-  return launch_early<cache_join_kernel<C::KT>>(kCaGrid * 4, 256, 0, s, L, kCaGrid);
+  return launch_early<cache_join_kernel<KIND>>(kCaGrid * 4, 256, 0, s, L, kCaGrid);
 }
 
 template <int KIND, int U>
