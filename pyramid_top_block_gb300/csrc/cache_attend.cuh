@@ -31,7 +31,7 @@ namespace pisa {
 
 constexpr int kPartFloats = 16 * 64 + 32;  // a partial result: O [16][64], row maxima, row sums
 constexpr int kCaGrid = 152;               // CTAs of the split form: one on each SM
-constexpr int kCaMinTiles = 12;            // places a CTA of the split form takes at least
+constexpr int kCaMinTiles = 12;            // places of the stream that a run has at least
 constexpr float kLog2e = 1.4426950408889634f;
 
 inline size_t part_bytes() { return (size_t)kCaGrid * 2 * kPartFloats * sizeof(float); }
@@ -954,49 +954,72 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_
   }
 }
 
-// Joins the partial results of the units that lie in several runs.  At most one such unit
-// begins in a run: the one that holds the run's last place.  Four CTAs a run, four rows each:
-// 4 rows x 16 quads x 4 groups of partials.  The kernel starts while the one before it runs,
-// and reads the lengths, which that one only reads too; the partial results after the wait,
-// which every CTA passes (a grid that ended without it would let the next kernel of the
-// stream overtake the one before).
-template <int KIND>
+// Joins the partial results of the units that lie in several runs.
+//   FEW: 16 CTAs a unit, one row each: 16 quads x 16 groups of partials (few units are cut into
+//     many runs each: a call for one sequence, two units, of 131072 tokens 15.0 -> 12.4 us).
+//   else: at most one such unit begins in a run, the one that holds the run's last place.  Four
+//     CTAs a run, four rows each: 4 rows x 16 quads x 4 groups of partials.
+// The kernel starts while the one before it runs, and reads the lengths, which that one only
+// reads too; the partial results after the wait, which every CTA passes (a grid that ended
+// without it would let the next kernel of the stream overtake the one before).
+template <int KIND, bool FEW>
 __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, int grid) {
-  __shared__ float4 so[4][4][16];
-  __shared__ float sm[4][4], sl[4][4];
+  constexpr int KT = Cfg<KIND>::KT;
+  constexpr int kRows = FEW ? 1 : 4, kGroups = 16 / kRows;
+  __shared__ float4 so[kGroups][kRows][16];
+  __shared__ float sm[kGroups][kRows], sl[kGroups][kRows];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const int quad = threadIdx.x & 15, rq = (threadIdx.x >> 4) & 3, grp = threadIdx.x >> 6;
+  const int quad = threadIdx.x & 15, rq = (threadIdx.x >> 4) % kRows, grp = (threadIdx.x >> 4) / kRows;
   const int RT = (a.T * a.G + 15) / 16, units = a.cache.Hkv * RT;
-  const int c0 = blockIdx.x >> 2, row = (blockIdx.x & 3) * 4 + rq;
+  const int row = (int)(blockIdx.x % (16 / kRows)) * kRows + rq;
   const long long total = places_before<KIND>(a, a.cache.B, units, lane);
   const long long per = run_length(total, grid);
-  const long long end = per * (c0 + 1);  // the run's end, if the stream goes on after it
-  bool cut = end < total;
   Unit u;
-  int c1 = 0;
-  if (cut) {
-    long long base;
-    u.b = seq_of<KIND>(a, end - 1, units, lane, base);
-    bool over;
-    u.n = seq_len(a, u.b, over);
-    const int nt = (u.n + Cfg<KIND>::KT - 1) / Cfg<KIND>::KT, places = unit_places<KIND>(nt);
-    const unsigned un = (unsigned)(end - 1 - base) / (unsigned)places;
+  int c0, c1 = 0;  // the runs that hold its tiles
+  bool cut;
+  auto set_unit = [&](unsigned un) {  // the unit's number in its sequence
     u.kv = un / RT;
     u.r0 = (un % RT) * 16;
     u.rows = a.T * a.G;
     u.t_first = 0;
     u.sel = nullptr;
-    const long long w0 = base + (long long)un * places, w1 = w0 + nt;
-    cut = w1 > end && w0 >= end - per;
-    c1 = (int)((w1 - 1) / per);
+  };
+  if (FEW) {
+    const unsigned id = blockIdx.x / 16;
+    u.b = id / units;
+    const unsigned un = id % units;
+    set_unit(un);
+    bool over;
+    u.n = seq_len(a, u.b, over);
+    const int nt = (u.n + KT - 1) / KT;
+    const long long w0 = places_before<KIND>(a, u.b, units, lane) + (long long)un * unit_places<KIND>(nt);
+    c0 = (int)(w0 / per);
+    c1 = (int)((w0 + nt - 1) / per);
+    cut = nt != 0 && c0 != c1;
+  } else {
+    c0 = blockIdx.x / 4;
+    const long long end = per * (c0 + 1);  // the run's end, if the stream goes on after it
+    cut = end < total;
+    if (cut) {
+      long long base;
+      u.b = seq_of<KIND>(a, end - 1, units, lane, base);
+      bool over;
+      u.n = seq_len(a, u.b, over);
+      const int nt = (u.n + KT - 1) / KT, places = unit_places<KIND>(nt);
+      const unsigned un = (unsigned)(end - 1 - base) / (unsigned)places;
+      set_unit(un);
+      const long long w0 = base + (long long)un * places, w1 = w0 + nt;
+      cut = w1 > end && w0 >= end - per;
+      c1 = (int)((w1 - 1) / per);
+    }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!cut) return;
   float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int c = c0 + grp; c <= c1; c += 4) {
+  for (int c = c0 + grp; c <= c1; c += kGroups) {
     const int slot = c == c0 ? 1 : 0;
     const float* p = a.part + ((long long)c * 2 + slot) * kPartFloats;
     const float mc = p[1024 + row], lc = p[1040 + row];
@@ -1017,11 +1040,13 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, in
   }
   __syncthreads();
   if (grp) return;
-  m = fmaxf(fmaxf(sm[0][rq], sm[1][rq]), fmaxf(sm[2][rq], sm[3][rq]));
+  m = sm[0][rq];
+#pragma unroll
+  for (int x = 1; x < kGroups; ++x) m = fmaxf(m, sm[x][rq]);
   acc = make_float4(0.f, 0.f, 0.f, 0.f);
   l = 0.f;
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
+  for (int x = 0; x < kGroups; ++x) {
     const float mx = sm[x][rq], lx = sl[x][rq];
     const float f = mx == -INFINITY ? 0.f : ex2_approx(mx - m);
     const float4 v = so[x][rq][quad];
@@ -1066,7 +1091,9 @@ static cudaError_t launch_attend(const CacheAttendLaunch& L, cudaStream_t s) {
   cudaError_t e = launch_early<cache_attend_split_kernel<KIND, U, NP>>(kCaGrid, C::kWarps * 32,
                                                                        attend_smem<KIND, C::kWarps>(), s, L);
   if (e != cudaSuccess) return e;
-  return launch_early<cache_join_kernel<KIND>>(kCaGrid * 4, 256, 0, s, L, kCaGrid);
+  if (units <= kCaGrid / 4)
+    return launch_early<cache_join_kernel<KIND, true>>((unsigned)units * 16, 256, 0, s, L, kCaGrid);
+  return launch_early<cache_join_kernel<KIND, false>>(kCaGrid * 4, 256, 0, s, L, kCaGrid);
 }
 
 template <int KIND, int U>
