@@ -9,12 +9,12 @@
 // keys, and the CTA's warps are merged through shared memory at the end.
 //
 // What bounds it.  Per key and KV head 72 or 256 bytes are read.  bf16 pages: the memory;
-// 8 ragged sequences up to 131072 tokens (384 MB) take 65.7 us = 5.84 TB/s, and a plain
+// 8 ragged sequences up to 131072 tokens (384 MB) take 62.2 us = 6.17 TB/s, and a plain
 // read-only sweep of as many bytes 59.5 us.  4-bit pages: the arithmetic; 16 x 131072 tokens
-// (302 MB) take 74.8 us = 4.04 TB/s, without the copies 63, without the products 50.  A tile of
-// 64 keys costs 64 HMMA of 8 clocks and 128 HMUL2 of 2 on each scheduler, which do not overlap
-// on this machine, beside 157 conversions and 37 logic operations on the other pipe (which
-// do): about 250 clocks of an SM a tile, where the tile's bytes take 196.
+// (302 MB) take 71.1 us = 4.25 TB/s.  A tile of 64 keys costs 64 HMMA of 8 clocks and 128 HMUL2
+// of 2 on its scheduler, which do not overlap on this machine, beside 157 conversions and 37
+// logic operations on the other pipe (which do): about 250 clocks of an SM a tile, of the 285
+// that it takes; the tile's bytes take 196.
 //
 // Three forms (launch_attend chooses):
 //   direct, 4 to 12 warps a CTA: one CTA per unit (sequence, KV head and query, or row tile),
