@@ -45,6 +45,13 @@ struct Cfg<PISA_CACHE_BF16> {
   static constexpr int kHalf = 4, kThird = 4;  // of the direct form where two CTAs, or more, share an SM
   static constexpr int kStages = 3;
   static constexpr int kRow = kRowBf16;
+  // Whether the split form's CTAs take a run's row tiles side by side, one each, so that they read
+  // the same pages at the same time; else the row tiles are units of the stream like others.
+  // Side by side / in the stream, us a call, two KV heads, G = 16 unless said:
+  //   bf16    4 x 65536 T = 2 31.1 / 44.5, T = 8 94.0 / 138   16 x 16384 T = 8, 8 heads, G = 4 100 / 158
+  //           (T = 16 ragged 139 / 134, one short sequence T = 9 33.0 / 31.5)
+  //   4 bits  4 x 65536 T = 2 25.4 / 25.3, T = 8 75.1 / 71.4 (bound by the arithmetic; some CTAs are left over)
+  static constexpr bool kSide = true;
   static constexpr int kChange = 36;  // places of the stream that a unit's end counts as (see unit_places)
   static constexpr float kShift = 0.f;  // weights are held times 2^kShift
   static constexpr float kSlack = 20.f;  // how far (base 2) a logit may pass the row's reference
@@ -56,6 +63,7 @@ struct Cfg<PISA_CACHE_E2M1> {
   static constexpr int kHalf = 6, kThird = 4;
   static constexpr int kStages = 3;
   static constexpr int kRow = kRowE2m1;
+  static constexpr bool kSide = false;
   static constexpr int kChange = 24;
   static constexpr float kShift = 10.f;
   static constexpr float kSlack = 5.f;
@@ -883,12 +891,12 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_
   Unit u;
   bool over;
   const int blk[2] = {-1, -1};
-  // this CTA's run of the stream
+  // this CTA's run of the stream (and its row tile, where the row tiles go side by side)
   const int RT = (a.T * a.G + 15) / 16;
-  const int units = a.cache.Hkv * RT;  // of a sequence
+  const int units = a.cache.Hkv * (C::kSide ? 1 : RT);  // of a sequence
   const long long total = places_before<KIND>(a, a.cache.B, units, lane);
-  const long long per = run_length(total, gridDim.x);
-  long long cur = per * blockIdx.x;
+  const long long per = run_length(total, C::kSide ? gridDim.x / RT : gridDim.x);
+  long long cur = per * (C::kSide ? blockIdx.x / RT : blockIdx.x);
   const long long end = cur + per < total ? cur + per : total;
   // sequences without tokens: zeros
   for (int b = blockIdx.x; b < a.cache.B; b += gridDim.x)
@@ -903,7 +911,7 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_
         }
       }
     }
-  if (cur >= end) return;
+  if (cur >= end) return;  // (CTAs left over where RT does not divide the grid, too)
   long long base;  // places before sequence u.b
   u.b = seq_of<KIND>(a, cur, units, lane, base);
   u.t_first = 0;
@@ -926,8 +934,8 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_
       continue;
     }
     const int i1 = (int)(end - cur < nt - i0 ? i0 + (end - cur) : nt);
-    u.kv = un / RT;
-    u.r0 = (un % RT) * 16;
+    u.kv = C::kSide ? un : un / RT;
+    u.r0 = ((C::kSide ? blockIdx.x : un) % RT) * 16;
     QueryWords q;
     fetch_q(a, u, lane, q);
     reset(s);
@@ -958,7 +966,7 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_
 //   FEW: 16 CTAs a unit, one row each: 16 quads x 16 groups of partials (few units are cut into
 //     many runs each: a call for one sequence, two units, of 131072 tokens 15.0 -> 12.4 us).
 //   else: at most one such unit begins in a run, the one that holds the run's last place.  Four
-//     CTAs a run, four rows each: 4 rows x 16 quads x 4 groups of partials.
+//     CTAs a run and row tile, four rows each: 4 rows x 16 quads x 4 groups of partials.
 // The kernel starts while the one before it runs, and reads the lengths, which that one only
 // reads too; the partial results after the wait, which every CTA passes (a grid that ended
 // without it would let the next kernel of the stream overtake the one before).
@@ -971,24 +979,28 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, in
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int quad = threadIdx.x & 15, rq = (threadIdx.x >> 4) % kRows, grp = (threadIdx.x >> 4) / kRows;
-  const int RT = (a.T * a.G + 15) / 16, units = a.cache.Hkv * RT;
+  constexpr bool kSide = Cfg<KIND>::kSide;
+  const int RT = (a.T * a.G + 15) / 16, side = kSide ? RT : 1;
+  const int runs = kSide ? grid / RT : grid, units = kSide ? a.cache.Hkv : a.cache.Hkv * RT;
   const int row = (int)(blockIdx.x % (16 / kRows)) * kRows + rq;
   const long long total = places_before<KIND>(a, a.cache.B, units, lane);
-  const long long per = run_length(total, grid);
+  const long long per = run_length(total, runs);
   Unit u;
   int c0, c1 = 0;  // the runs that hold its tiles
+  int beside;      // which of the row tiles side by side
   bool cut;
   auto set_unit = [&](unsigned un) {  // the unit's number in its sequence
-    u.kv = un / RT;
-    u.r0 = (un % RT) * 16;
+    u.kv = kSide ? un : un / RT;
+    u.r0 = (kSide ? beside : un % RT) * 16;
     u.rows = a.T * a.G;
     u.t_first = 0;
     u.sel = nullptr;
   };
   if (FEW) {
-    const unsigned id = blockIdx.x / 16;
-    u.b = id / units;
-    const unsigned un = id % units;
+    const unsigned id = blockIdx.x / 16, unit = kSide ? id / RT : id;
+    beside = kSide ? id - unit * RT : 0;
+    u.b = unit / units;
+    const unsigned un = unit % units;
     set_unit(un);
     bool over;
     u.n = seq_len(a, u.b, over);
@@ -998,7 +1010,9 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, in
     c1 = (int)((w0 + nt - 1) / per);
     cut = nt != 0 && c0 != c1;
   } else {
-    c0 = blockIdx.x / 4;
+    const int cta = blockIdx.x / 4;
+    c0 = kSide ? cta / RT : cta;
+    beside = kSide ? cta - c0 * RT : 0;
     const long long end = per * (c0 + 1);  // the run's end, if the stream goes on after it
     cut = end < total;
     if (cut) {
@@ -1021,7 +1035,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, in
 #pragma unroll 4
   for (int c = c0 + grp; c <= c1; c += kGroups) {
     const int slot = c == c0 ? 1 : 0;
-    const float* p = a.part + ((long long)c * 2 + slot) * kPartFloats;
+    const float* p = a.part + (((long long)c * side + beside) * 2 + slot) * kPartFloats;
     const float mc = p[1024 + row], lc = p[1040 + row];
     const float4 x = *reinterpret_cast<const float4*>(p + row * 64 + 4 * quad);
     const float n = fmaxf(m, mc);

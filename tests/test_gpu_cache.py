@@ -797,3 +797,26 @@ def test_many_sequences_in_a_wide_table(bits):
     for b in [b for b in range(B) if b % 16 == 1 or lengths[b] < 3]:
         one = pisa.PagedCache(cache.pages, table[b:b + 1].contiguous(), 64)
         check_attention(one, q[b:b + 1], lengths[b:b + 1], out[b:b + 1])
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("B,T,G,Hkv,page,lengths", [
+    (2, 3, 16, 2, 64, [9000, 777]),
+    (1, 5, 16, 1, 32, [30011]),
+    (3, 9, 16, 3, 16, [4097, 8, 10001]),
+    (40, 4, 8, 1, 64, [9001] + [(37 * b) % 1900 for b in range(1, 40)]),
+])
+def test_several_row_tiles_over_runs(bits, B, T, G, Hkv, page, lengths):
+    """Queries of 2 to 9 row tiles, which do not divide the grid, over units that lie in several runs."""
+    g = gen(B * 100 + T + 2)
+    cache = make_cache(g, B, max(lengths) + 40, Hkv, page, bits)
+    q = normal(g, B, T, G * Hkv, 64)
+    ws = pisa.cache_workspace(cache)
+    out = torch.full((B, T, G * Hkv, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    pisa.cache_attention(q, cache, i32(lengths), out=out, workspace=ws)
+    assert status(ws) == 0
+    check_attention(cache, q, lengths, out)
+    o32 = torch.full(out.shape, 7.0, dtype=torch.float32, device=DEV)
+    pisa.cache_attention(q, cache, i32(lengths), out=o32, workspace=ws)
+    check_attention(cache, q, lengths, o32)
+    assert torch.equal(pisa.cache_attention(q, cache, i32(lengths), workspace=ws), out)
