@@ -820,3 +820,20 @@ def test_several_row_tiles_over_runs(bits, B, T, G, Hkv, page, lengths):
     pisa.cache_attention(q, cache, i32(lengths), out=o32, workspace=ws)
     check_attention(cache, q, lengths, o32)
     assert torch.equal(pisa.cache_attention(q, cache, i32(lengths), workspace=ws), out)
+
+
+@pytest.mark.parametrize("n", [1, 100, 9000])
+def test_rows_whose_logits_are_all_minus_infinity(n):
+    """They get zeros, like rows that see nothing; the other rows of the tile are as ever."""
+    g = gen(23)
+    cache = make_cache(g, 1, n, 1, 64, 16)
+    cache.pages[:, :, :, 0, :, 5] = float("-inf")
+    q = normal(g, 1, 1, 16, 64)
+    q[..., 5] = 0.5
+    out = pisa.cache_attention(q, cache, i32([n]))
+    assert bool((out == 0).all())
+    one = int(cache.table[0, 0])
+    cache.pages[one, 0, 0, 0, 0, 5] = 0.25  # token 0 is finite: it has all the weight
+    out = pisa.cache_attention(q, cache, i32([n]))
+    want = cache.pages[one, 0, 0, 1, 0]
+    assert torch.equal(out[0, 0], want.expand(16, 64))
