@@ -5,10 +5,12 @@
 //   a' = a c - b s,  b' = b c + a s
 // Eight lanes hold one row of 64 (16 bytes each), a warp four rows.  In the split-halves
 // order the other member of a pair is rot/2 dims away, which is a whole number of lanes, so
-// it comes by shuffle; in the interleaved order it is the neighbouring element.
+// it comes by shuffle; in the interleaved order it is the neighbouring element.  Query rows
+// that turn as a whole in halves have four lanes, each with both members of eight pairs: no
+// shuffle, and each element is unpacked once (53.2 -> 50.7 us for 32768 tokens).
 //
 // Both kernels only move rows, so the bytes of the rows in and out bound them.  Measured: 32768
-// tokens of 32 + 2 + 2 heads into bf16 pages (319 MB) 56.3 us = 5.66 TB/s; 131072 tokens of 2
+// tokens of 32 + 2 + 2 heads into bf16 pages (319 MB) 50.7 us = 6.29 TB/s; 131072 tokens of 2
 // heads read back from 4 bits (86 MB) 16.4 us = 5.24 TB/s; 65 single tokens 4.2 us.
 #include "cache.cuh"
 
@@ -63,6 +65,45 @@ __device__ __forceinline__ void rotate8(uint32_t (&w)[4], const uint32_t (&o)[4]
   for (int k = 0; k < 4; ++k) w[k] = lo[k];
 }
 
+// Both members of eight pairs (a, b), from the same lane: a' = a c - b s, b' = b c + a s, the same
+// bits as rotate8 gives.
+__device__ __forceinline__ void rotate_pairs(uint32_t (&a)[4], uint32_t (&b)[4], const float (&c)[8],
+                                             const float (&s)[8], bool there) {
+  uint32_t na[4], nb[4], differ = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float r[2][2], e[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float x = __uint_as_float(h ? a[k] & 0xffff0000u : a[k] << 16);
+      const float y = __uint_as_float(h ? b[k] & 0xffff0000u : b[k] << 16);
+      const float m = y * -s[2 * k + h], n = x * s[2 * k + h];
+      r[0][h] = fmaf(x, c[2 * k + h], m);
+      r[1][h] = fmaf(y, c[2 * k + h], n);
+      e[0][h] = (fabsf(m) + fabsf(r[0][h])) * 0x1p-23f;
+      e[1][h] = (fabsf(n) + fabsf(r[1][h])) * 0x1p-23f;
+    }
+    na[k] = pack_bf16x2(r[0][0] - e[0][0], r[0][1] - e[0][1]);
+    nb[k] = pack_bf16x2(r[1][0] - e[1][0], r[1][1] - e[1][1]);
+    differ |= na[k] ^ pack_bf16x2(r[0][0] + e[0][0], r[0][1] + e[0][1]);
+    differ |= nb[k] ^ pack_bf16x2(r[1][0] + e[1][0], r[1][1] + e[1][1]);
+  }
+  if (differ && there) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float x0 = __uint_as_float(a[k] << 16), x1 = __uint_as_float(a[k] & 0xffff0000u);
+      const float y0 = __uint_as_float(b[k] << 16), y1 = __uint_as_float(b[k] & 0xffff0000u);
+      na[k] = pack_bf16x2(sum2(x0, c[2 * k], y0, -s[2 * k]), sum2(x1, c[2 * k + 1], y1, -s[2 * k + 1]));
+      nb[k] = pack_bf16x2(sum2(y0, c[2 * k], x0, s[2 * k]), sum2(y1, c[2 * k + 1], x1, s[2 * k + 1]));
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    a[k] = na[k];
+    b[k] = nb[k];
+  }
+}
+
 // The 4-bit form of a row: this lane's 8 of 64 values (bf16 pairs w) and, with the
 // neighbouring lane's, the scale of their 16.  Steps, each exact or rounded once:
 //   top = largest |x| (compared as integers, so that an infinity or a NaN is the largest)
@@ -102,12 +143,17 @@ __device__ __forceinline__ void quantise8(const uint32_t (&w)[4], int exp, uint3
 
 // The rotation of this lane's 8 dims at one position.
 struct Turn {
-  float c[8], s[8];  // cosines and signed sines
+  float c[8], s[8];  // cosines and (signed) sines
   int from;          // lane that holds the pairs' other members (split halves)
   bool on;           // whether the dims turn at all
 };
 
-template <bool INTER>
+// Whether a query row's pairs lie in one lane: the two halves of a row that turns as a whole.
+template <bool INTER, bool FULL>
+constexpr bool kPairs = FULL && !INTER;
+
+// SIGN: the sines of a row's low half are negated.
+template <bool INTER, bool SIGN>
 __device__ __forceinline__ void load_turn(const CacheAppendLaunch& a, long long p, int lane, Turn& t) {
   const int c = lane & 7;
   const int half = a.rot >> 4;  // lanes of one half of the rotated dims (split-halves order)
@@ -140,7 +186,7 @@ __device__ __forceinline__ void load_turn(const CacheAppendLaunch& a, long long 
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       t.c[e] = uu[e];
-      t.s[e] = low ? -vv[e] : vv[e];
+      t.s[e] = SIGN && low ? -vv[e] : vv[e];
     }
   }
 }
@@ -174,17 +220,29 @@ __global__ void __launch_bounds__(kAppWarps * 32, 6) cache_append_kernel(CacheAp
   const int Hkv = a.cache.Hkv, Hq = a.q.data ? a.Hq : 0;
   // (a prompt's rows behind its count are not even read; a single token's are, rather than wait)
   if (a.T > 1 && a.counts && t >= a.counts[b]) return;
-  const int gq = (Hq + 3) >> 2, groups = gq + ((2 * Hkv + 3) >> 2);
-  // the rows this lane has a part in: query row 4 i + sub of group i, row 4 (i - gq) + sub of
+  // PAIRS: a lane has dims 8 (lane & 3) .. + 7 of a query row, whose angles load_turn gives it, and
+  // their partners 32 dims on; a group is eight rows.  Else as in key and value rows.
+  constexpr bool PAIRS = kPairs<INTER, FULL>;
+  constexpr int kRows = PAIRS ? 8 : 4;
+  const int qsub = PAIRS ? lane >> 2 : sub, qcol = PAIRS ? 8 * (lane & 3) : 8 * c;
+  const int gq = (Hq + kRows - 1) / kRows, groups = gq + ((2 * Hkv + 3) >> 2);
+  // the rows this lane has a part in: query row kRows i + qsub of group i, row 4 (i - gq) + sub of
   // keys and values
-  const __nv_bfloat16* qs = a.q.data + b * a.q.sb + t * a.q.st + (4 * part + sub) * a.q.sh + 8 * c;
-  const long long step = 4 * parts * a.q.sh;
-  uint4 x[kAppBatch];
+  const __nv_bfloat16* qs = a.q.data + b * a.q.sb + t * a.q.st + (kRows * part + qsub) * a.q.sh + qcol;
+  const long long step = kRows * parts * a.q.sh;
+  constexpr int kTurns = PAIRS ? 1 : kAppBatch;  // groups of a batch
+  const int turns = kTurns * parts;
+  auto fetch_q = [&](int i, uint4 (&z)[kAppBatch]) {
 #pragma unroll
-  for (int n = 0; n < kAppBatch; ++n) {  // (these loads do not wait for the position)
-    x[n] = make_uint4(0, 0, 0, 0);
-    if (4 * (part + n * parts) + sub < Hq) x[n] = *reinterpret_cast<const uint4*>(qs + n * step);
-  }
+    for (int n = 0; n < kAppBatch; ++n) {
+      z[n] = make_uint4(0, 0, 0, 0);
+      const int g = PAIRS ? i : i + n * parts;
+      if (kRows * g + qsub < Hq) z[n] = *reinterpret_cast<const uint4*>(PAIRS ? qs + 32 * n : qs + n * step);
+    }
+    qs += kTurns * step;
+  };
+  uint4 x[kAppBatch];
+  fetch_q(part, x);  // (these loads do not wait for the position)
   int ikv = part - gq;
   if (ikv < 0) ikv += (-ikv + parts - 1) / parts * parts;
   auto fetch_kv = [&](int i) {
@@ -216,26 +274,27 @@ __global__ void __launch_bounds__(kAppWarps * 32, 6) cache_append_kernel(CacheAp
   Turn turn;
   if (ok) {
     page = __ldg(a.cache.table + (long long)b * a.cache.max_pages + (p >> a.cache.page_shift));
-    load_turn<INTER>(a, p, lane, turn);
+    load_turn<INTER, !kPairs<INTER, FULL>>(a, p, lane, turn);
     ok = page >= 0 && page < a.cache.n_pages;
   }
   if (!ok) {  // the token is left out
     if (lane == 0) set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
     return;
   }
-  __nv_bfloat16* qd = a.q_out.data + b * a.q_out.sb + t * a.q_out.st + sub * a.q_out.sh + 8 * c;
-  const long long step_out = 4 * parts * a.q_out.sh;
-  qd += (long long)(4 * part) * a.q_out.sh;
-  // (two batches a turn, so that neither is copied)
-  auto fetch_q = [&](int i, uint4 (&z)[kAppBatch]) {
-#pragma unroll
-    for (int n = 0; n < kAppBatch; ++n) {
-      z[n] = make_uint4(0, 0, 0, 0);
-      if (4 * (i + n * parts) + sub < Hq) z[n] = *reinterpret_cast<const uint4*>(qs + n * step);
-    }
-    qs += kAppBatch * step;
-  };
+  __nv_bfloat16* qd = a.q_out.data + b * a.q_out.sb + t * a.q_out.st + (kRows * part + qsub) * a.q_out.sh + qcol;
+  const long long step_out = kRows * parts * a.q_out.sh;
   auto put_q = [&](int i, const uint4 (&z)[kAppBatch]) {
+    if constexpr (PAIRS) {
+      const bool there = 8 * i + qsub < Hq;
+      uint32_t u[4] = {z[0].x, z[0].y, z[0].z, z[0].w}, w[4] = {z[1].x, z[1].y, z[1].z, z[1].w};
+      rotate_pairs(u, w, turn.c, turn.s, there);
+      if (there) {
+        *reinterpret_cast<uint4*>(qd) = make_uint4(u[0], u[1], u[2], u[3]);
+        *reinterpret_cast<uint4*>(qd + 32) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      qd += step_out;
+      return;
+    }
 #pragma unroll
     for (int n = 0; n < kAppBatch; ++n) {
       uint32_t w[4] = {z[n].x, z[n].y, z[n].z, z[n].w};
@@ -244,8 +303,7 @@ __global__ void __launch_bounds__(kAppWarps * 32, 6) cache_append_kernel(CacheAp
       qd += step_out;
     }
   };
-  const int turns = kAppBatch * parts;
-  qs += kAppBatch * step;
+  // (two batches a turn, so that neither is copied)
   for (int i = part; i < gq; i += 2 * turns) {
     uint4 y[kAppBatch];
     fetch_q(i + turns, y);
@@ -253,6 +311,10 @@ __global__ void __launch_bounds__(kAppWarps * 32, 6) cache_append_kernel(CacheAp
     if (i + turns >= gq) break;
     fetch_q(i + 2 * turns, x);
     put_q(i + turns, y);
+  }
+  if constexpr (PAIRS) {  // (a query row's two halves have their sines without sign)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) turn.s[e] = c < 4 ? -turn.s[e] : turn.s[e];
   }
   const int U = 1 << a.cache.rec_shift, u = (int)(p & (U - 1));
   for (int i = ikv; i < groups - gq; i += parts) {
@@ -369,7 +431,8 @@ __global__ void __launch_bounds__(256) cache_read_kernel(CacheReadLaunch a) {
 }
 
 cudaError_t launch_cache_append(const CacheAppendLaunch& L, cudaStream_t s) {
-  const int groups = ((L.q.data ? L.Hq : 0) + 3) / 4 + (2 * L.cache.Hkv + 3) / 4;
+  const int rows = L.rot == kD && !L.interleaved ? 8 : 4;  // of a group of query rows (see kPairs)
+  const int groups = ((L.q.data ? L.Hq : 0) + rows - 1) / rows + (2 * L.cache.Hkv + 3) / 4;
   // One warp a token where there are many; where there are few, as many as there are groups
   // of rows, so that a step's latency is one row's.
   const long long tokens = (long long)L.cache.B * L.T;

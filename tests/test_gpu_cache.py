@@ -837,3 +837,34 @@ def test_rows_whose_logits_are_all_minus_infinity(n):
     out = pisa.cache_attention(q, cache, i32([n]))
     want = cache.pages[one, 0, 0, 1, 0]
     assert torch.equal(out[0, 0], want.expand(16, 64))
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,page,bits,rot", [
+    (3, 1, 12, 3, 16, 16, 64), (2, 37, 5, 5, 64, 4, 64), (1, 1, 1, 1, 32, 4, 64), (2, 9, 40, 5, 128, 16, 64),
+    (1, 2500, 8, 1, 64, 4, 64), (2, 30, 12, 3, 64, 16, 48), (2, 30, 20, 5, 16, 4, 32), (1, 31, 1, 1, 64, 16, 16),
+])
+def test_append_of_odd_head_counts(B, T, Hq, Hkv, page, bits, rot):
+    """Query rows that do not fill their last group, in place and out of place."""
+    g = gen(B * 1000 + T + rot)
+    n_cap = T + 70
+    cache = make_cache(g, B, n_cap, Hkv, page, bits, fill=False)
+    before = cache.pages.clone()
+    qkv = normal(g, B, T, Hq + 2 * Hkv, 64)
+    q, k, v = qkv.split([Hq, Hkv, Hkv], 2)
+    start, counts = [5 * b for b in range(B)], [T if b == 0 else T // 2 for b in range(B)]
+    rotary = pisa.rotary_table(n_cap, rot)
+    ws = pisa.cache_workspace(cache)
+    q_out = torch.full((B, T, Hq, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    k_out = torch.full((B, T, Hkv, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    pisa.cache_append(q, k, v, cache, i32(start), rotary, counts=i32(counts), q_out=q_out, k_out=k_out, workspace=ws)
+    assert status(ws) == 0
+    check_append(cache, q, k, v, start, counts, rotary, False, q_out, k_out, before)
+    for b in range(B):
+        assert bool((q_out[b, counts[b]:] == 7).all()) and bool((k_out[b, counts[b]:] == 7).all())
+    whole = qkv.clone()
+    qi, ki, vi = qkv.split([Hq, Hkv, Hkv], 2)
+    pisa.cache_append(qi, ki, vi, cache, i32(start), rotary, counts=i32(counts), q_out=qi, k_out=ki, workspace=ws)
+    for b in range(B):
+        c = counts[b]
+        assert torch.equal(qi[b, :c], q_out[b, :c]) and torch.equal(ki[b, :c], k_out[b, :c])
+        assert torch.equal(qkv[b, c:], whole[b, c:]) and torch.equal(vi[b], whole[b, :, Hq + Hkv:])
