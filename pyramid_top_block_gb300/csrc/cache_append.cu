@@ -110,31 +110,36 @@ __device__ __forceinline__ void rotate_pairs(uint32_t (&a)[4], uint32_t (&b)[4],
 //   scale = e4m3(top 2^-exp / 6), to nearest even, at most 448; code = e2m1(x 2^-exp / scale)
 // x is a bf16 (8 bits) and a border between two codes times the scale has at most 7, so a
 // quotient that is not on a border is at least 2^-10 from it (borders lie in [1/4, 5], and
-// so does any quotient near one).  x times the rounded reciprocal is off by 2^-21 there at
-// most; rounding it to a multiple of 2^-11 (by adding 1.5 * 2^12) puts the quotients that are
-// on a border exactly there and moves no other one across, so the conversion's
-// ties-to-even rule decides them.
+// so does any quotient near one).  x times the reciprocal (off by 2^-23 of itself), rounded
+// once or, with the sum below fused, not at all, is off by 2^-20 there at most; rounding it
+// to a multiple of 2^-11 (by adding 1.5 * 2^12) puts the quotients that are on a border exactly
+// there and moves no other one across, so the conversion's ties-to-even rule decides them.
+// Likewise the scale: six times a border between two e4m3 numbers has at most 7 bits, so a
+// top / 6 that is not a border is at least 2^-8 of itself from it, and 16 bits hold every border.
 __device__ __forceinline__ void quantise8(const uint32_t (&w)[4], int exp, uint32_t& codes, uint32_t& scale) {
   uint32_t t = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
                         __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
   t = max(t & 0xffffu, t >> 16);
   t = max(t, __shfl_xor_sync(kFull, t, 1));
   const float down = exp2i(-exp);
-  const float s = __fdiv_rn(__uint_as_float(t << 16) * down, 6.f);
-  scale = __nv_cvt_float_to_fp8(s, __NV_SATFINITE, __NV_E4M3);
+  // top / 6, off by less than 2^-22 of it, snapped to 16 bits
+  const uint32_t q = (__float_as_uint(__uint_as_float(t << 16) * down * (1.f / 6.f)) + 0x80u) & 0xffffff00u;
+  scale = __nv_cvt_float_to_fp8(__uint_as_float(q), __NV_SATFINITE, __NV_E4M3);
   const float sv = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)scale, __NV_E4M3)));
-  const float inv = sv > 0.f ? __frcp_rn(sv) : 0.f;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(sv));
+  inv = sv > 0.f ? inv * down : 0.f;
   constexpr float kSnap = 6144.f;  // 1.5 * 2^12: sums near it are multiples of 2^-11
-  codes = 0;
+  float z[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float a = __uint_as_float(w[i] << 16) * down * inv, b = __uint_as_float(w[i] & 0xffff0000u) * down * inv;
-    a = (a + kSnap) - kSnap;
-    b = (b + kSnap) - kSnap;
-    uint32_t c;
-    asm("{ .reg .b8 x;\n cvt.rn.satfinite.e2m1x2.f32 x, %2, %1;\n cvt.u32.u8 %0, x; }" : "=r"(c) : "f"(a), "f"(b));
-    codes |= c << (8 * i);
+    z[2 * i] = (__uint_as_float(w[i] << 16) * inv + kSnap) - kSnap;
+    z[2 * i + 1] = (__uint_as_float(w[i] & 0xffff0000u) * inv + kSnap) - kSnap;
   }
+  asm("{ .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n mov.b32 %0, {a, b, c, d}; }"
+      : "=r"(codes)
+      : "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]), "f"(z[4]), "f"(z[5]), "f"(z[6]), "f"(z[7]));
   if (t >= 0x7f80u) {  // an infinity or a NaN among the 16: the block stands for NaNs
     scale = 0x7f;
     codes = 0;
