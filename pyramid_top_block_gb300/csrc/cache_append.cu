@@ -10,7 +10,7 @@
 // shuffle, and each element is unpacked once (53.2 -> 50.7 us for 32768 tokens).
 //
 // Both kernels only move rows, so the bytes of the rows in and out bound them.  Measured: 32768
-// tokens of 32 + 2 + 2 heads into bf16 pages (319 MB) 50.7 us = 6.29 TB/s; 131072 tokens of 2
+// tokens of 32 + 2 + 2 heads into bf16 pages (319 MB) 49.6 us = 6.43 TB/s; 131072 tokens of 2
 // heads read back from 4 bits (86 MB) 16.4 us = 5.24 TB/s; 65 single tokens 4.2 us.
 #include "cache.cuh"
 
@@ -148,7 +148,7 @@ __device__ __forceinline__ void quantise8(const uint32_t (&w)[4], int exp, uint3
 
 // The rotation of this lane's 8 dims at one position.
 struct Turn {
-  float c[8], s[8];  // cosines and (signed) sines
+  float c[8], s[8];  // cosines and signed sines
   int from;          // lane that holds the pairs' other members (split halves)
   bool on;           // whether the dims turn at all
 };
@@ -157,8 +157,7 @@ struct Turn {
 template <bool INTER, bool FULL>
 constexpr bool kPairs = FULL && !INTER;
 
-// SIGN: the sines of a row's low half are negated.
-template <bool INTER, bool SIGN>
+template <bool INTER>
 __device__ __forceinline__ void load_turn(const CacheAppendLaunch& a, long long p, int lane, Turn& t) {
   const int c = lane & 7;
   const int half = a.rot >> 4;  // lanes of one half of the rotated dims (split-halves order)
@@ -191,7 +190,7 @@ __device__ __forceinline__ void load_turn(const CacheAppendLaunch& a, long long 
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       t.c[e] = uu[e];
-      t.s[e] = SIGN && low ? -vv[e] : vv[e];
+      t.s[e] = low ? -vv[e] : vv[e];
     }
   }
 }
@@ -279,7 +278,7 @@ __global__ void __launch_bounds__(kAppWarps * 32, 6) cache_append_kernel(CacheAp
   Turn turn;
   if (ok) {
     page = __ldg(a.cache.table + (long long)b * a.cache.max_pages + (p >> a.cache.page_shift));
-    load_turn<INTER, !kPairs<INTER, FULL>>(a, p, lane, turn);
+    load_turn<INTER>(a, p, lane, turn);
     ok = page >= 0 && page < a.cache.n_pages;
   }
   if (!ok) {  // the token is left out
@@ -298,16 +297,51 @@ __global__ void __launch_bounds__(kAppWarps * 32, 6) cache_append_kernel(CacheAp
         *reinterpret_cast<uint4*>(qd + 32) = make_uint4(w[0], w[1], w[2], w[3]);
       }
       qd += step_out;
-      return;
-    }
+    } else {
 #pragma unroll
-    for (int n = 0; n < kAppBatch; ++n) {
-      uint32_t w[4] = {z[n].x, z[n].y, z[n].z, z[n].w};
-      turn_row<INTER, FULL>(turn, 4 * (i + n * parts) + sub < Hq, w);
-      if (4 * (i + n * parts) + sub < Hq) *reinterpret_cast<uint4*>(qd) = make_uint4(w[0], w[1], w[2], w[3]);
-      qd += step_out;
+      for (int n = 0; n < kAppBatch; ++n) {
+        uint32_t w[4] = {z[n].x, z[n].y, z[n].z, z[n].w};
+        turn_row<INTER, FULL>(turn, 4 * (i + n * parts) + sub < Hq, w);
+        if (4 * (i + n * parts) + sub < Hq) *reinterpret_cast<uint4*>(qd) = make_uint4(w[0], w[1], w[2], w[3]);
+        qd += step_out;
+      }
     }
   };
+  auto put_kv = [&] {
+    const int U = 1 << a.cache.rec_shift, u = (int)(p & (U - 1));
+    for (int i = ikv; i < groups - gq; i += parts) {
+      const int r = 4 * i + sub;
+      const bool is_v = r >= Hkv, there = r < 2 * Hkv;
+      const int kv = is_v ? r - Hkv : r;
+      uint32_t w[4] = {xkv.x, xkv.y, xkv.z, xkv.w};
+      xkv = fetch_kv(i + parts);
+      turn_row<INTER, false>(turn, !is_v && there, w);
+      const uint4 y = make_uint4(w[0], w[1], w[2], w[3]);
+      if (!is_v && a.k_out.data)
+        *reinterpret_cast<uint4*>(a.k_out.data + b * a.k_out.sb + t * a.k_out.st + kv * a.k_out.sh + 8 * c) = y;
+      if (KIND == PISA_CACHE_BF16) {
+        if (there) {
+          unsigned char* rec = a.cache.pages + cache_record(a.cache, kRowBf16, page, kv, p) + (is_v ? U * 128 : 0);
+          *reinterpret_cast<uint4*>(rec + u * 128 + 16 * c) = y;
+        }
+      } else {
+        uint32_t codes, scale;
+        quantise8(w, is_v ? a.cache.v_exp : a.cache.k_exp, codes, scale);
+        if (there) {
+          unsigned char* rec = a.cache.pages + cache_record(a.cache, kRowE2m1, page, kv, p) + (is_v ? U * 36 : 0);
+          *reinterpret_cast<uint32_t*>(rec + u * 32 + 4 * c) = codes;
+          if (!(c & 1)) rec[U * 32 + u * 4 + (c >> 1)] = (unsigned char)scale;
+        }
+      }
+    }
+  };
+  // Keys and values first, while the query rows are on their way (in the interleaved order last,
+  // which is faster there: 51.7 and 55.1 us for 32768 tokens; in halves 50.7 and 49.7).
+  if constexpr (PAIRS) {
+    put_kv();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) turn.s[e] = c < 4 ? -turn.s[e] : turn.s[e];  // (a lane has both halves of a query row)
+  }
   // (two batches a turn, so that neither is copied)
   for (int i = part; i < gq; i += 2 * turns) {
     uint4 y[kAppBatch];
@@ -317,36 +351,7 @@ __global__ void __launch_bounds__(kAppWarps * 32, 6) cache_append_kernel(CacheAp
     fetch_q(i + 2 * turns, x);
     put_q(i + turns, y);
   }
-  if constexpr (PAIRS) {  // (a query row's two halves have their sines without sign)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) turn.s[e] = c < 4 ? -turn.s[e] : turn.s[e];
-  }
-  const int U = 1 << a.cache.rec_shift, u = (int)(p & (U - 1));
-  for (int i = ikv; i < groups - gq; i += parts) {
-    const int r = 4 * i + sub;
-    const bool is_v = r >= Hkv, there = r < 2 * Hkv;
-    const int kv = is_v ? r - Hkv : r;
-    uint32_t w[4] = {xkv.x, xkv.y, xkv.z, xkv.w};
-    xkv = fetch_kv(i + parts);
-    turn_row<INTER, false>(turn, !is_v && there, w);
-    const uint4 y = make_uint4(w[0], w[1], w[2], w[3]);
-    if (!is_v && a.k_out.data)
-      *reinterpret_cast<uint4*>(a.k_out.data + b * a.k_out.sb + t * a.k_out.st + kv * a.k_out.sh + 8 * c) = y;
-    if (KIND == PISA_CACHE_BF16) {
-      if (there) {
-        unsigned char* rec = a.cache.pages + cache_record(a.cache, kRowBf16, page, kv, p) + (is_v ? U * 128 : 0);
-        *reinterpret_cast<uint4*>(rec + u * 128 + 16 * c) = y;
-      }
-    } else {
-      uint32_t codes, scale;
-      quantise8(w, is_v ? a.cache.v_exp : a.cache.k_exp, codes, scale);
-      if (there) {
-        unsigned char* rec = a.cache.pages + cache_record(a.cache, kRowE2m1, page, kv, p) + (is_v ? U * 36 : 0);
-        *reinterpret_cast<uint32_t*>(rec + u * 32 + 4 * c) = codes;
-        if (!(c & 1)) rec[U * 32 + u * 4 + (c >> 1)] = (unsigned char)scale;
-      }
-    }
-  }
+  if constexpr (!PAIRS) put_kv();
 }
 
 // A warp reads kReadBatch groups of four tokens of one head, eight lanes a token.
