@@ -340,7 +340,8 @@ int pisa_cache_read(const pisa_paged_cache* cache, int T, const int32_t* start, 
  *   out     : device [B, T, Hq, d] dense, 16-byte aligned, fp32 (out_f32 != 0) or bf16
  *   ws      : workspace of pisa_cache_workspace_bytes(), 256-byte aligned
  * A query that sees no token, or none whose logit is above minus infinity, gets zeros;
- * tokens that it does not see do not matter, whatever their values.  One that sees a token in a page outside [0, n_pages) gets NaNs,
+ * tokens that it does not see do not matter, whatever their values.  One that sees a
+ * token in a page outside [0, n_pages) gets NaNs,
  * and PISA_ERR_DEVICE_BOUNDS is flagged.  1 <= T <= 16, 1 <= Ksel <= 64, Hq/Hkv in
  * {1, 2, 4, 8, 16}, B * T * Hkv < 2^24.  Sums and softmax in fp32; the weights enter the
  * product with V as two bf16 parts (bf16 pages) or as fp16 (4-bit pages).

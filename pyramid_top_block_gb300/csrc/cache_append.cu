@@ -11,7 +11,7 @@
 //
 // Both kernels only move rows, so the bytes of the rows in and out bound them.  Measured: 32768
 // tokens of 32 + 2 + 2 heads into bf16 pages (319 MB) 49.6 us = 6.43 TB/s; 131072 tokens of 2
-// heads read back from 4 bits (86 MB) 16.4 us = 5.24 TB/s; 65 single tokens 4.2 us.
+// heads read back from 4 bits (86 MB) 15.9 us = 5.41 TB/s; 65 single tokens 1.9 us.
 #include "cache.cuh"
 
 #include <type_traits>

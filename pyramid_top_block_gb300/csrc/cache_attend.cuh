@@ -1097,7 +1097,7 @@ static cudaError_t launch_attend(const CacheAttendLaunch& L, cudaStream_t s) {
   const long long units = (long long)L.cache.B * L.cache.Hkv * (L.idx ? L.T : RT);
   if (L.idx || takes_direct(cap, units)) {
     // The more units there are, the fewer warps share one out, so that all CTAs run at once
-    // (128 x 2 units of 32 blocks: six warps 16.9 us, four 20.2, twelve 22.5).
+    // (128 x 2 units of 32 blocks: six warps 15.1 us, four 18.7, twelve 19.1).
     if (units <= kCaGrid) return launch_direct<KIND, U, NP, C::kWarps>(L, (unsigned)units, s);
     if (units <= 2 * kCaGrid) return launch_direct<KIND, U, NP, C::kHalf>(L, (unsigned)units, s);
     return launch_direct<KIND, U, NP, C::kThird>(L, (unsigned)units, s);
