@@ -122,7 +122,9 @@ struct CacheAttendLaunch {
 };
 
 // The launch is programmatic: a kernel may start while the one before it in the stream ends,
-// and touches memory only after this.
+// and touches memory only after this.  Its loads are plain ones: a read-only load (ld.global.nc)
+// promises that nothing writes the memory while the kernel lives, which begins before the one before
+// has ended, and the compiler may move it ahead of the wait.
 __device__ __forceinline__ void after_the_one_before() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

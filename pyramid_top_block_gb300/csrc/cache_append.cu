@@ -171,8 +171,8 @@ __device__ __forceinline__ void load_turn(const CacheAppendLaunch& a, long long 
   if (!t.on) return;
   const float* row = a.rotary + p * a.rot;
   if (INTER) {
-    const float4 u = __ldg(reinterpret_cast<const float4*>(row + 4 * c));
-    const float4 v = __ldg(reinterpret_cast<const float4*>(row + (a.rot >> 1) + 4 * c));
+    const float4 u = *reinterpret_cast<const float4*>(row + 4 * c);
+    const float4 v = *reinterpret_cast<const float4*>(row + (a.rot >> 1) + 4 * c);
     const float uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -184,7 +184,7 @@ __device__ __forceinline__ void load_turn(const CacheAppendLaunch& a, long long 
     t.from = low ? lane + half : lane - half;
     const float4* u = reinterpret_cast<const float4*>(row + 8 * (low ? c : c - half));
     const float4* v = reinterpret_cast<const float4*>(row + (a.rot >> 1) + 8 * (low ? c : c - half));
-    const float4 u0 = __ldg(u), u1 = __ldg(u + 1), v0 = __ldg(v), v1 = __ldg(v + 1);
+    const float4 u0 = u[0], u1 = u[1], v0 = v[0], v1 = v[1];
     const float uu[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
     const float vv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kAppWarps * 32, 6) cache_append_kernel(CacheAp
   int page = -1;
   Turn turn;
   if (ok) {
-    page = __ldg(a.cache.table + (long long)b * a.cache.max_pages + (p >> a.cache.page_shift));
+    page = a.cache.table[(long long)b * a.cache.max_pages + (p >> a.cache.page_shift)];
     load_turn<INTER>(a, p, lane, turn);
     ok = page >= 0 && page < a.cache.n_pages;
   }
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(256) cache_read_kernel(CacheReadLaunch a) {
     int page = 0;
     ok[i] = t < n;
     if (ok[i]) {
-      page = p >= 0 && p < cap ? __ldg(table + (p >> a.cache.page_shift)) : -1;
+      page = p >= 0 && p < cap ? table[p >> a.cache.page_shift] : -1;
       if (page < 0 || page >= a.cache.n_pages) {
         if (c == 0) set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
         ok[i] = false;

@@ -183,8 +183,8 @@ __device__ __forceinline__ void fetch_q(const CacheAttendLaunch& a, const Unit& 
       const int t = u.t_first + r / a.G, head = u.kv * a.G + r % a.G;
       const uint4* p =
           reinterpret_cast<const uint4*>(a.q.data + u.b * a.q.sb + (long long)t * a.q.st + head * a.q.sh) + 2 * j;
-      x0 = __ldg(p);
-      x1 = __ldg(p + 1);
+      x0 = p[0];
+      x1 = p[1];
     }
     q.w[h][0] = x0.x; q.w[h][1] = x0.y; q.w[h][2] = x0.z; q.w[h][3] = x0.w;
     q.w[h][4] = x1.x; q.w[h][5] = x1.y; q.w[h][6] = x1.z; q.w[h][7] = x1.w;
@@ -608,7 +608,7 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
     if (y < mine) {
       const int p = first_of(y) + (lane % E) * U;
       if (p < see.n_hi) {
-        page = __ldg(table + (p >> a.cache.page_shift));
+        page = table[p >> a.cache.page_shift];
         if (page >= 0 && page < a.cache.n_pages) {
           off = cache_record(a.cache, C::kRow, page, u.kv, p);
           // (bf16: the tile may start inside a record)
@@ -852,7 +852,7 @@ __global__ void __launch_bounds__(W * 32, Cfg<KIND>::kWarps / W) cache_attend_di
     u.sel = a.idx + (((long long)u.b * a.cache.Hkv + u.kv) * a.T + u.t_first) * a.Ksel;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      if (lane + 32 * h < a.Ksel) blk[h] = __ldg(u.sel + lane + 32 * h);
+      if (lane + 32 * h < a.Ksel) blk[h] = u.sel[lane + 32 * h];
   } else {
     const unsigned RT = (a.T * a.G + 15) / 16;
     u.t_first = 0;
