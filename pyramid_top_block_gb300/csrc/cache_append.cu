@@ -22,23 +22,29 @@ constexpr int kAppWarps = 4;
 constexpr int kAppPrefetch = 912;  // tokens ahead (six an SM) whose rows are asked into L2: 61.4 -> 57 us for 32768
 constexpr int kAppBatch = 2;  // groups of four rows whose loads a warp issues together, ahead of their use
 
-// x c + p s rounded to 32 bits from (nearly) twice as many: both products and their sum as
-// unevaluated pairs (the error of a product by fma, that of a sum by Knuth's two-sum).
+// x c + p s rounded to 32 bits from nearly twice as many: both products and their sum as
+// unevaluated pairs (the error of a product by fma, that of a sum by Knuth's two-sum), off by at
+// most 2^-46 (|x c| + |p s|) before the last rounding.  Every step is rounded by itself, by
+// intrinsics: a product fused into one of the sums would count its error twice.
 __device__ __forceinline__ float sum2(float x, float c, float p, float s) {
-  const float h1 = x * c, h2 = p * s;
-  const float l1 = fmaf(x, c, -h1), l2 = fmaf(p, s, -h2);
-  const float h = h1 + h2, z = h - h1;
-  const float l = (h1 - (h - z)) + (h2 - z) + (l1 + l2);
-  return fabsf(h) < INFINITY ? h + l : h;  // (an infinity has no error term)
+  const float h1 = __fmul_rn(x, c), h2 = __fmul_rn(p, s);
+  const float l1 = __fmaf_rn(x, c, -h1), l2 = __fmaf_rn(p, s, -h2);
+  const float h = __fadd_rn(h1, h2), z = __fsub_rn(h, h1);
+  const float e = __fadd_rn(__fsub_rn(h1, __fsub_rn(h, z)), __fsub_rn(h2, z));
+  const float l = __fadd_rn(e, __fadd_rn(l1, l2));
+  return fabsf(h) < INFINITY ? __fadd_rn(h, l) : h;  // (an infinity has no error term)
 }
 
 // Eight rotated elements x c + p s (p the pair's other member, s signed), as the bf16 values
 // that the exact sum rounds to (by way of 32 bits).  In 32 bits the sum r is off by at most
 // (|p s| + |r|) 2^-24 (results below 2^-100 aside); where every value within twice that
 // rounds to the same bf16 that is the answer, else (one element in some thousands) the sums
-// are taken with their errors.  So a key has the same bits however it was appended, which
-// matters where it is quantised next.  (64-bit arithmetic in that rare branch cost half of
-// the kernel's time: the compiler hoists the conversions, and the 64-bit pipe is slow.)
+// are taken with their errors.  (Whether the compiler fuses a product into e or r +- e does not
+// matter: twice the error leaves room for that.)  So a key has the same bits however it was
+// appended, which matters where it is quantised next.  The branch takes the products from here
+// because both are the same intrinsic; with * here the kernel took 53.4 us instead of 49.8 for
+// 32768 tokens.  (64-bit arithmetic in the branch cost half of the kernel's time: the compiler
+// hoists the conversions, and the 64-bit pipe is slow.)
 // there: whether the row exists and turns (the zeros of one that does not would take the
 // branch: r - e and r + e of a negative zero differ).
 __device__ __forceinline__ void rotate8(uint32_t (&w)[4], const uint32_t (&o)[4], const float (&c)[8],
@@ -48,7 +54,7 @@ __device__ __forceinline__ void rotate8(uint32_t (&w)[4], const uint32_t (&o)[4]
   for (int k = 0; k < 4; ++k) {
     const float x0 = __uint_as_float(w[k] << 16), x1 = __uint_as_float(w[k] & 0xffff0000u);
     const float p0 = __uint_as_float(o[k] << 16), p1 = __uint_as_float(o[k] & 0xffff0000u);
-    const float m0 = p0 * s[2 * k], m1 = p1 * s[2 * k + 1];
+    const float m0 = __fmul_rn(p0, s[2 * k]), m1 = __fmul_rn(p1, s[2 * k + 1]);
     const float r0 = fmaf(x0, c[2 * k], m0), r1 = fmaf(x1, c[2 * k + 1], m1);
     const float e0 = (fabsf(m0) + fabsf(r0)) * 0x1p-23f, e1 = (fabsf(m1) + fabsf(r1)) * 0x1p-23f;
     lo[k] = pack_bf16x2(r0 - e0, r1 - e1);
@@ -77,7 +83,7 @@ __device__ __forceinline__ void rotate_pairs(uint32_t (&a)[4], uint32_t (&b)[4],
     for (int h = 0; h < 2; ++h) {
       const float x = __uint_as_float(h ? a[k] & 0xffff0000u : a[k] << 16);
       const float y = __uint_as_float(h ? b[k] & 0xffff0000u : b[k] << 16);
-      const float m = y * -s[2 * k + h], n = x * s[2 * k + h];
+      const float m = __fmul_rn(y, -s[2 * k + h]), n = __fmul_rn(x, s[2 * k + h]);
       r[0][h] = fmaf(x, c[2 * k + h], m);
       r[1][h] = fmaf(y, c[2 * k + h], n);
       e[0][h] = (fabsf(m) + fabsf(r[0][h])) * 0x1p-23f;
