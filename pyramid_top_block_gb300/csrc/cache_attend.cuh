@@ -33,6 +33,8 @@ constexpr int kPartFloats = 16 * 64 + 32;  // a partial result: O [16][64], row 
 constexpr int kCaGrid = 152;               // CTAs of the split form: one on each SM
 constexpr int kCaMinTiles = 12;            // places of the stream that a run has at least
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNone = -0x1.fffffep127f;  // the reference of a row that has seen no logit above minus infinity
+constexpr float kFar = 0x1p22f;            // references from which on weigh takes differences in two steps
 
 inline size_t part_bytes() { return (size_t)kCaGrid * 2 * kPartFloats * sizeof(float); }
 
@@ -70,8 +72,10 @@ struct Cfg<PISA_CACHE_E2M1> {
 };
 template <int KIND>
 constexpr int kStageBytes = Cfg<KIND>::KT * Cfg<KIND>::kRow;
-constexpr int kScratch = 1024;  // bytes of a warp's own: a block list, or the weights of 16 keys
-static_assert(kScratch >= 16 * 16 * 4 && kScratch >= kCacheMaxSel * 4, "");
+// A warp's own shared memory: a block list or the weights of 16 keys, and from kFarAt on each lane's
+// factors and references of rows that are far (see weigh).
+constexpr int kFarAt = 1024, kScratch = kFarAt + 32 * 16;
+static_assert(kFarAt >= 16 * 16 * 4 && kFarAt >= kCacheMaxSel * 4, "");
 
 extern __shared__ __align__(128) unsigned char ca_smem[];
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -147,6 +151,7 @@ struct RowState {
   uint32_t qa[4][4];  // A fragments of the queries
   float f0, f1;       // logit factors of rows g and g + 8, base 2
   float m0, m1;       // the rows' references: weights are 2^(logit - m)
+  bool far;           // some row of the warp is far: factors and references are in shared memory
   float l0, l1;       // this lane's share of the sums of the weights
   float o[8][4];
   bool bad;  // a page out of range was met
@@ -193,7 +198,8 @@ __device__ __forceinline__ void fetch_q(const CacheAttendLaunch& a, const Unit& 
 
 template <int KIND>
 __device__ __forceinline__ void reset(RowState<KIND>& s) {
-  s.m0 = s.m1 = -INFINITY;
+  s.m0 = s.m1 = kNone;
+  s.far = false;
   s.l0 = s.l1 = 0.f;
   s.bad = false;
 #pragma unroll
@@ -433,9 +439,9 @@ __device__ __forceinline__ void weigh(uint32_t st, int first, const Sight& see, 
         if (key >= see.n1) sc[nt][2 + e] = -INFINITY;
       }
   }
-  // A row's reference m is the maximum of its logits up to where it was last set; it is set
-  // anew only when one passes it by more than kSlack, so that few tiles rescale O.  In fp16 a
-  // weight is held times 2^10: those down to 2^-24 of the reference keep all 11 bits (sums
+  // A row's reference m is, where it was last set, the maximum of its logits so far less kShift; it is
+  // set anew only when one passes that maximum by more than kSlack, so that few tiles rescale O.  In
+  // fp16 a weight is so held times 2^10: those down to 2^-24 of the reference keep all 11 bits (sums
   // of many small weights stay unbiased), and 2^kSlack times it still fits.
   float b0 = -INFINITY, b1 = -INFINITY;
 #pragma unroll
@@ -443,15 +449,27 @@ __device__ __forceinline__ void weigh(uint32_t st, int first, const Sight& see, 
     b0 = max3(b0, sc[nt][0], sc[nt][1]);
     b1 = max3(b1, sc[nt][2], sc[nt][3]);
   }
-  if (__any_sync(kFull, b0 * s.f0 > s.m0 + C::kSlack || b1 * s.f1 > s.m1 + C::kSlack)) {
+  constexpr float kTop = C::kShift + C::kSlack;
+  if (__any_sync(kFull, s.far || b0 * s.f0 > s.m0 + kTop || b1 * s.f1 > s.m1 + kTop)) {
 #pragma unroll
     for (int x = 1; x < 4; x <<= 1) {
       b0 = fmaxf(b0, __shfl_xor_sync(kFull, b0, x));
       b1 = fmaxf(b1, __shfl_xor_sync(kFull, b1, x));
     }
-    const float n0 = fmaxf(s.m0, b0 * s.f0), n1 = fmaxf(s.m1, b1 * s.f1);
-    const float a0 = n0 == -INFINITY ? 1.f : ex2_approx(s.m0 - n0);
-    const float a1 = n1 == -INFINITY ? 1.f : ex2_approx(s.m1 - n1);
+    float4& side = reinterpret_cast<float4*>(scratch + kFarAt / 4)[lane];
+    if (s.far) {
+      const float4 z = side;
+      s.f0 = z.x;
+      s.f1 = z.y;
+      s.m0 = z.z;
+      s.m1 = z.w;
+    }
+    // (past 2^26 a step of 32 bits is eight and more, too coarse for the shift; nothing that it is for
+    // is left there)
+    const float t0 = __fmul_rn(b0, s.f0), t1 = __fmul_rn(b1, s.f1);
+    const float n0 = fmaxf(s.m0, fabsf(t0) < 16.f * kFar ? t0 - C::kShift : t0);
+    const float n1 = fmaxf(s.m1, fabsf(t1) < 16.f * kFar ? t1 - C::kShift : t1);
+    const float a0 = ex2_approx(s.m0 - n0), a1 = ex2_approx(s.m1 - n1);
     s.m0 = n0;
     s.m1 = n1;
     s.l0 *= a0;
@@ -463,10 +481,27 @@ __device__ __forceinline__ void weigh(uint32_t st, int first, const Sight& see, 
       s.o[i][2] *= a1;
       s.o[i][3] *= a1;
     }
+    // Below, logit - m is the exact product less the reference, a rounded product: for the largest
+    // logit that is up to 2^-24 of the reference instead of zero.  It is no error, as all weights of
+    // the row have the factor, until the factor overflows.  So from kFar on the products are rounded
+    // first: differences of rounded products, taken here, are zero for the largest.  What is
+    // below then leaves them as they are, and the warp comes here for every tile.
+    if (__any_sync(kFull, s.far || (fabsf(n0) >= kFar && n0 != kNone) || (fabsf(n1) >= kFar && n1 != kNone))) {
+#pragma unroll
+      for (int nt = 0; nt < KT / 8; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          sc[nt][e] = __fsub_rn(__fmul_rn(sc[nt][e], s.f0), n0);
+          sc[nt][2 + e] = __fsub_rn(__fmul_rn(sc[nt][2 + e], s.f1), n1);
+        }
+      side = make_float4(s.f0, s.f1, n0, n1);
+      s.f0 = s.f1 = 1.f;
+      s.m0 = s.m1 = 0.f;
+      s.far = true;
+    }
   }
-  const float c0 = s.m0 == -INFINITY ? 0.f : C::kShift - s.m0, c1 = s.m1 == -INFINITY ? 0.f : C::kShift - s.m1;
   const unsigned long long f0 = f2_pack(s.f0, s.f0), f1 = f2_pack(s.f1, s.f1);
-  const unsigned long long cc0 = f2_pack(c0, c0), cc1 = f2_pack(c1, c1);
+  const unsigned long long cc0 = f2_pack(-s.m0, -s.m0), cc1 = f2_pack(-s.m1, -s.m1);
   unsigned long long l0 = f2_pack(s.l0, 0.f), l1 = f2_pack(s.l1, 0.f);
 #pragma unroll
   for (int nt = 0; nt < KT / 8; ++nt) {
@@ -675,6 +710,11 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
   }
   products<KIND, U, NP, false, true>(0, cur, lane, s, sc, w);
   cpa_wait<0>();
+  if (s.far) {
+    const float4 z = reinterpret_cast<const float4*>(scratch + kFarAt / 4)[lane];
+    s.m0 = z.z;
+    s.m1 = z.w;
+  }
 }
 
 // Puts the warps' partial sums where merged() finds them: O into the ring, which is idle then.
@@ -720,7 +760,7 @@ __device__ __forceinline__ void merge_warps(RowState<KIND>& s, float* mo, float 
 template <int W>
 __device__ __forceinline__ float4 merged(const float* mo, const float (*ml)[2][16], int row, int quad, float& m,
                                          float& l) {
-  m = -INFINITY;
+  m = kNone;
 #pragma unroll
   for (int w = 0; w < W; ++w) m = fmaxf(m, ml[w][0][row]);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -728,8 +768,8 @@ __device__ __forceinline__ float4 merged(const float* mo, const float (*ml)[2][1
 #pragma unroll
   for (int w = 0; w < W; ++w) {
     const float mw = ml[w][0][row], lw = ml[w][1][row];
-    const float f = mw == -INFINITY ? 0.f : ex2_approx(mw - m);
-    l += mw == -INFINITY ? lw : f * lw;  // (a warp without keys adds 0, or the NaN of a bad page)
+    const float f = ex2_approx(mw - m);
+    l = fmaf(f, lw, l);  // (a warp without keys adds 0, or the NaN of a bad page)
     const float4 x = *reinterpret_cast<const float4*>(mo + w * 1024 + merge_at(row, quad));
     acc.x = fmaf(f, x.x, acc.x);
     acc.y = fmaf(f, x.y, acc.y);
