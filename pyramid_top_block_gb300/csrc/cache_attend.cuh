@@ -210,7 +210,10 @@ __device__ __forceinline__ void reset(RowState<KIND>& s) {
 // In the 4-bit form the products are taken in fp16: the row is scaled by a power of two so
 // that its largest element lies in [1, 2), where fp16 holds all 8 bits of a bf16 down to
 // 2^-17 of it and is off by at most 2^-25 of it below (the fp32 sums of the products are
-// off by as much).
+// off by as much).  Rows above 2^126 lie in [1, 4), and so does what is finite in a row with an
+// infinity; rows below 2^-100 have logits of zero, whatever becomes of them.  A factor of the
+// logits that is past the range of 32 bits is cut to it: logits of zero stay so, and others, if
+// they fit 32 bits at all, still differ by far more than weights can show.
 template <int KIND>
 __device__ __forceinline__ void make_q(const CacheAttendLaunch& a, const QueryWords& q, int lane, RowState<KIND>& s) {
   const int j = lane & 3;
@@ -225,10 +228,9 @@ __device__ __forceinline__ void make_q(const CacheAttendLaunch& a, const QueryWo
       t = max(t & 0xffffu, t >> 16);
       t = max(t, __shfl_xor_sync(kFull, t, 1));
       t = max(t, __shfl_xor_sync(kFull, t, 2));
-      int e = (int)(t >> 7) - 127;              // the largest lies in [2^e, 2^(e + 1))
-      e = t == 0 || t >= 0x7f80u ? 0 : max(min(e, 100), -100);
+      const int e = max(min((int)(t >> 7) - 127, 126), -100);  // the largest lies in [2^e, 2^(e + 1))
       const float down = exp2i(-e);
-      f[h] *= exp2i(e) * exp2i(a.cache.k_exp);
+      f[h] = fminf(f[h] * exp2i(e) * exp2i(a.cache.k_exp), 0x1.fffffep127f);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         w[h][i] = pack_f16x2(__uint_as_float(q.w[h][i] << 16) * down, __uint_as_float(q.w[h][i] & 0xffff0000u) * down);

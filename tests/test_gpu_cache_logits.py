@@ -88,3 +88,58 @@ def test_large_logits_beside_ordinary_rows(bits):
         # equal weights, rounded alike; fp32 sums of n terms
         tol = n * 2.0 ** -23 * size + 2.0 ** -11 * size + 2.0 ** -9 * mean.abs()
         assert bool(((out - mean).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("e", [100, 114, 116, 120, 125])
+def test_query_rows_up_to_the_end_of_the_range(bits, e):
+    """Elements up to 2^127 over keys that are small enough for the logits to fit 32 bits."""
+    g = base.gen(e + bits)
+    n = 300
+    cache = base.make_cache(g, 1, n, 2, 64, bits, k_exp=-24 if bits == 4 else 0)
+    if bits == 16:
+        cache.pages[:, :, :, 0] *= 2.0 ** -24
+    q = (base.normal(g, 1, 1, 32, 64).clamp(-3.9, 3.9) * 2.0 ** e)
+    assert bool(torch.isfinite(q).all())
+    for c in (cache, base.in_a_wide_table(cache)):
+        check_one_hot(cache, q, n, pisa.cache_attention(q, c, base.i32([n])))
+    blocks = [4, 0, 3]
+    idx = base.i32(blocks).expand(1, 2, 1, 3).contiguous()
+    check_one_hot(cache, q, n, pisa.cache_attention(q, cache, base.i32([n]), idx=idx), blocks)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_large_queries_over_keys_of_zero(bits):
+    """Logits of zero stay zero, whatever the exponents: the mean of the values."""
+    g = base.gen(33)
+    n = 200
+    for k_exp in ((0, 24) if bits == 4 else (0,)):
+        cache = base.make_cache(g, 1, n, 1, 64, bits, k_exp=k_exp)
+        v = base.normal(g, 1, n, 1, 64)
+        pisa.cache_append(None, torch.zeros_like(v), v, cache, base.i32([0]), None)
+        _, vv = ref.tokens(cache, 0, n)
+        mean, size = vv[:, 0].mean(0), vv[:, 0].abs().mean(0)
+        q = base.normal(g, 1, 1, 16, 64).clamp(-3.9, 3.9) * 2.0 ** 125
+        out = pisa.cache_attention(q, cache, base.i32([n]))[0, 0].double()
+        tol = n * 2.0 ** -23 * size + 2.0 ** -11 * size + 2.0 ** -9 * mean.abs()
+        assert bool(((out - mean).abs() <= tol).all()), k_exp
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_an_infinite_element_beside_large_ones(bits):
+    """Every logit is minus infinity, whatever the row's finite elements are: zeros."""
+    g = base.gen(34)
+    n = 200
+    cache = base.make_cache(g, 1, n, 1, 64, bits)
+    k = base.normal(g, 1, n, 1, 64)
+    k[..., 7] = -1.0
+    pisa.cache_append(None, k, base.normal(g, 1, n, 1, 64), cache, base.i32([0]), None)
+    q = base.normal(g, 1, 1, 16, 64) * 2.0 ** 20
+    q[..., 7] = float("inf")
+    ordinary = base.normal(g, 64)
+    q[0, 0, 5] = ordinary
+    out = pisa.cache_attention(q, cache, base.i32([n]))
+    rows = [r for r in range(16) if r != 5]
+    assert bool((out[0, 0, rows] == 0).all())
+    base.check_attention(pisa.PagedCache(cache.pages, cache.table, 64), ordinary.expand(1, 1, 1, 64), [n],
+                         out[:, :, 5:6])
