@@ -24,6 +24,8 @@
 //     from 32-bit partial results.
 #pragma once
 
+#include <climits>
+
 #include "cache.cuh"
 #include "tc.cuh"
 
@@ -72,9 +74,10 @@ struct Cfg<PISA_CACHE_E2M1> {
 };
 template <int KIND>
 constexpr int kStageBytes = Cfg<KIND>::KT * Cfg<KIND>::kRow;
-// A warp's own shared memory: a block list or the weights of 16 keys, and from kFarAt on each lane's
-// factors and references of rows that are far (see weigh).
-constexpr int kFarAt = 1024, kScratch = kFarAt + 32 * 16;
+// A warp's own shared memory: a block list or the weights of 16 keys; from kFarAt on each lane's
+// factors and references of rows that are far (see weigh); at kBadAt the first token that lies in a
+// page out of range.
+constexpr int kFarAt = 1024, kBadAt = kFarAt + 32 * 16, kScratch = kBadAt + 16;
 static_assert(kFarAt >= 16 * 16 * 4 && kFarAt >= kCacheMaxSel * 4, "");
 
 extern __shared__ __align__(128) unsigned char ca_smem[];
@@ -642,6 +645,7 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
     int page = 0;
     off = 0;
     const int y = x + lane / E;
+    int* first_bad = reinterpret_cast<int*>(scratch + kBadAt / 4);
     if (y < mine) {
       const int p = first_of(y) + (lane % E) * U;
       if (p < see.n_hi) {
@@ -655,7 +659,12 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
         }
       }
     }
-    if (__any_sync(kFull, page < 0)) s.bad = true;
+    if (__any_sync(kFull, page < 0)) {
+      const int p = page < 0 ? first_of(y) + (lane % E) * U : INT_MAX, q = __reduce_min_sync(kFull, p);
+      if (lane == 0) *first_bad = s.bad ? min(*first_bad, q) : q;
+      s.bad = true;
+      __syncwarp();
+    }
   };
   auto issue = [&](int x, uint32_t dst) {  // the copies of the warp's tile number x
 #pragma unroll
@@ -717,6 +726,11 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
     s.m0 = z.z;
     s.m1 = z.w;
   }
+  if (s.bad) {  // the rows that see a page out of range become NaN
+    const int first_bad = *reinterpret_cast<const int*>(scratch + kBadAt / 4);
+    if (first_bad < see.n0) s.l0 = __int_as_float(0x7fc00000);
+    if (first_bad < see.n1) s.l1 = __int_as_float(0x7fc00000);
+  }
 }
 
 // Puts the warps' partial sums where merged() finds them: O into the ring, which is idle then.
@@ -729,7 +743,6 @@ __device__ __forceinline__ void merge_warps(RowState<KIND>& s, float* mo, float 
     s.l0 += __shfl_xor_sync(kFull, s.l0, x);
     s.l1 += __shfl_xor_sync(kFull, s.l1, x);
   }
-  if (s.bad) s.l0 = s.l1 = __int_as_float(0x7fc00000);  // a page out of range: the unit's rows become NaN
   if (j == 0) {
     ml[warp][0][g] = s.m0;
     ml[warp][0][g + 8] = s.m1;
