@@ -253,6 +253,7 @@ int pisa_decode_append_and_select(const void* q_new, const void* k_new, int Hq,
  *   table       : device int32 [B, max_pages]; entries of tokens a sequence does not hold
  *                 are not read.  Sequences may share pages that only are read.
  *   page_size   : 16, 32, 64, 128 or 256 tokens; max_pages * page_size <= 2^27
+ *   B, Hkv      : Hkv <= 32, B * Hkv <= 65535
  *   kind        : PISA_CACHE_BF16 or PISA_CACHE_E2M1
  *   k_exp, v_exp: E2M1: keys (values) are held divided by 2^k_exp (2^v_exp), within
  *                 [-24, 24]; BF16: 0
@@ -290,8 +291,9 @@ size_t pisa_cache_page_bytes(int page_size, int Hkv, int kind);
 /* Workspace bytes of the cache calls (the same for every size).  It starts with a status
  * word, which the cache calls set on an error and never clear: zero the workspace once,
  * before its first use, and read the word of any number of calls with
- * pisa_check_device_status.  Calls that share a workspace must not overlap on the GPU;
- * that includes replays of captured graphs. */
+ * pisa_check_device_status.  A call without a workspace, or with one that was not zeroed,
+ * meets the same errors in the same way, but nothing tells of them.  Calls that share a
+ * workspace must not overlap on the GPU; that includes replays of captured graphs. */
 size_t pisa_cache_workspace_bytes(void);
 
 /*
@@ -299,8 +301,9 @@ size_t pisa_cache_workspace_bytes(void);
  * Token t < counts[b] of sequence b has position start[b] + t.  In the first `rot` dims of
  * a query or key row the pairs (i, i + rot / 2) (interleaved != 0: (2 i, 2 i + 1)) become
  * (a c - b s, b c + a s), with c = rotary[p, i], s = rotary[p, rot / 2 + i]; each result is
- * the exact sum rounded to 32 bits and then to bf16 (below 2^-100 the last bit may differ),
- * and does not depend on the call's shape.  The rotated key, and the value, go into the page.
+ * the sum, off by at most 2^-46 of its two products' sizes, rounded to 32 bits and then to
+ * bf16 (below 2^-100 the last bit may differ), and does not depend on the call's shape.
+ * The rotated key, and the value, go into the page.
  *   q       : rows [B, T, Hq, d], or NULL; k, v: rows [B, T, Hkv, d]
  *   start   : device int32 [B]; counts: device int32 [B], or NULL (T of each)
  *   rotary  : device fp32 [n_rot, rot], 16-byte aligned; rot in {0, 16, 32, 48, 64}, 0: no
@@ -311,7 +314,8 @@ size_t pisa_cache_workspace_bytes(void);
  * Rows t >= counts[b] of the outputs are left as they were.  A token whose position is
  * outside [0, max_pages * page_size) or [0, n_rot), or whose page number is outside
  * [0, n_pages), is left out of every output and flags PISA_ERR_DEVICE_BOUNDS.  Two tokens of
- * one call must not share a place in the cache.  Hq/Hkv in {1, 2, 4, 8, 16}.
+ * one call must not share a place in the cache.  Hq/Hkv in {1, 2, 4, 8, 16};
+ * T * ((Hq + 2 Hkv + 7) / 4) < 2^31 - 1024 (Hq: 0 without q).
  */
 int pisa_cache_append(const pisa_paged_cache* cache, int T, const pisa_rows* q, int Hq, const pisa_rows* k,
                       const pisa_rows* v, const int32_t* start, const int32_t* counts, const float* rotary,
@@ -322,6 +326,7 @@ int pisa_cache_append(const pisa_paged_cache* cache, int T, const pisa_rows* q, 
  * pisa_cache_read -- cached tokens as dense bf16: row t < counts[b] (NULL: T) of k_out and
  * v_out (either may be NULL) is the token at position start[b] + t.  Exact: 4-bit values fit
  * bf16.  Other rows are left as they were; positions and pages out of range as above.
+ * T < 2^30.
  */
 int pisa_cache_read(const pisa_paged_cache* cache, int T, const int32_t* start, const int32_t* counts,
                     const pisa_rows* k_out, const pisa_rows* v_out, void* ws, void* stream);
@@ -340,11 +345,15 @@ int pisa_cache_read(const pisa_paged_cache* cache, int T, const int32_t* start, 
  *   out     : device [B, T, Hq, d] dense, 16-byte aligned, fp32 (out_f32 != 0) or bf16
  *   ws      : workspace of pisa_cache_workspace_bytes(), 256-byte aligned
  * A query that sees no token, or none whose logit is above minus infinity, gets zeros;
- * tokens that it does not see do not matter, whatever their values.  One that sees a
- * token in a page outside [0, n_pages) gets NaNs,
- * and PISA_ERR_DEVICE_BOUNDS is flagged.  1 <= T <= 16, 1 <= Ksel <= 64, Hq/Hkv in
- * {1, 2, 4, 8, 16}, B * T * Hkv < 2^24.  Sums and softmax in fp32; the weights enter the
- * product with V as two bf16 parts (bf16 pages) or as fp16 (4-bit pages).
+ * tokens that it does not see do not matter, whatever their values, nor do the pages they
+ * lie in.  One that sees a token in a page outside [0, n_pages) gets NaNs, and
+ * PISA_ERR_DEVICE_BOUNDS is flagged.  1 <= T <= 16, 1 <= Ksel <= 64, Hq/Hkv in
+ * {1, 2, 4, 8, 16}, B * T * Hkv < 2^24.  Sums, logits and softmax in fp32: a logit that does
+ * not fit (times log2 e, and bf16 pages: times 8) counts as infinite, and a row with one of
+ * plus infinity gets NaNs.  The weights enter the product with V rounded: for bf16 results
+ * as two bf16 parts (bf16 pages: 16 bits) or one fp16 part (4-bit pages: 11 bits, weights
+ * below 2^-24 of the row's largest fewer), which stays below the rounding of the result; for
+ * fp32 results as three bf16 parts or two fp16 parts.
  */
 int pisa_cache_attention(const pisa_paged_cache* cache, const pisa_rows* q, int T, int Hq, const int32_t* lengths,
                          const int32_t* idx, int Ksel, void* out, int out_f32, void* ws, size_t ws_bytes,

@@ -604,7 +604,8 @@ def cache_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache
     [n, rot], rot 16, 32, 48 or 64: cosines, then sines of each position (None: no rotation); pairs (i, i +
     rot / 2), or (2 i, 2 i + 1) when interleaved.  Returns (q_out, k_out): the rotated queries (None without q)
     and keys, allocated here when not given (rows t >= counts[b] are then not written); q_out may be q and
-    k_out may be k.  workspace: for the status word only, may be None.
+    k_out may be k.  workspace (of cache_workspace): for the status word only; without one, nothing tells of
+    tokens that are left out because their position or page is out of range.
     """
     guard = _on(cache, stream)
     if guard is not None:
@@ -650,7 +651,8 @@ def cache_read(cache: PagedCache, start: torch.Tensor, T: int, counts: torch.Ten
                k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None,
                workspace: torch.Tensor | None = None, stream=None):
     """Cached tokens start[b] .. start[b] + counts[b] - 1 (T where counts is None) as dense bf16 (k, v)
-    [B, T, Hkv, 64], exactly; allocated here when not given (rows t >= counts[b] are not written)."""
+    [B, T, Hkv, 64], exactly; allocated here when not given (rows t >= counts[b] are not written).  workspace
+    as in cache_append."""
     guard = _on(cache, stream)
     if guard is not None:
         with guard:
@@ -678,7 +680,10 @@ def cache_attention(q: torch.Tensor, cache: PagedCache, lengths: torch.Tensor, i
     q [B, T, Hq, 64] bf16, 1 <= T <= 16; query t sits at position lengths[b] - T + t (lengths int32 [B], the new
     tokens included) and sees the tokens up to its own.  idx int32 [B, Hkv, T, Ksel] ([B, Hkv, Ksel] when T is
     1, as decode_append_and_select returns it): blocks of 64 tokens, -1 skipped.  out [B, T, Hq, 64], bf16
-    (allocated here when not given) or fp32.
+    (allocated here when not given) or fp32.  workspace (of cache_workspace, one stream at a time): a decoding
+    program makes one and checks its status word (check_device_status); without one the call takes scratch of its
+    own and nothing tells of errors: a length past the table's capacity is cut to it, and queries that see a page
+    out of range are NaN.
     """
     guard = _on(cache, stream)
     if guard is not None:

@@ -10,8 +10,8 @@
 // shuffle, and each element is unpacked once (53.2 -> 50.7 us for 32768 tokens).
 //
 // Both kernels only move rows, so the bytes of the rows in and out bound them.  Measured: 32768
-// tokens of 32 + 2 + 2 heads into bf16 pages (319 MB) 49.6 us = 6.43 TB/s; 131072 tokens of 2
-// heads read back from 4 bits (86 MB) 15.9 us = 5.41 TB/s; 65 single tokens 1.9 us.
+// tokens of 32 + 2 + 2 heads into bf16 pages (319 MB) 49.8 us = 6.40 TB/s; 131072 tokens of 2
+// heads read back from 4 bits (86 MB) 16.1 us = 5.35 TB/s; 65 single tokens 1.9 us.
 #include "cache.cuh"
 
 #include <type_traits>
