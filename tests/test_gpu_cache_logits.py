@@ -143,3 +143,26 @@ def test_an_infinite_element_beside_large_ones(bits):
     assert bool((out[0, 0, rows] == 0).all())
     base.check_attention(pisa.PagedCache(cache.pages, cache.table, 64), ordinary.expand(1, 1, 1, 64), [n],
                          out[:, :, 5:6])
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("T,G,page,n", [(5, 8, 16, 130), (5, 8, 16, 3), (3, 16, 64, 9001), (16, 4, 32, 2059)])
+def test_large_logits_of_several_queries(bits, T, G, page, n):
+    """Each query has its own last token, rows that see nothing share the tile, NaNs lie behind all of them."""
+    g = base.gen(n + T)
+    cache = base.make_cache(g, 1, max(n + 20, 70), 1, page, bits)
+    for p in range(n, n + 20):
+        base.poison(cache, 0, p)
+    for e in (24, 31, 50, 110):
+        q = base.normal(g, 1, T, G, 64)
+        q[:, :, 1:] *= 2.0 ** e  # the first row of each query stays ordinary
+        for c in (cache, base.in_a_wide_table(cache)):
+            out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device=DEV)
+            pisa.cache_attention(q, c, base.i32([n]), out=out)
+            for t in range(T):
+                see = n - T + t + 1
+                if see <= 0:
+                    assert bool((out[0, t] == 0).all())
+                else:
+                    check_one_hot(cache, q[:, t:t + 1, 1:], see, out[:, t:t + 1, 1:])
+            base.check_attention(cache, q[:, :, :1], [n], out[:, :, :1])
