@@ -360,6 +360,118 @@ int pisa_cache_attention(const pisa_paged_cache* cache, const pisa_rows* q, int 
                          void* stream);
 
 /*
+ * pisa_cache_append_axes -- pisa_cache_append for tokens whose rotation has positions of its own
+ * on several axes (time, height and width in an image or a video).  Pair i of a row turns by
+ * the angles of rotary[positions[a, b, t], i], a = the axis of pair i; the token's place in
+ * the cache stays start[b] + t.
+ *   positions : device int32 [n_axes, B, T] dense; 1 <= n_axes <= 4
+ *   axis_of   : bits 2 i and 2 i + 1: the axis of pair i, i < rot / 2, below n_axes
+ * A token with a position outside [0, n_rot) is left out and flagged like one whose place is
+ * out of range.  rot in {16, 32, 48, 64}, n_rot <= 2^27.  Everything else as above.
+ */
+int pisa_cache_append_axes(const pisa_paged_cache* cache, int T, const pisa_rows* q, int Hq, const pisa_rows* k,
+                           const pisa_rows* v, const int32_t* start, const int32_t* counts, const float* rotary,
+                           int64_t n_rot, int rot, int interleaved, const int32_t* positions, int n_axes,
+                           uint64_t axis_of, const pisa_rows* q_out, const pisa_rows* k_out, void* ws, void* stream);
+
+/*
+ * pisa_cache_attention_scored -- pisa_cache_attention with scores that are not plain products,
+ * and with a window:
+ *   x = q . k / 8;  cap > 0: x = cap tanh(x / cap);  slopes: x -= slopes[h] |p - j|
+ * for a query at position p and a token at position j, which it sees if j <= p and (window >
+ * 0) j > p - window.
+ *   cap    : 0 (no cap), or 2^-20 .. 2^20
+ *   slopes : device fp32 [Hq], finite, or NULL
+ *   window : tokens, the query's own among them; 0: no window
+ * Tokens before the window do not matter either, nor do their pages, which may have been given
+ * away.  With a cap an infinite product is a logit of plus or minus cap.  The scores take one
+ * or two roundings of 32 bits more.  Everything else as above.
+ */
+int pisa_cache_attention_scored(const pisa_paged_cache* cache, const pisa_rows* q, int T, int Hq,
+                                const int32_t* lengths, const int32_t* idx, int Ksel, float cap, const float* slopes,
+                                int window, void* out, int out_f32, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * pisa_cache_prompt_attention -- a prompt's tokens, or those of a chunk of one, attend over the
+ * paged cache, in which they already are (pisa_cache_append).
+ *   q      : rows [B, T, Hq, d]; query t < counts[b] (NULL: T) of sequence b has position p =
+ *            start[b] + t; rows behind are neither read nor, in out, written
+ *   first  : device int32 [B, T], or NULL (0): query t sees no token before it (the start of
+ *            its document, say)
+ *   last   : device int32 [B, T], or NULL (p + 1): query t sees tokens before it only, up to
+ *            the sequence's newest at start[b] + counts[b] - 1 (a prefix, or an image, that is
+ *            seen from both sides)
+ *   cap, slopes, window : as above
+ *   out    : device bf16 [B, T, Hq, d] dense, 16-byte aligned
+ *   ws     : workspace of pisa_cache_workspace_bytes(), 256-byte aligned
+ * T from 1 up, B * T * Hkv < 2^30; Hq/Hkv in {1, 2, 4, 8, 16}.  Rows that see nothing, infinities,
+ * NaNs and pages out of range as above; a sequence that ends past the table's capacity is cut
+ * to it, one that starts before 0 has no tokens there, and PISA_ERR_DEVICE_BOUNDS is flagged.
+ */
+int pisa_cache_prompt_attention(const pisa_paged_cache* cache, const pisa_rows* q, int T, int Hq,
+                                const int32_t* start, const int32_t* counts, const int32_t* first,
+                                const int32_t* last, float cap, const float* slopes, int window, void* out, void* ws,
+                                size_t ws_bytes, void* stream);
+
+/*
+ * Pages that sequences share.  (A deployment part of this library; the paper has no counterpart.)
+ *   pages       : device, 16-byte aligned; a page is page_bytes bytes (a multiple of 16), page i
+ *                 starts page_stride bytes after page i - 1.  A page may hold the tokens of
+ *                 many layers; each layer's pisa_paged_cache then points into it.
+ *   table       : device int32 [B, max_pages]: the page of every page_size tokens of a sequence;
+ *                 an entry outside [0, n_pages) stands for no page
+ *   refs        : device int32 [n_pages]: how many table entries hold the page; 0: it is free
+ *   page_size   : 16, 32, 64, 128 or 256 tokens; max_pages * page_size <= 2^27
+ *   B, n_pages  : B <= 65535 (a fork: 32768), n_pages <= 2^30
+ * A new pool has a table of -1 and references of 0.  The calls keep refs in line with the table; a
+ * call on a pool where they are not in line reads and writes no other memory than the pool's.
+ * Calls on one pool must not overlap on the GPU.
+ */
+typedef struct {
+  void* pages;
+  int32_t* table;
+  int32_t* refs;
+  int64_t page_stride, page_bytes;
+  int B, page_size, n_pages, max_pages;
+} pisa_page_pool;
+
+/* Workspace bytes of pisa_cache_reserve and pisa_cache_compact (0 on bad arguments).  Its status
+ * word is that of the cache calls: only ever set, and to be zeroed before the first use. */
+size_t pisa_pool_workspace_bytes(int n_pages, int B);
+
+/*
+ * pisa_cache_fork -- all sequences at once become copies of others, by sharing their pages: row b of
+ * the table becomes the row that parents[b] had, lengths[b] the length that it had.  parents[b] = b
+ * keeps a sequence, a negative one frees it (a row of -1, length 0), one past B - 1 keeps it and
+ * flags PISA_ERR_DEVICE_BOUNDS.  Pages that no row holds any longer are free.
+ *   parents : device int32 [B]; lengths : device int32 [B]; ws : workspace for the status word, or NULL
+ */
+int pisa_cache_fork(const pisa_page_pool* pool, const int32_t* parents, int32_t* lengths, void* ws, void* stream);
+
+/*
+ * pisa_cache_reserve -- pages for the next counts[b] (0 to T; NULL: T) tokens of every sequence.  After
+ * it, the pages of positions lengths[b] .. lengths[b] + counts[b] - 1 are there and no other sequence's:
+ * where an entry has no page, or one with more than one reference, it gets a free one, and a shared page
+ * that holds tokens before lengths[b] is copied as a whole.  Free pages are taken lowest number first, by
+ * sequences in order and by a sequence's entries in order.  A sequence is served if it needs no page, or
+ * if all sequences up to it together need no more than were free at the call (pages that the call itself
+ * lets go count from the next one on); one that is not served stays as it is.
+ *   granted : device int32 [B]: counts[b], or 0 for a sequence that was not served (the counts of the
+ *             append that follows)
+ * A length that is negative, or that would pass max_pages * page_size, is not served and flags
+ * PISA_ERR_DEVICE_BOUNDS; a lack of pages is told by granted alone.
+ */
+int pisa_cache_reserve(const pisa_page_pool* pool, const int32_t* lengths, int T, const int32_t* counts,
+                       int32_t* granted, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * pisa_cache_compact -- moves the pages in use to the front of the pool.  With U pages in use (refs != 0),
+ * the i-th of those numbered U or more moves to the i-th free number below U, in the pool, in the table
+ * and in refs; the others stay.  used : device int32 [1] gets U: pages U and up are free.
+ */
+int pisa_cache_compact(const pisa_page_pool* pool, int32_t* used, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * pisa_select_prefill_noalloc -- the prefill selection above for callers that
  * cannot allocate device memory: no workspace argument.  (The paper has no
  * counterpart; this is a deployment convenience of this library.)

@@ -13,6 +13,7 @@ GQA head sum, §5.1 prefill and decoding kernels).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 from dataclasses import dataclass
@@ -28,7 +29,8 @@ __all__ = [
     "decode_workspace_bytes",
     "decode_append_and_select", "check_device_status", "status_string", "kernel_launches",
     "PagedCache", "cache_workspace", "cache_workspace_bytes", "cache_append", "cache_read", "cache_attention",
-    "rotary_table",
+    "cache_prompt_attention", "rotary_table",
+    "PagePool", "pool_workspace", "pool_workspace_bytes", "cache_fork", "cache_reserve", "cache_compact",
     "prefill_phases", "set_phase_events", "D", "C", "G_MERGE",
 ]
 
@@ -112,6 +114,23 @@ def load(path: str | None = None):
     lib.pisa_cache_read.restype = i32
     lib.pisa_cache_attention.argtypes = [vp, vp, i32, i32, vp, vp, i32, vp, i32, vp, sz, vp]
     lib.pisa_cache_attention.restype = i32
+    lib.pisa_cache_append_axes.argtypes = [vp, i32, vp, i32, vp, vp, vp, vp, vp, i64, i32, i32, vp, i32,
+                                           ctypes.c_uint64, vp, vp, vp, vp]
+    lib.pisa_cache_append_axes.restype = i32
+    lib.pisa_cache_attention_scored.argtypes = [vp, vp, i32, i32, vp, vp, i32, ctypes.c_float, vp, i32, vp, i32, vp, sz,
+                                                vp]
+    lib.pisa_cache_attention_scored.restype = i32
+    lib.pisa_cache_prompt_attention.argtypes = [vp, vp, i32, i32, vp, vp, vp, vp, ctypes.c_float, vp, i32, vp, vp, sz,
+                                                vp]
+    lib.pisa_cache_prompt_attention.restype = i32
+    lib.pisa_pool_workspace_bytes.argtypes = [i32, i32]
+    lib.pisa_pool_workspace_bytes.restype = sz
+    lib.pisa_cache_fork.argtypes = [vp, vp, vp, vp, vp]
+    lib.pisa_cache_fork.restype = i32
+    lib.pisa_cache_reserve.argtypes = [vp, vp, i32, vp, vp, vp, sz, vp]
+    lib.pisa_cache_reserve.restype = i32
+    lib.pisa_cache_compact.argtypes = [vp, vp, vp, sz, vp]
+    lib.pisa_cache_compact.restype = i32
     lib.pisa_event_elapsed_ms.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_float)]
     lib.pisa_event_elapsed_ms.restype = i32
     _lib = lib
@@ -593,10 +612,19 @@ def _cache_ws(workspace: torch.Tensor, cache: PagedCache, need: int) -> int:
     return workspace.data_ptr()
 
 
+@functools.lru_cache(maxsize=64)
+def _pack_axes(axes: tuple, A: int, rot: int) -> int:
+    """The axes of a row's pairs as the C ABI takes them (a function of the numbers alone)."""
+    if len(axes) != rot // 2 or not all(isinstance(a, int) and 0 <= a < A for a in axes):
+        raise ValueError(f"axes must be {rot // 2} whole numbers of 0 .. {A - 1}")
+    return sum(a << (2 * i) for i, a in enumerate(axes))
+
+
 def cache_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: PagedCache, start: torch.Tensor,
                  rotary: torch.Tensor | None, counts: torch.Tensor | None = None, interleaved: bool = False,
                  q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
-                 workspace: torch.Tensor | None = None, stream=None):
+                 workspace: torch.Tensor | None = None, stream=None, positions: torch.Tensor | None = None,
+                 axes: tuple | None = None):
     """Rotate new queries and keys by their positions and put keys and values into the cache.
 
     q [B, T, Hq, 64] (or None), k and v [B, T, Hkv, 64] bf16, any strides that are multiples of 8; token t of
@@ -605,12 +633,15 @@ def cache_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache
     rot / 2), or (2 i, 2 i + 1) when interleaved.  Returns (q_out, k_out): the rotated queries (None without q)
     and keys, allocated here when not given (rows t >= counts[b] are then not written); q_out may be q and
     k_out may be k.  workspace (of cache_workspace): for the status word only; without one, nothing tells of
-    tokens that are left out because their position or page is out of range.
+    tokens that are left out because their position or page is out of range.  positions int32 [A, B, T], A 1 to 4
+    (images and videos: time, height, width): token t of sequence b turns by them instead of by its place in the
+    cache, pair i by the position on axis axes[i] (rot / 2 numbers below A; None: all on axis 0).
     """
     guard = _on(cache, stream)
     if guard is not None:
         with guard:
-            return cache_append(q, k, v, cache, start, rotary, counts, interleaved, q_out, k_out, workspace)
+            return cache_append(q, k, v, cache, start, rotary, counts, interleaved, q_out, k_out, workspace, None,
+                                positions, axes)
     if k.dim() != 4:
         raise ValueError("k must be a bf16 tensor [B, T, Hkv, 64]")
     B, T = cache.B, k.shape[1]
@@ -639,6 +670,22 @@ def cache_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache
         if rot not in (16, 32, 48, 64):
             raise ValueError("rotary must be [n, rot] with rot 16, 32, 48 or 64")
         rp = rotary.data_ptr()
+    if positions is not None:
+        if rotary is None:
+            raise ValueError("positions without rotary")
+        if (positions.dtype is not torch.int32 or positions.dim() != 3 or positions.shape[1:] != (B, T)
+                or positions.get_device() != cache._index or not positions.is_contiguous()):
+            raise ValueError(f"positions must be a contiguous int32 tensor [A, {B}, {T}] on the cache's device")
+        A = positions.shape[0]
+        _check((_lib or load()).pisa_cache_append_axes(
+            cache._ref, T, qs, Hq, ks, vs, _per_sequence(start, "start", cache),
+            None if counts is None else _per_sequence(counts, "counts", cache), rp, n_rot, rot, 1 if interleaved else 0,
+            positions.data_ptr(), A, 0 if axes is None else _pack_axes(tuple(axes), A, rot), qo,
+            _rows(k_out, "k_out", cache, shape, True), None if workspace is None else _cache_ws(workspace, cache, 4),
+            _current(cache)), "pisa_cache_append_axes")
+        return q_out, k_out
+    if axes is not None:
+        raise ValueError("axes without positions")
     _check((_lib or load()).pisa_cache_append(
         cache._ref, T, qs, Hq, ks, vs, _per_sequence(start, "start", cache),
         None if counts is None else _per_sequence(counts, "counts", cache), rp, n_rot, rot, 1 if interleaved else 0,
@@ -673,8 +720,8 @@ def cache_read(cache: PagedCache, start: torch.Tensor, T: int, counts: torch.Ten
 
 
 def cache_attention(q: torch.Tensor, cache: PagedCache, lengths: torch.Tensor, idx: torch.Tensor | None = None,
-                    out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
-                    stream=None) -> torch.Tensor:
+                    out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None,
+                    cap: float = 0.0, slopes: torch.Tensor | None = None, window: int = 0) -> torch.Tensor:
     """The newest T tokens of every sequence attend over the cache: all of it, or the blocks of a selection.
 
     q [B, T, Hq, 64] bf16, 1 <= T <= 16; query t sits at position lengths[b] - T + t (lengths int32 [B], the new
@@ -683,12 +730,13 @@ def cache_attention(q: torch.Tensor, cache: PagedCache, lengths: torch.Tensor, i
     (allocated here when not given) or fp32.  workspace (of cache_workspace, one stream at a time): a decoding
     program makes one and checks its status word (check_device_status); without one the call takes scratch of its
     own and nothing tells of errors: a length past the table's capacity is cut to it, and queries that see a page
-    out of range are NaN.
+    out of range are NaN.  cap > 0: a score x (q . k / 8) counts as cap tanh(x / cap).  slopes fp32 [Hq]: a token
+    at distance n counts slopes[h] n less.  window > 0: a query sees the window tokens up to its own.
     """
     guard = _on(cache, stream)
     if guard is not None:
         with guard:
-            return cache_attention(q, cache, lengths, idx, out, workspace)
+            return cache_attention(q, cache, lengths, idx, out, workspace, None, cap, slopes, window)
     if q.dim() != 4:
         raise ValueError("q must be a bf16 tensor [B, T, Hq, 64]")
     _, T, Hq, _ = q.shape
@@ -712,11 +760,217 @@ def cache_attention(q: torch.Tensor, cache: PagedCache, lengths: torch.Tensor, i
     need = _cache_ws_bytes or cache_workspace_bytes()
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
+    if cap != 0 or slopes is not None or window != 0:
+        _check(lib.pisa_cache_attention_scored(cache._ref, qs, T, Hq, _per_sequence(lengths, "lengths", cache), ip, Ksel,
+                                               cap, _slopes(slopes, Hq, cache), _window(window), out.data_ptr(),
+                                               1 if out.dtype is torch.float32 else 0,
+                                               _cache_ws(workspace, cache, need), need, _current(cache)),
+               "pisa_cache_attention_scored")
+        return out
     _check(lib.pisa_cache_attention(cache._ref, qs, T, Hq,
                                     _per_sequence(lengths, "lengths", cache), ip, Ksel, out.data_ptr(),
                                     1 if out.dtype is torch.float32 else 0, _cache_ws(workspace, cache, need), need,
                                     _current(cache)), "pisa_cache_attention")
     return out
+
+
+def _slopes(slopes: torch.Tensor | None, Hq: int, cache: PagedCache):
+    if slopes is None:
+        return None
+    if (slopes.dtype is not torch.float32 or slopes.shape != (Hq,) or slopes.get_device() != cache._index
+            or not slopes.is_contiguous()):
+        raise ValueError(f"slopes must be a contiguous fp32 tensor [{Hq}] on the cache's device")
+    return slopes.data_ptr()
+
+
+def _window(window: int) -> int:
+    if window < 0:
+        raise ValueError("window must not be negative")
+    return min(window, (1 << 31) - 1)
+
+
+def cache_prompt_attention(q: torch.Tensor, cache: PagedCache, start: torch.Tensor, counts: torch.Tensor | None = None,
+                           out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None,
+                           cap: float = 0.0, slopes: torch.Tensor | None = None, window: int = 0,
+                           first: torch.Tensor | None = None, last: torch.Tensor | None = None) -> torch.Tensor:
+    """A prompt's tokens, or those of a chunk of one, attend over the cache, in which they already are.
+
+    q [B, T, Hq, 64] bf16, any T; query t < counts[b] (int32 [B]; None: all T) of sequence b has position
+    start[b] + t (int32 [B]) and sees the tokens up to its own.  window, cap and slopes as in cache_attention.
+    first int32 [B, T]: a query sees no token before it (documents).  last int32 [B, T]: it sees the tokens before
+    that one instead of those up to its own (a prefix that is seen from both sides).  out bf16 [B, T, Hq, 64]
+    (allocated here when not given; rows t >= counts[b] are not written).  workspace as in cache_attention.
+    """
+    guard = _on(cache, stream)
+    if guard is not None:
+        with guard:
+            return cache_prompt_attention(q, cache, start, counts, out, workspace, None, cap, slopes, window, first,
+                                          last)
+    if q.dim() != 4:
+        raise ValueError("q must be a bf16 tensor [B, T, Hq, 64]")
+    _, T, Hq, _ = q.shape
+    B = cache.B
+    shape = (B, T, Hq, D)
+    qs = _rows(q, "q", cache, shape)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+    elif (out.dtype is not torch.bfloat16 or out.get_device() != cache._index or out.shape != shape
+          or not out.is_contiguous()):
+        raise ValueError(f"out must be a contiguous bf16 tensor {list(shape)} on the cache's device")
+    spans = []
+    for x, what in ((first, "first"), (last, "last")):
+        if x is not None and (x.dtype is not torch.int32 or x.shape != (B, T) or x.get_device() != cache._index
+                              or not x.is_contiguous()):
+            raise ValueError(f"{what} must be a contiguous int32 tensor [{B}, {T}] on the cache's device")
+        spans.append(None if x is None else x.data_ptr())
+    lib = _lib or load()
+    need = _cache_ws_bytes or cache_workspace_bytes()
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
+    _check(lib.pisa_cache_prompt_attention(
+        cache._ref, qs, T, Hq, _per_sequence(start, "start", cache),
+        None if counts is None else _per_sequence(counts, "counts", cache), *spans, cap, _slopes(slopes, Hq, cache),
+        _window(window), out.data_ptr(), _cache_ws(workspace, cache, need), need, _current(cache)),
+        "pisa_cache_prompt_attention")
+    return out
+
+
+class _PoolStruct(ctypes.Structure):
+    _fields_ = [
+        ("pages", ctypes.c_void_p),
+        ("table", ctypes.c_void_p),
+        ("refs", ctypes.c_void_p),
+        ("page_stride", ctypes.c_int64),
+        ("page_bytes", ctypes.c_int64),
+        ("B", ctypes.c_int),
+        ("page_size", ctypes.c_int),
+        ("n_pages", ctypes.c_int),
+        ("max_pages", ctypes.c_int),
+    ]
+
+
+class PagePool:
+    """Pages that sequences share: the pages of one or more layers, the table that maps a sequence's tokens to them,
+    and how many table entries hold each page.
+
+    pages: any tensor [n_pages, ...] whose pages are contiguous and a multiple of 16 bytes.  table: int32
+    [B, max_pages], -1 where a sequence holds no page.  refs: int32 [n_pages], 0: the page is free.  cache_fork,
+    cache_reserve and cache_compact keep the two in line.  layer(i) gives the PagedCache of a pool that was made
+    by allocate.  The tensors' contents may change, the tensors may not.
+    """
+
+    __slots__ = ("pages", "table", "refs", "page_size", "B", "n_pages", "max_pages", "device", "_struct", "_ref",
+                 "_index")
+
+    def __init__(self, pages: torch.Tensor, table: torch.Tensor, refs: torch.Tensor, page_size: int):
+        if page_size not in (16, 32, 64, 128, 256):
+            raise ValueError("page_size must be 16, 32, 64, 128 or 256")
+        if pages.dim() < 2 or pages.shape[0] < 1 or not pages[0].is_contiguous():
+            raise ValueError("pages must be a tensor [n_pages, ...] whose pages are contiguous")
+        size = pages[0].numel() * pages.element_size()
+        if size < 16 or size % 16:
+            raise ValueError("a page must be a multiple of 16 bytes")
+        if table.dtype != torch.int32 or table.dim() != 2 or not table.is_contiguous() or table.numel() < 1:
+            raise ValueError("table must be a contiguous int32 tensor [B, max_pages]")
+        if refs.dtype != torch.int32 or refs.shape != pages.shape[:1] or not refs.is_contiguous():
+            raise ValueError("refs must be a contiguous int32 tensor [n_pages]")
+        if not pages.is_cuda or table.device != pages.device or refs.device != pages.device:
+            raise ValueError("pages, table and refs must be on the same CUDA device")
+        self.pages, self.table, self.refs, self.page_size = pages, table, refs, page_size
+        self.n_pages = pages.shape[0]
+        self.B, self.max_pages = table.shape
+        self.device = pages.device
+        self._index = pages.get_device()
+        stride = pages.stride(0) * pages.element_size() if self.n_pages > 1 else size
+        self._struct = _PoolStruct(pages.data_ptr(), table.data_ptr(), refs.data_ptr(), stride, size, self.B, page_size,
+                                   self.n_pages, self.max_pages)
+        self._ref = ctypes.byref(self._struct)
+
+    @classmethod
+    def allocate(cls, B: int, n_cap: int, Hkv: int, n_pages: int, page_size: int = 64, bits: int = 16, layers: int = 1,
+                 device="cuda") -> "PagePool":
+        """n_pages free pages of `layers` layers each, and an empty table for B sequences of up to n_cap tokens."""
+        if (page_size not in (16, 32, 64, 128, 256) or bits not in (4, 16)
+                or min(B, n_cap, Hkv, n_pages, layers) < 1):
+            raise ValueError("page_size 16, 32, 64, 128 or 256, bits 4 or 16, B, n_cap, Hkv, n_pages and layers at least 1")
+        U = min(page_size, 64)
+        shape = (n_pages, layers, Hkv, page_size // U) + ((2, U, D) if bits == 16 else (72 * U,))
+        pages = torch.zeros(shape, dtype=torch.bfloat16 if bits == 16 else torch.uint8, device=device)
+        table = torch.full((B, -(-n_cap // page_size)), -1, dtype=torch.int32, device=pages.device)
+        return cls(pages, table, torch.zeros(n_pages, dtype=torch.int32, device=pages.device), page_size)
+
+    def layer(self, i: int = 0, k_exp: int = 0, v_exp: int = 0) -> PagedCache:
+        """The cache of layer i of pages [n_pages, layers, Hkv, ...], with the pool's table."""
+        return PagedCache(self.pages[:, i], self.table, self.page_size, k_exp, v_exp)
+
+
+def pool_workspace_bytes(pool: PagePool) -> int:
+    return int(load().pisa_pool_workspace_bytes(pool.n_pages, pool.B))
+
+
+def pool_workspace(pool: PagePool) -> torch.Tensor:
+    """A workspace for the calls on this pool, its status word zero.  One stream at a time; the word keeps the first
+    error of all the calls (check_device_status)."""
+    return torch.zeros(pool_workspace_bytes(pool), dtype=torch.uint8, device=pool.device)
+
+
+def cache_fork(pool: PagePool, parents: torch.Tensor, lengths: torch.Tensor, workspace: torch.Tensor | None = None,
+               stream=None) -> None:
+    """Sequences become copies of others by sharing their pages, all at once: sequence b takes the pages and the
+    length that parents[b] had (int32 [B]; b: it stays as it is; -1: it is freed, its length 0).  lengths int32 [B] is
+    updated in place.  workspace (of pool_workspace): for the status word only."""
+    guard = _on(pool, stream)
+    if guard is not None:
+        with guard:
+            return cache_fork(pool, parents, lengths, workspace)
+    _check((_lib or load()).pisa_cache_fork(
+        pool._ref, _per_sequence(parents, "parents", pool), _per_sequence(lengths, "lengths", pool),
+        None if workspace is None else _cache_ws(workspace, pool, 4), _current(pool)), "pisa_cache_fork")
+
+
+def cache_reserve(pool: PagePool, lengths: torch.Tensor, T: int, counts: torch.Tensor | None = None,
+                  granted: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+    """Pages for the next counts[b] (0 to T; None: T) tokens of every sequence, its own alone: missing ones are taken
+    from the free pages, lowest number first, and shared ones are replaced, the one that holds tokens before lengths[b]
+    being copied.  Returns granted int32 [B]: counts[b], or 0 where the pages did not suffice (that sequence and those
+    after it that need any stay as they are); it is what cache_append takes as counts.  workspace of pool_workspace."""
+    guard = _on(pool, stream)
+    if guard is not None:
+        with guard:
+            return cache_reserve(pool, lengths, T, counts, granted, workspace)
+    if granted is None:
+        granted = torch.empty(pool.B, dtype=torch.int32, device=pool.device)
+    lib = _lib or load()
+    need = int(lib.pisa_pool_workspace_bytes(pool.n_pages, pool.B))
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=pool.device)
+    _check(lib.pisa_cache_reserve(
+        pool._ref, _per_sequence(lengths, "lengths", pool), T,
+        None if counts is None else _per_sequence(counts, "counts", pool), _per_sequence(granted, "granted", pool),
+        _cache_ws(workspace, pool, need), need, _current(pool)), "pisa_cache_reserve")
+    return granted
+
+
+def cache_compact(pool: PagePool, used: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+    """Moves the pages in use to the front of the pool, in the table and refs too.  Returns used int32 [1], how many
+    there are: pages from that number on are free.  workspace of pool_workspace."""
+    guard = _on(pool, stream)
+    if guard is not None:
+        with guard:
+            return cache_compact(pool, used, workspace)
+    if used is None:
+        used = torch.empty(1, dtype=torch.int32, device=pool.device)
+    elif used.dtype is not torch.int32 or used.shape != (1,) or used.get_device() != pool._index:
+        raise ValueError("used must be an int32 tensor [1] on the pool's device")
+    lib = _lib or load()
+    need = int(lib.pisa_pool_workspace_bytes(pool.n_pages, pool.B))
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=pool.device)
+    _check(lib.pisa_cache_compact(pool._ref, used.data_ptr(), _cache_ws(workspace, pool, need), need, _current(pool)),
+           "pisa_cache_compact")
+    return used
 
 
 def kernel_launches() -> int:

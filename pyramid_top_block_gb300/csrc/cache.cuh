@@ -19,6 +19,7 @@
 #include <cuda_fp8.h>
 
 #include "api.cuh"
+#include "scores.cuh"
 
 namespace pisa {
 
@@ -96,6 +97,9 @@ struct CacheAppendLaunch {
   const float* rotary;    // [n_rot, rot]: cosines, then sines
   long long n_rot;
   int rot, interleaved;
+  const int32_t* positions;  // [n_axes, B, T], or nullptr: a token turns by its position in the cache
+  int n_axes;
+  unsigned long long axis_of;  // the axis of pair i: bits 2 i and 2 i + 1
   int* status;  // may be nullptr
 };
 
@@ -119,6 +123,7 @@ struct CacheAttendLaunch {
   int out_f32;
   int* status;
   float* part;  // partial results (see cache_attend.cuh)
+  ScoreDev score;  // (of the scored forms only)
 };
 
 // The launch is programmatic: a kernel may start while the one before it in the stream ends,
@@ -165,6 +170,8 @@ cudaError_t launch_cache_append(const CacheAppendLaunch& L, cudaStream_t s);
 cudaError_t launch_cache_read(const CacheReadLaunch& L, cudaStream_t s);
 cudaError_t launch_cache_attend_bf16(const CacheAttendLaunch& L, cudaStream_t s);
 cudaError_t launch_cache_attend_e2m1(const CacheAttendLaunch& L, cudaStream_t s);
+cudaError_t launch_cache_score_bf16(const CacheAttendLaunch& L, cudaStream_t s);
+cudaError_t launch_cache_score_e2m1(const CacheAttendLaunch& L, cudaStream_t s);
 size_t cache_part_bytes();
 
 }  // namespace pisa

@@ -163,8 +163,33 @@ struct Turn {
 template <bool INTER, bool FULL>
 constexpr bool kPairs = FULL && !INTER;
 
-template <bool INTER>
-__device__ __forceinline__ void load_turn(const CacheAppendLaunch& a, long long p, int lane, Turn& t) {
+constexpr int kMaxAxes = 4;
+
+// Where the angles of a token's axes lie: its positions times rot / 16, in steps of 16 floats (positions are below
+// 2^27 where there are axes).
+struct AxisRows {
+  uint32_t at[kMaxAxes];
+  bool one;  // all axes agree, as in text
+};
+
+// The angles of pairs i .. i + N - 1, each from its own axis's row.  Pairs of one axis need not be
+// neighbours, so the words are loaded one by one; they come from three or four rows of at most 256 bytes.
+template <int N>
+__device__ __forceinline__ void load_axes(const CacheAppendLaunch& a, const AxisRows& rows, int i, float (&u)[N],
+                                          float (&v)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const unsigned axis = (unsigned)(a.axis_of >> (2 * (i + e))) & 3u;
+    const uint32_t lo = axis & 1 ? rows.at[1] : rows.at[0], hi = axis & 1 ? rows.at[3] : rows.at[2];
+    const float* row = a.rotary + (size_t)(axis & 2 ? hi : lo) * 16 + i + e;
+    u[e] = row[0];
+    v[e] = row[a.rot >> 1];
+  }
+}
+
+template <bool INTER, bool AXES>
+__device__ __forceinline__ void load_turn(const CacheAppendLaunch& a, long long p, const AxisRows& rows, int lane,
+                                          Turn& t) {
   const int c = lane & 7;
   const int half = a.rot >> 4;  // lanes of one half of the rotated dims (split-halves order)
   t.on = c < 2 * half;
@@ -177,9 +202,15 @@ __device__ __forceinline__ void load_turn(const CacheAppendLaunch& a, long long 
   if (!t.on) return;
   const float* row = a.rotary + p * a.rot;
   if (INTER) {
-    const float4 u = *reinterpret_cast<const float4*>(row + 4 * c);
-    const float4 v = *reinterpret_cast<const float4*>(row + (a.rot >> 1) + 4 * c);
-    const float uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+    float uu[4], vv[4];
+    if (AXES && !rows.one) {
+      load_axes(a, rows, 4 * c, uu, vv);
+    } else {
+      const float4 u = *reinterpret_cast<const float4*>(row + 4 * c);
+      const float4 v = *reinterpret_cast<const float4*>(row + (a.rot >> 1) + 4 * c);
+      uu[0] = u.x, uu[1] = u.y, uu[2] = u.z, uu[3] = u.w;
+      vv[0] = v.x, vv[1] = v.y, vv[2] = v.z, vv[3] = v.w;
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       t.c[e] = uu[e >> 1];
@@ -188,11 +219,16 @@ __device__ __forceinline__ void load_turn(const CacheAppendLaunch& a, long long 
   } else {
     const bool low = c < half;
     t.from = low ? lane + half : lane - half;
-    const float4* u = reinterpret_cast<const float4*>(row + 8 * (low ? c : c - half));
-    const float4* v = reinterpret_cast<const float4*>(row + (a.rot >> 1) + 8 * (low ? c : c - half));
-    const float4 u0 = u[0], u1 = u[1], v0 = v[0], v1 = v[1];
-    const float uu[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
-    const float vv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    float uu[8], vv[8];
+    if (AXES && !rows.one) {
+      load_axes(a, rows, 8 * (low ? c : c - half), uu, vv);
+    } else {
+      const float4* u = reinterpret_cast<const float4*>(row + 8 * (low ? c : c - half));
+      const float4* v = reinterpret_cast<const float4*>(row + (a.rot >> 1) + 8 * (low ? c : c - half));
+      const float4 u0 = u[0], u1 = u[1], v0 = v[0], v1 = v[1];
+      uu[0] = u0.x, uu[1] = u0.y, uu[2] = u0.z, uu[3] = u0.w, uu[4] = u1.x, uu[5] = u1.y, uu[6] = u1.z, uu[7] = u1.w;
+      vv[0] = v0.x, vv[1] = v0.y, vv[2] = v0.z, vv[3] = v0.w, vv[4] = v1.x, vv[5] = v1.y, vv[6] = v1.z, vv[7] = v1.w;
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       t.c[e] = uu[e];
@@ -220,7 +256,8 @@ __device__ __forceinline__ void turn_row(const Turn& t, bool rotate, uint32_t (&
 // A warp takes every parts-th group of four rows of one token: the groups of its query rows,
 // then those of its key and value rows (keys first).  FULL: all 64 dims turn (the query rows then
 // need no choice between old and new words: 55.8 -> 53.2 us for 32768 tokens).
-template <int KIND, bool INTER, bool FULL>
+// AXES: a token turns by positions of its own, one for each axis, instead of its place in the cache.
+template <int KIND, bool INTER, bool FULL, bool AXES>
 __global__ void __launch_bounds__(kAppWarps * 32, 6) cache_append_kernel(CacheAppendLaunch a, int parts) {
   after_the_one_before();
   const int lane = threadIdx.x & 31, sub = lane >> 3, c = lane & 7;
@@ -264,6 +301,23 @@ __global__ void __launch_bounds__(kAppWarps * 32, 6) cache_append_kernel(CacheAp
     return z;
   };
   uint4 xkv = fetch_kv(ikv);
+  AxisRows rows;
+  long long turn_at = 0;  // the position that a token whose axes agree turns by
+  bool placed = true;  // whether all positions are in the table
+  if constexpr (AXES) {
+    int at[kMaxAxes];
+#pragma unroll
+    for (int x = 0; x < kMaxAxes; ++x)
+      at[x] = x < a.n_axes ? a.positions[((long long)x * a.cache.B + b) * a.T + t] : at[0];
+    rows.one = true;
+    turn_at = at[0];
+#pragma unroll
+    for (int x = 0; x < kMaxAxes; ++x) {
+      placed = placed && at[x] >= 0 && at[x] < a.n_rot;
+      rows.one = rows.one && at[x] == at[0];
+      rows.at[x] = (uint32_t)at[x] * (uint32_t)(a.rot >> 4);
+    }
+  }
   const int count = a.counts ? a.counts[b] : a.T;
   const long long p = (long long)a.start[b] + t;
   if (t >= count) return;
@@ -275,16 +329,16 @@ __global__ void __launch_bounds__(kAppWarps * 32, 6) cache_append_kernel(CacheAp
       asm volatile("prefetch.global.L2 [%0];" ::"l"(from.data + b * from.sb + later * from.st + h * from.sh));
     }
     const long long at = (long long)a.start[b] + later;
-    if (lane < 2 && a.rot && at >= 0 && at < a.n_rot)
+    if (!AXES && lane < 2 && a.rot && at >= 0 && at < a.n_rot)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(a.rotary + at * a.rot + (a.rot > 32 ? 32 * lane : 0)));
   }
   const long long cap = (long long)a.cache.max_pages << a.cache.page_shift;
-  bool ok = p >= 0 && p < cap && (a.rot == 0 || p < a.n_rot);
+  bool ok = p >= 0 && p < cap && (AXES ? placed : a.rot == 0 || p < a.n_rot);
   int page = -1;
   Turn turn;
   if (ok) {
     page = a.cache.table[(long long)b * a.cache.max_pages + (p >> a.cache.page_shift)];
-    load_turn<INTER>(a, p, lane, turn);
+    load_turn<INTER, AXES>(a, AXES ? turn_at : p, rows, lane, turn);
     ok = page >= 0 && page < a.cache.n_pages;
   }
   if (!ok) {  // the token is left out
@@ -456,11 +510,14 @@ cudaError_t launch_cache_append(const CacheAppendLaunch& L, cudaStream_t s) {
   while (parts < groups && tokens * parts < 152 * 16) ++parts;
   const dim3 grid((unsigned)(((long long)L.T * parts + kAppWarps - 1) / kAppWarps), 1, (unsigned)L.cache.B);
   constexpr int kThreads = kAppWarps * 32;
-  const auto go = [&](auto kind, auto inter) {
+  const auto launch = [&](auto kind, auto inter, auto axes) {
     constexpr int kKind = decltype(kind)::value;
-    constexpr bool kInter = decltype(inter)::value;
-    return L.rot == kD ? launch_early<cache_append_kernel<kKind, kInter, true>>(grid, kThreads, 0, s, L, parts)
-                       : launch_early<cache_append_kernel<kKind, kInter, false>>(grid, kThreads, 0, s, L, parts);
+    constexpr bool kInter = decltype(inter)::value, kAxes = decltype(axes)::value;
+    return L.rot == kD ? launch_early<cache_append_kernel<kKind, kInter, true, kAxes>>(grid, kThreads, 0, s, L, parts)
+                       : launch_early<cache_append_kernel<kKind, kInter, false, kAxes>>(grid, kThreads, 0, s, L, parts);
+  };
+  const auto go = [&](auto kind, auto inter) {
+    return L.positions ? launch(kind, inter, std::true_type{}) : launch(kind, inter, std::false_type{});
   };
   using Bf16 = std::integral_constant<int, PISA_CACHE_BF16>;
   using E2m1 = std::integral_constant<int, PISA_CACHE_E2M1>;

@@ -158,6 +158,10 @@ struct RowState {
   float l0, l1;       // this lane's share of the sums of the weights
   float o[8][4];
   bool bad;  // a page out of range was met
+  // the scored forms:
+  float t0, t1;          // factors of the scores of rows g and g + 8
+  float slope0, slope1;  // what a token's distance takes off, base 2
+  int bad_rows;          // bits 0 and 1: rows g and g + 8 see a page out of range
 };
 
 // Where dims 4 c .. 4 c + 3 of row r lie in a warp's 16 x 64 part of the merge buffer (floats).
@@ -205,6 +209,7 @@ __device__ __forceinline__ void reset(RowState<KIND>& s) {
   s.far = false;
   s.l0 = s.l1 = 0.f;
   s.bad = false;
+  s.bad_rows = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) s.o[i][0] = s.o[i][1] = s.o[i][2] = s.o[i][3] = 0.f;
 }
@@ -217,10 +222,12 @@ __device__ __forceinline__ void reset(RowState<KIND>& s) {
 // infinity; rows below 2^-100 have logits of zero, whatever becomes of them.  A factor of the
 // logits that is past the range of 32 bits is cut to it: logits of zero stay so, and others, if
 // they fit 32 bits at all, still differ by far more than weights can show.
-template <int KIND>
-__device__ __forceinline__ void make_q(const CacheAttendLaunch& a, const QueryWords& q, int lane, RowState<KIND>& s) {
+template <int KIND, bool SCORED>
+__device__ __forceinline__ void make_q(const CacheAttendLaunch& a, const QueryWords& q, const Unit& u, int lane,
+                                       RowState<KIND>& s) {
   const int j = lane & 3;
-  float f[2] = {kScale * kLog2e, kScale * kLog2e};
+  constexpr float kFactor = SCORED ? kScale : kScale * kLog2e;  // (scored: base 2 comes with the logits)
+  float f[2] = {kFactor, kFactor};
   if (KIND == PISA_CACHE_E2M1) {
     uint32_t w[2][8];
 #pragma unroll
@@ -267,8 +274,20 @@ __device__ __forceinline__ void make_q(const CacheAttendLaunch& a, const QueryWo
         s.qa[ks][2 + h] = hi;
       }
   }
-  s.f0 = f[0];
-  s.f1 = f[1];
+  if constexpr (SCORED) {
+    s.t0 = f[0];
+    s.t1 = f[1];
+    s.f0 = s.f1 = 1.f;
+    s.slope0 = s.slope1 = 0.f;
+    const int r0 = u.r0 + (lane >> 2), r1 = r0 + 8;
+    if (a.score.slopes) {
+      if (r0 < u.rows) s.slope0 = a.score.slopes[u.kv * a.G + r0 % a.G] * kLog2e;
+      if (r1 < u.rows) s.slope1 = a.score.slopes[u.kv * a.G + r1 % a.G] * kLog2e;
+    }
+  } else {
+    s.f0 = f[0];
+    s.f1 = f[1];
+  }
 }
 
 // The key (of 16 in a group) behind column element (half h of the group, e) of lane j.
@@ -313,15 +332,15 @@ __device__ __forceinline__ void load_v(uint32_t st, int i, int lane, uint32_t (&
   }
 }
 
-// Makes the values of a staged tile's keys from `limit` on count as zeros, whatever the
-// memory holds (4 bits: a zero scale; a code is always finite).
+// Makes the values of a staged tile's keys before `from` and from `limit` on count as zeros, whatever
+// the memory holds (4 bits: a zero scale; a code is always finite).
 template <int KIND, int U>
-__device__ __forceinline__ void clear_v(uint32_t st, int lane, int limit) {
+__device__ __forceinline__ void clear_v(uint32_t st, int lane, int from, int limit) {
   constexpr int KT = Cfg<KIND>::KT;
 #pragma unroll
   for (int x = 0; x < KT / 32; ++x) {
     const int key = lane + 32 * x;
-    if (key < limit) continue;
+    if (key >= from && key < limit) continue;
     if (KIND == PISA_CACHE_E2M1) {
       using L = E2m1Tile<U>;
       *reinterpret_cast<uint32_t*>(ca_smem + st + L::vs(key >> 4) + (key & 15) * 4) = 0u;
@@ -421,27 +440,87 @@ __device__ __forceinline__ void products(uint32_t st_k, uint32_t st_v, int lane,
 }
 
 // What the rows of a row tile see of the tile of keys that starts at token `first`.
+// A row sees the tokens from l on and before n (plain attention: l is zero).
 struct Sight {
-  int n0, n1;      // tokens that rows g and g + 8 see
-  int n_lo, n_hi;  // tokens that all rows, that any row sees
+  int n0, n1;      // n of rows g and g + 8
+  int n_lo, n_hi;  // the least, the largest n
+  int l0, l1;      // l of rows g and g + 8
+  int l_lo, l_hi;  // the least, the largest l
 };
 
+// The scored forms: a tile's products as base-2 logits (s.f0 and s.f1 are 1 from here on).
+template <int KIND>
+__device__ __forceinline__ void score(const CacheAttendLaunch& a, int first, const Sight& see, int lane,
+                                      const RowState<KIND>& s, float (&sc)[Cfg<KIND>::KT / 8][4]) {
+  constexpr int KT = Cfg<KIND>::KT;
+  const int j = lane & 3;
+  if (a.score.cap > 0.f) {
+    const CapRow r0 = {s.t0 * a.score.inv_cap, s.t0 * kLog2e}, r1 = {s.t1 * a.score.inv_cap, s.t1 * kLog2e};
+    float b0 = 0.f, b1 = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < KT / 8; ++nt) {
+      b0 = max3(b0, fabsf(sc[nt][0]), fabsf(sc[nt][1]));
+      b1 = max3(b1, fabsf(sc[nt][2]), fabsf(sc[nt][3]));
+    }
+    // (a NaN passes the comparison unseen, and the polynomial keeps it)
+    if (__any_sync(kFull, b0 * r0.to_y > 1.f || b1 * r1.to_y > 1.f)) {
+      const float top = a.score.cap * kLog2e;
+#pragma unroll
+      for (int nt = 0; nt < KT / 8; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          sc[nt][e] = cap_any(sc[nt][e], r0, top);
+          sc[nt][2 + e] = cap_any(sc[nt][2 + e], r1, top);
+        }
+    } else {
+#pragma unroll
+      for (int nt = 0; nt < KT / 8; ++nt) {
+        cap_small(sc[nt][0], sc[nt][1], r0);
+        cap_small(sc[nt][2], sc[nt][3], r1);
+      }
+    }
+  } else {
+    const float t0 = s.t0 * kLog2e, t1 = s.t1 * kLog2e;
+#pragma unroll
+    for (int nt = 0; nt < KT / 8; ++nt) {
+      sc[nt][0] *= t0;
+      sc[nt][1] *= t0;
+      sc[nt][2] *= t1;
+      sc[nt][3] *= t1;
+    }
+  }
+  if (a.score.slopes) {
+    // (distances are whole numbers, exact up to 2^24; the row's own position is n - 1)
+    const float d0 = (float)(first - see.n0 + 1), d1 = (float)(first - see.n1 + 1);
+#pragma unroll
+    for (int nt = 0; nt < KT / 8; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float k = (float)(16 * (nt >> 1) + 8 * (nt & 1)) + (KIND == PISA_CACHE_BF16 ? 2 * j + e : j + 4 * e);
+        sc[nt][e] = fmaf(s.slope0, d0 + k, sc[nt][e]);
+        sc[nt][2 + e] = fmaf(s.slope1, d1 + k, sc[nt][2 + e]);
+      }
+  }
+}
+
 // The running softmax: logits to weights.  O must hold all earlier tiles.
-template <int KIND, int U, int NP>
-__device__ __forceinline__ void weigh(uint32_t st, int first, const Sight& see, int lane, RowState<KIND>& s,
-                                      float (&sc)[Cfg<KIND>::KT / 8][4], Weights<KIND, NP>& w, float* scratch) {
+template <int KIND, int U, int NP, bool SCORED>
+__device__ __forceinline__ void weigh(const CacheAttendLaunch& a, uint32_t st, int first, const Sight& see, int lane,
+                                      RowState<KIND>& s, float (&sc)[Cfg<KIND>::KT / 8][4], Weights<KIND, NP>& w,
+                                      float* scratch) {
   using C = Cfg<KIND>;
   constexpr int KT = C::KT;
   const int g = lane >> 2, j = lane & 3;
-  const bool masked = first + KT > see.n_lo;
+  if constexpr (SCORED) score<KIND>(a, first, see, lane, s, sc);
+  const bool masked = first + KT > see.n_lo || (SCORED && first < see.l_hi);
   if (masked) {
 #pragma unroll
     for (int nt = 0; nt < KT / 8; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int key = first + 16 * (nt >> 1) + key_of<KIND>(nt & 1, j, e);
-        if (key >= see.n0) sc[nt][e] = -INFINITY;
-        if (key >= see.n1) sc[nt][2 + e] = -INFINITY;
+        if (key >= see.n0 || (SCORED && key < see.l0)) sc[nt][e] = -INFINITY;
+        if (key >= see.n1 || (SCORED && key < see.l1)) sc[nt][2 + e] = -INFINITY;
       }
   }
   // A row's reference m is, where it was last set, the maximum of its logits so far less kShift; it is
@@ -527,20 +606,22 @@ __device__ __forceinline__ void weigh(uint32_t st, int first, const Sight& see, 
     // rows see (of the row tile's later queries) reach the others: these few keys are added
     // one by one to the rows that see them, and cleared like the rest.
     const int k_lo = min(max(see.n_lo - first, 0), KT), k_hi = min(max(see.n_hi - first, 0), KT);
-    if (k_lo < k_hi) {  // (at most 15 keys: those between the first and the last query)
+    // (the same for the tokens between the rows' first ones)
+    const int z_lo = SCORED ? min(max(see.l_lo - first, 0), KT) : 0, z_hi = SCORED ? min(max(see.l_hi - first, 0), KT) : 0;
+    const auto one_by_one = [&](int from, int to) {  // at most 16 keys
 #pragma unroll
       for (int nt = 0; nt < KT / 8; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int key = 16 * (nt >> 1) + key_of<KIND>(nt & 1, j, e) - k_lo;
+          const int key = 16 * (nt >> 1) + key_of<KIND>(nt & 1, j, e) - from;
           if (key >= 0 && key < 16) {
             scratch[key * 16 + g] = sc[nt][e];
             scratch[key * 16 + g + 8] = sc[nt][2 + e];
           }
         }
       __syncwarp();
-      for (int key = k_lo; key < k_hi; ++key) {
-        const float p0 = scratch[(key - k_lo) * 16 + g], p1 = scratch[(key - k_lo) * 16 + g + 8];
+      for (int key = from; key < to; ++key) {
+        const float p0 = scratch[(key - from) * 16 + g], p1 = scratch[(key - from) * 16 + g + 8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float v[2];
@@ -557,14 +638,23 @@ __device__ __forceinline__ void weigh(uint32_t st, int first, const Sight& see, 
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            if (first + key < see.n0) s.o[i][e] = fmaf(p0, v[e], s.o[i][e]);
-            if (first + key < see.n1) s.o[i][2 + e] = fmaf(p1, v[e], s.o[i][2 + e]);
+            if (first + key < see.n0 && (!SCORED || first + key >= see.l0)) s.o[i][e] = fmaf(p0, v[e], s.o[i][e]);
+            if (first + key < see.n1 && (!SCORED || first + key >= see.l1)) s.o[i][2 + e] = fmaf(p1, v[e], s.o[i][2 + e]);
           }
         }
       }
       __syncwarp();
+    };
+    if constexpr (SCORED) {
+      // keys z_hi .. k_lo - 1 are seen by all rows (none, where the windows are shorter than the rows are apart)
+      const int to = min(z_hi, k_hi);
+      if (z_lo < to) one_by_one(z_lo, to);  // (at most 15 keys: those between the first and the last query's window)
+      const int from = max(max(k_lo, z_hi), z_lo);
+      if (from < k_hi) one_by_one(from, k_hi);
+    } else {
+      if (k_lo < k_hi) one_by_one(k_lo, k_hi);  // (at most 15 keys: those between the first and the last query)
     }
-    clear_v<KIND, U>(st, lane, k_lo);
+    clear_v<KIND, U>(st, lane, z_hi, k_lo);
     __syncwarp();
   }
   // The weights go into the product with V as one fp16 part (4-bit pages) or two bf16 parts, and
@@ -601,7 +691,7 @@ __device__ __forceinline__ void weigh(uint32_t st, int first, const Sight& see, 
 // three stages: while one is on its way, the logits of the next tile and the products with V
 // of the one before are computed side by side.  (Keys and values in rings of their own, with
 // two tiles on their way, were 2 to 4 % slower: the memory system is full with one.)
-template <int KIND, int U, int NP, int W, bool LIST>
+template <int KIND, int U, int NP, int W, bool LIST, bool SCORED>
 __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit& u, const QueryWords& q,
                                           const int (&blk)[2], int i0, int i1, uint32_t ring, float* scratch, int warp,
                                           int lane, RowState<KIND>& s) {
@@ -611,20 +701,29 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
   constexpr int E = KT > U ? KT / U : 1;  // records of a tile
   constexpr int kAhead = 32 / E;          // tiles a look ahead covers
   constexpr uint32_t kStage = kStageBytes<KIND>;
+  constexpr int kLen = U < KT ? U : KT;  // tokens of a tile that lie in one record
   static_assert(C::kStages == 3, "");
   const int g = lane >> 2;
   // what each row sees: tokens before n_vis(t) = n - T + t + 1
   const int ra = u.r0 + g, rb = ra + 8;
   const int base = u.n - a.T + 1 + u.t_first;
   const int last = min(u.rows, u.r0 + 16) - 1;
-  const Sight see = {ra < u.rows ? base + ra / a.G : 0, rb < u.rows ? base + rb / a.G : 0, base + u.r0 / a.G,
-                     base + last / a.G};
+  Sight see = {ra < u.rows ? base + ra / a.G : 0, rb < u.rows ? base + rb / a.G : 0, base + u.r0 / a.G,
+               base + last / a.G, 0, 0, 0, 0};
+  if constexpr (SCORED) {
+    const int w = a.score.window;
+    see.l0 = max(see.n0 - w, 0);
+    see.l1 = max(see.n1 - w, 0);
+    see.l_lo = max(see.n_lo - w, 0);
+    see.l_hi = max(see.n_hi - w, 0);
+  }
   int* list = reinterpret_cast<int*>(scratch);  // (listed: a row tile is one query's, so weigh leaves it alone)
   if (listed) {  // the listed blocks that count, in the order of the list
     unsigned some[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      some[h] = __ballot_sync(kFull, blk[h] >= 0 && blk[h] < (1 << 21) && blk[h] * kC < see.n_hi);
+      some[h] = __ballot_sync(kFull, blk[h] >= 0 && blk[h] < (1 << 21) && blk[h] * kC < see.n_hi &&
+                                         (!SCORED || blk[h] * kC + kC > see.l_lo));
     const unsigned below = (1u << lane) - 1u;
     if (some[0] >> lane & 1) list[__popc(some[0] & below)] = blk[0];
     if (some[1] >> lane & 1) list[__popc(some[0]) + __popc(some[1] & below)] = blk[1];
@@ -632,6 +731,7 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
     i1 = (__popc(some[0]) + __popc(some[1])) * (kC / KT);
   } else {
     i1 = min(i1, (max(see.n_hi, 0) + KT - 1) / KT);
+    if constexpr (SCORED) i0 = max(i0, see.l_lo / KT);
   }
   const int mine = i1 - i0 > warp ? (i1 - i0 - warp + W - 1) / W : 0;  // the warp's tiles
   if (mine == 0) return;
@@ -651,7 +751,7 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
     int* first_bad = reinterpret_cast<int*>(scratch + kBadAt / 4);
     if (y < mine) {
       const int p = first_of(y) + (lane % E) * U;
-      if (p < see.n_hi) {
+      if (p < see.n_hi && (!SCORED || p + kLen > see.l_lo)) {
         page = table[p >> a.cache.page_shift];
         if (page >= 0 && page < a.cache.n_pages) {
           off = cache_record(a.cache, C::kRow, page, u.kv, p);
@@ -662,7 +762,14 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
         }
       }
     }
-    if (__any_sync(kFull, page < 0)) {
+    if constexpr (SCORED) {
+      for (unsigned m = __ballot_sync(kFull, page < 0); m; m &= m - 1) {
+        const int p = __shfl_sync(kFull, page < 0 ? first_of(y) + (lane % E) * U : 0, __ffs(m) - 1);
+        if (p < see.n0 && p + kLen > see.l0) s.bad_rows |= 1;
+        if (p < see.n1 && p + kLen > see.l1) s.bad_rows |= 2;
+        s.bad = true;
+      }
+    } else if (__any_sync(kFull, page < 0)) {
       const int p = page < 0 ? first_of(y) + (lane % E) * U : INT_MAX, q = __reduce_min_sync(kFull, p);
       if (lane == 0) *first_bad = s.bad ? min(*first_bad, q) : q;
       s.bad = true;
@@ -699,12 +806,12 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
   cpa_commit();
   if (mine > 1) issue(1, ring + kStage);
   cpa_commit();
-  make_q(a, q, lane, s);
+  make_q<KIND, SCORED>(a, q, u, lane, s);
   cpa_wait<1>();
   __syncwarp();
   const int f0 = first_of(0);
   products<KIND, U, NP, true, false>(ring, 0, lane, s, sc, w);
-  weigh<KIND, U, NP>(ring, f0, see, lane, s, sc, w, scratch);
+  weigh<KIND, U, NP, SCORED>(a, ring, f0, see, lane, s, sc, w, scratch);
   uint32_t cur = ring, next = ring + kStage, spare = ring + 2 * kStage;
   for (int x = 0; x + 1 < mine; ++x) {
     if (x + 2 < mine) {
@@ -715,7 +822,7 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
     cpa_wait<1>();  // tile x + 1 has come
     __syncwarp();
     products<KIND, U, NP, true, true>(next, cur, lane, s, sc, w);
-    weigh<KIND, U, NP>(next, first_of(x + 1), see, lane, s, sc, w, scratch);
+    weigh<KIND, U, NP, SCORED>(a, next, first_of(x + 1), see, lane, s, sc, w, scratch);
     __syncwarp();  // the reads of tile x are done before its stage is refilled
     const uint32_t t = cur;
     cur = next;
@@ -729,7 +836,10 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
     s.m0 = z.z;
     s.m1 = z.w;
   }
-  if (s.bad) {  // the rows that see a page out of range become NaN
+  if constexpr (SCORED) {
+    if (s.bad_rows & 1) s.l0 = __int_as_float(0x7fc00000);
+    if (s.bad_rows & 2) s.l1 = __int_as_float(0x7fc00000);
+  } else if (s.bad) {  // the rows that see a page out of range become NaN
     const int first_bad = *reinterpret_cast<const int*>(scratch + kBadAt / 4);
     if (first_bad < see.n0) s.l0 = __int_as_float(0x7fc00000);
     if (first_bad < see.n1) s.l1 = __int_as_float(0x7fc00000);
@@ -825,6 +935,17 @@ __device__ __forceinline__ int seq_len(const CacheAttendLaunch& a, int b, bool& 
   return n < 0 ? 0 : over ? (int)cap : n;
 }
 
+// The first tile that any query of a sequence of n tokens sees, and how many there are.
+template <int KIND, bool SCORED>
+__device__ __forceinline__ int first_tile(const CacheAttendLaunch& a, int n) {
+  return SCORED ? max(n - a.T + 1 - a.score.window, 0) / Cfg<KIND>::KT : 0;
+}
+template <int KIND, bool SCORED>
+__device__ __forceinline__ int unit_tiles(const CacheAttendLaunch& a, int n) {
+  constexpr int KT = Cfg<KIND>::KT;
+  return (n + KT - 1) / KT - first_tile<KIND, SCORED>(a, n);
+}
+
 // Places that a unit of nt tiles has in the stream: its tiles, and some for what a run spends at
 // its end (the warps' merge, the next unit's chain of loads; about 4 us), so that the runs that
 // change units take as long as the others.  Places at the end 0 / 12 / 24 / 36 / 48, us a call:
@@ -836,12 +957,11 @@ __device__ __forceinline__ int unit_places(int nt) {
 }
 
 // Places of all units before sequence b (b = B: of all): every warp computes it by itself.
-template <int KIND>
+template <int KIND, bool SCORED>
 __device__ __forceinline__ long long places_before(const CacheAttendLaunch& a, int b, int units, int lane) {
-  constexpr int KT = Cfg<KIND>::KT;
   long long sum = 0;
   bool over;
-  for (int i = lane; i < b; i += 32) sum += unit_places<KIND>((seq_len(a, i, over) + KT - 1) / KT);
+  for (int i = lane; i < b; i += 32) sum += unit_places<KIND>(unit_tiles<KIND, SCORED>(a, seq_len(a, i, over)));
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(kFull, sum, x);
   return sum * units;
@@ -849,14 +969,13 @@ __device__ __forceinline__ long long places_before(const CacheAttendLaunch& a, i
 
 // The sequence that place `at` of the stream belongs to, and the places before that sequence: 32
 // sequences at a time.
-template <int KIND>
+template <int KIND, bool SCORED>
 __device__ __forceinline__ int seq_of(const CacheAttendLaunch& a, long long at, int units, int lane, long long& base) {
-  constexpr int KT = Cfg<KIND>::KT;
   base = 0;
   for (int b0 = 0; b0 < a.cache.B; b0 += 32) {
     bool over;
     const int n = b0 + lane < a.cache.B ? seq_len(a, b0 + lane, over) : 0;
-    const long long t = (long long)unit_places<KIND>((n + KT - 1) / KT) * units;
+    const long long t = (long long)unit_places<KIND>(unit_tiles<KIND, SCORED>(a, n)) * units;
     long long inc = t;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
@@ -887,7 +1006,7 @@ constexpr int attend_smem() {
   return kRing<KIND, W> + W * (kScratch + 2 * 16 * 4);
 }
 
-template <int KIND, int U, int NP, int W>
+template <int KIND, int U, int NP, int W, bool SCORED>
 __global__ void __launch_bounds__(W * 32, Cfg<KIND>::kWarps / W) cache_attend_direct_kernel(CacheAttendLaunch a) {
   using C = Cfg<KIND>;
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (uniform to the compiler)
@@ -925,7 +1044,7 @@ __global__ void __launch_bounds__(W * 32, Cfg<KIND>::kWarps / W) cache_attend_di
   fetch_q(a, u, lane, q);
   RowState<KIND> s;
   reset(s);
-  run_tiles<KIND, U, NP, W, true>(a, u, q, blk, 0, 1 << 30, ring, scratch, warp, lane, s);
+  run_tiles<KIND, U, NP, W, true, SCORED>(a, u, q, blk, 0, 1 << 30, ring, scratch, warp, lane, s);
   if ((threadIdx.x == 0 && over) || (lane == 0 && s.bad)) set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
   merge_warps<KIND, W>(s, mo, ml, warp, lane);
   for (int i = threadIdx.x; i < 256; i += W * 32) {
@@ -935,10 +1054,10 @@ __global__ void __launch_bounds__(W * 32, Cfg<KIND>::kWarps / W) cache_attend_di
   }
 }
 
-template <int KIND, int U, int NP>
+template <int KIND, int U, int NP, bool SCORED>
 __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_kernel(CacheAttendLaunch a) {
   using C = Cfg<KIND>;
-  constexpr int KT = C::KT, W = C::kWarps;
+  constexpr int W = C::kWarps;
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t ring = warp * C::kStages * kStageBytes<KIND>;
   float* mo = reinterpret_cast<float*>(ca_smem);
@@ -952,7 +1071,7 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_
   // this CTA's run of the stream (and its row tile, where the row tiles go side by side)
   const int RT = (a.T * a.G + 15) / 16;
   const int units = a.cache.Hkv * (C::kSide ? 1 : RT);  // of a sequence
-  const long long total = places_before<KIND>(a, a.cache.B, units, lane);
+  const long long total = places_before<KIND, SCORED>(a, a.cache.B, units, lane);
   const long long per = run_length(total, C::kSide ? gridDim.x / RT : gridDim.x);
   long long cur = per * (C::kSide ? blockIdx.x / RT : blockIdx.x);
   const long long end = cur + per < total ? cur + per : total;
@@ -971,13 +1090,13 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_
     }
   if (cur >= end) return;  // (CTAs left over where RT does not divide the grid, too)
   long long base;  // places before sequence u.b
-  u.b = seq_of<KIND>(a, cur, units, lane, base);
+  u.b = seq_of<KIND, SCORED>(a, cur, units, lane, base);
   u.t_first = 0;
   u.rows = a.T * a.G;
   u.sel = nullptr;
   while (cur < end) {
     u.n = seq_len(a, u.b, over);
-    const int nt = (u.n + KT - 1) / KT;  // tiles of a unit of this sequence
+    const int nt = unit_tiles<KIND, SCORED>(a, u.n);  // tiles of a unit of this sequence
     const int places = unit_places<KIND>(nt);
     if (nt == 0 || cur >= base + (long long)places * units) {  // on to the next sequence
       base += (long long)places * units;
@@ -997,7 +1116,8 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_
     QueryWords q;
     fetch_q(a, u, lane, q);
     reset(s);
-    run_tiles<KIND, U, NP, W, false>(a, u, q, blk, i0, i1, ring, scratch, warp, lane, s);
+    const int t0 = first_tile<KIND, SCORED>(a, u.n);
+    run_tiles<KIND, U, NP, W, false, SCORED>(a, u, q, blk, t0 + i0, t0 + i1, ring, scratch, warp, lane, s);
     if ((threadIdx.x == 0 && over) || (lane == 0 && s.bad)) set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
     merge_warps<KIND, W>(s, mo, ml, warp, lane);
     if (threadIdx.x < 256) {
@@ -1028,7 +1148,7 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_
 // The kernel starts while the one before it runs, and reads the lengths, which that one only
 // reads too; the partial results after the wait, which every CTA passes (a grid that ended
 // without it would let the next kernel of the stream overtake the one before).
-template <int KIND, bool FEW>
+template <int KIND, bool FEW, bool SCORED>
 __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, int grid) {
   constexpr int KT = Cfg<KIND>::KT;
   constexpr int kRows = FEW ? 1 : 4, kGroups = 16 / kRows;
@@ -1041,7 +1161,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, in
   const int RT = (a.T * a.G + 15) / 16, side = kSide ? RT : 1;
   const int runs = kSide ? grid / RT : grid, units = kSide ? a.cache.Hkv : a.cache.Hkv * RT;
   const int row = (int)(blockIdx.x % (16 / kRows)) * kRows + rq;
-  const long long total = places_before<KIND>(a, a.cache.B, units, lane);
+  const long long total = places_before<KIND, SCORED>(a, a.cache.B, units, lane);
   const long long per = run_length(total, runs);
   Unit u;
   int c0, c1 = 0;  // the runs that hold its tiles
@@ -1062,8 +1182,8 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, in
     set_unit(un);
     bool over;
     u.n = seq_len(a, u.b, over);
-    const int nt = (u.n + KT - 1) / KT;
-    const long long w0 = places_before<KIND>(a, u.b, units, lane) + (long long)un * unit_places<KIND>(nt);
+    const int nt = unit_tiles<KIND, SCORED>(a, u.n);
+    const long long w0 = places_before<KIND, SCORED>(a, u.b, units, lane) + (long long)un * unit_places<KIND>(nt);
     c0 = (int)(w0 / per);
     c1 = (int)((w0 + nt - 1) / per);
     cut = nt != 0 && c0 != c1;
@@ -1075,7 +1195,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, in
     cut = end < total;
     if (cut) {
       long long base;
-      u.b = seq_of<KIND>(a, end - 1, units, lane, base);
+      u.b = seq_of<KIND, SCORED>(a, end - 1, units, lane, base);
       bool over;
       u.n = seq_len(a, u.b, over);
       const int nt = (u.n + KT - 1) / KT, places = unit_places<KIND>(nt);
@@ -1131,9 +1251,9 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, in
   write_out(a, u, row, quad, acc, l);
 }
 
-template <int KIND, int U, int NP, int W>
+template <int KIND, int U, int NP, int W, bool SCORED>
 static cudaError_t launch_direct(const CacheAttendLaunch& L, unsigned units, cudaStream_t s) {
-  return launch_early<cache_attend_direct_kernel<KIND, U, NP, W>>(units, W * 32, attend_smem<KIND, W>(), s, L);
+  return launch_early<cache_attend_direct_kernel<KIND, U, NP, W, SCORED>>(units, W * 32, attend_smem<KIND, W>(), s, L);
 }
 
 // Whether the direct form takes whole caches of up to `cap` tokens.  It saves the second kernel and
@@ -1147,39 +1267,40 @@ inline bool takes_direct(long long cap, long long units) {
   return cap <= (most > 2048 ? most : 2048);
 }
 
-template <int KIND, int U, int NP>
+template <int KIND, int U, int NP, bool SCORED>
 static cudaError_t launch_attend(const CacheAttendLaunch& L, cudaStream_t s) {
   using C = Cfg<KIND>;
   const int RT = (L.T * L.G + 15) / 16;
-  const long long cap = (long long)L.cache.max_pages << L.cache.page_shift;
+  long long cap = (long long)L.cache.max_pages << L.cache.page_shift;
+  if (SCORED && cap > L.score.window + L.T) cap = L.score.window + L.T;  // (what a unit sees at most)
   const long long units = (long long)L.cache.B * L.cache.Hkv * (L.idx ? L.T : RT);
   if (L.idx || takes_direct(cap, units)) {
     // The more units there are, the fewer warps share one out, so that all CTAs run at once
     // (128 x 2 units of 32 blocks: six warps 15.1 us, four 18.7, twelve 19.1).
-    if (units <= kCaGrid) return launch_direct<KIND, U, NP, C::kWarps>(L, (unsigned)units, s);
-    if (units <= 2 * kCaGrid) return launch_direct<KIND, U, NP, C::kHalf>(L, (unsigned)units, s);
-    return launch_direct<KIND, U, NP, C::kThird>(L, (unsigned)units, s);
+    if (units <= kCaGrid) return launch_direct<KIND, U, NP, C::kWarps, SCORED>(L, (unsigned)units, s);
+    if (units <= 2 * kCaGrid) return launch_direct<KIND, U, NP, C::kHalf, SCORED>(L, (unsigned)units, s);
+    return launch_direct<KIND, U, NP, C::kThird, SCORED>(L, (unsigned)units, s);
   }
-  cudaError_t e = launch_early<cache_attend_split_kernel<KIND, U, NP>>(kCaGrid, C::kWarps * 32,
+  cudaError_t e = launch_early<cache_attend_split_kernel<KIND, U, NP, SCORED>>(kCaGrid, C::kWarps * 32,
                                                                        attend_smem<KIND, C::kWarps>(), s, L);
   if (e != cudaSuccess) return e;
   if (units <= kCaGrid / 4)
-    return launch_early<cache_join_kernel<KIND, true>>((unsigned)units * 16, 256, 0, s, L, kCaGrid);
-  return launch_early<cache_join_kernel<KIND, false>>(kCaGrid * 4, 256, 0, s, L, kCaGrid);
+    return launch_early<cache_join_kernel<KIND, true, SCORED>>((unsigned)units * 16, 256, 0, s, L, kCaGrid);
+  return launch_early<cache_join_kernel<KIND, false, SCORED>>(kCaGrid * 4, 256, 0, s, L, kCaGrid);
 }
 
-template <int KIND, int U>
+template <int KIND, int U, bool SCORED>
 static cudaError_t launch_attend_u(const CacheAttendLaunch& L, cudaStream_t s) {
   constexpr int NP = KIND == PISA_CACHE_BF16 ? 2 : 1;  // parts of the weights (see weigh)
-  return L.out_f32 ? launch_attend<KIND, U, NP + 1>(L, s) : launch_attend<KIND, U, NP>(L, s);
+  return L.out_f32 ? launch_attend<KIND, U, NP + 1, SCORED>(L, s) : launch_attend<KIND, U, NP, SCORED>(L, s);
 }
 
-template <int KIND>
+template <int KIND, bool SCORED>
 static cudaError_t launch_attend_k(const CacheAttendLaunch& L, cudaStream_t s) {
   switch (L.cache.rec_shift) {
-    case 4: return launch_attend_u<KIND, 16>(L, s);
-    case 5: return launch_attend_u<KIND, 32>(L, s);
-    default: return launch_attend_u<KIND, 64>(L, s);
+    case 4: return launch_attend_u<KIND, 16, SCORED>(L, s);
+    case 5: return launch_attend_u<KIND, 32, SCORED>(L, s);
+    default: return launch_attend_u<KIND, 64, SCORED>(L, s);
   }
 }
 

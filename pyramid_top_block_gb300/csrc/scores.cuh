@@ -1,0 +1,64 @@
+// scores.cuh -- scores that are not plain products: capped by a tanh, with a bias by distance.
+//
+//   x = q . k / 8;  cap > 0: x = cap tanh(x / cap);  x -= slope |p - j|  (p the query's position, j the key's)
+// In base 2, as the softmax takes them.
+#pragma once
+
+#include "tc.cuh"
+
+namespace pisa {
+
+constexpr int kNoWindow = 1 << 28;  // past every position (tokens are below 2^27)
+
+// What is done to the scores of a call (cap 0: not capped; slopes nullptr: no bias; window kNoWindow: none).
+struct ScoreDev {
+  float cap, inv_cap;
+  const float* slopes;  // [Hq]
+  int window;           // a query sees tokens p - window + 1 and later
+};
+
+// tanh(y) / y as a polynomial in u = y y on 0 .. 1: the interpolation at the Chebyshev nodes of degree 6, off by
+// at most 6.0e-8 of the value (a rounding to 32 bits).  It costs 7 multiply-adds for two scores together and no
+// exponential, where 1 - 2 / (1 + e^(2 y)) takes two slow instructions each and loses small scores' last bits.
+struct Tanh {
+  float c[7] = {0x1.fffffep-1f, -0x1.555402p-2f, 0x1.10e5c6p-3f, -0x1.b5e03ap-5f,
+                0x1.4c4342p-6f, -0x1.95f386p-8f, 0x1.101cb0p-10f};
+};
+
+__device__ __forceinline__ unsigned long long f2_mul(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Factors of a row: y = score * to_y (to the cap's units), logit = score * to_l tanh(y) / y.
+struct CapRow {
+  float to_y, to_l;
+};
+
+// Two scores with |y| <= 1, capped.
+__device__ __forceinline__ void cap_small(float& a, float& b, const CapRow& r) {
+  const unsigned long long x = f2_pack(a, b), y = f2_mul(x, f2_pack(r.to_y, r.to_y)), u = f2_mul(y, y);
+  constexpr Tanh k;
+  unsigned long long q = f2_pack(k.c[6], k.c[6]);
+#pragma unroll
+  for (int i = 5; i >= 0; --i) q = f2_fma(q, u, f2_pack(k.c[i], k.c[i]));
+  f2_unpack(f2_mul(f2_mul(x, f2_pack(r.to_l, r.to_l)), q), a, b);
+}
+
+// One score of any size, capped; top = cap log2 e.  An infinity gives plus or minus top, a NaN a NaN.
+__device__ __forceinline__ float cap_any(float x, const CapRow& r, float top) {
+  const float y = fabsf(x * r.to_y);
+  if (!(y <= 1.f)) {
+    const float e = ex2_approx(-2.f * 1.4426950408889634f * y);  // tanh y = (1 - e) / (1 + e)
+    return copysignf(top, x) * __fdividef(1.f - e, 1.f + e);
+  }
+  const float u = y * y;
+  constexpr Tanh k;
+  float q = k.c[6];
+#pragma unroll
+  for (int i = 5; i >= 0; --i) q = fmaf(q, u, k.c[i]);
+  return x * r.to_l * q;
+}
+
+}  // namespace pisa
