@@ -252,7 +252,7 @@ int pisa_cache_prompt_attention(const pisa_paged_cache* cache, const pisa_rows* 
     return PISA_ERR_INVALID_ARG;
   if (!group_ok(Hq, cache->Hkv)) return PISA_ERR_UNSUPPORTED;
   // 32-bit numbers of rows and of row tiles
-  if (T > (1 << 27) || (long long)cache->B * T * cache->Hkv >= (1LL << 30)) return PISA_ERR_UNSUPPORTED;
+  if (T > (1 << 27) || (long long)cache->B * T * Hq >= (1LL << 30)) return PISA_ERR_UNSUPPORTED;
   if (ws_bytes < pisa_cache_workspace_bytes()) return PISA_ERR_WORKSPACE_TOO_SMALL;
   L.T = T;
   L.Hq = Hq;
