@@ -5,20 +5,23 @@
 //
 // Rows are (token, head) pairs of one KV head, heads fastest, so that a head group shares its keys.  A CTA takes
 // 256 rows, two tiles of 128, over tiles of 128 keys: S = Q K^T (tcgen05, operands from shared memory) -> registers,
-// a row a thread -> weights, back to tensor memory as the left operand of O += P V.  While one row tile's weights are
-// computed the tensor core works for the other; keys and values are read from L2 once for both.
-//   warps 0 .. 7   softmax, four for each row tile
-//   warps 8 .. 11  pages -> shared memory (bf16: asynchronous copies; 4 bits: through registers, as fp16)
-//   warp 12        issues the matrix instructions
+// two threads a row -> weights, back to tensor memory as the left operand of O += P V.  While one row tile's weights
+// are computed the tensor core works for the other; keys and values are read from L2 once for both.
+//   warps 0 .. 15   softmax, eight for each row tile: four for its first 64 columns, four for the others
+//   warps 16, 17    pages -> shared memory, every second tile each (bf16: by TMA; 4 bits: through registers, as fp16)
+//   warps 18, 19    issue the matrix instructions, one for each row tile
 // Tensor memory, for each row tile: S 128 columns, P 64, O 64; both together all 512.
 #include "cache_prompt.cuh"
 
 #include <climits>
+#include <mutex>
+
+#include <cudaTypedefs.h>
 
 namespace pisa {
 
 constexpr int kRowsTile = 128, kRowsCta = 256, kKeys = 128;
-constexpr int kSoftWarps = 8, kLoadWarps = 4, kPromptThreads = (kSoftWarps + kLoadWarps + 1) * 32;
+constexpr int kSoftWarps = 16, kLoadWarps = 2, kPromptThreads = (kSoftWarps + kLoadWarps + 2) * 32;
 constexpr int kPStages = 5;
 constexpr int kTileBytes = kKeys * kD * 2;  // keys or values of a tile: rows of 128 bytes, 128-byte swizzle
 constexpr int kPromptSmem = 2 * kTileBytes + kPStages * 2 * kTileBytes + 1024;
@@ -48,16 +51,13 @@ __device__ __forceinline__ uint64_t umma_desc_mn128(uint32_t addr) {
 
 struct PromptShared {
   uint64_t full[kPStages], empty[kPStages];
-  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], drain;
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], drain[2], landed[kLoadWarps];
   uint32_t tmem;
   int abort, odd, bad;
   int lo_min, lo_max, hi_min, hi_max;  // of the rows that see anything
   float factor[kRowsCta];              // 4-bit pages: the rows' logit factors
+  float half[2][kRowsCta];             // what the two threads of a row tell each other
 };
-
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
 
 // What of a CTA's rows a warp needs to know.
 struct PromptUnit {
@@ -71,36 +71,26 @@ struct PromptUnit {
 
 // ------------------------------------------------------------------------------------------------ loading
 
-// Where the 16-key pieces of a warp's 32 keys lie, for 16 tiles ahead: lane l has piece l & 1 of tile first + l / 2.
-// -1: no row sees any of it, or its page is out of range (noted); its keys and values become zeros.
-struct Pieces {
-  long long off;
-  int first;
-};
-
-template <int KIND>
-__device__ __forceinline__ void look(const CachePromptLaunch& a, const PromptUnit& u, PromptShared& sh, int warp, int lane,
-                                     int tile, Pieces& p) {
-  p.first = tile;
-  p.off = -1;
-  const int key = (tile + (lane >> 1)) * kKeys + 32 * warp + 16 * (lane & 1);
-  if (tile + (lane >> 1) < u.i1 && key < sh.hi_max && key + 16 > sh.lo_min) {
-    const int page = a.cache.table[(long long)u.b * a.cache.max_pages + (key >> a.cache.page_shift)];
-    if (page >= 0 && page < a.cache.n_pages)
-      p.off = cache_record(a.cache, KIND == PISA_CACHE_BF16 ? kRowBf16 : kRowE2m1, page, u.kv, key);
-    else
-      sh.bad = 1;
-  }
+// A loading warp takes every second tile, whole.  The pages of its tiles' records, four tiles ahead: lane l has record l % 8
+// (of 8, 4 or 2) of tile first + 2 (l / 8).  n_pages: no row sees any of it, or its page is out of range (noted); its
+// keys and values become zeros.
+__device__ __forceinline__ int look(const CachePromptLaunch& a, const PromptUnit& u, PromptShared& sh, int lane, int first) {
+  const int tile = first + kLoadWarps * (lane >> 3), U = 1 << a.cache.rec_shift, key = tile * kKeys + U * (lane & 7);
+  if (U * (lane & 7) >= kKeys || tile >= u.i1 || key >= sh.hi_max || key + U <= sh.lo_min) return a.cache.n_pages;
+  const int page = a.cache.table[(long long)u.b * a.cache.max_pages + (key >> a.cache.page_shift)];
+  if (page >= 0 && page < a.cache.n_pages) return page;
+  sh.bad = 1;
+  return a.cache.n_pages;
 }
 
-// A bf16 tile's values that this thread copied: those that are not finite become zeros, since 0 times them is
-// not zero; the rows that do see them get them at the end (odd_values).
-__device__ __forceinline__ void scrub(PromptShared& sh, unsigned char* v, int tile, int warp, int lane) {
+// A bf16 tile's values: those that are not finite become zeros, since 0 times them is not zero; the rows that do see them
+// get them at the end (odd_values).
+__device__ __forceinline__ void scrub(PromptShared& sh, unsigned char* v, int tile, int lane) {
   const int sub = lane >> 3, ch = lane & 7;
   bool odd = false;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int row = 32 * warp + 4 * j + sub;
+#pragma unroll 8
+  for (int j = 0; j < kKeys / 4; ++j) {
+    const int row = 4 * j + sub;
     uint4* at = reinterpret_cast<uint4*>(v + row * 128 + ((ch ^ (row & 7)) << 4));
     uint4 x = *at;
     uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -125,47 +115,6 @@ __device__ __forceinline__ void scrub(PromptShared& sh, unsigned char* v, int ti
   if (odd) sh.odd = 1;
 }
 
-// Tiles of bf16 pages: copied ahead by two tiles, then handed over.
-__device__ __forceinline__ bool load_bf16(const CachePromptLaunch& a, const PromptUnit& u, PromptShared& sh,
-                                          unsigned char* stages, unsigned kt, int warp, int lane) {
-  constexpr int kAhead = 2;
-  const int sub = lane >> 3, ch = lane & 7, U = 1 << a.cache.rec_shift, n = u.i1 - u.i0;
-  Pieces p;
-  bool ok = true;
-  for (int x = 0; x < n + kAhead && ok; ++x) {
-    if (x < n) {
-      const unsigned k = kt + x, st = k % kPStages;
-      if (k >= kPStages) ok = mbar_wait(&sh.empty[st], (k / kPStages - 1) & 1, &sh.abort);
-      ok = __all_sync(kFull, ok);
-      if (!ok) break;
-      const int tile = u.i0 + x;
-      if (x % 16 == 0) look<PISA_CACHE_BF16>(a, u, sh, warp, lane, tile, p);
-      const uint32_t base = smem_u32(stages) + st * 2 * kTileBytes;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int key = 4 * j + sub, row = 32 * warp + key;  // (of the tile)
-        const long long off = __shfl_sync(kFull, p.off, ((x % 16) << 1) | (j >> 2));
-        const int in = (tile * kKeys + row) & (U - 1);  // row of its record
-        const unsigned char* src = a.cache.pages + (off < 0 ? 0 : off + in * 128 + ch * 16);
-        const uint32_t dst = base + row * 128 + ((ch ^ (row & 7)) << 4);
-        cp16(dst, src, off >= 0);
-        cp16(dst + kTileBytes, off < 0 ? src : src + U * 128, off >= 0);
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    if (x >= kAhead) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
-      const unsigned st = (kt + x - kAhead) % kPStages;
-      const int tile = u.i0 + x - kAhead;
-      if (u.mixed(sh, tile)) scrub(sh, stages + st * 2 * kTileBytes + kTileBytes, tile, warp, lane);
-      fence_async_proxy();
-      mbar_arrive(&sh.full[st]);
-    }
-  }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  return ok;
-}
-
 // 16 dims of a token: 8 bytes of codes and a scale, as 16 fp16.
 __device__ __forceinline__ void dequant16(uint32_t c0, uint32_t c1, uint32_t scale, uint4& x, uint4& y) {
   const uint32_t s2 = e4m3x2(scale | scale << 8);
@@ -176,117 +125,148 @@ __device__ __forceinline__ void dequant16(uint32_t c0, uint32_t c1, uint32_t sca
   y = make_uint4(hmul2u(d[0], s2), hmul2u(d[1], s2), hmul2u(d[2], s2), hmul2u(d[3], s2));
 }
 
-// Tiles of 4-bit pages: a token a thread, the next tile's words on their way meanwhile.
-__device__ __forceinline__ bool load_e2m1(const CachePromptLaunch& a, const PromptUnit& u, PromptShared& sh,
-                                          unsigned char* stages, unsigned kt, int warp, int lane) {
-  const int U = 1 << a.cache.rec_shift, n = u.i1 - u.i0, row = 32 * warp + lane;
-  Pieces p;
+// A token's codes and scales.
+struct Codes {
   uint4 k0, k1, v0, v1;
   uint32_t ks, vs;
-  auto fetch = [&](int x) {
-    if (x % 16 == 0) look<PISA_CACHE_E2M1>(a, u, sh, warp, lane, u.i0 + x, p);
-    const long long off = __shfl_sync(kFull, p.off, ((x % 16) << 1) | (lane >> 4));
-    k0 = k1 = v0 = v1 = make_uint4(0, 0, 0, 0);
-    ks = vs = 0;
-    if (off >= 0) {
-      const int in = ((u.i0 + x) * kKeys + row) & (U - 1);
-      const unsigned char* r = a.cache.pages + off;
-      const uint4* kc = reinterpret_cast<const uint4*>(r + in * 32);
-      const uint4* vc = reinterpret_cast<const uint4*>(r + 36 * U + in * 32);
-      k0 = kc[0];
-      k1 = kc[1];
-      ks = *reinterpret_cast<const uint32_t*>(r + 32 * U + in * 4);
-      v0 = vc[0];
-      v1 = vc[1];
-      vs = *reinterpret_cast<const uint32_t*>(r + 68 * U + in * 4);
-    }
-  };
+};
+
+template <int KIND>
+__device__ __forceinline__ bool load_tiles(const CachePromptLaunch& a, const CUtensorMap* map, const PromptUnit& u,
+                                           PromptShared& sh, unsigned char* stages, int warp, int lane,
+                                           unsigned& next) {
+  const int rs = a.cache.rec_shift, U = 1 << rs;
   bool ok = true;
-  fetch(0);
-  for (int x = 0; x < n; ++x) {
-    const unsigned k = kt + x, st = k % kPStages;
+  int page = 0, mine = 0;
+  unsigned landings = 0;
+  for (int tile = u.i0 + warp; tile < u.i1; tile += kLoadWarps, ++mine) {
+    const unsigned k = tile - u.i0, st = k % kPStages;
+    if (mine % 4 == 0) page = look(a, u, sh, lane, tile);
     if (k >= kPStages) ok = mbar_wait(&sh.empty[st], (k / kPStages - 1) & 1, &sh.abort);
     ok = __all_sync(kFull, ok);
     if (!ok) break;
-    const int tile = u.i0 + x;
-    if (u.mixed(sh, tile)) {  // NaN blocks of values that not all rows see become zeros (see scrub)
-      uint32_t keep = 0xffffffffu;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if ((vs >> (8 * i) & 0x7fu) == 0x7fu) keep &= ~(0xffu << (8 * i));
-      if (keep != 0xffffffffu) {
-        vs &= keep;
-        const int key = tile * kKeys + row;
-        if (key >= sh.lo_min && key < sh.hi_max) sh.odd = 1;
+    unsigned char* stage = stages + st * 2 * kTileBytes;
+    const int piece0 = (mine % 4) * 8;
+    const bool mixed = u.mixed(sh, tile);
+    if constexpr (KIND == PISA_CACHE_BF16) {
+      // lane 2 i + h: the keys (h = 0) or values of record i; a page number of n_pages lies outside the map and gives zeros
+      uint64_t* bar = mixed ? &sh.landed[warp] : &sh.full[st];
+      if (lane == 0) mbar_expect_tx(bar, 2 * kTileBytes);
+      __syncwarp();
+      const int i = lane >> 1, h = lane & 1, from = __shfl_sync(kFull, page, (piece0 | i) & 31);
+      if (i < kKeys >> rs) {
+        const int key = tile * kKeys + (i << rs), rec = (key & ((1 << a.cache.page_shift) - 1)) >> rs;
+        tma_load_4d(stage + h * kTileBytes + (i << rs) * 128, map, 0, 0,
+                    (((u.kv << (a.cache.page_shift - rs)) + rec) << 1) + h, from, bar);
       }
+      if (mixed) {
+        ok = __all_sync(kFull, mbar_wait(bar, landings & 1, &sh.abort));
+        if (!ok) {  // (given up; the copies land first)
+          mbar_wait(bar, landings & 1, nullptr);
+          break;
+        }
+        ++landings;
+        scrub(sh, stage + kTileBytes, tile, lane);
+        fence_async_proxy();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.full[st]);
+      }
+      next = k + 1;
+    } else {
+      // a token a lane, four turns; the words of the next turn but one are on their way meanwhile
+      Codes c[3];
+      auto fetch = [&](int j, Codes& c) {
+        const int from = __shfl_sync(kFull, page, piece0 | ((32 * j + lane) >> rs));
+        c.k0 = c.k1 = c.v0 = c.v1 = make_uint4(0, 0, 0, 0);
+        c.ks = c.vs = 0;
+        if (from < a.cache.n_pages) {
+          const int key = tile * kKeys + 32 * j + lane, in = key & (U - 1);
+          const unsigned char* r = a.cache.pages + cache_record(a.cache, kRowE2m1, from, u.kv, key);
+          const uint4* kc = reinterpret_cast<const uint4*>(r + in * 32);
+          const uint4* vc = reinterpret_cast<const uint4*>(r + 36 * U + in * 32);
+          c.k0 = kc[0];
+          c.k1 = kc[1];
+          c.ks = *reinterpret_cast<const uint32_t*>(r + 32 * U + in * 4);
+          c.v0 = vc[0];
+          c.v1 = vc[1];
+          c.vs = *reinterpret_cast<const uint32_t*>(r + 68 * U + in * 4);
+        }
+      };
+      fetch(0, c[0]);
+      fetch(1, c[1]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j + 2 < 4) fetch(j + 2, c[(j + 2) % 3]);
+        const Codes& x = c[j % 3];
+        const int row = 32 * j + lane;
+        uint32_t vs = x.vs;
+        if (mixed) {  // NaN blocks of values that not all rows see become zeros (see scrub)
+          uint32_t keep = 0xffffffffu;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if ((vs >> (8 * i) & 0x7fu) == 0x7fu) keep &= ~(0xffu << (8 * i));
+          if (keep != 0xffffffffu) {
+            vs &= keep;
+            const int key = tile * kKeys + row;
+            if (key >= sh.lo_min && key < sh.hi_max) sh.odd = 1;
+          }
+        }
+        const uint32_t w[2][8] = {{x.k0.x, x.k0.y, x.k0.z, x.k0.w, x.k1.x, x.k1.y, x.k1.z, x.k1.w},
+                                  {x.v0.x, x.v0.y, x.v0.z, x.v0.w, x.v1.x, x.v1.y, x.v1.z, x.v1.w}};
+        const uint32_t sc[2] = {x.ks, vs};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint4 y, z;
+            dequant16(w[h][2 * i], w[h][2 * i + 1], sc[h] >> (8 * i) & 0xffu, y, z);
+            unsigned char* at = stage + h * kTileBytes + row * 128;
+            *reinterpret_cast<uint4*>(at + (((2 * i) ^ (row & 7)) << 4)) = y;
+            *reinterpret_cast<uint4*>(at + (((2 * i + 1) ^ (row & 7)) << 4)) = z;
+          }
+      }
+      fence_async_proxy();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.full[st]);
     }
-    unsigned char* kd = stages + st * 2 * kTileBytes + row * 128;
-    const uint32_t w[2][8] = {{k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w},
-                              {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w}};
-    const uint32_t sc[2] = {ks, vs};
-    uint4 y[2][8];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) dequant16(w[h][2 * i], w[h][2 * i + 1], sc[h] >> (8 * i) & 0xffu, y[h][2 * i], y[h][2 * i + 1]);
-    if (x + 1 < n) fetch(x + 1);
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(kd + h * kTileBytes + ((i ^ (row & 7)) << 4)) = y[h][i];
-    fence_async_proxy();
-    mbar_arrive(&sh.full[st]);
   }
   return ok;
 }
 
-// ------------------------------------------------------------------------------------------------ the MMA warp
+// ------------------------------------------------------------------------------------------------ the MMA warps
 
+// The products of row tile X, issued by one thread.  The next tile's S comes before the last one's P V, so that it is there
+// when the softmax is done with the last one.
 template <int KIND>
 __device__ __forceinline__ bool multiply(const PromptUnit& u, PromptShared& sh, const unsigned char* q,
-                                         const unsigned char* stages, unsigned kt, int lane, bool& issued) {
-  const int n = u.i1 - u.i0;
-  const uint32_t tmem = sh.tmem;
-  bool ok = true;
-  for (int x = 0; x <= n && ok; ++x) {
-    const unsigned k = kt + x, st = k % kPStages, before = (k - 1) % kPStages;
-    if (x < n) ok = mbar_wait(&sh.full[st], (k / kPStages) & 1, &sh.abort);
+                                         const unsigned char* stages, int X) {
+  const unsigned n = u.i1 - u.i0;
+  const uint32_t t = sh.tmem + 256 * X;
+  const uint64_t dq = umma_desc_sw128(q + X * kTileBytes);
+  for (unsigned k = 0; k <= n; ++k) {
+    const unsigned st = k % kPStages, before = (k + kPStages - 1) % kPStages;
+    if (k < n) {  // S = Q K^T
+      if (k > 0 && !mbar_wait(&sh.s_free[X], (k - 1) & 1, &sh.abort)) return false;
+      if (!mbar_wait(&sh.full[st], (k / kPStages) & 1, &sh.abort)) return false;
+      tc_fence_after();
+      const uint64_t db = umma_desc_sw128(stages + st * 2 * kTileBytes);
 #pragma unroll
-    for (int X = 0; X < 2; ++X) {
-      if (x < n) {  // S = Q K^T
-        if (k > 0) ok = ok && mbar_wait(&sh.s_free[X], (k - 1) & 1, &sh.abort);
-        ok = __all_sync(kFull, ok);
-        if (!ok) break;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint64_t da = umma_desc_sw128(q + X * kTileBytes);
-          const uint64_t db = umma_desc_sw128(stages + st * 2 * kTileBytes);
+      for (int i = 0; i < 4; ++i)  // (16 dims are 32 bytes, 2 in the descriptor's units)
+        umma_ss(t, dq + 2 * i, db + 2 * i, PCfg<KIND>::kIdescS, i);
+      umma_commit(&sh.s_full[X]);
+    }
+    if (k > 0) {  // O += P V of the tile before
+      if (!mbar_wait(&sh.p_full[X], (k - 1) & 1, &sh.abort)) return false;
+      tc_fence_after();
+      const uint64_t db = umma_desc_mn128(smem_u32(stages + before * 2 * kTileBytes + kTileBytes));
 #pragma unroll
-          for (int i = 0; i < 4; ++i)  // (16 dims are 32 bytes, 2 in the descriptor's units)
-            umma_ss(tmem + 256 * X, da + 2 * i, db + 2 * i, PCfg<KIND>::kIdescS, i);
-          umma_commit(&sh.s_full[X]);
-        }
-        issued = true;
-        __syncwarp();
-      }
-      if (x > 0) {  // O += P V of the tile before
-        ok = __all_sync(kFull, mbar_wait(&sh.p_full[X], (k - 1) & 1, &sh.abort));
-        if (!ok) break;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint64_t db = umma_desc_mn128(smem_u32(stages + before * 2 * kTileBytes + kTileBytes));
-#pragma unroll
-          for (int i = 0; i < 8; ++i)  // (16 keys are 2048 bytes of V and 8 columns of P)
-            umma_ts(tmem + 256 * X + 192, tmem + 256 * X + 128 + 8 * i, db + 128 * i, PCfg<KIND>::kIdescO,
-                    x > 1 || i > 0);
-          umma_commit(&sh.pv_done[X]);
-          if (X == 1) umma_commit(&sh.empty[before]);
-        }
-        __syncwarp();
-      }
+      for (int i = 0; i < 8; ++i)  // (16 keys are 2048 bytes of V and 8 columns of P)
+        umma_ts(t + 192, t + 128 + 8 * i, db + 128 * i, PCfg<KIND>::kIdescO, k > 1 || i > 0);
+      umma_commit(&sh.pv_done[X]);
+      umma_commit(&sh.empty[before]);
     }
   }
-  return ok;
+  return true;
 }
 
 // ------------------------------------------------------------------------------------------------ softmax
@@ -307,7 +287,8 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
   return d;
 }
 
-// 64 products of a row, of the keys from key0 on, as the logits that the softmax takes with factor ff.
+// 64 products of a row, of the keys from key0 on, as the logits that the softmax takes (times r.f if not SCORED and not
+// two_step).
 template <bool SCORED>
 __device__ __forceinline__ void logits(const CachePromptLaunch& a, const PromptRow& r, int key0, bool whole, bool two_step,
                                        float (&v)[64]) {
@@ -361,105 +342,102 @@ __device__ __forceinline__ void load64(uint32_t taddr, float (&v)[64]) {
   for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(w[i]);
 }
 
-// The softmax of one key tile for the warp's 32 rows.  s: the S columns of the warp's lanes.
+// Whether a predicate holds for any thread of the two warps that share 32 rows (named barrier id).
+__device__ __forceinline__ bool any_of_two(int id, bool x) {
+  int r;
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.b32 p, %1, 0; barrier.cta.red.or.pred q, %2, 64, p; selp.b32 %0, 1, 0, q; }"
+      : "=r"(r)
+      : "r"((int)x), "r"(id)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void sync_two(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
+
+// The softmax of one key tile, half of its columns, for the warp's 32 rows.  s: the tensor memory columns of the row tile at
+// the warp's lanes.
 template <int KIND, bool SCORED>
-__device__ __forceinline__ bool soften(const CachePromptLaunch& a, PromptShared& sh, PromptRow& r, uint32_t s, int X,
-                                       int lane, int tile, unsigned k, bool first, bool& two_step) {
+__device__ __forceinline__ void soften(const CachePromptLaunch& a, PromptShared& sh, PromptRow& r, uint32_t s, int X,
+                                       int half, int row, int id, int lane, int tile, unsigned k, bool& two_step,
+                                       bool& ok) {
   using C = PCfg<KIND>;
-  const int key0 = tile * kKeys;
+  const int key0 = tile * kKeys + 64 * half;
   // (rows that see nothing do not matter: they get zeros at the end, or do not exist)
-  const bool whole = __all_sync(kFull, r.lo >= r.hi || (r.lo <= key0 && r.hi >= key0 + kKeys));
-  bool ok = __all_sync(kFull, mbar_wait(&sh.s_full[X], k & 1, &sh.abort));
-  if (!ok) return false;
-  tc_fence_after();
+  const bool whole = __all_sync(kFull, r.lo >= r.hi || (r.lo <= key0 && r.hi >= key0 + 64));
+  // (a warp whose wait ran out goes on without waiting, so that its partner is not left at a barrier of both)
+  const auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (ok) ok = __all_sync(kFull, mbar_wait(bar, parity, &sh.abort));
+    tc_fence_after();
+  };
+  wait(&sh.s_full[X], k & 1);
+  float v[64];
+  load64(s + 64 * half, v);
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&sh.s_free[X]);  // S is in registers: the next product may overwrite it
+  logits<SCORED>(a, r, key0, whole, two_step, v);
   bool waited = k == 0;  // for the product before, which reads P and writes O
-  const auto wait_pv = [&] {
-    if (!waited) {
-      ok = __all_sync(kFull, mbar_wait(&sh.pv_done[X], (k - 1) & 1, &sh.abort));
-      tc_fence_after();
+  float ff = SCORED || two_step ? 1.f : r.f;
+  float b = __fmul_rn(max64(v), ff);
+  // A row's reference m is set anew only when a logit passes it by more than kTop, so that few tiles rescale O.
+  if (any_of_two(id, b > r.m + C::kTop)) {
+    sh.half[half][row] = b;
+    sync_two(id);
+    b = fmaxf(b, sh.half[half ^ 1][row]);
+    sync_two(id);  // (both have read before either writes again)
+    // (a step of 32 bits is too coarse for the shift from 2^24 on; nothing that it is for is left there)
+    const float n = fmaxf(r.m, fabsf(b) < 16.f * kFar ? b - C::kShift : b);
+    const float f = ex2_approx(r.m - n);
+    if (k > 0) {
+      wait(&sh.pv_done[X], (k - 1) & 1);
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {  // this half of O's columns
+        uint32_t o[16];
+        tmem_ld16_now(s + 192 + 32 * half + 16 * c, o);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+        tmem_st16(s + 192 + 32 * half + 16 * c, o);
+      }
       waited = true;
     }
-    return ok;
-  };
-  const auto factor = [&] { return SCORED || two_step ? 1.f : r.f; };
-  bool scan = first;
-  float sum;
-  while (true) {
-    if (scan) {  // a new reference: the largest logit, less the shift
-      float b = -INFINITY;
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        float v[64];
-        load64(s + 64 * h, v);
-        logits<SCORED>(a, r, key0 + 64 * h, whole, two_step, v);
-        b = fmaxf(b, max64(v));
-      }
-      const float t = __fmul_rn(b, factor());
-      const float n = fmaxf(r.m, fabsf(t) < 16.f * kFar ? t - C::kShift : t);
-      const float f = ex2_approx(r.m - n);
-      r.m = n;
-      r.l *= f;
-      if (!SCORED) two_step = two_step || __any_sync(kFull, fabsf(n) >= kFar && n != kNone);
-      if (!first) {  // what O holds has the old reference
-        if (!wait_pv()) return false;
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint32_t o[32];
-          tmem_ld32_now(s + 192 + 32 * h, o);
+    r.m = n;
+    r.l *= f;
+    // Below, a logit less m is an exact product less a rounded one: 2^-24 of m, no error as all weights of the row have
+    // it, until it overflows a weight.  From kFar on the products are rounded first.
+    if (!SCORED && !two_step && __any_sync(kFull, fabsf(n) >= kFar && n != kNone)) {
+      two_step = true;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-          tmem_st32(s + 192 + 32 * h, o);
-        }
-        tmem_st_wait();
-      }
+      for (int i = 0; i < 64; ++i) v[i] = __fmul_rn(v[i], r.f);
+      ff = 1.f;
     }
-    sum = 0.f;
-    bool again = false;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float v[64];
-      load64(s + 64 * h, v);
-      logits<SCORED>(a, r, key0 + 64 * h, whole, two_step, v);
-      const float ff = factor();
-      if (!scan && __any_sync(kFull, max64(v) * ff > r.m + C::kTop)) {
-        again = true;
-        break;
-      }
-      if (h == 1) {  // S is in registers: the next product may overwrite it
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.s_free[X]);
-      }
-      const unsigned long long f2 = f2_pack(ff, ff), m2 = f2_pack(-r.m, -r.m);
-      unsigned long long s0 = 0, s1 = 0;
-      uint32_t w[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        float x, y;
-        f2_unpack(f2_fma(f2_pack(v[2 * i], v[2 * i + 1]), f2, m2), x, y);
-        x = ex2_approx(x);
-        y = ex2_approx(y);
-        if (i & 1)
-          s1 = f2_add(s1, f2_pack(x, y));
-        else
-          s0 = f2_add(s0, f2_pack(x, y));
-        w[i] = KIND == PISA_CACHE_BF16 ? pack_bf16x2(x, y) : pack_f16x2(x, y);
-      }
-      float x, y;
-      f2_unpack(f2_add(s0, s1), x, y);
-      sum += x + y;
-      if (!wait_pv()) return false;
-      tmem_st32(s + 128 + 32 * h, w);
-    }
-    if (!again) break;
-    scan = true;
   }
-  r.l += sum;
+  const unsigned long long f2 = f2_pack(ff, ff), m2 = f2_pack(-r.m, -r.m);
+  unsigned long long s0 = 0, s1 = 0;
+  uint32_t w[2][16];
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float x, y;
+      f2_unpack(f2_fma(f2_pack(v[32 * c + 2 * i], v[32 * c + 2 * i + 1]), f2, m2), x, y);
+      x = ex2_approx(x);
+      y = ex2_approx(y);
+      if (i & 1)
+        s1 = f2_add(s1, f2_pack(x, y));
+      else
+        s0 = f2_add(s0, f2_pack(x, y));
+      w[c][i] = KIND == PISA_CACHE_BF16 ? pack_bf16x2(x, y) : pack_f16x2(x, y);
+    }
+  if (!waited) wait(&sh.pv_done[X], (k - 1) & 1);
+  tmem_st16(s + 128 + 32 * half, w[0]);
+  tmem_st16(s + 128 + 32 * half + 16, w[1]);
+  float x, y;
+  f2_unpack(f2_add(s0, s1), x, y);
+  r.l += x + y;
   tmem_st_wait();
   tc_fence_before();
   __syncwarp();
   if (lane == 0) mbar_arrive(&sh.p_full[X]);
-  return true;
 }
 
 // Values that scrub took out, of tokens that this row sees, in dims d0 .. d0 + 31 (an infinity, or a NaN, whatever
@@ -531,8 +509,8 @@ __device__ __forceinline__ void stage_queries(const CachePromptLaunch& a, const 
                                               unsigned char* q, int count, int g_shift) {
   const int ch = threadIdx.x & 7;
 #pragma unroll 4
-  for (int it = 0; it < 8; ++it) {
-    const int row = it * 32 + (threadIdx.x >> 3), r = u.r0 + row, t = r >> g_shift;
+  for (int it = 0; it < 4; ++it) {
+    const int row = it * 64 + (threadIdx.x >> 3), r = u.r0 + row, t = r >> g_shift;
     uint4 x = make_uint4(0, 0, 0, 0);
     if (t < count) {
       const int head = u.kv * a.G + (r & (a.G - 1));
@@ -559,7 +537,8 @@ __device__ __forceinline__ void stage_queries(const CachePromptLaunch& a, const 
 }
 
 template <int KIND, bool SCORED>
-__global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(CachePromptLaunch a, int g_shift, int row_tiles) {
+__global__ void __launch_bounds__(kPromptThreads, 1)
+    cache_prompt_kernel(const __grid_constant__ CUtensorMap map, CachePromptLaunch a, int g_shift, int row_tiles) {
   extern __shared__ unsigned char prompt_smem[];
   __shared__ PromptShared sh;
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -567,16 +546,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(CachePr
   unsigned char* stages = q + 2 * kTileBytes;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kPStages; ++i) {
-      mbar_init(&sh.full[i], kLoadWarps * 32);
-      mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 2);
     }
     for (int X = 0; X < 2; ++X) {
       mbar_init(&sh.s_full[X], 1);
-      mbar_init(&sh.s_free[X], 4);
-      mbar_init(&sh.p_full[X], 4);
+      mbar_init(&sh.s_free[X], 8);
+      mbar_init(&sh.p_full[X], 8);
       mbar_init(&sh.pv_done[X], 1);
+      mbar_init(&sh.drain[X], 1);
     }
-    mbar_init(&sh.drain, 1);
+    for (int i = 0; i < kLoadWarps; ++i) mbar_init(&sh.landed[i], 1);
     mbar_fence_init();
     sh.abort = sh.odd = sh.bad = 0;
     sh.lo_min = sh.hi_min = INT_MAX;
@@ -592,8 +572,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(CachePr
   u.r0 = (row_tiles - 1 - (int)(blockIdx.x / heads)) * kRowsCta;
   const int count = prompt_count(a, u.b);
   PromptRow r{};
+  // softmax warps: row tile X, lanes 32 quad .., half of the columns; row_of: the thread's row of the CTA's 256
+  const int X = (warp >> 3) & 1, half = (warp >> 2) & 1, quad = warp & 3, row_of = X * kRowsTile + quad * 32 + lane;
   if (warp < kSoftWarps) {
-    const int row = u.r0 + threadIdx.x;
+    const int row = u.r0 + row_of;
     r.t = row >> g_shift;
     r.head = u.kv * a.G + (row & (a.G - 1));
     r.there = r.t < count;
@@ -625,12 +607,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(CachePr
   tc_fence_after();
   u.i0 = sh.lo_min < sh.hi_max ? sh.lo_min / kKeys : 0;
   u.i1 = sh.lo_min < sh.hi_max ? (sh.hi_max + kKeys - 1) / kKeys : 0;
-  const unsigned kt = 0;
-  bool ok = true, issued = false;
+  bool ok = true;
+  unsigned next = 0;  // one past the last tile that this loading warp has asked for
+  const int n = u.i1 - u.i0;
   if (warp < kSoftWarps) {
-    const int X = warp >> 2, n = u.i1 - u.i0;
-    const uint32_t s = sh.tmem + 256 * X + ((uint32_t)(warp & 3) << 21);  // (lanes 32 (warp & 3) .. of the tile's columns)
-    r.f = KIND == PISA_CACHE_E2M1 ? sh.factor[threadIdx.x] : SCORED ? kScale : kScale * kLog2e;
+    const int id = 1 + X * 4 + quad;
+    const uint32_t s = sh.tmem + 256 * X + ((uint32_t)quad << 21);
+    r.f = KIND == PISA_CACHE_E2M1 ? sh.factor[row_of] : SCORED ? kScale : kScale * kLog2e;
     r.m = kNone;
     if (SCORED) {
       r.cap = CapRow{r.f * a.score.inv_cap, r.f * kLog2e};
@@ -641,53 +624,78 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(CachePr
       }
     }
     bool two_step = false;
-    for (int x = 0; x < n && ok; ++x)
-      ok = soften<KIND, SCORED>(a, sh, r, s, X, lane, u.i0 + x, kt + x, x == 0, two_step);
-    if (ok && n > 0) ok = __all_sync(kFull, mbar_wait(&sh.pv_done[X], (kt + n - 1) & 1, &sh.abort));
+    for (int x = 0; x < n; ++x)
+      soften<KIND, SCORED>(a, sh, r, s, X, half, row_of, id, lane, u.i0 + x, x, two_step, ok);
+    if (ok && n > 0) ok = __all_sync(kFull, mbar_wait(&sh.pv_done[X], (n - 1) & 1, &sh.abort));
+    sh.half[half][row_of] = r.l;
+    sync_two(id);
     if (ok) {
       tc_fence_after();
+      r.l += sh.half[half ^ 1][row_of];
       if (r.lo >= r.hi) r.l = 0.f;  // (its weights were never masked: see soften)
       if (sh.bad && sees_bad(a, u, r)) {
         r.l = __int_as_float(0x7fc00000);
         set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
       }
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        float o[32];
-        if (n > 0) {
-          uint32_t w[32];
-          tmem_ld32_now(s + 192 + 32 * h, w);
+      float o[32];  // dims 32 half ..
+      if (n > 0) {
+        uint32_t w[32];
+        tmem_ld32_now(s + 192 + 32 * half, w);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(w[i]);
-          if (sh.odd) odd_values<KIND>(a, u, sh, r, 32 * h, o);
-        }
-        write_row(a, u, r, 32 * h, o);
+        for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(w[i]);
+        if (sh.odd) odd_values<KIND>(a, u, sh, r, 32 * half, o);
       }
+      write_row(a, u, r, 32 * half, o);
       tc_fence_before();
     }
   } else if (warp < kSoftWarps + kLoadWarps) {
-    if (u.i0 < u.i1) {
-      if (KIND == PISA_CACHE_BF16)
-        ok = load_bf16(a, u, sh, stages, kt, warp - kSoftWarps, lane);
-      else
-        ok = load_e2m1(a, u, sh, stages, kt, warp - kSoftWarps, lane);
+    ok = load_tiles<KIND>(a, &map, u, sh, stages, warp - kSoftWarps, lane, next);
+  } else if (lane == 0) {
+    const int Y = warp - kSoftWarps - kLoadWarps;
+    ok = multiply<KIND>(u, sh, q, stages, Y);
+    if (!ok && n > 0) {  // its products end before tensor memory is given back
+      umma_commit(&sh.drain[Y]);
+      mbar_wait(&sh.drain[Y], 0, nullptr);
     }
-  } else if (u.i0 < u.i1) {
-    ok = multiply<KIND>(u, sh, q, stages, kt, lane, issued);
   }
-  if (!ok && lane == 0) {  // a wait ran out: the others give up, too
+  if (!ok) {  // a wait ran out: the others give up, too
     *const_cast<volatile int*>(&sh.abort) = 1;
     set_status(a.status, PISA_ERR_DEVICE_TIMEOUT);
   }
-  if (!ok && issued) {  // (the MMA warp: its products end before tensor memory is given back)
-    if (lane == 0) {
-      umma_commit(&sh.drain);
-      mbar_wait(&sh.drain, 0, nullptr);
-    }
-    __syncwarp();
+  __syncthreads();
+  if (KIND == PISA_CACHE_BF16 && sh.abort && warp >= kSoftWarps && warp < kSoftWarps + kLoadWarps && lane == 0) {
+    // given up: copies that are still on their way land before the shared memory is let go
+    for (unsigned k = next > kPStages ? next - kPStages : 0; k < next; ++k)
+      if (k % kLoadWarps == (unsigned)(warp - kSoftWarps)) mbar_wait(&sh.full[k % kPStages], (k / kPStages) & 1, nullptr);
   }
   __syncthreads();
   if (warp == kSoftWarps + kLoadWarps) tmem_dealloc<512>(sh.tmem);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// bf16 pages as [page][head, record, K or V][token of the record][64], a box of one record's keys or values.
+bool map_pages(CUtensorMap* m, const CacheDev& c) {
+  const auto encode = encode_tiled();
+  if (!encode) return false;
+  const cuuint64_t U = 1ull << c.rec_shift;
+  const cuuint64_t dims[4] = {kD, U, (cuuint64_t)c.Hkv << (c.page_shift - c.rec_shift + 1), (cuuint64_t)c.n_pages};
+  const cuuint64_t strides[3] = {2 * kD, 2 * kD * U, (cuuint64_t)c.page_stride};
+  const cuuint32_t box[4] = {kD, (cuuint32_t)U, 1, 1}, es[4] = {1, 1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, c.pages, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int KIND, bool SCORED>
@@ -696,7 +704,9 @@ static cudaError_t launch_prompt(const CachePromptLaunch& L, cudaStream_t s) {
   while ((1 << g_shift) < L.G) ++g_shift;
   const int row_tiles = (int)(((long long)L.T * L.G + kRowsCta - 1) / kRowsCta);
   const long long units = (long long)row_tiles * L.cache.B * L.cache.Hkv;
-  return launch_early<cache_prompt_kernel<KIND, SCORED>>((unsigned)units, kPromptThreads, kPromptSmem, s, L, g_shift,
+  CUtensorMap map{};
+  if (KIND == PISA_CACHE_BF16 && !map_pages(&map, L.cache)) return cudaErrorInvalidValue;
+  return launch_early<cache_prompt_kernel<KIND, SCORED>>((unsigned)units, kPromptThreads, kPromptSmem, s, map, L, g_shift,
                                                          row_tiles);
 }
 
