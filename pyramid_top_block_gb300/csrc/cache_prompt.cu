@@ -5,11 +5,11 @@
 //
 // Rows are (token, head) pairs of one KV head, heads fastest, so that a head group shares its keys.  A CTA takes
 // 256 rows, two tiles of 128, over tiles of 128 keys: S = Q K^T (tcgen05, operands from shared memory) -> registers,
-// two threads a row -> weights, back to tensor memory as the left operand of O += P V.  While one row tile's weights
+// a row a thread -> weights, back to tensor memory as the left operand of O += P V.  While one row tile's weights
 // are computed the tensor core works for the other; keys and values are read from L2 once for both.
-//   warps 0 .. 15   softmax, eight for each row tile: four for its first 64 columns, four for the others
-//   warps 16, 17    pages -> shared memory, every second tile each (bf16: by TMA; 4 bits: through registers, as fp16)
-//   warps 18, 19    issue the matrix instructions, one for each row tile
+//   warps 0 .. 7    softmax, four for each row tile
+//   warps 8, 9      pages -> shared memory, every second tile each (bf16: by TMA; 4 bits: through registers, as fp16)
+//   warps 10, 11    issue the matrix instructions, one for each row tile
 // Tensor memory, for each row tile: S 128 columns, P 64, O 64; both together all 512.
 #include "cache_prompt.cuh"
 
@@ -21,7 +21,7 @@
 namespace pisa {
 
 constexpr int kRowsTile = 128, kRowsCta = 256, kKeys = 128;
-constexpr int kSoftWarps = 16, kLoadWarps = 2, kPromptThreads = (kSoftWarps + kLoadWarps + 2) * 32;
+constexpr int kSoftWarps = 8, kLoadWarps = 2, kPromptThreads = (kSoftWarps + kLoadWarps + 2) * 32;
 constexpr int kPStages = 5;
 constexpr int kTileBytes = kKeys * kD * 2;  // keys or values of a tile: rows of 128 bytes, 128-byte swizzle
 constexpr int kPromptSmem = 2 * kTileBytes + kPStages * 2 * kTileBytes + 1024;
@@ -56,7 +56,6 @@ struct PromptShared {
   int abort, odd, bad;
   int lo_min, lo_max, hi_min, hi_max;  // of the rows that see anything
   float factor[kRowsCta];              // 4-bit pages: the rows' logit factors
-  float half[2][kRowsCta];             // what the two threads of a row tell each other
 };
 
 // What of a CTA's rows a warp needs to know.
@@ -287,116 +286,93 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
   return d;
 }
 
-// 64 products of a row, of the keys from key0 on, as the logits that the softmax takes (times r.f if not SCORED and not
+// A tile's products of a row, of the keys from key0 on, as the logits that the softmax takes (times r.f if not SCORED and not
 // two_step).
 template <bool SCORED>
 __device__ __forceinline__ void logits(const CachePromptLaunch& a, const PromptRow& r, int key0, bool whole, bool two_step,
-                                       float (&v)[64]) {
+                                       float (&v)[kKeys]) {
   if constexpr (SCORED) {
     if (a.score.cap > 0.f) {
       float b = 0.f;
 #pragma unroll
-      for (int i = 0; i < 64; i += 2) b = max3f(b, fabsf(v[i]), fabsf(v[i + 1]));
+      for (int i = 0; i < kKeys; i += 2) b = max3f(b, fabsf(v[i]), fabsf(v[i + 1]));
       if (__any_sync(kFull, b * r.cap.to_y > 1.f)) {
         const float top = a.score.cap * kLog2e;
 #pragma unroll
-        for (int i = 0; i < 64; ++i) v[i] = cap_any(v[i], r.cap, top);
+        for (int i = 0; i < kKeys; ++i) v[i] = cap_any(v[i], r.cap, top);
       } else {
 #pragma unroll
-        for (int i = 0; i < 64; i += 2) cap_small(v[i], v[i + 1], r.cap);
+        for (int i = 0; i < kKeys; i += 2) cap_small(v[i], v[i + 1], r.cap);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 64; ++i) v[i] *= r.f;
+      for (int i = 0; i < kKeys; ++i) v[i] *= r.f;
     }
     if (a.score.slopes) {  // -slope (|p - j| - |p - nearest|): whole numbers, exact up to 2^24
       const float d0 = (float)(key0 - r.pos);
 #pragma unroll
-      for (int i = 0; i < 64; ++i) v[i] = fmaf(-r.slope, fabsf(d0 + (float)i) - r.dref, v[i]);
+      for (int i = 0; i < kKeys; ++i) v[i] = fmaf(-r.slope, fabsf(d0 + (float)i) - r.dref, v[i]);
     }
   } else if (two_step) {
 #pragma unroll
-    for (int i = 0; i < 64; ++i) v[i] = __fmul_rn(v[i], r.f);
+    for (int i = 0; i < kKeys; ++i) v[i] = __fmul_rn(v[i], r.f);
   }
   if (!whole) {
     const int from = r.lo - key0, to = r.hi - key0;
 #pragma unroll
-    for (int i = 0; i < 64; ++i) v[i] = i >= from && i < to ? v[i] : -INFINITY;
+    for (int i = 0; i < kKeys; ++i) v[i] = i >= from && i < to ? v[i] : -INFINITY;
   }
 }
 
-__device__ __forceinline__ float max64(const float (&v)[64]) {
+__device__ __forceinline__ float max_of(const float (&v)[kKeys]) {
   float b0 = -INFINITY, b1 = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < 64; i += 4) {
+  for (int i = 0; i < kKeys; i += 4) {
     b0 = max3f(b0, v[i], v[i + 1]);
     b1 = max3f(b1, v[i + 2], v[i + 3]);
   }
   return fmaxf(b0, b1);
 }
 
-__device__ __forceinline__ void load64(uint32_t taddr, float (&v)[64]) {
-  uint32_t w[64];
-  tmem_ld64_now(taddr, w);
-#pragma unroll
-  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(w[i]);
-}
-
-// Whether a predicate holds for any thread of the two warps that share 32 rows (named barrier id).
-__device__ __forceinline__ bool any_of_two(int id, bool x) {
-  int r;
-  asm volatile(
-      "{ .reg .pred p, q; setp.ne.b32 p, %1, 0; barrier.cta.red.or.pred q, %2, 64, p; selp.b32 %0, 1, 0, q; }"
-      : "=r"(r)
-      : "r"((int)x), "r"(id)
-      : "memory");
-  return r != 0;
-}
-__device__ __forceinline__ void sync_two(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
-
-// The softmax of one key tile, half of its columns, for the warp's 32 rows.  s: the tensor memory columns of the row tile at
-// the warp's lanes.
+// The softmax of one key tile for the warp's 32 rows.  s: the tensor memory columns of the row tile at the warp's lanes.
 template <int KIND, bool SCORED>
-__device__ __forceinline__ void soften(const CachePromptLaunch& a, PromptShared& sh, PromptRow& r, uint32_t s, int X,
-                                       int half, int row, int id, int lane, int tile, unsigned k, bool& two_step,
-                                       bool& ok) {
+__device__ __forceinline__ bool soften(const CachePromptLaunch& a, PromptShared& sh, PromptRow& r, uint32_t s, int X,
+                                       int lane, int tile, unsigned k, bool& two_step) {
   using C = PCfg<KIND>;
-  const int key0 = tile * kKeys + 64 * half;
+  const int key0 = tile * kKeys;
   // (rows that see nothing do not matter: they get zeros at the end, or do not exist)
-  const bool whole = __all_sync(kFull, r.lo >= r.hi || (r.lo <= key0 && r.hi >= key0 + 64));
-  // (a warp whose wait ran out goes on without waiting, so that its partner is not left at a barrier of both)
-  const auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (ok) ok = __all_sync(kFull, mbar_wait(bar, parity, &sh.abort));
-    tc_fence_after();
-  };
-  wait(&sh.s_full[X], k & 1);
-  float v[64];
-  load64(s + 64 * half, v);
+  const bool whole = __all_sync(kFull, r.lo >= r.hi || (r.lo <= key0 && r.hi >= key0 + kKeys));
+  if (!__all_sync(kFull, mbar_wait(&sh.s_full[X], k & 1, &sh.abort))) return false;
+  tc_fence_after();
+  float v[kKeys];
+  {
+    uint32_t w[kKeys];
+    tmem_ld128_now(s, w);
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) v[i] = __uint_as_float(w[i]);
+  }
   tc_fence_before();
   __syncwarp();
   if (lane == 0) mbar_arrive(&sh.s_free[X]);  // S is in registers: the next product may overwrite it
   logits<SCORED>(a, r, key0, whole, two_step, v);
   bool waited = k == 0;  // for the product before, which reads P and writes O
   float ff = SCORED || two_step ? 1.f : r.f;
-  float b = __fmul_rn(max64(v), ff);
+  const float b = __fmul_rn(max_of(v), ff);
   // A row's reference m is set anew only when a logit passes it by more than kTop, so that few tiles rescale O.
-  if (any_of_two(id, b > r.m + C::kTop)) {
-    sh.half[half][row] = b;
-    sync_two(id);
-    b = fmaxf(b, sh.half[half ^ 1][row]);
-    sync_two(id);  // (both have read before either writes again)
+  if (__any_sync(kFull, b > r.m + C::kTop)) {
     // (a step of 32 bits is too coarse for the shift from 2^24 on; nothing that it is for is left there)
     const float n = fmaxf(r.m, fabsf(b) < 16.f * kFar ? b - C::kShift : b);
     const float f = ex2_approx(r.m - n);
     if (k > 0) {
-      wait(&sh.pv_done[X], (k - 1) & 1);
+      if (!__all_sync(kFull, mbar_wait(&sh.pv_done[X], (k - 1) & 1, &sh.abort))) return false;
+      tc_fence_after();
 #pragma unroll 1
-      for (int c = 0; c < 2; ++c) {  // this half of O's columns
-        uint32_t o[16];
-        tmem_ld16_now(s + 192 + 32 * half + 16 * c, o);
+      for (int h = 0; h < 2; ++h) {
+        uint32_t o[32];
+        tmem_ld32_now(s + 192 + 32 * h, o);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-        tmem_st16(s + 192 + 32 * half + 16 * c, o);
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+        tmem_st32(s + 192 + 32 * h, o);
       }
       waited = true;
     }
@@ -407,30 +383,31 @@ __device__ __forceinline__ void soften(const CachePromptLaunch& a, PromptShared&
     if (!SCORED && !two_step && __any_sync(kFull, fabsf(n) >= kFar && n != kNone)) {
       two_step = true;
 #pragma unroll
-      for (int i = 0; i < 64; ++i) v[i] = __fmul_rn(v[i], r.f);
+      for (int i = 0; i < kKeys; ++i) v[i] = __fmul_rn(v[i], r.f);
       ff = 1.f;
     }
   }
   const unsigned long long f2 = f2_pack(ff, ff), m2 = f2_pack(-r.m, -r.m);
   unsigned long long s0 = 0, s1 = 0;
-  uint32_t w[2][16];
+  uint32_t w[2][32];
 #pragma unroll
-  for (int c = 0; c < 2; ++c)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float x, y;
-      f2_unpack(f2_fma(f2_pack(v[32 * c + 2 * i], v[32 * c + 2 * i + 1]), f2, m2), x, y);
-      x = ex2_approx(x);
-      y = ex2_approx(y);
-      if (i & 1)
-        s1 = f2_add(s1, f2_pack(x, y));
-      else
-        s0 = f2_add(s0, f2_pack(x, y));
-      w[c][i] = KIND == PISA_CACHE_BF16 ? pack_bf16x2(x, y) : pack_f16x2(x, y);
-    }
-  if (!waited) wait(&sh.pv_done[X], (k - 1) & 1);
-  tmem_st16(s + 128 + 32 * half, w[0]);
-  tmem_st16(s + 128 + 32 * half + 16, w[1]);
+  for (int i = 0; i < kKeys / 2; ++i) {
+    float x, y;
+    f2_unpack(f2_fma(f2_pack(v[2 * i], v[2 * i + 1]), f2, m2), x, y);
+    x = ex2_approx(x);
+    y = ex2_approx(y);
+    if (i & 1)
+      s1 = f2_add(s1, f2_pack(x, y));
+    else
+      s0 = f2_add(s0, f2_pack(x, y));
+    w[i >> 5][i & 31] = KIND == PISA_CACHE_BF16 ? pack_bf16x2(x, y) : pack_f16x2(x, y);
+  }
+  if (!waited) {
+    if (!__all_sync(kFull, mbar_wait(&sh.pv_done[X], (k - 1) & 1, &sh.abort))) return false;
+    tc_fence_after();
+  }
+  tmem_st32(s + 128, w[0]);
+  tmem_st32(s + 160, w[1]);
   float x, y;
   f2_unpack(f2_add(s0, s1), x, y);
   r.l += x + y;
@@ -438,6 +415,7 @@ __device__ __forceinline__ void soften(const CachePromptLaunch& a, PromptShared&
   tc_fence_before();
   __syncwarp();
   if (lane == 0) mbar_arrive(&sh.p_full[X]);
+  return true;
 }
 
 // Values that scrub took out, of tokens that this row sees, in dims d0 .. d0 + 31 (an infinity, or a NaN, whatever
@@ -509,8 +487,8 @@ __device__ __forceinline__ void stage_queries(const CachePromptLaunch& a, const 
                                               unsigned char* q, int count, int g_shift) {
   const int ch = threadIdx.x & 7;
 #pragma unroll 4
-  for (int it = 0; it < 4; ++it) {
-    const int row = it * 64 + (threadIdx.x >> 3), r = u.r0 + row, t = r >> g_shift;
+  for (int it = 0; it < 8; ++it) {
+    const int row = it * 32 + (threadIdx.x >> 3), r = u.r0 + row, t = r >> g_shift;
     uint4 x = make_uint4(0, 0, 0, 0);
     if (t < count) {
       const int head = u.kv * a.G + (r & (a.G - 1));
@@ -551,8 +529,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
     for (int X = 0; X < 2; ++X) {
       mbar_init(&sh.s_full[X], 1);
-      mbar_init(&sh.s_free[X], 8);
-      mbar_init(&sh.p_full[X], 8);
+      mbar_init(&sh.s_free[X], 4);
+      mbar_init(&sh.p_full[X], 4);
       mbar_init(&sh.pv_done[X], 1);
       mbar_init(&sh.drain[X], 1);
     }
@@ -572,10 +550,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   u.r0 = (row_tiles - 1 - (int)(blockIdx.x / heads)) * kRowsCta;
   const int count = prompt_count(a, u.b);
   PromptRow r{};
-  // softmax warps: row tile X, lanes 32 quad .., half of the columns; row_of: the thread's row of the CTA's 256
-  const int X = (warp >> 3) & 1, half = (warp >> 2) & 1, quad = warp & 3, row_of = X * kRowsTile + quad * 32 + lane;
   if (warp < kSoftWarps) {
-    const int row = u.r0 + row_of;
+    const int row = u.r0 + threadIdx.x;
     r.t = row >> g_shift;
     r.head = u.kv * a.G + (row & (a.G - 1));
     r.there = r.t < count;
@@ -611,9 +587,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   unsigned next = 0;  // one past the last tile that this loading warp has asked for
   const int n = u.i1 - u.i0;
   if (warp < kSoftWarps) {
-    const int id = 1 + X * 4 + quad;
-    const uint32_t s = sh.tmem + 256 * X + ((uint32_t)quad << 21);
-    r.f = KIND == PISA_CACHE_E2M1 ? sh.factor[row_of] : SCORED ? kScale : kScale * kLog2e;
+    const int X = warp >> 2;
+    const uint32_t s = sh.tmem + 256 * X + ((uint32_t)(warp & 3) << 21);  // (the warp's lanes: 32 (warp & 3) ..)
+    r.f = KIND == PISA_CACHE_E2M1 ? sh.factor[threadIdx.x] : SCORED ? kScale : kScale * kLog2e;
     r.m = kNone;
     if (SCORED) {
       r.cap = CapRow{r.f * a.score.inv_cap, r.f * kLog2e};
@@ -624,28 +600,27 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
     }
     bool two_step = false;
-    for (int x = 0; x < n; ++x)
-      soften<KIND, SCORED>(a, sh, r, s, X, half, row_of, id, lane, u.i0 + x, x, two_step, ok);
+    for (int x = 0; x < n && ok; ++x) ok = soften<KIND, SCORED>(a, sh, r, s, X, lane, u.i0 + x, x, two_step);
     if (ok && n > 0) ok = __all_sync(kFull, mbar_wait(&sh.pv_done[X], (n - 1) & 1, &sh.abort));
-    sh.half[half][row_of] = r.l;
-    sync_two(id);
     if (ok) {
       tc_fence_after();
-      r.l += sh.half[half ^ 1][row_of];
       if (r.lo >= r.hi) r.l = 0.f;  // (its weights were never masked: see soften)
       if (sh.bad && sees_bad(a, u, r)) {
         r.l = __int_as_float(0x7fc00000);
         set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
       }
-      float o[32];  // dims 32 half ..
-      if (n > 0) {
-        uint32_t w[32];
-        tmem_ld32_now(s + 192 + 32 * half, w);
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        float o[32];
+        if (n > 0) {
+          uint32_t w[32];
+          tmem_ld32_now(s + 192 + 32 * h, w);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(w[i]);
-        if (sh.odd) odd_values<KIND>(a, u, sh, r, 32 * half, o);
+          for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(w[i]);
+          if (sh.odd) odd_values<KIND>(a, u, sh, r, 32 * h, o);
+        }
+        write_row(a, u, r, 32 * h, o);
       }
-      write_row(a, u, r, 32 * half, o);
       tc_fence_before();
     }
   } else if (warp < kSoftWarps + kLoadWarps) {
