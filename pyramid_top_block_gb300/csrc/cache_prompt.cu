@@ -9,7 +9,7 @@
 // are computed the tensor core works for the other; keys and values are read from L2 once for both.
 //   warps 0 .. 7    softmax, four for each row tile
 //   warps 8, 9      pages -> shared memory, every second tile each (bf16: by TMA; 4 bits: through registers, as fp16)
-//   warps 10, 11    issue the matrix instructions, one for each row tile
+//   warps 10, 11    issue the matrix instructions: one S = Q K^T, the other O += P V
 // Tensor memory, for each row tile: S 128 columns, P 64, O 64; both together all 512.
 #include "cache_prompt.cuh"
 
@@ -22,9 +22,8 @@ namespace pisa {
 
 constexpr int kRowsTile = 128, kRowsCta = 256, kKeys = 128;
 constexpr int kSoftWarps = 8, kLoadWarps = 2, kPromptThreads = (kSoftWarps + kLoadWarps + 2) * 32;
-constexpr int kPStages = 5;
 constexpr int kTileBytes = kKeys * kD * 2;  // keys or values of a tile: rows of 128 bytes, 128-byte swizzle
-constexpr int kPromptSmem = 2 * kTileBytes + kPStages * 2 * kTileBytes + 1024;
+constexpr int kRawBytes = kKeys * kRowE2m1;  // a tile as 4-bit pages hold it
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -0x1.fffffep127f;  // the reference of a row that has seen no logit above minus infinity
 constexpr float kFar = 0x1p20f;            // references from which on differences are taken in two steps
@@ -36,6 +35,9 @@ template <int KIND>
 struct PCfg {
   static constexpr float kShift = KIND == PISA_CACHE_BF16 ? 0.f : 10.f;
   static constexpr float kTop = kShift + (KIND == PISA_CACHE_BF16 ? 20.f : 5.f);  // how far a logit may pass m
+  static constexpr int kStages = KIND == PISA_CACHE_BF16 ? 5 : 4;  // tiles of keys and values in shared memory
+  static constexpr int kSmem =
+      1024 + (2 + 2 * kStages) * kTileBytes + (KIND == PISA_CACHE_BF16 ? 0 : 2 * kLoadWarps * kRawBytes);
   static constexpr uint32_t kType = KIND == PISA_CACHE_BF16 ? 1u : 0u;
   // fp32 accumulator, A and B of the type; the second has B with its columns (dims) contiguous
   static constexpr uint32_t kIdescS = (1u << 4) | (kType << 7) | (kType << 10) | ((kKeys >> 3) << 17) | ((kRowsTile >> 4) << 24);
@@ -50,8 +52,9 @@ __device__ __forceinline__ uint64_t umma_desc_mn128(uint32_t addr) {
 }
 
 struct PromptShared {
-  uint64_t full[kPStages], empty[kPStages];
-  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], drain[2], landed[kLoadWarps];
+  uint64_t full[5], empty[5];
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], drain[2];
+  uint64_t landed[kLoadWarps][2];  // (bf16: the first; 4 bits: of each raw buffer)
   uint32_t tmem;
   int abort, odd, bad;
   int lo_min, lo_max, hi_min, hi_max;  // of the rows that see anything
@@ -124,17 +127,17 @@ __device__ __forceinline__ void dequant16(uint32_t c0, uint32_t c1, uint32_t sca
   y = make_uint4(hmul2u(d[0], s2), hmul2u(d[1], s2), hmul2u(d[2], s2), hmul2u(d[3], s2));
 }
 
-// A token's codes and scales.
-struct Codes {
-  uint4 k0, k1, v0, v1;
-  uint32_t ks, vs;
-};
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
 
-template <int KIND>
-__device__ __forceinline__ bool load_tiles(const CachePromptLaunch& a, const CUtensorMap* map, const PromptUnit& u,
-                                           PromptShared& sh, unsigned char* stages, int warp, int lane,
-                                           unsigned& next) {
-  const int rs = a.cache.rec_shift, U = 1 << rs;
+// bf16 pages by TMA.  next: one past the last tile asked for.
+__device__ __forceinline__ bool load_bf16(const CachePromptLaunch& a, const CUtensorMap* map, const PromptUnit& u,
+                                          PromptShared& sh, unsigned char* stages, int warp, int lane, unsigned& next) {
+  constexpr unsigned kPStages = PCfg<PISA_CACHE_BF16>::kStages;
+  const int rs = a.cache.rec_shift;
   bool ok = true;
   int page = 0, mine = 0;
   unsigned landings = 0;
@@ -145,125 +148,158 @@ __device__ __forceinline__ bool load_tiles(const CachePromptLaunch& a, const CUt
     ok = __all_sync(kFull, ok);
     if (!ok) break;
     unsigned char* stage = stages + st * 2 * kTileBytes;
-    const int piece0 = (mine % 4) * 8;
     const bool mixed = u.mixed(sh, tile);
-    if constexpr (KIND == PISA_CACHE_BF16) {
-      // lane 2 i + h: the keys (h = 0) or values of record i; a page number of n_pages lies outside the map and gives zeros
-      uint64_t* bar = mixed ? &sh.landed[warp] : &sh.full[st];
-      if (lane == 0) mbar_expect_tx(bar, 2 * kTileBytes);
-      __syncwarp();
-      const int i = lane >> 1, h = lane & 1, from = __shfl_sync(kFull, page, (piece0 | i) & 31);
-      if (i < kKeys >> rs) {
-        const int key = tile * kKeys + (i << rs), rec = (key & ((1 << a.cache.page_shift) - 1)) >> rs;
-        tma_load_4d(stage + h * kTileBytes + (i << rs) * 128, map, 0, 0,
-                    (((u.kv << (a.cache.page_shift - rs)) + rec) << 1) + h, from, bar);
+    // lane 2 i + h: the keys (h = 0) or values of record i; a page number of n_pages lies outside the map and gives zeros
+    uint64_t* bar = mixed ? &sh.landed[warp][0] : &sh.full[st];
+    if (lane == 0) mbar_expect_tx(bar, 2 * kTileBytes);
+    __syncwarp();
+    const int i = lane >> 1, h = lane & 1, from = __shfl_sync(kFull, page, ((mine % 4) * 8 + i) & 31);
+    if (i < kKeys >> rs) {
+      const int key = tile * kKeys + (i << rs), rec = (key & ((1 << a.cache.page_shift) - 1)) >> rs;
+      tma_load_4d(stage + h * kTileBytes + (i << rs) * 128, map, 0, 0,
+                  (((u.kv << (a.cache.page_shift - rs)) + rec) << 1) + h, from, bar);
+    }
+    if (mixed) {
+      ok = __all_sync(kFull, mbar_wait(bar, landings & 1, &sh.abort));
+      if (!ok) {  // (given up; the copies land first)
+        mbar_wait(bar, landings & 1, nullptr);
+        break;
       }
-      if (mixed) {
-        ok = __all_sync(kFull, mbar_wait(bar, landings & 1, &sh.abort));
-        if (!ok) {  // (given up; the copies land first)
-          mbar_wait(bar, landings & 1, nullptr);
-          break;
-        }
-        ++landings;
-        scrub(sh, stage + kTileBytes, tile, lane);
-        fence_async_proxy();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.full[st]);
-      }
-      next = k + 1;
-    } else {
-      // a token a lane, four turns; the words of the next turn but one are on their way meanwhile
-      Codes c[3];
-      auto fetch = [&](int j, Codes& c) {
-        const int from = __shfl_sync(kFull, page, piece0 | ((32 * j + lane) >> rs));
-        c.k0 = c.k1 = c.v0 = c.v1 = make_uint4(0, 0, 0, 0);
-        c.ks = c.vs = 0;
-        if (from < a.cache.n_pages) {
-          const int key = tile * kKeys + 32 * j + lane, in = key & (U - 1);
-          const unsigned char* r = a.cache.pages + cache_record(a.cache, kRowE2m1, from, u.kv, key);
-          const uint4* kc = reinterpret_cast<const uint4*>(r + in * 32);
-          const uint4* vc = reinterpret_cast<const uint4*>(r + 36 * U + in * 32);
-          c.k0 = kc[0];
-          c.k1 = kc[1];
-          c.ks = *reinterpret_cast<const uint32_t*>(r + 32 * U + in * 4);
-          c.v0 = vc[0];
-          c.v1 = vc[1];
-          c.vs = *reinterpret_cast<const uint32_t*>(r + 68 * U + in * 4);
-        }
-      };
-      fetch(0, c[0]);
-      fetch(1, c[1]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j + 2 < 4) fetch(j + 2, c[(j + 2) % 3]);
-        const Codes& x = c[j % 3];
-        const int row = 32 * j + lane;
-        uint32_t vs = x.vs;
-        if (mixed) {  // NaN blocks of values that not all rows see become zeros (see scrub)
-          uint32_t keep = 0xffffffffu;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if ((vs >> (8 * i) & 0x7fu) == 0x7fu) keep &= ~(0xffu << (8 * i));
-          if (keep != 0xffffffffu) {
-            vs &= keep;
-            const int key = tile * kKeys + row;
-            if (key >= sh.lo_min && key < sh.hi_max) sh.odd = 1;
-          }
-        }
-        const uint32_t w[2][8] = {{x.k0.x, x.k0.y, x.k0.z, x.k0.w, x.k1.x, x.k1.y, x.k1.z, x.k1.w},
-                                  {x.v0.x, x.v0.y, x.v0.z, x.v0.w, x.v1.x, x.v1.y, x.v1.z, x.v1.w}};
-        const uint32_t sc[2] = {x.ks, vs};
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint4 y, z;
-            dequant16(w[h][2 * i], w[h][2 * i + 1], sc[h] >> (8 * i) & 0xffu, y, z);
-            unsigned char* at = stage + h * kTileBytes + row * 128;
-            *reinterpret_cast<uint4*>(at + (((2 * i) ^ (row & 7)) << 4)) = y;
-            *reinterpret_cast<uint4*>(at + (((2 * i + 1) ^ (row & 7)) << 4)) = z;
-          }
-      }
+      ++landings;
+      scrub(sh, stage + kTileBytes, tile, lane);
       fence_async_proxy();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.full[st]);
     }
+    next = k + 1;
+  }
+  return ok;
+}
+
+// 4-bit pages: records by bulk copies into one of the warp's two raw buffers, a tile ahead; from there as fp16 into the stage,
+// a token a lane.  next: raw buffers asked for.
+__device__ __forceinline__ bool load_e2m1(const CachePromptLaunch& a, const PromptUnit& u, PromptShared& sh,
+                                          unsigned char* stages, unsigned char* raw, int warp, int lane, unsigned& next) {
+  constexpr unsigned kPStages = PCfg<PISA_CACHE_E2M1>::kStages;
+  const int rs = a.cache.rec_shift, U = 1 << rs;
+  const uint32_t rec_bytes = U * kRowE2m1;
+  int page = 0, page_next = 0;
+  bool ok = true;
+  // asks for the records of the warp's tile number x
+  const auto ask = [&](int x) {
+    const int tile = u.i0 + warp + kLoadWarps * x;
+    if (x % 4 == 0) page_next = look(a, u, sh, lane, tile);
+    const int from = __shfl_sync(kFull, page_next, ((x % 4) * 8 + lane) & 31);
+    const bool there = lane < kKeys >> rs && from < a.cache.n_pages;
+    const uint32_t bytes = __popc(__ballot_sync(kFull, there)) * rec_bytes;
+    uint64_t* bar = &sh.landed[warp][x & 1];
+    if (lane == 0) mbar_expect_tx(bar, bytes);
+    __syncwarp();
+    if (there)
+      bulk_load(raw + (x & 1) * kRawBytes + lane * rec_bytes,
+                a.cache.pages + cache_record(a.cache, kRowE2m1, from, u.kv, tile * kKeys + (lane << rs)), rec_bytes, bar);
+    next = x + 1;
+  };
+  int x = 0;
+  if (u.i0 + warp < u.i1) ask(0);
+  for (int tile = u.i0 + warp; tile < u.i1; tile += kLoadWarps, ++x) {
+    const unsigned k = tile - u.i0, st = k % kPStages;
+    if (x % 4 == 0) page = page_next;
+    if (tile + kLoadWarps < u.i1) ask(x + 1);
+    if (k >= kPStages) ok = mbar_wait(&sh.empty[st], (k / kPStages - 1) & 1, &sh.abort);
+    ok = ok && mbar_wait(&sh.landed[warp][x & 1], (x >> 1) & 1, &sh.abort);
+    ok = __all_sync(kFull, ok);
+    if (!ok) break;
+    const bool mixed = u.mixed(sh, tile);
+    unsigned char* stage = stages + st * 2 * kTileBytes;
+#pragma unroll 2
+    for (int j = 0; j < 4; ++j) {
+      const int row = 32 * j + lane, rec = row >> rs, in = row & (U - 1);
+      const bool there = __shfl_sync(kFull, page, ((x % 4) * 8 + rec) & 31) < a.cache.n_pages;
+      const unsigned char* r = raw + (x & 1) * kRawBytes + rec * rec_bytes;
+      const uint4 c[2][2] = {{reinterpret_cast<const uint4*>(r + in * 32)[0], reinterpret_cast<const uint4*>(r + in * 32)[1]},
+                             {reinterpret_cast<const uint4*>(r + 36 * U + in * 32)[0],
+                              reinterpret_cast<const uint4*>(r + 36 * U + in * 32)[1]}};
+      // (a scale of zero makes zeros of whatever the codes are)
+      uint32_t sc[2] = {there ? *reinterpret_cast<const uint32_t*>(r + 32 * U + in * 4) : 0u,
+                        there ? *reinterpret_cast<const uint32_t*>(r + 68 * U + in * 4) : 0u};
+      if (mixed) {  // NaN blocks of values that not all rows see become zeros (see scrub)
+        uint32_t keep = 0xffffffffu;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if ((sc[1] >> (8 * i) & 0x7fu) == 0x7fu) keep &= ~(0xffu << (8 * i));
+        if (keep != 0xffffffffu) {
+          sc[1] &= keep;
+          const int key = tile * kKeys + row;
+          if (key >= sh.lo_min && key < sh.hi_max) sh.odd = 1;
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t w[8] = {c[h][0].x, c[h][0].y, c[h][0].z, c[h][0].w, c[h][1].x, c[h][1].y, c[h][1].z, c[h][1].w};
+        unsigned char* at = stage + h * kTileBytes + row * 128;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint4 y, z;
+          dequant16(w[2 * i], w[2 * i + 1], sc[h] >> (8 * i) & 0xffu, y, z);
+          *reinterpret_cast<uint4*>(at + (((2 * i) ^ (row & 7)) << 4)) = y;
+          *reinterpret_cast<uint4*>(at + (((2 * i + 1) ^ (row & 7)) << 4)) = z;
+        }
+      }
+    }
+    fence_async_proxy();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.full[st]);
   }
   return ok;
 }
 
 // ------------------------------------------------------------------------------------------------ the MMA warps
 
-// The products of row tile X, issued by one thread.  The next tile's S comes before the last one's P V, so that it is there
-// when the softmax is done with the last one.
+// One thread issues the S products of both row tiles, another one the products with V: issuing takes as long as the
+// products themselves, so that one thread for both would hold the next S back behind a product with V (158 -> XXX us).
 template <int KIND>
-__device__ __forceinline__ bool multiply(const PromptUnit& u, PromptShared& sh, const unsigned char* q,
-                                         const unsigned char* stages, int X) {
+__device__ __forceinline__ bool multiply_s(const PromptUnit& u, PromptShared& sh, const unsigned char* q,
+                                           const unsigned char* stages) {
+  constexpr unsigned kPStages = PCfg<KIND>::kStages;
   const unsigned n = u.i1 - u.i0;
-  const uint32_t t = sh.tmem + 256 * X;
-  const uint64_t dq = umma_desc_sw128(q + X * kTileBytes);
-  for (unsigned k = 0; k <= n; ++k) {
-    const unsigned st = k % kPStages, before = (k + kPStages - 1) % kPStages;
-    if (k < n) {  // S = Q K^T
-      if (k > 0 && !mbar_wait(&sh.s_free[X], (k - 1) & 1, &sh.abort)) return false;
-      if (!mbar_wait(&sh.full[st], (k / kPStages) & 1, &sh.abort)) return false;
-      tc_fence_after();
-      const uint64_t db = umma_desc_sw128(stages + st * 2 * kTileBytes);
+  const uint64_t dq = umma_desc_sw128(q);
+  for (unsigned k = 0; k < n; ++k) {
+    const unsigned st = k % kPStages;
+    if (!mbar_wait(&sh.full[st], (k / kPStages) & 1, &sh.abort)) return false;
+    const uint64_t dk = umma_desc_sw128(stages + st * 2 * kTileBytes);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)  // (16 dims are 32 bytes, 2 in the descriptor's units)
-        umma_ss(t, dq + 2 * i, db + 2 * i, PCfg<KIND>::kIdescS, i);
+    for (int X = 0; X < 2; ++X) {
+      if (k > 0 && !mbar_wait(&sh.s_free[X], (k - 1) & 1, &sh.abort)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int i = 0; i < 4; ++i)  // (16 dims are 32 bytes; descriptors count in 16)
+        umma_ss(sh.tmem + 256 * X, dq + X * (kTileBytes / 16) + 2 * i, dk + 2 * i, PCfg<KIND>::kIdescS, i);
       umma_commit(&sh.s_full[X]);
     }
-    if (k > 0) {  // O += P V of the tile before
-      if (!mbar_wait(&sh.p_full[X], (k - 1) & 1, &sh.abort)) return false;
+  }
+  return true;
+}
+
+template <int KIND>
+__device__ __forceinline__ bool multiply_v(const PromptUnit& u, PromptShared& sh, const unsigned char* stages) {
+  constexpr unsigned kPStages = PCfg<KIND>::kStages;
+  const unsigned n = u.i1 - u.i0;
+  for (unsigned k = 0; k < n; ++k) {
+    const unsigned st = k % kPStages;
+    if (!mbar_wait(&sh.full[st], (k / kPStages) & 1, &sh.abort)) return false;
+    const uint64_t dv = umma_desc_mn128(smem_u32(stages + st * 2 * kTileBytes + kTileBytes));
+#pragma unroll
+    for (int X = 0; X < 2; ++X) {
+      const uint32_t t = sh.tmem + 256 * X;
+      if (!mbar_wait(&sh.p_full[X], k & 1, &sh.abort)) return false;
       tc_fence_after();
-      const uint64_t db = umma_desc_mn128(smem_u32(stages + before * 2 * kTileBytes + kTileBytes));
 #pragma unroll
       for (int i = 0; i < 8; ++i)  // (16 keys are 2048 bytes of V and 8 columns of P)
-        umma_ts(t + 192, t + 128 + 8 * i, db + 128 * i, PCfg<KIND>::kIdescO, k > 1 || i > 0);
+        umma_ts(t + 192, t + 128 + 8 * i, dv + 128 * i, PCfg<KIND>::kIdescO, k > 0 || i > 0);
       umma_commit(&sh.pv_done[X]);
-      umma_commit(&sh.empty[before]);
     }
+    umma_commit(&sh.empty[st]);  // (S of this tile is long done: its weights are here)
   }
   return true;
 }
@@ -287,16 +323,13 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
 }
 
 // A tile's products of a row, of the keys from key0 on, as the logits that the softmax takes (times r.f if not SCORED and not
-// two_step).
+// two_step).  size: the largest magnitude among the products (if SCORED).
 template <bool SCORED>
 __device__ __forceinline__ void logits(const CachePromptLaunch& a, const PromptRow& r, int key0, bool whole, bool two_step,
-                                       float (&v)[kKeys]) {
+                                       float size, float (&v)[kKeys]) {
   if constexpr (SCORED) {
     if (a.score.cap > 0.f) {
-      float b = 0.f;
-#pragma unroll
-      for (int i = 0; i < kKeys; i += 2) b = max3f(b, fabsf(v[i]), fabsf(v[i + 1]));
-      if (__any_sync(kFull, b * r.cap.to_y > 1.f)) {
+      if (__any_sync(kFull, size * r.cap.to_y > 1.f)) {
         const float top = a.score.cap * kLog2e;
 #pragma unroll
         for (int i = 0; i < kKeys; ++i) v[i] = cap_any(v[i], r.cap, top);
@@ -334,38 +367,45 @@ __device__ __forceinline__ float max_of(const float (&v)[kKeys]) {
   return fmaxf(b0, b1);
 }
 
+// The exponentials of the two row tiles take turns: the warps of one tile that share a scheduler (named barriers 1 .. 4
+// for the first tile, 5 .. 8 for the second) let those of the other one begin when theirs are done.  Left to themselves
+// both tiles compute them at the same time, each at half the rate, and then both wait for the rest.
+__device__ __forceinline__ void take_turn(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void give_turn(int id) { asm volatile("barrier.cta.arrive %0, 64;" ::"r"(id) : "memory"); }
+
 // The softmax of one key tile for the warp's 32 rows.  s: the tensor memory columns of the row tile at the warp's lanes.
+// ok becomes false if a wait ran out; what follows goes on without waiting, so that no other warp is left at a barrier.
 template <int KIND, bool SCORED>
-__device__ __forceinline__ bool soften(const CachePromptLaunch& a, PromptShared& sh, PromptRow& r, uint32_t s, int X,
-                                       int lane, int tile, unsigned k, bool& two_step) {
+__device__ __forceinline__ void soften(const CachePromptLaunch& a, PromptShared& sh, PromptRow& r, uint32_t s, int X,
+                                       int lane, int turn, bool last, int tile, unsigned k, bool& two_step, bool& ok) {
   using C = PCfg<KIND>;
   const int key0 = tile * kKeys;
   // (rows that see nothing do not matter: they get zeros at the end, or do not exist)
   const bool whole = __all_sync(kFull, r.lo >= r.hi || (r.lo <= key0 && r.hi >= key0 + kKeys));
-  if (!__all_sync(kFull, mbar_wait(&sh.s_full[X], k & 1, &sh.abort))) return false;
-  tc_fence_after();
-  float v[kKeys];
-  {
-    uint32_t w[kKeys];
-    tmem_ld128_now(s, w);
-#pragma unroll
-    for (int i = 0; i < kKeys; ++i) v[i] = __uint_as_float(w[i]);
-  }
+  const auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (ok) ok = __all_sync(kFull, mbar_wait(bar, parity, &sh.abort));
+    tc_fence_after();
+  };
+  wait(&sh.s_full[X], k & 1);
+  float v[kKeys], b;
+  tmem_ld128_top<SCORED>(s, v, b);
   tc_fence_before();
   __syncwarp();
   if (lane == 0) mbar_arrive(&sh.s_free[X]);  // S is in registers: the next product may overwrite it
-  logits<SCORED>(a, r, key0, whole, two_step, v);
-  bool waited = k == 0;  // for the product before, which reads P and writes O
   float ff = SCORED || two_step ? 1.f : r.f;
-  const float b = __fmul_rn(max_of(v), ff);
+  if (SCORED || two_step || !whole) {
+    logits<SCORED>(a, r, key0, whole, two_step, b, v);
+    b = max_of(v);
+  }
+  b = __fmul_rn(b, ff);
+  bool waited = k == 0;  // for the product before, which reads P and writes O
   // A row's reference m is set anew only when a logit passes it by more than kTop, so that few tiles rescale O.
   if (__any_sync(kFull, b > r.m + C::kTop)) {
     // (a step of 32 bits is too coarse for the shift from 2^24 on; nothing that it is for is left there)
     const float n = fmaxf(r.m, fabsf(b) < 16.f * kFar ? b - C::kShift : b);
     const float f = ex2_approx(r.m - n);
     if (k > 0) {
-      if (!__all_sync(kFull, mbar_wait(&sh.pv_done[X], (k - 1) & 1, &sh.abort))) return false;
-      tc_fence_after();
+      wait(&sh.pv_done[X], (k - 1) & 1);
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         uint32_t o[32];
@@ -387,8 +427,10 @@ __device__ __forceinline__ bool soften(const CachePromptLaunch& a, PromptShared&
       ff = 1.f;
     }
   }
-  const unsigned long long f2 = f2_pack(ff, ff), m2 = f2_pack(-r.m, -r.m);
-  unsigned long long s0 = 0, s1 = 0;
+  take_turn(turn + 4 * X);
+  const unsigned long long f2 = f2_pack(ff, ff);
+  unsigned long long m2 = f2_pack(-r.m, -r.m), s0 = 0, s1 = 0;
+  asm volatile("" : "+l"(m2));  // (nothing that uses it moves ahead of the turn)
   uint32_t w[2][32];
 #pragma unroll
   for (int i = 0; i < kKeys / 2; ++i) {
@@ -402,10 +444,9 @@ __device__ __forceinline__ bool soften(const CachePromptLaunch& a, PromptShared&
       s0 = f2_add(s0, f2_pack(x, y));
     w[i >> 5][i & 31] = KIND == PISA_CACHE_BF16 ? pack_bf16x2(x, y) : pack_f16x2(x, y);
   }
-  if (!waited) {
-    if (!__all_sync(kFull, mbar_wait(&sh.pv_done[X], (k - 1) & 1, &sh.abort))) return false;
-    tc_fence_after();
-  }
+  asm volatile("" : "+l"(s0), "+l"(s1));
+  if (X == 0 || !last) give_turn(turn + 4 * (X ^ 1));
+  if (!waited) wait(&sh.pv_done[X], (k - 1) & 1);
   tmem_st32(s + 128, w[0]);
   tmem_st32(s + 160, w[1]);
   float x, y;
@@ -415,7 +456,6 @@ __device__ __forceinline__ bool soften(const CachePromptLaunch& a, PromptShared&
   tc_fence_before();
   __syncwarp();
   if (lane == 0) mbar_arrive(&sh.p_full[X]);
-  return true;
 }
 
 // Values that scrub took out, of tokens that this row sees, in dims d0 .. d0 + 31 (an infinity, or a NaN, whatever
@@ -523,9 +563,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   unsigned char* q = prompt_smem + ((1024 - (smem_u32(prompt_smem) & 1023)) & 1023);
   unsigned char* stages = q + 2 * kTileBytes;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kPStages; ++i) {
+    for (int i = 0; i < PCfg<KIND>::kStages; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], 2);
+      mbar_init(&sh.empty[i], 1);
     }
     for (int X = 0; X < 2; ++X) {
       mbar_init(&sh.s_full[X], 1);
@@ -534,7 +574,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_init(&sh.pv_done[X], 1);
       mbar_init(&sh.drain[X], 1);
     }
-    for (int i = 0; i < kLoadWarps; ++i) mbar_init(&sh.landed[i], 1);
+    for (int i = 0; i < 2 * kLoadWarps; ++i) mbar_init(&sh.landed[i >> 1][i & 1], 1);
     mbar_fence_init();
     sh.abort = sh.odd = sh.bad = 0;
     sh.lo_min = sh.hi_min = INT_MAX;
@@ -584,7 +624,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   u.i0 = sh.lo_min < sh.hi_max ? sh.lo_min / kKeys : 0;
   u.i1 = sh.lo_min < sh.hi_max ? (sh.hi_max + kKeys - 1) / kKeys : 0;
   bool ok = true;
-  unsigned next = 0;  // one past the last tile that this loading warp has asked for
+  unsigned next = 0;  // what this loading warp has asked for
   const int n = u.i1 - u.i0;
   if (warp < kSoftWarps) {
     const int X = warp >> 2;
@@ -600,7 +640,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
     }
     bool two_step = false;
-    for (int x = 0; x < n && ok; ++x) ok = soften<KIND, SCORED>(a, sh, r, s, X, lane, u.i0 + x, x, two_step);
+    const int turn = 1 + (warp & 3);
+    if (X == 1 && n > 0) give_turn(turn);
+    for (int x = 0; x < n; ++x)
+      soften<KIND, SCORED>(a, sh, r, s, X, lane, turn, x + 1 == n, u.i0 + x, x, two_step, ok);
     if (ok && n > 0) ok = __all_sync(kFull, mbar_wait(&sh.pv_done[X], (n - 1) & 1, &sh.abort));
     if (ok) {
       tc_fence_after();
@@ -624,10 +667,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       tc_fence_before();
     }
   } else if (warp < kSoftWarps + kLoadWarps) {
-    ok = load_tiles<KIND>(a, &map, u, sh, stages, warp - kSoftWarps, lane, next);
+    const int w = warp - kSoftWarps;
+    if constexpr (KIND == PISA_CACHE_BF16)
+      ok = load_bf16(a, &map, u, sh, stages, w, lane, next);
+    else
+      ok = load_e2m1(a, u, sh, stages, stages + 2 * PCfg<KIND>::kStages * kTileBytes + 2 * w * kRawBytes, w, lane, next);
   } else if (lane == 0) {
     const int Y = warp - kSoftWarps - kLoadWarps;
-    ok = multiply<KIND>(u, sh, q, stages, Y);
+    ok = Y == 0 ? multiply_s<KIND>(u, sh, q, stages) : multiply_v<KIND>(u, sh, stages);
     if (!ok && n > 0) {  // its products end before tensor memory is given back
       umma_commit(&sh.drain[Y]);
       mbar_wait(&sh.drain[Y], 0, nullptr);
@@ -638,10 +685,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     set_status(a.status, PISA_ERR_DEVICE_TIMEOUT);
   }
   __syncthreads();
-  if (KIND == PISA_CACHE_BF16 && sh.abort && warp >= kSoftWarps && warp < kSoftWarps + kLoadWarps && lane == 0) {
+  if (sh.abort && warp >= kSoftWarps && warp < kSoftWarps + kLoadWarps && lane == 0) {
     // given up: copies that are still on their way land before the shared memory is let go
-    for (unsigned k = next > kPStages ? next - kPStages : 0; k < next; ++k)
-      if (k % kLoadWarps == (unsigned)(warp - kSoftWarps)) mbar_wait(&sh.full[k % kPStages], (k / kPStages) & 1, nullptr);
+    constexpr unsigned kPStages = PCfg<KIND>::kStages;
+    const int w = warp - kSoftWarps;
+    if (KIND == PISA_CACHE_BF16) {
+      for (unsigned k = next > kPStages ? next - kPStages : 0; k < next; ++k)
+        if (k % kLoadWarps == (unsigned)w) mbar_wait(&sh.full[k % kPStages], (k / kPStages) & 1, nullptr);
+    } else {
+      for (unsigned x = next > 2 ? next - 2 : 0; x < next; ++x) mbar_wait(&sh.landed[w][x & 1], (x >> 1) & 1, nullptr);
+    }
   }
   __syncthreads();
   if (warp == kSoftWarps + kLoadWarps) tmem_dealloc<512>(sh.tmem);
@@ -681,7 +734,7 @@ static cudaError_t launch_prompt(const CachePromptLaunch& L, cudaStream_t s) {
   const long long units = (long long)row_tiles * L.cache.B * L.cache.Hkv;
   CUtensorMap map{};
   if (KIND == PISA_CACHE_BF16 && !map_pages(&map, L.cache)) return cudaErrorInvalidValue;
-  return launch_early<cache_prompt_kernel<KIND, SCORED>>((unsigned)units, kPromptThreads, kPromptSmem, s, map, L, g_shift,
+  return launch_early<cache_prompt_kernel<KIND, SCORED>>((unsigned)units, kPromptThreads, PCfg<KIND>::kSmem, s, map, L, g_shift,
                                                          row_tiles);
 }
 
