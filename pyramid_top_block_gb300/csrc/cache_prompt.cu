@@ -62,9 +62,12 @@ struct PromptShared {
 };
 
 // What of a CTA's rows a warp needs to know.
+// Key tiles go from the last to the first: where a bias by distance grows towards a row's own position, the first
+// tile then has the largest logits, and the reference stays.
 struct PromptUnit {
   int b, kv, r0;   // rows r0 .. r0 + 255 of (b, kv)
   int i0, i1;      // key tiles
+  __device__ __forceinline__ int tile(int k) const { return i1 - 1 - k; }  // the k-th
   // whether some row does not see some key of the tile
   __device__ __forceinline__ bool mixed(const PromptShared& sh, int tile) const {
     return tile * kKeys < sh.lo_max || (tile + 1) * kKeys > sh.hi_min;
@@ -74,11 +77,11 @@ struct PromptUnit {
 // ------------------------------------------------------------------------------------------------ loading
 
 // A loading warp takes every second tile, whole.  The pages of its tiles' records, four tiles ahead: lane l has record l % 8
-// (of 8, 4 or 2) of tile first + 2 (l / 8).  n_pages: no row sees any of it, or its page is out of range (noted); its
+// (of 8, 4 or 2) of the tile number first + 2 (l / 8).  n_pages: no row sees any of it, or its page is out of range (noted); its
 // keys and values become zeros.
 __device__ __forceinline__ int look(const CachePromptLaunch& a, const PromptUnit& u, PromptShared& sh, int lane, int first) {
-  const int tile = first + kLoadWarps * (lane >> 3), U = 1 << a.cache.rec_shift, key = tile * kKeys + U * (lane & 7);
-  if (U * (lane & 7) >= kKeys || tile >= u.i1 || key >= sh.hi_max || key + U <= sh.lo_min) return a.cache.n_pages;
+  const int tile = u.tile(first + kLoadWarps * (lane >> 3)), U = 1 << a.cache.rec_shift, key = tile * kKeys + U * (lane & 7);
+  if (U * (lane & 7) >= kKeys || tile < u.i0 || key >= sh.hi_max || key + U <= sh.lo_min) return a.cache.n_pages;
   const int page = a.cache.table[(long long)u.b * a.cache.max_pages + (key >> a.cache.page_shift)];
   if (page >= 0 && page < a.cache.n_pages) return page;
   sh.bad = 1;
@@ -141,9 +144,11 @@ __device__ __forceinline__ bool load_bf16(const CachePromptLaunch& a, const CUte
   bool ok = true;
   int page = 0, mine = 0;
   unsigned landings = 0;
-  for (int tile = u.i0 + warp; tile < u.i1; tile += kLoadWarps, ++mine) {
-    const unsigned k = tile - u.i0, st = k % kPStages;
-    if (mine % 4 == 0) page = look(a, u, sh, lane, tile);
+  const unsigned n = u.i1 - u.i0;
+  for (unsigned k = warp; k < n; k += kLoadWarps, ++mine) {
+    const unsigned st = k % kPStages;
+    const int tile = u.tile(k);
+    if (mine % 4 == 0) page = look(a, u, sh, lane, k);
     if (k >= kPStages) ok = mbar_wait(&sh.empty[st], (k / kPStages - 1) & 1, &sh.abort);
     ok = __all_sync(kFull, ok);
     if (!ok) break;
@@ -187,8 +192,8 @@ __device__ __forceinline__ bool load_e2m1(const CachePromptLaunch& a, const Prom
   bool ok = true;
   // asks for the records of the warp's tile number x
   const auto ask = [&](int x) {
-    const int tile = u.i0 + warp + kLoadWarps * x;
-    if (x % 4 == 0) page_next = look(a, u, sh, lane, tile);
+    const int k = warp + kLoadWarps * x, tile = u.tile(k);
+    if (x % 4 == 0) page_next = look(a, u, sh, lane, k);
     const int from = __shfl_sync(kFull, page_next, ((x % 4) * 8 + lane) & 31);
     const bool there = lane < kKeys >> rs && from < a.cache.n_pages;
     const uint32_t bytes = __popc(__ballot_sync(kFull, there)) * rec_bytes;
@@ -201,11 +206,13 @@ __device__ __forceinline__ bool load_e2m1(const CachePromptLaunch& a, const Prom
     next = x + 1;
   };
   int x = 0;
-  if (u.i0 + warp < u.i1) ask(0);
-  for (int tile = u.i0 + warp; tile < u.i1; tile += kLoadWarps, ++x) {
-    const unsigned k = tile - u.i0, st = k % kPStages;
+  const unsigned n = u.i1 - u.i0;
+  if (warp < (int)n) ask(0);
+  for (unsigned k = warp; k < n; k += kLoadWarps, ++x) {
+    const unsigned st = k % kPStages;
+    const int tile = u.tile(k);
     if (x % 4 == 0) page = page_next;
-    if (tile + kLoadWarps < u.i1) ask(x + 1);
+    if (k + kLoadWarps < n) ask(x + 1);
     if (k >= kPStages) ok = mbar_wait(&sh.empty[st], (k / kPStages - 1) & 1, &sh.abort);
     ok = ok && mbar_wait(&sh.landed[warp][x & 1], (x >> 1) & 1, &sh.abort);
     ok = __all_sync(kFull, ok);
@@ -312,7 +319,8 @@ struct PromptRow {
   bool there;       // whether the row exists
   float f;          // logit factor
   float m, l;       // reference and sum of weights
-  float slope, dref;  // bias by distance, base 2, relative to the nearest token that is seen
+  float slope;      // bias by distance, base 2
+  int nearest;      // the token in sight that is nearest to the row's position
   CapRow cap;
 };
 
@@ -342,9 +350,9 @@ __device__ __forceinline__ void logits(const CachePromptLaunch& a, const PromptR
       for (int i = 0; i < kKeys; ++i) v[i] *= r.f;
     }
     if (a.score.slopes) {  // -slope (|p - j| - |p - nearest|): whole numbers, exact up to 2^24
-      const float d0 = (float)(key0 - r.pos);
+      const float d0 = (float)(key0 - r.pos), least = (float)abs(r.pos - r.nearest);
 #pragma unroll
-      for (int i = 0; i < kKeys; ++i) v[i] = fmaf(-r.slope, fabsf(d0 + (float)i) - r.dref, v[i]);
+      for (int i = 0; i < kKeys; ++i) v[i] = fmaf(-r.slope, fabsf(d0 + (float)i) - least, v[i]);
     }
   } else if (two_step) {
 #pragma unroll
@@ -367,45 +375,56 @@ __device__ __forceinline__ float max_of(const float (&v)[kKeys]) {
   return fmaxf(b0, b1);
 }
 
-// The exponentials of the two row tiles take turns: the warps of one tile that share a scheduler (named barriers 1 .. 4
-// for the first tile, 5 .. 8 for the second) let those of the other one begin when theirs are done.  Left to themselves
-// both tiles compute them at the same time, each at half the rate, and then both wait for the rest.
-__device__ __forceinline__ void take_turn(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ void give_turn(int id) { asm volatile("barrier.cta.arrive %0, 64;" ::"r"(id) : "memory"); }
-
 // The softmax of one key tile for the warp's 32 rows.  s: the tensor memory columns of the row tile at the warp's lanes.
-// ok becomes false if a wait ran out; what follows goes on without waiting, so that no other warp is left at a barrier.
 template <int KIND, bool SCORED>
-__device__ __forceinline__ void soften(const CachePromptLaunch& a, PromptShared& sh, PromptRow& r, uint32_t s, int X,
-                                       int lane, int turn, bool last, int tile, unsigned k, bool& two_step, bool& ok) {
+__device__ __forceinline__ bool soften(const CachePromptLaunch& a, PromptShared& sh, PromptRow& r, uint32_t s, int X,
+                                       int lane, int tile, unsigned k, bool& two_step) {
   using C = PCfg<KIND>;
   const int key0 = tile * kKeys;
   // (rows that see nothing do not matter: they get zeros at the end, or do not exist)
   const bool whole = __all_sync(kFull, r.lo >= r.hi || (r.lo <= key0 && r.hi >= key0 + kKeys));
-  const auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (ok) ok = __all_sync(kFull, mbar_wait(bar, parity, &sh.abort));
-    tc_fence_after();
-  };
-  wait(&sh.s_full[X], k & 1);
+  if (!__all_sync(kFull, mbar_wait(&sh.s_full[X], k & 1, &sh.abort))) return false;
+  tc_fence_after();
   float v[kKeys], b;
   tmem_ld128_top<SCORED>(s, v, b);
+  const float size = b;  // (if SCORED: the largest magnitude)
   tc_fence_before();
   __syncwarp();
   if (lane == 0) mbar_arrive(&sh.s_free[X]);  // S is in registers: the next product may overwrite it
   float ff = SCORED || two_step ? 1.f : r.f;
-  if (SCORED || two_step || !whole) {
-    logits<SCORED>(a, r, key0, whole, two_step, b, v);
+  // Scores that need no mask become logits in the step that takes the reference off (weights): a cap by its
+  // polynomial, a bias by a line, for keys that no row of the warp lies before.  b: at least the largest logit.
+  bool capped = false, line = false;
+  const float bias = r.slope * (float)(key0 - r.nearest);  // of the tile's first key, relative to the nearest one
+  if constexpr (SCORED) {
+    const bool cap = a.score.cap > 0.f, slopes = a.score.slopes != nullptr;
+    capped = whole && cap && !slopes && !__any_sync(kFull, b * r.cap.to_y > 1.f);
+    line = whole && slopes && !cap && !__any_sync(kFull, key0 + kKeys > r.pos + 1 && r.lo < r.hi);
+  }
+  if (capped)
+    b = cap_any(b, r.cap, 0.f);
+  else if (line)
+    b = fmaf(b, r.f, fmaxf(bias, fmaf(r.slope, (float)(kKeys - 1), bias)));
+  else if (SCORED || two_step || !whole) {
+    logits<SCORED>(a, r, key0, whole, two_step, size, v);
     b = max_of(v);
   }
-  b = __fmul_rn(b, ff);
+  if (!SCORED) b = __fmul_rn(b, ff);
   bool waited = k == 0;  // for the product before, which reads P and writes O
   // A row's reference m is set anew only when a logit passes it by more than kTop, so that few tiles rescale O.
   if (__any_sync(kFull, b > r.m + C::kTop)) {
+    if (capped) b = cap_any(max_of(v), r.cap, 0.f);  // (the cap keeps the order)
+    if (line) {
+      b = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i) b = fmaxf(b, fmaf(v[i], r.f, fmaf(r.slope, (float)i, bias)));
+    }
     // (a step of 32 bits is too coarse for the shift from 2^24 on; nothing that it is for is left there)
     const float n = fmaxf(r.m, fabsf(b) < 16.f * kFar ? b - C::kShift : b);
     const float f = ex2_approx(r.m - n);
     if (k > 0) {
-      wait(&sh.pv_done[X], (k - 1) & 1);
+      if (!__all_sync(kFull, mbar_wait(&sh.pv_done[X], (k - 1) & 1, &sh.abort))) return false;
+      tc_fence_after();
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         uint32_t o[32];
@@ -427,28 +446,55 @@ __device__ __forceinline__ void soften(const CachePromptLaunch& a, PromptShared&
       ff = 1.f;
     }
   }
-  take_turn(turn + 4 * X);
-  const unsigned long long f2 = f2_pack(ff, ff);
-  unsigned long long m2 = f2_pack(-r.m, -r.m), s0 = 0, s1 = 0;
-  asm volatile("" : "+l"(m2));  // (nothing that uses it moves ahead of the turn)
-  uint32_t w[2][32];
-#pragma unroll
-  for (int i = 0; i < kKeys / 2; ++i) {
+  const unsigned long long m2 = f2_pack(-r.m, -r.m);
+  unsigned long long s0 = 0, s1 = 0;
+  uint32_t w[32];
+  bool ok = true;
+  // Weights of a pair from their base-2 logits less the reference, their sum and their form for the product,
+  // stored half a tile at a time.  (The product before may still read the last tile's weights when the first are ready.)
+  const auto weigh2 = [&](int i, unsigned long long t) {
     float x, y;
-    f2_unpack(f2_fma(f2_pack(v[2 * i], v[2 * i + 1]), f2, m2), x, y);
+    f2_unpack(t, x, y);
     x = ex2_approx(x);
     y = ex2_approx(y);
     if (i & 1)
       s1 = f2_add(s1, f2_pack(x, y));
     else
       s0 = f2_add(s0, f2_pack(x, y));
-    w[i >> 5][i & 31] = KIND == PISA_CACHE_BF16 ? pack_bf16x2(x, y) : pack_f16x2(x, y);
+    w[i & 31] = KIND == PISA_CACHE_BF16 ? pack_bf16x2(x, y) : pack_f16x2(x, y);
+    if (i == 31 && !waited) {
+      ok = __all_sync(kFull, mbar_wait(&sh.pv_done[X], (k - 1) & 1, &sh.abort));
+      tc_fence_after();
+    }
+    if ((i & 31) == 31) tmem_st32(s + 128 + (i & 32), w);
+  };
+  if (SCORED && capped) {
+    const unsigned long long fy = f2_pack(r.cap.to_y, r.cap.to_y), fl = f2_pack(r.cap.to_l, r.cap.to_l);
+    if (__any_sync(kFull, size * r.cap.to_y > 0.5f)) {
+#pragma unroll
+      for (int i = 0; i < kKeys / 2; ++i) {
+        const unsigned long long x = f2_pack(v[2 * i], v[2 * i + 1]);
+        weigh2(i, f2_fma(f2_mul(x, fl), tanh_ratio<Tanh>(f2_mul(x, fy)), m2));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kKeys / 2; ++i) {
+        const unsigned long long x = f2_pack(v[2 * i], v[2 * i + 1]);
+        weigh2(i, f2_fma(f2_mul(x, fl), tanh_ratio<TanhHalf>(f2_mul(x, fy)), m2));
+      }
+    }
+  } else if (SCORED && line) {
+    const unsigned long long f2 = f2_pack(r.f, r.f), sl = f2_pack(r.slope, r.slope);
+    const unsigned long long c = f2_add(m2, f2_pack(bias, bias));
+#pragma unroll
+    for (int i = 0; i < kKeys / 2; ++i)
+      weigh2(i, f2_fma(f2_pack(v[2 * i], v[2 * i + 1]), f2, f2_fma(sl, f2_pack(2.f * i, 2.f * i + 1.f), c)));
+  } else {
+    const unsigned long long f2 = f2_pack(ff, ff);
+#pragma unroll
+    for (int i = 0; i < kKeys / 2; ++i) weigh2(i, f2_fma(f2_pack(v[2 * i], v[2 * i + 1]), f2, m2));
   }
-  asm volatile("" : "+l"(s0), "+l"(s1));
-  if (X == 0 || !last) give_turn(turn + 4 * (X ^ 1));
-  if (!waited) wait(&sh.pv_done[X], (k - 1) & 1);
-  tmem_st32(s + 128, w[0]);
-  tmem_st32(s + 160, w[1]);
+  if (!ok) return false;
   float x, y;
   f2_unpack(f2_add(s0, s1), x, y);
   r.l += x + y;
@@ -456,6 +502,7 @@ __device__ __forceinline__ void soften(const CachePromptLaunch& a, PromptShared&
   tc_fence_before();
   __syncwarp();
   if (lane == 0) mbar_arrive(&sh.p_full[X]);
+  return true;
 }
 
 // Values that scrub took out, of tokens that this row sees, in dims d0 .. d0 + 31 (an infinity, or a NaN, whatever
@@ -636,14 +683,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       r.f *= kLog2e;
       if (a.score.slopes && r.there) {
         r.slope = a.score.slopes[r.head] * kLog2e;
-        r.dref = (float)abs(r.pos - max(min(r.pos, r.hi - 1), r.lo));
+        r.nearest = max(min(r.pos, r.hi - 1), r.lo);
       }
     }
     bool two_step = false;
-    const int turn = 1 + (warp & 3);
-    if (X == 1 && n > 0) give_turn(turn);
-    for (int x = 0; x < n; ++x)
-      soften<KIND, SCORED>(a, sh, r, s, X, lane, turn, x + 1 == n, u.i0 + x, x, two_step, ok);
+    for (int x = 0; x < n && ok; ++x) ok = soften<KIND, SCORED>(a, sh, r, s, X, lane, u.tile(x), x, two_step);
     if (ok && n > 0) ok = __all_sync(kFull, mbar_wait(&sh.pv_done[X], (n - 1) & 1, &sh.abort));
     if (ok) {
       tc_fence_after();

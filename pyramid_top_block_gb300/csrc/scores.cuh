@@ -17,18 +17,33 @@ struct ScoreDev {
   int window;           // a query sees tokens p - window + 1 and later
 };
 
-// tanh(y) / y as a polynomial in u = y y on 0 .. 1: the interpolation at the Chebyshev nodes of degree 6, off by
-// at most 6.0e-8 of the value (a rounding to 32 bits).  It costs 7 multiply-adds for two scores together and no
-// exponential, where 1 - 2 / (1 + e^(2 y)) takes two slow instructions each and loses small scores' last bits.
+// tanh(y) / y as polynomials in u = y y: the interpolations at the Chebyshev nodes, of degree 6 on |y| <= 1, off by at
+// most 6.0e-8 of the value (a rounding to 32 bits), and of degree 3 on |y| <= 1/2 (5.6e-07).  One minus twice the
+// reciprocal of 1 + e^(2 y) would take two slow instructions a score, and loses small scores' last bits.
 struct Tanh {
-  float c[7] = {0x1.fffffep-1f, -0x1.555402p-2f, 0x1.10e5c6p-3f, -0x1.b5e03ap-5f,
+  static constexpr int n = 7;
+  float c[n] = {0x1.fffffep-1f, -0x1.555402p-2f, 0x1.10e5c6p-3f, -0x1.b5e03ap-5f,
                 0x1.4c4342p-6f, -0x1.95f386p-8f, 0x1.101cb0p-10f};
 };
-
+struct TanhHalf {
+  static constexpr int n = 4;
+  float c[n] = {0x1.ffffeep-1f, -0x1.5542dap-2f, 0x1.0e2146p-3f, -0x1.6baa52p-5f};
+};
 __device__ __forceinline__ unsigned long long f2_mul(unsigned long long a, unsigned long long b) {
   unsigned long long d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+
+// tanh(y) / y of two values.
+template <typename P>
+__device__ __forceinline__ unsigned long long tanh_ratio(unsigned long long y) {
+  constexpr P k;
+  const unsigned long long u = f2_mul(y, y);
+  unsigned long long q = f2_pack(k.c[P::n - 1], k.c[P::n - 1]);
+#pragma unroll
+  for (int i = P::n - 2; i >= 0; --i) q = f2_fma(q, u, f2_pack(k.c[i], k.c[i]));
+  return q;
 }
 
 // Factors of a row: y = score * to_y (to the cap's units), logit = score * to_l tanh(y) / y.
@@ -38,12 +53,8 @@ struct CapRow {
 
 // Two scores with |y| <= 1, capped.
 __device__ __forceinline__ void cap_small(float& a, float& b, const CapRow& r) {
-  const unsigned long long x = f2_pack(a, b), y = f2_mul(x, f2_pack(r.to_y, r.to_y)), u = f2_mul(y, y);
-  constexpr Tanh k;
-  unsigned long long q = f2_pack(k.c[6], k.c[6]);
-#pragma unroll
-  for (int i = 5; i >= 0; --i) q = f2_fma(q, u, f2_pack(k.c[i], k.c[i]));
-  f2_unpack(f2_mul(f2_mul(x, f2_pack(r.to_l, r.to_l)), q), a, b);
+  const unsigned long long x = f2_pack(a, b);
+  f2_unpack(f2_mul(f2_mul(x, f2_pack(r.to_l, r.to_l)), tanh_ratio<Tanh>(f2_mul(x, f2_pack(r.to_y, r.to_y)))), a, b);
 }
 
 // One score of any size, capped; top = cap log2 e.  An infinity gives plus or minus top, a NaN a NaN.
