@@ -118,7 +118,10 @@ size_t pisa_cache_page_bytes(int page_size, int Hkv, int kind) {
   return (size_t)page_size * Hkv * (kind == PISA_CACHE_BF16 ? kRowBf16 : kRowE2m1);
 }
 
-size_t pisa_cache_workspace_bytes(void) { return kCacheStatusBytes + cache_part_bytes(); }
+size_t pisa_cache_workspace_bytes(void) {
+  const size_t a = cache_part_bytes(), b = cache_prompt_part_bytes();
+  return kCacheStatusBytes + (a > b ? a : b);
+}
 
 static int cache_append(const pisa_paged_cache* cache, int T, const pisa_rows* q, int Hq, const pisa_rows* k,
                       const pisa_rows* v, const int32_t* start, const int32_t* counts, const float* rotary,
@@ -263,7 +266,10 @@ int pisa_cache_prompt_attention(const pisa_paged_cache* cache, const pisa_rows* 
   L.last = last;
   L.out = static_cast<__nv_bfloat16*>(out);
   L.status = static_cast<int*>(ws);
-  L.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kCacheStatusBytes);
+  L.plan.piece = reinterpret_cast<PromptPiece*>(static_cast<char*>(ws) + kCacheStatusBytes);
+  L.plan.cut = reinterpret_cast<int2*>(L.plan.piece + kPromptUnits + kPromptRuns);
+  L.plan.tiles = reinterpret_cast<int32_t*>(L.plan.cut + kPromptRuns);
+  L.part = reinterpret_cast<float*>(L.plan.tiles + kPromptUnits);
   return cuda_code(launch_cache_prompt(L, static_cast<cudaStream_t>(stream)));
 }
 

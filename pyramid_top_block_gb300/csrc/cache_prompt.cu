@@ -20,6 +20,14 @@
 
 namespace pisa {
 
+// Where there are few row tiles of a CTA (units) for their length, the key tiles of all units form one stream that is cut into
+// runs of equal length, one for each SM, and where a unit ends: a CTA takes a piece, the longest first.  Units in
+// several pieces leave partial results, which a last kernel joins (takes_stream says when).  (A CTA for a run, with a loop
+// over its pieces, was slower: the loop costs the softmax the registers that hold its scores, 138 -> 233 us for 1216
+// tokens at 16384.)
+constexpr int kRuns = kPromptRuns, kMaxUnits = kPromptUnits;
+constexpr int kUnitEnd = 4;            // places of the stream that a unit counts beside its tiles: what its begin and end cost
+constexpr int kPartRow = 66;           // a partial result, for each of 256 rows: O [64], reference, sum of weights
 constexpr int kRowsTile = 128, kRowsCta = 256, kKeys = 128;
 constexpr int kSoftWarps = 8, kLoadWarps = 2, kPromptThreads = (kSoftWarps + kLoadWarps + 2) * 32;
 constexpr int kTileBytes = kKeys * kD * 2;  // keys or values of a tile: rows of 128 bytes, 128-byte swizzle
@@ -51,6 +59,21 @@ __device__ __forceinline__ uint64_t umma_desc_mn128(uint32_t addr) {
   return (uint64_t)((addr >> 4) & 0x3fff) | (64ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
 
+// Key tiles go from the last to the first: where a bias by distance grows towards a row's own position, the first
+// tile then has the largest logits, and the reference stays.
+struct PromptUnit {
+  int b, kv, r0;   // rows r0 .. r0 + 255 of (b, kv)
+  int i0, i1;      // key tiles that this CTA takes
+  __device__ __forceinline__ unsigned n() const { return i1 - i0; }
+  __device__ __forceinline__ int tile(int k) const { return i1 - 1 - k; }  // the k-th
+};
+
+// What a loading warp has asked for.
+struct Asked {
+  unsigned count;   // waits on its own landing barrier (bf16), raw buffers (4 bits)
+  unsigned stages;  // bf16: bit i: stage i, bit 8 + i: the parity of the phase in which that lands
+};
+
 struct PromptShared {
   uint64_t full[5], empty[5];
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], drain[2];
@@ -58,21 +81,18 @@ struct PromptShared {
   uint32_t tmem;
   int abort, odd, bad;
   int lo_min, lo_max, hi_min, hi_max;  // of the rows that see anything
+  Asked asked[kLoadWarps];
+  // what the softmax needs at its end alone (its registers are full of scores)
+  PromptUnit unit;
+  int slot;
   float factor[kRowsCta];              // 4-bit pages: the rows' logit factors
 };
 
 // What of a CTA's rows a warp needs to know.
-// Key tiles go from the last to the first: where a bias by distance grows towards a row's own position, the first
-// tile then has the largest logits, and the reference stays.
-struct PromptUnit {
-  int b, kv, r0;   // rows r0 .. r0 + 255 of (b, kv)
-  int i0, i1;      // key tiles
-  __device__ __forceinline__ int tile(int k) const { return i1 - 1 - k; }  // the k-th
-  // whether some row does not see some key of the tile
-  __device__ __forceinline__ bool mixed(const PromptShared& sh, int tile) const {
-    return tile * kKeys < sh.lo_max || (tile + 1) * kKeys > sh.hi_min;
-  }
-};
+// Whether some row of the CTA does not see some key of the tile.
+__device__ __forceinline__ bool mixed_tile(const PromptShared& sh, int tile) {
+  return tile * kKeys < sh.lo_max || (tile + 1) * kKeys > sh.hi_min;
+}
 
 // ------------------------------------------------------------------------------------------------ loading
 
@@ -136,24 +156,21 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-// bf16 pages by TMA.  next: one past the last tile asked for.
+// bf16 pages by TMA.
 __device__ __forceinline__ bool load_bf16(const CachePromptLaunch& a, const CUtensorMap* map, const PromptUnit& u,
-                                          PromptShared& sh, unsigned char* stages, int warp, int lane, unsigned& next) {
+                                          PromptShared& sh, unsigned char* stages, int warp, int lane) {
   constexpr unsigned kPStages = PCfg<PISA_CACHE_BF16>::kStages;
+  Asked asked = {0, 0};
   const int rs = a.cache.rec_shift;
-  bool ok = true;
   int page = 0, mine = 0;
-  unsigned landings = 0;
-  const unsigned n = u.i1 - u.i0;
-  for (unsigned k = warp; k < n; k += kLoadWarps, ++mine) {
+  for (unsigned k = warp; k < u.n(); k += kLoadWarps, ++mine) {
     const unsigned st = k % kPStages;
     const int tile = u.tile(k);
     if (mine % 4 == 0) page = look(a, u, sh, lane, k);
-    if (k >= kPStages) ok = mbar_wait(&sh.empty[st], (k / kPStages - 1) & 1, &sh.abort);
-    ok = __all_sync(kFull, ok);
-    if (!ok) break;
+    const bool ok = k < kPStages || mbar_wait(&sh.empty[st], (k / kPStages - 1) & 1, &sh.abort);
+    if (!__all_sync(kFull, ok)) return false;
     unsigned char* stage = stages + st * 2 * kTileBytes;
-    const bool mixed = u.mixed(sh, tile);
+    const bool mixed = mixed_tile(sh, tile);
     // lane 2 i + h: the keys (h = 0) or values of record i; a page number of n_pages lies outside the map and gives zeros
     uint64_t* bar = mixed ? &sh.landed[warp][0] : &sh.full[st];
     if (lane == 0) mbar_expect_tx(bar, 2 * kTileBytes);
@@ -165,31 +182,30 @@ __device__ __forceinline__ bool load_bf16(const CachePromptLaunch& a, const CUte
                   (((u.kv << (a.cache.page_shift - rs)) + rec) << 1) + h, from, bar);
     }
     if (mixed) {
-      ok = __all_sync(kFull, mbar_wait(bar, landings & 1, &sh.abort));
-      if (!ok) {  // (given up; the copies land first)
-        mbar_wait(bar, landings & 1, nullptr);
-        break;
+      if (!__all_sync(kFull, mbar_wait(bar, asked.count & 1, &sh.abort))) {
+        mbar_wait(bar, asked.count & 1, nullptr);  // (given up; the copies land first)
+        return false;
       }
-      ++landings;
+      ++asked.count;
       scrub(sh, stage + kTileBytes, tile, lane);
       fence_async_proxy();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.full[st]);
     }
-    next = k + 1;
+    asked.stages = (asked.stages & ~(0x100u << st)) | (1u << st) | (((k / kPStages) & 1) << (8 + st));
+    if (lane == 0) sh.asked[warp] = asked;
   }
-  return ok;
+  return true;
 }
 
 // 4-bit pages: records by bulk copies into one of the warp's two raw buffers, a tile ahead; from there as fp16 into the stage,
-// a token a lane.  next: raw buffers asked for.
+// a token a lane.
 __device__ __forceinline__ bool load_e2m1(const CachePromptLaunch& a, const PromptUnit& u, PromptShared& sh,
-                                          unsigned char* stages, unsigned char* raw, int warp, int lane, unsigned& next) {
+                                          unsigned char* stages, unsigned char* raw, int warp, int lane) {
   constexpr unsigned kPStages = PCfg<PISA_CACHE_E2M1>::kStages;
   const int rs = a.cache.rec_shift, U = 1 << rs;
   const uint32_t rec_bytes = U * kRowE2m1;
   int page = 0, page_next = 0;
-  bool ok = true;
   // asks for the records of the warp's tile number x
   const auto ask = [&](int x) {
     const int k = warp + kLoadWarps * x, tile = u.tile(k);
@@ -203,21 +219,19 @@ __device__ __forceinline__ bool load_e2m1(const CachePromptLaunch& a, const Prom
     if (there)
       bulk_load(raw + (x & 1) * kRawBytes + lane * rec_bytes,
                 a.cache.pages + cache_record(a.cache, kRowE2m1, from, u.kv, tile * kKeys + (lane << rs)), rec_bytes, bar);
-    next = x + 1;
+    if (lane == 0) sh.asked[warp].count = x + 1;
   };
   int x = 0;
-  const unsigned n = u.i1 - u.i0;
-  if (warp < (int)n) ask(0);
-  for (unsigned k = warp; k < n; k += kLoadWarps, ++x) {
+  if (warp < (int)u.n()) ask(0);
+  for (unsigned k = warp; k < u.n(); k += kLoadWarps, ++x) {
     const unsigned st = k % kPStages;
     const int tile = u.tile(k);
     if (x % 4 == 0) page = page_next;
-    if (k + kLoadWarps < n) ask(x + 1);
-    if (k >= kPStages) ok = mbar_wait(&sh.empty[st], (k / kPStages - 1) & 1, &sh.abort);
+    if (k + kLoadWarps < u.n()) ask(x + 1);
+    bool ok = k < kPStages || mbar_wait(&sh.empty[st], (k / kPStages - 1) & 1, &sh.abort);
     ok = ok && mbar_wait(&sh.landed[warp][x & 1], (x >> 1) & 1, &sh.abort);
-    ok = __all_sync(kFull, ok);
-    if (!ok) break;
-    const bool mixed = u.mixed(sh, tile);
+    if (!__all_sync(kFull, ok)) return false;
+    const bool mixed = mixed_tile(sh, tile);
     unsigned char* stage = stages + st * 2 * kTileBytes;
 #pragma unroll 2
     for (int j = 0; j < 4; ++j) {
@@ -258,20 +272,19 @@ __device__ __forceinline__ bool load_e2m1(const CachePromptLaunch& a, const Prom
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.full[st]);
   }
-  return ok;
+  return true;
 }
 
 // ------------------------------------------------------------------------------------------------ the MMA warps
 
 // One thread issues the S products of both row tiles, another one the products with V: issuing takes as long as the
-// products themselves, so that one thread for both would hold the next S back behind a product with V (158 -> XXX us).
+// products themselves, so that one thread for both would hold the next S back behind a product with V.
 template <int KIND>
 __device__ __forceinline__ bool multiply_s(const PromptUnit& u, PromptShared& sh, const unsigned char* q,
                                            const unsigned char* stages) {
   constexpr unsigned kPStages = PCfg<KIND>::kStages;
-  const unsigned n = u.i1 - u.i0;
   const uint64_t dq = umma_desc_sw128(q);
-  for (unsigned k = 0; k < n; ++k) {
+  for (unsigned k = 0; k < u.n(); ++k) {
     const unsigned st = k % kPStages;
     if (!mbar_wait(&sh.full[st], (k / kPStages) & 1, &sh.abort)) return false;
     const uint64_t dk = umma_desc_sw128(stages + st * 2 * kTileBytes);
@@ -291,8 +304,7 @@ __device__ __forceinline__ bool multiply_s(const PromptUnit& u, PromptShared& sh
 template <int KIND>
 __device__ __forceinline__ bool multiply_v(const PromptUnit& u, PromptShared& sh, const unsigned char* stages) {
   constexpr unsigned kPStages = PCfg<KIND>::kStages;
-  const unsigned n = u.i1 - u.i0;
-  for (unsigned k = 0; k < n; ++k) {
+  for (unsigned k = 0; k < u.n(); ++k) {
     const unsigned st = k % kPStages;
     if (!mbar_wait(&sh.full[st], (k / kPStages) & 1, &sh.abort)) return false;
     const uint64_t dv = umma_desc_mn128(smem_u32(stages + st * 2 * kTileBytes + kTileBytes));
@@ -314,14 +326,14 @@ __device__ __forceinline__ bool multiply_v(const PromptUnit& u, PromptShared& sh
 // ------------------------------------------------------------------------------------------------ softmax
 
 struct PromptRow {
-  int lo, hi, pos;  // the row's span (empty where lo >= hi) and position
-  int head, t;
-  bool there;       // whether the row exists
+  int lo, hi;       // the row's span (empty where lo >= hi)
   float f;          // logit factor
   float m, l;       // reference and sum of weights
-  float slope;      // bias by distance, base 2
-  int nearest;      // the token in sight that is nearest to the row's position
+  // scored:
   CapRow cap;
+  float slope;      // bias by distance, base 2
+  int pos;          // the row's position
+  int nearest;      // the token in sight that is nearest to it
 };
 
 __device__ __forceinline__ float max3f(float a, float b, float c) {
@@ -375,7 +387,8 @@ __device__ __forceinline__ float max_of(const float (&v)[kKeys]) {
   return fmaxf(b0, b1);
 }
 
-// The softmax of one key tile for the warp's 32 rows.  s: the tensor memory columns of the row tile at the warp's lanes.
+// The softmax of one key tile, the k-th, for the warp's 32 rows.  s: the tensor memory columns of the row tile at the warp's
+// lanes.
 template <int KIND, bool SCORED>
 __device__ __forceinline__ bool soften(const CachePromptLaunch& a, PromptShared& sh, PromptRow& r, uint32_t s, int X,
                                        int lane, int tile, unsigned k, bool& two_step) {
@@ -451,7 +464,7 @@ __device__ __forceinline__ bool soften(const CachePromptLaunch& a, PromptShared&
   uint32_t w[32];
   bool ok = true;
   // Weights of a pair from their base-2 logits less the reference, their sum and their form for the product,
-  // stored half a tile at a time.  (The product before may still read the last tile's weights when the first are ready.)
+  // stored half a tile at a time.  (The product before may still read the last tile's when the first are ready.)
   const auto weigh2 = [&](int i, unsigned long long t) {
     float x, y;
     f2_unpack(t, x, y);
@@ -512,7 +525,7 @@ __device__ __forceinline__ void odd_values(const CachePromptLaunch& a, const Pro
                                            const PromptRow& r, int d0, float (&o)[32]) {
   const int U = 1 << a.cache.rec_shift;
   for (int tile = u.i0; tile < u.i1; ++tile) {
-    if (!u.mixed(sh, tile)) continue;
+    if (!mixed_tile(sh, tile)) continue;
     for (int key = max(tile * kKeys, r.lo); key < min((tile + 1) * kKeys, r.hi); ++key) {
       const int page = a.cache.table[(long long)u.b * a.cache.max_pages + (key >> a.cache.page_shift)];
       if (page < 0 || page >= a.cache.n_pages) continue;
@@ -550,17 +563,16 @@ __device__ __forceinline__ bool sees_bad(const CachePromptLaunch& a, const Promp
   return false;
 }
 
-__device__ __forceinline__ void write_row(const CachePromptLaunch& a, const PromptUnit& u, const PromptRow& r, int d0,
+__device__ __forceinline__ void write_row(const CachePromptLaunch& a, const PromptUnit& u, int t, int head, float l, int d0,
                                           const float (&o)[32]) {
-  if (!r.there) return;
-  const float f = r.l == 0.f ? 0.f : exp2i(a.cache.kind == PISA_CACHE_E2M1 ? a.cache.v_exp : 0) / r.l;
-  uint4* dst = reinterpret_cast<uint4*>(a.out + (((long long)u.b * a.T + r.t) * a.Hq + r.head) * kD + d0);
+  const float f = l == 0.f ? 0.f : exp2i(a.cache.kind == PISA_CACHE_E2M1 ? a.cache.v_exp : 0) / l;
+  uint4* dst = reinterpret_cast<uint4*>(a.out + (((long long)u.b * a.T + t) * a.Hq + head) * kD + d0);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint32_t w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      w[j] = r.l == 0.f ? 0u : pack_bf16x2(o[8 * i + 2 * j] * f, o[8 * i + 2 * j + 1] * f);
+      w[j] = l == 0.f ? 0u : pack_bf16x2(o[8 * i + 2 * j] * f, o[8 * i + 2 * j + 1] * f);
     dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
@@ -601,9 +613,206 @@ __device__ __forceinline__ void stage_queries(const CachePromptLaunch& a, const 
   }
 }
 
-template <int KIND, bool SCORED>
+// Unit number x: the row tile and (sequence, KV head) that it is.
+__device__ __forceinline__ void set_unit(const CachePromptLaunch& a, int x, int row_tiles, PromptUnit& u) {
+  const int bk = x / row_tiles;
+  u.b = bk / a.cache.Hkv;
+  u.kv = bk - u.b * a.cache.Hkv;
+  u.r0 = (x - bk * row_tiles) * kRowsCta;
+}
+
+// Key tiles of a unit whose rows see the tokens lo .. hi - 1 together.
+__device__ __forceinline__ int tiles_of(int lo, int hi) { return lo < hi ? (hi + kKeys - 1) / kKeys - lo / kKeys : 0; }
+
+// The stream form: key tiles of each unit, a warp a unit, where the spans are listed.
+__global__ void __launch_bounds__(256) cache_prompt_tiles_kernel(CachePromptLaunch a, int g_shift, int row_tiles, int units) {
+  after_the_one_before();
+  const int x = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (x >= units) return;
+  PromptUnit u;
+  set_unit(a, x, row_tiles, u);
+  const int count = prompt_count(a, u.b);
+  int lo = INT_MAX, hi = 0;
+  for (int t = (u.r0 >> g_shift) + lane; t < count && t <= (u.r0 + kRowsCta - 1) >> g_shift; t += 32) {
+    bool over;
+    const Span s = span_of(a, u.b, t, count, over);
+    if (s.lo < s.hi) {
+      lo = min(lo, s.lo);
+      hi = max(hi, s.hi);
+    }
+  }
+  lo = __reduce_min_sync(kFull, lo);
+  hi = __reduce_max_sync(kFull, hi);
+  if (lane == 0) a.plan.tiles[x] = tiles_of(lo, hi);
+}
+
+// The stream form's plan, by one CTA: the pieces in order of length, and for each run the unit that begins in it and goes
+// on.  Unit x has the places from place[x] on, its tiles and kUnitEnd more; run r those from r per on.  A piece
+// begins where a unit or a run does.
+__global__ void __launch_bounds__(1024) cache_prompt_plan_kernel(CachePromptLaunch a, int g_shift, int row_tiles, int units) {
+  constexpr int kBuckets = 256;
+  __shared__ int place[kMaxUnits + 1], bucket[kBuckets], sums[32];
+  after_the_one_before();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // places, by three scans of consecutive units a thread
+  constexpr int kEach = (kMaxUnits + 1023) / 1024;
+  int own[kEach], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int x = tid * kEach + i;
+    own[i] = 0;
+    if (x < units) {
+      int n;
+      if (a.first || a.last) {
+        n = a.plan.tiles[x];
+      } else {  // the spans' ends move with the rows
+        PromptUnit u;
+        set_unit(a, x, row_tiles, u);
+        const int count = prompt_count(a, u.b), t0 = u.r0 >> g_shift;
+        const int t1 = min((u.r0 + kRowsCta - 1) >> g_shift, count - 1);
+        bool over;
+        n = t0 > t1 ? 0 : tiles_of(span_of(a, u.b, t0, count, over).lo, span_of(a, u.b, t1, count, over).hi);
+      }
+      own[i] = n + kUnitEnd;
+    }
+    sum += own[i];
+  }
+  int inc = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(kFull, inc, d);
+    if (lane >= d) inc += y;
+  }
+  if (lane == 31) sums[warp] = inc;
+  if (tid < kBuckets) bucket[tid] = 0;
+  __syncthreads();
+  int at = inc - sum;
+  for (int w = 0; w < warp; ++w) at += sums[w];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int x = tid * kEach + i;
+    if (x < units) place[x] = at;
+    at += own[i];
+    if (x == units - 1) place[units] = at;
+  }
+  __syncthreads();
+  const int total = place[units], per = (total + kRuns - 1) / kRuns;
+  if (tid < kRuns) a.plan.cut[tid] = make_int2(-1, 0);
+  __syncthreads();
+  // the pieces: one begins with each unit, and one with each run
+  const auto piece = [&](int j, PromptPiece& p) {  // false: nothing of it is left
+    int begin, x;
+    if (j < units) {
+      x = j;
+      begin = place[x];
+    } else {
+      begin = (j - units) * per;
+      if (begin >= total) return false;
+      int y = units;  // the last unit that begins at or before it
+      x = 0;
+      while (y - x > 1) {
+        const int z = (x + y) >> 1;
+        (place[z] <= begin ? x : y) = z;
+      }
+      if (place[x] == begin) return false;  // (the unit's own piece)
+    }
+    const int run = begin / per, all = place[x + 1] - place[x] - kUnitEnd, k0 = begin - place[x];
+    const int k1 = min((run + 1) * per - place[x], all);
+    if (k0 >= all && k0 > 0) return false;
+    p.unit = x;
+    p.k0 = k0;
+    p.k1 = k1;
+    p.slot = k0 == 0 && k1 == all ? -1 : 2 * run + (k0 == 0);
+    if (k0 == 0 && k1 < all) a.plan.cut[run] = make_int2(x, (place[x] + all - 1) / per);
+    return true;
+  };
+  constexpr int kPieces = (kMaxUnits + kRuns + 1023) / 1024;
+  PromptPiece p[kPieces];
+  int b[kPieces];
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int j = tid + 1024 * i;
+    b[i] = -1;
+    if (j < units + kRuns && piece(j, p[i])) {
+      b[i] = kBuckets - 1 - (int)((long long)(p[i].k1 - p[i].k0) * (kBuckets - 1) / per);
+      atomicAdd(&bucket[b[i]], 1);
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {  // each bucket's first place
+    int before = 0;
+    for (int i = lane; i < kBuckets; i += 32) {
+      const int n = bucket[i];
+      int s = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(kFull, s, d);
+        if (lane >= d) s += y;
+      }
+      bucket[i] = before + s - n;
+      before += __shfl_sync(kFull, s, 31);
+    }
+    if (lane == 0) sums[0] = before;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i)
+    if (b[i] >= 0) a.plan.piece[atomicAdd(&bucket[b[i]], 1)] = p[i];
+  for (int j = sums[0] + tid; j < units + kRuns; j += 1024) a.plan.piece[j].unit = -1;
+}
+
+// The softmax of a piece for the warp's rows, and its result: to the output, or to a partial result.
+template <int KIND, bool SCORED, bool STREAM>
+__device__ __forceinline__ bool soften_piece(const CachePromptLaunch& a, PromptShared& sh, PromptRow& r, int i1, int n,
+                                             int g_shift) {
+  const int lane = threadIdx.x & 31, X = threadIdx.x >> 7;
+  const uint32_t s = sh.tmem + 256 * X + ((threadIdx.x >> 5 & 3) << 21);  // (the warp's lanes: 32 (warp % 4) ..)
+  bool two_step = false;
+  for (int k = 0; k < n; ++k)
+    if (!soften<KIND, SCORED>(a, sh, r, s, X, lane, i1 - 1 - k, k, two_step)) return false;
+  if (n > 0 && !__all_sync(kFull, mbar_wait(&sh.pv_done[X], (n - 1) & 1, &sh.abort))) return false;
+  tc_fence_after();
+  int row = threadIdx.x;
+  asm volatile("" : "+r"(row));  // (what follows is computed here, not kept since the beginning)
+  const PromptUnit u = sh.unit;
+  const int t = (u.r0 + row) >> g_shift, head = u.kv * a.G + ((u.r0 + row) & (a.G - 1));
+  float l = r.l;
+  if (r.lo >= r.hi) l = 0.f;  // (its weights were never masked: see soften)
+  if (sh.bad && sees_bad(a, u, r)) {
+    l = __int_as_float(0x7fc00000);
+    set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
+  }
+  float* part = STREAM && sh.slot >= 0 ? a.part + (size_t)sh.slot * kRowsCta * kPartRow + row : nullptr;
+  const bool there = t < prompt_count(a, u.b);
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    float o[32];
+    if (n > 0) {
+      uint32_t w[32];
+      tmem_ld32_now(s + 192 + 32 * h, w);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(w[i]);
+      if (sh.odd) odd_values<KIND>(a, u, sh, r, 32 * h, o);
+    }
+    if (part) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) part[(32 * h + i) * kRowsCta] = o[i];
+    } else if (there) {
+      write_row(a, u, t, head, l, 32 * h, o);
+    }
+  }
+  if (part) {
+    part[64 * kRowsCta] = r.m;
+    part[65 * kRowsCta] = l;
+  }
+  tc_fence_before();
+  return true;
+}
+
+template <int KIND, bool SCORED, bool STREAM>
 __global__ void __launch_bounds__(kPromptThreads, 1)
-    cache_prompt_kernel(const __grid_constant__ CUtensorMap map, CachePromptLaunch a, int g_shift, int row_tiles) {
+    cache_prompt_kernel(const __grid_constant__ CUtensorMap map, CachePromptLaunch a, int g_shift, int row_tiles,
+                        int units) {
   extern __shared__ unsigned char prompt_smem[];
   __shared__ PromptShared sh;
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -626,30 +835,37 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     sh.abort = sh.odd = sh.bad = 0;
     sh.lo_min = sh.hi_min = INT_MAX;
     sh.lo_max = sh.hi_max = 0;
+    for (int i = 0; i < kLoadWarps; ++i) sh.asked[i] = Asked{0, 0};
   }
   after_the_one_before();
+  PromptPiece piece = {0, 0, INT_MAX, -1};
+  if constexpr (STREAM) {
+    piece = a.plan.piece[blockIdx.x];
+    if (piece.unit < 0) return;
+  } else {  // the longest row tiles first
+    const int heads = units / row_tiles;
+    piece.unit = (int)(blockIdx.x % heads) * row_tiles + row_tiles - 1 - (int)(blockIdx.x / heads);
+  }
   if (warp == kSoftWarps + kLoadWarps) tmem_alloc<512>(&sh.tmem);  // (held by no kernel that waits for another one)
-  // the longest row tiles first
   PromptUnit u;
-  const int heads = a.cache.B * a.cache.Hkv, bk = blockIdx.x % heads;
-  u.b = bk / a.cache.Hkv;
-  u.kv = bk % a.cache.Hkv;
-  u.r0 = (row_tiles - 1 - (int)(blockIdx.x / heads)) * kRowsCta;
+  set_unit(a, piece.unit, row_tiles, u);
   const int count = prompt_count(a, u.b);
   PromptRow r{};
   if (warp < kSoftWarps) {
-    const int row = u.r0 + threadIdx.x;
-    r.t = row >> g_shift;
-    r.head = u.kv * a.G + (row & (a.G - 1));
-    r.there = r.t < count;
-    if (r.there) {
+    const int row = u.r0 + threadIdx.x, t = row >> g_shift;
+    if (t < count) {
       bool over;
-      const Span s = span_of(a, u.b, r.t, count, over);
+      const Span s = span_of(a, u.b, t, count, over);
       if (over) set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
       r.lo = s.lo;
       r.hi = s.hi;
-      r.pos = s.pos;
+      if (SCORED && a.score.slopes) {
+        r.slope = a.score.slopes[u.kv * a.G + (row & (a.G - 1))] * kLog2e;
+        r.pos = s.pos;
+        r.nearest = max(min(s.pos, s.hi - 1), s.lo);
+      }
     }
+    r.m = kNone;
   }
   __syncthreads();
   if (warp < kSoftWarps) {
@@ -670,56 +886,31 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   tc_fence_after();
   u.i0 = sh.lo_min < sh.hi_max ? sh.lo_min / kKeys : 0;
   u.i1 = sh.lo_min < sh.hi_max ? (sh.hi_max + kKeys - 1) / kKeys : 0;
+  // the piece of it
+  u.i1 -= min(piece.k0, u.i1 - u.i0);
+  u.i0 = max(u.i0, u.i1 - (piece.k1 - piece.k0));
+  if (threadIdx.x == kPromptThreads - 1) {  // (read after many barriers)
+    sh.unit = u;
+    sh.slot = piece.slot;
+  }
   bool ok = true;
-  unsigned next = 0;  // what this loading warp has asked for
-  const int n = u.i1 - u.i0;
   if (warp < kSoftWarps) {
-    const int X = warp >> 2;
-    const uint32_t s = sh.tmem + 256 * X + ((uint32_t)(warp & 3) << 21);  // (the warp's lanes: 32 (warp & 3) ..)
     r.f = KIND == PISA_CACHE_E2M1 ? sh.factor[threadIdx.x] : SCORED ? kScale : kScale * kLog2e;
-    r.m = kNone;
     if (SCORED) {
       r.cap = CapRow{r.f * a.score.inv_cap, r.f * kLog2e};
       r.f *= kLog2e;
-      if (a.score.slopes && r.there) {
-        r.slope = a.score.slopes[r.head] * kLog2e;
-        r.nearest = max(min(r.pos, r.hi - 1), r.lo);
-      }
     }
-    bool two_step = false;
-    for (int x = 0; x < n && ok; ++x) ok = soften<KIND, SCORED>(a, sh, r, s, X, lane, u.tile(x), x, two_step);
-    if (ok && n > 0) ok = __all_sync(kFull, mbar_wait(&sh.pv_done[X], (n - 1) & 1, &sh.abort));
-    if (ok) {
-      tc_fence_after();
-      if (r.lo >= r.hi) r.l = 0.f;  // (its weights were never masked: see soften)
-      if (sh.bad && sees_bad(a, u, r)) {
-        r.l = __int_as_float(0x7fc00000);
-        set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
-      }
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        float o[32];
-        if (n > 0) {
-          uint32_t w[32];
-          tmem_ld32_now(s + 192 + 32 * h, w);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(w[i]);
-          if (sh.odd) odd_values<KIND>(a, u, sh, r, 32 * h, o);
-        }
-        write_row(a, u, r, 32 * h, o);
-      }
-      tc_fence_before();
-    }
+    ok = soften_piece<KIND, SCORED, STREAM>(a, sh, r, u.i1, u.n(), g_shift);
   } else if (warp < kSoftWarps + kLoadWarps) {
     const int w = warp - kSoftWarps;
     if constexpr (KIND == PISA_CACHE_BF16)
-      ok = load_bf16(a, &map, u, sh, stages, w, lane, next);
+      ok = load_bf16(a, &map, u, sh, stages, w, lane);
     else
-      ok = load_e2m1(a, u, sh, stages, stages + 2 * PCfg<KIND>::kStages * kTileBytes + 2 * w * kRawBytes, w, lane, next);
+      ok = load_e2m1(a, u, sh, stages, stages + 2 * PCfg<KIND>::kStages * kTileBytes + 2 * w * kRawBytes, w, lane);
   } else if (lane == 0) {
     const int Y = warp - kSoftWarps - kLoadWarps;
     ok = Y == 0 ? multiply_s<KIND>(u, sh, q, stages) : multiply_v<KIND>(u, sh, stages);
-    if (!ok && n > 0) {  // its products end before tensor memory is given back
+    if (!ok) {  // its products end before tensor memory is given back
       umma_commit(&sh.drain[Y]);
       mbar_wait(&sh.drain[Y], 0, nullptr);
     }
@@ -731,17 +922,89 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   __syncthreads();
   if (sh.abort && warp >= kSoftWarps && warp < kSoftWarps + kLoadWarps && lane == 0) {
     // given up: copies that are still on their way land before the shared memory is let go
-    constexpr unsigned kPStages = PCfg<KIND>::kStages;
+    const Asked asked = sh.asked[warp - kSoftWarps];
     const int w = warp - kSoftWarps;
     if (KIND == PISA_CACHE_BF16) {
-      for (unsigned k = next > kPStages ? next - kPStages : 0; k < next; ++k)
-        if (k % kLoadWarps == (unsigned)w) mbar_wait(&sh.full[k % kPStages], (k / kPStages) & 1, nullptr);
+      for (int i = 0; i < PCfg<KIND>::kStages; ++i)
+        if (asked.stages >> i & 1) mbar_wait(&sh.full[i], asked.stages >> (8 + i) & 1, nullptr);
     } else {
-      for (unsigned x = next > 2 ? next - 2 : 0; x < next; ++x) mbar_wait(&sh.landed[w][x & 1], (x >> 1) & 1, nullptr);
+      for (unsigned i = asked.count > 2 ? asked.count - 2 : 0; i < asked.count; ++i)
+        mbar_wait(&sh.landed[w][i & 1], (i >> 1) & 1, nullptr);
     }
   }
   __syncthreads();
   if (warp == kSoftWarps + kLoadWarps) tmem_dealloc<512>(sh.tmem);
+}
+
+// Joins the partial results of the units that lie in several runs: those of the unit that begins in run c and goes on.
+// Sixteen CTAs a run, sixteen rows each; a thread has 16 dims of a row and every fourth partial result.
+__global__ void __launch_bounds__(256) cache_prompt_join_kernel(CachePromptLaunch a, int g_shift, int row_tiles) {
+  __shared__ float so[4][16][4][17];
+  __shared__ float sm[4][16], sl[4][16];
+  after_the_one_before();
+  const int c = blockIdx.x >> 4;
+  const int2 cut = a.plan.cut[c];
+  if (cut.x < 0) return;
+  PromptUnit u;
+  set_unit(a, cut.x, row_tiles, u);
+  const int row_in = threadIdx.x & 15, quad = (threadIdx.x >> 4) & 3, grp = threadIdx.x >> 6;
+  const int row = (blockIdx.x & 15) * 16 + row_in;
+  float m = -INFINITY, l = 0.f, o[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) o[i] = 0.f;
+  for (int i = c + grp; i <= cut.y; i += 4) {
+    const float* p = a.part + ((size_t)i * 2 + (i == c)) * kRowsCta * kPartRow + row;
+    const float mi = p[64 * kRowsCta], li = p[65 * kRowsCta];
+    float y[16];
+#pragma unroll
+    for (int d = 0; d < 16; ++d) y[d] = p[(16 * quad + d) * kRowsCta];
+    const float n = fmaxf(m, mi), f = ex2_approx(m - n), h = ex2_approx(mi - n);
+    m = n;
+    l = l * f + li * h;
+#pragma unroll
+    for (int d = 0; d < 16; ++d) o[d] = li == 0.f ? o[d] * f : o[d] * f + y[d] * h;  // (what a part without keys holds is nothing)
+  }
+  sm[grp][row_in] = m;
+  sl[grp][row_in] = l;
+#pragma unroll
+  for (int d = 0; d < 16; ++d) so[grp][row_in][quad][d] = o[d];
+  __syncthreads();
+  if (grp) return;
+  const int r = u.r0 + row, t = r >> g_shift;
+  if (t >= prompt_count(a, u.b)) return;
+#pragma unroll
+  for (int x = 1; x < 4; ++x) m = fmaxf(m, sm[x][row_in]);
+  l = 0.f;
+#pragma unroll
+  for (int d = 0; d < 16; ++d) o[d] = 0.f;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const float lx = sl[x][row_in], f = lx == 0.f ? 0.f : ex2_approx(sm[x][row_in] - m);
+    l += lx == 0.f ? 0.f : lx * f;
+#pragma unroll
+    for (int d = 0; d < 16; ++d) o[d] += lx == 0.f ? 0.f : so[x][row_in][quad][d] * f;
+  }
+  const float f = l == 0.f ? 0.f : exp2i(a.cache.kind == PISA_CACHE_E2M1 ? a.cache.v_exp : 0) / l;
+  uint4* dst = reinterpret_cast<uint4*>(a.out + (((long long)u.b * a.T + t) * a.Hq + u.kv * a.G + (r & (a.G - 1))) * kD + 16 * quad);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = l == 0.f ? 0u : pack_bf16x2(o[8 * i + 2 * j] * f, o[8 * i + 2 * j + 1] * f);
+    dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+size_t cache_prompt_part_bytes() { return kPromptPlanBytes + (size_t)kRuns * 2 * kRowsCta * kPartRow * 4; }
+
+// Whether the stream form takes a call: `units` row tiles that see up to `tiles` key tiles each.  A CTA for each unit takes as
+// long as its last wave; the stream's CTAs end together, but the plan, the pieces' begins and the join cost it about as
+// much as 16 tiles, and the lengths (known to the device alone) a tenth.
+inline bool takes_stream(long long units, long long tiles) {
+  if (units > kMaxUnits) return false;
+  const long long waves = (units + kRuns - 1) / kRuns;
+  return 10 * kRuns * waves * tiles > 11 * units * tiles + 160 * kRuns;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
@@ -775,11 +1038,24 @@ static cudaError_t launch_prompt(const CachePromptLaunch& L, cudaStream_t s) {
   int g_shift = 0;
   while ((1 << g_shift) < L.G) ++g_shift;
   const int row_tiles = (int)(((long long)L.T * L.G + kRowsCta - 1) / kRowsCta);
-  const long long units = (long long)row_tiles * L.cache.B * L.cache.Hkv;
+  const int units = row_tiles * L.cache.B * L.cache.Hkv;
   CUtensorMap map{};
   if (KIND == PISA_CACHE_BF16 && !map_pages(&map, L.cache)) return cudaErrorInvalidValue;
-  return launch_early<cache_prompt_kernel<KIND, SCORED>>((unsigned)units, kPromptThreads, PCfg<KIND>::kSmem, s, map, L, g_shift,
-                                                         row_tiles);
+  long long keys = (long long)L.cache.max_pages << L.cache.page_shift;  // what a unit sees at most
+  const long long reach = (long long)L.score.window + kRowsCta / L.G;
+  if (!L.last && keys > reach) keys = reach;
+  constexpr int kSmem = PCfg<KIND>::kSmem;
+  if (!takes_stream(units, keys / kKeys))
+    return launch_early<cache_prompt_kernel<KIND, SCORED, false>>((unsigned)units, kPromptThreads, kSmem, s, map, L, g_shift,
+                                                                  row_tiles, units);
+  cudaError_t e = cudaSuccess;
+  if (L.first || L.last)
+    e = launch_early<cache_prompt_tiles_kernel>((unsigned)(units + 7) / 8, 256, 0, s, L, g_shift, row_tiles, units);
+  if (e == cudaSuccess) e = launch_early<cache_prompt_plan_kernel>(1, 1024, 0, s, L, g_shift, row_tiles, units);
+  if (e != cudaSuccess) return e;
+  e = launch_early<cache_prompt_kernel<KIND, SCORED, true>>((unsigned)(units + kRuns), kPromptThreads, kSmem, s, map, L, g_shift, row_tiles, units);
+  if (e != cudaSuccess) return e;
+  return launch_early<cache_prompt_join_kernel>(kRuns * 16, 256, 0, s, L, g_shift, row_tiles);
 }
 
 cudaError_t launch_cache_prompt(const CachePromptLaunch& L, cudaStream_t s) {

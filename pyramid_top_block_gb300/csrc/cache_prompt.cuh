@@ -5,6 +5,22 @@
 
 namespace pisa {
 
+constexpr int kPromptRuns = 152;               // CTAs of the stream form: one on each SM
+constexpr int kPromptUnits = 8 * kPromptRuns;  // row tiles that it takes at most
+
+// A piece of the stream: tiles k0 .. k1 - 1 of a unit (-1: none), and which partial result it leaves (-1: it is the whole unit).
+struct PromptPiece {
+  int unit, k0, k1, slot;
+};
+// In the workspace.
+struct PromptPlan {
+  PromptPiece* piece;  // [kPromptUnits + kPromptRuns]
+  int2* cut;           // [kPromptRuns] the unit that begins in a run and goes on (-1: none), and the last run that it lies in
+  int32_t* tiles;      // [kPromptUnits]
+};
+constexpr size_t kPromptPlanBytes = (kPromptUnits + kPromptRuns) * sizeof(PromptPiece) + kPromptRuns * sizeof(int2) +
+                                    kPromptUnits * sizeof(int32_t);
+
 struct CachePromptLaunch {
   CacheDev cache;
   RowsDev q;
@@ -16,6 +32,8 @@ struct CachePromptLaunch {
   ScoreDev score;
   __nv_bfloat16* out;  // [B, T, Hq, 64]
   int* status;
+  // of the stream form (cache_prompt.cu):
+  PromptPlan plan;
   float* part;  // partial results
 };
 
@@ -43,6 +61,7 @@ __device__ __forceinline__ int prompt_count(const CachePromptLaunch& a, int b) {
   return a.counts ? min(max(a.counts[b], 0), a.T) : a.T;
 }
 
+size_t cache_prompt_part_bytes();
 cudaError_t launch_cache_prompt(const CachePromptLaunch& L, cudaStream_t s);
 
 }  // namespace pisa
