@@ -342,172 +342,256 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
   return d;
 }
 
-// A tile's products of a row, of the keys from key0 on, as the logits that the softmax takes (times r.f if not SCORED and not
-// two_step).  size: the largest magnitude among the products (if SCORED).
-template <bool SCORED>
-__device__ __forceinline__ void logits(const CachePromptLaunch& a, const PromptRow& r, int key0, bool whole, bool two_step,
-                                       float size, float (&v)[kKeys]) {
-  if constexpr (SCORED) {
-    if (a.score.cap > 0.f) {
-      if (__any_sync(kFull, size * r.cap.to_y > 1.f)) {
-        const float top = a.score.cap * kLog2e;
+// A new reference for the warp's rows, given each row's largest logit b: O and the sums of weights follow.  Returns false
+// if the wait for the product before, which writes O, ran out.
+template <int KIND>
+__device__ __forceinline__ bool refer(PromptShared& sh, PromptRow& r, uint32_t s, int X, unsigned k, float b) {
+  // (a step of 32 bits is too coarse for the shift from 2^24 on; nothing that it is for is left there)
+  const float n = fmaxf(r.m, fabsf(b) < 16.f * kFar ? b - PCfg<KIND>::kShift : b);
+  const float f = ex2_approx(r.m - n);
+  if (k > 0) {
+    if (!__all_sync(kFull, mbar_wait(&sh.pv_done[X], (k - 1) & 1, &sh.abort))) return false;
+    tc_fence_after();
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      uint32_t o[32];
+      tmem_ld32_now(s + 192 + 32 * h, o);
 #pragma unroll
-        for (int i = 0; i < kKeys; ++i) v[i] = cap_any(v[i], r.cap, top);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kKeys; i += 2) cap_small(v[i], v[i + 1], r.cap);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kKeys; ++i) v[i] *= r.f;
+      for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+      tmem_st32(s + 192 + 32 * h, o);
     }
-    if (a.score.slopes) {  // -slope (|p - j| - |p - nearest|): whole numbers, exact up to 2^24
-      const float d0 = (float)(key0 - r.pos), least = (float)abs(r.pos - r.nearest);
-#pragma unroll
-      for (int i = 0; i < kKeys; ++i) v[i] = fmaf(-r.slope, fabsf(d0 + (float)i) - least, v[i]);
-    }
-  } else if (two_step) {
-#pragma unroll
-    for (int i = 0; i < kKeys; ++i) v[i] = __fmul_rn(v[i], r.f);
   }
-  if (!whole) {
-    const int from = r.lo - key0, to = r.hi - key0;
-#pragma unroll
-    for (int i = 0; i < kKeys; ++i) v[i] = i >= from && i < to ? v[i] : -INFINITY;
-  }
+  r.m = n;
+  r.l *= f;
+  return true;
 }
 
-__device__ __forceinline__ float max_of(const float (&v)[kKeys]) {
-  float b0 = -INFINITY, b1 = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kKeys; i += 4) {
-    b0 = max3f(b0, v[i], v[i + 1]);
-    b1 = max3f(b1, v[i + 2], v[i + 3]);
-  }
-  return fmaxf(b0, b1);
+template <int KIND>
+__device__ __forceinline__ uint32_t pack_weights(float x, float y) {
+  return KIND == PISA_CACHE_BF16 ? pack_bf16x2(x, y) : pack_f16x2(x, y);
 }
 
-// The softmax of one key tile, the k-th, for the warp's 32 rows.  s: the tensor memory columns of the row tile at the warp's
-// lanes.
-template <int KIND, bool SCORED>
-__device__ __forceinline__ bool soften(const CachePromptLaunch& a, PromptShared& sh, PromptRow& r, uint32_t s, int X,
-                                       int lane, int tile, unsigned k, bool& two_step) {
-  using C = PCfg<KIND>;
+// The softmax of one key tile, the k-th, for the warp's 32 rows, plain scores.  s: the tensor memory columns of the row tile
+// at the warp's lanes.
+template <int KIND>
+__device__ __forceinline__ bool soften(PromptShared& sh, PromptRow& r, uint32_t s, int X, int lane, int tile, unsigned k,
+                                       bool& two_step) {
   const int key0 = tile * kKeys;
   // (rows that see nothing do not matter: they get zeros at the end, or do not exist)
   const bool whole = __all_sync(kFull, r.lo >= r.hi || (r.lo <= key0 && r.hi >= key0 + kKeys));
   if (!__all_sync(kFull, mbar_wait(&sh.s_full[X], k & 1, &sh.abort))) return false;
   tc_fence_after();
   float v[kKeys], b;
-  tmem_ld128_top<SCORED>(s, v, b);
-  const float size = b;  // (if SCORED: the largest magnitude)
+  tmem_ld128_top<false>(s, v, b);
   tc_fence_before();
   __syncwarp();
   if (lane == 0) mbar_arrive(&sh.s_free[X]);  // S is in registers: the next product may overwrite it
-  float ff = SCORED || two_step ? 1.f : r.f;
-  // Scores that need no mask become logits in the step that takes the reference off (weights): a cap by its
-  // polynomial, a bias by a line, for keys that no row of the warp lies before.  b: at least the largest logit.
-  bool capped = false, line = false;
-  const float bias = r.slope * (float)(key0 - r.nearest);  // of the tile's first key, relative to the nearest one
-  if constexpr (SCORED) {
-    const bool cap = a.score.cap > 0.f, slopes = a.score.slopes != nullptr;
-    capped = whole && cap && !slopes && !__any_sync(kFull, b * r.cap.to_y > 1.f);
-    line = whole && slopes && !cap && !__any_sync(kFull, key0 + kKeys > r.pos + 1 && r.lo < r.hi);
+  float ff = two_step ? 1.f : r.f;
+  if (two_step || !whole) {
+    if (two_step) {
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i) v[i] = __fmul_rn(v[i], r.f);
+    }
+    if (!whole) {
+      const int from = r.lo - key0, to = r.hi - key0;
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i) v[i] = i >= from && i < to ? v[i] : -INFINITY;
+    }
+    float b1 = b = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kKeys; i += 4) {
+      b = max3f(b, v[i], v[i + 1]);
+      b1 = max3f(b1, v[i + 2], v[i + 3]);
+    }
+    b = fmaxf(b, b1);
   }
-  if (capped)
-    b = cap_any(b, r.cap, 0.f);
-  else if (line)
-    b = fmaf(b, r.f, fmaxf(bias, fmaf(r.slope, (float)(kKeys - 1), bias)));
-  else if (SCORED || two_step || !whole) {
-    logits<SCORED>(a, r, key0, whole, two_step, size, v);
-    b = max_of(v);
-  }
-  if (!SCORED) b = __fmul_rn(b, ff);
+  b = __fmul_rn(b, ff);
   bool waited = k == 0;  // for the product before, which reads P and writes O
   // A row's reference m is set anew only when a logit passes it by more than kTop, so that few tiles rescale O.
-  if (__any_sync(kFull, b > r.m + C::kTop)) {
-    if (capped) b = cap_any(max_of(v), r.cap, 0.f);  // (the cap keeps the order)
-    if (line) {
-      b = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < kKeys; ++i) b = fmaxf(b, fmaf(v[i], r.f, fmaf(r.slope, (float)i, bias)));
-    }
-    // (a step of 32 bits is too coarse for the shift from 2^24 on; nothing that it is for is left there)
-    const float n = fmaxf(r.m, fabsf(b) < 16.f * kFar ? b - C::kShift : b);
-    const float f = ex2_approx(r.m - n);
-    if (k > 0) {
-      if (!__all_sync(kFull, mbar_wait(&sh.pv_done[X], (k - 1) & 1, &sh.abort))) return false;
-      tc_fence_after();
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        uint32_t o[32];
-        tmem_ld32_now(s + 192 + 32 * h, o);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-        tmem_st32(s + 192 + 32 * h, o);
-      }
-      waited = true;
-    }
-    r.m = n;
-    r.l *= f;
+  if (__any_sync(kFull, b > r.m + PCfg<KIND>::kTop)) {
+    if (!refer<KIND>(sh, r, s, X, k, b)) return false;
+    waited = true;
     // Below, a logit less m is an exact product less a rounded one: 2^-24 of m, no error as all weights of the row have
     // it, until it overflows a weight.  From kFar on the products are rounded first.
-    if (!SCORED && !two_step && __any_sync(kFull, fabsf(n) >= kFar && n != kNone)) {
+    if (!two_step && __any_sync(kFull, fabsf(r.m) >= kFar && r.m != kNone)) {
       two_step = true;
 #pragma unroll
       for (int i = 0; i < kKeys; ++i) v[i] = __fmul_rn(v[i], r.f);
       ff = 1.f;
     }
   }
-  const unsigned long long m2 = f2_pack(-r.m, -r.m);
+  const unsigned long long f2 = f2_pack(ff, ff), m2 = f2_pack(-r.m, -r.m);
   unsigned long long s0 = 0, s1 = 0;
   uint32_t w[32];
-  bool ok = true;
-  // Weights of a pair from their base-2 logits less the reference, their sum and their form for the product,
-  // stored half a tile at a time.  (The product before may still read the last tile's when the first are ready.)
-  const auto weigh2 = [&](int i, unsigned long long t) {
+#pragma unroll
+  for (int i = 0; i < kKeys / 2; ++i) {
     float x, y;
-    f2_unpack(t, x, y);
+    f2_unpack(f2_fma(f2_pack(v[2 * i], v[2 * i + 1]), f2, m2), x, y);
     x = ex2_approx(x);
     y = ex2_approx(y);
     if (i & 1)
       s1 = f2_add(s1, f2_pack(x, y));
     else
       s0 = f2_add(s0, f2_pack(x, y));
-    w[i & 31] = KIND == PISA_CACHE_BF16 ? pack_bf16x2(x, y) : pack_f16x2(x, y);
+    w[i & 31] = pack_weights<KIND>(x, y);
+    // stored half a tile at a time (the product before may still read the last weights when the first are ready)
     if (i == 31 && !waited) {
-      ok = __all_sync(kFull, mbar_wait(&sh.pv_done[X], (k - 1) & 1, &sh.abort));
+      if (!__all_sync(kFull, mbar_wait(&sh.pv_done[X], (k - 1) & 1, &sh.abort))) return false;
       tc_fence_after();
     }
     if ((i & 31) == 31) tmem_st32(s + 128 + (i & 32), w);
-  };
-  if (SCORED && capped) {
-    const unsigned long long fy = f2_pack(r.cap.to_y, r.cap.to_y), fl = f2_pack(r.cap.to_l, r.cap.to_l);
-    if (__any_sync(kFull, size * r.cap.to_y > 0.5f)) {
-#pragma unroll
-      for (int i = 0; i < kKeys / 2; ++i) {
-        const unsigned long long x = f2_pack(v[2 * i], v[2 * i + 1]);
-        weigh2(i, f2_fma(f2_mul(x, fl), tanh_ratio<Tanh>(f2_mul(x, fy)), m2));
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kKeys / 2; ++i) {
-        const unsigned long long x = f2_pack(v[2 * i], v[2 * i + 1]);
-        weigh2(i, f2_fma(f2_mul(x, fl), tanh_ratio<TanhHalf>(f2_mul(x, fy)), m2));
-      }
-    }
-  } else if (SCORED && line) {
-    const unsigned long long f2 = f2_pack(r.f, r.f), sl = f2_pack(r.slope, r.slope);
-    const unsigned long long c = f2_add(m2, f2_pack(bias, bias));
-#pragma unroll
-    for (int i = 0; i < kKeys / 2; ++i)
-      weigh2(i, f2_fma(f2_pack(v[2 * i], v[2 * i + 1]), f2, f2_fma(sl, f2_pack(2.f * i, 2.f * i + 1.f), c)));
-  } else {
-    const unsigned long long f2 = f2_pack(ff, ff);
-#pragma unroll
-    for (int i = 0; i < kKeys / 2; ++i) weigh2(i, f2_fma(f2_pack(v[2 * i], v[2 * i + 1]), f2, m2));
   }
-  if (!ok) return false;
+  float x, y;
+  f2_unpack(f2_add(s0, s1), x, y);
+  r.l += x + y;
+  tmem_st_wait();
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&sh.p_full[X]);
+  return true;
+}
+
+// The same for scores that are not plain products.  Their arithmetic is two to six times as long, so it is kept in a loop over
+// 64 columns at a time, which read S once more (unrolled over all 128 the longer forms do not fit the instruction
+// cache: a cap that the scores pass took 1557 us instead of 307 for 1216 tokens at 16384).
+enum ScoreForm {
+  kCapHalf,   // capped, |score| at most half the cap: a short polynomial
+  kCapWhole,  // capped, |score| at most the cap: a longer one
+  kCapFar,    // capped at 128 or less: exponentials
+  kLine,      // a bias, where no row of the warp sees a later token than its own: a line
+  kAnyScore,  // anything else
+};
+
+// 64 products of a row, of the keys from key0 on, as logits less a reference (m2: minus the reference, twice).
+__device__ __forceinline__ void logits64(const CachePromptLaunch& a, const PromptRow& r, ScoreForm form, bool whole, int key0,
+                                         unsigned long long m2, float (&v)[64]) {
+  const unsigned long long fy = f2_pack(r.cap.to_y, r.cap.to_y), fl = f2_pack(r.cap.to_l, r.cap.to_l);
+  if (form == kCapHalf) {
+#pragma unroll
+    for (int i = 0; i < 64; i += 2) {
+      const unsigned long long x = f2_pack(v[i], v[i + 1]);
+      f2_unpack(f2_fma(f2_mul(x, fl), tanh_ratio<TanhHalf>(f2_mul(x, fy)), m2), v[i], v[i + 1]);
+    }
+  } else if (form == kCapWhole) {
+#pragma unroll
+    for (int i = 0; i < 64; i += 2) {
+      const unsigned long long x = f2_pack(v[i], v[i + 1]);
+      f2_unpack(f2_fma(f2_mul(x, fl), tanh_ratio<Tanh>(f2_mul(x, fy)), m2), v[i], v[i + 1]);
+    }
+  } else if (form == kCapFar) {
+    // cap tanh y = cap - 2 cap / (1 + e^(2 y)): off by up to 2^-20.5 of the cap, 1.3e-4 in base 2 for 128
+    const float two = 2.f * kLog2e * r.cap.to_y, top = a.score.cap * kLog2e;
+    const unsigned long long fe = f2_pack(two, two), ft = f2_pack(-2.f * top, -2.f * top), one = f2_pack(1.f, 1.f);
+    const unsigned long long mt = f2_add(m2, f2_pack(top, top));
+#pragma unroll
+    for (int i = 0; i < 64; i += 2) {
+      float x, y;
+      f2_unpack(f2_mul(f2_pack(v[i], v[i + 1]), fe), x, y);
+      f2_unpack(f2_add(f2_pack(ex2_approx(x), ex2_approx(y)), one), x, y);
+      f2_unpack(f2_fma(f2_pack(rcp_approx(x), rcp_approx(y)), ft, mt), v[i], v[i + 1]);
+    }
+  } else if (form == kLine) {
+    const float bias = r.slope * (float)(key0 - r.nearest);  // of the first key, relative to the nearest one in sight
+    const unsigned long long f2 = f2_pack(r.f, r.f), sl = f2_pack(r.slope, r.slope), c = f2_add(m2, f2_pack(bias, bias));
+#pragma unroll
+    for (int i = 0; i < 64; i += 2)
+      f2_unpack(f2_fma(f2_pack(v[i], v[i + 1]), f2, f2_fma(sl, f2_pack((float)i, (float)(i + 1)), c)), v[i], v[i + 1]);
+  } else {
+    const bool cap = a.score.cap > 0.f;
+    const float top = a.score.cap * kLog2e;
+    float m, unused;
+    f2_unpack(m2, m, unused);
+    // -slope (|p - j| - |p - nearest|): whole numbers, exact up to 2^24 (without slopes the slope is zero)
+    const float d0 = (float)(key0 - r.pos), least = (float)abs(r.pos - r.nearest);
+#pragma unroll
+    for (int i = 0; i < 64; ++i) {
+      const float x = cap ? cap_any(v[i], r.cap, top) : v[i] * r.f;
+      v[i] = fmaf(-r.slope, fabsf(d0 + (float)i) - least, x) + m;
+    }
+  }
+  if (!whole) {
+    const int from = r.lo - key0, to = r.hi - key0;
+#pragma unroll
+    for (int i = 0; i < 64; ++i) v[i] = i >= from && i < to ? v[i] : -INFINITY;
+  }
+}
+
+template <int KIND>
+__device__ __forceinline__ bool soften_scored(const CachePromptLaunch& a, PromptShared& sh, PromptRow& r, uint32_t s, int X,
+                                              int lane, int tile, unsigned k) {
+  const int key0 = tile * kKeys;
+  const bool whole = __all_sync(kFull, r.lo >= r.hi || (r.lo <= key0 && r.hi >= key0 + kKeys));
+  const bool cap = a.score.cap > 0.f, slopes = a.score.slopes != nullptr;
+  if (!__all_sync(kFull, mbar_wait(&sh.s_full[X], k & 1, &sh.abort))) return false;
+  tc_fence_after();
+  float size;  // the largest product's magnitude
+  {
+    float v[kKeys];
+    tmem_ld128_top<true>(s, v, size);
+  }
+  ScoreForm form = kAnyScore;
+  if (cap && !slopes) {
+    if (!__any_sync(kFull, size * r.cap.to_y > 0.5f))
+      form = kCapHalf;
+    else if (!__any_sync(kFull, size * r.cap.to_y > 1.f))
+      form = kCapWhole;
+    else if (a.score.cap <= 128.f)
+      form = kCapFar;
+  } else if (!cap && !__any_sync(kFull, key0 + kKeys > r.pos + 1 && r.hi > r.pos + 1)) {
+    form = kLine;  // (rows that see no later tokens than their own: such are masked)
+  }
+  // at least the row's largest logit: the nearer end of the line adds the more (or the less negative)
+  float b = cap ? cap_any(size, r.cap, a.score.cap * kLog2e) : size * r.f;
+  if (slopes) {
+    const float d0 = (float)(key0 - r.pos), d1 = d0 + (float)(kKeys - 1), least = (float)abs(r.pos - r.nearest);
+    const float near = d0 > 0.f ? d0 : d1 < 0.f ? -d1 : 0.f, far = fmaxf(fabsf(d0), fabsf(d1));
+    b -= r.slope * ((r.slope > 0.f ? near : far) - least);
+  }
+  bool waited = k == 0;
+  if (__any_sync(kFull, b > r.m + PCfg<KIND>::kTop)) {
+    b = -INFINITY;
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      float v[64];
+      tmem_ld64_now(s + 64 * h, v);
+      logits64(a, r, form, whole, key0 + 64 * h, 0, v);
+#pragma unroll
+      for (int i = 0; i < 64; i += 2) b = max3f(b, v[i], v[i + 1]);
+    }
+    if (__any_sync(kFull, b > r.m + PCfg<KIND>::kTop)) {
+      if (!refer<KIND>(sh, r, s, X, k, b)) return false;
+      waited = true;
+    }
+  }
+  const unsigned long long m2 = f2_pack(-r.m, -r.m);
+  unsigned long long s0 = 0, s1 = 0;
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    float v[64];
+    tmem_ld64_now(s + 64 * h, v);
+    if (h == 1) {  // S is in registers: the next product may overwrite it
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.s_free[X]);
+    }
+    logits64(a, r, form, whole, key0 + 64 * h, m2, v);
+    uint32_t w[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float x = ex2_approx(v[2 * i]), y = ex2_approx(v[2 * i + 1]);
+      if (i & 1)
+        s1 = f2_add(s1, f2_pack(x, y));
+      else
+        s0 = f2_add(s0, f2_pack(x, y));
+      w[i] = pack_weights<KIND>(x, y);
+    }
+    if (!waited) {
+      if (!__all_sync(kFull, mbar_wait(&sh.pv_done[X], (k - 1) & 1, &sh.abort))) return false;
+      tc_fence_after();
+      waited = true;
+    }
+    tmem_st32(s + 128 + 32 * h, w);
+  }
   float x, y;
   f2_unpack(f2_add(s0, s1), x, y);
   r.l += x + y;
@@ -769,7 +853,9 @@ __device__ __forceinline__ bool soften_piece(const CachePromptLaunch& a, PromptS
   const uint32_t s = sh.tmem + 256 * X + ((threadIdx.x >> 5 & 3) << 21);  // (the warp's lanes: 32 (warp % 4) ..)
   bool two_step = false;
   for (int k = 0; k < n; ++k)
-    if (!soften<KIND, SCORED>(a, sh, r, s, X, lane, i1 - 1 - k, k, two_step)) return false;
+    if (!(SCORED ? soften_scored<KIND>(a, sh, r, s, X, lane, i1 - 1 - k, k)
+                 : soften<KIND>(sh, r, s, X, lane, i1 - 1 - k, k, two_step)))
+      return false;
   if (n > 0 && !__all_sync(kFull, mbar_wait(&sh.pv_done[X], (n - 1) & 1, &sh.abort))) return false;
   tc_fence_after();
   int row = threadIdx.x;

@@ -46,6 +46,12 @@ __device__ __forceinline__ unsigned long long tanh_ratio(unsigned long long y) {
   return q;
 }
 
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Factors of a row: y = score * to_y (to the cap's units), logit = score * to_l tanh(y) / y.
 struct CapRow {
   float to_y, to_l;

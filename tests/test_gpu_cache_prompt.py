@@ -89,6 +89,13 @@ def spans(kind, start, counts, T, seed=0):
     (2, 190, 16, 2, 64, [3, 900], [190, 150], "any", 50, 10.0, True),
     (1, 17, 16, 1, 64, [30000], [17], "causal", 0, 0.0, False),
     (1, 1100, 16, 1, 64, [1500], [1100], "causal", 0, 0.0, False),
+    (2, 300, 4, 2, 64, [700, 0], [300, 280], "prefix", 0, 0.0, True),
+    (1, 400, 2, 1, 128, [100], [400], "any", 0, 0.0, True),
+    (1, 700, 8, 1, 64, [0], [700], "documents", 200, 0.0, True),
+    (1, 300, 16, 1, 64, [200], [300], "causal", 0, 2.0, False),      # scores past the cap
+    (1, 200, 4, 1, 64, [100], [200], "prefix", 0, 300.0, False),
+    (1, 200, 4, 1, 64, [100], [200], "causal", 0, 0.75, True),
+    (2, 530, 16, 1, 64, [6000, 12000], [530, 100], "causal", 0, 8.0, True),
 ])
 def test_prompt_attention(bits, B, T, G, Hkv, page, start, counts, kind, window, cap, slopes):
     g = gen(T * 10 + page)
