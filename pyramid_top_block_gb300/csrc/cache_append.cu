@@ -172,18 +172,24 @@ struct AxisRows {
   bool one;  // all axes agree, as in text
 };
 
-// The angles of pairs i .. i + N - 1, each from its own axis's row.  Pairs of one axis need not be
-// neighbours, so the words are loaded one by one; they come from three or four rows of at most 256 bytes.
+// The angles of pairs i .. i + N - 1, each from its own axis's row: every lane of the warp loads those of the pair of its
+// number, and the lanes take them from one another (each its own pairs' by word loads took XXX instead of XXX us for
+// 32768 tokens).
 template <int N>
-__device__ __forceinline__ void load_axes(const CacheAppendLaunch& a, const AxisRows& rows, int i, float (&u)[N],
+__device__ __forceinline__ void load_axes(const CacheAppendLaunch& a, const AxisRows& rows, int lane, int i, float (&u)[N],
                                           float (&v)[N]) {
+  float c = 0.f, s = 0.f;
+  if (lane < a.rot >> 1) {
+    const unsigned axis = (unsigned)(a.axis_of >> (2 * lane)) & 3u;
+    const uint32_t lo = axis & 1 ? rows.at[1] : rows.at[0], hi = axis & 1 ? rows.at[3] : rows.at[2];
+    const float* row = a.rotary + (size_t)(axis & 2 ? hi : lo) * 16 + lane;
+    c = row[0];
+    s = row[a.rot >> 1];
+  }
 #pragma unroll
   for (int e = 0; e < N; ++e) {
-    const unsigned axis = (unsigned)(a.axis_of >> (2 * (i + e))) & 3u;
-    const uint32_t lo = axis & 1 ? rows.at[1] : rows.at[0], hi = axis & 1 ? rows.at[3] : rows.at[2];
-    const float* row = a.rotary + (size_t)(axis & 2 ? hi : lo) * 16 + i + e;
-    u[e] = row[0];
-    v[e] = row[a.rot >> 1];
+    u[e] = __shfl_sync(kFull, c, i + e);
+    v[e] = __shfl_sync(kFull, s, i + e);
   }
 }
 
@@ -199,13 +205,15 @@ __device__ __forceinline__ void load_turn(const CacheAppendLaunch& a, long long 
     t.c[e] = 1.f;
     t.s[e] = 0.f;
   }
+  const bool low = c < half;
+  constexpr int kAngles = INTER ? 4 : 8;  // of a lane
+  float uu[kAngles], vv[kAngles];
+  const bool apart = AXES && !rows.one;  // (the same for the whole warp)
+  if (apart) load_axes(a, rows, lane, INTER ? 4 * c : 8 * (low ? c : c - half), uu, vv);
   if (!t.on) return;
   const float* row = a.rotary + p * a.rot;
-  if (INTER) {
-    float uu[4], vv[4];
-    if (AXES && !rows.one) {
-      load_axes(a, rows, 4 * c, uu, vv);
-    } else {
+  if constexpr (INTER) {
+    if (!apart) {
       const float4 u = *reinterpret_cast<const float4*>(row + 4 * c);
       const float4 v = *reinterpret_cast<const float4*>(row + (a.rot >> 1) + 4 * c);
       uu[0] = u.x, uu[1] = u.y, uu[2] = u.z, uu[3] = u.w;
@@ -217,12 +225,8 @@ __device__ __forceinline__ void load_turn(const CacheAppendLaunch& a, long long 
       t.s[e] = (e & 1) ? vv[e >> 1] : -vv[e >> 1];
     }
   } else {
-    const bool low = c < half;
     t.from = low ? lane + half : lane - half;
-    float uu[8], vv[8];
-    if (AXES && !rows.one) {
-      load_axes(a, rows, 8 * (low ? c : c - half), uu, vv);
-    } else {
+    if (!apart) {
       const float4* u = reinterpret_cast<const float4*>(row + 8 * (low ? c : c - half));
       const float4* v = reinterpret_cast<const float4*>(row + (a.rot >> 1) + 8 * (low ? c : c - half));
       const float4 u0 = u[0], u1 = u[1], v0 = v[0], v1 = v[1];

@@ -479,7 +479,7 @@ __device__ __forceinline__ void logits64(const CachePromptLaunch& a, const Promp
       f2_unpack(f2_fma(f2_mul(x, fl), tanh_ratio<Tanh>(f2_mul(x, fy)), m2), v[i], v[i + 1]);
     }
   } else if (form == kCapFar) {
-    // cap tanh y = cap - 2 cap / (1 + e^(2 y)): off by up to 2^-20.5 of the cap, 1.3e-4 in base 2 for 128
+    // (as cap_exp, with the reference in its last step)
     const float two = 2.f * kLog2e * r.cap.to_y, top = a.score.cap * kLog2e;
     const unsigned long long fe = f2_pack(two, two), ft = f2_pack(-2.f * top, -2.f * top), one = f2_pack(1.f, 1.f);
     const unsigned long long mt = f2_add(m2, f2_pack(top, top));
@@ -535,7 +535,7 @@ __device__ __forceinline__ bool soften_scored(const CachePromptLaunch& a, Prompt
       form = kCapHalf;
     else if (!__any_sync(kFull, size * r.cap.to_y > 1.f))
       form = kCapWhole;
-    else if (a.score.cap <= 128.f)
+    else if (a.score.cap <= kCapExp)
       form = kCapFar;
   } else if (!cap && !__any_sync(kFull, key0 + kKeys > r.pos + 1 && r.hi > r.pos + 1)) {
     form = kLine;  // (rows that see no later tokens than their own: such are masked)

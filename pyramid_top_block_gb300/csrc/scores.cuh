@@ -63,6 +63,17 @@ __device__ __forceinline__ void cap_small(float& a, float& b, const CapRow& r) {
   f2_unpack(f2_mul(f2_mul(x, f2_pack(r.to_l, r.to_l)), tanh_ratio<Tanh>(f2_mul(x, f2_pack(r.to_y, r.to_y)))), a, b);
 }
 
+// Two scores of any size, capped: cap tanh y = cap - 2 cap / (1 + e^(2 y)), off by up to 2^-20.5 of the cap (so 1.3e-4 in
+// base 2 for a cap of 128, the largest that this is used for).  An infinity gives plus or minus the cap, a NaN a NaN.
+// two = 2 log2 e to_y, top = cap log2 e.
+__device__ __forceinline__ void cap_exp(float& a, float& b, float two, float top) {
+  float x, y;
+  f2_unpack(f2_mul(f2_pack(a, b), f2_pack(two, two)), x, y);
+  f2_unpack(f2_add(f2_pack(ex2_approx(x), ex2_approx(y)), f2_pack(1.f, 1.f)), x, y);
+  f2_unpack(f2_fma(f2_pack(rcp_approx(x), rcp_approx(y)), f2_pack(-2.f * top, -2.f * top), f2_pack(top, top)), a, b);
+}
+constexpr float kCapExp = 128.f;
+
 // One score of any size, capped; top = cap log2 e.  An infinity gives plus or minus top, a NaN a NaN.
 __device__ __forceinline__ float cap_any(float x, const CapRow& r, float top) {
   const float y = fabsf(x * r.to_y);
