@@ -112,32 +112,30 @@ __device__ __forceinline__ int look(const CachePromptLaunch& a, const PromptUnit
 // get them at the end (odd_values).
 __device__ __forceinline__ void scrub(PromptShared& sh, unsigned char* v, int tile, int lane) {
   const int sub = lane >> 3, ch = lane & 7;
-  bool odd = false;
+  const auto at = [&](int j) {
+    const int row = 4 * j + sub;
+    return reinterpret_cast<uint4*>(v + row * 128 + ((ch ^ (row & 7)) << 4));
+  };
+  // an exponent of all ones carries into the sign's place
+  const auto test = [](uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
+  uint32_t some = 0;  // bit j: something in this lane's row number j
 #pragma unroll 8
   for (int j = 0; j < kKeys / 4; ++j) {
-    const int row = 4 * j + sub;
-    uint4* at = reinterpret_cast<uint4*>(v + row * 128 + ((ch ^ (row & 7)) << 4));
-    uint4 x = *at;
+    const uint4 x = *at(j);
+    if (test(x.x) | test(x.y) | test(x.z) | test(x.w)) some |= 1u << j;
+  }
+  for (; some; some &= some - 1) {
+    const int j = __ffs(some) - 1, key = tile * kKeys + 4 * j + sub;
+    const uint4 x = *at(j);
     uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    bool any = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if ((w[i] & 0x7f80u) == 0x7f80u) {
-        w[i] &= 0xffff0000u;
-        any = true;
-      }
-      if ((w[i] & 0x7f800000u) == 0x7f800000u) {
-        w[i] &= 0xffffu;
-        any = true;
-      }
+      if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
+      if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu;
     }
-    if (any) {
-      *at = make_uint4(w[0], w[1], w[2], w[3]);
-      const int key = tile * kKeys + row;
-      odd = odd || (key >= sh.lo_min && key < sh.hi_max);
-    }
+    *at(j) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (key >= sh.lo_min && key < sh.hi_max) sh.odd = 1;
   }
-  if (odd) sh.odd = 1;
 }
 
 // 16 dims of a token: 8 bytes of codes and a scale, as 16 fp16.
@@ -663,22 +661,33 @@ __device__ __forceinline__ void write_row(const CachePromptLaunch& a, const Prom
 
 // ------------------------------------------------------------------------------------------------ the kernel
 
-// The queries of the CTA's rows as two swizzled operands, by the softmax warps: eight threads a row.  4-bit pages:
-// as fp16, the row scaled by a power of two so that its largest element lies in [1, 2) (cache_attend.cuh, make_q).
-template <int KIND, bool SCORED>
-__device__ __forceinline__ void stage_queries(const CachePromptLaunch& a, const PromptUnit& u, PromptShared& sh,
-                                              unsigned char* q, int count, int g_shift) {
+// The queries of the CTA's rows, by the softmax warps, eight threads a row and eight rows a thread ..
+__device__ __forceinline__ void fetch_queries(const CachePromptLaunch& a, const PromptUnit& u, int count, int g_shift,
+                                              uint4 (&x)[8]) {
   const int ch = threadIdx.x & 7;
-#pragma unroll 4
+#pragma unroll
   for (int it = 0; it < 8; ++it) {
-    const int row = it * 32 + (threadIdx.x >> 3), r = u.r0 + row, t = r >> g_shift;
-    uint4 x = make_uint4(0, 0, 0, 0);
+    const int r = u.r0 + it * 32 + (threadIdx.x >> 3), t = r >> g_shift;
+    x[it] = make_uint4(0, 0, 0, 0);
     if (t < count) {
       const int head = u.kv * a.G + (r & (a.G - 1));
-      x = *reinterpret_cast<const uint4*>(a.q.data + u.b * a.q.sb + (long long)t * a.q.st + head * a.q.sh + 8 * ch);
+      x[it] = *reinterpret_cast<const uint4*>(a.q.data + u.b * a.q.sb + (long long)t * a.q.st + head * a.q.sh + 8 * ch);
     }
+  }
+}
+
+// .. as two swizzled operands.  4-bit pages: as fp16, the row scaled by a power of two so that its largest element lies in
+// [1, 2) (cache_attend.cuh, make_q).
+template <int KIND, bool SCORED>
+__device__ __forceinline__ void stage_queries(const CachePromptLaunch& a, PromptShared& sh, unsigned char* q,
+                                              const uint4 (&x)[8]) {
+  const int ch = threadIdx.x & 7;
+#pragma unroll
+  for (int it = 0; it < 8; ++it) {
+    const int row = it * 32 + (threadIdx.x >> 3);
+    uint4 y = x[it];
     if (KIND == PISA_CACHE_E2M1) {
-      uint32_t w[4] = {x.x, x.y, x.z, x.w}, m = 0;
+      uint32_t w[4] = {y.x, y.y, y.z, y.w}, m = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
       m = max(m & 0xffffu, m >> 16);
@@ -689,11 +698,11 @@ __device__ __forceinline__ void stage_queries(const CachePromptLaunch& a, const 
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         w[i] = pack_f16x2(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xffff0000u) * down);
-      x = make_uint4(w[0], w[1], w[2], w[3]);
+      y = make_uint4(w[0], w[1], w[2], w[3]);
       constexpr float kFactor = SCORED ? kScale : kScale * kLog2e;
       if (ch == 0) sh.factor[row] = fminf(kFactor * exp2i(e) * exp2i(a.cache.k_exp), 0x1.fffffep127f);
     }
-    *reinterpret_cast<uint4*>(q + row * 128 + ((ch ^ (row & 7)) << 4)) = x;
+    *reinterpret_cast<uint4*>(q + row * 128 + ((ch ^ (row & 7)) << 4)) = y;
   }
 }
 
@@ -937,7 +946,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   set_unit(a, piece.unit, row_tiles, u);
   const int count = prompt_count(a, u.b);
   PromptRow r{};
+  uint4 queries[8];
   if (warp < kSoftWarps) {
+    fetch_queries(a, u, count, g_shift, queries);  // (on their way while the spans come)
     const int row = u.r0 + threadIdx.x, t = row >> g_shift;
     if (t < count) {
       bool over;
@@ -964,7 +975,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       atomicMin(&sh.hi_min, hi_min);
       atomicMax(&sh.hi_max, hi_max);
     }
-    stage_queries<KIND, SCORED>(a, u, sh, q, count, g_shift);
+    stage_queries<KIND, SCORED>(a, sh, q, queries);
     fence_async_proxy();
   }
   tc_fence_before();
