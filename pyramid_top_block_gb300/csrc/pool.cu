@@ -6,6 +6,8 @@
 //
 // What bounds it: copying pages (the memory, read and write); planning is a few dependent loads and
 // barriers, a few microseconds.
+#include <climits>
+
 #include <cooperative_groups.h>
 
 #include "pool.cuh"
@@ -14,7 +16,9 @@ namespace pisa {
 
 namespace cg = cooperative_groups;
 
-constexpr int kPlanCtas = 8;  // one cluster plans: it can hand sums around without another launch
+// One cluster plans: it can hand sums around without another launch.  For small pools it has one CTA, whose barriers take
+// less (plans_alone).
+constexpr int kPlanCtas = 8;
 constexpr int kPlanThreads = 1024;
 
 __device__ __forceinline__ bool is_page(const PoolDev& p, int x) { return x >= 0 && x < p.n_pages; }
@@ -22,12 +26,22 @@ __device__ __forceinline__ bool is_page(const PoolDev& p, int x) { return x >= 0
 // ------------------------------------------------------------------------------------------------- fork
 
 // Row b becomes row parents[b] of the table as it was.  A CTA holds `cols` columns of all rows in shared
-// memory, so that rows can be taken from one another in place.
+// memory, so that rows can be taken from one another in place; one more CTA does the same with the lengths.
 __global__ void __launch_bounds__(512) pool_fork_kernel(PoolForkLaunch a, int cols_shift) {
   extern __shared__ int32_t fork_smem[];
   after_the_one_before();
   const PoolDev& p = a.pool;
   const int cols = 1 << cols_shift, c0 = blockIdx.x << cols_shift;
+  if (c0 >= p.max_pages) {
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) fork_smem[b] = a.lengths[b];
+    __syncthreads();
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+      const int q = a.parents[b];
+      if (q >= p.B) set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
+      if (q < p.B && q != b) a.lengths[b] = q < 0 ? 0 : fork_smem[q];
+    }
+    return;
+  }
   const int n = p.B << cols_shift;
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
     const int b = i >> cols_shift, c = c0 + (i & (cols - 1));
@@ -45,22 +59,15 @@ __global__ void __launch_bounds__(512) pool_fork_kernel(PoolForkLaunch a, int co
     if (is_page(p, was)) atomicAdd(p.refs + was, -1);
     if (is_page(p, is)) atomicAdd(p.refs + is, 1);
   }
-  if (blockIdx.x) return;
-  __syncthreads();
-  for (int b = threadIdx.x; b < p.B; b += blockDim.x) fork_smem[b] = a.lengths[b];
-  __syncthreads();
-  for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
-    const int q = a.parents[b];
-    if (q >= p.B) set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
-    if (q < p.B && q != b) a.lengths[b] = q < 0 ? 0 : fork_smem[q];
-  }
 }
 
 cudaError_t launch_pool_fork(const PoolForkLaunch& L, cudaStream_t s) {
-  // Columns of a CTA: 32 (a row's 128 bytes) where they fit 96 KB, else fewer.
-  int shift = 5;
+  // Columns of a CTA: up to 32 (a row's 128 bytes), as few as spread the table over 64 CTAs (256 sequences of 28
+  // pages: one CTA took 19.0 us), and no more than fit 96 KB.
+  int shift = 0;
+  while (shift < 5 && (L.pool.max_pages >> shift) > 64) ++shift;
   while (shift > 0 && ((long long)L.pool.B << shift) > 24576) --shift;
-  const unsigned grid = (unsigned)((L.pool.max_pages + (1 << shift) - 1) >> shift);
+  const unsigned grid = (unsigned)((L.pool.max_pages + (1 << shift) - 1) >> shift) + 1;
   // (the attribute is set at the largest size, once on each device)
   const int need = L.pool.B << shift;
   if (need * 4 <= 48 * 1024) return launch_early<pool_fork_kernel>(grid, 512, need * 4, s, L, shift);
@@ -73,6 +80,7 @@ cudaError_t launch_pool_fork(const PoolForkLaunch& L, cudaStream_t s) {
 struct PlanShared {
   long long warp[32];
   long long sum[2];  // of this CTA: read by the others
+  int count[32];
 };
 
 // Sum of x over the threads before this one; total: over all.
@@ -109,13 +117,54 @@ __device__ __forceinline__ long long count_pages(const PoolDev& p, int from, int
   return total;
 }
 
+template <int CTAS>
+__device__ __forceinline__ void sync_cluster(cg::cluster_group& cluster) {
+  if constexpr (CTAS == 1)
+    __syncthreads();
+  else
+    cluster.sync();
+}
+
+// Calls f(page, held, pages before it that are as WANTED) for the pages of a slice, `at` being those before the slice, until
+// `at` has reached `most`: 8192 pages a turn, a warp 256 consecutive ones.
+template <bool FREE, typename F>
+__device__ __forceinline__ void each_page(const PoolDev& p, int from, int to, long long at, long long most, PlanShared& sh,
+                                          F f) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int c = from; c < to && at < most; c += 8 * kPlanThreads) {
+    const int first = c + 256 * warp + lane;
+    int ref[8];
+    unsigned mask[8];
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ref[j] = first + 32 * j < to ? p.refs[first + 32 * j] : 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      mask[j] = __ballot_sync(kFull, first + 32 * j < to && (ref[j] == 0) == FREE);
+      n += __popc(mask[j]);
+    }
+    __syncthreads();
+    if (lane == 0) sh.count[warp] = n;
+    __syncthreads();
+    const int other = sh.count[lane], total = __reduce_add_sync(kFull, other);
+    long long before = at + __reduce_add_sync(kFull, lane < warp ? other : 0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (first + 32 * j < to) f(first + 32 * j, ref[j] != 0, before + __popc(mask[j] & ((1u << lane) - 1u)));
+      before += __popc(mask[j]);
+    }
+    at += total;
+  }
+}
+
 // One number of each CTA of the cluster: the sum of those before this one, and of all.
+template <int CTAS>
 __device__ __forceinline__ long long before_in_cluster(cg::cluster_group& cluster, long long* mine, int rank,
                                                        long long& total) {
   long long before = 0;
   total = 0;
-  for (int r = 0; r < kPlanCtas; ++r) {
-    const long long x = *cluster.map_shared_rank(mine, r);
+  for (int r = 0; r < CTAS; ++r) {
+    const long long x = CTAS == 1 ? *mine : *cluster.map_shared_rank(mine, r);
     if (r < rank) before += x;
     total += x;
   }
@@ -159,8 +208,8 @@ __device__ __forceinline__ bool takes_fresh(const PoolDev& p, int entry, int& ol
 //   3. it lists its free pages by rank, as far as they are needed;
 //   4. its sequences take the pages of their ranks; 5. the pages that were replaced lose a reference (only now:
 //      up to here whether a page is shared is read).
-__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
-    pool_reserve_kernel(PoolReserveLaunch a) {
+template <int CTAS>
+__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kPlanThreads) pool_reserve_kernel(PoolReserveLaunch a) {
   __shared__ PlanShared sh;
   after_the_one_before();
   cg::cluster_group cluster = cg::this_cluster();
@@ -169,7 +218,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   const int lane = tid % kSeqLanes, group = tid / kSeqLanes;
   constexpr int kGroups = kPlanThreads / kSeqLanes;
   const unsigned lanes = 0xffu << (tid & 24);  // the group's lanes of its warp
-  const int slice = (p.n_pages + kPlanCtas - 1) / kPlanCtas, part = (p.B + kPlanCtas - 1) / kPlanCtas;
+  const int slice = (p.n_pages + CTAS - 1) / CTAS, part = (p.B + CTAS - 1) / CTAS;
   const int p0 = min(rank * slice, p.n_pages), p1 = min(p0 + slice, p.n_pages);
   const int b0 = min(rank * part, p.B), b1 = min(b0 + part, p.B);
   int32_t* at_of = a.ws.per_seq;
@@ -197,11 +246,11 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     sh.sum[0] = mine;
     sh.sum[1] = need_here;
   }
-  cluster.sync();
+  sync_cluster<CTAS>(cluster);
   // 2.
   long long free_all, need_all;
-  long long at_page = before_in_cluster(cluster, &sh.sum[0], rank, free_all);
-  long long at_need = before_in_cluster(cluster, &sh.sum[1], rank, need_all);
+  const long long at_page = before_in_cluster<CTAS>(cluster, &sh.sum[0], rank, free_all);
+  long long at_need = before_in_cluster<CTAS>(cluster, &sh.sum[1], rank, need_all);
   for (int c = b0; c < b1; c += kPlanThreads) {
     const int b = c + tid, need = b < b1 ? at_of[b] : 0;
     long long total;
@@ -217,18 +266,12 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   }
   // 3.
   const int list = (int)min(free_all, need_all);
-  for (int c = p0; c < p1 && at_page < list; c += kPlanThreads) {
-    const int i = c + tid;
-    const bool free = i < p1 && p.refs[i] == 0;
-    long long total;
-    const long long r = at_page + scan_block(free, sh, total);
-    if (free && r < list) {
-      a.ws.list_a[r] = i;
-      a.ws.list_b[r] = -1;
-    }
-    at_page += total;
-  }
-  cluster.sync();  // (and what was written before it is there for all of the cluster)
+  each_page<true>(p, p0, p1, at_page, list, sh, [&](int page, bool held, long long r) {
+    if (held || r >= list) return;
+    a.ws.list_a[r] = page;
+    a.ws.list_b[r] = -1;
+  });
+  sync_cluster<CTAS>(cluster);  // (and what was written before it is there for all of the cluster)
   // 4.
   for (int b = b0 + group; b < b1; b += kGroups) {
     int r = at_of[b];
@@ -254,9 +297,9 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
       r += __popc(all);
     }
   }
-  cluster.sync();
+  sync_cluster<CTAS>(cluster);
   // 5.
-  for (int x = rank * kPlanThreads + tid; x < list; x += kPlanCtas * kPlanThreads) {
+  for (int x = rank * kPlanThreads + tid; x < list; x += CTAS * kPlanThreads) {
     const int old = a.ws.list_b[x];
     if (old >= 0) atomicAdd(p.refs + old, -1);
   }
@@ -293,10 +336,15 @@ __global__ void __launch_bounds__(kCopyThreads) pool_copy_kernel(PoolDev p, cons
   }
 }
 
+// Whether one CTA plans.  One CTA / a cluster of eight, us: reserve of 16 sequences, 1200 pages 5.7 / 8.6, 64 and 2300
+// 6.4 / 8.7, 256 and 8000 8.9 / 8.9; compact 5.0 / 7.1, 5.8 / 7.3, 9.9 / 7.3.
+static bool plans_alone(const PoolDev& p) { return p.n_pages <= 4096 && p.B <= 256; }
+
 static unsigned copy_grid(long long jobs) { return (unsigned)(jobs < 152 * 8 ? jobs : 152 * 8); }
 
 cudaError_t launch_pool_reserve(const PoolReserveLaunch& L, cudaStream_t s) {
-  cudaError_t e = launch_early<pool_reserve_kernel>(kPlanCtas, kPlanThreads, 0, s, L);
+  cudaError_t e = plans_alone(L.pool) ? launch_early<pool_reserve_kernel<1>>(1, kPlanThreads, 0, s, L)
+                                      : launch_early<pool_reserve_kernel<kPlanCtas>>(kPlanCtas, kPlanThreads, 0, s, L);
   if (e != cudaSuccess) return e;
   const int pieces = (int)((L.pool.page_bytes + kCopyBytes - 1) / kCopyBytes);
   return launch_early<pool_copy_kernel>(copy_grid((long long)L.pool.B * pieces), kCopyThreads, 0, s, L.pool,
@@ -309,56 +357,49 @@ cudaError_t launch_pool_reserve(const PoolReserveLaunch& L, cudaStream_t s) {
 // Plans a compaction in one cluster.  U pages are in use; the i-th of those at U and behind moves to the i-th
 // free place before U.  With h(p) the pages in use before p: a free place p < U has rank p - h(p), a page p >= U
 // in use has rank h(p) - h(U).
-__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
-    pool_compact_kernel(PoolCompactLaunch a) {
+template <int CTAS>
+__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kPlanThreads) pool_compact_kernel(PoolCompactLaunch a) {
   __shared__ PlanShared sh;
   after_the_one_before();
   cg::cluster_group cluster = cg::this_cluster();
   const PoolDev& p = a.pool;
   const int rank = (int)cluster.block_rank(), tid = threadIdx.x;
-  const int slice = (p.n_pages + kPlanCtas - 1) / kPlanCtas;
+  const int slice = (p.n_pages + CTAS - 1) / CTAS;
   const int p0 = min(rank * slice, p.n_pages), p1 = min(p0 + slice, p.n_pages);
   const long long mine = count_pages<false>(p, p0, p1, sh);
   if (tid == 0) sh.sum[0] = mine;
-  cluster.sync();
+  sync_cluster<CTAS>(cluster);
   long long used_all;
-  int h = (int)before_in_cluster(cluster, &sh.sum[0], rank, used_all);
+  const int h = (int)before_in_cluster<CTAS>(cluster, &sh.sum[0], rank, used_all);
   const int used = (int)used_all;
   const long long below = count_pages<false>(p, p0, max(p0, min(p1, used)), sh);
   if (tid == 0) sh.sum[1] = below;
-  cluster.sync();
+  sync_cluster<CTAS>(cluster);
   long long below_all;
-  before_in_cluster(cluster, &sh.sum[1], rank, below_all);
+  before_in_cluster<CTAS>(cluster, &sh.sum[1], rank, below_all);
   const int h_used = (int)below_all;
   const int moves = used - h_used;
-  for (int c = p0; c < p1; c += kPlanThreads) {
-    const int i = c + tid;
-    const bool held = i < p1 && p.refs[i] != 0;
-    long long total;
-    const int before = h + (int)scan_block(held, sh, total);
-    if (i < p1) {
-      if (i < used) {
-        if (!held) a.ws.list_b[i - before] = i;
-      } else {
-        if (held) a.ws.list_a[before - h_used] = i;
-        a.ws.list_c[i] = i;
-      }
+  each_page<false>(p, p0, p1, h, LLONG_MAX, sh, [&](int page, bool held, long long before) {
+    if (page < used) {
+      if (!held) a.ws.list_b[page - before] = page;
+    } else {
+      if (held) a.ws.list_a[before - h_used] = page;
+      a.ws.list_c[page] = page;
     }
-    h += (int)total;
-  }
+  });
   if (rank == 0 && tid == 0) {
     a.ws.counts[0] = used;
     a.ws.counts[1] = moves;
     *a.used = used;
   }
-  cluster.sync();
-  for (int x = rank * kPlanThreads + tid; x < moves; x += kPlanCtas * kPlanThreads) {
+  sync_cluster<CTAS>(cluster);
+  for (int x = rank * kPlanThreads + tid; x < moves; x += CTAS * kPlanThreads) {
     const int from = a.ws.list_a[x], to = a.ws.list_b[x];
     a.ws.list_c[from] = to;
     p.refs[to] = p.refs[from];
     p.refs[from] = 0;
   }
-  cluster.sync();  // (no CTA leaves while another may still read its sums)
+  sync_cluster<CTAS>(cluster);  // (no CTA leaves while another may still read its sums)
 }
 
 // Moves the pages and renames them in the table.  (Pages come from behind U and go before it: no order among them.)
@@ -383,7 +424,8 @@ __global__ void __launch_bounds__(kCopyThreads) pool_move_kernel(PoolCompactLaun
 }
 
 cudaError_t launch_pool_compact(const PoolCompactLaunch& L, cudaStream_t s) {
-  cudaError_t e = launch_early<pool_compact_kernel>(kPlanCtas, kPlanThreads, 0, s, L);
+  cudaError_t e = plans_alone(L.pool) ? launch_early<pool_compact_kernel<1>>(1, kPlanThreads, 0, s, L)
+                                      : launch_early<pool_compact_kernel<kPlanCtas>>(kPlanCtas, kPlanThreads, 0, s, L);
   if (e != cudaSuccess) return e;
   const int pieces = (int)((L.pool.page_bytes + kCopyBytes - 1) / kCopyBytes);
   const long long jobs = (long long)(L.pool.n_pages / 2) * pieces;  // at most half of the pages move
