@@ -170,8 +170,12 @@ cudaError_t launch_cache_append(const CacheAppendLaunch& L, cudaStream_t s);
 cudaError_t launch_cache_read(const CacheReadLaunch& L, cudaStream_t s);
 cudaError_t launch_cache_attend_bf16(const CacheAttendLaunch& L, cudaStream_t s);
 cudaError_t launch_cache_attend_e2m1(const CacheAttendLaunch& L, cudaStream_t s);
-cudaError_t launch_cache_score_bf16(const CacheAttendLaunch& L, cudaStream_t s);
-cudaError_t launch_cache_score_e2m1(const CacheAttendLaunch& L, cudaStream_t s);
+cudaError_t launch_cache_window_bf16(const CacheAttendLaunch& L, cudaStream_t s);
+cudaError_t launch_cache_window_e2m1(const CacheAttendLaunch& L, cudaStream_t s);
+cudaError_t launch_cache_bias_bf16(const CacheAttendLaunch& L, cudaStream_t s);
+cudaError_t launch_cache_bias_e2m1(const CacheAttendLaunch& L, cudaStream_t s);
+cudaError_t launch_cache_cap_bf16(const CacheAttendLaunch& L, cudaStream_t s);
+cudaError_t launch_cache_cap_e2m1(const CacheAttendLaunch& L, cudaStream_t s);
 size_t cache_part_bytes();
 
 }  // namespace pisa

@@ -219,7 +219,9 @@ static int cache_attention(const pisa_paged_cache* cache, const pisa_rows* q, in
   const bool bf16 = cache->kind == PISA_CACHE_BF16;
   if (score) {
     L.score = *score;
-    const auto launch = bf16 ? launch_cache_score_bf16 : launch_cache_score_e2m1;
+    const auto launch = score->cap > 0.f ? (bf16 ? launch_cache_cap_bf16 : launch_cache_cap_e2m1)
+                        : score->slopes  ? (bf16 ? launch_cache_bias_bf16 : launch_cache_bias_e2m1)
+                                         : (bf16 ? launch_cache_window_bf16 : launch_cache_window_e2m1);
     return cuda_code(launch(L, static_cast<cudaStream_t>(stream)));
   }
   const auto launch = bf16 ? launch_cache_attend_bf16 : launch_cache_attend_e2m1;

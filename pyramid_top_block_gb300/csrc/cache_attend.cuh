@@ -31,6 +31,15 @@
 
 namespace pisa {
 
+// What is done to the scores: a kernel for each, as what the others need would take registers and instructions from it (window
+// alone 78.3 instead of XXX us in 4 bits, 82.6 instead of XXX in bf16, three queries).
+enum ScoreMode {
+  kPlain,   // nothing, and no window
+  kWindow,  // a window (or none, as below)
+  kBias,    // a bias by distance
+  kCapped,  // a cap, with or without a bias
+};
+
 constexpr int kPartFloats = 16 * 64 + 32;  // a partial result: O [16][64], row maxima, row sums
 constexpr int kCaGrid = 152;               // CTAs of the split form: one on each SM
 constexpr int kCaMinTiles = 12;            // places of the stream that a run has at least
@@ -159,8 +168,9 @@ struct RowState {
   float o[8][4];
   bool bad;  // a page out of range was met
   // the scored forms:
-  float t0, t1;          // factors of the scores of rows g and g + 8
-  float slope0, slope1;  // what a token's distance takes off, base 2
+  float t0, t1;        // with a cap: factors of the scores of rows g and g + 8
+  float bias0, bias1;  // what a token's distance takes off (base 2; without a cap over the logit factor)
+  int from0, from1;    // this lane's first key of a tile less the rows' positions
   int bad_rows;          // bits 0 and 1: rows g and g + 8 see a page out of range
 };
 
@@ -222,11 +232,11 @@ __device__ __forceinline__ void reset(RowState<KIND>& s) {
 // infinity; rows below 2^-100 have logits of zero, whatever becomes of them.  A factor of the
 // logits that is past the range of 32 bits is cut to it: logits of zero stay so, and others, if
 // they fit 32 bits at all, still differ by far more than weights can show.
-template <int KIND, bool SCORED>
+template <int KIND, int MODE>
 __device__ __forceinline__ void make_q(const CacheAttendLaunch& a, const QueryWords& q, const Unit& u, int lane,
                                        RowState<KIND>& s) {
   const int j = lane & 3;
-  constexpr float kFactor = SCORED ? kScale : kScale * kLog2e;  // (scored: base 2 comes with the logits)
+  constexpr float kFactor = kScale * kLog2e;
   float f[2] = {kFactor, kFactor};
   if (KIND == PISA_CACHE_E2M1) {
     uint32_t w[2][8];
@@ -238,7 +248,9 @@ __device__ __forceinline__ void make_q(const CacheAttendLaunch& a, const QueryWo
       t = max(t & 0xffffu, t >> 16);
       t = max(t, __shfl_xor_sync(kFull, t, 1));
       t = max(t, __shfl_xor_sync(kFull, t, 2));
-      const int e = max(min((int)(t >> 7) - 127, 126), -100);  // the largest lies in [2^e, 2^(e + 1))
+      // the largest lies in [2^e, 2^(e + 1)) (scored: rows below 2^-60 have products of zero, so that a bias fits 32 bits
+      // over the factor)
+      const int e = max(min((int)(t >> 7) - 127, 126), MODE != kPlain ? -60 : -100);
       const float down = exp2i(-e);
       f[h] = fminf(f[h] * exp2i(e) * exp2i(a.cache.k_exp), 0x1.fffffep127f);
 #pragma unroll
@@ -274,19 +286,28 @@ __device__ __forceinline__ void make_q(const CacheAttendLaunch& a, const QueryWo
         s.qa[ks][2 + h] = hi;
       }
   }
-  if constexpr (SCORED) {
-    s.t0 = f[0];
-    s.t1 = f[1];
-    s.f0 = s.f1 = 1.f;
-    s.slope0 = s.slope1 = 0.f;
+  s.f0 = f[0];
+  s.f1 = f[1];
+  if constexpr (MODE == kBias || MODE == kCapped) {
+    s.bias0 = s.bias1 = 0.f;
     const int r0 = u.r0 + (lane >> 2), r1 = r0 + 8;
     if (a.score.slopes) {
-      if (r0 < u.rows) s.slope0 = a.score.slopes[u.kv * a.G + r0 % a.G] * kLog2e;
-      if (r1 < u.rows) s.slope1 = a.score.slopes[u.kv * a.G + r1 % a.G] * kLog2e;
+      if (r0 < u.rows) s.bias0 = a.score.slopes[u.kv * a.G + r0 % a.G] * kLog2e;
+      if (r1 < u.rows) s.bias1 = a.score.slopes[u.kv * a.G + r1 % a.G] * kLog2e;
     }
-  } else {
-    s.f0 = f[0];
-    s.f1 = f[1];
+    // this lane's keys of a tile lie from 2 j (bf16) or j (4 bits) on; a row's position is n - 1 of what it sees
+    const int base = u.n - a.T + u.t_first, at = KIND == PISA_CACHE_BF16 ? 2 * j : j;
+    s.from0 = at - (base + r0 / a.G);
+    s.from1 = at - (base + r1 / a.G);
+  }
+  if constexpr (MODE == kCapped) {  // the factors to base 2 come with the cap
+    s.t0 = f[0] * (1.f / kLog2e);
+    s.t1 = f[1] * (1.f / kLog2e);
+    s.f0 = s.f1 = 1.f;
+  }
+  if constexpr (MODE == kBias) {
+    s.bias0 /= f[0];
+    s.bias1 /= f[1];
   }
 }
 
@@ -378,8 +399,9 @@ struct Weights {
 
 // The products of two tiles, their instructions side by side: the logits of the tile staged
 // at st_k (QK), and O += P V for the tile staged at st_v with the weights w (PV).
-template <int KIND, int U, int NP, bool QK, bool PV>
-__device__ __forceinline__ void products(uint32_t st_k, uint32_t st_v, int lane, RowState<KIND>& s,
+// BIAS: the logits begin with the bias of their distances (RowState::bias0) in place of zeros.
+template <int KIND, int U, int NP, bool QK, bool PV, bool BIAS>
+__device__ __forceinline__ void products(uint32_t st_k, uint32_t st_v, int first, int lane, RowState<KIND>& s,
                                          float (&sc)[Cfg<KIND>::KT / 8][4], const Weights<KIND, NP>& w) {
   constexpr int KT = Cfg<KIND>::KT;
   const int g = lane >> 2, j = lane & 3;
@@ -389,6 +411,18 @@ __device__ __forceinline__ void products(uint32_t st_k, uint32_t st_v, int lane,
       float(&d0)[4] = sc[2 * i];
       float(&d1)[4] = sc[2 * i + 1];
       d0[0] = d0[1] = d0[2] = d0[3] = d1[0] = d1[1] = d1[2] = d1[3] = 0.f;
+      if constexpr (BIAS) {
+        // (distances are whole numbers, exact up to 2^24)
+        constexpr float kNext = KIND == PISA_CACHE_BF16 ? 1.f : 4.f;  // keys from an element to the next
+        const unsigned long long b0 = f2_pack(s.bias0, s.bias0), b1 = f2_pack(s.bias1, s.bias1);
+        const float x0 = s.bias0 * (float)(first + s.from0), x1 = s.bias1 * (float)(first + s.from1);
+        const unsigned long long y0 = f2_pack(x0, x0), y1 = f2_pack(x1, x1);
+        const unsigned long long k0 = f2_pack(16.f * i, 16.f * i + kNext), k1 = f2_pack(16.f * i + 8, 16.f * i + 8 + kNext);
+        f2_unpack(f2_fma(b0, k0, y0), d0[0], d0[1]);
+        f2_unpack(f2_fma(b1, k0, y1), d0[2], d0[3]);
+        f2_unpack(f2_fma(b0, k1, y0), d1[0], d1[1]);
+        f2_unpack(f2_fma(b1, k1, y1), d1[2], d1[3]);
+      }
       if (KIND == PISA_CACHE_E2M1) {
         using L = E2m1Tile<U>;
         const int key = (g >> 1) + 4 * (g & 1);
@@ -448,23 +482,22 @@ struct Sight {
   int l_lo, l_hi;  // the least, the largest l
 };
 
-// The scored forms: a tile's products as base-2 logits (s.f0 and s.f1 are 1 from here on).
+// Scores with a cap: a tile's products as base-2 logits (s.f0 and s.f1 are 1).
 template <int KIND>
-__device__ __forceinline__ void score(const CacheAttendLaunch& a, int first, const Sight& see, int lane,
-                                      const RowState<KIND>& s, float (&sc)[Cfg<KIND>::KT / 8][4]) {
+__device__ __forceinline__ void score(const CacheAttendLaunch& a, int first, int lane, const RowState<KIND>& s,
+                                      float (&sc)[Cfg<KIND>::KT / 8][4]) {
   constexpr int KT = Cfg<KIND>::KT;
-  const int j = lane & 3;
-  if (a.score.cap > 0.f && a.score.cap <= kCapExp && !a.out_f32) {
+  const float top = a.score.cap * kLog2e;
+  if (a.score.cap <= kCapExp && !a.out_f32) {
     // by exponentials, whose units have nothing else to do here; the polynomial would share the multiply-add
-    // units with the scales of the 4-bit pages (16 x 131072 tokens 96.1 instead of XXX us)
+    // units with the scales of the 4-bit pages (16 x 131072 tokens 91.6 us, by the polynomial 96.1)
     const float two0 = 2.f * kLog2e * s.t0 * a.score.inv_cap, two1 = 2.f * kLog2e * s.t1 * a.score.inv_cap;
-    const float top = a.score.cap * kLog2e;
 #pragma unroll
     for (int nt = 0; nt < KT / 8; ++nt) {
       cap_exp(sc[nt][0], sc[nt][1], two0, top);
       cap_exp(sc[nt][2], sc[nt][3], two1, top);
     }
-  } else if (a.score.cap > 0.f) {
+  } else {
     const CapRow r0 = {s.t0 * a.score.inv_cap, s.t0 * kLog2e}, r1 = {s.t1 * a.score.inv_cap, s.t1 * kLog2e};
     float b0 = 0.f, b1 = 0.f;
 #pragma unroll
@@ -474,7 +507,6 @@ __device__ __forceinline__ void score(const CacheAttendLaunch& a, int first, con
     }
     // (a NaN passes the comparison unseen, and the polynomial keeps it)
     if (__any_sync(kFull, b0 * r0.to_y > 1.f || b1 * r1.to_y > 1.f)) {
-      const float top = a.score.cap * kLog2e;
 #pragma unroll
       for (int nt = 0; nt < KT / 8; ++nt)
 #pragma unroll
@@ -489,48 +521,39 @@ __device__ __forceinline__ void score(const CacheAttendLaunch& a, int first, con
         cap_small(sc[nt][2], sc[nt][3], r1);
       }
     }
-  } else {
-    const float t0 = s.t0 * kLog2e, t1 = s.t1 * kLog2e;
-#pragma unroll
-    for (int nt = 0; nt < KT / 8; ++nt) {
-      sc[nt][0] *= t0;
-      sc[nt][1] *= t0;
-      sc[nt][2] *= t1;
-      sc[nt][3] *= t1;
-    }
   }
   if (a.score.slopes) {
-    // (distances are whole numbers, exact up to 2^24; the row's own position is n - 1)
-    const float d0 = (float)(first - see.n0 + 1), d1 = (float)(first - see.n1 + 1);
+    constexpr float kNext = KIND == PISA_CACHE_BF16 ? 1.f : 4.f;
+    const unsigned long long b0 = f2_pack(s.bias0, s.bias0), b1 = f2_pack(s.bias1, s.bias1);
+    const float x0 = s.bias0 * (float)(first + s.from0), x1 = s.bias1 * (float)(first + s.from1);
+    const unsigned long long y0 = f2_pack(x0, x0), y1 = f2_pack(x1, x1);
 #pragma unroll
-    for (int nt = 0; nt < KT / 8; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float k = (float)(16 * (nt >> 1) + 8 * (nt & 1)) + (KIND == PISA_CACHE_BF16 ? 2 * j + e : j + 4 * e);
-        sc[nt][e] = fmaf(s.slope0, d0 + k, sc[nt][e]);
-        sc[nt][2 + e] = fmaf(s.slope1, d1 + k, sc[nt][2 + e]);
-      }
+    for (int nt = 0; nt < KT / 8; ++nt) {
+      const unsigned long long k = f2_pack(8.f * nt, 8.f * nt + kNext);
+      f2_unpack(f2_add(f2_pack(sc[nt][0], sc[nt][1]), f2_fma(b0, k, y0)), sc[nt][0], sc[nt][1]);
+      f2_unpack(f2_add(f2_pack(sc[nt][2], sc[nt][3]), f2_fma(b1, k, y1)), sc[nt][2], sc[nt][3]);
+    }
   }
 }
 
 // The running softmax: logits to weights.  O must hold all earlier tiles.
-template <int KIND, int U, int NP, bool SCORED>
+template <int KIND, int U, int NP, int MODE>
 __device__ __forceinline__ void weigh(const CacheAttendLaunch& a, uint32_t st, int first, const Sight& see, int lane,
                                       RowState<KIND>& s, float (&sc)[Cfg<KIND>::KT / 8][4], Weights<KIND, NP>& w,
                                       float* scratch) {
   using C = Cfg<KIND>;
   constexpr int KT = C::KT;
   const int g = lane >> 2, j = lane & 3;
-  if constexpr (SCORED) score<KIND>(a, first, see, lane, s, sc);
-  const bool masked = first + KT > see.n_lo || (SCORED && first < see.l_hi);
+  if constexpr (MODE == kCapped) score<KIND>(a, first, lane, s, sc);
+  const bool masked = first + KT > see.n_lo || (MODE != kPlain && first < see.l_hi);
   if (masked) {
 #pragma unroll
     for (int nt = 0; nt < KT / 8; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int key = first + 16 * (nt >> 1) + key_of<KIND>(nt & 1, j, e);
-        if (key >= see.n0 || (SCORED && key < see.l0)) sc[nt][e] = -INFINITY;
-        if (key >= see.n1 || (SCORED && key < see.l1)) sc[nt][2 + e] = -INFINITY;
+        if (key >= see.n0 || (MODE != kPlain && key < see.l0)) sc[nt][e] = -INFINITY;
+        if (key >= see.n1 || (MODE != kPlain && key < see.l1)) sc[nt][2 + e] = -INFINITY;
       }
   }
   // A row's reference m is, where it was last set, the maximum of its logits so far less kShift; it is
@@ -617,7 +640,7 @@ __device__ __forceinline__ void weigh(const CacheAttendLaunch& a, uint32_t st, i
     // one by one to the rows that see them, and cleared like the rest.
     const int k_lo = min(max(see.n_lo - first, 0), KT), k_hi = min(max(see.n_hi - first, 0), KT);
     // (the same for the tokens between the rows' first ones)
-    const int z_lo = SCORED ? min(max(see.l_lo - first, 0), KT) : 0, z_hi = SCORED ? min(max(see.l_hi - first, 0), KT) : 0;
+    const int z_lo = MODE != kPlain ? min(max(see.l_lo - first, 0), KT) : 0, z_hi = MODE != kPlain ? min(max(see.l_hi - first, 0), KT) : 0;
     const auto one_by_one = [&](int from, int to) {  // at most 16 keys
 #pragma unroll
       for (int nt = 0; nt < KT / 8; ++nt)
@@ -648,14 +671,14 @@ __device__ __forceinline__ void weigh(const CacheAttendLaunch& a, uint32_t st, i
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            if (first + key < see.n0 && (!SCORED || first + key >= see.l0)) s.o[i][e] = fmaf(p0, v[e], s.o[i][e]);
-            if (first + key < see.n1 && (!SCORED || first + key >= see.l1)) s.o[i][2 + e] = fmaf(p1, v[e], s.o[i][2 + e]);
+            if (first + key < see.n0 && (MODE == kPlain || first + key >= see.l0)) s.o[i][e] = fmaf(p0, v[e], s.o[i][e]);
+            if (first + key < see.n1 && (MODE == kPlain || first + key >= see.l1)) s.o[i][2 + e] = fmaf(p1, v[e], s.o[i][2 + e]);
           }
         }
       }
       __syncwarp();
     };
-    if constexpr (SCORED) {
+    if constexpr (MODE != kPlain) {
       // keys z_hi .. k_lo - 1 are seen by all rows (none, where the windows are shorter than the rows are apart)
       const int to = min(z_hi, k_hi);
       if (z_lo < to) one_by_one(z_lo, to);  // (at most 15 keys: those between the first and the last query's window)
@@ -701,7 +724,7 @@ __device__ __forceinline__ void weigh(const CacheAttendLaunch& a, uint32_t st, i
 // three stages: while one is on its way, the logits of the next tile and the products with V
 // of the one before are computed side by side.  (Keys and values in rings of their own, with
 // two tiles on their way, were 2 to 4 % slower: the memory system is full with one.)
-template <int KIND, int U, int NP, int W, bool LIST, bool SCORED>
+template <int KIND, int U, int NP, int W, bool LIST, int MODE>
 __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit& u, const QueryWords& q,
                                           const int (&blk)[2], int i0, int i1, uint32_t ring, float* scratch, int warp,
                                           int lane, RowState<KIND>& s) {
@@ -720,28 +743,33 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
   const int last = min(u.rows, u.r0 + 16) - 1;
   Sight see = {ra < u.rows ? base + ra / a.G : 0, rb < u.rows ? base + rb / a.G : 0, base + u.r0 / a.G,
                base + last / a.G, 0, 0, 0, 0};
-  if constexpr (SCORED) {
+  if constexpr (MODE != kPlain) {
     const int w = a.score.window;
     see.l0 = max(see.n0 - w, 0);
     see.l1 = max(see.n1 - w, 0);
     see.l_lo = max(see.n_lo - w, 0);
     see.l_hi = max(see.n_hi - w, 0);
   }
+  int farther = 0;  // how much farther the nearest token in sight is than the query itself
   int* list = reinterpret_cast<int*>(scratch);  // (listed: a row tile is one query's, so weigh leaves it alone)
   if (listed) {  // the listed blocks that count, in the order of the list
     unsigned some[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       some[h] = __ballot_sync(kFull, blk[h] >= 0 && blk[h] < (1 << 21) && blk[h] * kC < see.n_hi &&
-                                         (!SCORED || blk[h] * kC + kC > see.l_lo));
+                                         (MODE == kPlain || blk[h] * kC + kC > see.l_lo));
     const unsigned below = (1u << lane) - 1u;
     if (some[0] >> lane & 1) list[__popc(some[0] & below)] = blk[0];
     if (some[1] >> lane & 1) list[__popc(some[0]) + __popc(some[1] & below)] = blk[1];
     __syncwarp();
     i1 = (__popc(some[0]) + __popc(some[1])) * (kC / KT);
+    if constexpr (MODE == kBias || MODE == kCapped) {
+      const int near = max(some[0] >> lane & 1 ? blk[0] * kC + kC : 0, some[1] >> lane & 1 ? blk[1] * kC + kC : 0);
+      farther = max(see.n_hi - __reduce_max_sync(kFull, near), 0);
+    }
   } else {
     i1 = min(i1, (max(see.n_hi, 0) + KT - 1) / KT);
-    if constexpr (SCORED) i0 = max(i0, see.l_lo / KT);
+    if constexpr (MODE != kPlain) i0 = max(i0, see.l_lo / KT);
   }
   const int mine = i1 - i0 > warp ? (i1 - i0 - warp + W - 1) / W : 0;  // the warp's tiles
   if (mine == 0) return;
@@ -761,7 +789,7 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
     int* first_bad = reinterpret_cast<int*>(scratch + kBadAt / 4);
     if (y < mine) {
       const int p = first_of(y) + (lane % E) * U;
-      if (p < see.n_hi && (!SCORED || p + kLen > see.l_lo)) {
+      if (p < see.n_hi && (MODE == kPlain || p + kLen > see.l_lo)) {
         page = table[p >> a.cache.page_shift];
         if (page >= 0 && page < a.cache.n_pages) {
           off = cache_record(a.cache, C::kRow, page, u.kv, p);
@@ -772,7 +800,7 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
         }
       }
     }
-    if constexpr (SCORED) {
+    if constexpr (MODE != kPlain) {
       for (unsigned m = __ballot_sync(kFull, page < 0); m; m &= m - 1) {
         const int p = __shfl_sync(kFull, page < 0 ? first_of(y) + (lane % E) * U : 0, __ffs(m) - 1);
         if (p < see.n0 && p + kLen > see.l0) s.bad_rows |= 1;
@@ -816,12 +844,16 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
   cpa_commit();
   if (mine > 1) issue(1, ring + kStage);
   cpa_commit();
-  make_q<KIND, SCORED>(a, q, u, lane, s);
+  make_q<KIND, MODE>(a, q, u, lane, s);
+  if constexpr (MODE == kBias || MODE == kCapped) {  // (the bias is taken relative to the nearest token's: far ones' would drown the scores in 32 bits)
+    s.from0 += farther;
+    s.from1 += farther;
+  }
   cpa_wait<1>();
   __syncwarp();
   const int f0 = first_of(0);
-  products<KIND, U, NP, true, false>(ring, 0, lane, s, sc, w);
-  weigh<KIND, U, NP, SCORED>(a, ring, f0, see, lane, s, sc, w, scratch);
+  products<KIND, U, NP, true, false, MODE == kBias>(ring, 0, f0, lane, s, sc, w);
+  weigh<KIND, U, NP, MODE>(a, ring, f0, see, lane, s, sc, w, scratch);
   uint32_t cur = ring, next = ring + kStage, spare = ring + 2 * kStage;
   for (int x = 0; x + 1 < mine; ++x) {
     if (x + 2 < mine) {
@@ -831,22 +863,22 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
     cpa_commit();
     cpa_wait<1>();  // tile x + 1 has come
     __syncwarp();
-    products<KIND, U, NP, true, true>(next, cur, lane, s, sc, w);
-    weigh<KIND, U, NP, SCORED>(a, next, first_of(x + 1), see, lane, s, sc, w, scratch);
+    products<KIND, U, NP, true, true, MODE == kBias>(next, cur, first_of(x + 1), lane, s, sc, w);
+    weigh<KIND, U, NP, MODE>(a, next, first_of(x + 1), see, lane, s, sc, w, scratch);
     __syncwarp();  // the reads of tile x are done before its stage is refilled
     const uint32_t t = cur;
     cur = next;
     next = spare;
     spare = t;
   }
-  products<KIND, U, NP, false, true>(0, cur, lane, s, sc, w);
+  products<KIND, U, NP, false, true, false>(0, cur, 0, lane, s, sc, w);
   cpa_wait<0>();
   if (s.far) {
     const float4 z = reinterpret_cast<const float4*>(scratch + kFarAt / 4)[lane];
     s.m0 = z.z;
     s.m1 = z.w;
   }
-  if constexpr (SCORED) {
+  if constexpr (MODE != kPlain) {
     if (s.bad_rows & 1) s.l0 = __int_as_float(0x7fc00000);
     if (s.bad_rows & 2) s.l1 = __int_as_float(0x7fc00000);
   } else if (s.bad) {  // the rows that see a page out of range become NaN
@@ -946,14 +978,14 @@ __device__ __forceinline__ int seq_len(const CacheAttendLaunch& a, int b, bool& 
 }
 
 // The first tile that any query of a sequence of n tokens sees, and how many there are.
-template <int KIND, bool SCORED>
+template <int KIND, int MODE>
 __device__ __forceinline__ int first_tile(const CacheAttendLaunch& a, int n) {
-  return SCORED ? max(n - a.T + 1 - a.score.window, 0) / Cfg<KIND>::KT : 0;
+  return MODE != kPlain ? max(n - a.T + 1 - a.score.window, 0) / Cfg<KIND>::KT : 0;
 }
-template <int KIND, bool SCORED>
+template <int KIND, int MODE>
 __device__ __forceinline__ int unit_tiles(const CacheAttendLaunch& a, int n) {
   constexpr int KT = Cfg<KIND>::KT;
-  return (n + KT - 1) / KT - first_tile<KIND, SCORED>(a, n);
+  return (n + KT - 1) / KT - first_tile<KIND, MODE>(a, n);
 }
 
 // Places that a unit of nt tiles has in the stream: its tiles, and some for what a run spends at
@@ -967,11 +999,11 @@ __device__ __forceinline__ int unit_places(int nt) {
 }
 
 // Places of all units before sequence b (b = B: of all): every warp computes it by itself.
-template <int KIND, bool SCORED>
+template <int KIND, int MODE>
 __device__ __forceinline__ long long places_before(const CacheAttendLaunch& a, int b, int units, int lane) {
   long long sum = 0;
   bool over;
-  for (int i = lane; i < b; i += 32) sum += unit_places<KIND>(unit_tiles<KIND, SCORED>(a, seq_len(a, i, over)));
+  for (int i = lane; i < b; i += 32) sum += unit_places<KIND>(unit_tiles<KIND, MODE>(a, seq_len(a, i, over)));
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(kFull, sum, x);
   return sum * units;
@@ -979,13 +1011,13 @@ __device__ __forceinline__ long long places_before(const CacheAttendLaunch& a, i
 
 // The sequence that place `at` of the stream belongs to, and the places before that sequence: 32
 // sequences at a time.
-template <int KIND, bool SCORED>
+template <int KIND, int MODE>
 __device__ __forceinline__ int seq_of(const CacheAttendLaunch& a, long long at, int units, int lane, long long& base) {
   base = 0;
   for (int b0 = 0; b0 < a.cache.B; b0 += 32) {
     bool over;
     const int n = b0 + lane < a.cache.B ? seq_len(a, b0 + lane, over) : 0;
-    const long long t = (long long)unit_places<KIND>(unit_tiles<KIND, SCORED>(a, n)) * units;
+    const long long t = (long long)unit_places<KIND>(unit_tiles<KIND, MODE>(a, n)) * units;
     long long inc = t;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
@@ -1016,7 +1048,7 @@ constexpr int attend_smem() {
   return kRing<KIND, W> + W * (kScratch + 2 * 16 * 4);
 }
 
-template <int KIND, int U, int NP, int W, bool SCORED>
+template <int KIND, int U, int NP, int W, int MODE>
 __global__ void __launch_bounds__(W * 32, Cfg<KIND>::kWarps / W) cache_attend_direct_kernel(CacheAttendLaunch a) {
   using C = Cfg<KIND>;
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (uniform to the compiler)
@@ -1054,7 +1086,7 @@ __global__ void __launch_bounds__(W * 32, Cfg<KIND>::kWarps / W) cache_attend_di
   fetch_q(a, u, lane, q);
   RowState<KIND> s;
   reset(s);
-  run_tiles<KIND, U, NP, W, true, SCORED>(a, u, q, blk, 0, 1 << 30, ring, scratch, warp, lane, s);
+  run_tiles<KIND, U, NP, W, true, MODE>(a, u, q, blk, 0, 1 << 30, ring, scratch, warp, lane, s);
   if ((threadIdx.x == 0 && over) || (lane == 0 && s.bad)) set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
   merge_warps<KIND, W>(s, mo, ml, warp, lane);
   for (int i = threadIdx.x; i < 256; i += W * 32) {
@@ -1064,7 +1096,7 @@ __global__ void __launch_bounds__(W * 32, Cfg<KIND>::kWarps / W) cache_attend_di
   }
 }
 
-template <int KIND, int U, int NP, bool SCORED>
+template <int KIND, int U, int NP, int MODE>
 __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_kernel(CacheAttendLaunch a) {
   using C = Cfg<KIND>;
   constexpr int W = C::kWarps;
@@ -1081,7 +1113,7 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_
   // this CTA's run of the stream (and its row tile, where the row tiles go side by side)
   const int RT = (a.T * a.G + 15) / 16;
   const int units = a.cache.Hkv * (C::kSide ? 1 : RT);  // of a sequence
-  const long long total = places_before<KIND, SCORED>(a, a.cache.B, units, lane);
+  const long long total = places_before<KIND, MODE>(a, a.cache.B, units, lane);
   const long long per = run_length(total, C::kSide ? gridDim.x / RT : gridDim.x);
   long long cur = per * (C::kSide ? blockIdx.x / RT : blockIdx.x);
   const long long end = cur + per < total ? cur + per : total;
@@ -1100,13 +1132,13 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_
     }
   if (cur >= end) return;  // (CTAs left over where RT does not divide the grid, too)
   long long base;  // places before sequence u.b
-  u.b = seq_of<KIND, SCORED>(a, cur, units, lane, base);
+  u.b = seq_of<KIND, MODE>(a, cur, units, lane, base);
   u.t_first = 0;
   u.rows = a.T * a.G;
   u.sel = nullptr;
   while (cur < end) {
     u.n = seq_len(a, u.b, over);
-    const int nt = unit_tiles<KIND, SCORED>(a, u.n);  // tiles of a unit of this sequence
+    const int nt = unit_tiles<KIND, MODE>(a, u.n);  // tiles of a unit of this sequence
     const int places = unit_places<KIND>(nt);
     if (nt == 0 || cur >= base + (long long)places * units) {  // on to the next sequence
       base += (long long)places * units;
@@ -1126,8 +1158,8 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_
     QueryWords q;
     fetch_q(a, u, lane, q);
     reset(s);
-    const int t0 = first_tile<KIND, SCORED>(a, u.n);
-    run_tiles<KIND, U, NP, W, false, SCORED>(a, u, q, blk, t0 + i0, t0 + i1, ring, scratch, warp, lane, s);
+    const int t0 = first_tile<KIND, MODE>(a, u.n);
+    run_tiles<KIND, U, NP, W, false, MODE>(a, u, q, blk, t0 + i0, t0 + i1, ring, scratch, warp, lane, s);
     if ((threadIdx.x == 0 && over) || (lane == 0 && s.bad)) set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
     merge_warps<KIND, W>(s, mo, ml, warp, lane);
     if (threadIdx.x < 256) {
@@ -1158,7 +1190,7 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_
 // The kernel starts while the one before it runs, and reads the lengths, which that one only
 // reads too; the partial results after the wait, which every CTA passes (a grid that ended
 // without it would let the next kernel of the stream overtake the one before).
-template <int KIND, bool FEW, bool SCORED>
+template <int KIND, bool FEW, int MODE>
 __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, int grid) {
   constexpr int KT = Cfg<KIND>::KT;
   constexpr int kRows = FEW ? 1 : 4, kGroups = 16 / kRows;
@@ -1171,7 +1203,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, in
   const int RT = (a.T * a.G + 15) / 16, side = kSide ? RT : 1;
   const int runs = kSide ? grid / RT : grid, units = kSide ? a.cache.Hkv : a.cache.Hkv * RT;
   const int row = (int)(blockIdx.x % (16 / kRows)) * kRows + rq;
-  const long long total = places_before<KIND, SCORED>(a, a.cache.B, units, lane);
+  const long long total = places_before<KIND, MODE>(a, a.cache.B, units, lane);
   const long long per = run_length(total, runs);
   Unit u;
   int c0, c1 = 0;  // the runs that hold its tiles
@@ -1192,8 +1224,8 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, in
     set_unit(un);
     bool over;
     u.n = seq_len(a, u.b, over);
-    const int nt = unit_tiles<KIND, SCORED>(a, u.n);
-    const long long w0 = places_before<KIND, SCORED>(a, u.b, units, lane) + (long long)un * unit_places<KIND>(nt);
+    const int nt = unit_tiles<KIND, MODE>(a, u.n);
+    const long long w0 = places_before<KIND, MODE>(a, u.b, units, lane) + (long long)un * unit_places<KIND>(nt);
     c0 = (int)(w0 / per);
     c1 = (int)((w0 + nt - 1) / per);
     cut = nt != 0 && c0 != c1;
@@ -1205,7 +1237,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, in
     cut = end < total;
     if (cut) {
       long long base;
-      u.b = seq_of<KIND, SCORED>(a, end - 1, units, lane, base);
+      u.b = seq_of<KIND, MODE>(a, end - 1, units, lane, base);
       bool over;
       u.n = seq_len(a, u.b, over);
       const int nt = (u.n + KT - 1) / KT, places = unit_places<KIND>(nt);
@@ -1261,9 +1293,9 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, in
   write_out(a, u, row, quad, acc, l);
 }
 
-template <int KIND, int U, int NP, int W, bool SCORED>
+template <int KIND, int U, int NP, int W, int MODE>
 static cudaError_t launch_direct(const CacheAttendLaunch& L, unsigned units, cudaStream_t s) {
-  return launch_early<cache_attend_direct_kernel<KIND, U, NP, W, SCORED>>(units, W * 32, attend_smem<KIND, W>(), s, L);
+  return launch_early<cache_attend_direct_kernel<KIND, U, NP, W, MODE>>(units, W * 32, attend_smem<KIND, W>(), s, L);
 }
 
 // Whether the direct form takes whole caches of up to `cap` tokens.  It saves the second kernel and
@@ -1277,40 +1309,40 @@ inline bool takes_direct(long long cap, long long units) {
   return cap <= (most > 2048 ? most : 2048);
 }
 
-template <int KIND, int U, int NP, bool SCORED>
+template <int KIND, int U, int NP, int MODE>
 static cudaError_t launch_attend(const CacheAttendLaunch& L, cudaStream_t s) {
   using C = Cfg<KIND>;
   const int RT = (L.T * L.G + 15) / 16;
   long long cap = (long long)L.cache.max_pages << L.cache.page_shift;
-  if (SCORED && cap > L.score.window + L.T) cap = L.score.window + L.T;  // (what a unit sees at most)
+  if (MODE != kPlain && cap > L.score.window + L.T) cap = L.score.window + L.T;  // (what a unit sees at most)
   const long long units = (long long)L.cache.B * L.cache.Hkv * (L.idx ? L.T : RT);
   if (L.idx || takes_direct(cap, units)) {
     // The more units there are, the fewer warps share one out, so that all CTAs run at once
     // (128 x 2 units of 32 blocks: six warps 15.1 us, four 18.7, twelve 19.1).
-    if (units <= kCaGrid) return launch_direct<KIND, U, NP, C::kWarps, SCORED>(L, (unsigned)units, s);
-    if (units <= 2 * kCaGrid) return launch_direct<KIND, U, NP, C::kHalf, SCORED>(L, (unsigned)units, s);
-    return launch_direct<KIND, U, NP, C::kThird, SCORED>(L, (unsigned)units, s);
+    if (units <= kCaGrid) return launch_direct<KIND, U, NP, C::kWarps, MODE>(L, (unsigned)units, s);
+    if (units <= 2 * kCaGrid) return launch_direct<KIND, U, NP, C::kHalf, MODE>(L, (unsigned)units, s);
+    return launch_direct<KIND, U, NP, C::kThird, MODE>(L, (unsigned)units, s);
   }
-  cudaError_t e = launch_early<cache_attend_split_kernel<KIND, U, NP, SCORED>>(kCaGrid, C::kWarps * 32,
+  cudaError_t e = launch_early<cache_attend_split_kernel<KIND, U, NP, MODE>>(kCaGrid, C::kWarps * 32,
                                                                        attend_smem<KIND, C::kWarps>(), s, L);
   if (e != cudaSuccess) return e;
   if (units <= kCaGrid / 4)
-    return launch_early<cache_join_kernel<KIND, true, SCORED>>((unsigned)units * 16, 256, 0, s, L, kCaGrid);
-  return launch_early<cache_join_kernel<KIND, false, SCORED>>(kCaGrid * 4, 256, 0, s, L, kCaGrid);
+    return launch_early<cache_join_kernel<KIND, true, MODE>>((unsigned)units * 16, 256, 0, s, L, kCaGrid);
+  return launch_early<cache_join_kernel<KIND, false, MODE>>(kCaGrid * 4, 256, 0, s, L, kCaGrid);
 }
 
-template <int KIND, int U, bool SCORED>
+template <int KIND, int U, int MODE>
 static cudaError_t launch_attend_u(const CacheAttendLaunch& L, cudaStream_t s) {
   constexpr int NP = KIND == PISA_CACHE_BF16 ? 2 : 1;  // parts of the weights (see weigh)
-  return L.out_f32 ? launch_attend<KIND, U, NP + 1, SCORED>(L, s) : launch_attend<KIND, U, NP, SCORED>(L, s);
+  return L.out_f32 ? launch_attend<KIND, U, NP + 1, MODE>(L, s) : launch_attend<KIND, U, NP, MODE>(L, s);
 }
 
-template <int KIND, bool SCORED>
+template <int KIND, int MODE>
 static cudaError_t launch_attend_k(const CacheAttendLaunch& L, cudaStream_t s) {
   switch (L.cache.rec_shift) {
-    case 4: return launch_attend_u<KIND, 16, SCORED>(L, s);
-    case 5: return launch_attend_u<KIND, 32, SCORED>(L, s);
-    default: return launch_attend_u<KIND, 64, SCORED>(L, s);
+    case 4: return launch_attend_u<KIND, 16, MODE>(L, s);
+    case 5: return launch_attend_u<KIND, 32, MODE>(L, s);
+    default: return launch_attend_u<KIND, 64, MODE>(L, s);
   }
 }
 

@@ -6,7 +6,7 @@ namespace pisa {
 size_t cache_part_bytes() { return part_bytes(); }
 
 cudaError_t launch_cache_attend_bf16(const CacheAttendLaunch& L, cudaStream_t s) {
-  return launch_attend_k<PISA_CACHE_BF16, false>(L, s);
+  return launch_attend_k<PISA_CACHE_BF16, kPlain>(L, s);
 }
 
 }  // namespace pisa

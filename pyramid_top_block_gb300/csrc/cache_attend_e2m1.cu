@@ -4,7 +4,7 @@
 namespace pisa {
 
 cudaError_t launch_cache_attend_e2m1(const CacheAttendLaunch& L, cudaStream_t s) {
-  return launch_attend_k<PISA_CACHE_E2M1, false>(L, s);
+  return launch_attend_k<PISA_CACHE_E2M1, kPlain>(L, s);
 }
 
 }  // namespace pisa

@@ -45,6 +45,9 @@ def check(got, want):
 
 @pytest.mark.parametrize("bits", [16, 4])
 @pytest.mark.parametrize("B,T,G,Hkv,page,lengths,window,cap,slopes,scale", [
+    (2, 3, 8, 2, 64, [20000, 300], 0, 0.0, True, 1.0),
+    (1, 2, 4, 1, 32, [5000], 0, 0.0, True, 2.0 ** -70),       # queries so small that the bias alone decides
+    (1, 2, 4, 1, 32, [500], 0, 500.0, True, 3.0),             # a cap taken by the polynomial
     (1, 1, 1, 1, 16, [1], 0, 5.0, True, 3.0),
     (2, 1, 16, 2, 64, [300, 0], 0, 2.0, False, 4.0),          # scores past the cap
     (3, 1, 8, 2, 64, [4097, 65, 64], 64, 0.0, False, 1.0),
@@ -77,7 +80,16 @@ def test_scores_with_listed_blocks(bits):
     cache = make_cache(g, 2, 1100, 2, 64, bits)
     q, lengths = normal(g, 2, 1, 16, 64) * 2, [1090, 200]
     idx = i32([[[0, 4, 9, 16, 17], [16, 3, -1, 2, 15]], [[3, 0, -1, -1, -1], [1, 2, 3, -1, -1]]])
-    window, cap, s = 150, 4.0, slopes_of(16)
+    check_listed(cache, q, lengths, idx, 150, 4.0, slopes_of(16))
+    # far blocks alone: the bias of the nearest one would drown the scores in 32 bits
+    cache = make_cache(g, 2, 90000, 2, 64, bits)
+    idx = i32([[[0, 4, 9, -1], [2, 1, -1, 700]], [[3, 0, -1, -1], [1, 2, 3, 1200]]])
+    check_listed(cache, q, [90000, 77000], idx, 0, 0.0, slopes_of(16) * 4)
+    check_listed(cache, q, [90000, 77000], idx, 0, 3.0, slopes_of(16))
+
+
+def check_listed(cache, q, lengths, idx, window, cap, s):
+    bits = cache.bits
     ws = pisa.cache_workspace(cache)
     got = pisa.cache_attention(q, cache, i32(lengths), idx=idx, workspace=ws, cap=cap, slopes=s, window=window)
     assert status(ws) == 0
@@ -89,14 +101,15 @@ def test_scores_with_listed_blocks(bits):
             for x in idx[b, kv].tolist():
                 if x >= 0:
                     listed[64 * x:64 * x + 64] = True
-            listed[:max(0, n - window)] = False
+            if window:
+                listed[:max(0, n - window)] = False
             at = listed.nonzero()[:, 0]
             heads = slice(8 * kv, 8 * kv + 8)
             if at.numel() == 0:
                 assert not got[b, 0, heads].any()
                 continue
             x = q[b, 0, heads].double() @ k[at, kv].T / 8
-            x = cap * torch.tanh(x / cap) - s[heads, None].double() * (n - 1 - at)
+            x = (cap * torch.tanh(x / cap) if cap else x) - s[heads, None].double() * (n - 1 - at)
             p = torch.softmax(x, -1)
             o, pv = p @ v[at, kv], p @ v[at, kv].abs()
             big = (q[b, 0, heads].double().abs() @ k[at, kv].abs().T / 8).amax(1, keepdim=True)
