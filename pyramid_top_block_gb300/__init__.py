@@ -860,7 +860,7 @@ class PagePool:
     """
 
     __slots__ = ("pages", "table", "refs", "page_size", "B", "n_pages", "max_pages", "device", "_struct", "_ref",
-                 "_index")
+                 "_index", "_need")
 
     def __init__(self, pages: torch.Tensor, table: torch.Tensor, refs: torch.Tensor, page_size: int):
         if page_size not in (16, 32, 64, 128, 256):
@@ -885,6 +885,7 @@ class PagePool:
         self._struct = _PoolStruct(pages.data_ptr(), table.data_ptr(), refs.data_ptr(), stride, size, self.B, page_size,
                                    self.n_pages, self.max_pages)
         self._ref = ctypes.byref(self._struct)
+        self._need = int(load().pisa_pool_workspace_bytes(self.n_pages, self.B))
 
     @classmethod
     def allocate(cls, B: int, n_cap: int, Hkv: int, n_pages: int, page_size: int = 64, bits: int = 16, layers: int = 1,
@@ -905,7 +906,7 @@ class PagePool:
 
 
 def pool_workspace_bytes(pool: PagePool) -> int:
-    return int(load().pisa_pool_workspace_bytes(pool.n_pages, pool.B))
+    return pool._need
 
 
 def pool_workspace(pool: PagePool) -> torch.Tensor:
@@ -923,7 +924,7 @@ def cache_fork(pool: PagePool, parents: torch.Tensor, lengths: torch.Tensor, wor
     if guard is not None:
         with guard:
             return cache_fork(pool, parents, lengths, workspace)
-    _check((_lib or load()).pisa_cache_fork(
+    _check(_lib.pisa_cache_fork(
         pool._ref, _per_sequence(parents, "parents", pool), _per_sequence(lengths, "lengths", pool),
         None if workspace is None else _cache_ws(workspace, pool, 4), _current(pool)), "pisa_cache_fork")
 
@@ -941,11 +942,10 @@ def cache_reserve(pool: PagePool, lengths: torch.Tensor, T: int, counts: torch.T
             return cache_reserve(pool, lengths, T, counts, granted, workspace)
     if granted is None:
         granted = torch.empty(pool.B, dtype=torch.int32, device=pool.device)
-    lib = _lib or load()
-    need = int(lib.pisa_pool_workspace_bytes(pool.n_pages, pool.B))
+    need = pool._need
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=pool.device)
-    _check(lib.pisa_cache_reserve(
+    _check(_lib.pisa_cache_reserve(
         pool._ref, _per_sequence(lengths, "lengths", pool), T,
         None if counts is None else _per_sequence(counts, "counts", pool), _per_sequence(granted, "granted", pool),
         _cache_ws(workspace, pool, need), need, _current(pool)), "pisa_cache_reserve")
@@ -964,11 +964,10 @@ def cache_compact(pool: PagePool, used: torch.Tensor | None = None, workspace: t
         used = torch.empty(1, dtype=torch.int32, device=pool.device)
     elif used.dtype is not torch.int32 or used.shape != (1,) or used.get_device() != pool._index:
         raise ValueError("used must be an int32 tensor [1] on the pool's device")
-    lib = _lib or load()
-    need = int(lib.pisa_pool_workspace_bytes(pool.n_pages, pool.B))
+    need = pool._need
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=pool.device)
-    _check(lib.pisa_cache_compact(pool._ref, used.data_ptr(), _cache_ws(workspace, pool, need), need, _current(pool)),
+    _check(_lib.pisa_cache_compact(pool._ref, used.data_ptr(), _cache_ws(workspace, pool, need), need, _current(pool)),
            "pisa_cache_compact")
     return used
 

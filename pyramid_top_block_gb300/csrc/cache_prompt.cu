@@ -527,6 +527,15 @@ __device__ __forceinline__ bool soften_scored(const CachePromptLaunch& a, Prompt
     float v[kKeys];
     tmem_ld128_top<true>(s, v, size);
   }
+  // at least the row's largest logit: the nearer end of the line adds the more (or the less negative)
+  float b = cap ? cap_any(size, r.cap, a.score.cap * kLog2e) : size * r.f;
+  // (from kFar on, an exact product less a rounded reference may be far from zero for the largest: see soften)
+  const bool far = __any_sync(kFull, b >= kFar);
+  if (slopes) {
+    const float d0 = (float)(key0 - r.pos), d1 = d0 + (float)(kKeys - 1), least = (float)abs(r.pos - r.nearest);
+    const float near = d0 > 0.f ? d0 : d1 < 0.f ? -d1 : 0.f, most = fmaxf(fabsf(d0), fabsf(d1));
+    b -= r.slope * ((r.slope > 0.f ? near : most) - least);
+  }
   ScoreForm form = kAnyScore;
   if (cap && !slopes) {
     if (!__any_sync(kFull, size * r.cap.to_y > 0.5f))
@@ -535,15 +544,8 @@ __device__ __forceinline__ bool soften_scored(const CachePromptLaunch& a, Prompt
       form = kCapWhole;
     else if (a.score.cap <= kCapExp)
       form = kCapFar;
-  } else if (!cap && !__any_sync(kFull, key0 + kKeys > r.pos + 1 && r.hi > r.pos + 1)) {
+  } else if (!cap && !far && !__any_sync(kFull, b >= kFar || (key0 + kKeys > r.pos + 1 && r.hi > r.pos + 1))) {
     form = kLine;  // (rows that see no later tokens than their own: such are masked)
-  }
-  // at least the row's largest logit: the nearer end of the line adds the more (or the less negative)
-  float b = cap ? cap_any(size, r.cap, a.score.cap * kLog2e) : size * r.f;
-  if (slopes) {
-    const float d0 = (float)(key0 - r.pos), d1 = d0 + (float)(kKeys - 1), least = (float)abs(r.pos - r.nearest);
-    const float near = d0 > 0.f ? d0 : d1 < 0.f ? -d1 : 0.f, far = fmaxf(fabsf(d0), fabsf(d1));
-    b -= r.slope * ((r.slope > 0.f ? near : far) - least);
   }
   bool waited = k == 0;
   if (__any_sync(kFull, b > r.m + PCfg<KIND>::kTop)) {
@@ -986,10 +988,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   // the piece of it
   u.i1 -= min(piece.k0, u.i1 - u.i0);
   u.i0 = max(u.i0, u.i1 - (piece.k1 - piece.k0));
-  if (threadIdx.x == kPromptThreads - 1) {  // (read after many barriers)
+  if (threadIdx.x == 0) {
     sh.unit = u;
     sh.slot = piece.slot;
   }
+  __syncthreads();
   bool ok = true;
   if (warp < kSoftWarps) {
     r.f = KIND == PISA_CACHE_E2M1 ? sh.factor[threadIdx.x] : SCORED ? kScale : kScale * kLog2e;

@@ -96,6 +96,11 @@ def spans(kind, start, counts, T, seed=0):
     (1, 200, 4, 1, 64, [100], [200], "prefix", 0, 300.0, False),
     (1, 200, 4, 1, 64, [100], [200], "causal", 0, 0.75, True),
     (2, 530, 16, 1, 64, [6000, 12000], [530, 100], "causal", 0, 8.0, True),
+    (1, 40, 16, 1, 64, [20000], [40], "prefix", 0, 0.0, False),      # listed spans, in pieces
+    (2, 20, 8, 2, 128, [9000, 17000], [20, 9], "any", 0, 0.0, True),
+    (1, 90, 4, 1, 16, [12345], [90], "documents", 7000, 30.0, False),
+    (2, 18, 16, 3, 32, [25000, 300], [18, 18], "causal", 0, 0.0, False),
+    (40, 3, 4, 2, 64, [11 * b for b in range(40)], [b % 4 for b in range(40)], "causal", 0, 0.0, False),
 ])
 def test_prompt_attention(bits, B, T, G, Hkv, page, start, counts, kind, window, cap, slopes):
     g = gen(T * 10 + page)
@@ -222,6 +227,116 @@ def test_large_scores():
         want = v.repeat_interleave(4, 1).permute(1, 0, 2)[torch.arange(8, device=DEV), two.indices[..., 0]]
         off = (got[0].double() - want).abs()
         assert bool((off[sure] <= 2.0 ** -7 * want[sure].abs()).all())
+
+
+def test_large_scores_with_slopes():
+    """The same with a bias by distance, which they drown."""
+    g = gen(32)
+    for bits, scale in ((16, 2.0 ** 30), (4, 2.0 ** 40), (16, 2.0 ** 14), (4, 2.0 ** 16)):
+        cache = make_cache(g, 1, 700, 1, 64, bits)
+        T, at = 250, 400
+        q = normal(g, 1, T, 4, 64) * scale
+        s = slopes_of(4)
+        for got in (pisa.cache_prompt_attention(q, cache, i32([at]), slopes=s)[0],
+                    torch.cat([pisa.cache_attention(q[:, t:t + 10], cache, i32([at + t + 10]), slopes=s)[0]
+                               for t in range(0, T, 10)])):
+            assert bool(torch.isfinite(got).all())
+            k, v = ref.tokens(cache, 0, at + T)
+            j, p = torch.arange(at + T, device=DEV), at + torch.arange(T, device=DEV)
+            x = torch.einsum("thd,nd->thn", q[0].double(), k[:, 0]) / 8 - s.double()[:, None] * (p[:, None, None] - j).abs()
+            x = torch.where((j <= p[:, None])[:, None], x, -INF)
+            two = x.topk(2, -1)
+            mag = torch.einsum("thd,nd->thn", q[0].double().abs(), k[:, 0].abs()).amax(-1) / 8
+            sure = two.values[..., 0] - two.values[..., 1] > 100 + 2.0 ** -14 * mag
+            assert bool(sure.any())
+            want = v[:, 0][two.indices[..., 0]]
+            assert bool(((got.double() - want).abs()[sure] <= 2.0 ** -7 * want[sure].abs()).all())
+
+
+def test_nobody_sees_anything():
+    """Whole row tiles without a token: zeros, whatever the output held; rows behind the count as they were."""
+    g = gen(33)
+    cache = make_cache(g, 2, 9000, 2, 64, 16)
+    for T, start in ((300, [0, 100]), (20, [8000, 70])):
+        q = normal(g, 2, T, 8, 64)
+        first = torch.full((2, T), 1 << 29, dtype=torch.int32, device=DEV)
+        first[1, T // 2:] = 0
+        out = torch.full((2, T, 8, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+        counts = [T, T - 3]
+        pisa.cache_prompt_attention(q, cache, i32(start), counts=i32(counts), first=first, out=out)
+        check(out, expected(q, cache, start, counts, first))
+        last = torch.zeros(2, T, dtype=torch.int32, device=DEV)
+        out.fill_(7.0)
+        pisa.cache_prompt_attention(q, cache, i32(start), counts=i32([0, 1]), last=last, out=out)
+        assert not bool(out[1, 0].any()) and bool((out[0] == 7).all()) and bool((out[1, 1:] == 7).all())
+
+
+@pytest.mark.parametrize("T,cap", [(300, 1000), (24, 40000)])
+def test_captured_with_other_starts_and_counts(T, cap):
+    """A call in a graph, replayed with other contents: both forms of the kernel; two graphs that share a workspace, one
+    after the other."""
+    g = gen(T)
+    for bits in (16, 4):
+        cache = make_cache(g, 2, cap, 2, 64, bits)
+        q, start, counts = normal(g, 2, T, 8, 64), i32([5, 0]), i32([T, T])
+        out, ws = torch.zeros_like(q), pisa.cache_workspace(cache)
+        step = lambda: pisa.cache_prompt_attention(q, cache, start, counts=counts, out=out, workspace=ws)  # noqa: E731
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step()
+        torch.cuda.current_stream().wait_stream(side)
+        graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+        for cg in graphs:
+            with torch.cuda.graph(cg):
+                step()
+        for i, (a, c) in enumerate((([cap - T, 3], [T, 2]), ([0, cap // 2], [1, T]), ([cap // 3, 0], [T - 1, 0]))):
+            start.copy_(i32(a))
+            counts.copy_(i32(c))
+            q.copy_(normal(g, 2, T, 8, 64))
+            out.fill_(7.0)
+            graphs[i % 2].replay()
+            check(out, expected(q, cache, a, c))
+        assert status(ws) == 0
+
+
+def test_two_streams_with_workspaces_of_their_own():
+    g = gen(41)
+    cache = make_cache(g, 1, 30000, 2, 64, 4)
+    qs = [normal(g, 1, 40, 16, 64), normal(g, 1, 700, 16, 64)]
+    starts = [i32([29000]), i32([100])]
+    want = [pisa.cache_prompt_attention(q, cache, s).clone() for q, s in zip(qs, starts)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    wss = [pisa.cache_workspace(cache) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [pisa.cache_prompt_attention(q, cache, s, workspace=w, stream=st)
+               for q, s, w, st in zip(qs, starts, wss, streams)]
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_pages_past_four_gigabytes():
+    """Pages of a pool of layers whose distance from the first is more than 2^32 bytes."""
+    g = gen(42)
+    for bits in (16, 4):
+        Hkv, page, n = 2, 256, 1300
+        inner = (Hkv, 4, 2, 64, 64) if bits == 16 else (Hkv, 4, 72 * 64)
+        per = torch.Size(inner).numel() * (2 if bits == 16 else 1)
+        layers = -(-(5 << 30) // (per * 40))  # forty pages of so many layers are more than 5 GB
+        pool = torch.empty((40, layers) + inner, dtype=torch.bfloat16 if bits == 16 else torch.uint8, device=DEV)
+        small = make_cache(g, 1, n, Hkv, page, bits)
+        table = torch.arange(39, 39 - small.table.shape[1], -1, dtype=torch.int32, device=DEV)[None].contiguous()
+        far = pool[:, layers - 1]
+        far[table[0].long()] = small.pages[small.table[0].long()]
+        cache = pisa.PagedCache(far, table, page)
+        q, start = normal(g, 1, 200, 8, 64), i32([n - 200])
+        assert torch.equal(pisa.cache_prompt_attention(q, cache, start), pisa.cache_prompt_attention(q, small, start))
+        a, b = (pisa.cache_attention(q[:, -1:], c, start + 200, window=900, cap=5.0) for c in (cache, small))
+        assert torch.equal(a, b)
+        del pool, far, cache
 
 
 def test_far_positions_and_slopes():
