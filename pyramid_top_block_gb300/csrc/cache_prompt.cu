@@ -27,6 +27,7 @@ namespace pisa {
 // tokens at 16384.)
 constexpr int kRuns = kPromptRuns, kMaxUnits = kPromptUnits;
 constexpr int kUnitEnd = 4;            // places of the stream that a unit counts beside its tiles: what its begin and end cost
+constexpr int kMinRun = 4;             // places that a run has at least
 constexpr int kPartRow = 66;           // a partial result, for each of 256 rows: O [64], reference, sum of weights
 constexpr int kRowsTile = 128, kRowsCta = 256, kKeys = 128;
 constexpr int kSoftWarps = 8, kLoadWarps = 2, kPromptThreads = (kSoftWarps + kLoadWarps + 2) * 32;
@@ -88,7 +89,6 @@ struct PromptShared {
   float factor[kRowsCta];              // 4-bit pages: the rows' logit factors
 };
 
-// What of a CTA's rows a warp needs to know.
 // Whether some row of the CTA does not see some key of the tile.
 __device__ __forceinline__ bool mixed_tile(const PromptShared& sh, int tile) {
   return tile * kKeys < sh.lo_max || (tile + 1) * kKeys > sh.hi_min;
@@ -791,7 +791,7 @@ __global__ void __launch_bounds__(1024) cache_prompt_plan_kernel(CachePromptLaun
     if (x == units - 1) place[units] = at;
   }
   __syncthreads();
-  const int total = place[units], per = (total + kRuns - 1) / kRuns;
+  const int total = place[units], per = max((total + kRuns - 1) / kRuns, kMinRun);
   if (tid < kRuns) a.plan.cut[tid] = make_int2(-1, 0);
   __syncthreads();
   // the pieces: one begins with each unit, and one with each run

@@ -125,8 +125,8 @@ __device__ __forceinline__ void sync_cluster(cg::cluster_group& cluster) {
     cluster.sync();
 }
 
-// Calls f(page, held, pages before it that are as WANTED) for the pages of a slice, `at` being those before the slice, until
-// `at` has reached `most`: 8192 pages a turn, a warp 256 consecutive ones.
+// Calls f(page, held, rank) for the pages of a slice, rank being the number of free pages (FREE) or of held ones before
+// it, `at` before the slice; ends when `at` has reached `most`.  8192 pages a turn, a warp 256 consecutive ones.
 template <bool FREE, typename F>
 __device__ __forceinline__ void each_page(const PoolDev& p, int from, int to, long long at, long long most, PlanShared& sh,
                                           F f) {
