@@ -404,7 +404,9 @@ int pisa_cache_attention_scored(const pisa_paged_cache* cache, const pisa_rows* 
  *   cap, slopes, window : as above
  *   out    : device bf16 [B, T, Hq, d] dense, 16-byte aligned
  *   ws     : workspace of pisa_cache_workspace_bytes(), 256-byte aligned
- * T from 1 up, B * T * Hq < 2^30; Hq/Hkv in {1, 2, 4, 8, 16}.  Rows that see nothing, infinities,
+ * T from 1 up, B * T * Hq < 2^30; Hq/Hkv in {1, 2, 4, 8, 16}.  Sums, scores and softmax in fp32; the
+ * weights enter the product with V as one bf16 part (bf16 pages: 8 bits, as the result has) or one
+ * fp16 part (4-bit pages).  Rows that see nothing, infinities,
  * NaNs and pages out of range as above; a sequence that ends past the table's capacity is cut
  * to it, one that starts before 0 has no tokens there, and PISA_ERR_DEVICE_BOUNDS is flagged.
  */
