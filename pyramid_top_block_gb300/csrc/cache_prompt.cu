@@ -15,6 +15,7 @@
 
 #include <climits>
 #include <mutex>
+#include <type_traits>
 
 #include <cudaTypedefs.h>
 
@@ -449,64 +450,157 @@ __device__ __forceinline__ bool soften(PromptShared& sh, PromptRow& r, uint32_t 
   return true;
 }
 
-// The same for scores that are not plain products.  Their arithmetic is two to six times as long, so it is kept in a loop over
-// 64 columns at a time, which read S once more (unrolled over all 128 the longer forms do not fit the instruction
-// cache: a cap that the scores pass took 1557 us instead of 307 for 1216 tokens at 16384).
+// The same for scores that are not plain products.  What bounds it is the arithmetic units: two packed operations take four
+// clocks a scheduler, so that a cap's short polynomial (5 a pair) and the sums take 1536 for the two warps' rows, next to
+// 1024 of the exponentials.  So both stand in one block, where one unit works beside the other (apart: 240 instead of
+// 208 us for 1216 tokens at 16384), and the row's factors are in the polynomial's coefficients (7 a pair: 231).
+// The usual tile (whole, within the short polynomial or a line, no new reference) comes from the registers that its maximum
+// came with (read once more: 208 instead of 182 us, with slopes 173 instead of 161).  The rest is a loop over 64 columns, which
+// reads S again: the longer forms unrolled over all 128 do not fit the instruction cache.  (A shorter polynomial up to
+// a quarter of the cap: 168 instead of 177 us where it is enough, 321 instead of 269 where all forms take turns.)
+enum PromptMode {  // a kernel for each: with all forms in one the usual ones have fewer registers (231 instead of 211 us)
+  kPromptPlain,
+  kPromptCapped,  // a cap of kCapExp or less
+  kPromptBias,
+  kPromptEither,  // a larger cap, or a cap and a bias
+};
 enum ScoreForm {
-  kCapHalf,   // capped, |score| at most half the cap: a short polynomial
-  kCapWhole,  // capped, |score| at most the cap: a longer one
-  kCapFar,    // capped at 128 or less: exponentials
-  kLine,      // a bias, where no row of the warp sees a later token than its own: a line
-  kAnyScore,  // anything else
+  kCapHalf,     // capped, |score| at most half the cap: a short polynomial
+  kCapWhole,    // capped, |score| at most the cap: a longer one
+  kCapFar,      // capped at kCapExp or less: exponentials
+  kCapAny,      // capped at more: either, and a choice
+  kCapFarBias,  // the last two with a bias
+  kCapAnyBias,
+  kLine,        // a bias, where no row of the warp sees a later token than its own: a line
+  kBias,        // a bias
 };
 
-// 64 products of a row, of the keys from key0 on, as logits less a reference (m2: minus the reference, twice).
+// Factors of the short polynomial: logit = x (c[0] + x x (c[1] + ..)), x the product.  They stay in range for
+// kCapLeast <= to_y <= kCapMost; 4-bit pages' products are below 2^19, so that there what falls below the range is
+// below 2^-20 of the logit.
+struct CapPoly {
+  float c[TanhHalf::n];
+};
+constexpr float kCapLeast = 0x1p-18f, kCapMost = 0x1p18f;
+__device__ __forceinline__ CapPoly cap_poly(const CapRow& r) {
+  constexpr TanhHalf k;
+  CapPoly p;
+  float f = r.to_l;
+#pragma unroll
+  for (int i = 0; i < TanhHalf::n; ++i, f = f * r.to_y * r.to_y) p.c[i] = k.c[i] * f;
+  return p;
+}
+
+// Products of a row, of the keys from key0 on, as logits less a reference (m2: minus the reference, twice).
+template <ScoreForm FORM>
+struct Logits {
+  static constexpr bool kAny = FORM == kCapAny || FORM == kCapAnyBias, kFarther = FORM == kCapFar || FORM == kCapFarBias || kAny;
+  static constexpr bool kAway = FORM == kCapFarBias || FORM == kCapAnyBias || FORM == kBias;
+  static constexpr int n = FORM == kCapHalf ? TanhHalf::n : FORM == kCapWhole || kAny ? Tanh::n : 1;
+  unsigned long long f, two, top2, c, p[n];
+  float top1, slope, d0, least;
+
+  __device__ __forceinline__ Logits(const CachePromptLaunch& a, const PromptRow& r, int key0, unsigned long long m2) {
+    const float top = a.score.cap * kLog2e;
+    c = m2;
+    if constexpr (FORM == kCapHalf) {
+      const CapPoly q = cap_poly(r.cap);
+#pragma unroll
+      for (int i = 0; i < n; ++i) p[i] = f2_pack(q.c[i], q.c[i]);
+    } else if constexpr (FORM == kCapWhole || kAny) {
+      constexpr Tanh k;
+      f = f2_pack(r.cap.to_y, r.cap.to_y);
+#pragma unroll
+      for (int i = 0; i < n; ++i) p[i] = f2_pack(top * k.c[i], top * k.c[i]);
+    } else if constexpr (FORM == kLine || FORM == kBias) {
+      f = f2_pack(r.f, r.f);
+    }
+    if constexpr (kFarther) {
+      const float x = 2.f * kLog2e * r.cap.to_y;
+      two = f2_pack(x, x);
+      top2 = f2_pack(-2.f * top, -2.f * top);
+      c = f2_add(m2, f2_pack(top, top));
+    }
+    if constexpr (FORM == kLine) {
+      const float bias = r.slope * (float)(key0 - r.nearest);  // of the first key, relative to the nearest one in sight
+      slope = r.slope;
+      c = f2_add(m2, f2_pack(bias, bias));
+    }
+    if constexpr (kAway) {  // -slope (|p - j| - |p - nearest|): whole numbers, exact up to 2^24
+      slope = -r.slope;
+      d0 = (float)(key0 - r.pos);
+      least = (float)abs(r.pos - r.nearest);
+    }
+    if constexpr (kAny || kAway) c = m2;
+    top1 = top;
+  }
+
+  // those of the keys key0 + i and the next
+  __device__ __forceinline__ unsigned long long operator()(int i, float v, float w) const {
+    const unsigned long long x = f2_pack(v, w);
+    unsigned long long z = 0;
+    if constexpr (FORM == kLine) z = f2_fma(x, f, f2_fma(f2_pack(slope, slope), f2_pack((float)i, (float)(i + 1)), c));
+    if constexpr (FORM == kBias) z = f2_mul(x, f);
+    if constexpr (kFarther) {  // (as cap_exp; the reference in its last step where nothing else follows)
+      float e, g;
+      f2_unpack(f2_mul(x, two), e, g);
+      f2_unpack(f2_add(f2_pack(ex2_approx(e), ex2_approx(g)), f2_pack(1.f, 1.f)), e, g);
+      z = f2_fma(f2_pack(rcp_approx(e), rcp_approx(g)), top2, FORM == kCapFar ? c : f2_pack(top1, top1));
+    }
+    if constexpr (FORM == kCapHalf || FORM == kCapWhole || kAny) {
+      const unsigned long long y = FORM == kCapHalf ? x : f2_mul(x, f), u = f2_mul(y, y);
+      unsigned long long q = p[n - 1];
+#pragma unroll
+      for (int j = n - 2; j >= 0; --j) q = f2_fma(q, u, p[j]);
+      if constexpr (kAny) {
+        float y0, y1, z0, z1, q0, q1;
+        f2_unpack(y, y0, y1);
+        f2_unpack(z, z0, z1);
+        f2_unpack(f2_mul(y, q), q0, q1);
+        z = f2_pack(fabsf(y0) <= 1.f ? q0 : z0, fabsf(y1) <= 1.f ? q1 : z1);
+      } else {
+        z = f2_fma(y, q, c);
+      }
+    }
+    if constexpr (kAway) {
+      float z0, z1;
+      f2_unpack(z, z0, z1);
+      z = f2_pack(fmaf(slope, fabsf(d0 + (float)i) - least, z0), fmaf(slope, fabsf(d0 + (float)(i + 1)) - least, z1));
+    }
+    if constexpr (kAny || kAway) z = f2_add(z, c);
+    return z;
+  }
+};
+
+// The form as a constant, to use.
+template <ScoreForm FORM, typename Use>
+__device__ __forceinline__ void use_form(const Use& use) {
+  use(std::integral_constant<ScoreForm, FORM>());
+}
+template <PromptMode MODE, typename Use>
+__device__ __forceinline__ void with_form(ScoreForm form, const Use& use) {
+  if constexpr (MODE == kPromptBias) {
+    if (form == kLine) return use_form<kLine>(use);
+    return use_form<kBias>(use);
+  } else {
+    if (form == kCapHalf) return use_form<kCapHalf>(use);
+    if (form == kCapWhole) return use_form<kCapWhole>(use);
+    if constexpr (MODE == kPromptCapped) return use_form<kCapFar>(use);
+    if (form == kCapAny) return use_form<kCapAny>(use);
+    if (form == kCapFarBias) return use_form<kCapFarBias>(use);
+    return use_form<kCapAnyBias>(use);
+  }
+}
+
+// 64 of them, masked.
+template <PromptMode MODE>
 __device__ __forceinline__ void logits64(const CachePromptLaunch& a, const PromptRow& r, ScoreForm form, bool whole, int key0,
                                          unsigned long long m2, float (&v)[64]) {
-  const unsigned long long fy = f2_pack(r.cap.to_y, r.cap.to_y), fl = f2_pack(r.cap.to_l, r.cap.to_l);
-  if (form == kCapHalf) {
+  with_form<MODE>(form, [&](auto f) {
+    const Logits<f()> logits(a, r, key0, m2);
 #pragma unroll
-    for (int i = 0; i < 64; i += 2) {
-      const unsigned long long x = f2_pack(v[i], v[i + 1]);
-      f2_unpack(f2_fma(f2_mul(x, fl), tanh_ratio<TanhHalf>(f2_mul(x, fy)), m2), v[i], v[i + 1]);
-    }
-  } else if (form == kCapWhole) {
-#pragma unroll
-    for (int i = 0; i < 64; i += 2) {
-      const unsigned long long x = f2_pack(v[i], v[i + 1]);
-      f2_unpack(f2_fma(f2_mul(x, fl), tanh_ratio<Tanh>(f2_mul(x, fy)), m2), v[i], v[i + 1]);
-    }
-  } else if (form == kCapFar) {
-    // (as cap_exp, with the reference in its last step)
-    const float two = 2.f * kLog2e * r.cap.to_y, top = a.score.cap * kLog2e;
-    const unsigned long long fe = f2_pack(two, two), ft = f2_pack(-2.f * top, -2.f * top), one = f2_pack(1.f, 1.f);
-    const unsigned long long mt = f2_add(m2, f2_pack(top, top));
-#pragma unroll
-    for (int i = 0; i < 64; i += 2) {
-      float x, y;
-      f2_unpack(f2_mul(f2_pack(v[i], v[i + 1]), fe), x, y);
-      f2_unpack(f2_add(f2_pack(ex2_approx(x), ex2_approx(y)), one), x, y);
-      f2_unpack(f2_fma(f2_pack(rcp_approx(x), rcp_approx(y)), ft, mt), v[i], v[i + 1]);
-    }
-  } else if (form == kLine) {
-    const float bias = r.slope * (float)(key0 - r.nearest);  // of the first key, relative to the nearest one in sight
-    const unsigned long long f2 = f2_pack(r.f, r.f), sl = f2_pack(r.slope, r.slope), c = f2_add(m2, f2_pack(bias, bias));
-#pragma unroll
-    for (int i = 0; i < 64; i += 2)
-      f2_unpack(f2_fma(f2_pack(v[i], v[i + 1]), f2, f2_fma(sl, f2_pack((float)i, (float)(i + 1)), c)), v[i], v[i + 1]);
-  } else {
-    const bool cap = a.score.cap > 0.f;
-    const float top = a.score.cap * kLog2e;
-    float m, unused;
-    f2_unpack(m2, m, unused);
-    // -slope (|p - j| - |p - nearest|): whole numbers, exact up to 2^24 (without slopes the slope is zero)
-    const float d0 = (float)(key0 - r.pos), least = (float)abs(r.pos - r.nearest);
-#pragma unroll
-    for (int i = 0; i < 64; ++i) {
-      const float x = cap ? cap_any(v[i], r.cap, top) : v[i] * r.f;
-      v[i] = fmaf(-r.slope, fabsf(d0 + (float)i) - least, x) + m;
-    }
-  }
+    for (int i = 0; i < 64; i += 2) f2_unpack(logits(i, v[i], v[i + 1]), v[i], v[i + 1]);
+  });
   if (!whole) {
     const int from = r.lo - key0, to = r.hi - key0;
 #pragma unroll
@@ -514,19 +608,35 @@ __device__ __forceinline__ void logits64(const CachePromptLaunch& a, const Promp
   }
 }
 
+// The sum of a tile's weights, and the weights of 64 products at a time.
 template <int KIND>
+struct Weights {
+  unsigned long long s0 = 0, s1 = 0;
+  uint32_t w[32];
+  __device__ __forceinline__ void operator()(int i, unsigned long long logits) {  // of the keys 2 i and 2 i + 1
+    float x, y;
+    f2_unpack(logits, x, y);
+    x = ex2_approx(x);
+    y = ex2_approx(y);
+    if (i & 1)
+      s1 = f2_add(s1, f2_pack(x, y));
+    else
+      s0 = f2_add(s0, f2_pack(x, y));
+    w[i & 31] = pack_weights<KIND>(x, y);
+  }
+};
+
+template <int KIND, PromptMode MODE>
 __device__ __forceinline__ bool soften_scored(const CachePromptLaunch& a, PromptShared& sh, PromptRow& r, uint32_t s, int X,
                                               int lane, int tile, unsigned k) {
   const int key0 = tile * kKeys;
   const bool whole = __all_sync(kFull, r.lo >= r.hi || (r.lo <= key0 && r.hi >= key0 + kKeys));
-  const bool cap = a.score.cap > 0.f, slopes = a.score.slopes != nullptr;
+  constexpr bool cap = MODE != kPromptBias;
+  const bool slopes = MODE == kPromptBias || (MODE == kPromptEither && a.score.slopes);
   if (!__all_sync(kFull, mbar_wait(&sh.s_full[X], k & 1, &sh.abort))) return false;
   tc_fence_after();
-  float size;  // the largest product's magnitude
-  {
-    float v[kKeys];
-    tmem_ld128_top<true>(s, v, size);
-  }
+  float all[kKeys], size;  // the products, and the largest one's magnitude
+  tmem_ld128_top<true>(s, all, size);
   // at least the row's largest logit: the nearer end of the line adds the more (or the less negative)
   float b = cap ? cap_any(size, r.cap, a.score.cap * kLog2e) : size * r.f;
   // (from kFar on, an exact product less a rounded reference may be far from zero for the largest: see soften)
@@ -536,64 +646,84 @@ __device__ __forceinline__ bool soften_scored(const CachePromptLaunch& a, Prompt
     const float near = d0 > 0.f ? d0 : d1 < 0.f ? -d1 : 0.f, most = fmaxf(fabsf(d0), fabsf(d1));
     b -= r.slope * ((r.slope > 0.f ? near : most) - least);
   }
-  ScoreForm form = kAnyScore;
-  if (cap && !slopes) {
-    if (!__any_sync(kFull, size * r.cap.to_y > 0.5f))
+  ScoreForm form = kBias;
+  if (cap && slopes) {
+    form = a.score.cap <= kCapExp ? kCapFarBias : kCapAnyBias;
+  } else if (cap) {
+    const bool in_range = r.cap.to_y <= kCapMost && (KIND == PISA_CACHE_E2M1 || r.cap.to_y >= kCapLeast);
+    if (!__any_sync(kFull, !in_range || size * r.cap.to_y > 0.5f))
       form = kCapHalf;
     else if (!__any_sync(kFull, size * r.cap.to_y > 1.f))
       form = kCapWhole;
-    else if (a.score.cap <= kCapExp)
-      form = kCapFar;
-  } else if (!cap && !far && !__any_sync(kFull, b >= kFar || (key0 + kKeys > r.pos + 1 && r.hi > r.pos + 1))) {
+    else
+      form = a.score.cap <= kCapExp ? kCapFar : kCapAny;
+  } else if (!far && !__any_sync(kFull, b >= kFar || (key0 + kKeys > r.pos + 1 && r.hi > r.pos + 1))) {
     form = kLine;  // (rows that see no later tokens than their own: such are masked)
   }
   bool waited = k == 0;
-  if (__any_sync(kFull, b > r.m + PCfg<KIND>::kTop)) {
-    b = -INFINITY;
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      float v[64];
-      tmem_ld64_now(s + 64 * h, v);
-      logits64(a, r, form, whole, key0 + 64 * h, 0, v);
-#pragma unroll
-      for (int i = 0; i < 64; i += 2) b = max3f(b, v[i], v[i + 1]);
-    }
-    if (__any_sync(kFull, b > r.m + PCfg<KIND>::kTop)) {
-      if (!refer<KIND>(sh, r, s, X, k, b)) return false;
-      waited = true;
-    }
-  }
-  const unsigned long long m2 = f2_pack(-r.m, -r.m);
-  unsigned long long s0 = 0, s1 = 0;
-#pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
-    float v[64];
-    tmem_ld64_now(s + 64 * h, v);
-    if (h == 1) {  // S is in registers: the next product may overwrite it
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.s_free[X]);
-    }
-    logits64(a, r, form, whole, key0 + 64 * h, m2, v);
-    uint32_t w[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float x = ex2_approx(v[2 * i]), y = ex2_approx(v[2 * i + 1]);
-      if (i & 1)
-        s1 = f2_add(s1, f2_pack(x, y));
-      else
-        s0 = f2_add(s0, f2_pack(x, y));
-      w[i] = pack_weights<KIND>(x, y);
-    }
+  const bool over = __any_sync(kFull, b > r.m + PCfg<KIND>::kTop);
+  Weights<KIND> weigh;
+  const auto store = [&](int h) {
     if (!waited) {
       if (!__all_sync(kFull, mbar_wait(&sh.pv_done[X], (k - 1) & 1, &sh.abort))) return false;
       tc_fence_after();
       waited = true;
     }
-    tmem_st32(s + 128 + 32 * h, w);
+    tmem_st32(s + 128 + 32 * h, weigh.w);
+    return true;
+  };
+  const auto release = [&] {  // S is in registers: the next product may overwrite it
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.s_free[X]);
+  };
+  constexpr ScoreForm kUsual = MODE == kPromptBias ? kLine : kCapHalf;
+  if (MODE != kPromptEither && whole && !over && form == kUsual) {
+    release();
+    const Logits<kUsual> logits(a, r, key0, f2_pack(-r.m, -r.m));
+#pragma unroll
+    for (int i = 0; i < kKeys / 2; ++i) {
+      weigh(i, logits(2 * i, all[2 * i], all[2 * i + 1]));
+      if ((i & 31) == 31 && !store(i >> 5)) return false;
+    }
+  } else {
+    if (over) {
+      b = -INFINITY;
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        float v[64];
+        tmem_ld64_now(s + 64 * h, v);
+        logits64<MODE>(a, r, form, whole, key0 + 64 * h, 0, v);
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) b = max3f(b, v[i], v[i + 1]);
+      }
+      if (__any_sync(kFull, b > r.m + PCfg<KIND>::kTop)) {
+        if (!refer<KIND>(sh, r, s, X, k, b)) return false;
+        waited = true;
+      }
+    }
+    const unsigned long long m2 = f2_pack(-r.m, -r.m);
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      float v[64];
+      tmem_ld64_now(s + 64 * h, v);
+      if (h == 1) release();
+      if (whole) {
+        with_form<MODE>(form, [&](auto f) {
+          const Logits<f()> logits(a, r, key0 + 64 * h, m2);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) weigh(i, logits(2 * i, v[2 * i], v[2 * i + 1]));
+        });
+      } else {
+        logits64<MODE>(a, r, form, whole, key0 + 64 * h, m2, v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) weigh(i, f2_pack(v[2 * i], v[2 * i + 1]));
+      }
+      if (!store(h)) return false;
+    }
   }
   float x, y;
-  f2_unpack(f2_add(s0, s1), x, y);
+  f2_unpack(f2_add(weigh.s0, weigh.s1), x, y);
   r.l += x + y;
   tmem_st_wait();
   tc_fence_before();
@@ -680,7 +810,7 @@ __device__ __forceinline__ void fetch_queries(const CachePromptLaunch& a, const 
 
 // .. as two swizzled operands.  4-bit pages: as fp16, the row scaled by a power of two so that its largest element lies in
 // [1, 2) (cache_attend.cuh, make_q).
-template <int KIND, bool SCORED>
+template <int KIND, PromptMode MODE>
 __device__ __forceinline__ void stage_queries(const CachePromptLaunch& a, PromptShared& sh, unsigned char* q,
                                               const uint4 (&x)[8]) {
   const int ch = threadIdx.x & 7;
@@ -701,7 +831,7 @@ __device__ __forceinline__ void stage_queries(const CachePromptLaunch& a, Prompt
       for (int i = 0; i < 4; ++i)
         w[i] = pack_f16x2(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xffff0000u) * down);
       y = make_uint4(w[0], w[1], w[2], w[3]);
-      constexpr float kFactor = SCORED ? kScale : kScale * kLog2e;
+      constexpr float kFactor = MODE != kPromptPlain ? kScale : kScale * kLog2e;
       if (ch == 0) sh.factor[row] = fminf(kFactor * exp2i(e) * exp2i(a.cache.k_exp), 0x1.fffffep127f);
     }
     *reinterpret_cast<uint4*>(q + row * 128 + ((ch ^ (row & 7)) << 4)) = y;
@@ -857,14 +987,14 @@ __global__ void __launch_bounds__(1024) cache_prompt_plan_kernel(CachePromptLaun
 }
 
 // The softmax of a piece for the warp's rows, and its result: to the output, or to a partial result.
-template <int KIND, bool SCORED, bool STREAM>
+template <int KIND, PromptMode MODE, bool STREAM>
 __device__ __forceinline__ bool soften_piece(const CachePromptLaunch& a, PromptShared& sh, PromptRow& r, int i1, int n,
                                              int g_shift) {
   const int lane = threadIdx.x & 31, X = threadIdx.x >> 7;
   const uint32_t s = sh.tmem + 256 * X + ((threadIdx.x >> 5 & 3) << 21);  // (the warp's lanes: 32 (warp % 4) ..)
   bool two_step = false;
   for (int k = 0; k < n; ++k)
-    if (!(SCORED ? soften_scored<KIND>(a, sh, r, s, X, lane, i1 - 1 - k, k)
+    if (!(MODE != kPromptPlain ? soften_scored<KIND, MODE>(a, sh, r, s, X, lane, i1 - 1 - k, k)
                  : soften<KIND>(sh, r, s, X, lane, i1 - 1 - k, k, two_step)))
       return false;
   if (n > 0 && !__all_sync(kFull, mbar_wait(&sh.pv_done[X], (n - 1) & 1, &sh.abort))) return false;
@@ -906,7 +1036,7 @@ __device__ __forceinline__ bool soften_piece(const CachePromptLaunch& a, PromptS
   return true;
 }
 
-template <int KIND, bool SCORED, bool STREAM>
+template <int KIND, PromptMode MODE, bool STREAM>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     cache_prompt_kernel(const __grid_constant__ CUtensorMap map, CachePromptLaunch a, int g_shift, int row_tiles,
                         int units) {
@@ -958,7 +1088,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (over) set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
       r.lo = s.lo;
       r.hi = s.hi;
-      if (SCORED && a.score.slopes) {
+      if (MODE != kPromptPlain && a.score.slopes) {
         r.slope = a.score.slopes[u.kv * a.G + (row & (a.G - 1))] * kLog2e;
         r.pos = s.pos;
         r.nearest = max(min(s.pos, s.hi - 1), s.lo);
@@ -977,7 +1107,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       atomicMin(&sh.hi_min, hi_min);
       atomicMax(&sh.hi_max, hi_max);
     }
-    stage_queries<KIND, SCORED>(a, sh, q, queries);
+    stage_queries<KIND, MODE>(a, sh, q, queries);
     fence_async_proxy();
   }
   tc_fence_before();
@@ -995,12 +1125,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   __syncthreads();
   bool ok = true;
   if (warp < kSoftWarps) {
-    r.f = KIND == PISA_CACHE_E2M1 ? sh.factor[threadIdx.x] : SCORED ? kScale : kScale * kLog2e;
-    if (SCORED) {
+    r.f = KIND == PISA_CACHE_E2M1 ? sh.factor[threadIdx.x] : MODE != kPromptPlain ? kScale : kScale * kLog2e;
+    if (MODE != kPromptPlain) {
       r.cap = CapRow{r.f * a.score.inv_cap, r.f * kLog2e};
       r.f *= kLog2e;
     }
-    ok = soften_piece<KIND, SCORED, STREAM>(a, sh, r, u.i1, u.n(), g_shift);
+    ok = soften_piece<KIND, MODE, STREAM>(a, sh, r, u.i1, u.n(), g_shift);
   } else if (warp < kSoftWarps + kLoadWarps) {
     const int w = warp - kSoftWarps;
     if constexpr (KIND == PISA_CACHE_BF16)
@@ -1133,7 +1263,7 @@ bool map_pages(CUtensorMap* m, const CacheDev& c) {
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int KIND, bool SCORED>
+template <int KIND, PromptMode MODE>
 static cudaError_t launch_prompt(const CachePromptLaunch& L, cudaStream_t s) {
   int g_shift = 0;
   while ((1 << g_shift) < L.G) ++g_shift;
@@ -1146,23 +1276,27 @@ static cudaError_t launch_prompt(const CachePromptLaunch& L, cudaStream_t s) {
   if (!L.last && keys > reach) keys = reach;
   constexpr int kSmem = PCfg<KIND>::kSmem;
   if (!takes_stream(units, keys / kKeys))
-    return launch_early<cache_prompt_kernel<KIND, SCORED, false>>((unsigned)units, kPromptThreads, kSmem, s, map, L, g_shift,
+    return launch_early<cache_prompt_kernel<KIND, MODE, false>>((unsigned)units, kPromptThreads, kSmem, s, map, L, g_shift,
                                                                   row_tiles, units);
   cudaError_t e = cudaSuccess;
   if (L.first || L.last)
     e = launch_early<cache_prompt_tiles_kernel>((unsigned)(units + 7) / 8, 256, 0, s, L, g_shift, row_tiles, units);
   if (e == cudaSuccess) e = launch_early<cache_prompt_plan_kernel>(1, 1024, 0, s, L, g_shift, row_tiles, units);
   if (e != cudaSuccess) return e;
-  e = launch_early<cache_prompt_kernel<KIND, SCORED, true>>((unsigned)(units + kRuns), kPromptThreads, kSmem, s, map, L, g_shift, row_tiles, units);
+  e = launch_early<cache_prompt_kernel<KIND, MODE, true>>((unsigned)(units + kRuns), kPromptThreads, kSmem, s, map, L, g_shift, row_tiles, units);
   if (e != cudaSuccess) return e;
   return launch_early<cache_prompt_join_kernel>(kRuns * 16, 256, 0, s, L, g_shift, row_tiles);
 }
 
+template <int KIND>
+static cudaError_t launch_prompt_mode(const CachePromptLaunch& L, cudaStream_t s) {
+  if (L.score.cap <= 0.f) return L.score.slopes ? launch_prompt<KIND, kPromptBias>(L, s) : launch_prompt<KIND, kPromptPlain>(L, s);
+  if (L.score.slopes || L.score.cap > kCapExp) return launch_prompt<KIND, kPromptEither>(L, s);
+  return launch_prompt<KIND, kPromptCapped>(L, s);
+}
+
 cudaError_t launch_cache_prompt(const CachePromptLaunch& L, cudaStream_t s) {
-  const bool scored = L.score.cap > 0.f || L.score.slopes;
-  if (L.cache.kind == PISA_CACHE_BF16)
-    return scored ? launch_prompt<PISA_CACHE_BF16, true>(L, s) : launch_prompt<PISA_CACHE_BF16, false>(L, s);
-  return scored ? launch_prompt<PISA_CACHE_E2M1, true>(L, s) : launch_prompt<PISA_CACHE_E2M1, false>(L, s);
+  return L.cache.kind == PISA_CACHE_BF16 ? launch_prompt_mode<PISA_CACHE_BF16>(L, s) : launch_prompt_mode<PISA_CACHE_E2M1>(L, s);
 }
 
 }  // namespace pisa
