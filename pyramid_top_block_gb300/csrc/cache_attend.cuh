@@ -488,17 +488,17 @@ __device__ __forceinline__ void score(const CacheAttendLaunch& a, int first, int
                                       float (&sc)[Cfg<KIND>::KT / 8][4]) {
   constexpr int KT = Cfg<KIND>::KT;
   const float top = a.score.cap * kLog2e;
+  const CapRow r0 = cap_row(s.t0, a.score.inv_cap), r1 = cap_row(s.t1, a.score.inv_cap);
   if (a.score.cap <= kCapExp && !a.out_f32) {
     // by exponentials, whose units have nothing else to do here; the polynomial would share the multiply-add
     // units with the scales of the 4-bit pages (16 x 131072 tokens 91.6 us, by the polynomial 96.1)
-    const float two0 = 2.f * kLog2e * s.t0 * a.score.inv_cap, two1 = 2.f * kLog2e * s.t1 * a.score.inv_cap;
+    const float two0 = 2.f * kLog2e * r0.to_y, two1 = 2.f * kLog2e * r1.to_y;
 #pragma unroll
     for (int nt = 0; nt < KT / 8; ++nt) {
       cap_exp(sc[nt][0], sc[nt][1], two0, top);
       cap_exp(sc[nt][2], sc[nt][3], two1, top);
     }
   } else {
-    const CapRow r0 = {s.t0 * a.score.inv_cap, s.t0 * kLog2e}, r1 = {s.t1 * a.score.inv_cap, s.t1 * kLog2e};
     float b0 = 0.f, b1 = 0.f;
 #pragma unroll
     for (int nt = 0; nt < KT / 8; ++nt) {

@@ -475,13 +475,13 @@ enum ScoreForm {
   kBias,        // a bias
 };
 
-// Factors of the short polynomial: logit = x (c[0] + x x (c[1] + ..)), x the product.  They stay in range for
-// kCapLeast <= to_y <= kCapMost; 4-bit pages' products are below 2^19, so that there what falls below the range is
-// below 2^-20 of the logit.
+// Factors of the short polynomial: logit = x (c[0] + x x (c[1] + ..)), x the product.  They fit 32 bits for
+// kCapLeast <= to_y <= kCapMost (caps are at most 2^20); 4-bit pages' products are below 2^19, so that with a smaller to_y
+// what is lost of the last is below 2^-20 of the logit.
 struct CapPoly {
   float c[TanhHalf::n];
 };
-constexpr float kCapLeast = 0x1p-18f, kCapMost = 0x1p18f;
+constexpr float kCapLeast = 0x1p-18f, kCapMost = 0x1p10f;
 __device__ __forceinline__ CapPoly cap_poly(const CapRow& r) {
   constexpr TanhHalf k;
   CapPoly p;
@@ -1127,8 +1127,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   if (warp < kSoftWarps) {
     r.f = KIND == PISA_CACHE_E2M1 ? sh.factor[threadIdx.x] : MODE != kPromptPlain ? kScale : kScale * kLog2e;
     if (MODE != kPromptPlain) {
-      r.cap = CapRow{r.f * a.score.inv_cap, r.f * kLog2e};
-      r.f *= kLog2e;
+      r.cap = cap_row(r.f, a.score.inv_cap);
+      r.f = r.cap.to_l;
     }
     ok = soften_piece<KIND, MODE, STREAM>(a, sh, r, u.i1, u.n(), g_shift);
   } else if (warp < kSoftWarps + kLoadWarps) {

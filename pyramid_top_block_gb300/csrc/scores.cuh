@@ -53,9 +53,13 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 
 // Factors of a row: y = score * to_y (to the cap's units), logit = score * to_l tanh(y) / y.
+// Large ones are cut, so that a product of zero stays zero: a 4-bit page's other products, 2^-34 or more, are far past the cap then.
 struct CapRow {
   float to_y, to_l;
 };
+__device__ __forceinline__ CapRow cap_row(float factor, float inv_cap) {
+  return CapRow{fminf(factor * inv_cap, 0x1p100f), fminf(factor * 1.4426950408889634f, 0x1.fffffep127f)};
+}
 
 // Two scores with |y| <= 1, capped.
 __device__ __forceinline__ void cap_small(float& a, float& b, const CapRow& r) {

@@ -119,6 +119,26 @@ def test_prompt_attention(bits, B, T, G, Hkv, page, start, counts, kind, window,
     check(got, expected(q, cache, start, counts, first, last, window, cap, s))
 
 
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("slopes", [False, True])
+@pytest.mark.parametrize("cap", [20.0, 128.0, 129.0, 40000.0])
+def test_scores_below_and_past_a_cap(bits, slopes, cap):
+    """Rows whose scores stay far below the cap, come near it and pass it, side by side and far apart."""
+    g = gen(int(cap))
+    start, T, Hkv, G = 200, 300, 1, 4
+    cache = make_cache(g, 1, start + T, Hkv, 64, bits)
+    s = slopes_of(G) if slopes else None
+    k, _ = ref.tokens(cache, 0, start + T)
+    size = float((normal(g, 64, 64).double() @ k[:, 0].T / 8).abs().amax())  # of the largest of many scores
+    for scale in (torch.tensor([0.1, 0.4, 0.9, 3.0], device=DEV)[None, :, None].expand(T, G, 1),
+                  torch.tensor([0.1, 0.4, 0.9, 3.0], device=DEV)[torch.arange(T, device=DEV) * 4 // T][:, None, None]):
+        q = (normal(g, 1, T, G, 64) * (scale * cap / size)).to(torch.bfloat16)
+        ws = pisa.cache_workspace(cache)
+        got = pisa.cache_prompt_attention(q, cache, i32([start]), workspace=ws, cap=cap, slopes=s)
+        assert status(ws) == 0
+        check(got, expected(q, cache, [start], [T], cap=cap, slopes=s))
+
+
 def test_a_prompt_equals_its_tokens_one_by_one():
     """The last sixteen tokens of a prompt, as cache_attention gives them, with the same scores."""
     g = gen(2)

@@ -170,6 +170,31 @@ def test_capped_infinities():
     assert bool(torch.isnan(pisa.cache_attention(q, cache, n, window=30)).all())
 
 
+@pytest.mark.parametrize("cap", [2.0 ** -20, 5.0, 500.0, 2.0 ** 20])
+@pytest.mark.parametrize("slopes", [False, True])
+def test_huge_queries_and_keys_of_zero(cap, slopes):
+    """4-bit keys of zero have scores of zero whatever the queries are, the others plus or minus the cap."""
+    g = gen(31)
+    cache = make_cache(g, 1, 256, 1, 64, 4, k_exp=10)
+    n, T = 200, 3
+    cache.pages.view(cache.pages.shape[0], 144, 32)[:, 0:64:3] = 0  # codes of keys: every third is zero
+    k, v = ref.tokens(cache, 0, n)
+    q = torch.sign(normal(g, 1, T, 4, 64)) * 2.0 ** 124
+    q[:, 1] = 0.0
+    q[:, 2, :, 1:] = 0.0
+    q = q.to(torch.bfloat16)
+    s = slopes_of(4) if slopes else None
+    at = n - T + torch.arange(T, device=DEV)
+    o, pv, big = score_ref.attention(q[0].double(), k, v, at, torch.zeros_like(at), at + 1, cap, s)
+    # products are zero or past the cap; weights of 2^-11, of all tokens (the sum and the weights), and the result's step
+    tol = 2 * (2.0 ** -11 + 2.0 ** -16 + 32 * 2.0 ** -24 * cap) * pv + 2.0 ** -8 * (o.abs() + pv * 2.0 ** -9)
+    tol += 2.0 ** -25 * v.abs().sum(0)  # fp16 weights' steps
+    prompt = pisa.cache_prompt_attention(q, cache, i32([n - T]), cap=cap, slopes=s)
+    token = pisa.cache_attention(q, cache, i32([n]), cap=cap, slopes=s)
+    for got in (prompt, token):
+        assert bool(((got[0].double() - o).abs() <= tol).all()), float(((got[0].double() - o).abs() / tol).max())
+
+
 def test_zero_scores_are_plain_attention():
     """No cap, no slopes and no window is the plain call, to the bit; a window that holds everything is close."""
     g = gen(4)
