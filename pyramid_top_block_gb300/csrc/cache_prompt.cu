@@ -475,22 +475,6 @@ enum ScoreForm {
   kBias,        // a bias
 };
 
-// Factors of the short polynomial: logit = x (c[0] + x x (c[1] + ..)), x the product.  They fit 32 bits for
-// kCapLeast <= to_y <= kCapMost (caps are at most 2^20); 4-bit pages' products are below 2^19, so that with a smaller to_y
-// what is lost of the last is below 2^-20 of the logit.
-struct CapPoly {
-  float c[TanhHalf::n];
-};
-constexpr float kCapLeast = 0x1p-18f, kCapMost = 0x1p10f;
-__device__ __forceinline__ CapPoly cap_poly(const CapRow& r) {
-  constexpr TanhHalf k;
-  CapPoly p;
-  float f = r.to_l;
-#pragma unroll
-  for (int i = 0; i < TanhHalf::n; ++i, f = f * r.to_y * r.to_y) p.c[i] = k.c[i] * f;
-  return p;
-}
-
 // Products of a row, of the keys from key0 on, as logits less a reference (m2: minus the reference, twice).
 template <ScoreForm FORM>
 struct Logits {
@@ -1124,6 +1108,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   }
   __syncthreads();
   bool ok = true;
+  // More registers for the softmax, whose scores spilled (1216 tokens at 16384 136 -> 132 us, 4 bits 151 -> 143): 8 x 32 x
+  // 200 + 4 x 32 x 96 of the 384 x 168 that the CTA has.
+  if (warp < kSoftWarps)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
   if (warp < kSoftWarps) {
     r.f = KIND == PISA_CACHE_E2M1 ? sh.factor[threadIdx.x] : MODE != kPromptPlain ? kScale : kScale * kLog2e;
     if (MODE != kPromptPlain) {

@@ -61,6 +61,22 @@ __device__ __forceinline__ CapRow cap_row(float factor, float inv_cap) {
   return CapRow{fminf(factor * inv_cap, 0x1p100f), fminf(factor * 1.4426950408889634f, 0x1.fffffep127f)};
 }
 
+// Factors of the short polynomial: logit = x (c[0] + x x (c[1] + ..)), x the product.  They fit 32 bits for
+// kCapLeast <= to_y <= kCapMost (caps are at most 2^20); 4-bit pages' products are below 2^19, so that with a smaller to_y
+// what is lost of the last is below 2^-20 of the logit.
+struct CapPoly {
+  float c[TanhHalf::n];
+};
+constexpr float kCapLeast = 0x1p-18f, kCapMost = 0x1p10f;
+__device__ __forceinline__ CapPoly cap_poly(const CapRow& r) {
+  constexpr TanhHalf k;
+  CapPoly p;
+  float f = r.to_l;
+#pragma unroll
+  for (int i = 0; i < TanhHalf::n; ++i, f = f * r.to_y * r.to_y) p.c[i] = k.c[i] * f;
+  return p;
+}
+
 // Two scores with |y| <= 1, capped.
 __device__ __forceinline__ void cap_small(float& a, float& b, const CapRow& r) {
   const unsigned long long x = f2_pack(a, b);
