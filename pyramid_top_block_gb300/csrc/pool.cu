@@ -4,8 +4,9 @@
 // All numbers are whole and every order is fixed (pages by their number, sequences by theirs, a sequence's
 // entries by position), so that a call gives the same table however it is scheduled; atomics only count.
 //
-// What bounds it: copying pages (the memory, read and write); planning is a few dependent loads and
-// barriers, a few microseconds.
+// What bounds it: copying pages (the memory, read and write: 356 MB moved in 54.4 us = 6.55 TB/s); planning is a few
+// dependent loads and barriers.  Fork 1.6 us (16 sequences of 64 pages) to 7.3 (64 of 8192), reserve 5.6 (1200 pages) to 10.6
+// (530000), planning a compaction 5.3 to 33.7.
 #include <climits>
 
 #include <cooperative_groups.h>
