@@ -478,6 +478,7 @@ enum ScoreForm {
   kCapFarBias,  // the last two with a bias
   kCapAnyBias,
   kLine,        // a bias, where no row of the warp sees a later token than its own: a line
+  kCapLine,     // kCapHalf with such a bias
   kBias,        // a bias
 };
 
@@ -486,14 +487,15 @@ template <ScoreForm FORM>
 struct Logits {
   static constexpr bool kAny = FORM == kCapAny || FORM == kCapAnyBias, kFarther = FORM == kCapFar || FORM == kCapFarBias || kAny;
   static constexpr bool kAway = FORM == kCapFarBias || FORM == kCapAnyBias || FORM == kBias;
-  static constexpr int n = FORM == kCapHalf ? TanhHalf::n : FORM == kCapWhole || kAny ? Tanh::n : 1;
+  static constexpr bool kHalf = FORM == kCapHalf || FORM == kCapLine, kStraight = FORM == kLine || FORM == kCapLine;
+  static constexpr int n = kHalf ? TanhHalf::n : FORM == kCapWhole || kAny ? Tanh::n : 1;
   unsigned long long f, two, top2, c, p[n];
   float top1, slope, d0, least;
 
   __device__ __forceinline__ Logits(const CachePromptLaunch& a, const PromptRow& r, int key0, unsigned long long m2) {
     const float top = a.score.cap * kLog2e;
     c = m2;
-    if constexpr (FORM == kCapHalf) {
+    if constexpr (kHalf) {
       const CapPoly q = cap_poly(r.cap);
 #pragma unroll
       for (int i = 0; i < n; ++i) p[i] = f2_pack(q.c[i], q.c[i]);
@@ -511,7 +513,7 @@ struct Logits {
       top2 = f2_pack(-2.f * top, -2.f * top);
       c = f2_add(m2, f2_pack(top, top));
     }
-    if constexpr (FORM == kLine) {
+    if constexpr (kStraight) {
       const float bias = r.slope * (float)(key0 - r.nearest);  // of the first key, relative to the nearest one in sight
       slope = r.slope;
       c = f2_add(m2, f2_pack(bias, bias));
@@ -529,7 +531,9 @@ struct Logits {
   __device__ __forceinline__ unsigned long long operator()(int i, float v, float w) const {
     const unsigned long long x = f2_pack(v, w);
     unsigned long long z = 0;
-    if constexpr (FORM == kLine) z = f2_fma(x, f, f2_fma(f2_pack(slope, slope), f2_pack((float)i, (float)(i + 1)), c));
+    unsigned long long add = c;
+    if constexpr (kStraight) add = f2_fma(f2_pack(slope, slope), f2_pack((float)i, (float)(i + 1)), c);
+    if constexpr (FORM == kLine) z = f2_fma(x, f, add);
     if constexpr (FORM == kBias) z = f2_mul(x, f);
     if constexpr (kFarther) {  // (as cap_exp; the reference in its last step where nothing else follows)
       float e, g;
@@ -537,8 +541,8 @@ struct Logits {
       f2_unpack(f2_add(f2_pack(ex2_approx(e), ex2_approx(g)), f2_pack(1.f, 1.f)), e, g);
       z = f2_fma(f2_pack(rcp_approx(e), rcp_approx(g)), top2, FORM == kCapFar ? c : f2_pack(top1, top1));
     }
-    if constexpr (FORM == kCapHalf || FORM == kCapWhole || kAny) {
-      const unsigned long long y = FORM == kCapHalf ? x : f2_mul(x, f), u = f2_mul(y, y);
+    if constexpr (kHalf || FORM == kCapWhole || kAny) {
+      const unsigned long long y = kHalf ? x : f2_mul(x, f), u = f2_mul(y, y);
       unsigned long long q = p[n - 1];
 #pragma unroll
       for (int j = n - 2; j >= 0; --j) q = f2_fma(q, u, p[j]);
@@ -549,7 +553,7 @@ struct Logits {
         f2_unpack(f2_mul(y, q), q0, q1);
         z = f2_pack(fabsf(y0) <= 1.f ? q0 : z0, fabsf(y1) <= 1.f ? q1 : z1);
       } else {
-        z = f2_fma(y, q, c);
+        z = f2_fma(y, q, add);
       }
     }
     if constexpr (kAway) {
@@ -577,6 +581,7 @@ __device__ __forceinline__ void with_form(ScoreForm form, const Use& use) {
     if (form == kCapWhole) return use_form<kCapWhole>(use);
     if constexpr (MODE == kPromptCapped) return use_form<kCapFar>(use);
     if (form == kCapAny) return use_form<kCapAny>(use);
+    if (form == kCapLine) return use_form<kCapLine>(use);
     if (form == kCapFarBias) return use_form<kCapFarBias>(use);
     return use_form<kCapAnyBias>(use);
   }
@@ -636,20 +641,19 @@ __device__ __forceinline__ bool soften_scored(const CachePromptLaunch& a, Prompt
     const float near = d0 > 0.f ? d0 : d1 < 0.f ? -d1 : 0.f, most = fmaxf(fabsf(d0), fabsf(d1));
     b -= r.slope * ((r.slope > 0.f ? near : most) - least);
   }
-  ScoreForm form = kBias;
-  if (cap && slopes) {
-    form = a.score.cap <= kCapExp ? kCapFarBias : kCapAnyBias;
-  } else if (cap) {
-    const bool in_range = r.cap.to_y <= kCapMost && (KIND == PISA_CACHE_E2M1 || r.cap.to_y >= kCapLeast);
-    if (!__any_sync(kFull, !in_range || size * r.cap.to_y > 0.5f))
-      form = kCapHalf;
-    else if (!__any_sync(kFull, size * r.cap.to_y > 1.f))
-      form = kCapWhole;
-    else
-      form = a.score.cap <= kCapExp ? kCapFar : kCapAny;
-  } else if (!far && !__any_sync(kFull, b >= kFar || (key0 + kKeys > r.pos + 1 && r.hi > r.pos + 1))) {
-    form = kLine;  // (rows that see no later tokens than their own: such are masked)
-  }
+  const bool in_range = r.cap.to_y <= kCapMost && (KIND == PISA_CACHE_E2M1 || r.cap.to_y >= kCapLeast);
+  const bool half = cap && !__any_sync(kFull, !in_range || size * r.cap.to_y > 0.5f);
+  // (rows that see no later tokens than their own: such are masked)
+  const bool line = slopes && !far && !__any_sync(kFull, b >= kFar || (key0 + kKeys > r.pos + 1 && r.hi > r.pos + 1));
+  ScoreForm form = line ? kLine : kBias;
+  if (cap && slopes)
+    form = half && line ? kCapLine : a.score.cap <= kCapExp ? kCapFarBias : kCapAnyBias;
+  else if (half)
+    form = kCapHalf;
+  else if (cap && !__any_sync(kFull, size * r.cap.to_y > 1.f))
+    form = kCapWhole;
+  else if (cap)
+    form = a.score.cap <= kCapExp ? kCapFar : kCapAny;
   bool waited = k == 0;
   const bool over = __any_sync(kFull, b > r.m + PCfg<KIND>::kTop);
   Weights<KIND> weigh;
