@@ -671,15 +671,22 @@ __device__ __forceinline__ bool soften_scored(const CachePromptLaunch& a, Prompt
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.s_free[X]);
   };
-  constexpr ScoreForm kUsual = MODE == kPromptBias ? kLine : kCapHalf;
-  if (MODE != kPromptEither && whole && !over && form == kUsual) {
+  // The usual tile; false: a wait ran out.
+  const auto at_once = [&](auto f) {
     release();
-    const Logits<kUsual> logits(a, r, key0, f2_pack(-r.m, -r.m));
+    const Logits<f()> logits(a, r, key0, f2_pack(-r.m, -r.m));
 #pragma unroll
     for (int i = 0; i < kKeys / 2; ++i) {
       weigh(i, logits(2 * i, all[2 * i], all[2 * i + 1]));
       if ((i & 31) == 31 && !store(i >> 5)) return false;
     }
+    return true;
+  };
+  using Usual = std::integral_constant<ScoreForm, MODE == kPromptBias ? kLine : MODE == kPromptCapped ? kCapHalf : kCapLine>;
+  if (whole && !over && form == Usual()) {
+    if (!at_once(Usual())) return false;
+  } else if (MODE == kPromptEither && whole && !over && form == kCapHalf) {
+    if (!at_once(std::integral_constant<ScoreForm, kCapHalf>())) return false;
   } else {
     if (over) {
       b = -INFINITY;
