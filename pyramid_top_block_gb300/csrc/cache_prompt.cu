@@ -632,19 +632,21 @@ __device__ __forceinline__ bool soften_scored(const CachePromptLaunch& a, Prompt
   tc_fence_after();
   float all[kKeys], size;  // the products, and the largest one's magnitude
   tmem_ld128_top<true>(s, all, size);
-  // at least the row's largest logit: the nearer end of the line adds the more (or the less negative)
-  float b = cap ? cap_any(size, r.cap, a.score.cap * kLog2e) : size * r.f;
-  // (from kFar on, an exact product less a rounded reference may be far from zero for the largest: see soften)
-  const bool far = __any_sync(kFull, b >= kFar);
+  const bool in_range = r.cap.to_y <= kCapMost && (KIND == PISA_CACHE_E2M1 || r.cap.to_y >= kCapLeast);
+  const bool half = cap && !__any_sync(kFull, !in_range || size * r.cap.to_y > 0.5f);
+  // at least the row's largest logit (a cap makes none larger; the nearer end of the line adds the more, or the less negative)
+  float b = size * r.f;
+  if (cap && !half) b = cap_any(size, r.cap, a.score.cap * kLog2e);
+  bool line = false;
   if (slopes) {
     const float d0 = (float)(key0 - r.pos), d1 = d0 + (float)(kKeys - 1), least = (float)abs(r.pos - r.nearest);
     const float near = d0 > 0.f ? d0 : d1 < 0.f ? -d1 : 0.f, most = fmaxf(fabsf(d0), fabsf(d1));
+    const float x = b;
     b -= r.slope * ((r.slope > 0.f ? near : most) - least);
+    // (rows that see no later tokens than their own: such are masked; from kFar on, an exact product less a rounded reference may
+    // be far from zero for the largest: see soften)
+    line = !__any_sync(kFull, x >= kFar || b >= kFar || (key0 + kKeys > r.pos + 1 && r.hi > r.pos + 1));
   }
-  const bool in_range = r.cap.to_y <= kCapMost && (KIND == PISA_CACHE_E2M1 || r.cap.to_y >= kCapLeast);
-  const bool half = cap && !__any_sync(kFull, !in_range || size * r.cap.to_y > 0.5f);
-  // (rows that see no later tokens than their own: such are masked)
-  const bool line = slopes && !far && !__any_sync(kFull, b >= kFar || (key0 + kKeys > r.pos + 1 && r.hi > r.pos + 1));
   ScoreForm form = line ? kLine : kBias;
   if (cap && slopes)
     form = half && line ? kCapLine : a.score.cap <= kCapExp ? kCapFarBias : kCapAnyBias;
