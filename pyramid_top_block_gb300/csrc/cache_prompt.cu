@@ -15,8 +15,8 @@
 // What bounds it: a step of 256 rows and 128 keys takes the tensor core 1552 clocks (the product with V has 64 columns, and takes
 // as long as with 128) and the exponentials 1024, and each row tile waits for its product, takes its scores into registers,
 // weighs them and hands the weights back: about 2000 clocks.  32 heads on 2, bf16 (4-bit) pages: 32768 tokens 3.51 ms =
-// 1.25 PFLOP/s (3.81 ms), 2048 at 131072 1.68 ms = 1.30 PFLOP/s (1.82), 1216 at 16384 132 us (142), capped 173 to 180, with
-// slopes 163; a library's bf16 product of matrices reaches 1.90 PFLOP/s.
+// 1.25 PFLOP/s (3.81 ms), 2048 at 131072 1.68 ms = 1.30 PFLOP/s (1.82), 1216 at 16384 132 us (142), capped 171 to 179, with
+// slopes 162; a library's bf16 product of matrices reaches 1.90 PFLOP/s.
 #include "cache_prompt.cuh"
 
 #include <climits>
