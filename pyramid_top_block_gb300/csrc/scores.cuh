@@ -62,8 +62,8 @@ __device__ __forceinline__ CapRow cap_row(float factor, float inv_cap) {
 }
 
 // Factors of the short polynomial: logit = x (c[0] + x x (c[1] + ..)), x the product.  They fit 32 bits for
-// kCapLeast <= to_y <= kCapMost (caps are at most 2^20); 4-bit pages' products are below 2^19, so that with a smaller to_y
-// what is lost of the last is below 2^-20 of the logit.
+// kCapLeast <= to_y <= kCapMost (caps are at most 2^20).  4-bit pages' products are below 2^19: with a smaller to_y the last
+// factor may fall below 2^-149, but what is lost of a logit is below 2^-18 of the larger of it and 1.
 struct CapPoly {
   float c[TanhHalf::n];
 };
