@@ -27,6 +27,7 @@
 #include <climits>
 
 #include "cache.cuh"
+#include "cache_stream.cuh"
 #include "tc.cuh"
 
 namespace pisa {
@@ -42,7 +43,6 @@ enum ScoreMode {
 
 constexpr int kPartFloats = 16 * 64 + 32;  // a partial result: O [16][64], row maxima, row sums
 constexpr int kCaGrid = 152;               // CTAs of the split form: one on each SM
-constexpr int kCaMinTiles = 12;            // places of the stream that a run has at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -0x1.fffffep127f;  // the reference of a row that has seen no logit above minus infinity
 constexpr float kFar = 0x1p22f;            // references from which on weigh takes differences in two steps
@@ -65,7 +65,7 @@ struct Cfg<PISA_CACHE_BF16> {
   //           (T = 16 ragged 139 / 134, one short sequence T = 9 33.0 / 31.5)
   //   4 bits  4 x 65536 T = 2 25.4 / 25.3, T = 8 75.1 / 71.4 (bound by the arithmetic; some CTAs are left over)
   static constexpr bool kSide = true;
-  static constexpr int kChange = 36;  // places of the stream that a unit's end counts as (see unit_places)
+  static constexpr int kChange = 36;  // places of the stream that a unit's end counts as (see tiles_of_seq)
   static constexpr float kShift = 0.f;  // weights are held times 2^kShift
   static constexpr float kSlack = 20.f;  // how far (base 2) a logit may pass the row's reference
 };
@@ -977,25 +977,15 @@ __device__ __forceinline__ int seq_len(const CacheAttendLaunch& a, int b, bool& 
   return n < 0 ? 0 : over ? (int)cap : n;
 }
 
-// The first tile that any query of a sequence of n tokens sees, and how many there are.
-template <int KIND, int MODE>
-__device__ __forceinline__ int first_tile(const CacheAttendLaunch& a, int n) {
-  return MODE != kPlain ? max(n - a.T + 1 - a.score.window, 0) / Cfg<KIND>::KT : 0;
-}
-template <int KIND, int MODE>
-__device__ __forceinline__ int unit_tiles(const CacheAttendLaunch& a, int n) {
-  constexpr int KT = Cfg<KIND>::KT;
-  return (n + KT - 1) / KT - first_tile<KIND, MODE>(a, n);
-}
-
-// Places that a unit of nt tiles has in the stream: its tiles, and some for what a run spends at
+// The tiles and places of a unit of a sequence of n tokens (cache_stream.cuh).
+// A unit has places in the stream for its tiles, and some for what a run spends at
 // its end (the warps' merge, the next unit's chain of loads; about 4 us), so that the runs that
 // change units take as long as the others.  Places at the end 0 / 12 / 24 / 36 / 48, us a call:
 //   4 bits  16 x 131072 73.5 / 72.1 / 71.5 / 71.6 / 71.9   64 x 9000 ragged, 8 heads 88.8 / 63.6 / 56.7 / 57.5 / 59.8
 //   bf16    8 x 131072 ragged 64.8 / 63.8 / 63.3 / 63.0 / 63.3   64 x 9000 ragged, 8 heads 119.7 / 103 / 96.3 / 96.5 / 97.4
-template <int KIND>
-__device__ __forceinline__ int unit_places(int nt) {
-  return nt ? nt + Cfg<KIND>::kChange : 0;
+template <int KIND, int MODE>
+__device__ __forceinline__ SeqTiles tiles_of_seq(const CacheAttendLaunch& a, int n) {
+  return seq_tiles<Cfg<KIND>::KT, MODE != kPlain>(n, a.T, a.score.window, Cfg<KIND>::kChange);
 }
 
 // Places of all units before sequence b (b = B: of all): every warp computes it by itself.
@@ -1003,7 +993,7 @@ template <int KIND, int MODE>
 __device__ __forceinline__ long long places_before(const CacheAttendLaunch& a, int b, int units, int lane) {
   long long sum = 0;
   bool over;
-  for (int i = lane; i < b; i += 32) sum += unit_places<KIND>(unit_tiles<KIND, MODE>(a, seq_len(a, i, over)));
+  for (int i = lane; i < b; i += 32) sum += tiles_of_seq<KIND, MODE>(a, seq_len(a, i, over)).places;
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(kFull, sum, x);
   return sum * units;
@@ -1017,7 +1007,7 @@ __device__ __forceinline__ int seq_of(const CacheAttendLaunch& a, long long at, 
   for (int b0 = 0; b0 < a.cache.B; b0 += 32) {
     bool over;
     const int n = b0 + lane < a.cache.B ? seq_len(a, b0 + lane, over) : 0;
-    const long long t = (long long)unit_places<KIND>(unit_tiles<KIND, MODE>(a, n)) * units;
+    const long long t = (long long)tiles_of_seq<KIND, MODE>(a, n).places * units;
     long long inc = t;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
@@ -1033,12 +1023,6 @@ __device__ __forceinline__ int seq_of(const CacheAttendLaunch& a, long long at, 
     base += __shfl_sync(kFull, inc, 31);
   }
   return a.cache.B;  // (past the last place)
-}
-
-// Places per CTA of the split form.
-__device__ __forceinline__ long long run_length(long long total, int grid) {
-  const long long per = total < (1 << 30) ? ((int)total + grid - 1) / grid : (total + grid - 1) / grid;
-  return per < kCaMinTiles ? kCaMinTiles : per;
 }
 
 template <int KIND, int W>
@@ -1138,16 +1122,15 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_
   u.sel = nullptr;
   while (cur < end) {
     u.n = seq_len(a, u.b, over);
-    const int nt = unit_tiles<KIND, MODE>(a, u.n);  // tiles of a unit of this sequence
-    const int places = unit_places<KIND>(nt);
+    const SeqTiles unit = tiles_of_seq<KIND, MODE>(a, u.n);
+    const int nt = unit.tiles, places = unit.places;
     if (nt == 0 || cur >= base + (long long)places * units) {  // on to the next sequence
       base += (long long)places * units;
       ++u.b;
       continue;
     }
-    // (places of one sequence: below 2^22 * 32 heads * 16 row tiles + 2^15, within 32 bits)
-    const unsigned at = (unsigned)(cur - base), un = at / (unsigned)places;
-    const int i0 = (int)(at - un * places);
+    const unsigned un = unit_at(cur - base, places);
+    const int i0 = (int)((unsigned)(cur - base) - un * places);
     if (i0 >= nt) {  // behind a unit's tiles
       cur += places - i0;
       continue;
@@ -1158,7 +1141,7 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_
     QueryWords q;
     fetch_q(a, u, lane, q);
     reset(s);
-    const int t0 = first_tile<KIND, MODE>(a, u.n);
+    const int t0 = unit.first;
     run_tiles<KIND, U, NP, W, false, MODE>(a, u, q, blk, t0 + i0, t0 + i1, ring, scratch, warp, lane, s);
     if ((threadIdx.x == 0 && over) || (lane == 0 && s.bad)) set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
     merge_warps<KIND, W>(s, mo, ml, warp, lane);
@@ -1192,7 +1175,6 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_
 // without it would let the next kernel of the stream overtake the one before).
 template <int KIND, bool FEW, int MODE>
 __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, int grid) {
-  constexpr int KT = Cfg<KIND>::KT;
   constexpr int kRows = FEW ? 1 : 4, kGroups = 16 / kRows;
   __shared__ float4 so[kGroups][kRows][16];
   __shared__ float sm[kGroups][kRows], sl[kGroups][kRows];
@@ -1224,11 +1206,10 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, in
     set_unit(un);
     bool over;
     u.n = seq_len(a, u.b, over);
-    const int nt = unit_tiles<KIND, MODE>(a, u.n);
-    const long long w0 = places_before<KIND, MODE>(a, u.b, units, lane) + (long long)un * unit_places<KIND>(nt);
+    const SeqTiles unit_is = tiles_of_seq<KIND, MODE>(a, u.n);
+    const long long w0 = places_before<KIND, MODE>(a, u.b, units, lane) + (long long)un * unit_is.places;
     c0 = (int)(w0 / per);
-    c1 = (int)((w0 + nt - 1) / per);
-    cut = nt != 0 && c0 != c1;
+    cut = goes_on(w0, unit_is.tiles, per, c0, c1);
   } else {
     const int cta = blockIdx.x / 4;
     c0 = kSide ? cta / RT : cta;
@@ -1240,12 +1221,10 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, in
       u.b = seq_of<KIND, MODE>(a, end - 1, units, lane, base);
       bool over;
       u.n = seq_len(a, u.b, over);
-      const int nt = (u.n + KT - 1) / KT, places = unit_places<KIND>(nt);
-      const unsigned un = (unsigned)(end - 1 - base) / (unsigned)places;
+      const SeqTiles unit_is = tiles_of_seq<KIND, MODE>(a, u.n);
+      const unsigned un = unit_at(end - 1 - base, unit_is.places);
       set_unit(un);
-      const long long w0 = base + (long long)un * places, w1 = w0 + nt;
-      cut = w1 > end && w0 >= end - per;
-      c1 = (int)((w1 - 1) / per);
+      cut = goes_on(base + (long long)un * unit_is.places, unit_is.tiles, per, c0, c1);
     }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
