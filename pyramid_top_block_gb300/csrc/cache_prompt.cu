@@ -641,11 +641,13 @@ __device__ __forceinline__ bool soften_scored(const CachePromptLaunch& a, Prompt
   if (slopes) {
     const float d0 = (float)(key0 - r.pos), d1 = d0 + (float)(kKeys - 1), least = (float)abs(r.pos - r.nearest);
     const float near = d0 > 0.f ? d0 : d1 < 0.f ? -d1 : 0.f, most = fmaxf(fabsf(d0), fabsf(d1));
-    const float x = b;
-    b -= r.slope * ((r.slope > 0.f ? near : most) - least);
-    // (rows that see no later tokens than their own: such are masked; from kFar on, an exact product less a rounded reference may
-    // be far from zero for the largest: see soften)
-    line = !__any_sync(kFull, x >= kFar || b >= kFar || (key0 + kKeys > r.pos + 1 && r.hi > r.pos + 1));
+    const float x = b, at_near = r.slope * (least - near), at_most = r.slope * (least - most);  // the tile's biases
+    b += fmaxf(at_near, at_most);
+    // (rows that see no later tokens than their own: such are masked; from kFar on, an exact logit less a rounded reference may
+    // be far from zero for the largest, see soften, and so it is below -kFar: in a piece of far tiles alone the reference is
+    // of that size)
+    line = !__any_sync(kFull, x >= kFar || fmaxf(fabsf(at_near), fabsf(at_most)) >= kFar ||
+                                  (key0 + kKeys > r.pos + 1 && r.hi > r.pos + 1));
   }
   ScoreForm form = line ? kLine : kBias;
   if (cap && slopes)
