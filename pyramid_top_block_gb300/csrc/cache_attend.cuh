@@ -751,6 +751,7 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
     see.l_hi = max(see.n_hi - w, 0);
   }
   int farther = 0;  // how much farther the nearest token in sight is than the query itself
+  int begin = 0;    // listed: the first token of the blocks that count
   int* list = reinterpret_cast<int*>(scratch);  // (listed: a row tile is one query's, so weigh leaves it alone)
   if (listed) {  // the listed blocks that count, in the order of the list
     unsigned some[2];
@@ -766,6 +767,7 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
     if constexpr (MODE == kBias || MODE == kCapped) {
       const int near = max(some[0] >> lane & 1 ? blk[0] * kC + kC : 0, some[1] >> lane & 1 ? blk[1] * kC + kC : 0);
       farther = max(see.n_hi - __reduce_max_sync(kFull, near), 0);
+      begin = __reduce_min_sync(kFull, min(some[0] >> lane & 1 ? blk[0] * kC : INT_MAX, some[1] >> lane & 1 ? blk[1] * kC : INT_MAX));
     }
   } else {
     i1 = min(i1, (max(see.n_hi, 0) + KT - 1) / KT);
@@ -845,9 +847,11 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
   if (mine > 1) issue(1, ring + kStage);
   cpa_commit();
   make_q<KIND, MODE>(a, q, u, lane, s);
-  if constexpr (MODE == kBias || MODE == kCapped) {  // (the bias is taken relative to the nearest token's: far ones' would drown the scores in 32 bits)
-    s.from0 += farther;
-    s.from1 += farther;
+  if constexpr (MODE == kBias || MODE == kCapped) {
+    // The bias is taken relative to the largest one in sight, the nearest token's or with a negative slope the farthest one's: others'
+    // would drown the scores in 32 bits.
+    s.from0 += s.bias0 < 0.f ? see.n0 - 1 - max(see.l0, begin) : farther;
+    s.from1 += s.bias1 < 0.f ? see.n1 - 1 - max(see.l1, begin) : farther;
   }
   cpa_wait<1>();
   __syncwarp();

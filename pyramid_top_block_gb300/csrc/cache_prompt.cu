@@ -338,7 +338,8 @@ struct PromptRow {
   CapRow cap;
   float slope;      // bias by distance, base 2
   int pos;          // the row's position
-  int nearest;      // the token in sight that is nearest to it
+  int zero;         // biases are relative to the one of this token, as far before the position as the token in sight that is
+                    // nearest to it, or with a negative slope farthest from it: the row's largest one
 };
 
 __device__ __forceinline__ float max3f(float a, float b, float c) {
@@ -490,7 +491,7 @@ struct Logits {
   static constexpr bool kHalf = FORM == kCapHalf || FORM == kCapLine, kStraight = FORM == kLine || FORM == kCapLine;
   static constexpr int n = kHalf ? TanhHalf::n : FORM == kCapWhole || kAny ? Tanh::n : 1;
   unsigned long long f, two, top2, c, p[n];
-  float top1, slope, d0, least;
+  float top1, slope, d0, e0;
 
   __device__ __forceinline__ Logits(const CachePromptLaunch& a, const PromptRow& r, int key0, unsigned long long m2) {
     const float top = a.score.cap * kLog2e;
@@ -514,14 +515,14 @@ struct Logits {
       c = f2_add(m2, f2_pack(top, top));
     }
     if constexpr (kStraight) {
-      const float bias = r.slope * (float)(key0 - r.nearest);  // of the first key, relative to the nearest one in sight
+      const float bias = r.slope * (float)(key0 - r.zero);  // of the first key
       slope = r.slope;
       c = f2_add(m2, f2_pack(bias, bias));
     }
-    if constexpr (kAway) {  // -slope (|p - j| - |p - nearest|): whole numbers, exact up to 2^24
+    if constexpr (kAway) {  // -slope (|p - j| - (p - zero)), the larger of zero - j and j - 2 p + zero: whole numbers, exact up to 2^24
       slope = -r.slope;
-      d0 = (float)(key0 - r.pos);
-      least = (float)abs(r.pos - r.nearest);
+      d0 = (float)(key0 - 2 * r.pos + r.zero);
+      e0 = (float)(r.zero - key0);
     }
     if constexpr (kAny || kAway) c = m2;
     top1 = top;
@@ -559,7 +560,8 @@ struct Logits {
     if constexpr (kAway) {
       float z0, z1;
       f2_unpack(z, z0, z1);
-      z = f2_pack(fmaf(slope, fabsf(d0 + (float)i) - least, z0), fmaf(slope, fabsf(d0 + (float)(i + 1)) - least, z1));
+      z = f2_pack(fmaf(slope, fmaxf(d0 + (float)i, e0 - (float)i), z0),
+                  fmaf(slope, fmaxf(d0 + (float)(i + 1), e0 - (float)(i + 1)), z1));
     }
     if constexpr (kAny || kAway) z = f2_add(z, c);
     return z;
@@ -639,15 +641,18 @@ __device__ __forceinline__ bool soften_scored(const CachePromptLaunch& a, Prompt
   if (cap && !half) b = cap_any(size, r.cap, a.score.cap * kLog2e);
   bool line = false;
   if (slopes) {
-    const float d0 = (float)(key0 - r.pos), d1 = d0 + (float)(kKeys - 1), least = (float)abs(r.pos - r.nearest);
-    const float near = d0 > 0.f ? d0 : d1 < 0.f ? -d1 : 0.f, most = fmaxf(fabsf(d0), fabsf(d1));
-    const float x = b, at_near = r.slope * (least - near), at_most = r.slope * (least - most);  // the tile's biases
-    b += fmaxf(at_near, at_most);
+    const float first = r.slope * (float)(key0 - r.zero), last = fmaf(r.slope, (float)(kKeys - 1), first);  // on the line
     // (rows that see no later tokens than their own: such are masked; from kFar on, an exact logit less a rounded reference may
     // be far from zero for the largest, see soften, and so it is below -kFar: in a piece of far tiles alone the reference is
     // of that size)
-    line = !__any_sync(kFull, x >= kFar || fmaxf(fabsf(at_near), fabsf(at_most)) >= kFar ||
+    line = !__any_sync(kFull, b >= kFar || fmaxf(fabsf(first), fabsf(last)) >= kFar ||
                                   (key0 + kKeys > r.pos + 1 && r.hi > r.pos + 1));
+    if (line) {
+      b += fmaxf(first, last);
+    } else {
+      const int d0 = key0 - r.pos, d1 = d0 + kKeys - 1, near = max(max(d0, -d1), 0), most = max(abs(d0), abs(d1));
+      b += fmaxf(r.slope * (float)(r.pos - r.zero - near), r.slope * (float)(r.pos - r.zero - most));
+    }
   }
   ScoreForm form = line ? kLine : kBias;
   if (cap && slopes)
@@ -1096,7 +1101,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (MODE != kPromptPlain && a.score.slopes) {
         r.slope = a.score.slopes[u.kv * a.G + (row & (a.G - 1))] * kLog2e;
         r.pos = s.pos;
-        r.nearest = max(min(s.pos, s.hi - 1), s.lo);
+        r.zero = s.pos - (r.slope < 0.f ? max(abs(s.pos - s.lo), abs(s.pos - s.hi + 1))
+                                        : abs(s.pos - max(min(s.pos, s.hi - 1), s.lo)));
       }
     }
     r.m = kNone;

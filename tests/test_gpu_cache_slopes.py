@@ -20,7 +20,7 @@ def expected(q, k, v, at, lo, hi, cap, slopes, weight, dtype):
     n <= 2^20, twice.  fp16 weights (4-bit pages) have steps of 2^-24 at least, relative to a reference of at most the largest
     one, so those that count are also off by 2^-25 each."""
     G = q.shape[1] // k.shape[1]
-    o, pv, big = score_ref.attention(q, k, v, at, lo, hi, cap, slopes)
+    o, pv, big = score_ref.attention(q, k, v, at.double(), lo, hi, cap, slopes)  # (whole numbers times a float are 32 bits)
     x = torch.einsum("thd,nhd->thn", q, k.repeat_interleave(G, 1)) / 8
     if cap:
         x = cap * torch.tanh(x / cap)
@@ -38,6 +38,93 @@ def check(got, want):
     off = (got.double() - o).abs()
     bad = ~(off <= tol)
     assert not bool(bad.any()), (bad.nonzero()[0].tolist(), float((off / tol)[bad].nan_to_num(nan=1e30).max()))
+
+
+def both(q, cache, n, T, cap, s, window=0):
+    """The newest T tokens by the prompts' call and by the single tokens' (bf16 and 32 bits), checked."""
+    k, v = ref.tokens(cache, 0, n)
+    at = n - T + torch.arange(T, device=DEV)
+    lo = (at - window + 1).clamp(min=0) if window else torch.zeros_like(at)
+    bf16 = cache.bits == 16
+    for dtype, weight in ((torch.bfloat16, 2.0 ** (-16 if bf16 else -11)), (torch.float32, 2.0 ** (-22 if bf16 else -20))):
+        out = torch.full((1, T, q.shape[2], 64), 7.0, dtype=dtype, device=DEV)
+        got = pisa.cache_attention(q, cache, i32([n]), out=out, cap=cap, slopes=s, window=window)
+        check(got[0], expected(q[0].double(), k, v, at, lo, at + 1, cap, s, weight, dtype))
+    got = pisa.cache_prompt_attention(q, cache, i32([n - T]), cap=cap, slopes=s, window=window)
+    check(got[0], expected(q[0].double(), k, v, at, lo, at + 1, cap, s, 2.0 ** (-8 if bf16 else -11), torch.bfloat16))
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("cap", [0.0, 40.0, 300.0])
+@pytest.mark.parametrize("n,T,window", [(90000, 3, 0), (1000, 16, 0), (30000, 2, 9000), (50, 5, 20)])
+def test_negative_slopes(bits, cap, n, T, window):
+    """Biases that grow with the distance: the first tokens in sight count, whose own bias is large."""
+    g = gen(n + T)
+    cache = make_cache(g, 1, n + 5, 1, 64, bits)
+    both(normal(g, 1, T, 8, 64) * 3, cache, n, T, cap, f32([-30.0, -4.0, -1.0, -0.1, 0.1, 1.0, 4.0, 30.0]), window)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_negative_slopes_of_prefixes(bits):
+    """Tokens behind a query in sight, the farthest ones there or before it."""
+    g = gen(3)
+    T, start = 700, 300
+    cache = make_cache(g, 1, start + T, 1, 64, bits)
+    q, s = normal(g, 1, T, 4, 64) * 3, f32([-8.0, -0.5, -0.02, 0.5])
+    last = torch.maximum(start + torch.arange(T) + 1, torch.tensor(start + 500)).to(torch.int32)[None].to(DEV)
+    k, v = ref.tokens(cache, 0, start + T)
+    at = start + torch.arange(T, device=DEV)
+    for cap in (0.0, 50.0):
+        got = pisa.cache_prompt_attention(q, cache, i32([start]), last=last, cap=cap, slopes=s)
+        check(got[0], expected(q[0].double(), k, v, at, torch.zeros_like(at), last[0].long(), cap, s,
+                               2.0 ** (-8 if bits == 16 else -11), torch.bfloat16))
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_negative_slopes_of_listed_blocks(bits):
+    g = gen(4)
+    n = 80000
+    cache = make_cache(g, 1, n, 1, 64, bits)
+    q, s = normal(g, 1, 1, 4, 64) * 3, f32([-10.0, -1.0, -0.05, 1.0])
+    blocks = [1000, 500, 777, 1200, 501]
+    at = torch.cat([torch.arange(64 * x, 64 * x + 64) for x in blocks]).sort().values.to(DEV)
+    k, v = ref.tokens(cache, 0, n)
+    keep = torch.zeros(n, dtype=torch.bool, device=DEV)
+    for window, cap in ((0, 0.0), (0, 20.0), (n - 64 * 501 - 7, 0.0)):
+        keep.zero_()
+        keep[at] = True
+        if window:
+            keep[:n - window] = False
+        j = keep.nonzero()[:, 0]
+        got = pisa.cache_attention(q, cache, i32([n]), idx=i32([[blocks + [-1]]]), cap=cap, slopes=s, window=window)
+        x = q[0, 0].double() @ k[j, 0].T / 8
+        x = (cap * torch.tanh(x / cap) if cap else x) - s.double()[:, None] * (n - 1 - j)
+        p = torch.softmax(x, -1)
+        o, pv = p @ v[j, 0], p @ v[j, 0].abs()
+        big = (q[0, 0].double().abs() @ k[j, 0].abs().T / 8).amax(1, keepdim=True)
+        tol = score_ref.tolerance(o, pv, big, j.numel(), 2.0 ** (-16 if bits == 16 else -11), torch.bfloat16, cap)
+        check(got[0, 0], (o, tol + 2.0 ** -25 * v[j, 0].abs().sum(0)))
+
+
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_negative_slopes_past_two_to_the_24(cap):
+    """Distances that 32 bits do not hold exactly, between tokens that count.  All entries of the table hold one of
+    a few pages, so that the cache is small."""
+    g = gen(5)
+    n, T, page, few = (1 << 24) + 5000, 3, 256, 8
+    for bits in (16, 4):
+        small = make_cache(g, 1, few * page, 1, page, bits)
+        e = torch.arange(-(-n // page), device=DEV)
+        table = small.table[0, e % few][None].contiguous()
+        cache = pisa.PagedCache(small.pages, table, page)
+        q, s = normal(g, 1, T, 2, 64) * 6, f32([-0.5, -2.0])
+        m = 500  # tokens that can count: the bias of the others is 100 less, which the scores (below 40) do not make up for
+        k, v = ref.tokens(cache, 0, m)
+        at = n - T + torch.arange(T, device=DEV)
+        zero = torch.zeros_like(at)
+        want = expected(q[0].double(), k, v, at, zero, zero + m, cap, s, 2.0 ** (-8 if bits == 16 else -11), torch.bfloat16)
+        check(pisa.cache_prompt_attention(q, cache, i32([n - T]), cap=cap, slopes=s)[0], want)
+        check(pisa.cache_attention(q, cache, i32([n]), cap=cap, slopes=s)[0], want)
 
 
 @pytest.mark.parametrize("bits", [16, 4])
