@@ -981,15 +981,19 @@ __device__ __forceinline__ int seq_len(const CacheAttendLaunch& a, int b, bool& 
   return n < 0 ? 0 : over ? (int)cap : n;
 }
 
-// The tiles and places of a unit of a sequence of n tokens (cache_stream.cuh).
+// The tiles of a unit of a sequence of n tokens, and the places of so many (cache_stream.cuh).
 // A unit has places in the stream for its tiles, and some for what a run spends at
 // its end (the warps' merge, the next unit's chain of loads; about 4 us), so that the runs that
 // change units take as long as the others.  Places at the end 0 / 12 / 24 / 36 / 48, us a call:
 //   4 bits  16 x 131072 73.5 / 72.1 / 71.5 / 71.6 / 71.9   64 x 9000 ragged, 8 heads 88.8 / 63.6 / 56.7 / 57.5 / 59.8
 //   bf16    8 x 131072 ragged 64.8 / 63.8 / 63.3 / 63.0 / 63.3   64 x 9000 ragged, 8 heads 119.7 / 103 / 96.3 / 96.5 / 97.4
 template <int KIND, int MODE>
-__device__ __forceinline__ SeqTiles tiles_of_seq(const CacheAttendLaunch& a, int n) {
-  return seq_tiles<Cfg<KIND>::KT, MODE != kPlain>(n, a.T, a.score.window, Cfg<KIND>::kChange);
+__device__ __forceinline__ int tiles_of_seq(const CacheAttendLaunch& a, int n) {
+  return unit_tiles<Cfg<KIND>::KT, MODE != kPlain>(n, a.T, a.score.window);
+}
+template <int KIND>
+__device__ __forceinline__ int places_of(int tiles) {
+  return unit_places<Cfg<KIND>::kChange>(tiles);
 }
 
 // Places of all units before sequence b (b = B: of all): every warp computes it by itself.
@@ -997,7 +1001,7 @@ template <int KIND, int MODE>
 __device__ __forceinline__ long long places_before(const CacheAttendLaunch& a, int b, int units, int lane) {
   long long sum = 0;
   bool over;
-  for (int i = lane; i < b; i += 32) sum += tiles_of_seq<KIND, MODE>(a, seq_len(a, i, over)).places;
+  for (int i = lane; i < b; i += 32) sum += places_of<KIND>(tiles_of_seq<KIND, MODE>(a, seq_len(a, i, over)));
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(kFull, sum, x);
   return sum * units;
@@ -1011,7 +1015,7 @@ __device__ __forceinline__ int seq_of(const CacheAttendLaunch& a, long long at, 
   for (int b0 = 0; b0 < a.cache.B; b0 += 32) {
     bool over;
     const int n = b0 + lane < a.cache.B ? seq_len(a, b0 + lane, over) : 0;
-    const long long t = (long long)tiles_of_seq<KIND, MODE>(a, n).places * units;
+    const long long t = (long long)places_of<KIND>(tiles_of_seq<KIND, MODE>(a, n)) * units;
     long long inc = t;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
@@ -1126,8 +1130,7 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_
   u.sel = nullptr;
   while (cur < end) {
     u.n = seq_len(a, u.b, over);
-    const SeqTiles unit = tiles_of_seq<KIND, MODE>(a, u.n);
-    const int nt = unit.tiles, places = unit.places;
+    const int nt = tiles_of_seq<KIND, MODE>(a, u.n), places = places_of<KIND>(nt);
     if (nt == 0 || cur >= base + (long long)places * units) {  // on to the next sequence
       base += (long long)places * units;
       ++u.b;
@@ -1145,7 +1148,7 @@ __global__ void __launch_bounds__(Cfg<KIND>::kWarps * 32, 1) cache_attend_split_
     QueryWords q;
     fetch_q(a, u, lane, q);
     reset(s);
-    const int t0 = unit.first;
+    const int t0 = first_tile<C::KT, MODE != kPlain>(u.n, a.T, a.score.window);
     run_tiles<KIND, U, NP, W, false, MODE>(a, u, q, blk, t0 + i0, t0 + i1, ring, scratch, warp, lane, s);
     if ((threadIdx.x == 0 && over) || (lane == 0 && s.bad)) set_status(a.status, PISA_ERR_DEVICE_BOUNDS);
     merge_warps<KIND, W>(s, mo, ml, warp, lane);
@@ -1210,10 +1213,10 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, in
     set_unit(un);
     bool over;
     u.n = seq_len(a, u.b, over);
-    const SeqTiles unit_is = tiles_of_seq<KIND, MODE>(a, u.n);
-    const long long w0 = places_before<KIND, MODE>(a, u.b, units, lane) + (long long)un * unit_is.places;
+    const int nt = tiles_of_seq<KIND, MODE>(a, u.n);
+    const long long w0 = places_before<KIND, MODE>(a, u.b, units, lane) + (long long)un * places_of<KIND>(nt);
     c0 = (int)(w0 / per);
-    cut = goes_on(w0, unit_is.tiles, per, c0, c1);
+    cut = goes_on(w0, nt, per, c0, c1);
   } else {
     const int cta = blockIdx.x / 4;
     c0 = kSide ? cta / RT : cta;
@@ -1225,10 +1228,10 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendLaunch a, in
       u.b = seq_of<KIND, MODE>(a, end - 1, units, lane, base);
       bool over;
       u.n = seq_len(a, u.b, over);
-      const SeqTiles unit_is = tiles_of_seq<KIND, MODE>(a, u.n);
-      const unsigned un = unit_at(end - 1 - base, unit_is.places);
+      const int nt = tiles_of_seq<KIND, MODE>(a, u.n), places = places_of<KIND>(nt);
+      const unsigned un = unit_at(end - 1 - base, places);
       set_unit(un);
-      cut = goes_on(base + (long long)un * unit_is.places, unit_is.tiles, per, c0, c1);
+      cut = goes_on(base + (long long)un * places, nt, per, c0, c1);
     }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -8,20 +8,22 @@ namespace pisa {
 
 constexpr int kCaMinTiles = 12;  // places of the stream that a run has at least
 
-// A unit (KV head and row tile) of a sequence of n tokens, whose newest T queries it holds.
-struct SeqTiles {
-  int first;   // the first tile that any of the queries sees
-  int tiles;   // how many there are
-  int places;  // places of the stream: the tiles, and `change` more for the unit's end
-};
+// A unit (KV head and row tile) of a sequence of n tokens, whose newest T are queries: the first tile that any of them sees ..
 template <int KT, bool WINDOWED>
-__host__ __device__ __forceinline__ SeqTiles seq_tiles(int n, int T, int window, int change) {
-  SeqTiles s;
+__host__ __device__ __forceinline__ int first_tile(int n, int T, int window) {
   const int before = WINDOWED ? n - T + 1 - window : 0;  // tokens before the first query's window
-  s.first = before > 0 ? before / KT : 0;
-  s.tiles = (n + KT - 1) / KT - s.first;
-  s.places = s.tiles ? s.tiles + change : 0;
-  return s;
+  return before > 0 ? before / KT : 0;
+}
+// .. how many there are, ..
+template <int KT, bool WINDOWED>
+__host__ __device__ __forceinline__ int unit_tiles(int n, int T, int window) {
+  return (n + KT - 1) / KT - first_tile<KT, WINDOWED>(n, T, window);
+}
+// .. and their places in the stream: the tiles, and CHANGE more for the unit's end.
+// (All three as one struct from one function: 8 x 131072 tokens of bf16, T = 3, 141.2 instead of 137.5 us, T = 8 352 instead of 342.)
+template <int CHANGE>
+__host__ __device__ __forceinline__ int unit_places(int tiles) {
+  return tiles ? tiles + CHANGE : 0;
 }
 
 // Places of a run.

@@ -22,6 +22,12 @@ HOST = r"""
 using namespace pisa;
 
 struct Part { int b; unsigned un; int i0, i1; };
+struct SeqTiles { int first, tiles, places; };
+template <int KT, bool WINDOWED>
+static SeqTiles seq_tiles(int n, int T, int window, int change) {
+  const int tiles = unit_tiles<KT, WINDOWED>(n, T, window);
+  return {first_tile<KT, WINDOWED>(n, T, window), tiles, change == 36 ? unit_places<36>(tiles) : unit_places<24>(tiles)};
+}
 
 // Replays a call on `runs` runs, `units` units a sequence.  Returns 0, or which rule does not hold.
 template <int KT, bool WINDOWED>
@@ -168,8 +174,9 @@ def test_the_kernels_take_the_arithmetic_from_the_header():
     text = code_of("cache_attend.cuh")
     for name in ("cache_attend_split_kernel", "cache_join_kernel"):
         body = re.search(name + r"\(CacheAttendLaunch a.*?\n}\n", text, re.S).group(0)
-        assert "tiles_of_seq<KIND, MODE>" in body and "run_length(" in body and "unit_at(" in body
-        assert not re.search(r"\bKT\b|kChange|/ per|/ \(unsigned\)", body.replace("c0 = (int)(w0 / per)", ""))
+        assert "tiles_of_seq<KIND, MODE>" in body and "places_of<KIND>" in body and "run_length(" in body and "unit_at(" in body
+        body = body.replace("c0 = (int)(w0 / per)", "").replace("first_tile<C::KT, ", "")
+        assert not re.search(r"\bKT\b|kChange|/ per|/ \(unsigned\)", body)
     assert text.count("goes_on(") == 2
 
 
