@@ -381,7 +381,7 @@ int pisa_cache_append_axes(const pisa_paged_cache* cache, int T, const pisa_rows
  * for a query at position p and a token at position j, which it sees if j <= p and (window >
  * 0) j > p - window.
  *   cap    : 0 (no cap), or 2^-20 .. 2^20
- *   slopes : device fp32 [Hq], finite, of either sign, or NULL
+ *   slopes : device fp32 [Hq], finite, of either sign, or NULL; past 2^96 they count as 2^96
  *   window : tokens, the query's own among them; 0: no window
  * Tokens before the window do not matter either, nor do their pages, which may have been given
  * away.  With a cap an infinite product is a logit of plus or minus cap.  The scores take one

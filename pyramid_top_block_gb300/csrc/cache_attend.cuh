@@ -292,8 +292,8 @@ __device__ __forceinline__ void make_q(const CacheAttendLaunch& a, const QueryWo
     s.bias0 = s.bias1 = 0.f;
     const int r0 = u.r0 + (lane >> 2), r1 = r0 + 8;
     if (a.score.slopes) {
-      if (r0 < u.rows) s.bias0 = a.score.slopes[u.kv * a.G + r0 % a.G] * kLog2e;
-      if (r1 < u.rows) s.bias1 = a.score.slopes[u.kv * a.G + r1 % a.G] * kLog2e;
+      if (r0 < u.rows) s.bias0 = slope2(a.score, u.kv * a.G + r0 % a.G);
+      if (r1 < u.rows) s.bias1 = slope2(a.score, u.kv * a.G + r1 % a.G);
     }
     // this lane's keys of a tile lie from 2 j (bf16) or j (4 bits) on; a row's position is n - 1 of what it sees
     const int base = u.n - a.T + u.t_first, at = KIND == PISA_CACHE_BF16 ? 2 * j : j;
@@ -306,8 +306,11 @@ __device__ __forceinline__ void make_q(const CacheAttendLaunch& a, const QueryWo
     s.f0 = s.f1 = 1.f;
   }
   if constexpr (MODE == kBias) {
-    s.bias0 /= f[0];
-    s.bias1 /= f[1];
+    // (cut at 2^99 of the products' units, for the same reason as a slope is: 4-bit pages' products, below 2^19, do not make up for
+    // a token's distance then, and with bf16 pages it is the slope's own cut)
+    const float most0 = 0x1p99f * f[0], most1 = 0x1p99f * f[1];
+    s.bias0 = fminf(fmaxf(s.bias0, -most0), most0) / f[0];
+    s.bias1 = fminf(fmaxf(s.bias1, -most1), most1) / f[1];
   }
 }
 

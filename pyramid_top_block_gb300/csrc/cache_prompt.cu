@@ -1099,7 +1099,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       r.lo = s.lo;
       r.hi = s.hi;
       if (MODE != kPromptPlain && a.score.slopes) {
-        r.slope = a.score.slopes[u.kv * a.G + (row & (a.G - 1))] * kLog2e;
+        r.slope = slope2(a.score, u.kv * a.G + (row & (a.G - 1)));
         r.pos = s.pos;
         r.zero = s.pos - (r.slope < 0.f ? max(abs(s.pos - s.lo), abs(s.pos - s.hi + 1))
                                         : abs(s.pos - max(min(s.pos, s.hi - 1), s.lo)));

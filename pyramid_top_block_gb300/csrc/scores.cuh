@@ -17,6 +17,11 @@ struct ScoreDev {
   int window;           // a query sees tokens p - window + 1 and later
 };
 
+// A head's slope in base 2.  Past 2^96 it is cut, so that times a distance, below 2^28, it fits 32 bits.
+__device__ __forceinline__ float slope2(const ScoreDev& s, int head) {
+  return fminf(fmaxf(s.slopes[head], -0x1p96f), 0x1p96f) * 1.4426950408889634f;
+}
+
 // tanh(y) / y as polynomials in u = y y: the interpolations at the Chebyshev nodes, of degree 6 on |y| <= 1, off by at
 // most 6.0e-8 of the value (a rounding to 32 bits), and of degree 3 on |y| <= 1/2 (5.6e-07).  One minus twice the
 // reciprocal of 1 + e^(2 y) would take two slow instructions a score, and loses small scores' last bits.

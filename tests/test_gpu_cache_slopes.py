@@ -140,3 +140,25 @@ def test_steep_slopes_over_long_caches(bits, cap, n, T):
     zero = torch.zeros_like(at)
     got = pisa.cache_prompt_attention(q, cache, i32([n - T]), cap=cap, slopes=s)
     check(got[0], expected(q[0].double(), k, v, at, zero, at + 1, cap, s, 2.0 ** (-8 if bits == 16 else -11), torch.bfloat16))
+
+
+@pytest.mark.parametrize("bits,size", [(16, 1.0), (4, 1.0), (4, 2.0 ** -75)])
+@pytest.mark.parametrize("cap", [0.0, 40.0])
+def test_slopes_of_any_size(bits, size, cap):
+    """The header asks for finite ones alone."""
+    g = gen(8)
+    n, T = 5000, 4
+    cache = make_cache(g, 1, n, 1, 64, bits, k_exp=-24 if size < 1 else 0)
+    q = (normal(g, 1, T, 8, 64) * size).to(torch.bfloat16)
+    for s in ([1e5, -1e5, 1e12, -1e12, 1e30, -1e30, 3e38, -3e38], [1e-30, -1e-30, 1e-44, -1e-44, 0.0, -0.0, 1e-20, -1e-20]):
+        both(q, cache, n, T, cap, f32(s))
+
+
+def test_slopes_of_huge_queries_over_keys_of_zero():
+    """4-bit keys of zero have scores of zero whatever the queries are, so that the bias alone decides."""
+    g = gen(10)
+    n, T = 3000, 3
+    cache = make_cache(g, 1, n, 1, 64, 4, k_exp=10)
+    cache.pages.view(cache.pages.shape[0], 144, 32)[:, 0:64] = 0
+    q = (torch.sign(normal(g, 1, T, 4, 64)) * 2.0 ** 126).to(torch.bfloat16)
+    both(q, cache, n, T, 0.0, f32([0.002, -0.003, 0.7, 1e-5]))
