@@ -47,11 +47,13 @@ __device__ __forceinline__ Span span_of(const CachePromptLaunch& a, int b, int t
   const long long start = a.start[b], p = start + t, end = start + count;
   over = start < 0 || end > cap;
   Span s;
-  s.pos = (int)p;
+  // (one past either end of the table as the end itself: that adds as much to the distance of all that it sees, and stays far
+  // from 32 bits' ends)
+  s.pos = (int)(p < 0 ? 0 : p > cap ? cap : p);
   long long hi = a.last ? a.last[(long long)b * a.T + t] : p + 1, lo = a.first ? a.first[(long long)b * a.T + t] : 0;
   hi = hi < end ? hi : end;
   hi = hi < cap ? hi : cap;
-  if (p - a.score.window + 1 > lo) lo = p - a.score.window + 1;
+  if (a.score.window < kNoWindow && p - a.score.window + 1 > lo) lo = p - a.score.window + 1;
   s.lo = (int)(lo < 0 ? 0 : lo > cap ? cap : lo);
   s.hi = (int)(hi < 0 ? 0 : hi);
   return s;

@@ -162,3 +162,26 @@ def test_slopes_of_huge_queries_over_keys_of_zero():
     cache.pages.view(cache.pages.shape[0], 144, 32)[:, 0:64] = 0
     q = (torch.sign(normal(g, 1, T, 4, 64)) * 2.0 ** 126).to(torch.bfloat16)
     both(q, cache, n, T, 0.0, f32([0.002, -0.003, 0.7, 1e-5]))
+
+
+def test_positions_past_the_table_with_slopes():
+    """Starts at both ends of 32 bits: flagged, and what is in sight still counts by the distances between the tokens."""
+    g = gen(9)
+    for bits in (16, 4):
+        cache = make_cache(g, 1, 512, 1, 64, bits)
+        n, T = 512, 12
+        q, s = normal(g, 1, T, 4, 64) * 3, f32([0.05, -0.05, 1.0, 0.0])
+        k, v = ref.tokens(cache, 0, n)
+        for cap in (0.0, 6.0):
+            for start, last in (((1 << 31) - 16, None), (-(1 << 31) + 8, [[0, 5, 512] * 4])):
+                at = start + torch.arange(T, device=DEV)
+                hi = torch.full_like(at, n)
+                ws = pisa.cache_workspace(cache)
+                got = pisa.cache_prompt_attention(q, cache, i32([start]), last=None if last is None else i32(last), cap=cap,
+                                                  slopes=s, workspace=ws)
+                assert status(ws) == 6
+                if last is not None:  # (no token of the sequence is there: it ends before 0)
+                    assert not bool(got.any())
+                    continue
+                check(got[0], expected(q[0].double(), k, v, at, torch.zeros_like(at), hi, cap, s,
+                                       2.0 ** (-8 if bits == 16 else -11), torch.bfloat16))
