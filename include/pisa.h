@@ -446,7 +446,7 @@ size_t pisa_pool_workspace_bytes(int n_pages, int B);
  * the table becomes the row that parents[b] had, lengths[b] the length that it had.  parents[b] = b
  * keeps a sequence, a negative one frees it (a row of -1, length 0), one past B - 1 keeps it and
  * flags PISA_ERR_DEVICE_BOUNDS.  Pages that no row holds any longer are free.
- *   parents : device int32 [B]; lengths : device int32 [B]; ws : workspace for the status word, or NULL
+ *   parents : device int32 [B]; lengths : device int32 [B], apart from it; ws : workspace for the status word, or NULL
  */
 int pisa_cache_fork(const pisa_page_pool* pool, const int32_t* parents, int32_t* lengths, void* ws, void* stream);
 
@@ -459,7 +459,7 @@ int pisa_cache_fork(const pisa_page_pool* pool, const int32_t* parents, int32_t*
  * if all sequences up to it together need no more than were free at the call (pages that the call itself
  * lets go count from the next one on); one that is not served stays as it is.
  *   granted : device int32 [B]: counts[b], or 0 for a sequence that was not served (the counts of the
- *             append that follows)
+ *             append that follows); may be counts itself, else apart from it, and from lengths
  * A length that is negative, or that would pass max_pages * page_size, is not served and flags
  * PISA_ERR_DEVICE_BOUNDS; a lack of pages is told by granted alone.
  */

@@ -94,6 +94,17 @@ int check_pool(const pisa_page_pool* c, PoolDev& d) {
   return PISA_OK;
 }
 
+// Whether two lists of whole numbers share entries (none: nullptr).
+bool overlap(const int32_t* a, long long n, const int32_t* b, long long m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + 4 * (uintptr_t)m && y < x + 4 * (uintptr_t)n;
+}
+
+// Whether a list of n entries that a call writes lies in what it keeps in line.
+bool in_pool(const PoolDev& p, const int32_t* x, long long n) {
+  return overlap(x, n, p.table, (long long)p.B * p.max_pages) || overlap(x, n, p.refs, p.n_pages);
+}
+
 // The lists of whole numbers behind the status word.
 PoolScratch pool_scratch(const PoolDev& p, void* ws) {
   int32_t* x = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + kCacheStatusBytes);
@@ -286,6 +297,7 @@ int pisa_cache_fork(const pisa_page_pool* pool, const int32_t* parents, int32_t*
   if (st) return st;
   if (!parents || !lengths || !aligned(parents, 4) || !aligned(lengths, 4) || !aligned(ws, 4)) return PISA_ERR_INVALID_ARG;
   if (pool->B > kForkMaxB) return PISA_ERR_UNSUPPORTED;
+  if (overlap(parents, pool->B, lengths, pool->B) || in_pool(L.pool, lengths, pool->B)) return PISA_ERR_INVALID_ARG;
   L.parents = parents;
   L.lengths = lengths;
   L.status = static_cast<int*>(ws);
@@ -299,6 +311,10 @@ int pisa_cache_reserve(const pisa_page_pool* pool, const int32_t* lengths, int T
   if (st) return st;
   if (!lengths || T < 1 || !granted || !ws) return PISA_ERR_INVALID_ARG;
   if (!aligned(lengths, 4) || !aligned(counts, 4) || !aligned(granted, 4) || !aligned(ws, 256)) return PISA_ERR_INVALID_ARG;
+  // (lengths and counts are read again when some grants are written; a grant in its count's place is that count, or is not read again)
+  if (overlap(granted, pool->B, lengths, pool->B) || (granted != counts && overlap(granted, pool->B, counts, pool->B)) ||
+      in_pool(L.pool, granted, pool->B))
+    return PISA_ERR_INVALID_ARG;
   if (ws_bytes < pisa_pool_workspace_bytes(pool->n_pages, pool->B)) return PISA_ERR_WORKSPACE_TOO_SMALL;
   L.ws = pool_scratch(L.pool, ws);
   L.lengths = lengths;
@@ -313,7 +329,7 @@ int pisa_cache_compact(const pisa_page_pool* pool, int32_t* used, void* ws, size
   PoolCompactLaunch L{};
   const int st = check_pool(pool, L.pool);
   if (st) return st;
-  if (!used || !aligned(used, 4) || !ws || !aligned(ws, 256)) return PISA_ERR_INVALID_ARG;
+  if (!used || !aligned(used, 4) || !ws || !aligned(ws, 256) || in_pool(L.pool, used, 1)) return PISA_ERR_INVALID_ARG;
   if (ws_bytes < pisa_pool_workspace_bytes(pool->n_pages, pool->B)) return PISA_ERR_WORKSPACE_TOO_SMALL;
   L.ws = pool_scratch(L.pool, ws);
   L.used = used;
