@@ -296,6 +296,10 @@ size_t pisa_cache_page_bytes(int page_size, int Hkv, int kind);
  * workspace must not overlap on the GPU; that includes replays of captured graphs. */
 size_t pisa_cache_workspace_bytes(void);
 
+/* What pisa_cache_attention and pisa_cache_attention_scored need of it: enough for a program that has no
+ * prompts to attend (1.3 MB instead of 21). */
+size_t pisa_cache_attention_workspace_bytes(void);
+
 /*
  * pisa_cache_append -- rotate new queries and keys, put keys and values into the cache.
  * Token t < counts[b] of sequence b has position start[b] + t.  In the first `rot` dims of
@@ -343,7 +347,7 @@ int pisa_cache_read(const pisa_paged_cache* cache, int T, const int32_t* start, 
  *             negative or begin after the query are skipped, one listed twice counts
  *             twice; NULL: every token (Ksel ignored)
  *   out     : device [B, T, Hq, d] dense, 16-byte aligned, fp32 (out_f32 != 0) or bf16
- *   ws      : workspace of pisa_cache_workspace_bytes(), 256-byte aligned
+ *   ws      : workspace of pisa_cache_attention_workspace_bytes() or more, 256-byte aligned
  * A query that sees no token, or none whose logit is above minus infinity, gets zeros;
  * tokens that it does not see do not matter, whatever their values, nor do the pages they
  * lie in.  One that sees a token in a page outside [0, n_pages) gets NaNs, and

@@ -108,6 +108,8 @@ def load(path: str | None = None):
     lib.pisa_cache_page_bytes.restype = sz
     lib.pisa_cache_workspace_bytes.argtypes = []
     lib.pisa_cache_workspace_bytes.restype = sz
+    lib.pisa_cache_attention_workspace_bytes.argtypes = []
+    lib.pisa_cache_attention_workspace_bytes.restype = sz
     lib.pisa_cache_append.argtypes = [vp, i32, vp, i32, vp, vp, vp, vp, vp, i64, i32, i32, vp, vp, vp, vp]
     lib.pisa_cache_append.restype = i32
     lib.pisa_cache_read.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp]
@@ -538,19 +540,23 @@ def rotary_table(n: int, rot: int = D, base: float = 10000.0, device="cuda") -> 
     return torch.cat([angle.cos(), angle.sin()], 1).float()
 
 
-_cache_ws_bytes = 0  # asked once: it is the same for every size
+_cache_ws_bytes = _token_ws_bytes = 0  # asked once: they are the same for every size
 
 
-def cache_workspace_bytes() -> int:
-    global _cache_ws_bytes
-    _cache_ws_bytes = int(load().pisa_cache_workspace_bytes())
-    return _cache_ws_bytes
+def cache_workspace_bytes(prompts: bool = True) -> int:
+    """Bytes that suffice for every cache call, or for all but cache_prompt_attention."""
+    global _cache_ws_bytes, _token_ws_bytes
+    if not _cache_ws_bytes:
+        _token_ws_bytes = int(load().pisa_cache_attention_workspace_bytes())
+        _cache_ws_bytes = int(load().pisa_cache_workspace_bytes())
+    return _cache_ws_bytes if prompts else _token_ws_bytes
 
 
-def cache_workspace(cache: PagedCache) -> torch.Tensor:
+def cache_workspace(cache: PagedCache, prompts: bool = True) -> torch.Tensor:
     """A workspace for the cache calls on this cache's device, its status word zero.  One stream at a time; the
-    word keeps the first error of all the calls (check_device_status)."""
-    return torch.zeros(cache_workspace_bytes(), dtype=torch.uint8, device=cache.device)
+    word keeps the first error of all the calls (check_device_status).  Without prompts it is too small for
+    cache_prompt_attention (1.3 MB instead of 21)."""
+    return torch.zeros(cache_workspace_bytes(prompts), dtype=torch.uint8, device=cache.device)
 
 
 # (the current stream's handle and the current device's number without the objects around them: a decoding step
@@ -757,7 +763,7 @@ def cache_attention(q: torch.Tensor, cache: PagedCache, lengths: torch.Tensor, i
           or out.shape != shape or not out.is_contiguous()):
         raise ValueError(f"out must be a contiguous bf16 or fp32 tensor {list(shape)}")
     lib = _lib or load()
-    need = _cache_ws_bytes or cache_workspace_bytes()
+    need = _token_ws_bytes or cache_workspace_bytes(False)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
     if cap != 0 or slopes is not None or window != 0:

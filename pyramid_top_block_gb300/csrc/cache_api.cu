@@ -134,6 +134,8 @@ size_t pisa_cache_workspace_bytes(void) {
   return kCacheStatusBytes + (a > b ? a : b);
 }
 
+size_t pisa_cache_attention_workspace_bytes(void) { return kCacheStatusBytes + cache_part_bytes(); }
+
 static int cache_append(const pisa_paged_cache* cache, int T, const pisa_rows* q, int Hq, const pisa_rows* k,
                       const pisa_rows* v, const int32_t* start, const int32_t* counts, const float* rotary,
                       int64_t n_rot, int rot, int interleaved, const pisa_rows* q_out, const pisa_rows* k_out,
@@ -216,7 +218,7 @@ static int cache_attention(const pisa_paged_cache* cache, const pisa_rows* q, in
   if (T > kCacheMaxT || !group_ok(Hq, cache->Hkv)) return PISA_ERR_UNSUPPORTED;
   if (idx && (Ksel < 1 || Ksel > kCacheMaxSel)) return PISA_ERR_UNSUPPORTED;
   if ((long long)cache->B * T * cache->Hkv >= (1LL << 24)) return PISA_ERR_UNSUPPORTED;
-  if (ws_bytes < pisa_cache_workspace_bytes()) return PISA_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < pisa_cache_attention_workspace_bytes()) return PISA_ERR_WORKSPACE_TOO_SMALL;
   L.T = T;
   L.Hq = Hq;
   L.G = Hq / cache->Hkv;
