@@ -946,6 +946,8 @@ def cache_reserve(pool: PagePool, lengths: torch.Tensor, T: int, counts: torch.T
     if guard is not None:
         with guard:
             return cache_reserve(pool, lengths, T, counts, granted, workspace)
+    if not -1 << 31 <= T < 1 << 31:  # (what a C int would be cut from)
+        raise ValueError("T must fit 32 bits")
     if granted is None:
         granted = torch.empty(pool.B, dtype=torch.int32, device=pool.device)
     need = pool._need
