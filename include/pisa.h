@@ -430,7 +430,10 @@ int pisa_cache_prompt_attention(const pisa_paged_cache* cache, const pisa_rows* 
  *   page_size   : 16, 32, 64, 128 or 256 tokens; max_pages * page_size <= 2^27
  *   B, n_pages  : B <= 65535 (a fork: 32768), n_pages <= 2^30
  * A new pool has a table of -1 and references of 0.  The calls keep refs in line with the table; a
- * call on a pool where they are not in line reads and writes no other memory than the pool's.
+ * call on a pool where they are not in line reads and writes no other memory than the pool's.  So every
+ * reference is an entry of the table: pages that are to outlive their sequences (of a prefix that others will
+ * begin with) are held by a sequence of the pool, not by a count of their own, since a compaction moves pages
+ * and tells the table alone.
  * Calls on one pool must not overlap on the GPU.
  */
 typedef struct {
@@ -450,6 +453,9 @@ size_t pisa_pool_workspace_bytes(int n_pages, int B);
  * the table becomes the row that parents[b] had, lengths[b] the length that it had.  parents[b] = b
  * keeps a sequence, a negative one frees it (a row of -1, length 0), one past B - 1 keeps it and
  * flags PISA_ERR_DEVICE_BOUNDS.  Pages that no row holds any longer are free.
+ * What else a sequence has goes with the caller: a layer that selects has its pyramid (keys, summaries and
+ * lengths), which is not paged, so its rows are copied by the same parents, or the selection that follows
+ * is made from another sequence's history.
  *   parents : device int32 [B]; lengths : device int32 [B], apart from it; ws : workspace for the status word, or NULL
  */
 int pisa_cache_fork(const pisa_page_pool* pool, const int32_t* parents, int32_t* lengths, void* ws, void* stream);
@@ -459,7 +465,9 @@ int pisa_cache_fork(const pisa_page_pool* pool, const int32_t* parents, int32_t*
  * it, the pages of positions lengths[b] .. lengths[b] + counts[b] - 1 are there and no other sequence's:
  * where an entry has no page, or one with more than one reference, it gets a free one, and a shared page
  * that holds tokens before lengths[b] is copied as a whole.  Free pages are taken lowest number first, by
- * sequences in order and by a sequence's entries in order.  A sequence is served if it needs no page, or
+ * sequences in order and by a sequence's entries in order.  Every sharer of a page that is about to be
+ * written gets a copy, the last one too: n sequences on one page need n pages, and the page that they
+ * shared is free after the call.  A sequence is served if it needs no page, or
  * if all sequences up to it together need no more than were free at the call (pages that the call itself
  * lets go count from the next one on); one that is not served stays as it is.
  *   granted : device int32 [B]: counts[b], or 0 for a sequence that was not served (the counts of the

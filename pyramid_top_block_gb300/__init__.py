@@ -925,7 +925,8 @@ def cache_fork(pool: PagePool, parents: torch.Tensor, lengths: torch.Tensor, wor
                stream=None) -> None:
     """Sequences become copies of others by sharing their pages, all at once: sequence b takes the pages and the
     length that parents[b] had (int32 [B]; b: it stays as it is; -1: it is freed, its length 0).  lengths int32 [B] is
-    updated in place.  workspace (of pool_workspace): for the status word only."""
+    updated in place.  workspace (of pool_workspace): for the status word only.  A layer that selects copies its
+    pyramid's rows as well (keys and summaries: x.copy_(x[parents])), which are not paged."""
     guard = _on(pool, stream)
     if guard is not None:
         with guard:
@@ -940,8 +941,9 @@ def cache_reserve(pool: PagePool, lengths: torch.Tensor, T: int, counts: torch.T
                   stream=None) -> torch.Tensor:
     """Pages for the next counts[b] (0 to T; None: T) tokens of every sequence, its own alone: missing ones are taken
     from the free pages, lowest number first, and shared ones are replaced, the one that holds tokens before lengths[b]
-    being copied.  Returns granted int32 [B]: counts[b], or 0 where the pages did not suffice (that sequence and those
-    after it that need any stay as they are); it is what cache_append takes as counts.  workspace of pool_workspace."""
+    being copied (for each of its sharers).  Returns granted int32 [B]: counts[b], or 0 where the pages did not suffice
+    (that sequence and those after it that need any stay as they are); it is what cache_append takes as counts, and may be
+    given as counts itself.  workspace of pool_workspace."""
     guard = _on(pool, stream)
     if guard is not None:
         with guard:
@@ -963,7 +965,8 @@ def cache_reserve(pool: PagePool, lengths: torch.Tensor, T: int, counts: torch.T
 def cache_compact(pool: PagePool, used: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                   stream=None) -> torch.Tensor:
     """Moves the pages in use to the front of the pool, in the table and refs too.  Returns used int32 [1], how many
-    there are: pages from that number on are free.  workspace of pool_workspace."""
+    there are: pages from that number on are free.  The table alone is told where pages went: nothing else may hold
+    page numbers over the call.  workspace of pool_workspace."""
     guard = _on(pool, stream)
     if guard is not None:
         with guard:
