@@ -491,7 +491,7 @@ struct Logits {
   static constexpr bool kHalf = FORM == kCapHalf || FORM == kCapLine, kStraight = FORM == kLine || FORM == kCapLine;
   static constexpr int n = kHalf ? TanhHalf::n : FORM == kCapWhole || kAny ? Tanh::n : 1;
   unsigned long long f, two, top2, c, p[n];
-  float top1, slope, d0, e0;
+  float top1, slope, d0, least;
 
   __device__ __forceinline__ Logits(const CachePromptLaunch& a, const PromptRow& r, int key0, unsigned long long m2) {
     const float top = a.score.cap * kLog2e;
@@ -519,10 +519,13 @@ struct Logits {
       slope = r.slope;
       c = f2_add(m2, f2_pack(bias, bias));
     }
-    if constexpr (kAway) {  // -slope (|p - j| - (p - zero)), the larger of zero - j and j - 2 p + zero: whole numbers, exact up to 2^24
+    if constexpr (kAway) {
+      // -slope (|j - p| - (p - zero)): whole numbers, exact up to 2^24.  Both distances less what all keys of the tile have of the
+      // second, so that they are small where their difference is.
+      const int d = key0 - r.pos, away = r.pos - r.zero, both = min(max(max(d, 1 - kKeys - d), 0), away);
       slope = -r.slope;
-      d0 = (float)(key0 - 2 * r.pos + r.zero);
-      e0 = (float)(r.zero - key0);
+      d0 = (float)(d < 0 ? d + both : d - both);
+      least = (float)(away - both);
     }
     if constexpr (kAny || kAway) c = m2;
     top1 = top;
@@ -560,8 +563,7 @@ struct Logits {
     if constexpr (kAway) {
       float z0, z1;
       f2_unpack(z, z0, z1);
-      z = f2_pack(fmaf(slope, fmaxf(d0 + (float)i, e0 - (float)i), z0),
-                  fmaf(slope, fmaxf(d0 + (float)(i + 1), e0 - (float)(i + 1)), z1));
+      z = f2_pack(fmaf(slope, fabsf(d0 + (float)i) - least, z0), fmaf(slope, fabsf(d0 + (float)(i + 1)) - least, z1));
     }
     if constexpr (kAny || kAway) z = f2_add(z, c);
     return z;
@@ -636,23 +638,18 @@ __device__ __forceinline__ bool soften_scored(const CachePromptLaunch& a, Prompt
   tmem_ld128_top<true>(s, all, size);
   const bool in_range = r.cap.to_y <= kCapMost && (KIND == PISA_CACHE_E2M1 || r.cap.to_y >= kCapLeast);
   const bool half = cap && !__any_sync(kFull, !in_range || size * r.cap.to_y > 0.5f);
-  // at least the row's largest logit (a cap makes none larger; the nearer end of the line adds the more, or the less negative)
+  // at least the row's largest logit (a cap makes none larger)
   float b = size * r.f;
   if (cap && !half) b = cap_any(size, r.cap, a.score.cap * kLog2e);
   bool line = false;
   if (slopes) {
-    const float first = r.slope * (float)(key0 - r.zero), last = fmaf(r.slope, (float)(kKeys - 1), first);  // on the line
-    // (rows that see no later tokens than their own: such are masked; from kFar on, an exact logit less a rounded reference may
-    // be far from zero for the largest, see soften, and so it is below -kFar: in a piece of far tiles alone the reference is
-    // of that size)
-    line = !__any_sync(kFull, b >= kFar || fmaxf(fabsf(first), fabsf(last)) >= kFar ||
-                                  (key0 + kKeys > r.pos + 1 && r.hi > r.pos + 1));
-    if (line) {
-      b += fmaxf(first, last);
-    } else {
-      const int d0 = key0 - r.pos, d1 = d0 + kKeys - 1, near = max(max(d0, -d1), 0), most = max(abs(d0), abs(d1));
-      b += fmaxf(r.slope * (float)(r.pos - r.zero - near), r.slope * (float)(r.pos - r.zero - most));
-    }
+    const int d0 = key0 - r.pos, d1 = d0 + kKeys - 1, near = max(max(d0, -d1), 0), most = max(abs(d0), abs(d1));
+    const float top = r.slope * (float)(r.pos - r.zero - (r.slope > 0.f ? near : most));  // the tile's largest bias
+    const float span = fabsf(r.slope) * (float)(kKeys - 1);
+    // (rows that see no later tokens than their own: such are masked; from kFar on, an exact logit less a rounded reference may be
+    // far from zero for the largest, see soften, and so it is below -kFar, where the reference is of a piece of far tiles alone)
+    line = !__any_sync(kFull, b >= kFar || fabsf(top) + span >= kFar || (d1 > 0 && r.hi > r.pos + 1));
+    b += top;
   }
   ScoreForm form = line ? kLine : kBias;
   if (cap && slopes)
