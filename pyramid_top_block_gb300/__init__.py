@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 import struct
 from dataclasses import dataclass
@@ -768,7 +769,7 @@ def cache_attention(q: torch.Tensor, cache: PagedCache, lengths: torch.Tensor, i
         workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
     if cap != 0 or slopes is not None or window != 0:
         _check(lib.pisa_cache_attention_scored(cache._ref, qs, T, Hq, _per_sequence(lengths, "lengths", cache), ip, Ksel,
-                                               cap, _slopes(slopes, Hq, cache), _window(window), out.data_ptr(),
+                                               _cap(cap), _slopes(slopes, Hq, cache), _window(window), out.data_ptr(),
                                                1 if out.dtype is torch.float32 else 0,
                                                _cache_ws(workspace, cache, need), need, _current(cache)),
                "pisa_cache_attention_scored")
@@ -787,6 +788,11 @@ def _slopes(slopes: torch.Tensor | None, Hq: int, cache: PagedCache):
             or not slopes.is_contiguous()):
         raise ValueError(f"slopes must be a contiguous fp32 tensor [{Hq}] on the cache's device")
     return slopes.data_ptr()
+
+
+def _cap(cap: float) -> float:
+    """One below the floats' range as the least of them, which the library refuses, and not as none."""
+    return cap if cap == 0 or not abs(cap) < 2.0 ** -149 else math.copysign(2.0 ** -149, cap)
 
 
 def _window(window: int) -> int:
@@ -835,7 +841,7 @@ def cache_prompt_attention(q: torch.Tensor, cache: PagedCache, start: torch.Tens
         workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
     _check(lib.pisa_cache_prompt_attention(
         cache._ref, qs, T, Hq, _per_sequence(start, "start", cache),
-        None if counts is None else _per_sequence(counts, "counts", cache), *spans, cap, _slopes(slopes, Hq, cache),
+        None if counts is None else _per_sequence(counts, "counts", cache), *spans, _cap(cap), _slopes(slopes, Hq, cache),
         _window(window), out.data_ptr(), _cache_ws(workspace, cache, need), need, _current(cache)),
         "pisa_cache_prompt_attention")
     return out
