@@ -768,9 +768,9 @@ def cache_attention(q: torch.Tensor, cache: PagedCache, lengths: torch.Tensor, i
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
     if cap != 0 or slopes is not None or window != 0:
-        _check(lib.pisa_cache_attention_scored(cache._ref, qs, T, Hq, _per_sequence(lengths, "lengths", cache), ip, Ksel,
-                                               _cap(cap), _slopes(slopes, Hq, cache), _window(window), out.data_ptr(),
-                                               1 if out.dtype is torch.float32 else 0,
+        _check(lib.pisa_cache_attention_scored(cache._ref, qs, T, Hq, _per_sequence(lengths, "lengths", cache), ip,
+                                               Ksel, _cap(cap), _slopes(slopes, Hq, cache), _window(window),
+                                               out.data_ptr(), 1 if out.dtype is torch.float32 else 0,
                                                _cache_ws(workspace, cache, need), need, _current(cache)),
                "pisa_cache_attention_scored")
         return out
@@ -841,8 +841,9 @@ def cache_prompt_attention(q: torch.Tensor, cache: PagedCache, start: torch.Tens
         workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
     _check(lib.pisa_cache_prompt_attention(
         cache._ref, qs, T, Hq, _per_sequence(start, "start", cache),
-        None if counts is None else _per_sequence(counts, "counts", cache), *spans, _cap(cap), _slopes(slopes, Hq, cache),
-        _window(window), out.data_ptr(), _cache_ws(workspace, cache, need), need, _current(cache)),
+        None if counts is None else _per_sequence(counts, "counts", cache), *spans, _cap(cap),
+        _slopes(slopes, Hq, cache), _window(window), out.data_ptr(), _cache_ws(workspace, cache, need), need,
+        _current(cache)),
         "pisa_cache_prompt_attention")
     return out
 
@@ -905,7 +906,8 @@ class PagePool:
         """n_pages free pages of `layers` layers each, and an empty table for B sequences of up to n_cap tokens."""
         if (page_size not in (16, 32, 64, 128, 256) or bits not in (4, 16)
                 or min(B, n_cap, Hkv, n_pages, layers) < 1):
-            raise ValueError("page_size 16, 32, 64, 128 or 256, bits 4 or 16, B, n_cap, Hkv, n_pages and layers at least 1")
+            raise ValueError("page_size 16, 32, 64, 128 or 256, bits 4 or 16, B, n_cap, Hkv, n_pages and layers at "
+                             "least 1")
         U = min(page_size, 64)
         shape = (n_pages, layers, Hkv, page_size // U) + ((2, U, D) if bits == 16 else (72 * U,))
         pages = torch.zeros(shape, dtype=torch.bfloat16 if bits == 16 else torch.uint8, device=device)
@@ -948,8 +950,8 @@ def cache_reserve(pool: PagePool, lengths: torch.Tensor, T: int, counts: torch.T
     """Pages for the next counts[b] (0 to T; None: T) tokens of every sequence, its own alone: missing ones are taken
     from the free pages, lowest number first, and shared ones are replaced, the one that holds tokens before lengths[b]
     being copied (for each of its sharers).  Returns granted int32 [B]: counts[b], or 0 where the pages did not suffice
-    (that sequence and those after it that need any stay as they are); it is what cache_append takes as counts, and may be
-    given as counts itself.  workspace of pool_workspace."""
+    (that sequence and those after it that need any stay as they are); it is what cache_append takes as counts, and may
+    be given as counts itself.  workspace of pool_workspace."""
     guard = _on(pool, stream)
     if guard is not None:
         with guard:

@@ -74,7 +74,8 @@ int check_score(float cap, const float* slopes, int window, ScoreDev& d) {
 // Checks a pool descriptor.
 int check_pool(const pisa_page_pool* c, PoolDev& d) {
   if (!c || !c->pages || !c->table || !c->refs) return PISA_ERR_INVALID_ARG;
-  if (c->B < 1 || c->n_pages < 1 || c->max_pages < 1 || c->page_size < 1 || c->page_bytes < 1) return PISA_ERR_INVALID_ARG;
+  if (c->B < 1 || c->n_pages < 1 || c->max_pages < 1 || c->page_size < 1 || c->page_bytes < 1)
+    return PISA_ERR_INVALID_ARG;
   if (!aligned(c->pages, 16) || !aligned(c->table, 4) || !aligned(c->refs, 4)) return PISA_ERR_INVALID_ARG;
   if (c->page_bytes % 16 || c->page_stride % 16 || c->page_stride < c->page_bytes) return PISA_ERR_INVALID_ARG;
   if (c->page_stride > (INT64_MAX >> 1) / c->n_pages) return PISA_ERR_INVALID_ARG;
@@ -297,7 +298,8 @@ int pisa_cache_fork(const pisa_page_pool* pool, const int32_t* parents, int32_t*
   PoolForkLaunch L{};
   const int st = check_pool(pool, L.pool);
   if (st) return st;
-  if (!parents || !lengths || !aligned(parents, 4) || !aligned(lengths, 4) || !aligned(ws, 4)) return PISA_ERR_INVALID_ARG;
+  if (!parents || !lengths || !aligned(parents, 4) || !aligned(lengths, 4) || !aligned(ws, 4))
+    return PISA_ERR_INVALID_ARG;
   if (pool->B > kForkMaxB) return PISA_ERR_UNSUPPORTED;
   if (overlap(parents, pool->B, lengths, pool->B) || in_pool(L.pool, lengths, pool->B)) return PISA_ERR_INVALID_ARG;
   L.parents = parents;
@@ -312,9 +314,12 @@ int pisa_cache_reserve(const pisa_page_pool* pool, const int32_t* lengths, int T
   const int st = check_pool(pool, L.pool);
   if (st) return st;
   if (!lengths || T < 1 || !granted || !ws) return PISA_ERR_INVALID_ARG;
-  if (!aligned(lengths, 4) || !aligned(counts, 4) || !aligned(granted, 4) || !aligned(ws, 256)) return PISA_ERR_INVALID_ARG;
-  // (lengths and counts are read again when some grants are written; a grant in its count's place is that count, or is not read again)
-  if (overlap(granted, pool->B, lengths, pool->B) || (granted != counts && overlap(granted, pool->B, counts, pool->B)) ||
+  if (!aligned(lengths, 4) || !aligned(counts, 4) || !aligned(granted, 4) || !aligned(ws, 256))
+    return PISA_ERR_INVALID_ARG;
+  // (lengths and counts are read again when some grants are written; a grant in its count's place is that count, or is
+  // not read again)
+  if (overlap(granted, pool->B, lengths, pool->B) ||
+      (granted != counts && overlap(granted, pool->B, counts, pool->B)) ||
       in_pool(L.pool, granted, pool->B))
     return PISA_ERR_INVALID_ARG;
   if (ws_bytes < pisa_pool_workspace_bytes(pool->n_pages, pool->B)) return PISA_ERR_WORKSPACE_TOO_SMALL;

@@ -173,12 +173,12 @@ struct AxisRows {
   bool one;  // all axes agree, as in text
 };
 
-// The angles of pairs i .. i + N - 1, each from its own axis's row: every lane of the warp loads those of the pair of its
-// number, and the lanes take them from one another (each its own pairs' by word loads took 59.6 instead of
+// The angles of pairs i .. i + N - 1, each from its own axis's row: every lane of the warp loads those of the pair of
+// its number, and the lanes take them from one another (each its own pairs' by word loads took 59.6 instead of
 // 58.7 us for 32768 tokens).
 template <int N>
-__device__ __forceinline__ void load_axes(const CacheAppendLaunch& a, const AxisRows& rows, int lane, int i, float (&u)[N],
-                                          float (&v)[N]) {
+__device__ __forceinline__ void load_axes(const CacheAppendLaunch& a, const AxisRows& rows, int lane, int i,
+                                          float (&u)[N], float (&v)[N]) {
   float c = 0.f, s = 0.f;
   if (lane < a.rot >> 1) {
     const unsigned axis = (unsigned)(a.axis_of >> (2 * lane)) & 3u;

@@ -32,8 +32,9 @@
 
 namespace pisa {
 
-// What is done to the scores: a kernel for each, as what the others need would take registers and instructions from it (window
-// alone, 16 x 131072 tokens in 4 bits, 73.2 instead of 78.3 us; three queries over 8 x 131072 in bf16 71.1 instead of 82.6).
+// What is done to the scores: a kernel for each, as what the others need would take registers and instructions from it
+// (window alone, 16 x 131072 tokens in 4 bits, 73.2 instead of 78.3 us; three queries over 8 x 131072 in bf16 71.1
+// instead of 82.6).
 enum ScoreMode {
   kPlain,   // nothing, and no window
   kWindow,  // a window (or none, as below)
@@ -248,8 +249,8 @@ __device__ __forceinline__ void make_q(const CacheAttendLaunch& a, const QueryWo
       t = max(t & 0xffffu, t >> 16);
       t = max(t, __shfl_xor_sync(kFull, t, 1));
       t = max(t, __shfl_xor_sync(kFull, t, 2));
-      // the largest lies in [2^e, 2^(e + 1)) (scored: rows below 2^-60 have products of zero, so that a bias fits 32 bits
-      // over the factor)
+      // the largest lies in [2^e, 2^(e + 1)) (scored: rows below 2^-60 have products of zero, so that a bias fits 32
+      // bits over the factor)
       const int e = max(min((int)(t >> 7) - 127, 126), MODE != kPlain ? -60 : -100);
       const float down = exp2i(-e);
       f[h] = fminf(f[h] * exp2i(e) * exp2i(a.cache.k_exp), 0x1.fffffep127f);
@@ -306,8 +307,8 @@ __device__ __forceinline__ void make_q(const CacheAttendLaunch& a, const QueryWo
     s.f0 = s.f1 = 1.f;
   }
   if constexpr (MODE == kBias) {
-    // (cut at 2^99 of the products' units, for the same reason as a slope is: 4-bit pages' products, below 2^19, do not make up for
-    // a token's distance then, and with bf16 pages it is the slope's own cut)
+    // (cut at 2^99 of the products' units, for the same reason as a slope is: 4-bit pages' products, below 2^19, do not
+    // make up for a token's distance then, and with bf16 pages it is the slope's own cut)
     const float most0 = 0x1p99f * f[0], most1 = 0x1p99f * f[1];
     s.bias0 = fminf(fmaxf(s.bias0, -most0), most0) / f[0];
     s.bias1 = fminf(fmaxf(s.bias1, -most1), most1) / f[1];
@@ -420,7 +421,8 @@ __device__ __forceinline__ void products(uint32_t st_k, uint32_t st_v, int first
         const unsigned long long b0 = f2_pack(s.bias0, s.bias0), b1 = f2_pack(s.bias1, s.bias1);
         const float x0 = s.bias0 * (float)(first + s.from0), x1 = s.bias1 * (float)(first + s.from1);
         const unsigned long long y0 = f2_pack(x0, x0), y1 = f2_pack(x1, x1);
-        const unsigned long long k0 = f2_pack(16.f * i, 16.f * i + kNext), k1 = f2_pack(16.f * i + 8, 16.f * i + 8 + kNext);
+        const unsigned long long k0 = f2_pack(16.f * i, 16.f * i + kNext);
+        const unsigned long long k1 = f2_pack(16.f * i + 8, 16.f * i + 8 + kNext);
         f2_unpack(f2_fma(b0, k0, y0), d0[0], d0[1]);
         f2_unpack(f2_fma(b1, k0, y1), d0[2], d0[3]);
         f2_unpack(f2_fma(b0, k1, y0), d1[0], d1[1]);
@@ -643,7 +645,8 @@ __device__ __forceinline__ void weigh(const CacheAttendLaunch& a, uint32_t st, i
     // one by one to the rows that see them, and cleared like the rest.
     const int k_lo = min(max(see.n_lo - first, 0), KT), k_hi = min(max(see.n_hi - first, 0), KT);
     // (the same for the tokens between the rows' first ones)
-    const int z_lo = MODE != kPlain ? min(max(see.l_lo - first, 0), KT) : 0, z_hi = MODE != kPlain ? min(max(see.l_hi - first, 0), KT) : 0;
+    const int z_lo = MODE != kPlain ? min(max(see.l_lo - first, 0), KT) : 0;
+    const int z_hi = MODE != kPlain ? min(max(see.l_hi - first, 0), KT) : 0;
     const auto one_by_one = [&](int from, int to) {  // at most 16 keys
 #pragma unroll
       for (int nt = 0; nt < KT / 8; ++nt)
@@ -674,8 +677,9 @@ __device__ __forceinline__ void weigh(const CacheAttendLaunch& a, uint32_t st, i
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            if (first + key < see.n0 && (MODE == kPlain || first + key >= see.l0)) s.o[i][e] = fmaf(p0, v[e], s.o[i][e]);
-            if (first + key < see.n1 && (MODE == kPlain || first + key >= see.l1)) s.o[i][2 + e] = fmaf(p1, v[e], s.o[i][2 + e]);
+            const int at = first + key;
+            if (at < see.n0 && (MODE == kPlain || at >= see.l0)) s.o[i][e] = fmaf(p0, v[e], s.o[i][e]);
+            if (at < see.n1 && (MODE == kPlain || at >= see.l1)) s.o[i][2 + e] = fmaf(p1, v[e], s.o[i][2 + e]);
           }
         }
       }
@@ -770,7 +774,8 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
     if constexpr (MODE == kBias || MODE == kCapped) {
       const int near = max(some[0] >> lane & 1 ? blk[0] * kC + kC : 0, some[1] >> lane & 1 ? blk[1] * kC + kC : 0);
       farther = max(see.n_hi - __reduce_max_sync(kFull, near), 0);
-      begin = __reduce_min_sync(kFull, min(some[0] >> lane & 1 ? blk[0] * kC : INT_MAX, some[1] >> lane & 1 ? blk[1] * kC : INT_MAX));
+      const int far = min(some[0] >> lane & 1 ? blk[0] * kC : INT_MAX, some[1] >> lane & 1 ? blk[1] * kC : INT_MAX);
+      begin = __reduce_min_sync(kFull, far);
     }
   } else {
     i1 = min(i1, (max(see.n_hi, 0) + KT - 1) / KT);
@@ -851,8 +856,8 @@ __device__ __forceinline__ void run_tiles(const CacheAttendLaunch& a, const Unit
   cpa_commit();
   make_q<KIND, MODE>(a, q, u, lane, s);
   if constexpr (MODE == kBias || MODE == kCapped) {
-    // The bias is taken relative to the largest one in sight, the nearest token's or with a negative slope the farthest one's: others'
-    // would drown the scores in 32 bits.
+    // The bias is taken relative to the largest one in sight, the nearest token's or with a negative slope the farthest
+    // one's: others' would drown the scores in 32 bits.
     s.from0 += s.bias0 < 0.f ? see.n0 - 1 - max(see.l0, begin) : farther;
     s.from1 += s.bias1 < 0.f ? see.n1 - 1 - max(see.l1, begin) : farther;
   }
@@ -989,7 +994,7 @@ __device__ __forceinline__ int seq_len(const CacheAttendLaunch& a, int b, bool& 
 // its end (the warps' merge, the next unit's chain of loads; about 4 us), so that the runs that
 // change units take as long as the others.  Places at the end 0 / 12 / 24 / 36 / 48, us a call:
 //   4 bits  16 x 131072 73.5 / 72.1 / 71.5 / 71.6 / 71.9   64 x 9000 ragged, 8 heads 88.8 / 63.6 / 56.7 / 57.5 / 59.8
-//   bf16    8 x 131072 ragged 64.8 / 63.8 / 63.3 / 63.0 / 63.3   64 x 9000 ragged, 8 heads 119.7 / 103 / 96.3 / 96.5 / 97.4
+//   bf16    8 x 131072 ragged 64.8 / 63.8 / 63.3 / 63.0 / 63.3   64 x 9000 the same 119.7 / 103 / 96.3 / 96.5 / 97.4
 template <int KIND, int MODE>
 __device__ __forceinline__ int tiles_of_seq(const CacheAttendLaunch& a, int n) {
   return unit_tiles<Cfg<KIND>::KT, MODE != kPlain>(n, a.T, a.score.window);

@@ -12,11 +12,11 @@
 //   warps 10, 11    issue the matrix instructions: one S = Q K^T, the other O += P V
 // Tensor memory, for each row tile: S 128 columns, P 64, O 64; both together all 512.
 //
-// What bounds it: a step of 256 rows and 128 keys takes the tensor core 1552 clocks (the product with V has 64 columns, and takes
-// as long as with 128) and the exponentials 1024, and each row tile waits for its product, takes its scores into registers,
-// weighs them and hands the weights back: about 2000 clocks.  32 heads on 2, bf16 (4-bit) pages: 32768 tokens 3.51 ms =
-// 1.25 PFLOP/s (3.81 ms), 2048 at 131072 1.68 ms = 1.30 PFLOP/s (1.82), 1216 at 16384 132 us (142), capped 171 to 179, with
-// slopes 162; a library's bf16 product of matrices reaches 1.90 PFLOP/s.
+// What bounds it: a step of 256 rows and 128 keys takes the tensor core 1552 clocks (the product with V has 64 columns,
+// and takes as long as with 128) and the exponentials 1024, and each row tile waits for its product, takes its scores
+// into registers, weighs them and hands the weights back: about 2000 clocks.  32 heads on 2, bf16 (4-bit) pages: 32768
+// tokens 3.51 ms = 1.25 PFLOP/s (3.81 ms), 2048 at 131072 1.68 ms = 1.30 PFLOP/s (1.82), 1216 at 16384 132 us (142),
+// capped 171 to 179, with slopes 162; a library's bf16 product of matrices reaches 1.90 PFLOP/s.
 #include "cache_prompt.cuh"
 
 #include <climits>
@@ -27,13 +27,14 @@
 
 namespace pisa {
 
-// Where there are few row tiles of a CTA (units) for their length, the key tiles of all units form one stream that is cut into
-// runs of equal length, one for each SM, and where a unit ends: a CTA takes a piece, the longest first.  Units in
-// several pieces leave partial results, which a last kernel joins (takes_stream says when).  (A CTA for a run, with a loop
-// over its pieces, was slower: the loop costs the softmax the registers that hold its scores, 138 -> 233 us for 1216
-// tokens at 16384.)
+// Where there are few row tiles of a CTA (units) for their length, the key tiles of all units form one stream that is
+// cut into runs of equal length, one for each SM, and where a unit ends: a CTA takes a piece, the longest first.  Units
+// in several pieces leave partial results, which a last kernel joins (takes_stream says when).  (A CTA for a run, with
+// a loop over its pieces, was slower: the loop costs the softmax the registers that hold its scores, 138 -> 233 us for
+// 1216 tokens at 16384.)
 constexpr int kRuns = kPromptRuns, kMaxUnits = kPromptUnits;
-constexpr int kUnitEnd = 4;            // places of the stream that a unit counts beside its tiles: what its begin and end cost
+// places of the stream that a unit counts beside its tiles: what its begin and end cost
+constexpr int kUnitEnd = 4;
 constexpr int kMinRun = 4;             // places that a run has at least
 constexpr int kPartRow = 66;           // a partial result, for each of 256 rows: O [64], reference, sum of weights
 constexpr int kRowsTile = 128, kRowsCta = 256, kKeys = 128;
@@ -56,7 +57,8 @@ struct PCfg {
       1024 + (2 + 2 * kStages) * kTileBytes + (KIND == PISA_CACHE_BF16 ? 0 : 2 * kLoadWarps * kRawBytes);
   static constexpr uint32_t kType = KIND == PISA_CACHE_BF16 ? 1u : 0u;
   // fp32 accumulator, A and B of the type; the second has B with its columns (dims) contiguous
-  static constexpr uint32_t kIdescS = (1u << 4) | (kType << 7) | (kType << 10) | ((kKeys >> 3) << 17) | ((kRowsTile >> 4) << 24);
+  static constexpr uint32_t kIdescS =
+      (1u << 4) | (kType << 7) | (kType << 10) | ((kKeys >> 3) << 17) | ((kRowsTile >> 4) << 24);
   static constexpr uint32_t kIdescO =
       (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) | ((kD >> 3) << 17) | ((kRowsTile >> 4) << 24);
 };
@@ -103,11 +105,13 @@ __device__ __forceinline__ bool mixed_tile(const PromptShared& sh, int tile) {
 
 // ------------------------------------------------------------------------------------------------ loading
 
-// A loading warp takes every second tile, whole.  The pages of its tiles' records, four tiles ahead: lane l has record l % 8
-// (of 8, 4 or 2) of the tile number first + 2 (l / 8).  n_pages: no row sees any of it, or its page is out of range (noted); its
-// keys and values become zeros.
-__device__ __forceinline__ int look(const CachePromptLaunch& a, const PromptUnit& u, PromptShared& sh, int lane, int first) {
-  const int tile = u.tile(first + kLoadWarps * (lane >> 3)), U = 1 << a.cache.rec_shift, key = tile * kKeys + U * (lane & 7);
+// A loading warp takes every second tile, whole.  The pages of its tiles' records, four tiles ahead: lane l has record
+// l % 8 (of 8, 4 or 2) of the tile number first + 2 (l / 8).  n_pages: no row sees any of it, or its page is out of
+// range (noted); its keys and values become zeros.
+__device__ __forceinline__ int look(const CachePromptLaunch& a, const PromptUnit& u, PromptShared& sh, int lane,
+                                    int first) {
+  const int tile = u.tile(first + kLoadWarps * (lane >> 3)), U = 1 << a.cache.rec_shift;
+  const int key = tile * kKeys + U * (lane & 7);
   if (U * (lane & 7) >= kKeys || tile < u.i0 || key >= sh.hi_max || key + U <= sh.lo_min) return a.cache.n_pages;
   const int page = a.cache.table[(long long)u.b * a.cache.max_pages + (key >> a.cache.page_shift)];
   if (page >= 0 && page < a.cache.n_pages) return page;
@@ -115,8 +119,8 @@ __device__ __forceinline__ int look(const CachePromptLaunch& a, const PromptUnit
   return a.cache.n_pages;
 }
 
-// A bf16 tile's values: those that are not finite become zeros, since 0 times them is not zero; the rows that do see them
-// get them at the end (odd_values).
+// A bf16 tile's values: those that are not finite become zeros, since 0 times them is not zero; the rows that do see
+// them get them at the end (odd_values).
 __device__ __forceinline__ void scrub(PromptShared& sh, unsigned char* v, int tile, int lane) {
   const int sub = lane >> 3, ch = lane & 7;
   const auto at = [&](int j) {
@@ -156,7 +160,8 @@ __device__ __forceinline__ void dequant16(uint32_t c0, uint32_t c1, uint32_t sca
 }
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(smem_u32(dst)),
                "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
@@ -176,7 +181,8 @@ __device__ __forceinline__ bool load_bf16(const CachePromptLaunch& a, const CUte
     if (!__all_sync(kFull, ok)) return false;
     unsigned char* stage = stages + st * 2 * kTileBytes;
     const bool mixed = mixed_tile(sh, tile);
-    // lane 2 i + h: the keys (h = 0) or values of record i; a page number of n_pages lies outside the map and gives zeros
+    // lane 2 i + h: the keys (h = 0) or values of record i; a page number of n_pages lies outside the map and gives
+    // zeros
     uint64_t* bar = mixed ? &sh.landed[warp][0] : &sh.full[st];
     if (lane == 0) mbar_expect_tx(bar, 2 * kTileBytes);
     __syncwarp();
@@ -203,8 +209,8 @@ __device__ __forceinline__ bool load_bf16(const CachePromptLaunch& a, const CUte
   return true;
 }
 
-// 4-bit pages: records by bulk copies into one of the warp's two raw buffers, a tile ahead; from there as fp16 into the stage,
-// a token a lane.
+// 4-bit pages: records by bulk copies into one of the warp's two raw buffers, a tile ahead; from there as fp16 into the
+// stage, a token a lane.
 __device__ __forceinline__ bool load_e2m1(const CachePromptLaunch& a, const PromptUnit& u, PromptShared& sh,
                                           unsigned char* stages, unsigned char* raw, int warp, int lane) {
   constexpr unsigned kPStages = PCfg<PISA_CACHE_E2M1>::kStages;
@@ -223,7 +229,8 @@ __device__ __forceinline__ bool load_e2m1(const CachePromptLaunch& a, const Prom
     __syncwarp();
     if (there)
       bulk_load(raw + (x & 1) * kRawBytes + lane * rec_bytes,
-                a.cache.pages + cache_record(a.cache, kRowE2m1, from, u.kv, tile * kKeys + (lane << rs)), rec_bytes, bar);
+                a.cache.pages + cache_record(a.cache, kRowE2m1, from, u.kv, tile * kKeys + (lane << rs)), rec_bytes,
+                bar);
     if (lane == 0) sh.asked[warp].count = x + 1;
   };
   int x = 0;
@@ -243,7 +250,8 @@ __device__ __forceinline__ bool load_e2m1(const CachePromptLaunch& a, const Prom
       const int row = 32 * j + lane, rec = row >> rs, in = row & (U - 1);
       const bool there = __shfl_sync(kFull, page, ((x % 4) * 8 + rec) & 31) < a.cache.n_pages;
       const unsigned char* r = raw + (x & 1) * kRawBytes + rec * rec_bytes;
-      const uint4 c[2][2] = {{reinterpret_cast<const uint4*>(r + in * 32)[0], reinterpret_cast<const uint4*>(r + in * 32)[1]},
+      const uint4 c[2][2] = {{reinterpret_cast<const uint4*>(r + in * 32)[0],
+                              reinterpret_cast<const uint4*>(r + in * 32)[1]},
                              {reinterpret_cast<const uint4*>(r + 36 * U + in * 32)[0],
                               reinterpret_cast<const uint4*>(r + 36 * U + in * 32)[1]}};
       // (a scale of zero makes zeros of whatever the codes are)
@@ -338,8 +346,9 @@ struct PromptRow {
   CapRow cap;
   float slope;      // bias by distance, base 2
   int pos;          // the row's position
-  int zero;         // biases are relative to the one of this token, as far before the position as the token in sight that is
-                    // nearest to it, or with a negative slope farthest from it: the row's largest one
+  // Biases are relative to the one of this token, as far before the position as the token in sight that is nearest to
+  // it, or with a negative slope farthest from it: the row's largest one.
+  int zero;
 };
 
 __device__ __forceinline__ float max3f(float a, float b, float c) {
@@ -348,8 +357,8 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
   return d;
 }
 
-// A new reference for the warp's rows, given each row's largest logit b: O and the sums of weights follow.  Returns false
-// if the wait for the product before, which writes O, ran out.
+// A new reference for the warp's rows, given each row's largest logit b: O and the sums of weights follow.  Returns
+// false if the wait for the product before, which writes O, ran out.
 template <int KIND>
 __device__ __forceinline__ bool refer(PromptShared& sh, PromptRow& r, uint32_t s, int X, unsigned k, float b) {
   // (a step of 32 bits is too coarse for the shift from 2^24 on; nothing that it is for is left there)
@@ -377,11 +386,11 @@ __device__ __forceinline__ uint32_t pack_weights(float x, float y) {
   return KIND == PISA_CACHE_BF16 ? pack_bf16x2(x, y) : pack_f16x2(x, y);
 }
 
-// The softmax of one key tile, the k-th, for the warp's 32 rows, plain scores.  s: the tensor memory columns of the row tile
-// at the warp's lanes.
+// The softmax of one key tile, the k-th, for the warp's 32 rows, plain scores.  s: the tensor memory columns of the row
+// tile at the warp's lanes.
 template <int KIND>
-__device__ __forceinline__ bool soften(PromptShared& sh, PromptRow& r, uint32_t s, int X, int lane, int tile, unsigned k,
-                                       bool& two_step) {
+__device__ __forceinline__ bool soften(PromptShared& sh, PromptRow& r, uint32_t s, int X, int lane, int tile,
+                                       unsigned k, bool& two_step) {
   const int key0 = tile * kKeys;
   // (rows that see nothing do not matter: they get zeros at the end, or do not exist)
   const bool whole = __all_sync(kFull, r.lo >= r.hi || (r.lo <= key0 && r.hi >= key0 + kKeys));
@@ -457,15 +466,18 @@ __device__ __forceinline__ bool soften(PromptShared& sh, PromptRow& r, uint32_t 
   return true;
 }
 
-// The same for scores that are not plain products.  What bounds it is the arithmetic units: two packed operations take four
-// clocks a scheduler, so that a cap's short polynomial (5 a pair) and the sums take 1536 for the two warps' rows, next to
-// 1024 of the exponentials.  So both stand in one block, where one unit works beside the other (apart: 240 instead of
-// 208 us for 1216 tokens at 16384), and the row's factors are in the polynomial's coefficients (7 a pair: 231).
-// The usual tile (whole, within the short polynomial or a line, no new reference) comes from the registers that its maximum
-// came with (read once more: 208 instead of 182 us, with slopes 173 instead of 161).  The rest is a loop over 64 columns, which
-// reads S again: the longer forms unrolled over all 128 do not fit the instruction cache.  (A shorter polynomial up to
-// a quarter of the cap: 168 instead of 177 us where it is enough, 321 instead of 269 where all forms take turns.)
-enum PromptMode {  // a kernel for each: with all forms in one the usual ones have fewer registers (231 instead of 211 us)
+// The same for scores that are not plain products.  What bounds it is the arithmetic units: two packed operations take
+// four clocks a scheduler, so that a cap's short polynomial (5 a pair) and the sums take 1536 for the two warps' rows,
+// next to 1024 of the exponentials.  So both stand in one block, where one unit works beside the other (apart: 240
+// instead of 208 us for 1216 tokens at 16384), and the row's factors are in the polynomial's coefficients (7 a pair:
+// 231).
+// The usual tile (whole, within the short polynomial or a line, no new reference) comes from the registers that
+// its maximum came with (read once more: 208 instead of 182 us, with slopes 173 instead of 161).  The rest is a loop
+// over 64 columns, which reads S again: the longer forms unrolled over all 128 do not fit the instruction cache.  (A
+// shorter polynomial up to a quarter of the cap: 168 instead of 177 us where it is enough, 321 instead of 269 where all
+// forms take turns.)
+// a kernel for each: with all forms in one the usual ones have fewer registers (231 instead of 211 us)
+enum PromptMode {
   kPromptPlain,
   kPromptCapped,  // a cap of kCapExp or less
   kPromptBias,
@@ -486,7 +498,8 @@ enum ScoreForm {
 // Products of a row, of the keys from key0 on, as logits less a reference (m2: minus the reference, twice).
 template <ScoreForm FORM>
 struct Logits {
-  static constexpr bool kAny = FORM == kCapAny || FORM == kCapAnyBias, kFarther = FORM == kCapFar || FORM == kCapFarBias || kAny;
+  static constexpr bool kAny = FORM == kCapAny || FORM == kCapAnyBias;
+  static constexpr bool kFarther = FORM == kCapFar || FORM == kCapFarBias || kAny;
   static constexpr bool kAway = FORM == kCapFarBias || FORM == kCapAnyBias || FORM == kBias;
   static constexpr bool kHalf = FORM == kCapHalf || FORM == kCapLine, kStraight = FORM == kLine || FORM == kCapLine;
   static constexpr int n = kHalf ? TanhHalf::n : FORM == kCapWhole || kAny ? Tanh::n : 1;
@@ -520,8 +533,8 @@ struct Logits {
       c = f2_add(m2, f2_pack(bias, bias));
     }
     if constexpr (kAway) {
-      // -slope (|j - p| - (p - zero)): whole numbers, exact up to 2^24.  Both distances less what all keys of the tile have of the
-      // second, so that they are small where their difference is.
+      // -slope (|j - p| - (p - zero)): whole numbers, exact up to 2^24.  Both distances less what all keys of the tile
+      // have of the second, so that they are small where their difference is.
       const int d = key0 - r.pos, away = r.pos - r.zero, both = min(max(max(d, 1 - kKeys - d), 0), away);
       slope = -r.slope;
       d0 = (float)(d < 0 ? d + both : d - both);
@@ -593,8 +606,8 @@ __device__ __forceinline__ void with_form(ScoreForm form, const Use& use) {
 
 // 64 of them, masked.
 template <PromptMode MODE>
-__device__ __forceinline__ void logits64(const CachePromptLaunch& a, const PromptRow& r, ScoreForm form, bool whole, int key0,
-                                         unsigned long long m2, float (&v)[64]) {
+__device__ __forceinline__ void logits64(const CachePromptLaunch& a, const PromptRow& r, ScoreForm form, bool whole,
+                                         int key0, unsigned long long m2, float (&v)[64]) {
   with_form<MODE>(form, [&](auto f) {
     const Logits<f()> logits(a, r, key0, m2);
 #pragma unroll
@@ -626,8 +639,8 @@ struct Weights {
 };
 
 template <int KIND, PromptMode MODE>
-__device__ __forceinline__ bool soften_scored(const CachePromptLaunch& a, PromptShared& sh, PromptRow& r, uint32_t s, int X,
-                                              int lane, int tile, unsigned k) {
+__device__ __forceinline__ bool soften_scored(const CachePromptLaunch& a, PromptShared& sh, PromptRow& r, uint32_t s,
+                                              int X, int lane, int tile, unsigned k) {
   const int key0 = tile * kKeys;
   const bool whole = __all_sync(kFull, r.lo >= r.hi || (r.lo <= key0 && r.hi >= key0 + kKeys));
   constexpr bool cap = MODE != kPromptBias;
@@ -646,8 +659,9 @@ __device__ __forceinline__ bool soften_scored(const CachePromptLaunch& a, Prompt
     const int d0 = key0 - r.pos, d1 = d0 + kKeys - 1, near = max(max(d0, -d1), 0), most = max(abs(d0), abs(d1));
     const float top = r.slope * (float)(r.pos - r.zero - (r.slope > 0.f ? near : most));  // the tile's largest bias
     const float span = fabsf(r.slope) * (float)(kKeys - 1);
-    // (rows that see no later tokens than their own: such are masked; from kFar on, an exact logit less a rounded reference may be
-    // far from zero for the largest, see soften, and so it is below -kFar, where the reference is of a piece of far tiles alone)
+    // (rows that see no later tokens than their own: such are masked; from kFar on, an exact logit less a rounded
+    // reference may be far from zero for the largest, see soften, and so it is below -kFar, where the reference is of a
+    // piece of far tiles alone)
     line = !__any_sync(kFull, b >= kFar || fabsf(top) + span >= kFar || (d1 > 0 && r.hi > r.pos + 1));
     b += top;
   }
@@ -688,7 +702,8 @@ __device__ __forceinline__ bool soften_scored(const CachePromptLaunch& a, Prompt
     }
     return true;
   };
-  using Usual = std::integral_constant<ScoreForm, MODE == kPromptBias ? kLine : MODE == kPromptCapped ? kCapHalf : kCapLine>;
+  constexpr ScoreForm kUsual = MODE == kPromptBias ? kLine : MODE == kPromptCapped ? kCapHalf : kCapLine;
+  using Usual = std::integral_constant<ScoreForm, kUsual>;
   if (whole && !over && form == Usual()) {
     if (!at_once(Usual())) return false;
   } else if (MODE == kPromptEither && whole && !over && form == kCapHalf) {
@@ -752,7 +767,8 @@ __device__ __forceinline__ void odd_values(const CachePromptLaunch& a, const Pro
       if (page < 0 || page >= a.cache.n_pages) continue;
       const int in = key & (U - 1);
       if (KIND == PISA_CACHE_BF16) {
-        const unsigned char* v = a.cache.pages + cache_record(a.cache, kRowBf16, page, u.kv, key) + U * 128 + in * 128 + 2 * d0;
+        const unsigned char* v = a.cache.pages + cache_record(a.cache, kRowBf16, page, u.kv, key) + U * 128 + in * 128;
+        v += 2 * d0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint4 x = reinterpret_cast<const uint4*>(v)[i];
@@ -764,7 +780,8 @@ __device__ __forceinline__ void odd_values(const CachePromptLaunch& a, const Pro
           }
         }
       } else {
-        const unsigned char* s = a.cache.pages + cache_record(a.cache, kRowE2m1, page, u.kv, key) + 68 * U + in * 4 + d0 / 16;
+        const unsigned char* s = a.cache.pages + cache_record(a.cache, kRowE2m1, page, u.kv, key) + 68 * U + in * 4;
+        s += d0 / 16;
 #pragma unroll
         for (int i = 0; i < 32; ++i)
           if ((s[i / 16] & 0x7f) == 0x7f) o[i] = __int_as_float(0x7fc00000);
@@ -784,8 +801,8 @@ __device__ __forceinline__ bool sees_bad(const CachePromptLaunch& a, const Promp
   return false;
 }
 
-__device__ __forceinline__ void write_row(const CachePromptLaunch& a, const PromptUnit& u, int t, int head, float l, int d0,
-                                          const float (&o)[32]) {
+__device__ __forceinline__ void write_row(const CachePromptLaunch& a, const PromptUnit& u, int t, int head, float l,
+                                          int d0, const float (&o)[32]) {
   const float f = l == 0.f ? 0.f : exp2i(a.cache.kind == PISA_CACHE_E2M1 ? a.cache.v_exp : 0) / l;
   uint4* dst = reinterpret_cast<uint4*>(a.out + (((long long)u.b * a.T + t) * a.Hq + head) * kD + d0);
 #pragma unroll
@@ -815,8 +832,8 @@ __device__ __forceinline__ void fetch_queries(const CachePromptLaunch& a, const 
   }
 }
 
-// .. as two swizzled operands.  4-bit pages: as fp16, the row scaled by a power of two so that its largest element lies in
-// [1, 2) (cache_attend.cuh, make_q).
+// .. as two swizzled operands.  4-bit pages: as fp16, the row scaled by a power of two so that its largest element lies
+// in [1, 2) (cache_attend.cuh, make_q).
 template <int KIND, PromptMode MODE>
 __device__ __forceinline__ void stage_queries(const CachePromptLaunch& a, PromptShared& sh, unsigned char* q,
                                               const uint4 (&x)[8]) {
@@ -857,7 +874,8 @@ __device__ __forceinline__ void set_unit(const CachePromptLaunch& a, int x, int 
 __device__ __forceinline__ int tiles_of(int lo, int hi) { return lo < hi ? (hi + kKeys - 1) / kKeys - lo / kKeys : 0; }
 
 // The stream form: key tiles of each unit, a warp a unit, where the spans are listed.
-__global__ void __launch_bounds__(256) cache_prompt_tiles_kernel(CachePromptLaunch a, int g_shift, int row_tiles, int units) {
+__global__ void __launch_bounds__(256) cache_prompt_tiles_kernel(CachePromptLaunch a, int g_shift, int row_tiles,
+                                                                 int units) {
   after_the_one_before();
   const int x = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (x >= units) return;
@@ -878,10 +896,11 @@ __global__ void __launch_bounds__(256) cache_prompt_tiles_kernel(CachePromptLaun
   if (lane == 0) a.plan.tiles[x] = tiles_of(lo, hi);
 }
 
-// The stream form's plan, by one CTA: the pieces in order of length, and for each run the unit that begins in it and goes
-// on.  Unit x has the places from place[x] on, its tiles and kUnitEnd more; run r those from r per on.  A piece
+// The stream form's plan, by one CTA: the pieces in order of length, and for each run the unit that begins in it and
+// goes on.  Unit x has the places from place[x] on, its tiles and kUnitEnd more; run r those from r per on.  A piece
 // begins where a unit or a run does.
-__global__ void __launch_bounds__(1024) cache_prompt_plan_kernel(CachePromptLaunch a, int g_shift, int row_tiles, int units) {
+__global__ void __launch_bounds__(1024) cache_prompt_plan_kernel(CachePromptLaunch a, int g_shift, int row_tiles,
+                                                                 int units) {
   constexpr int kBuckets = 256;
   __shared__ int place[kMaxUnits + 1], bucket[kBuckets], sums[32];
   after_the_one_before();
@@ -1107,8 +1126,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   __syncthreads();
   if (warp < kSoftWarps) {
     const bool sees = r.lo < r.hi;
-    const int lo_min = __reduce_min_sync(kFull, sees ? r.lo : INT_MAX), lo_max = __reduce_max_sync(kFull, sees ? r.lo : 0);
-    const int hi_min = __reduce_min_sync(kFull, sees ? r.hi : INT_MAX), hi_max = __reduce_max_sync(kFull, sees ? r.hi : 0);
+    const int lo_min = __reduce_min_sync(kFull, sees ? r.lo : INT_MAX);
+    const int lo_max = __reduce_max_sync(kFull, sees ? r.lo : 0);
+    const int hi_min = __reduce_min_sync(kFull, sees ? r.hi : INT_MAX);
+    const int hi_max = __reduce_max_sync(kFull, sees ? r.hi : 0);
     if (lane == 0) {
       atomicMin(&sh.lo_min, lo_min);
       atomicMax(&sh.lo_max, lo_max);
@@ -1132,8 +1153,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   }
   __syncthreads();
   bool ok = true;
-  // More registers for the softmax, whose scores spilled (1216 tokens at 16384 136 -> 132 us, 4 bits 151 -> 143): 8 x 32 x
-  // 200 + 4 x 32 x 96 of the 384 x 168 that the CTA has.
+  // More registers for the softmax, whose scores spilled (1216 tokens at 16384 136 -> 132 us, 4 bits 151 -> 143): 8 x
+  // 32 x 200 + 4 x 32 x 96 of the 384 x 168 that the CTA has.
   if (warp < kSoftWarps)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
   else
@@ -1206,7 +1227,8 @@ __global__ void __launch_bounds__(256) cache_prompt_join_kernel(CachePromptLaunc
     m = n;
     l = l * f + li * h;
 #pragma unroll
-    for (int d = 0; d < 16; ++d) o[d] = li == 0.f ? o[d] * f : o[d] * f + y[d] * h;  // (what a part without keys holds is nothing)
+    for (int d = 0; d < 16; ++d)  // (what a part without keys holds is nothing)
+      o[d] = li == 0.f ? o[d] * f : o[d] * f + y[d] * h;
   }
   sm[grp][row_in] = m;
   sl[grp][row_in] = l;
@@ -1229,7 +1251,8 @@ __global__ void __launch_bounds__(256) cache_prompt_join_kernel(CachePromptLaunc
     for (int d = 0; d < 16; ++d) o[d] += lx == 0.f ? 0.f : so[x][row_in][quad][d] * f;
   }
   const float f = l == 0.f ? 0.f : exp2i(a.cache.kind == PISA_CACHE_E2M1 ? a.cache.v_exp : 0) / l;
-  uint4* dst = reinterpret_cast<uint4*>(a.out + (((long long)u.b * a.T + t) * a.Hq + u.kv * a.G + (r & (a.G - 1))) * kD + 16 * quad);
+  const long long at = ((long long)u.b * a.T + t) * a.Hq + u.kv * a.G + (r & (a.G - 1));
+  uint4* dst = reinterpret_cast<uint4*>(a.out + at * kD + 16 * quad);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     uint32_t w[4];
@@ -1242,9 +1265,9 @@ __global__ void __launch_bounds__(256) cache_prompt_join_kernel(CachePromptLaunc
 
 size_t cache_prompt_part_bytes() { return kPromptPlanBytes + (size_t)kRuns * 2 * kRowsCta * kPartRow * 4; }
 
-// Whether the stream form takes a call: `units` row tiles that see up to `tiles` key tiles each.  A CTA for each unit takes as
-// long as its last wave; the stream's CTAs end together, but the plan, the pieces' begins and the join cost it about as
-// much as 16 tiles, and the lengths (known to the device alone) a tenth.
+// Whether the stream form takes a call: `units` row tiles that see up to `tiles` key tiles each.  A CTA for each unit
+// takes as long as its last wave; the stream's CTAs end together, but the plan, the pieces' begins and the join cost it
+// about as much as 16 tiles, and the lengths (known to the device alone) a tenth.
 inline bool takes_stream(long long units, long long tiles) {
   if (units > kMaxUnits) return false;
   const long long waves = (units + kRuns - 1) / kRuns;
@@ -1290,27 +1313,30 @@ static cudaError_t launch_prompt(const CachePromptLaunch& L, cudaStream_t s) {
   if (!L.last && keys > reach) keys = reach;
   constexpr int kSmem = PCfg<KIND>::kSmem;
   if (!takes_stream(units, keys / kKeys))
-    return launch_early<cache_prompt_kernel<KIND, MODE, false>>((unsigned)units, kPromptThreads, kSmem, s, map, L, g_shift,
-                                                                  row_tiles, units);
+    return launch_early<cache_prompt_kernel<KIND, MODE, false>>((unsigned)units, kPromptThreads, kSmem, s, map, L,
+                                                                g_shift, row_tiles, units);
   cudaError_t e = cudaSuccess;
   if (L.first || L.last)
     e = launch_early<cache_prompt_tiles_kernel>((unsigned)(units + 7) / 8, 256, 0, s, L, g_shift, row_tiles, units);
   if (e == cudaSuccess) e = launch_early<cache_prompt_plan_kernel>(1, 1024, 0, s, L, g_shift, row_tiles, units);
   if (e != cudaSuccess) return e;
-  e = launch_early<cache_prompt_kernel<KIND, MODE, true>>((unsigned)(units + kRuns), kPromptThreads, kSmem, s, map, L, g_shift, row_tiles, units);
+  e = launch_early<cache_prompt_kernel<KIND, MODE, true>>((unsigned)(units + kRuns), kPromptThreads, kSmem, s, map, L,
+                                                          g_shift, row_tiles, units);
   if (e != cudaSuccess) return e;
   return launch_early<cache_prompt_join_kernel>(kRuns * 16, 256, 0, s, L, g_shift, row_tiles);
 }
 
 template <int KIND>
 static cudaError_t launch_prompt_mode(const CachePromptLaunch& L, cudaStream_t s) {
-  if (L.score.cap <= 0.f) return L.score.slopes ? launch_prompt<KIND, kPromptBias>(L, s) : launch_prompt<KIND, kPromptPlain>(L, s);
+  if (L.score.cap <= 0.f)
+    return L.score.slopes ? launch_prompt<KIND, kPromptBias>(L, s) : launch_prompt<KIND, kPromptPlain>(L, s);
   if (L.score.slopes || L.score.cap > kCapExp) return launch_prompt<KIND, kPromptEither>(L, s);
   return launch_prompt<KIND, kPromptCapped>(L, s);
 }
 
 cudaError_t launch_cache_prompt(const CachePromptLaunch& L, cudaStream_t s) {
-  return L.cache.kind == PISA_CACHE_BF16 ? launch_prompt_mode<PISA_CACHE_BF16>(L, s) : launch_prompt_mode<PISA_CACHE_E2M1>(L, s);
+  return L.cache.kind == PISA_CACHE_BF16 ? launch_prompt_mode<PISA_CACHE_BF16>(L, s)
+                                         : launch_prompt_mode<PISA_CACHE_E2M1>(L, s);
 }
 
 }  // namespace pisa

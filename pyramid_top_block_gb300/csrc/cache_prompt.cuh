@@ -8,14 +8,16 @@ namespace pisa {
 constexpr int kPromptRuns = 152;               // CTAs of the stream form: one on each SM
 constexpr int kPromptUnits = 8 * kPromptRuns;  // row tiles that it takes at most
 
-// A piece of the stream: tiles k0 .. k1 - 1 of a unit (-1: none), and which partial result it leaves (-1: it is the whole unit).
+// A piece of the stream: tiles k0 .. k1 - 1 of a unit (-1: none), and which partial result it leaves (-1: it is the
+// whole unit).
 struct PromptPiece {
   int unit, k0, k1, slot;
 };
 // In the workspace.
 struct PromptPlan {
   PromptPiece* piece;  // [kPromptUnits + kPromptRuns]
-  int2* cut;           // [kPromptRuns] the unit that begins in a run and goes on (-1: none), and the last run that it lies in
+  // [kPromptRuns] the unit that begins in a run and goes on (-1: none), and the last run that it lies in
+  int2* cut;
   int32_t* tiles;      // [kPromptUnits]
 };
 constexpr size_t kPromptPlanBytes = (kPromptUnits + kPromptRuns) * sizeof(PromptPiece) + kPromptRuns * sizeof(int2) +
@@ -47,8 +49,8 @@ __device__ __forceinline__ Span span_of(const CachePromptLaunch& a, int b, int t
   const long long start = a.start[b], p = start + t, end = start + count;
   over = start < 0 || end > cap;
   Span s;
-  // (one past either end of the table as the end itself: that adds as much to the distance of all that it sees, and stays far
-  // from 32 bits' ends)
+  // (one past either end of the table as the end itself: that adds as much to the distance of all that it sees, and
+  // stays far from 32 bits' ends)
   s.pos = (int)(p < 0 ? 0 : p > cap ? cap : p);
   long long hi = a.last ? a.last[(long long)b * a.T + t] : p + 1, lo = a.first ? a.first[(long long)b * a.T + t] : 0;
   hi = hi < end ? hi : end;

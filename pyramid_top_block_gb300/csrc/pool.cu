@@ -5,8 +5,8 @@
 // entries by position), so that a call gives the same table however it is scheduled; atomics only count.
 //
 // What bounds it: copying pages (the memory, read and write: 356 MB moved in 54.4 us = 6.55 TB/s); planning is a few
-// dependent loads and barriers.  Fork 1.6 us (16 sequences of 64 pages) to 7.3 (64 of 8192), reserve 5.6 (1200 pages) to 10.6
-// (530000), planning a compaction 5.3 to 33.7.
+// dependent loads and barriers.  Fork 1.6 us (16 sequences of 64 pages) to 7.3 (64 of 8192), reserve 5.6 (1200 pages)
+// to 10.6 (530000), planning a compaction 5.3 to 33.7.
 #include <climits>
 
 #include <cooperative_groups.h>
@@ -17,8 +17,8 @@ namespace pisa {
 
 namespace cg = cooperative_groups;
 
-// One cluster plans: it can hand sums around without another launch.  For small pools it has one CTA, whose barriers take
-// less (plans_alone).
+// One cluster plans: it can hand sums around without another launch.  For small pools it has one CTA, whose barriers
+// take less (plans_alone).
 constexpr int kPlanCtas = 8;
 constexpr int kPlanThreads = 1024;
 
@@ -129,8 +129,8 @@ __device__ __forceinline__ void sync_cluster(cg::cluster_group& cluster) {
 // Calls f(page, held, rank) for the pages of a slice, rank being the number of free pages (FREE) or of held ones before
 // it, `at` before the slice; ends when `at` has reached `most`.  8192 pages a turn, a warp 256 consecutive ones.
 template <bool FREE, typename F>
-__device__ __forceinline__ void each_page(const PoolDev& p, int from, int to, long long at, long long most, PlanShared& sh,
-                                          F f) {
+__device__ __forceinline__ void each_page(const PoolDev& p, int from, int to, long long at, long long most,
+                                          PlanShared& sh, F f) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int c = from; c < to && at < most; c += 8 * kPlanThreads) {
     const int first = c + 256 * warp + lane;

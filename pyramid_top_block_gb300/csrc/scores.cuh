@@ -58,7 +58,8 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 
 // Factors of a row: y = score * to_y (to the cap's units), logit = score * to_l tanh(y) / y.
-// Large ones are cut, so that a product of zero stays zero: a 4-bit page's other products, 2^-34 or more, are far past the cap then.
+// Large ones are cut, so that a product of zero stays zero: a 4-bit page's other products, 2^-34 or more, are far past
+// the cap then.
 struct CapRow {
   float to_y, to_l;
 };
@@ -67,8 +68,8 @@ __device__ __forceinline__ CapRow cap_row(float factor, float inv_cap) {
 }
 
 // Factors of the short polynomial: logit = x (c[0] + x x (c[1] + ..)), x the product.  They fit 32 bits for
-// kCapLeast <= to_y <= kCapMost (caps are at most 2^20).  4-bit pages' products are below 2^19: with a smaller to_y the last
-// factor may fall below 2^-149, but what is lost of a logit is below 2^-18 of the larger of it and 1.
+// kCapLeast <= to_y <= kCapMost (caps are at most 2^20).  4-bit pages' products are below 2^19: with a smaller to_y the
+// last factor may fall below 2^-149, but what is lost of a logit is below 2^-18 of the larger of it and 1.
 struct CapPoly {
   float c[TanhHalf::n];
 };
@@ -88,9 +89,9 @@ __device__ __forceinline__ void cap_small(float& a, float& b, const CapRow& r) {
   f2_unpack(f2_mul(f2_mul(x, f2_pack(r.to_l, r.to_l)), tanh_ratio<Tanh>(f2_mul(x, f2_pack(r.to_y, r.to_y)))), a, b);
 }
 
-// Two scores of any size, capped: cap tanh y = cap - 2 cap / (1 + e^(2 y)), off by up to 2^-20.5 of the cap (so 1.3e-4 in
-// base 2 for a cap of 128, the largest that this is used for).  An infinity gives plus or minus the cap, a NaN a NaN.
-// two = 2 log2 e to_y, top = cap log2 e.
+// Two scores of any size, capped: cap tanh y = cap - 2 cap / (1 + e^(2 y)), off by up to 2^-20.5 of the cap (so 1.3e-4
+// in base 2 for a cap of 128, the largest that this is used for).  An infinity gives plus or minus the cap, a NaN a
+// NaN.  two = 2 log2 e to_y, top = cap log2 e.
 __device__ __forceinline__ void cap_exp(float& a, float& b, float two, float top) {
   float x, y;
   f2_unpack(f2_mul(f2_pack(a, b), f2_pack(two, two)), x, y);
