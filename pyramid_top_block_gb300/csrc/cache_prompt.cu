@@ -650,7 +650,21 @@ __device__ __forceinline__ bool soften_scored(const CachePromptLaunch& a, Prompt
   float all[kKeys], size;  // the products, and the largest one's magnitude
   tmem_ld128_top<true>(s, all, size);
   const bool in_range = r.cap.to_y <= kCapMost && (KIND == PISA_CACHE_E2M1 || r.cap.to_y >= kCapLeast);
-  const bool half = cap && !__any_sync(kFull, !in_range || size * r.cap.to_y > 0.5f);
+  // Whether the usual form does.  It goes by the products that are seen alone, and with it each logit's last bit: where
+  // one is past it that some row may not see, the largest one in sight is looked for.
+  const auto fits = [&] {
+    return __all_sync(kFull, (!cap || (in_range && size * r.cap.to_y <= 0.5f)) && (!slopes || size * r.f < kFar));
+  };
+  bool usual = fits();
+  if (__builtin_expect(!whole && !usual, 0)) {
+    const int from = r.lo - key0, to = r.hi - key0;
+    size = 0.f;
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) size = fmaxf(size, i >= from && i < to ? fabsf(all[i]) : 0.f);
+    usual = fits();
+  }
+  // (where `usual` is false already, the largest product alone decides)
+  const bool half = cap && (slopes ? !__any_sync(kFull, !in_range || size * r.cap.to_y > 0.5f) : usual);
   // at least the row's largest logit (a cap makes none larger)
   float b = size * r.f;
   if (cap && !half) b = cap_any(size, r.cap, a.score.cap * kLog2e);
