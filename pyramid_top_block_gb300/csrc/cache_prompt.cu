@@ -149,6 +149,10 @@ __device__ __forceinline__ void scrub(PromptShared& sh, unsigned char* v, int ti
   }
 }
 
+// Whether no row sees the key.  (In a mixed tile such keys become zeros: a row's logits do not count them, but the largest
+// product of a tile chooses how capped ones are computed.)
+__device__ __forceinline__ bool unseen(const PromptShared& sh, int key) { return key < sh.lo_min || key >= sh.hi_max; }
+
 // 16 dims of a token: 8 bytes of codes and a scale, as 16 fp16.
 __device__ __forceinline__ void dequant16(uint32_t c0, uint32_t c1, uint32_t scale, uint4& x, uint4& y) {
   const uint32_t s2 = e4m3x2(scale | scale << 8);
@@ -199,6 +203,9 @@ __device__ __forceinline__ bool load_bf16(const CachePromptLaunch& a, const CUte
       }
       ++asked.count;
       scrub(sh, stage + kTileBytes, tile, lane);
+#pragma unroll 4
+      for (int j = lane; j < kKeys * 8; j += 32)
+        if (unseen(sh, tile * kKeys + (j >> 3))) reinterpret_cast<uint4*>(stage)[j] = make_uint4(0, 0, 0, 0);
       fence_async_proxy();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.full[st]);
@@ -258,6 +265,7 @@ __device__ __forceinline__ bool load_e2m1(const CachePromptLaunch& a, const Prom
       uint32_t sc[2] = {there ? *reinterpret_cast<const uint32_t*>(r + 32 * U + in * 4) : 0u,
                         there ? *reinterpret_cast<const uint32_t*>(r + 68 * U + in * 4) : 0u};
       if (mixed) {  // NaN blocks of values that not all rows see become zeros (see scrub)
+        if (unseen(sh, tile * kKeys + row)) sc[0] = 0u;
         uint32_t keep = 0xffffffffu;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -650,21 +658,7 @@ __device__ __forceinline__ bool soften_scored(const CachePromptLaunch& a, Prompt
   float all[kKeys], size;  // the products, and the largest one's magnitude
   tmem_ld128_top<true>(s, all, size);
   const bool in_range = r.cap.to_y <= kCapMost && (KIND == PISA_CACHE_E2M1 || r.cap.to_y >= kCapLeast);
-  // Whether the usual form does.  It goes by the products that are seen alone, and with it each logit's last bit: where
-  // one is past it that some row may not see, the largest one in sight is looked for.
-  const auto fits = [&] {
-    return __all_sync(kFull, (!cap || (in_range && size * r.cap.to_y <= 0.5f)) && (!slopes || size * r.f < kFar));
-  };
-  bool usual = fits();
-  if (__builtin_expect(!whole && !usual, 0)) {
-    const int from = r.lo - key0, to = r.hi - key0;
-    size = 0.f;
-#pragma unroll
-    for (int i = 0; i < kKeys; ++i) size = fmaxf(size, i >= from && i < to ? fabsf(all[i]) : 0.f);
-    usual = fits();
-  }
-  // (where `usual` is false already, the largest product alone decides)
-  const bool half = cap && (slopes ? !__any_sync(kFull, !in_range || size * r.cap.to_y > 0.5f) : usual);
+  const bool half = cap && !__any_sync(kFull, !in_range || size * r.cap.to_y > 0.5f);
   // at least the row's largest logit (a cap makes none larger)
   float b = size * r.f;
   if (cap && !half) b = cap_any(size, r.cap, a.score.cap * kLog2e);
