@@ -149,8 +149,9 @@ __device__ __forceinline__ void scrub(PromptShared& sh, unsigned char* v, int ti
   }
 }
 
-// Whether no row sees the key.  (In a mixed tile such keys become zeros: a row's logits do not count them, but the largest
-// product of a tile chooses how capped ones are computed.)
+// Whether no row sees the key.  (In a scored call's mixed tile such keys become zeros: no row's logits count them, but
+// the largest product of a tile chooses how scores are computed.)
+__device__ __forceinline__ bool is_scored(const CachePromptLaunch& a) { return a.score.cap > 0.f || a.score.slopes; }
 __device__ __forceinline__ bool unseen(const PromptShared& sh, int key) { return key < sh.lo_min || key >= sh.hi_max; }
 
 // 16 dims of a token: 8 bytes of codes and a scale, as 16 fp16.
@@ -203,9 +204,11 @@ __device__ __forceinline__ bool load_bf16(const CachePromptLaunch& a, const CUte
       }
       ++asked.count;
       scrub(sh, stage + kTileBytes, tile, lane);
+      if (is_scored(a)) {
 #pragma unroll 4
-      for (int j = lane; j < kKeys * 8; j += 32)
-        if (unseen(sh, tile * kKeys + (j >> 3))) reinterpret_cast<uint4*>(stage)[j] = make_uint4(0, 0, 0, 0);
+        for (int j = lane; j < kKeys * 8; j += 32)
+          if (unseen(sh, tile * kKeys + (j >> 3))) reinterpret_cast<uint4*>(stage)[j] = make_uint4(0, 0, 0, 0);
+      }
       fence_async_proxy();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.full[st]);
@@ -265,7 +268,7 @@ __device__ __forceinline__ bool load_e2m1(const CachePromptLaunch& a, const Prom
       uint32_t sc[2] = {there ? *reinterpret_cast<const uint32_t*>(r + 32 * U + in * 4) : 0u,
                         there ? *reinterpret_cast<const uint32_t*>(r + 68 * U + in * 4) : 0u};
       if (mixed) {  // NaN blocks of values that not all rows see become zeros (see scrub)
-        if (unseen(sh, tile * kKeys + row)) sc[0] = 0u;
+        if (is_scored(a) && unseen(sh, tile * kKeys + row)) sc[0] = 0u;
         uint32_t keep = 0xffffffffu;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
