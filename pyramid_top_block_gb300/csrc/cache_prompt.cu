@@ -16,7 +16,7 @@
 // and takes as long as with 128) and the exponentials 1024, and each row tile waits for its product, takes its scores
 // into registers, weighs them and hands the weights back: about 2000 clocks.  32 heads on 2, bf16 (4-bit) pages: 32768
 // tokens 3.51 ms = 1.25 PFLOP/s (3.81 ms), 2048 at 131072 1.68 ms = 1.30 PFLOP/s (1.82), 1216 at 16384 132 us (142),
-// capped 171 to 179, with slopes 162; a library's bf16 product of matrices reaches 1.90 PFLOP/s.
+// capped 170 to 180, with slopes 161; a library's bf16 product of matrices reaches 1.90 PFLOP/s.
 #include "cache_prompt.cuh"
 
 #include <climits>
