@@ -26,14 +26,16 @@ struct SeqTiles { int first, tiles, places; };
 template <int KT, bool WINDOWED>
 static SeqTiles seq_tiles(int n, int T, int window, int change) {
   const int tiles = unit_tiles<KT, WINDOWED>(n, T, window);
-  return {first_tile<KT, WINDOWED>(n, T, window), tiles, change == 36 ? unit_places<36>(tiles) : unit_places<24>(tiles)};
+  const int places = change == 36 ? unit_places<36>(tiles) : unit_places<24>(tiles);
+  return {first_tile<KT, WINDOWED>(n, T, window), tiles, places};
 }
 
 // Replays a call on `runs` runs, `units` units a sequence.  Returns 0, or which rule does not hold.
 template <int KT, bool WINDOWED>
 static int replay(const int* n, int B, int T, int window, int change, int units, int runs, int64_t* cuts) {
   std::vector<long long> base(B + 1, 0);
-  for (int b = 0; b < B; ++b) base[b + 1] = base[b] + (long long)seq_tiles<KT, WINDOWED>(n[b], T, window, change).places * units;
+  for (int b = 0; b < B; ++b)
+    base[b + 1] = base[b] + (long long)seq_tiles<KT, WINDOWED>(n[b], T, window, change).places * units;
   const long long total = base[B], per = run_length(total, runs);
   if (per * runs < total) return 1;
   // the split kernel: a unit's result, or up to two partial ones a run (slot 1: the unit begins in the run)
@@ -70,7 +72,8 @@ static int replay(const int* n, int B, int T, int window, int change, int units,
     long long lo = WINDOWED ? (long long)n[b] - T + 1 - window : 0;
     if (lo < 0) lo = 0;
     if (n[b] && (s.first * (long long)KT > lo || (s.first + 1) * (long long)KT <= lo)) return 4;
-    if (n[b] && ((long long)(s.first + s.tiles) * KT < n[b] || (long long)(s.first + s.tiles - 1) * KT >= n[b])) return 5;
+    const long long stop = s.first + s.tiles;
+    if (n[b] && (stop * KT < n[b] || (stop - 1) * KT >= n[b])) return 5;
     for (int un = 0; un < units; ++un)
       if (tiles[{b, un}] != s.tiles) return 6;
   }
@@ -112,9 +115,11 @@ static int replay(const int* n, int B, int T, int window, int change, int units,
         if (whole[{b, un}] + j[{b, un}] != (n[b] > 0)) return 20;
   return 0;
 }
-extern "C" int call(const int* n, int B, int T, int window, int kt, int change, int units, int runs, int windowed, int64_t* cuts) {
-  if (kt == 32) return windowed ? replay<32, true>(n, B, T, window, change, units, runs, cuts) : replay<32, false>(n, B, T, window, change, units, runs, cuts);
-  return windowed ? replay<64, true>(n, B, T, window, change, units, runs, cuts) : replay<64, false>(n, B, T, window, change, units, runs, cuts);
+extern "C" int call(const int* n, int B, int T, int window, int kt, int change, int units, int runs, int windowed,
+                    int64_t* cuts) {
+  const auto f = kt == 32 ? (windowed ? replay<32, true> : replay<32, false>)
+                          : (windowed ? replay<64, true> : replay<64, false>);
+  return f(n, B, T, window, change, units, runs, cuts);
 }
 """
 
@@ -123,14 +128,14 @@ extern "C" int call(const int* n, int B, int T, int window, int kt, int change, 
 def call(tmp_path_factory):
     d = tmp_path_factory.mktemp("stream")
     (d / "s.cpp").write_text(HOST)
-    subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-I" + CSRC, str(d / "s.cpp"), "-o", str(d / "s.so")],
-                   check=True)
+    subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-I" + CSRC, str(d / "s.cpp"), "-o",
+                    str(d / "s.so")], check=True)
     fn = ctypes.CDLL(str(d / "s.so")).call
 
     def run(lengths, T, window, kt, change, units, runs):
         n, cuts = np.asarray(lengths, np.int32), ctypes.c_int64()
-        bad = fn(n.ctypes.data_as(ctypes.c_void_p), n.size, T, 1 << 28 if window is None else window, kt, change, units, runs,
-                 int(window is not None), ctypes.byref(cuts))
+        bad = fn(n.ctypes.data_as(ctypes.c_void_p), n.size, T, 1 << 28 if window is None else window, kt, change,
+                 units, runs, int(window is not None), ctypes.byref(cuts))
         return bad, cuts.value
 
     return run
@@ -174,7 +179,8 @@ def test_the_kernels_take_the_arithmetic_from_the_header():
     text = code_of("cache_attend.cuh")
     for name in ("cache_attend_split_kernel", "cache_join_kernel"):
         body = re.search(name + r"\(CacheAttendLaunch a.*?\n}\n", text, re.S).group(0)
-        assert "tiles_of_seq<KIND, MODE>" in body and "places_of<KIND>" in body and "run_length(" in body and "unit_at(" in body
+        for part in ("tiles_of_seq<KIND, MODE>", "places_of<KIND>", "run_length(", "unit_at("):
+            assert part in body
         body = body.replace("c0 = (int)(w0 / per)", "").replace("first_tile<C::KT, ", "")
         assert not re.search(r"\bKT\b|kChange|/ per|/ \(unsigned\)", body)
     assert text.count("goes_on(") == 2

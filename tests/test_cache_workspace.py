@@ -1,4 +1,4 @@
-"""What the attention calls ask for of a workspace: the single tokens' call no more than its own partial results take."""
+"""What the attention calls ask for of a workspace: the single tokens' call no more than its partial results take."""
 import pytest
 import torch
 
@@ -10,7 +10,7 @@ from test_more_cache_abi import prompt, scored
 def test_a_decoding_programs_workspace():
     lib = pisa.load()
     token, every = lib.pisa_cache_attention_workspace_bytes(), lib.pisa_cache_workspace_bytes()
-    # two partial results (16 rows of 64 sums, a reference and a sum of weights) for each of 152 CTAs, and the status word
+    # two partial results (16 rows of 64 sums, a reference and a sum of weights) for each of 152 CTAs, and the status
     assert token == 256 + 152 * 2 * 16 * 66 * 4 < every
     assert pisa.cache_workspace_bytes(prompts=False) == token and pisa.cache_workspace_bytes() == every
     assert attend(cache(), ws_bytes=token - 1) == 3 and scored(cache(), ws_bytes=token - 1) == 3

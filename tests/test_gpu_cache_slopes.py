@@ -15,12 +15,13 @@ def f32(x):
 
 
 def expected(q, k, v, at, lo, hi, cap, slopes, weight, dtype):
-    """(o, tolerance): score_ref's, its sums over the keys that count, those of at least 2^-40 of the row's largest weight.
-    The others are off by at most themselves, so by 2^-40 sum |v| and, of the sum of weights, by n 2^-40 <= 2^-20 for
-    n <= 2^20, twice.  fp16 weights (4-bit pages) have steps of 2^-24 at least, relative to a reference of at most the largest
-    one, so those that count are also off by 2^-25 each."""
+    """(o, tolerance): score_ref's, its sums over the keys that count, those of at least 2^-40 of the row's largest
+    weight.  The others are off by at most themselves, so by 2^-40 sum |v| and, of the sum of weights, by n 2^-40 <=
+    2^-20 for n <= 2^20, twice.  fp16 weights (4-bit pages) have steps of 2^-24 at least, relative to a reference of at
+    most the largest one, so those that count are also off by 2^-25 each.  (Positions as doubles: whole numbers times a
+    float are 32 bits.)"""
     G = q.shape[1] // k.shape[1]
-    o, pv, big = score_ref.attention(q, k, v, at.double(), lo, hi, cap, slopes)  # (whole numbers times a float are 32 bits)
+    o, pv, big = score_ref.attention(q, k, v, at.double(), lo, hi, cap, slopes)
     x = torch.einsum("thd,nhd->thn", q, k.repeat_interleave(G, 1)) / 8
     if cap:
         x = cap * torch.tanh(x / cap)
@@ -46,7 +47,8 @@ def both(q, cache, n, T, cap, s, window=0):
     at = n - T + torch.arange(T, device=DEV)
     lo = (at - window + 1).clamp(min=0) if window else torch.zeros_like(at)
     bf16 = cache.bits == 16
-    for dtype, weight in ((torch.bfloat16, 2.0 ** (-16 if bf16 else -11)), (torch.float32, 2.0 ** (-22 if bf16 else -20))):
+    for dtype, weight in ((torch.bfloat16, 2.0 ** (-16 if bf16 else -11)),
+                          (torch.float32, 2.0 ** (-22 if bf16 else -20))):
         out = torch.full((1, T, q.shape[2], 64), 7.0, dtype=dtype, device=DEV)
         got = pisa.cache_attention(q, cache, i32([n]), out=out, cap=cap, slopes=s, window=window)
         check(got[0], expected(q[0].double(), k, v, at, lo, at + 1, cap, s, weight, dtype))
@@ -118,11 +120,12 @@ def test_negative_slopes_past_two_to_the_24(cap):
         table = small.table[0, e % few][None].contiguous()
         cache = pisa.PagedCache(small.pages, table, page)
         q, s = normal(g, 1, T, 2, 64) * 6, f32([-0.5, -2.0])
-        m = 500  # tokens that can count: the bias of the others is 100 less, which the scores (below 40) do not make up for
+        m = 500  # tokens that can count: the others' bias is 100 less, which the scores (below 40) do not make up for
         k, v = ref.tokens(cache, 0, m)
         at = n - T + torch.arange(T, device=DEV)
         zero = torch.zeros_like(at)
-        want = expected(q[0].double(), k, v, at, zero, zero + m, cap, s, 2.0 ** (-8 if bits == 16 else -11), torch.bfloat16)
+        weight = 2.0 ** (-8 if bits == 16 else -11)
+        want = expected(q[0].double(), k, v, at, zero, zero + m, cap, s, weight, torch.bfloat16)
         check(pisa.cache_prompt_attention(q, cache, i32([n - T]), cap=cap, slopes=s)[0], want)
         check(pisa.cache_attention(q, cache, i32([n]), cap=cap, slopes=s)[0], want)
 
@@ -139,7 +142,8 @@ def test_steep_slopes_over_long_caches(bits, cap, n, T):
     at = n - T + torch.arange(T, device=DEV)
     zero = torch.zeros_like(at)
     got = pisa.cache_prompt_attention(q, cache, i32([n - T]), cap=cap, slopes=s)
-    check(got[0], expected(q[0].double(), k, v, at, zero, at + 1, cap, s, 2.0 ** (-8 if bits == 16 else -11), torch.bfloat16))
+    weight = 2.0 ** (-8 if bits == 16 else -11)
+    check(got[0], expected(q[0].double(), k, v, at, zero, at + 1, cap, s, weight, torch.bfloat16))
 
 
 @pytest.mark.parametrize("bits,size", [(16, 1.0), (4, 1.0), (4, 2.0 ** -75)])
@@ -150,7 +154,8 @@ def test_slopes_of_any_size(bits, size, cap):
     n, T = 5000, 4
     cache = make_cache(g, 1, n, 1, 64, bits, k_exp=-24 if size < 1 else 0)
     q = (normal(g, 1, T, 8, 64) * size).to(torch.bfloat16)
-    for s in ([1e5, -1e5, 1e12, -1e12, 1e30, -1e30, 3e38, -3e38], [1e-30, -1e-30, 1e-44, -1e-44, 0.0, -0.0, 1e-20, -1e-20]):
+    for s in ([1e5, -1e5, 1e12, -1e12, 1e30, -1e30, 3e38, -3e38],
+              [1e-30, -1e-30, 1e-44, -1e-44, 0.0, -0.0, 1e-20, -1e-20]):
         both(q, cache, n, T, cap, f32(s))
 
 
@@ -165,7 +170,7 @@ def test_slopes_of_huge_queries_over_keys_of_zero():
 
 
 def test_positions_past_the_table_with_slopes():
-    """Starts at both ends of 32 bits: flagged, and what is in sight still counts by the distances between the tokens."""
+    """Starts at both ends of 32 bits: flagged, and what is in sight still counts by the tokens' distances."""
     g = gen(9)
     for bits in (16, 4):
         cache = make_cache(g, 1, 512, 1, 64, bits)
@@ -177,8 +182,8 @@ def test_positions_past_the_table_with_slopes():
                 at = start + torch.arange(T, device=DEV)
                 hi = torch.full_like(at, n)
                 ws = pisa.cache_workspace(cache)
-                got = pisa.cache_prompt_attention(q, cache, i32([start]), last=None if last is None else i32(last), cap=cap,
-                                                  slopes=s, workspace=ws)
+                got = pisa.cache_prompt_attention(q, cache, i32([start]), last=None if last is None else i32(last),
+                                                  cap=cap, slopes=s, workspace=ws)
                 assert status(ws) == 6
                 if last is not None:  # (no token of the sequence is there: it ends before 0)
                     assert not bool(got.any())

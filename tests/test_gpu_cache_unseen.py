@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+import cache_ref as ref
 import pyramid_top_block_gb300 as pisa
 from test_gpu_cache import DEV, gen, i32, make_cache, normal
 
@@ -23,13 +24,12 @@ def scaled_keys(cache, positions, factor):
 @pytest.mark.parametrize("cap,slopes", [(0.0, False), (6.0, False), (40.0, True), (300.0, False), (0.0, True)])
 @pytest.mark.parametrize("window,start,T", [(0, 100, 300), (50, 300, 200), (0, 5000, 20)])
 def test_unseen_keys_do_not_choose_how_scores_are_computed(bits, cap, slopes, window, start, T):
-    """The scores that are seen stay below half the cap; those behind the sequence, and before the windows, pass it or do not."""
+    """Scores that are seen stay below half the cap; those behind the sequence and before the windows may pass it."""
     g = gen(bits + T)
     n = start + T
     cache = make_cache(g, 1, n + 100, 2, 64, bits)
     q = normal(g, 1, T, 32, 64)
     if cap:  # the largest seen score is a third of the cap
-        import cache_ref as ref
         k, _ = ref.tokens(cache, 0, n)
         q = (q * (cap / 3 / float((q[0, :, 0].double() @ k[:, 0].T / 8).abs().max()) / 1.5)).to(torch.bfloat16)
     s = torch.tensor([2.0 ** (-8 * (h + 1) / 32) for h in range(32)], device=DEV) if slopes else None

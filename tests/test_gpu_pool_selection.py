@@ -1,4 +1,4 @@
-"""Forked sequences of layers that select: the pages are shared, the pyramid's rows are copied by the caller, as documented."""
+"""Forked sequences of layers that select: pages are shared, and the caller copies the pyramid's rows, as documented."""
 import pytest
 import torch
 

@@ -23,7 +23,7 @@ def reserve(granted, counts=COUNTS):
 
 @pytest.mark.parametrize("at", INSIDE)
 def test_granted_in_lengths(at):
-    """The lengths are read again after the first sequences' grants are written: pages would be looked up past the list."""
+    """The lengths are read again after the first grants are written: pages would be looked up past the list."""
     assert reserve(LENGTHS + at) == 1 and reserve(LENGTHS + at, counts=None) == 1
 
 
@@ -32,7 +32,8 @@ def test_granted_beside_counts(at):
     assert reserve(COUNTS + at) == 1
 
 
-@pytest.mark.parametrize("granted", [TABLE, TABLE + 4 * (B * MAX_PAGES - 1), REFS + 4 * (N_PAGES - 1), REFS - 4 * (B - 1)])
+@pytest.mark.parametrize("granted", [TABLE, TABLE + 4 * (B * MAX_PAGES - 1), REFS + 4 * (N_PAGES - 1),
+                                     REFS - 4 * (B - 1)])
 def test_granted_in_the_pool(granted):
     assert reserve(granted) == 1
 
